@@ -27,7 +27,8 @@ from ._native import (E4M3, E5M2, INT8, OUT_BF16, OUT_F32, SCALE_CHANNEL_STATIC,
 __all__ = ["kv_append_quant", "kv_append_quant_segment", "segment_scale_heads",
            "kv_channel_scales", "kv_channel_absmax_update",
            "kv_scales_from_absmax", "paged_decode_attention", "paged_multiquery_attention",
-           "decode_step", "decode_workspace_bytes", "get_device_error", "set_decode_workers",
+           "kv_append_rope", "paged_decode_attention_mod", "paged_prefill_attention",
+           "prefill_workspace_bytes", "decode_step", "decode_workspace_bytes", "get_device_error", "set_decode_workers",
            "version", "E4M3", "E5M2", "INT8", "SCALE_TOKEN_HEAD", "SCALE_CHANNEL_STATIC",
            "SCALE_TOKEN_GROUP", "SCALE_MX_BLOCK", "SCALE_SEGMENT", "SEGMENT_TOKENS", "OUT_BF16",
            "OUT_F32", "Fp8paError"]
@@ -332,6 +333,232 @@ def decode_step(k_new, v_new, slot_mapping, q, k_cache, v_cache, k_scale, v_scal
             float(sm_scale), nb, _ptr(out), odt, _ptr(workspace),
             0 if workspace is None else workspace.numel(), _stream(stream))
     N.check(rc, "decode_step")
+    return out
+
+
+def _check_cache(k_cache, v_cache, k_scale, v_scale, n_kv_heads, head_dim, scale_mode,
+                 group_size, dev):
+    """The shapes of a paged cache and its scales; returns (num_blocks, block_size)."""
+    if k_cache.dim() != 4 or k_cache.shape[1] != n_kv_heads or k_cache.shape[3] != head_dim:
+        raise ValueError(f"k_cache must be [num_blocks, {n_kv_heads}, block_size, {head_dim}], "
+                         f"got {tuple(k_cache.shape)}")
+    nb, _, bs, _ = k_cache.shape
+    if scale_mode == SCALE_CHANNEL_STATIC:
+        numel = n_kv_heads * head_dim
+    elif scale_mode == SCALE_SEGMENT:
+        numel = nb * segment_scale_heads(n_kv_heads)
+    elif scale_mode in (SCALE_MX_BLOCK, SCALE_TOKEN_GROUP):
+        numel = nb * n_kv_heads * bs * (head_dim // max(int(group_size), 1))
+    else:
+        numel = nb * n_kv_heads * bs
+    sdt = torch.uint8 if scale_mode == SCALE_MX_BLOCK else torch.float32
+    for cache, scale, name in ((k_cache, k_scale, "k"), (v_cache, v_scale, "v")):
+        if cache is None and scale is None and name == "v":
+            continue
+        if cache is None or scale is None:
+            raise ValueError(f"{name}_cache and {name}_scale come together")
+        _need(cache, torch.uint8, name + "_cache", dev)
+        _need(scale, sdt, name + "_scale", dev)
+        if cache.shape != k_cache.shape:
+            raise ValueError(f"{name}_cache must have k_cache's shape")
+        if scale.numel() != numel:
+            raise ValueError(f"{name}_scale must hold {numel} values, got {scale.numel()}")
+    return nb, bs
+
+
+def _rows(t, name, n, heads, d, dev):
+    """A bf16 [n, heads, d] tensor whose tokens may be strided; returns the stride."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if tuple(t.shape) != (n, heads, d):
+        raise ValueError(f"{name} must be {(n, heads, d)}, got {tuple(t.shape)}")
+    s = t.stride()
+    if (d > 1 and s[2] != 1) or (heads > 1 and s[1] != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return s[0] if n > 1 else heads * d
+
+
+def kv_append_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+                   rot_offset=0, interleaved=False, fmt=E4M3, scale_mode=SCALE_TOKEN_HEAD,
+                   group_size=64, q_out=None, stream=None):
+    """Turn q and k by their tokens' rotary angles, then quantise K and V into
+    the paged cache.  q: bf16 [N, Hq, D] (None: no queries); k, v: bf16
+    [N, Hkv, D] (v None for the MLA latent); their tokens may be strided (slices
+    of a fused projection).  positions: int32 [N]; cos_sin: float32
+    [max_position, rot_dim], cosines then sines of rot_dim / 2 angles; the dims
+    rot_offset .. rot_offset + rot_dim - 1 of each row are turned, halves paired
+    (or neighbours, interleaved=True).  Returns q_out (q_out=q: in place)."""
+    if k.dim() != 3:
+        raise ValueError("k must be [num_tokens, n_kv_heads, head_dim]")
+    dev = k.device
+    n, hkv, d = k.shape
+    ks = _rows(k, "k", n, hkv, d, dev)
+    vs = 0 if v is None else _rows(v, "v", n, hkv, d, dev)
+    hq = qs = qos = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [num_tokens, n_q_heads, head_dim]")
+        hq = q.shape[1]
+        qs = _rows(q, "q", n, hq, d, dev)
+        if q_out is None:
+            q_out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=dev)
+            if stream is not None:
+                q_out.record_stream(stream)
+        qos = _rows(q_out, "q_out", n, hq, d, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _need(positions, torch.int32, "positions", dev)
+    _need(slot_mapping, torch.int32, "slot_mapping", dev)
+    _need(cos_sin, torch.float32, "cos_sin", dev)
+    if positions.numel() != n or slot_mapping.numel() != n:
+        raise ValueError(f"positions and slot_mapping must hold {n} entries")
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_position, rot_dim]")
+    if v is not None and (v_cache is None or v_scale is None):
+        raise ValueError("v needs v_cache and v_scale")
+    nb, bs = _check_cache(k_cache, None if v is None else v_cache, k_scale,
+                          None if v is None else v_scale, hkv, d, scale_mode, group_size, dev)
+    with _on(dev):
+        rc = N.lib.fp8pa_kv_append_rope(
+            _ptr(q), _ptr(q_out), _ptr(k), _ptr(v), qs, qos, ks, vs, _ptr(positions),
+            _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], rot_offset, 1 if interleaved else 0,
+            _ptr(slot_mapping), n, hq, hkv, d, fmt, scale_mode, group_size, _ptr(k_cache),
+            _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), nb, bs, _stream(stream))
+    N.check(rc, "kv_append_rope")
+    return q_out
+
+
+def _check_mods(prefix_lens, alibi_slopes, batch, hq, dev):
+    _need(prefix_lens, torch.int32, "prefix_lens", dev)
+    _need(alibi_slopes, torch.float32, "alibi_slopes", dev)
+    if prefix_lens is not None and prefix_lens.numel() != batch:
+        raise ValueError(f"prefix_lens must hold {batch} entries")
+    if alibi_slopes is not None and alibi_slopes.numel() != hq:
+        raise ValueError(f"alibi_slopes must hold {hq} entries")
+
+
+def _check_tables(block_tables, seq_lens, dev):
+    _need(block_tables, torch.int32, "block_tables", dev)
+    _need(seq_lens, torch.int32, "seq_lens", dev)
+    if block_tables.dim() != 2 or seq_lens.dim() != 1 or (
+            block_tables.shape[0] != seq_lens.shape[0]):
+        raise ValueError("block_tables must be [batch, max_blocks] and seq_lens [batch]")
+    return block_tables.shape
+
+
+def _output(out, shape, out_dtype, dev, stream):
+    """The output tensor and its element code."""
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=dev)
+        if stream is not None:
+            out.record_stream(stream)
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("out must be bf16 or float32")
+    _need(out, out.dtype, "out", dev)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"out must be {tuple(shape)}, got {tuple(out.shape)}")
+    return out, OUT_F32 if out.dtype == torch.float32 else OUT_BF16
+
+
+def _scratch(need, dev, stream):
+    """Workspace of one call: freed for reuse only behind the call's own stream."""
+    if need == 0:
+        return None
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def paged_decode_attention_mod(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
+                               n_kv_heads, sm_scale, window=0, prefix_lens=None, logit_cap=0.0,
+                               alibi_slopes=None, fmt=E4M3, scale_mode=SCALE_TOKEN_HEAD,
+                               group_size=64, out=None, out_dtype=None, workspace=None,
+                               stream=None):
+    """paged_decode_attention (GQA layout) with score modifiers: a sliding
+    window of `window` tokens (0: none), the first prefix_lens[b] tokens (int32
+    [B]) always visible, scores capped as logit_cap * tanh(z / logit_cap)
+    (0: not), and alibi_slopes[h] (float32 [Hq]) times the distance subtracted.
+    Pages without a visible token are not read.  Returns out [B, Hq, D]."""
+    _need(q, torch.bfloat16, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [batch, n_q_heads, head_dim]")
+    dev = q.device
+    B, hq, d = q.shape
+    rows, max_blocks = _check_tables(block_tables, seq_lens, dev)
+    if rows != B:
+        raise ValueError(f"block_tables and seq_lens must have {B} rows")
+    if v_cache is None or v_scale is None:
+        raise ValueError("v_cache and v_scale are required")
+    nb, bs = _check_cache(k_cache, v_cache, k_scale, v_scale, n_kv_heads, d, scale_mode,
+                          group_size, dev)
+    _check_mods(prefix_lens, alibi_slopes, B, hq, dev)
+    out, odt = _output(out, (B, hq, d), out_dtype, dev, stream)
+    with _on(dev):
+        if workspace is None:
+            workspace = _scratch(int(N.lib.fp8pa_decode_workspace_bytes(
+                B, hq, n_kv_heads, d, d, bs, max_blocks)), dev, stream)
+        _need(workspace, torch.uint8, "workspace", dev)
+        rc = N.lib.fp8pa_paged_decode_attention_mod(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(block_tables), max_blocks, _ptr(seq_lens), B, bs, hq, n_kv_heads, d, fmt,
+            scale_mode, group_size, float(sm_scale), window, _ptr(prefix_lens), float(logit_cap),
+            _ptr(alibi_slopes), nb, _ptr(out), odt, _ptr(workspace),
+            0 if workspace is None else workspace.numel(), _stream(stream))
+    N.check(rc, "paged_decode_attention_mod")
+    return out
+
+
+def prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, device=None) -> int:
+    """Workspace bytes of paged_prefill_attention for these sizes."""
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        nbytes = int(N.lib.fp8pa_prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads,
+                                                         head_dim))
+    if nbytes == 0:
+        raise Fp8paError(N.ERR_UNSUPPORTED, "prefill_workspace_bytes")
+    return nbytes
+
+
+def paged_prefill_attention(q, q_offsets, k_cache, v_cache, k_scale, v_scale, block_tables,
+                            seq_lens, n_kv_heads, sm_scale, window=0, prefix_lens=None,
+                            logit_cap=0.0, alibi_slopes=None, fmt=E4M3,
+                            scale_mode=SCALE_TOKEN_HEAD, group_size=64, out=None, out_dtype=None,
+                            workspace=None, stream=None):
+    """Causal attention of ragged query chunks over the paged cache, with the
+    score modifiers of paged_decode_attention_mod.  q: bf16 [total_q, Hq, D],
+    request b's chunk in rows q_offsets[b] .. q_offsets[b+1]-1 (int32 [B + 1]),
+    already appended; seq_lens counts it.  The first prefix_lens[b] tokens are
+    visible to every query, also to those before them.  Rows outside every
+    chunk are left as they were.  Returns out [total_q, Hq, D]."""
+    _need(q, torch.bfloat16, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [total_q, n_q_heads, head_dim]")
+    dev = q.device
+    total, hq, d = q.shape
+    B, max_blocks = _check_tables(block_tables, seq_lens, dev)
+    _need(q_offsets, torch.int32, "q_offsets", dev)
+    if q_offsets.numel() != B + 1:
+        raise ValueError(f"q_offsets must hold {B + 1} entries")
+    if v_cache is None or v_scale is None:
+        raise ValueError("v_cache and v_scale are required")
+    nb, bs = _check_cache(k_cache, v_cache, k_scale, v_scale, n_kv_heads, d, scale_mode,
+                          group_size, dev)
+    _check_mods(prefix_lens, alibi_slopes, B, hq, dev)
+    out, odt = _output(out, (total, hq, d), out_dtype, dev, stream)
+    with _on(dev):
+        if workspace is None:
+            workspace = _scratch(int(N.lib.fp8pa_prefill_workspace_bytes(
+                total, B, hq, n_kv_heads, d)), dev, stream)
+        _need(workspace, torch.uint8, "workspace", dev)
+        rc = N.lib.fp8pa_paged_prefill_attention(
+            _ptr(q), _ptr(q_offsets), total, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+            _ptr(v_scale), _ptr(block_tables), max_blocks, _ptr(seq_lens), B, bs, hq, n_kv_heads,
+            d, fmt, scale_mode, group_size, float(sm_scale), window, _ptr(prefix_lens),
+            float(logit_cap), _ptr(alibi_slopes), nb, _ptr(out), odt, _ptr(workspace),
+            0 if workspace is None else workspace.numel(), _stream(stream))
+    N.check(rc, "paged_prefill_attention")
     return out
 
 

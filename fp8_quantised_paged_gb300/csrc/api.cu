@@ -2,6 +2,7 @@
 // validation, dispatch to the kernels, tensor-map encoding, the per-device
 // error word and status strings.  No call allocates device memory.
 #include <cudaTypedefs.h>
+#include <float.h>
 
 #include <mutex>
 #include <utility>
@@ -9,6 +10,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "score_mods.cuh"
 
 namespace fp8pa {
 
@@ -369,6 +371,16 @@ int append_prepare(const void* k, const void* v, const int32_t* slot_mapping, in
   return FP8PA_OK;
 }
 
+// The sizes of a prefill call that its workspace depends on.
+int prefill_shape(int total_q, int batch, int hq, int hkv, int d) {
+  if (total_q < 0 || batch < 0 || hq <= 0 || hkv <= 0 || hq % hkv != 0)
+    return FP8PA_ERR_BAD_SHAPE;
+  if (d != 64 && d != 128) return FP8PA_ERR_UNSUPPORTED;
+  if ((static_cast<long long>(total_q) + 256ll * batch) * hq >= (1ll << 31))
+    return FP8PA_ERR_UNSUPPORTED;
+  return FP8PA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -597,6 +609,173 @@ int fp8pa_decode_step(const void* k_new, const void* v_new, const int32_t* slot_
   if (e != cudaSuccess) return FP8PA_ERR_CUDA;
   a.plan_ready = true;
   return cuda_status(launch_decode(path, a, cs));
+}
+
+int fp8pa_kv_append_rope(const void* q, void* q_out, const void* k, const void* v,
+                         long long q_stride, long long q_out_stride, long long k_stride,
+                         long long v_stride, const int32_t* positions, const float* cos_sin,
+                         int max_position, int rot_dim, int rot_offset, int interleaved,
+                         const int32_t* slot_mapping, int num_tokens, int n_q_heads,
+                         int n_kv_heads, int head_dim, int fmt, int scale_mode, int group_size,
+                         uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale,
+                         int num_blocks, int block_size, void* stream) {
+  AppendArgs ap;
+  const int st = append_prepare(k, v, slot_mapping, num_tokens, n_kv_heads, head_dim, fmt,
+                                scale_mode, group_size, k_cache, v_cache, k_scale, v_scale,
+                                num_blocks, block_size, &ap);
+  if (st != FP8PA_OK) return st;
+  if ((q == nullptr) != (q_out == nullptr) && num_tokens > 0) return FP8PA_ERR_NULL_POINTER;
+  if (max_position <= 0 || rot_dim <= 0 || rot_offset < 0 || rot_dim > head_dim ||
+      rot_offset > head_dim - rot_dim || (q && n_q_heads <= 0))
+    return FP8PA_ERR_BAD_SHAPE;
+  if (interleaved != 0 && interleaved != 1) return FP8PA_ERR_BAD_ENUM;
+  if (rot_dim % 16 != 0 || rot_offset % 8 != 0) return FP8PA_ERR_UNSUPPORTED;
+  if (head_dim > 256 && rot_offset / 256 != (rot_offset + rot_dim - 1) / 256)
+    return FP8PA_ERR_UNSUPPORTED;
+  const long long rows = static_cast<long long>(q ? n_q_heads : 0) + n_kv_heads * (v ? 2ll : 1ll);
+  if (rows * num_tokens >= (1ll << 31) || rows * head_dim >= (1ll << 31))
+    return FP8PA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return FP8PA_OK;
+  if (!positions || !cos_sin) return FP8PA_ERR_NULL_POINTER;
+  const long long kv_row = static_cast<long long>(n_kv_heads) * head_dim;
+  const long long q_row = static_cast<long long>(q ? n_q_heads : 0) * head_dim;
+  if (k_stride < kv_row || (v && v_stride < kv_row) ||
+      (q && (q_stride < q_row || q_out_stride < q_row)))
+    return FP8PA_ERR_BAD_SHAPE;
+  if (k_stride % 8 != 0 || (v && v_stride % 8 != 0) ||
+      (q && (q_stride % 8 != 0 || q_out_stride % 8 != 0 || !aligned16(q) || !aligned16(q_out))) ||
+      !aligned16(cos_sin))
+    return FP8PA_ERR_ALIGNMENT;
+  RopeArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_stride = q_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.positions = positions;
+  a.slot_mapping = slot_mapping;
+  a.cos_sin = cos_sin;
+  for (int i = 0; i < 2; ++i) {
+    a.cache[i] = ap.cache[i];
+    a.scale[i] = ap.scale[i];
+  }
+  a.max_position = max_position;
+  a.rot_dim = rot_dim;
+  a.rot_offset = rot_offset;
+  a.interleaved = interleaved;
+  a.num_tokens = num_tokens;
+  a.hq = q ? n_q_heads : 0;
+  a.hkv = n_kv_heads;
+  a.d = head_dim;
+  a.gs = ap.gs;
+  a.num_blocks = num_blocks;
+  a.bs = block_size;
+  a.rows = static_cast<int>(rows);
+  a.div_bs = ap.div_bs;
+  a.err = device_error_ptr(static_cast<cudaStream_t>(stream), nullptr);
+  if (!a.err) return FP8PA_ERR_CUDA;
+  return cuda_status(launch_append_rope(a, fmt, scale_mode, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8pa_paged_decode_attention_mod(const void* q, const uint8_t* k_cache,
+                                     const uint8_t* v_cache, const float* k_scale,
+                                     const float* v_scale, const int32_t* block_tables,
+                                     int max_blocks_per_seq, const int32_t* seq_lens, int batch,
+                                     int block_size, int n_q_heads, int n_kv_heads, int head_dim,
+                                     int fmt, int scale_mode, int group_size, float sm_scale,
+                                     int window, const int32_t* prefix_lens, float logit_cap,
+                                     const float* alibi_slopes, int num_blocks, void* out,
+                                     int out_dtype, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  if (window < 0) return FP8PA_ERR_BAD_SHAPE;
+  if (!(logit_cap >= 0.f) || logit_cap > FLT_MAX || head_dim == 576) return FP8PA_ERR_UNSUPPORTED;
+  DecodePath path;
+  DecodeArgs a;
+  const int st = attention_prepare(q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                   max_blocks_per_seq, seq_lens, batch, 1, block_size, n_q_heads,
+                                   n_kv_heads, head_dim, head_dim, fmt, scale_mode, group_size,
+                                   sm_scale, num_blocks, out, out_dtype, workspace,
+                                   workspace_bytes, static_cast<cudaStream_t>(stream), &path, &a);
+  if (st != FP8PA_OK || batch == 0) return st;
+  const ScoreMods mods{prefix_lens, alibi_slopes, logit_cap, window};
+  return cuda_status(launch_decode_mod(path.shape, a, mods, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp8pa_prefill_workspace_bytes(int total_q, int batch, int n_q_heads, int n_kv_heads,
+                                     int head_dim) {
+  if (prefill_shape(total_q, batch, n_q_heads, n_kv_heads, head_dim) != FP8PA_OK) return 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, dev);
+}
+
+int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int total_q,
+                                  const uint8_t* k_cache, const uint8_t* v_cache,
+                                  const float* k_scale, const float* v_scale,
+                                  const int32_t* block_tables, int max_blocks_per_seq,
+                                  const int32_t* seq_lens, int batch, int block_size,
+                                  int n_q_heads, int n_kv_heads, int head_dim, int fmt,
+                                  int scale_mode, int group_size, float sm_scale, int window,
+                                  const int32_t* prefix_lens, float logit_cap,
+                                  const float* alibi_slopes, int num_blocks, void* out,
+                                  int out_dtype, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  if (window < 0) return FP8PA_ERR_BAD_SHAPE;
+  int st = prefill_shape(total_q, batch, n_q_heads, n_kv_heads, head_dim);
+  if (st != FP8PA_OK) return st;
+  // formats, scale modes, block sizes and pool sizes as the decode's GQA layout
+  st = decode_path(1, 1, n_kv_heads, n_kv_heads, head_dim, head_dim, block_size,
+                   max_blocks_per_seq, fmt, scale_mode, group_size, num_blocks, out_dtype)
+           .status;
+  if (st != FP8PA_OK) return st;
+  if (!(logit_cap >= 0.f) || logit_cap > FLT_MAX) return FP8PA_ERR_UNSUPPORTED;
+  if (batch == 0 || total_q == 0) return FP8PA_OK;
+  if (!q || !q_offsets || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables ||
+      !seq_lens || !out || !workspace)
+    return FP8PA_ERR_NULL_POINTER;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) ||
+      !aligned16(v_scale) || !aligned16(workspace) || !aligned16(out))
+    return FP8PA_ERR_ALIGNMENT;
+  int dev = 0;
+  PrefillArgs a{};
+  a.err = device_error_ptr(static_cast<cudaStream_t>(stream), &dev);
+  if (!a.err) return FP8PA_ERR_CUDA;
+  if (workspace_bytes <
+      prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, dev))
+    return FP8PA_ERR_WORKSPACE;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_offsets = q_offsets;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.prefix_lens = prefix_lens;
+  a.slopes = alibi_slopes;
+  a.cap = logit_cap;
+  a.sm_scale = sm_scale;
+  a.window = window;
+  a.total_q = total_q;
+  a.batch = batch;
+  a.hq = n_q_heads;
+  a.hkv = n_kv_heads;
+  a.G = n_q_heads / n_kv_heads;
+  a.d = head_dim;
+  a.bs = block_size;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.fmt = fmt;
+  a.mode = scale_mode;
+  a.gs = group_size;
+  a.hp = segment_scale_heads(n_kv_heads);
+  a.out_f32 = out_dtype == FP8PA_OUT_F32;
+  a.out = out;
+  a.workspace = workspace;
+  return cuda_status(launch_prefill(a, static_cast<cudaStream_t>(stream)));
 }
 
 int fp8pa_selftest_bounded_wait(long long limit_cycles, void* stream) {

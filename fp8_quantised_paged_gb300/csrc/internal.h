@@ -91,6 +91,29 @@ cudaError_t launch_channel_absmax(const uint16_t* x, int num_tokens, int hd, flo
 cudaError_t launch_scales_from_absmax(const float* amax, int n, int fmt, float* out,
                                       cudaStream_t stream);
 
+// The append with rotary positions (append_rope.cu): a token's rows are its
+// q rows, its K rows, its V rows.
+struct RopeArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* q_out;
+  long long q_stride, q_out_stride, k_stride, v_stride;  // elements per token
+  const int32_t* positions;
+  const int32_t* slot_mapping;
+  const float* cos_sin;  // [max_position][rot_dim]
+  uint8_t* cache[2];
+  float* scale[2];
+  int max_position, rot_dim, rot_offset, interleaved;
+  int num_tokens, hq, hkv, d, gs, num_blocks, bs;
+  int rows;  // hq + hkv (+ hkv with V)
+  uint32_t warps_per_token;
+  FastDiv div_warps;  // by warps_per_token
+  FastDiv div_bs;     // by bs
+  uint32_t* err;
+};
+cudaError_t launch_append_rope(const RopeArgs& a, int fmt, int mode, cudaStream_t stream);
+
 // Workspace layout of the split-K decode, shared by planner, split and merge.
 struct DecodeShape {
   int batch, hq, hkv, d, dv, bs, max_blocks;
@@ -112,6 +135,8 @@ inline int gqa_qw(const DecodeShape& s) {
 }
 
 size_t decode_workspace_bytes(const DecodeShape& s);
+
+struct ScoreMods;  // score_mods.cuh
 
 struct DecodeArgs {
   const uint16_t* q;
@@ -157,6 +182,33 @@ cudaError_t launch_merge(const int* plan, const float* part_ml, const float* par
 cudaError_t launch_decode_gqa(const DecodeShape& s, const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_mla(const DecodeShape& s, const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_mla_tc(const DecodeShape& s, const DecodeArgs& a, cudaStream_t stream);
+// The grouped-query decode with score modifiers (decode_mod.cu); it fits the
+// workspace of the plain decode of the same shape.
+cudaError_t launch_decode_mod(const DecodeShape& s, const DecodeArgs& a, const ScoreMods& mods,
+                              cudaStream_t stream);
+
+// Attention of ragged query chunks (prefill.cu).
+struct PrefillArgs {
+  const uint16_t* q;
+  const int32_t* q_offsets;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* prefix_lens;
+  const float* slopes;
+  float cap, sm_scale;
+  int window;
+  int total_q, batch, hq, hkv, G, d, bs, max_blocks, num_blocks, fmt, mode, gs, hp, out_f32;
+  void* out;
+  void* workspace;
+  uint32_t* err;
+};
+size_t prefill_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, int device);
+cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
+
 // The tensor-core kernel for a causal chunk over the grouped-query layout:
 // FP8 codes, per-token scales, head_dim 128, G x q_len = 16 or 32 columns.
 bool gqa_tc_eligible(int fmt, int mode, int d, int dv, int bs, int hq, int hkv, int qlen);

@@ -27,31 +27,18 @@ __device__ __forceinline__ int warp_incl_scan(int x) {
   return x;
 }
 
-// Run by one whole warp.  `groups` multiplies the units of a request (1: the
-// split kernels cover every head group of a page in one unit).  A planned
-// request b holds the qw queries b*qw .. b*qw + qw - 1 of a causal chunk of
-// qlen (qw = 1: one virtual request per query; qw = qlen: one per real
-// request); its pages are those its last query sees.
-// A unit is `upages` blocks of `bs` tokens (the latent tensor-core kernel
-// works on page pairs).
-__device__ __forceinline__ void plan_warp(const int32_t* seq_lens, int B, int qlen, int qw,
-                                          int groups, int bs, int max_blocks, int workers,
-                                          int* ws, uint32_t* err, int upages = 1) {
+// Run by one whole warp; pages(b) is the number of units of planned request b
+// (one lane per request, b < B).
+template <class Pages>
+__device__ __forceinline__ void plan_warp_pages(int B, int groups, int workers, int* ws,
+                                                Pages pages) {
   const int lane = threadIdx.x & 31;
-  const int cap = max_blocks * bs;
-  const int ut = bs * upages;  // tokens per unit
   int* uprefix = ws + kPlanHeader;
   int* segbase = uprefix + B + 1;
   int carry = 0;
   for (int base = 0; base < B; base += 32) {
     const int b = base + lane;
-    int n = 0;
-    if (b < B) {
-      bool bad;
-      const int L = visible_len(seq_lens, b * qw + qw - 1, qlen, cap, &bad);
-      if (bad) raise_error(err, FP8PA_DEVERR_SEQ_LEN);
-      n = (L + ut - 1) / ut;
-    }
+    const int n = b < B ? pages(b) : 0;
     const int incl = warp_incl_scan(n);
     if (b < B) uprefix[b] = (carry + incl - n) * groups;
     carry += __shfl_sync(0xffffffffu, incl, 31);
@@ -82,6 +69,26 @@ __device__ __forceinline__ void plan_warp(const int32_t* seq_lens, int B, int ql
     carry += __shfl_sync(0xffffffffu, incl, 31);
   }
   if (lane == 0) segbase[E] = carry;
+}
+
+// Run by one whole warp.  `groups` multiplies the units of a request (1: the
+// split kernels cover every head group of a page in one unit).  A planned
+// request b holds the qw queries b*qw .. b*qw + qw - 1 of a causal chunk of
+// qlen (qw = 1: one virtual request per query; qw = qlen: one per real
+// request); its pages are those its last query sees.
+// A unit is `upages` blocks of `bs` tokens (the latent tensor-core kernel
+// works on page pairs).
+__device__ __forceinline__ void plan_warp(const int32_t* seq_lens, int B, int qlen, int qw,
+                                          int groups, int bs, int max_blocks, int workers,
+                                          int* ws, uint32_t* err, int upages = 1) {
+  const int cap = max_blocks * bs;
+  const int ut = bs * upages;  // tokens per unit
+  plan_warp_pages(B, groups, workers, ws, [&](int b) {
+    bool bad;
+    const int L = visible_len(seq_lens, b * qw + qw - 1, qlen, cap, &bad);
+    if (bad) raise_error(err, FP8PA_DEVERR_SEQ_LEN);
+    return (L + ut - 1) / ut;
+  });
 }
 
 }  // namespace fp8pa

@@ -1,0 +1,46 @@
+// score_mods.cuh -- the score modifiers of the decode and prefill calls: a
+// tanh cap, a distance bias, a sliding window and an always-visible prefix.
+#pragma once
+
+#include "common.cuh"
+
+namespace fp8pa {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct ScoreMods {
+  const int32_t* prefix_lens;  // [requests] or NULL
+  const float* slopes;         // [n_q_heads] or NULL
+  float cap;                   // 0: scores are not capped
+  int window;                  // 0: none
+};
+
+// Visible keys of a query at position `pos` of a request of `L` cached
+// tokens: [first, last] and [0, prefix).
+__device__ __forceinline__ int prefix_len(const ScoreMods& m, int b, int L) {
+  return m.prefix_lens ? min(max(__ldg(m.prefix_lens + b), 0), L) : 0;
+}
+__device__ __forceinline__ int window_first(const ScoreMods& m, int pos) {
+  return m.window > 0 ? max(pos - m.window + 1, 0) : 0;
+}
+
+// tanh x to a relative error of about 2^-21, so that cap * tanh(z / cap) is
+// as near to z as fp32 for any cap.  Above 0.55, 1 - 2 / (e^2|x| + 1) loses at
+// most one bit to the subtraction; below, the Taylor series to x^13, whose
+// first dropped term is 1.46e-3 x^14 = 3.4e-7 of x at 0.55.
+__device__ __forceinline__ float tanh_f32(float x) {
+  const float x2 = x * x;
+  float p = 21844.0f / 6081075.0f;
+  p = fmaf(p, x2, -1382.0f / 155925.0f);
+  p = fmaf(p, x2, 62.0f / 2835.0f);
+  p = fmaf(p, x2, -17.0f / 315.0f);
+  p = fmaf(p, x2, 2.0f / 15.0f);
+  p = fmaf(p, x2, -1.0f / 3.0f);
+  const float small = fmaf(p * x2, x, x);
+  const float a = fabsf(x);
+  const float e = ex2(a * (2.0f * kLog2e));
+  const float big = copysignf(1.0f - __fdividef(2.0f, e + 1.0f), x);
+  return a < 0.55f ? small : big;
+}
+
+}  // namespace fp8pa

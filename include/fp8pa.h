@@ -78,6 +78,8 @@ extern "C" {
 #define FP8PA_DEVERR_BLOCK_RANGE 2u  /* decode: block id outside [0, num_blocks) (page masked) */
 #define FP8PA_DEVERR_SEQ_LEN 4u      /* decode: seq_len < 0 or > max_blocks_per_seq*block_size (clamped) */
 #define FP8PA_DEVERR_TIMEOUT 8u      /* decode: a bounded wait on an async copy ran out (work abandoned) */
+#define FP8PA_DEVERR_POSITION 16u    /* append_rope: position outside the table (token skipped) */
+#define FP8PA_DEVERR_Q_OFFSETS 32u   /* prefill: query offsets not increasing within [0, total_q] (request skipped) */
 
 /* Code formats: FP8 E4M3 and E5M2, and symmetric INT8 (the alternate KV
  * codec; FMAX = 127, integer codes in [-127, 127] stored as the byte
@@ -346,6 +348,135 @@ int fp8pa_decode_step(const void* k_new, const void* v_new, const int32_t* slot_
                       int head_dim_v, int fmt, int scale_mode, int group_size, float sm_scale,
                       int num_blocks, void* out, int out_dtype, void* workspace,
                       size_t workspace_bytes, void* stream);
+
+/*
+ * Append with rotary positions: every query and key row is turned by its
+ * token's angles, then K and V are quantised and scattered as by
+ * fp8pa_kv_append_quant.  The pages' models rotate q and k before the cache
+ * (the latent layout keeps 64 rope dims, "DeepSeek V4 950",
+ * 2kiu.com/news/4508674, sec. 2.2); doing it here saves the rotated rows'
+ * trip through memory.
+ *
+ * A pair (a, b) of a row's dims at angle (c, s) becomes
+ *   (a c - b s, b c + a s)
+ * in fp32, every product and sum rounded on its own (no fused multiply-add),
+ * so that the result is the same wherever it is computed.  The rotated K row
+ * is quantised from fp32 (IEEE fp32 division by its scale, as V); the rotated
+ * q row is rounded once, to bf16.
+ *
+ * q, q_out      bf16 [num_tokens][n_q_heads][head_dim], q_out may be q (in
+ *               place); both NULL for an append without queries (n_q_heads is
+ *               then ignored).
+ * k, v          bf16 [num_tokens][n_kv_heads][head_dim]; v may be NULL.
+ * q_stride, q_out_stride, k_stride, v_stride  elements from one token's rows
+ *               to the next token's (at least heads * head_dim and a multiple
+ *               of 8): q, k and v may be slices of one fused projection.
+ * positions     i32 [num_tokens].
+ * cos_sin       f32 [max_position][rot_dim]: the rot_dim / 2 cosines of a
+ *               position, then its rot_dim / 2 sines.
+ * rot_dim, rot_offset  dims [rot_offset, rot_offset + rot_dim) of every q and
+ *               k row are turned, the others pass unchanged.
+ * interleaved   0: dim i of the first half of the range pairs with dim i of
+ *               the second half; 1: neighbours (2i, 2i + 1) pair.
+ * slot_mapping  as fp8pa_kv_append_quant; a negative slot leaves the cache
+ *               alone and still turns q.
+ * A token whose position is outside [0, max_position) is skipped whole (its
+ * q_out rows are left as they were) and sets FP8PA_DEVERR_POSITION, unless
+ * its slot is negative too: that is padding, skipped without an error.
+ * Requirements  those of fp8pa_kv_append_quant (every scale mode but
+ *               SEGMENT), rot_dim a positive multiple of 16, rot_offset a
+ *               multiple of 8, the range inside head_dim and, where head_dim
+ *               exceeds 256, inside one aligned span of 256 dims; 16-byte
+ *               aligned q, q_out and cos_sin.
+ */
+int fp8pa_kv_append_rope(const void* q, void* q_out, const void* k, const void* v,
+                         long long q_stride, long long q_out_stride, long long k_stride,
+                         long long v_stride, const int32_t* positions, const float* cos_sin,
+                         int max_position, int rot_dim, int rot_offset, int interleaved,
+                         const int32_t* slot_mapping, int num_tokens, int n_q_heads,
+                         int n_kv_heads, int head_dim, int fmt, int scale_mode, int group_size,
+                         uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale,
+                         int num_blocks, int block_size, void* stream);
+
+/*
+ * Score modifiers, shared by the two calls below.  For the query at position
+ * i of its request and the cached token at position j < seq_len, with
+ * z = sm_scale * q . k^_j:
+ *   logit_cap > 0   z = logit_cap * tanh(z / logit_cap)       (0: no cap)
+ *   alibi_slopes    z = z - alibi_slopes[h] * |i - j|         (NULL: none;
+ *                   f32 [n_q_heads], device)
+ *   j is visible if  j <= i and (window == 0 or i - j < window),
+ *   or j < prefix_lens[request]      (NULL: no prefix; i32 [batch], device).
+ * The prefix is visible to every query, also those before its end: a
+ * bidirectional prefix in a prefill, tokens kept ahead of a sliding window in
+ * a decode step.  Values outside [0, seq_len] are taken as the nearer end.
+ * A row that sees no token is zero.  What a masked token's codes and scales
+ * hold (infinities and NaN among it) does not reach the output.
+ */
+
+/*
+ * fp8pa_paged_decode_attention of the GQA layout with score modifiers: one
+ * query per request, at position seq_lens[b] - 1.  Pages that hold no visible
+ * token are not read.  Workspace: fp8pa_decode_workspace_bytes.
+ * The other arguments, limits and errors are those of
+ * fp8pa_paged_decode_attention with head_dim_v = head_dim; a negative window
+ * is FP8PA_ERR_BAD_SHAPE, a cap that is negative, infinite or NaN
+ * FP8PA_ERR_UNSUPPORTED, and so is the MLA layout.
+ */
+int fp8pa_paged_decode_attention_mod(const void* q, const uint8_t* k_cache,
+                                     const uint8_t* v_cache, const float* k_scale,
+                                     const float* v_scale, const int32_t* block_tables,
+                                     int max_blocks_per_seq, const int32_t* seq_lens, int batch,
+                                     int block_size, int n_q_heads, int n_kv_heads, int head_dim,
+                                     int fmt, int scale_mode, int group_size, float sm_scale,
+                                     int window, const int32_t* prefix_lens, float logit_cap,
+                                     const float* alibi_slopes, int num_blocks, void* out,
+                                     int out_dtype, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
+ * Attention of ragged query chunks of any length over the paged cache, causal
+ * with score modifiers: the chunk of each request was appended first, so
+ * query i of request b's n = q_offsets[b+1] - q_offsets[b] is at position
+ * seq_lens[b] - n + i.  Serves whole prompts and the chunks of chunked
+ * prefill ("Llama 3 70B FP8 deployment", dpshk.com/news/5605006, sec. 2.1 and
+ * 3.3), with the softmax in FP32 ("DeepSeek V4 950", 2kiu.com/news/4508674,
+ * sec. 2.3) over blocks of the context ("DeepSeek-V4.1 512K",
+ * hotelren.com/news/5711065, sec. 2.2).
+ *
+ * q            bf16 [total_q][n_q_heads][head_dim], the requests' chunks one
+ *              after the other.
+ * q_offsets    i32 [batch + 1] (device).  Rows outside every request's range
+ *              are not written.  Offsets that decrease or leave [0, total_q]
+ *              set FP8PA_DEVERR_Q_OFFSETS and skip that request.
+ * seq_lens     i32 [batch], the cached length including the chunk.  A request
+ *              shorter than its chunk (or outside [0, cap]) sets
+ *              FP8PA_DEVERR_SEQ_LEN.
+ * head_dim     64 or 128; n_q_heads a multiple of n_kv_heads; block_size 16,
+ *              32 or 64; scale_mode TOKEN_HEAD, CHANNEL_STATIC, MX_BLOCK or
+ *              SEGMENT; every code format (MX_BLOCK: FP8).
+ * out          [total_q][n_q_heads][head_dim], bf16 or f32.
+ * workspace    at least fp8pa_prefill_workspace_bytes(), 16-byte aligned; no
+ *              initialisation; calls that share it must be stream-ordered.
+ */
+int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int total_q,
+                                  const uint8_t* k_cache, const uint8_t* v_cache,
+                                  const float* k_scale, const float* v_scale,
+                                  const int32_t* block_tables, int max_blocks_per_seq,
+                                  const int32_t* seq_lens, int batch, int block_size,
+                                  int n_q_heads, int n_kv_heads, int head_dim, int fmt,
+                                  int scale_mode, int group_size, float sm_scale, int window,
+                                  const int32_t* prefix_lens, float logit_cap,
+                                  const float* alibi_slopes, int num_blocks, void* out,
+                                  int out_dtype, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
+ * Bytes of device workspace fp8pa_paged_prefill_attention needs for these
+ * sizes on the current device; 0 if they are rejected.
+ */
+size_t fp8pa_prefill_workspace_bytes(int total_q, int batch, int n_q_heads, int n_kv_heads,
+                                     int head_dim);
 
 /*
  * Size of the scratch array built into the library for
