@@ -732,6 +732,12 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
            .status;
   if (st != FP8PA_OK) return st;
   if (!(logit_cap >= 0.f) || logit_cap > FLT_MAX) return FP8PA_ERR_UNSUPPORTED;
+  // the planner counts (256-row block, KV head, 128-token tile) units in 32 bits
+  const long long blocks =
+      static_cast<long long>(total_q) * (n_q_heads / n_kv_heads) / 256 + 1 + batch;
+  if (blocks * n_kv_heads * (static_cast<long long>(max_blocks_per_seq) * block_size / 128 + 1) >=
+      (1ll << 31))
+    return FP8PA_ERR_UNSUPPORTED;
   if (batch == 0 || total_q == 0) return FP8PA_OK;
   if (!q || !q_offsets || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables ||
       !seq_lens || !out || !workspace)

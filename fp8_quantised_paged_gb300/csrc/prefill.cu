@@ -1,204 +1,1061 @@
 // prefill.cu -- attention of ragged query chunks over the paged cache, causal
-// with score modifiers.
+// with score modifiers, on the fifth-generation tensor cores.
 //
 //   z_j = sm_scale q_i . k^_j;  z_j = cap tanh(z_j / cap);  z_j -= slope |i - j|
 //   out_i = sum_j softmax(z)_j v^_j over j < prefix or i - window < j <= i
 //
-// One warp per (query, head) walks its visible tokens 32 at a time: a lane
-// scores one token, then the lanes share the dims of the weighted sum.  FP32
-// throughout, online softmax in the log2 domain.
+// Rows.  The G heads that share a KV head see the same keys, so the (query,
+// head) pairs of one request and KV head are flattened into rows r = query * G
+// + head; a CTA takes a block of 256 rows as two tiles of M = 128, one TMEM
+// lane per row, and walks the 128-token tiles of its visible context:
+//   S_t = Q_t K^T (A, B in shared memory), P_t = softmax part (TMEM -> registers
+//   -> TMEM), O_t += P_t V (A = P_t in TMEM, B in shared memory).
+// Each K or V code is read and converted once for 256 rows.
+//
+// Work is the flat list of (row block, KV head, token tile) units.  A planner
+// kernel counts the tiles that each row block can see and cuts the list into
+// one contiguous range per SM; where a cut falls inside an item (it is moved
+// to an item's edge when that is a few tiles away) the pieces leave partial
+// results that a merge kernel folds with the log-sum-exp rule.  A long chunk
+// and a few rows over a long context are balanced alike.
+//
+// Numerics.  Codes become f16 exactly (E4M3 scaled by 2^-8).  q is exact in
+// f16 after a power-of-two normaliser per row (CHANNEL_STATIC folds the K
+// scales into it and rounds once, 2^-11).  K scales multiply the fp32 scores;
+// V scales go into P, which enters the second product as f16 (2^-11).  The
+// running reference of a row is a bound of max(z + log2 v_scale), so P stays
+// inside f16 whatever the scales; it moves only when passed by 2^kTau, which
+// is exact, as sums and O carry the same reference.
+//
+// Roles (13 warps): 0-3 and 4-7 softmax of row tiles 0 and 1 (a thread per
+// row), 8-11 convert codes into shared memory, 12 issues the MMAs.  While the
+// tensor cores work on one row tile, the other's softmax runs.  Every wait is
+// bounded.
 #include <float.h>
 
 #include "common.cuh"
 #include "internal.h"
 #include "score_mods.cuh"
+#include "tc.cuh"
 
 namespace fp8pa {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kRows = 256;   // rows of a block: two tiles of 128
+constexpr int kT = 128;      // tokens per tile
+constexpr int kThreads = 13 * 32;
+constexpr int kSnap = 4;     // a cut this near an item's edge moves to it
+constexpr float kShift = 12.f;  // P = 2^(z - ref + 12): at most 2^15 with the lazy bound
+constexpr float kTau = 3.f;     // the reference may lag by 2^3
+constexpr float kNegBig = -1e30f;
 
-template <int FMT>
-__device__ __forceinline__ void codes4_to_f32(uint32_t w, float (&f)[4]) {
-  uint32_t lo, hi;
-  codes4_to_f16x2x2<FMT>(w, lo, hi);
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  f[0] = a.x;
-  f[1] = a.y;
-  f[2] = b.x;
-  f[3] = b.y;
+// ---------------------------------------------------------------- plan
+// Workspace: header, block prefix of the requests, then per row block its
+// request and the prefix of its tiles, then the ranges' first units, then the
+// partial pieces.
+struct PlanView {
+  int* head;     // [0] units, [1] units per range (before cuts move)
+  int* rbase;    // [batch + 1] first row block of a request
+  int* rb_b;     // [blocks] request of a row block
+  int* rb_pre;   // [blocks + 1] tiles before a row block (of one KV head)
+  int* start;    // [ranges + 1] first unit of a range
+  int* item;     // [ranges + 1] the item that holds it
+  float2* ml;    // [2 * ranges][kRows] reference and sum of a piece
+  float* o;      // [2 * ranges][kRows][d]
+  int blocks;    // bound of the row blocks
+};
+
+__host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+inline int block_bound(int total_q, int batch, int G) {
+  return static_cast<int>((static_cast<long long>(total_q) * G + kRows - 1) / kRows) + batch;
 }
 
-// Scale of dim d of cached row `row` = (block * hkv + kvh) * bs + offset.
-__device__ __forceinline__ float row_scale(const PrefillArgs& a, const float* sc, long row,
-                                           long blk, int kvh, int d) {
-  switch (a.mode) {
-    case FP8PA_SCALE_TOKEN_HEAD: return __ldg(sc + row);
-    case FP8PA_SCALE_CHANNEL_STATIC: return __ldg(sc + kvh * a.d + d);
-    case FP8PA_SCALE_SEGMENT: return __ldg(sc + blk * a.hp + kvh);
-    default: {
-      const int e = __ldg(reinterpret_cast<const uint8_t*>(sc) + row * (a.d / a.gs) + d / a.gs);
-      return e == 0 ? __int_as_float(1 << 22) : __int_as_float(e << 23);
-    }
+inline size_t plan_layout(char* ws, int total_q, int batch, int G, int d, int ranges,
+                          PlanView* v) {
+  const int nb = block_bound(total_q, batch, G);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* p = ws + at;
+    at += align256(bytes);
+    return p;
+  };
+  PlanView t;
+  t.head = reinterpret_cast<int*>(take(16));
+  t.rbase = reinterpret_cast<int*>(take(sizeof(int) * (batch + 1)));
+  t.rb_b = reinterpret_cast<int*>(take(sizeof(int) * nb));
+  t.rb_pre = reinterpret_cast<int*>(take(sizeof(int) * (nb + 1)));
+  t.start = reinterpret_cast<int*>(take(sizeof(int) * (ranges + 1)));
+  t.item = reinterpret_cast<int*>(take(sizeof(int) * (ranges + 1)));
+  t.ml = reinterpret_cast<float2*>(take(sizeof(float2) * 2 * ranges * kRows));
+  t.o = reinterpret_cast<float*>(take(sizeof(float) * 2 * ranges * kRows * d));
+  t.blocks = nb;
+  if (v) *v = t;
+  return at;
+}
+
+// A request's chunk and its visible extent.
+struct Chunk {
+  int qlo, n, L, pre;
+};
+__device__ __forceinline__ Chunk load_chunk(const PrefillArgs& a, int b, bool* bad_off,
+                                            bool* bad_len) {
+  Chunk c;
+  const int lo = __ldg(a.q_offsets + b), hi = __ldg(a.q_offsets + b + 1);
+  *bad_off = lo < 0 || hi < lo || hi > a.total_q;
+  c.qlo = lo;
+  c.n = *bad_off ? 0 : hi - lo;
+  const int cap = a.max_blocks * a.bs;
+  const int L = __ldg(a.seq_lens + b);
+  *bad_len = L < 0 || L > cap || L < c.n;
+  c.L = min(max(L, 0), cap);
+  const ScoreMods m{a.prefix_lens, nullptr, 0.f, a.window};
+  c.pre = prefix_len(m, b, c.L);
+  return c;
+}
+
+// The token tiles of row block t of a chunk: tiles [0, np) of the prefix, then
+// from tile np + skip on; `count` in all (at least one, so that rows that see
+// nothing are written).
+struct Tiles {
+  int np, skip, count;
+};
+__device__ __forceinline__ Tiles block_tiles(const Chunk& c, int window, int G, int t) {
+  const int q0 = t * kRows / G, q1 = min((t * kRows + kRows - 1) / G, c.n - 1);
+  const int p0 = c.L - c.n + q0, p1 = c.L - c.n + q1;
+  const int wf = window > 0 ? max(p0 - window + 1, 0) : 0;
+  Tiles r;
+  r.np = (c.pre + kT - 1) / kT;
+  r.skip = max(wf / kT - r.np, 0);
+  const int last = (max(max(p1 + 1, c.pre), 0) + kT - 1) / kT;
+  r.count = max(last - r.skip, 1);
+  return r;
+}
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive scan of one int per thread over the CTA; returns the total.
+__device__ __forceinline__ int block_scan(int x, int* excl, int* s_warp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int v = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
   }
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += t;
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  *excl = v - x + (warp ? s_warp[warp - 1] : 0);
+  const int total = s_warp[kPlanThreads / 32 - 1];
+  __syncthreads();
+  return total;
 }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(kWarps * 32) prefill_kernel(const PrefillArgs a) {
-  __shared__ float s_q[kWarps][D];
+// Largest i in [0, n) with a[i] <= x (a nondecreasing, a[0] <= x).
+__device__ __forceinline__ int last_le(const int* a, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PrefillArgs a,
+                                                                    const PlanView v, int ranges) {
+  __shared__ int s_warp[kPlanThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long row = static_cast<long>(blockIdx.x) * kWarps + warp;
-  if (row >= static_cast<long>(a.total_q) * a.hq) return;
-  const int t = static_cast<int>(row / a.hq), h = static_cast<int>(row % a.hq);
-  const int kvh = h / a.G;
-  // the request whose chunk holds row t
-  int b = -1, qlo = 0, qn = 0;
-  for (int base = 0; base < a.batch && b < 0; base += 32) {
-    const int k = base + lane;
-    bool in = false;
-    if (k < a.batch) {
-      const int lo = __ldg(a.q_offsets + k), hi = __ldg(a.q_offsets + k + 1);
-      if (lo < 0 || hi < lo || hi > a.total_q) {
-        if (row == 0) raise_error(a.err, FP8PA_DEVERR_Q_OFFSETS);
-      } else {
-        in = lo <= t && t < hi;
+  const int tid = threadIdx.x;
+  int carry = 0;
+  for (int base = 0; base < a.batch; base += kPlanThreads) {
+    const int b = base + tid;
+    int n = 0;
+    if (b < a.batch) {
+      bool bo, bl;
+      const Chunk c = load_chunk(a, b, &bo, &bl);
+      if (bo) raise_error(a.err, FP8PA_DEVERR_Q_OFFSETS);
+      if (bl) raise_error(a.err, FP8PA_DEVERR_SEQ_LEN);
+      // overlapping or repeated offsets cannot add blocks beyond the bound
+      n = static_cast<int>((static_cast<long long>(c.n) * a.G + kRows - 1) / kRows);
+    }
+    int ex;
+    const int total = block_scan(n, &ex, s_warp);
+    if (b < a.batch) v.rbase[b] = min(carry + ex, v.blocks);
+    carry = min(carry + total, v.blocks);
+  }
+  if (tid == 0) v.rbase[a.batch] = carry;
+  __syncthreads();
+  const int blocks = carry;
+  carry = 0;
+  for (int base = 0; base < blocks; base += kPlanThreads) {
+    const int i = base + tid;
+    int n = 0;
+    if (i < blocks) {
+      const int b = last_le(v.rbase, a.batch, i);
+      bool bo, bl;
+      const Chunk c = load_chunk(a, b, &bo, &bl);
+      n = block_tiles(c, a.window, a.G, i - v.rbase[b]).count;
+      v.rb_b[i] = b;
+    }
+    int ex;
+    const int total = block_scan(n, &ex, s_warp);
+    if (i < blocks) v.rb_pre[i] = carry + ex;
+    carry += total;
+  }
+  if (tid == 0) v.rb_pre[blocks] = carry;
+  __syncthreads();
+  const int U = carry * a.hkv;
+  const int upw = max(1, (U + ranges - 1) / ranges);
+  if (tid == 0) {
+    v.head[0] = U;
+    v.head[1] = upw;
+  }
+  for (int w = tid; w <= ranges; w += kPlanThreads) {
+    const long long want = static_cast<long long>(w) * upw;
+    int u = want < U ? static_cast<int>(want) : U, it = blocks * a.hkv;
+    if (u < U) {
+      const int rb = last_le(v.rb_pre, blocks, u / a.hkv);
+      const int pre = v.rb_pre[rb], c = v.rb_pre[rb + 1] - pre;
+      const int h = (u - pre * a.hkv) / c, f = pre * a.hkv + h * c;
+      it = rb * a.hkv + h;
+      if (u - f < kSnap) {
+        u = f;
+      } else if (f + c - u < kSnap) {
+        u = f + c;
+        ++it;
       }
     }
-    const unsigned m = __ballot_sync(0xffffffffu, in);
-    if (m) {
-      b = base + __ffs(m) - 1;
-      qlo = __ldg(a.q_offsets + b);
-      qn = __ldg(a.q_offsets + b + 1) - qlo;
-    }
-  }
-  if (b < 0) return;
-  const int cap = a.max_blocks * a.bs;
-  int L = __ldg(a.seq_lens + b);
-  if ((L < 0 || L > cap || L < qn) && lane == 0) raise_error(a.err, FP8PA_DEVERR_SEQ_LEN);
-  L = min(max(L, 0), cap);
-  const ScoreMods mods{a.prefix_lens, a.slopes, a.cap, a.window};
-  const int pos = L - qn + (t - qlo);
-  const int wf = window_first(mods, pos), pre = prefix_len(mods, b, L);
-  const int last = max(pos + 1, pre);  // keys [0, last) hold every visible one
-  const float slope = a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
-
-  for (int d = lane; d < D; d += 32) {
-    float x = __uint_as_float(static_cast<uint32_t>(a.q[row * D + d]) << 16);
-    if (a.mode == FP8PA_SCALE_CHANNEL_STATIC) x *= __ldg(a.k_scale + kvh * D + d);
-    s_q[warp][d] = x;
-  }
-  __syncwarp();
-  constexpr int PER = D / 32;
-  float m = -FLT_MAX, l = 0.f, o[PER];
-#pragma unroll
-  for (int e = 0; e < PER; ++e) o[e] = 0.f;
-
-  for (int j0 = 0; j0 < last; j0 += 32) {
-    const int j = j0 + lane;
-    bool vis = (j <= pos && j >= wf) || j < pre;
-    if (!__any_sync(0xffffffffu, vis)) continue;
-    long krow = 0, blk = 0;
-    if (vis) {
-      blk = __ldg(a.block_tables + static_cast<long>(b) * a.max_blocks + j / a.bs);
-      if (blk < 0 || blk >= a.num_blocks) {
-        raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
-        vis = false;
-      } else {
-        krow = (blk * a.hkv + kvh) * a.bs + j % a.bs;
-      }
-    }
-    float z = __int_as_float(0xff800000);
-    if (vis) {
-      float acc = 0.f;
-      const uint4* src = reinterpret_cast<const uint4*>(a.k_cache + krow * D);
-      for (int c = 0; c < D / 16; ++c) {
-        const uint4 u = __ldg(src + c);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        float part = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float f[4];
-          codes4_to_f32<FMT>(w[i], f);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) part = fmaf(f[e], s_q[warp][c * 16 + 4 * i + e], part);
-        }
-        if (a.mode == FP8PA_SCALE_MX_BLOCK) part *= row_scale(a, a.k_scale, krow, blk, kvh, c * 16);
-        acc += part;
-      }
-      if (a.mode == FP8PA_SCALE_TOKEN_HEAD || a.mode == FP8PA_SCALE_SEGMENT)
-        acc *= row_scale(a, a.k_scale, krow, blk, kvh, 0);
-      z = acc * a.sm_scale;
-      if (a.cap > 0.f) z = a.cap * tanh_f32(z / a.cap);
-      z = fmaf(-slope, fabsf(static_cast<float>(pos - j)), z * kLog2e);
-    }
-    float mx = z;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-    const float mn = fmaxf(m, mx);
-    const float al = ex2(m - mn);
-    const float p = vis ? ex2(z - mn) : 0.f;
-    float sum = p;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-    l = l * al + sum;
-    m = mn;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] *= al;
-    const unsigned seen = __ballot_sync(0xffffffffu, vis);
-    for (unsigned rest = seen; rest; rest &= rest - 1) {
-      const int k = __ffs(rest) - 1;
-      const float pk = __shfl_sync(0xffffffffu, p, k);
-      const long r = __shfl_sync(0xffffffffu, krow, k), bk = __shfl_sync(0xffffffffu, blk, k);
-      float f[4];
-      const uint8_t* src = a.v_cache + r * D + lane * PER;
-      const uint32_t w = PER == 4 ? __ldg(reinterpret_cast<const uint32_t*>(src))
-                                  : __ldg(reinterpret_cast<const uint16_t*>(src));
-      codes4_to_f32<FMT>(w, f);
-#pragma unroll
-      for (int e = 0; e < PER; ++e)
-        o[e] = fmaf(pk * row_scale(a, a.v_scale, r, bk, kvh, lane * PER + e), f[e], o[e]);
-    }
-  }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll
-  for (int e = 0; e < PER; ++e) {
-    const float v = o[e] * inv;
-    const long at = row * D + lane * PER + e;
-    if (a.out_f32)
-      reinterpret_cast<float*>(a.out)[at] = v;
-    else
-      reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+    v.start[w] = u;
+    v.item[w] = it;
   }
 }
 
+// ---------------------------------------------------------------- shared memory
 template <int D>
-auto pick_prefill(int fmt) {
-  return fmt == FP8PA_E4M3   ? prefill_kernel<D, FP8PA_E4M3>
-         : fmt == FP8PA_E5M2 ? prefill_kernel<D, FP8PA_E5M2>
-                             : prefill_kernel<D, FP8PA_INT8>;
+struct Smem {
+  static constexpr int kTile = kT * D * 2;  // a 128-row f16 tile
+  static constexpr int kQ = 0;              // two row tiles
+  static constexpr int kK = 2 * kTile;      // two stages
+  static constexpr int kV = 4 * kTile;      // two stages
+  static constexpr int kScale = 6 * kTile;  // four stages of [K scales][V scales] f32
+  static constexpr int kInfo = kScale + 4 * 2 * kT * 4;  // four stages of StageInfo
+  static constexpr int kBars = kInfo + 4 * 64;
+  static constexpr int kBytes = kBars + 256;
+};
+struct StageInfo {
+  uint32_t valid[4];  // tokens whose page exists
+  float vmax[4];      // largest V scale of each 32 tokens
+};
+
+// Barriers: one arrival per warp of a group of four on the first twelve, one
+// commit of the tensor cores on the others.
+enum { kBarQ = 0, kBarScale = 2, kBarKFull = 6, kBarVFull = 8, kBarP = 10, kBarKFree = 12,
+       kBarVFree = 14, kBarS = 16, kBarO = 18, kBarDrain = 20, kNumBars = 21 };
+
+// ---------------------------------------------------------------- conversions
+// 16 codes -> 16 f16 (two 16-byte core-matrix rows), exactly; E4M3 values come
+// out times 2^-8, with the bits only moved.
+template <int FMT>
+__device__ __forceinline__ void codes16_to_f16(const uint4& c, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (FMT == FP8PA_INT8) {
+      r[2 * i] = int8x2_to_f16x2(w[i], 0x5140u);
+      r[2 * i + 1] = int8x2_to_f16x2(w[i], 0x5342u);
+    } else {
+      const uint32_t a = prmt(w[i], 0u, 0x1404u), b = prmt(w[i], 0u, 0x3424u);
+      if constexpr (FMT == FP8PA_E5M2) {
+        r[2 * i] = a;
+        r[2 * i + 1] = b;
+      } else {
+        r[2 * i] = (a & 0x80008000u) | ((a >> 1) & 0x3F803F80u);
+        r[2 * i + 1] = (b & 0x80008000u) | ((b >> 1) & 0x3F803F80u);
+      }
+    }
+  }
+  lo = make_uint4(r[0], r[1], r[2], r[3]);
+  hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+template <int FMT>
+__host__ __device__ constexpr float code_unit() {  // what codes16_to_f16 leaves out
+  return FMT == FP8PA_E4M3 ? 256.f : 1.f;
+}
+
+// Whether any of 16 codes is an infinity or a NaN.
+template <int FMT>
+__device__ __forceinline__ bool codes_nonfinite(const uint4& c) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (FMT == FP8PA_E4M3) bad |= __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    if constexpr (FMT == FP8PA_E5M2) bad |= __vcmpeq4(w[i] & 0x7C7C7C7Cu, 0x7C7C7C7Cu);
+  }
+  return bad != 0;
+}
+
+__device__ __forceinline__ uint4 hmul8(const uint4& a, uint32_t f) {
+  auto m = [&](uint32_t x) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x),
+                              *reinterpret_cast<const __half2*>(&f));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  };
+  return make_uint4(m(a.x), m(a.y), m(a.z), m(a.w));
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], one thread.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                              bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+// Bits t of a 32-token word at token t0 with lo <= t0 + t < hi.
+__device__ __forceinline__ uint32_t word_bits(int t0, int lo, int hi) {
+  const int a = min(max(lo - t0, 0), 32), b = min(max(hi - t0, 0), 32);
+  const uint32_t below_b = b == 32 ? 0xFFFFFFFFu : (1u << b) - 1u;
+  const uint32_t below_a = a == 32 ? 0xFFFFFFFFu : (1u << a) - 1u;
+  return below_b & ~below_a;
+}
+
+// One item of a CTA's range: a row block of a request for one KV head, tiles
+// [t0, t1) of its list.
+struct Item {
+  int b, kvh, row0, rows;  // first row within the request, rows of the block
+  Chunk c;
+  Tiles tl;
+  int t0, t1;
+};
+
+__device__ __forceinline__ Item load_item(const PrefillArgs& a, const PlanView& v, int it, int u,
+                                          int u1) {
+  Item r;
+  const int rb = it / a.hkv;
+  r.kvh = it - rb * a.hkv;
+  r.b = v.rb_b[rb];
+  const int pre = v.rb_pre[rb], cnt = v.rb_pre[rb + 1] - pre;
+  const int f = pre * a.hkv + r.kvh * cnt;
+  bool x, y;
+  r.c = load_chunk(a, r.b, &x, &y);
+  const int t = rb - v.rbase[r.b];
+  r.row0 = t * kRows;
+  r.rows = min(kRows, r.c.n * a.G - r.row0);
+  r.tl = block_tiles(r.c, a.window, a.G, t);
+  r.t0 = u - f;
+  r.t1 = min(r.tl.count, u1 - f);
+  return r;
+}
+
+__device__ __forceinline__ int tile_token(const Item& it, int k) {
+  return (k < it.tl.np ? k : k + it.tl.skip) * kT;
+}
+
+// ---------------------------------------------------------------- kernel
+// VAR: 0 no score modifier but the masks, 1 distance bias, 2 capped scores
+// (with or without a bias).
+template <int D, int FMT, int VAR>
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs a,
+                                                              const PlanView pv) {
+  using SM = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
+  float* scales = reinterpret_cast<float*>(sm + SM::kScale);
+  StageInfo* infos = reinterpret_cast<StageInfo*>(sm + SM::kInfo);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  griddep_wait();
+  griddep_launch_dependents();
+  const int u0 = pv.start[blockIdx.x], u1 = pv.start[blockIdx.x + 1];
+  if (u0 >= u1) return;
+  const int it0 = pv.item[blockIdx.x];
+
+  if (warp == 12) tmem_alloc(&s_tmem, 512);
+  if (tid == 0) {
+    s_abort = 0;
+    for (int i = 0; i < kNumBars; ++i) {
+      mbar_init(bars + i, i < kBarKFree ? 4 : 1);
+    }
+    fence_barrier_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_relinquish();
+  const uint32_t tmem = s_tmem;
+  int* abort_flag = &s_abort;
+  auto wait = [&](int bar, uint32_t parity) {
+    return tc_wait(bars + bar, parity, abort_flag, a.err);
+  };
+  // a wait of a whole warp: one answer for all lanes
+  auto wait_warp = [&](int bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, tc_wait(bars + bar, parity, abort_flag, a.err)) != 0;
+  };
+
+  if (warp == 12) {
+    // ================================================= MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc_s = tc_idesc(0, 0, 0, 0, 128, kT);  // f16, both K-major
+      const uint32_t idesc_o = tc_idesc(0, 0, 0, 1, 128, D);   // A in TMEM, B MN-major
+      const uint32_t base = smem_u32(sm);
+      const uint64_t dq[2] = {tc_desc(base + SM::kQ, 2048, 128, 0),
+                              tc_desc(base + SM::kQ + SM::kTile, 2048, 128, 0)};
+      const uint64_t dk[2] = {tc_desc(base + SM::kK, 2048, 128, 0),
+                              tc_desc(base + SM::kK + SM::kTile, 2048, 128, 0)};
+      const uint64_t dv[2] = {tc_desc(base + SM::kV, D * 16, 128, 0),
+                              tc_desc(base + SM::kV + SM::kTile, D * 16, 128, 0)};
+      auto mma_s = [&](int t, int st) {  // S_t = Q_t K^T
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma_f16(tmem + t * kT, dq[t] + k * (4096 >> 4), dk[st] + k * (4096 >> 4), idesc_s,
+                     k > 0);
+      };
+      auto mma_o = [&](int t, int st, bool first) {  // O_t += P_t V
+#pragma unroll
+        for (int k = 0; k < kT / 16; ++k)
+          tc_mma_f16_ts(tmem + 256 + t * 128, tmem + t * kT + k * 8,
+                        dv[st] + k * (2 * D * 16 >> 4), idesc_o, !(first && k == 0));
+      };
+      uint32_t g = 0;     // tiles done by this CTA
+      uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;  // Q and P tiles consumed
+      bool ok = true;
+      for (int it = it0, u = u0; u < u1 && ok; ++it) {
+        const Item im = load_item(a, pv, it, u, u1);
+        const int n = im.t1 - im.t0;
+        u += n;
+        const bool two = im.rows > 128;
+        ok = wait(kBarQ, nq0 & 1) && (!two || wait(kBarQ + 1, nq1 & 1)) &&
+             wait(kBarKFull + (g & 1), (g >> 1) & 1);
+        if (!ok) break;
+        ++nq0;
+        nq1 += two ? 1 : 0;
+        tc_fence_after();
+        mma_s(0, g & 1);
+        tc_commit(bars + kBarS);
+        if (two) {
+          mma_s(1, g & 1);
+          tc_commit(bars + kBarS + 1);
+        }
+        tc_commit(bars + kBarKFree + (g & 1));
+        for (int k = 0; k < n && ok; ++k, ++g) {
+          const uint32_t g1 = g + 1;
+          const bool more = k + 1 < n;
+          if (more) ok = wait(kBarKFull + (g1 & 1), (g1 >> 1) & 1);
+          ok = ok && wait(kBarVFull + (g & 1), (g >> 1) & 1) && wait(kBarP, np0 & 1);
+          if (!ok) break;
+          ++np0;
+          tc_fence_after();
+          mma_o(0, g & 1, k == 0);
+          if (!two) tc_commit(bars + kBarVFree + (g & 1));
+          if (more) {
+            mma_s(0, g1 & 1);
+            tc_commit(bars + kBarS);
+          } else {
+            tc_commit(bars + kBarO);
+          }
+          if (two) {
+            if (!(ok = wait(kBarP + 1, np1 & 1))) break;
+            ++np1;
+            tc_fence_after();
+            mma_o(1, g & 1, k == 0);
+            tc_commit(bars + kBarVFree + (g & 1));
+            if (more) {
+              mma_s(1, g1 & 1);
+              tc_commit(bars + kBarS + 1);
+            } else {
+              tc_commit(bars + kBarO + 1);
+            }
+          }
+          if (more) tc_commit(bars + kBarKFree + (g1 & 1));
+        }
+      }
+    }
+  } else if (warp >= 8) {
+    // ================================================= converting warps
+    const int dw = warp - 8, r8 = lane & 7, c4 = lane >> 3;
+    constexpr int H = D / 64;  // 16-byte chunks of a row per lane
+    const int nbx = a.mode == FP8PA_SCALE_MX_BLOCK ? D / a.gs : 0;
+    uint4 kb[4][H], vb[4][H];
+    long row[4];       // code rows of the lane's four tokens (8-token groups)
+    uint32_t okm = 0;  // ... whose page exists and whose token is cached
+    float ksc, vsc;    // scales of token dw * 32 + lane
+    bool sok;
+
+    // The tokens that some row of the item sees: [lo, hi) and [0, c.pre).
+    // Others are neither looked up nor read.
+    int lo = 0, hi = 0;
+    // Addresses and codes of one tile.
+    auto locate = [&](const Item& im, int j0, long (&r)[4], uint32_t& m) {
+      m = 0;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int j = j0 + dw * 32 + g * 8;
+        r[g] = 0;
+        if ((j < hi && j + 8 > lo) || j < im.c.pre) {
+          const int blk = __ldg(a.block_tables + static_cast<long>(im.b) * a.max_blocks + j / a.bs);
+          if (blk >= 0 && blk < a.num_blocks) {
+            r[g] = (static_cast<long>(blk) * a.hkv + im.kvh) * a.bs + j % a.bs + r8;
+            const int t = j + r8;
+            if ((t < hi && t >= lo) || t < im.c.pre) m |= 1u << g;
+          } else if (r8 == 0 && c4 == 0) {
+            raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
+          }
+        }
+      }
+    };
+    auto load_codes = [&](const uint8_t* cache, uint4 (&buf)[4][H]) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+          buf[g][h] = (okm >> g) & 1
+                          ? __ldg(reinterpret_cast<const uint4*>(cache + row[g] * D) + h * 4 + c4)
+                          : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto load_scales = [&](const Item& im, int j0) {
+      const int j = j0 + dw * 32 + lane;
+      sok = false;
+      ksc = vsc = 1.f;
+      if ((j < hi && j >= lo) || j < im.c.pre) {
+        const int blk = __ldg(a.block_tables + static_cast<long>(im.b) * a.max_blocks + j / a.bs);
+        if (blk >= 0 && blk < a.num_blocks) {
+          sok = true;
+          const long rw = (static_cast<long>(blk) * a.hkv + im.kvh) * a.bs + j % a.bs;
+          if (a.mode == FP8PA_SCALE_TOKEN_HEAD) {
+            ksc = __ldg(a.k_scale + rw);
+            vsc = __ldg(a.v_scale + rw);
+          } else if (a.mode == FP8PA_SCALE_SEGMENT) {
+            ksc = __ldg(a.k_scale + static_cast<long>(blk) * a.hp + im.kvh);
+            vsc = __ldg(a.v_scale + static_cast<long>(blk) * a.hp + im.kvh);
+          } else if (a.mode == FP8PA_SCALE_MX_BLOCK) {
+            int ek = 0, ev = 0;
+            for (int x = 0; x < nbx; ++x) {
+              ek = max(ek, static_cast<int>(
+                               __ldg(reinterpret_cast<const uint8_t*>(a.k_scale) + rw * nbx + x)));
+              ev = max(ev, static_cast<int>(
+                               __ldg(reinterpret_cast<const uint8_t*>(a.v_scale) + rw * nbx + x)));
+            }
+            ksc = exp2i(ek - 127);
+            vsc = exp2i(ev - 127);
+          }
+        }
+      }
+    };
+    // Convert the buffered codes into a tile; MX blocks take their power of
+    // two relative to the row's largest.
+    auto store_tile = [&](const uint4 (&buf)[4][H], uint8_t* tile, bool is_v, const float* sc,
+                          const uint8_t* mx, uint32_t zero) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int grp = dw * 4 + g;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          uint4 lo, hi;
+          codes16_to_f16<FMT>(buf[g][h], lo, hi);
+          const int ch = h * 4 + c4;
+          if (nbx && ((okm >> g) & 1)) {
+            // the row's largest exponent came with its scale
+            const int em = static_cast<int>(__float_as_uint(sc[grp * 8 + r8]) >> 23);
+            const int e = __ldg(mx + row[g] * nbx + ch * 16 / a.gs);
+            const float f = __int_as_float((max(e - em, -126) + 127) << 23);
+            const __half2 f2 = __floats2half2_rn(f, f);
+            const uint32_t fw = *reinterpret_cast<const uint32_t*>(&f2);
+            lo = hmul8(lo, fw);
+            hi = hmul8(hi, fw);
+          }
+          if (((okm & ~zero) >> g & 1) == 0) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+          uint8_t* dst = is_v ? tile + grp * (D * 16) + ch * 256 + r8 * 16
+                              : tile + ch * 4096 + grp * 128 + r8 * 16;
+          *reinterpret_cast<uint4*>(dst) = lo;
+          *reinterpret_cast<uint4*>(dst + (is_v ? 128 : 2048)) = hi;
+        }
+      }
+    };
+
+    uint32_t g = 0;
+    bool ok = true;
+    for (int it = it0, u = u0; u < u1 && ok; ++it) {
+      const Item im = load_item(a, pv, it, u, u1);
+      const int n = im.t1 - im.t0;
+      u += n;
+      // keys that every row of the block sees: V codes there need no check
+      const int pA = im.c.L - im.c.n + im.row0 / a.G;
+      const int pB = im.c.L - im.c.n + (im.row0 + im.rows - 1) / a.G;
+      const int wB = a.window > 0 ? max(pB - a.window + 1, 0) : 0;
+      lo = a.window > 0 ? max(pA - a.window + 1, 0) : 0;
+      hi = pB + 1;
+      for (int k = 0; k < n && ok; ++k, ++g) {
+        const int j0 = tile_token(im, im.t0 + k);
+        locate(im, j0, row, okm);
+        load_codes(a.k_cache, kb);
+        load_codes(a.v_cache, vb);
+        load_scales(im, j0);
+        const int st = g & 1, s4 = g & 3;
+        float* sk = scales + s4 * 2 * kT;
+        float* sv = sk + kT;
+        // Scale stage s4 was last read by the softmax of tile g - 4, whose P V
+        // is done: the V stage of tile g - 1 was waited for, and with it P V of
+        // tile g - 3.
+        if (g >= 2 && !wait_warp(kBarKFree + st, ((g >> 1) - 1) & 1)) { ok = false; break; }
+        sk[dw * 32 + lane] = ksc;
+        sv[dw * 32 + lane] = vsc;
+        const uint32_t vmask = __ballot_sync(0xffffffffu, sok);
+        const float vmx = warp_max_f32(sok && vsc <= FLT_MAX ? vsc : 0.f);
+        if (lane == 0) {
+          infos[s4].valid[dw] = vmask;
+          infos[s4].vmax[dw] = vmx;
+        }
+        __syncwarp();
+        store_tile(kb, sm + SM::kK + st * SM::kTile, false, sk,
+                   reinterpret_cast<const uint8_t*>(a.k_scale), 0u);
+        // In a tile that some row does not see whole, a non-finite V code
+        // would reach rows that mask its token (0 * NaN): it is zeroed and
+        // its token's scale made NaN, for the rows that do see it.
+        uint32_t bad = 0;
+        const bool whole = (j0 >= wB && j0 + kT - 1 <= pA) || j0 + kT <= im.c.pre;
+        if (FMT != FP8PA_INT8 && !whole) {
+#pragma unroll
+          for (int gg = 0; gg < 4; ++gg) {
+            bool nf = false;
+#pragma unroll
+            for (int h = 0; h < H; ++h) nf = nf || codes_nonfinite<FMT>(vb[gg][h]);
+            uint32_t any = nf ? 1u : 0u;
+            any |= __shfl_xor_sync(0xffffffffu, any, 8);
+            any |= __shfl_xor_sync(0xffffffffu, any, 16);
+            if (any && ((okm >> gg) & 1)) {
+              bad |= 1u << gg;
+              if (c4 == 0) sv[dw * 32 + gg * 8 + r8] = __int_as_float(0x7FC00000);
+            }
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bars + kBarScale + s4);
+          mbar_arrive(bars + kBarKFull + st);
+        }
+        if (g >= 2 && !wait_warp(kBarVFree + st, ((g >> 1) - 1) & 1)) { ok = false; break; }
+        store_tile(vb, sm + SM::kV + st * SM::kTile, true, sv,
+                   reinterpret_cast<const uint8_t*>(a.v_scale), bad);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + kBarVFull + st);
+      }
+    }
+  } else {
+    // ================================================= softmax warps
+    const int t = warp >> 2;            // row tile
+    const int rl = (warp & 3) * 32 + lane;  // row within it
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + t * kT + lanes, to = tmem + 256 + t * 128 + lanes;
+    uint32_t g = 0, ns = 0, no = 0;  // tiles of the CTA; S tiles and O tiles of this row tile
+    bool ok = true;
+    for (int it = it0, u = u0; u < u1 && ok; ++it) {
+      const Item im = load_item(a, pv, it, u, u1);
+      const int n = im.t1 - im.t0;
+      u += n;
+      const bool active = t == 0 || im.rows > 128;  // row tile 1 of a short block idles
+      const int r = t * 128 + rl;  // row of the block
+      const bool live = r < im.rows;
+      const int rr = im.row0 + min(r, im.rows - 1);
+      const int qi = rr / a.G, h = im.kvh * a.G + rr % a.G;
+      const long grow = (static_cast<long>(im.c.qlo) + qi) * a.hq + h;  // row of q and out
+      if (!active) {  // a block of at most 128 rows
+        g += n;
+        continue;
+      }
+      float zs;
+      {
+        // ---- the row of q, normalised by a power of two, into shared memory
+        // (every QK^T of the previous item is done: its last S was read)
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + grow * D);
+        const float sgn = a.sm_scale < 0.f ? -1.f : 1.f;
+        const bool st = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
+        const float* kc = a.k_scale + static_cast<long>(im.kvh) * D;
+        uint4 raw[D / 8];
+        float amax = 0.f;
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) raw[x] = __ldg(src + x);
+        auto get = [&](int x, float (&f)[8]) {
+          const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[2 * e] = __uint_as_float(w[e] << 16) * sgn;
+            f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * sgn;
+          }
+          if (st) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] *= __ldg(kc + x * 8 + e);
+          }
+        };
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) {
+          float f[8];
+          get(x, f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+        }
+        const int eq = amax > 0.f ? exp_above(amax) : 0;
+        const float fq = exp2i(14 - eq);
+        uint8_t* dst = sm + SM::kQ + t * SM::kTile + (rl >> 3) * 128 + (rl & 7) * 16;
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) {
+          float f[8];
+          get(x, f);
+          const uint4 o = make_uint4(pack_half2(f[0] * fq, f[1] * fq),
+                                     pack_half2(f[2] * fq, f[3] * fq),
+                                     pack_half2(f[4] * fq, f[5] * fq),
+                                     pack_half2(f[6] * fq, f[7] * fq));
+          *reinterpret_cast<uint4*>(dst + x * 2048) = o;
+        }
+        // log2-domain factor of a raw score (natural for capped scores); never
+        // zero, so that a masked -inf stays -inf
+        zs = fmaxf(fabsf(a.sm_scale) * exp2i(eq - 14) * code_unit<FMT>() *
+                       (VAR == 2 ? 1.f : kLog2e),
+                   1e-37f);
+        fence_proxy_async();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + kBarQ + t);
+      const int pos = im.c.L - im.c.n + qi;
+      const int wf = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+      const int pre = im.c.pre;
+      // extremes over the warp's rows (positions rise with the row)
+      const int pA = __shfl_sync(0xffffffffu, pos, 0), wB = __shfl_sync(0xffffffffu, wf, 31);
+      const float slope = (VAR > 0 && a.slopes) ? __ldg(a.slopes + h) * kLog2e : 0.f;
+      const float inv_cap = VAR == 2 ? 1.f / a.cap : 0.f, cap_log2 = VAR == 2 ? a.cap * kLog2e : 0.f;
+      float ref = kNegBig, l = 0.f;
+
+      for (int k = 0; k < n; ++k, ++g) {
+        const int j0 = tile_token(im, im.t0 + k);
+        const int s4 = g & 3;
+        if (!wait_warp(kBarScale + s4, (g >> 2) & 1) || !wait_warp(kBarS + t, ns & 1)) {
+          ok = false;
+          break;
+        }
+        ++ns;
+        tc_fence_after();
+        const float* sk = scales + s4 * 2 * kT;
+        const float* sv = sk + kT;
+        const uint4 val = *reinterpret_cast<const uint4*>(infos[s4].valid);
+        const float4 vm = *reinterpret_cast<const float4*>(infos[s4].vmax);
+        const bool whole = ((j0 >= wB && j0 + kT - 1 <= pA) || j0 + kT <= pre) &&
+                           (val.x & val.y & val.z & val.w) == 0xFFFFFFFFu;
+        const uint32_t vw[4] = {val.x, val.y, val.z, val.w};
+        float vmax = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
+        float mx = __int_as_float(0xff800000);
+        // ---- pass 1: the largest score (and, in masked tiles, the largest V
+        // scale the row sees)
+        if (!whole) vmax = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t raw[32];
+          tmem_ld32(ts + c * 32, raw);
+          tmem_ld_wait();
+          const uint32_t mw =
+              whole ? 0xFFFFFFFFu
+                    : (word_bits(j0 + c * 32, wf, pos + 1) | word_bits(j0 + c * 32, 0, pre)) & vw[c];
+          float z[32];
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 s = *reinterpret_cast<const float4*>(sk + c * 32 + i);
+            z[i] = __uint_as_float(raw[i]) * s.x;
+            z[i + 1] = __uint_as_float(raw[i + 1]) * s.y;
+            z[i + 2] = __uint_as_float(raw[i + 2]) * s.z;
+            z[i + 3] = __uint_as_float(raw[i + 3]) * s.w;
+          }
+          if constexpr (VAR > 0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float x = z[i] * zs;
+              if constexpr (VAR == 2) x = cap_log2 * tanh_f32(x * inv_cap);
+              z[i] = fmaf(-slope, fabsf(static_cast<float>(pos - (j0 + c * 32 + i))), x);
+            }
+          }
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              z[i] = (mw >> i) & 1 ? z[i] : __int_as_float(0xff800000);
+              if ((mw >> i) & 1) vmax = fmaxf(vmax, sv[c * 32 + i]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, z[i]);
+          if (VAR > 0 || !whole) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(z[i]);
+            tmem_st32(ts + c * 32, w);
+          }
+        }
+        if (VAR > 0 || !whole) tmem_st_wait();
+        // ---- the reference: a bound of z + log2(V scale), moved when passed
+        // by 2^kTau
+        const float zf = VAR > 0 ? 1.f : zs;
+        const float e = static_cast<float>(min(max(exp_above(vmax), -60), 120));
+        const float bound = fmaf(mx, zf, e);
+        float al = 1.f;
+        if (bound > ref + kTau) {
+          al = ex2(ref - bound);
+          ref = bound;
+        }
+        if (__any_sync(0xffffffffu, al != 1.f)) {
+          l *= al;
+          if (k > 0) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(to + c * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+              tmem_st32(to + c * 32, o);
+            }
+          }
+        }
+        // ---- pass 2: P and its sum
+        const float c0 = kShift - ref;
+        // scores as they stand in TMEM: raw (K scale still to come), or final
+        const bool fin = VAR > 0 || !whole;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t raw[32];
+          tmem_ld32(ts + c * 32, raw);
+          tmem_ld_wait();
+          uint32_t pw[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            float z[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) z[x] = __uint_as_float(raw[i + x]);
+            if (!fin) {
+              const float4 s = *reinterpret_cast<const float4*>(sk + c * 32 + i);
+              z[0] *= s.x;
+              z[1] *= s.y;
+              z[2] *= s.z;
+              z[3] *= s.w;
+            }
+            float p[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) p[x] = ex2(fmaf(z[x], zf, c0));
+            l0 += p[0] + p[2];
+            l1 += p[1] + p[3];
+            const float4 v4 = *reinterpret_cast<const float4*>(sv + c * 32 + i);
+            const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) p[x] = (whole || p[x] != 0.f) ? p[x] * vv[x] : 0.f;
+            pw[i / 2] = pack_half2(p[0], p[1]);
+            pw[i / 2 + 1] = pack_half2(p[2], p[3]);
+          }
+          tmem_st16(ts + c * 16, pw);
+        }
+        l += l0 + l1;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + kBarP + t);
+      }
+      if (!ok) break;
+
+      // ---- the block's result, or this range's piece of it
+      if (!wait_warp(kBarO + t, no & 1)) {
+        ok = false;
+        break;
+      }
+      ++no;
+      tc_fence_after();
+      const bool piece = im.t0 > 0 || im.t1 < im.tl.count;
+      const float inv = piece ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+      const float unit = code_unit<FMT>() * inv;
+      const int slot = blockIdx.x * 2 + (im.t0 > 0 ? 0 : 1);
+      const bool stat = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
+      const float* vch = a.v_scale + static_cast<long>(im.kvh) * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(to + c * 32, o);
+        tmem_ld_wait();
+        if (!live) continue;
+        float f[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          f[i] = __uint_as_float(o[i]) * unit;
+          if (stat) f[i] *= __ldg(vch + c * 32 + i);
+        }
+        if (piece || a.out_f32) {
+          float* dst = piece ? pv.o + (static_cast<long>(slot) * kRows + r) * D + c * 32
+                             : reinterpret_cast<float*>(a.out) + grow * D + c * 32;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(dst + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + grow * D +
+                                                c * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const __nv_bfloat162 b2 =
+                  __floats2bfloat162_rn(f[8 * i + 2 * x], f[8 * i + 2 * x + 1]);
+              w[x] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (piece && live) pv.ml[static_cast<long>(slot) * kRows + r] = make_float2(ref, l);
+      tc_fence_before();
+    }
+  }
+
+  // ---- drain and free: no MMA may still be in flight
+  __syncwarp();
+  if (warp == 12 && lane == 0) {
+    tc_commit(bars + kBarDrain);
+    (void)mbar_wait_bounded(bars + kBarDrain, 0, kWaitLimitCycles);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- merge
+// CTA (w, part): if cut w + 1 is the first inside its item, fold the pieces of
+// 32 of the item's rows: the first ends range w, the others open the ranges
+// behind it.
+constexpr int kMergeRows = 32;
+
+template <int D>
+__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a, const PlanView pv,
+                                                            int ranges) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int w = blockIdx.x;
+  const int cut = pv.start[w + 1], U = pv.head[0];
+  if (cut >= U) return;
+  const int it = pv.item[w + 1], rb = it / a.hkv, kvh = it - rb * a.hkv;
+  const int pre = pv.rb_pre[rb], c = pv.rb_pre[rb + 1] - pre;
+  const int f = pre * a.hkv + kvh * c;
+  // an earlier cut inside the item folds it
+  if (cut <= f || pv.start[w] > f) return;
+  const int b = pv.rb_b[rb];
+  bool x, y;
+  const Chunk ch = load_chunk(a, b, &x, &y);
+  const int row0 = (rb - pv.rbase[b]) * kRows, rows = min(kRows, ch.n * a.G - row0);
+  constexpr int TPR = D / 4;        // threads per row
+  constexpr int RPC = 256 / TPR;    // rows at a time
+  const int sub = threadIdx.x / TPR, d0 = (threadIdx.x % TPR) * 4;
+  for (int r = blockIdx.y * kMergeRows + sub; r < min(rows, (static_cast<int>(blockIdx.y) + 1) * kMergeRows);
+       r += RPC) {
+    float M = kNegBig, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = w; k < ranges; ++k) {
+      if (k > w && pv.start[k] >= f + c) break;
+      if (k > w && pv.start[k] == pv.start[k + 1]) continue;  // an empty range
+      const long p = (static_cast<long>(2 * k + (k == w ? 1 : 0)) * kRows) + r;
+      const float2 ml = pv.ml[p];
+      const float4 o = *reinterpret_cast<const float4*>(pv.o + p * D + d0);
+      const float mn = fmaxf(M, ml.x);
+      const float s0 = ex2(M - mn), s1 = ex2(ml.x - mn);
+      L = L * s0 + ml.y * s1;
+      acc.x = acc.x * s0 + o.x * s1;
+      acc.y = acc.y * s0 + o.y * s1;
+      acc.z = acc.z * s0 + o.z * s1;
+      acc.w = acc.w * s0 + o.w * s1;
+      M = mn;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int rr = row0 + r;
+    const long grow = (static_cast<long>(ch.qlo) + rr / a.G) * a.hq + kvh * a.G + rr % a.G;
+    if (a.out_f32) {
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + grow * D + d0) =
+          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    } else {
+      __nv_bfloat162 o[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv),
+                             __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + grow * D + d0) =
+          *reinterpret_cast<const uint2*>(o);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host side
+using PrefillFn = void (*)(const PrefillArgs, const PlanView);
+
+template <int D, int FMT>
+PrefillFn pick_var(int var) {
+  return var == 0 ? prefill_kernel<D, FMT, 0>
+                  : (var == 1 ? prefill_kernel<D, FMT, 1> : prefill_kernel<D, FMT, 2>);
+}
+template <int D>
+PrefillFn pick_fmt(int fmt, int var) {
+  return fmt == FP8PA_E4M3   ? pick_var<D, FP8PA_E4M3>(var)
+         : fmt == FP8PA_E5M2 ? pick_var<D, FP8PA_E5M2>(var)
+                             : pick_var<D, FP8PA_INT8>(var);
 }
 
 }  // namespace
 
-size_t prefill_workspace_bytes(int, int, int, int, int, int) { return 256; }
+size_t prefill_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, int device) {
+  return plan_layout(nullptr, total_q, batch, hq / hkv, d, sm_count(device), nullptr);
+}
 
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int ranges = sm_count(dev);
+  PlanView pv;
+  plan_layout(static_cast<char*>(a.workspace), a.total_q, a.batch, a.G, a.d, ranges, &pv);
+  const int var = a.cap > 0.f ? 2 : (a.slopes ? 1 : 0);
+  const PrefillFn fn = a.d == 128 ? pick_fmt<128>(a.fmt, var) : pick_fmt<64>(a.fmt, var);
+  const int smem = (a.d == 128 ? Smem<128>::kBytes : Smem<64>::kBytes) + 128;
+  if ((e = ensure_smem_attr(reinterpret_cast<const void*>(fn), smem)) != cudaSuccess) return e;
+
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const long rows = static_cast<long>(a.total_q) * a.hq;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps));
-  cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, a.d == 128 ? pick_prefill<128>(a.fmt) : pick_prefill<64>(a.fmt),
-                            a);
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kPlanThreads);
+  if ((e = cudaLaunchKernelEx(&cfg, prefill_plan_kernel, a, pv, ranges)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(ranges));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  if ((e = cudaLaunchKernelEx(&cfg, fn, a, pv)) != cudaSuccess) return e;
+  if (ranges < 2) return cudaSuccess;
+  cfg.gridDim = dim3(static_cast<unsigned>(ranges - 1), kRows / kMergeRows);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return a.d == 128 ? cudaLaunchKernelEx(&cfg, prefill_merge_kernel<128>, a, pv, ranges)
+                    : cudaLaunchKernelEx(&cfg, prefill_merge_kernel<64>, a, pv, ranges);
 }
 
 }  // namespace fp8pa

@@ -33,10 +33,8 @@ class Batch:
         self.sm = d ** -0.5
 
     def values(self):
-        kc, vc, ks, vs = self.cache
         f = self.form
-        return tuple(R.dequant(c, s, f["fmt"], f["scale_mode"], f["group_size"])
-                     for c, s in ((kc, ks), (vc, vs)))
+        return R.chunk_values(self.cache, f["fmt"], f["scale_mode"], f["group_size"])
 
     def ref(self, device="cpu", **mods):
         return R.chunk_ref(self.q, self.offsets, self.lens, self.bt, self.values(), self.hkv,
@@ -293,8 +291,7 @@ def test_the_operators_in_a_row(F):
         else:
             got = F.paged_prefill_attention(q, i32(off), kc, vc, ks, vs, bt.to(DEV), i32(lens),
                                             hkv, d ** -0.5, **common)
-        values = (R.dequant(kc, ks, fmt, R.TOKEN_HEAD, 0).cpu(),
-                  R.dequant(vc, vs, fmt, R.TOKEN_HEAD, 0).cpu())
+        values = tuple(x.cpu() for x in R.chunk_values((kc, vc, ks, vs), fmt, R.TOKEN_HEAD, 0))
         ref = R.chunk_ref(q.cpu(), off, lens, bt, values, hkv, d ** -0.5, bs, prefix=prefix,
                           **mods)
         R.check(got, ref, d, f16_p=not decode)
