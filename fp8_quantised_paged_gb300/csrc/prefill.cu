@@ -28,9 +28,9 @@
 // is exact, as sums and O carry the same reference.
 //
 // Roles (13 warps): 0-3 and 4-7 softmax of row tiles 0 and 1 (a thread per
-// row), 8-11 convert codes into shared memory, 12 issues the MMAs.  While the
-// tensor cores work on one row tile, the other's softmax runs.  Every wait is
-// bounded.
+// row), 8-11 convert codes into shared memory (the next tile's loads in flight
+// meanwhile), 12 issues the MMAs.  While the tensor cores work on one row tile,
+// the other's softmax runs.  Every wait is bounded.
 #include <float.h>
 
 #include "common.cuh"
@@ -49,6 +49,10 @@ constexpr int kSnap = 4;     // a cut this near an item's edge moves to it
 constexpr float kShift = 12.f;  // P = 2^(z - ref + 12): at most 2^15 with the lazy bound
 constexpr float kTau = 3.f;     // the reference may lag by 2^3
 constexpr float kNegBig = -1e30f;
+// Caps up to this take tanh as 1 - 2 / (e^2x + 1) whatever x is: the quotient is
+// good to 2^-21, so the score is off by 2^-20 cap at most, 2^-14 here.  Larger
+// caps need tanh_f32, good relative to the score.
+constexpr float kCapFast = 64.f;
 
 // ---------------------------------------------------------------- plan
 // Workspace: header, block prefix of the requests, then per row block its
@@ -266,34 +270,13 @@ enum { kBarQ = 0, kBarScale = 2, kBarKFull = 6, kBarVFull = 8, kBarP = 10, kBarK
        kBarVFree = 14, kBarS = 16, kBarO = 18, kBarDrain = 20, kNumBars = 21 };
 
 // ---------------------------------------------------------------- conversions
-// 16 codes -> 16 f16 (two 16-byte core-matrix rows), exactly; E4M3 values come
-// out times 2^-8, with the bits only moved.
+// 16 codes -> 16 f16 (two 16-byte core-matrix rows), exactly.
 template <int FMT>
 __device__ __forceinline__ void codes16_to_f16(const uint4& c, uint4& lo, uint4& hi) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  uint32_t r[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (FMT == FP8PA_INT8) {
-      r[2 * i] = int8x2_to_f16x2(w[i], 0x5140u);
-      r[2 * i + 1] = int8x2_to_f16x2(w[i], 0x5342u);
-    } else {
-      const uint32_t a = prmt(w[i], 0u, 0x1404u), b = prmt(w[i], 0u, 0x3424u);
-      if constexpr (FMT == FP8PA_E5M2) {
-        r[2 * i] = a;
-        r[2 * i + 1] = b;
-      } else {
-        r[2 * i] = (a & 0x80008000u) | ((a >> 1) & 0x3F803F80u);
-        r[2 * i + 1] = (b & 0x80008000u) | ((b >> 1) & 0x3F803F80u);
-      }
-    }
-  }
-  lo = make_uint4(r[0], r[1], r[2], r[3]);
-  hi = make_uint4(r[4], r[5], r[6], r[7]);
-}
-template <int FMT>
-__host__ __device__ constexpr float code_unit() {  // what codes16_to_f16 leaves out
-  return FMT == FP8PA_E4M3 ? 256.f : 1.f;
+  codes4_to_f16x2x2<FMT>(c.x, lo.x, lo.y);
+  codes4_to_f16x2x2<FMT>(c.y, lo.z, lo.w);
+  codes4_to_f16x2x2<FMT>(c.z, hi.x, hi.y);
+  codes4_to_f16x2x2<FMT>(c.w, hi.z, hi.w);
 }
 
 // Whether any of 16 codes is an infinity or a NaN.
@@ -316,6 +299,31 @@ __device__ __forceinline__ uint4 hmul8(const uint4& a, uint32_t f) {
     return *reinterpret_cast<const uint32_t*>(&r);
   };
   return make_uint4(m(a.x), m(a.y), m(a.z), m(a.w));
+}
+
+// Packed fp32 pairs: half the issue slots of scalar operations.
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 // D[tmem] (+)= A[tmem] * B[smem], one thread.
@@ -405,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
   if (warp == 12) tmem_relinquish();
   const uint32_t tmem = s_tmem;
   int* abort_flag = &s_abort;
+  const int lgbs = 31 - __clz(a.bs);  // block sizes are powers of two
   auto wait = [&](int bar, uint32_t parity) {
     return tc_wait(bars + bar, parity, abort_flag, a.err);
   };
@@ -493,175 +502,216 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
     }
   } else if (warp >= 8) {
     // ================================================= converting warps
+    // Warp dw has tokens 32 dw .. + 31 of a tile: four groups of 8 rows, of
+    // which a lane holds row r8 and the 16-byte chunks c4 (and c4 + 4).  Loads
+    // take 64 contiguous bytes of 8 rows, stores 8 rows of a core matrix.
     const int dw = warp - 8, r8 = lane & 7, c4 = lane >> 3;
     constexpr int H = D / 64;  // 16-byte chunks of a row per lane
-    const int nbx = a.mode == FP8PA_SCALE_MX_BLOCK ? D / a.gs : 0;
-    uint4 kb[4][H], vb[4][H];
-    long row[4];       // code rows of the lane's four tokens (8-token groups)
-    uint32_t okm = 0;  // ... whose page exists and whose token is cached
-    float ksc, vsc;    // scales of token dw * 32 + lane
-    bool sok;
+    const bool mx = a.mode == FP8PA_SCALE_MX_BLOCK;
+    const int nbx = mx ? D / a.gs : 0;
+    uint8_t* kdst = sm + SM::kK + dw * 512 + c4 * 4096 + r8 * 16;
+    uint8_t* vdst = sm + SM::kV + dw * (D * 64) + c4 * 256 + r8 * 16;
 
-    // The tokens that some row of the item sees: [lo, hi) and [0, c.pre).
-    // Others are neither looked up nor read.
-    int lo = 0, hi = 0;
-    // Addresses and codes of one tile.
-    auto locate = [&](const Item& im, int j0, long (&r)[4], uint32_t& m) {
-      m = 0;
+    // The tile being loaded: its item, and what a lane keeps of it.  Tokens
+    // that no row of the item sees are neither looked up nor read.
+    struct Next {
+      uint32_t row[4];  // code rows of the lane's tokens
+      uint32_t kx[H], vx[H];  // MX: exponent bytes of the lane's chunks, by group
+      uint32_t okm;     // ... that are to be read
+      float ks, vs;     // scales of token 32 dw + lane
+      bool sok, whole;  // ... that exists; every row sees every token
+    };
+    int it = it0, u = u0, k = 0, n = 0;
+    Item im;
+    int lo = 0, hi = 0, wB = 0, pA = 0;
+    auto open_item = [&]() {
+      im = load_item(a, pv, it, u, u1);
+      n = im.t1 - im.t0;
+      u += n;
+      pA = im.c.L - im.c.n + im.row0 / a.G;
+      const int pB = im.c.L - im.c.n + (im.row0 + im.rows - 1) / a.G;
+      wB = a.window > 0 ? max(pB - a.window + 1, 0) : 0;
+      lo = a.window > 0 ? max(pA - a.window + 1, 0) : 0;
+      hi = pB + 1;
+    };
+    auto block_of = [&](int j) {
+      const int blk = __ldg(a.block_tables + static_cast<long>(im.b) * a.max_blocks +
+                            static_cast<int>(static_cast<uint32_t>(j) >> lgbs));
+      return blk >= 0 && blk < a.num_blocks ? blk : -1;
+    };
+    auto locate = [&](Next& t) {
+      const int j0 = tile_token(im, im.t0 + k);
+      t.whole = (j0 >= wB && j0 + kT - 1 <= pA) || j0 + kT <= im.c.pre;
+      t.okm = 0;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int j = j0 + dw * 32 + g * 8;
-        r[g] = 0;
+        t.row[g] = 0;
         if ((j < hi && j + 8 > lo) || j < im.c.pre) {
-          const int blk = __ldg(a.block_tables + static_cast<long>(im.b) * a.max_blocks + j / a.bs);
-          if (blk >= 0 && blk < a.num_blocks) {
-            r[g] = (static_cast<long>(blk) * a.hkv + im.kvh) * a.bs + j % a.bs + r8;
-            const int t = j + r8;
-            if ((t < hi && t >= lo) || t < im.c.pre) m |= 1u << g;
-          } else if (r8 == 0 && c4 == 0) {
+          const int blk = block_of(j);
+          if (blk >= 0) {
+            t.row[g] = (static_cast<uint32_t>(blk) * a.hkv + im.kvh) * a.bs + (j & (a.bs - 1)) + r8;
+            const int x = j + r8;
+            if ((x < hi && x >= lo) || x < im.c.pre) t.okm |= 1u << g;
+          } else if (lane == 0) {
             raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
           }
         }
       }
-    };
-    auto load_codes = [&](const uint8_t* cache, uint4 (&buf)[4][H]) {
+      if (FMT != FP8PA_INT8 && mx) {
+        auto byte_of = [&](const float* sc, int g, int h) {
+          return static_cast<uint32_t>(__ldg(reinterpret_cast<const uint8_t*>(sc) +
+                                             static_cast<size_t>(t.row[g]) * nbx +
+                                             (h * 4 + c4) * 16 / a.gs));
+        };
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
+        for (int h = 0; h < H; ++h) {
+          t.kx[h] = t.vx[h] = 0;
 #pragma unroll
-        for (int h = 0; h < H; ++h)
-          buf[g][h] = (okm >> g) & 1
-                          ? __ldg(reinterpret_cast<const uint4*>(cache + row[g] * D) + h * 4 + c4)
-                          : make_uint4(0u, 0u, 0u, 0u);
-    };
-    auto load_scales = [&](const Item& im, int j0) {
+          for (int g = 0; g < 4; ++g) {
+            if (!((t.okm >> g) & 1)) continue;
+            t.kx[h] |= byte_of(a.k_scale, g, h) << (8 * g);
+            t.vx[h] |= byte_of(a.v_scale, g, h) << (8 * g);
+          }
+        }
+      }
       const int j = j0 + dw * 32 + lane;
-      sok = false;
-      ksc = vsc = 1.f;
+      t.sok = false;
+      t.ks = t.vs = 1.f;
       if ((j < hi && j >= lo) || j < im.c.pre) {
-        const int blk = __ldg(a.block_tables + static_cast<long>(im.b) * a.max_blocks + j / a.bs);
-        if (blk >= 0 && blk < a.num_blocks) {
-          sok = true;
-          const long rw = (static_cast<long>(blk) * a.hkv + im.kvh) * a.bs + j % a.bs;
+        const int blk = block_of(j);
+        if (blk >= 0) {
+          t.sok = true;
+          const long rw = (static_cast<long>(blk) * a.hkv + im.kvh) * a.bs + (j & (a.bs - 1));
           if (a.mode == FP8PA_SCALE_TOKEN_HEAD) {
-            ksc = __ldg(a.k_scale + rw);
-            vsc = __ldg(a.v_scale + rw);
+            t.ks = __ldg(a.k_scale + rw);
+            t.vs = __ldg(a.v_scale + rw);
           } else if (a.mode == FP8PA_SCALE_SEGMENT) {
-            ksc = __ldg(a.k_scale + static_cast<long>(blk) * a.hp + im.kvh);
-            vsc = __ldg(a.v_scale + static_cast<long>(blk) * a.hp + im.kvh);
-          } else if (a.mode == FP8PA_SCALE_MX_BLOCK) {
+            t.ks = __ldg(a.k_scale + static_cast<long>(blk) * a.hp + im.kvh);
+            t.vs = __ldg(a.v_scale + static_cast<long>(blk) * a.hp + im.kvh);
+          } else if (mx) {
+            const uint8_t* kx = reinterpret_cast<const uint8_t*>(a.k_scale) + rw * nbx;
+            const uint8_t* vx = reinterpret_cast<const uint8_t*>(a.v_scale) + rw * nbx;
             int ek = 0, ev = 0;
             for (int x = 0; x < nbx; ++x) {
-              ek = max(ek, static_cast<int>(
-                               __ldg(reinterpret_cast<const uint8_t*>(a.k_scale) + rw * nbx + x)));
-              ev = max(ev, static_cast<int>(
-                               __ldg(reinterpret_cast<const uint8_t*>(a.v_scale) + rw * nbx + x)));
+              ek = max(ek, static_cast<int>(__ldg(kx + x)));
+              ev = max(ev, static_cast<int>(__ldg(vx + x)));
             }
-            ksc = exp2i(ek - 127);
-            vsc = exp2i(ev - 127);
+            t.ks = exp2i(ek - 127);
+            t.vs = exp2i(ev - 127);
           }
         }
       }
     };
-    // Convert the buffered codes into a tile; MX blocks take their power of
-    // two relative to the row's largest.
-    auto store_tile = [&](const uint4 (&buf)[4][H], uint8_t* tile, bool is_v, const float* sc,
-                          const uint8_t* mx, uint32_t zero) {
+    auto load_codes = [&](const Next& t, const uint8_t* cache, uint4 (&buf)[4][H]) {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const int grp = dw * 4 + g;
+        const uint4* src =
+            reinterpret_cast<const uint4*>(cache + static_cast<size_t>(t.row[g]) * D) + c4;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+          buf[g][h] = (t.okm >> g) & 1 ? __ldg(src + h * 4) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    // Convert the buffered codes into a tile.  `keep`: groups whose row is
+    // wanted, the others become zero.  MX blocks take their power of two
+    // relative to the row's largest, which the row's scale `sc` holds.
+    auto store_tile = [&](const uint4 (&buf)[4][H], uint8_t* dst, int gstep, int cstep, int hstep,
+                          const float* sc, const uint32_t (&ex)[H], uint32_t keep) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-          uint4 lo, hi;
-          codes16_to_f16<FMT>(buf[g][h], lo, hi);
-          const int ch = h * 4 + c4;
-          if (nbx && ((okm >> g) & 1)) {
-            // the row's largest exponent came with its scale
-            const int em = static_cast<int>(__float_as_uint(sc[grp * 8 + r8]) >> 23);
-            const int e = __ldg(mx + row[g] * nbx + ch * 16 / a.gs);
+          uint4 x, y;
+          codes16_to_f16<FMT>(buf[g][h], x, y);
+          if (FMT != FP8PA_INT8 && mx && ((keep >> g) & 1)) {
+            const int em = static_cast<int>(__float_as_uint(sc[g * 8 + r8]) >> 23);
+            const int e = (ex[h] >> (8 * g)) & 0xFF;
             const float f = __int_as_float((max(e - em, -126) + 127) << 23);
             const __half2 f2 = __floats2half2_rn(f, f);
             const uint32_t fw = *reinterpret_cast<const uint32_t*>(&f2);
-            lo = hmul8(lo, fw);
-            hi = hmul8(hi, fw);
+            x = hmul8(x, fw);
+            y = hmul8(y, fw);
           }
-          if (((okm & ~zero) >> g & 1) == 0) lo = hi = make_uint4(0u, 0u, 0u, 0u);
-          uint8_t* dst = is_v ? tile + grp * (D * 16) + ch * 256 + r8 * 16
-                              : tile + ch * 4096 + grp * 128 + r8 * 16;
-          *reinterpret_cast<uint4*>(dst) = lo;
-          *reinterpret_cast<uint4*>(dst + (is_v ? 128 : 2048)) = hi;
+          if (keep != 0xFu && ((keep >> g) & 1) == 0) x = y = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(dst + g * gstep + h * cstep) = x;
+          *reinterpret_cast<uint4*>(dst + g * gstep + h * cstep + hstep) = y;
         }
       }
     };
 
-    uint32_t g = 0;
-    bool ok = true;
-    for (int it = it0, u = u0; u < u1 && ok; ++it) {
-      const Item im = load_item(a, pv, it, u, u1);
-      const int n = im.t1 - im.t0;
-      u += n;
-      // keys that every row of the block sees: V codes there need no check
-      const int pA = im.c.L - im.c.n + im.row0 / a.G;
-      const int pB = im.c.L - im.c.n + (im.row0 + im.rows - 1) / a.G;
-      const int wB = a.window > 0 ? max(pB - a.window + 1, 0) : 0;
-      lo = a.window > 0 ? max(pA - a.window + 1, 0) : 0;
-      hi = pB + 1;
-      for (int k = 0; k < n && ok; ++k, ++g) {
-        const int j0 = tile_token(im, im.t0 + k);
-        locate(im, j0, row, okm);
-        load_codes(a.k_cache, kb);
-        load_codes(a.v_cache, vb);
-        load_scales(im, j0);
-        const int st = g & 1, s4 = g & 3;
-        float* sk = scales + s4 * 2 * kT;
-        float* sv = sk + kT;
-        // Scale stage s4 was last read by the softmax of tile g - 4, whose P V
-        // is done: the V stage of tile g - 1 was waited for, and with it P V of
-        // tile g - 3.
-        if (g >= 2 && !wait_warp(kBarKFree + st, ((g >> 1) - 1) & 1)) { ok = false; break; }
-        sk[dw * 32 + lane] = ksc;
-        sv[dw * 32 + lane] = vsc;
-        const uint32_t vmask = __ballot_sync(0xffffffffu, sok);
-        const float vmx = warp_max_f32(sok && vsc <= FLT_MAX ? vsc : 0.f);
-        if (lane == 0) {
-          infos[s4].valid[dw] = vmask;
-          infos[s4].vmax[dw] = vmx;
-        }
-        __syncwarp();
-        store_tile(kb, sm + SM::kK + st * SM::kTile, false, sk,
-                   reinterpret_cast<const uint8_t*>(a.k_scale), 0u);
-        // In a tile that some row does not see whole, a non-finite V code
-        // would reach rows that mask its token (0 * NaN): it is zeroed and
-        // its token's scale made NaN, for the rows that do see it.
-        uint32_t bad = 0;
-        const bool whole = (j0 >= wB && j0 + kT - 1 <= pA) || j0 + kT <= im.c.pre;
-        if (FMT != FP8PA_INT8 && !whole) {
+    uint4 kb[4][H], vb[4][H];
+    Next t;
+    open_item();
+    locate(t);
+    load_codes(t, a.k_cache, kb);
+    load_codes(t, a.v_cache, vb);
+    for (uint32_t g = 0;; ++g) {
+      const int st = g & 1, s4 = g & 3;
+      float* sk = scales + s4 * 2 * kT + dw * 32;
+      float* sv = sk + kT;
+      // Scale stage s4 was last read by the softmax of tile g - 4, whose P V
+      // is done: the V stage of tile g - 1 was waited for, and with it P V of
+      // tile g - 3.
+      if (g >= 2 && !wait_warp(kBarKFree + st, ((g >> 1) - 1) & 1)) break;
+      const uint32_t vmask = __ballot_sync(0xffffffffu, t.sok);
+      const float vmx = warp_max_f32(t.sok && t.vs <= FLT_MAX ? t.vs : 0.f);
+      sk[lane] = t.ks;
+      sv[lane] = t.vs;
+      if (lane == 0) {
+        infos[s4].valid[dw] = vmask;
+        infos[s4].vmax[dw] = vmx;
+      }
+      __syncwarp();
+      store_tile(kb, kdst + st * SM::kTile, 128, 4 * 4096, 2048, sk, t.kx, t.okm);
+      // In a tile that some row does not see whole, a non-finite V code would
+      // reach rows that mask its token (0 * NaN): it is zeroed and its token's
+      // scale made NaN, for the rows that do see it.
+      uint32_t keep = t.okm;
+      if (FMT != FP8PA_INT8 && !t.whole) {
 #pragma unroll
-          for (int gg = 0; gg < 4; ++gg) {
-            bool nf = false;
+        for (int gg = 0; gg < 4; ++gg) {
+          bool nf = false;
 #pragma unroll
-            for (int h = 0; h < H; ++h) nf = nf || codes_nonfinite<FMT>(vb[gg][h]);
-            uint32_t any = nf ? 1u : 0u;
-            any |= __shfl_xor_sync(0xffffffffu, any, 8);
-            any |= __shfl_xor_sync(0xffffffffu, any, 16);
-            if (any && ((okm >> gg) & 1)) {
-              bad |= 1u << gg;
-              if (c4 == 0) sv[dw * 32 + gg * 8 + r8] = __int_as_float(0x7FC00000);
-            }
+          for (int h = 0; h < H; ++h) nf = nf || codes_nonfinite<FMT>(vb[gg][h]);
+          uint32_t any = nf ? 1u : 0u;
+          any |= __shfl_xor_sync(0xffffffffu, any, 8);
+          any |= __shfl_xor_sync(0xffffffffu, any, 16);
+          if (any && ((t.okm >> gg) & 1)) {
+            keep &= ~(1u << gg);
+            if (c4 == 0) sv[gg * 8 + r8] = __int_as_float(0x7FC00000);
           }
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bars + kBarScale + s4);
-          mbar_arrive(bars + kBarKFull + st);
-        }
-        if (g >= 2 && !wait_warp(kBarVFree + st, ((g >> 1) - 1) & 1)) { ok = false; break; }
-        store_tile(vb, sm + SM::kV + st * SM::kTile, true, sv,
-                   reinterpret_cast<const uint8_t*>(a.v_scale), bad);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars + kBarVFull + st);
       }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bars + kBarScale + s4);
+        mbar_arrive(bars + kBarKFull + st);
+      }
+      // the tile behind this one: its K codes are on their way while V is
+      // converted, its V codes while the next K is
+      uint32_t vx[H];
+#pragma unroll
+      for (int h = 0; h < H; ++h) vx[h] = t.vx[h];
+      bool more = true;
+      if (++k == n) {
+        k = 0;
+        ++it;
+        more = u < u1;
+        if (more) open_item();
+      }
+      if (more) {
+        locate(t);
+        load_codes(t, a.k_cache, kb);
+      }
+      if (g >= 2 && !wait_warp(kBarVFree + st, ((g >> 1) - 1) & 1)) break;
+      store_tile(vb, vdst + st * SM::kTile, D * 16, 4 * 256, 128, sv, vx, keep);
+      if (more) load_codes(t, a.v_cache, vb);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + kBarVFull + st);
+      if (!more) break;
     }
   } else {
     // ================================================= softmax warps
@@ -729,10 +779,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
                                      pack_half2(f[6] * fq, f[7] * fq));
           *reinterpret_cast<uint4*>(dst + x * 2048) = o;
         }
-        // log2-domain factor of a raw score (natural for capped scores); never
+        // log2-domain factor of a raw score (capped scores: of 2 z / cap); never
         // zero, so that a masked -inf stays -inf
-        zs = fmaxf(fabsf(a.sm_scale) * exp2i(eq - 14) * code_unit<FMT>() *
-                       (VAR == 2 ? 1.f : kLog2e),
+        zs = fmaxf(fabsf(a.sm_scale) * exp2i(eq - 14) * kLog2e *
+                       (VAR == 2 ? 2.f / a.cap : 1.f),
                    1e-37f);
         fence_proxy_async();
       }
@@ -744,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
       // extremes over the warp's rows (positions rise with the row)
       const int pA = __shfl_sync(0xffffffffu, pos, 0), wB = __shfl_sync(0xffffffffu, wf, 31);
       const float slope = (VAR > 0 && a.slopes) ? __ldg(a.slopes + h) * kLog2e : 0.f;
-      const float inv_cap = VAR == 2 ? 1.f / a.cap : 0.f, cap_log2 = VAR == 2 ? a.cap * kLog2e : 0.f;
+      const float cap_log2 = VAR == 2 ? a.cap * kLog2e : 0.f;
       float ref = kNegBig, l = 0.f;
 
       for (int k = 0; k < n; ++k, ++g) {
@@ -760,118 +810,176 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
         const float* sv = sk + kT;
         const uint4 val = *reinterpret_cast<const uint4*>(infos[s4].valid);
         const float4 vm = *reinterpret_cast<const float4*>(infos[s4].vmax);
-        const bool whole = ((j0 >= wB && j0 + kT - 1 <= pA) || j0 + kT <= pre) &&
-                           (val.x & val.y & val.z & val.w) == 0xFFFFFFFFu;
-        const uint32_t vw[4] = {val.x, val.y, val.z, val.w};
-        float vmax = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
-        float mx = __int_as_float(0xff800000);
-        // ---- pass 1: the largest score (and, in masked tiles, the largest V
-        // scale the row sees)
-        if (!whole) vmax = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t raw[32];
-          tmem_ld32(ts + c * 32, raw);
-          tmem_ld_wait();
-          const uint32_t mw =
-              whole ? 0xFFFFFFFFu
-                    : (word_bits(j0 + c * 32, wf, pos + 1) | word_bits(j0 + c * 32, 0, pre)) & vw[c];
-          float z[32];
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 s = *reinterpret_cast<const float4*>(sk + c * 32 + i);
-            z[i] = __uint_as_float(raw[i]) * s.x;
-            z[i + 1] = __uint_as_float(raw[i + 1]) * s.y;
-            z[i + 2] = __uint_as_float(raw[i + 2]) * s.z;
-            z[i + 3] = __uint_as_float(raw[i + 3]) * s.w;
+        const bool whole =
+            ((j0 >= wB && j0 + kT - 1 <= pA) || (VAR == 0 && j0 + kT <= pre)) &&
+            (val.x & val.y & val.z & val.w) == 0xFFFFFFFFu;
+        // Raise the reference to `bound` where it was passed by 2^kTau, and
+        // with it the sum and O.
+        auto move_ref = [&](float bound) {
+          float al = 1.f;
+          if (bound > ref + kTau) {
+            al = ex2(ref - bound);
+            ref = bound;
           }
-          if constexpr (VAR > 0) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float x = z[i] * zs;
-              if constexpr (VAR == 2) x = cap_log2 * tanh_f32(x * inv_cap);
-              z[i] = fmaf(-slope, fabsf(static_cast<float>(pos - (j0 + c * 32 + i))), x);
-            }
-          }
-          if (!whole) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              z[i] = (mw >> i) & 1 ? z[i] : __int_as_float(0xff800000);
-              if ((mw >> i) & 1) vmax = fmaxf(vmax, sv[c * 32 + i]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, z[i]);
-          if (VAR > 0 || !whole) {
-            uint32_t w[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(z[i]);
-            tmem_st32(ts + c * 32, w);
-          }
-        }
-        if (VAR > 0 || !whole) tmem_st_wait();
-        // ---- the reference: a bound of z + log2(V scale), moved when passed
-        // by 2^kTau
-        const float zf = VAR > 0 ? 1.f : zs;
-        const float e = static_cast<float>(min(max(exp_above(vmax), -60), 120));
-        const float bound = fmaf(mx, zf, e);
-        float al = 1.f;
-        if (bound > ref + kTau) {
-          al = ex2(ref - bound);
-          ref = bound;
-        }
-        if (__any_sync(0xffffffffu, al != 1.f)) {
+          if (!__any_sync(0xffffffffu, al != 1.f)) return;
           l *= al;
-          if (k > 0) {
+          if (k == 0) return;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(to + c * 32, o);
+            tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(to + c * 32, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-              tmem_st32(to + c * 32, o);
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+            tmem_st32(to + c * 32, o);
+          }
+        };
+        auto bound_of = [&](float zmax, float vmax) {
+          return zmax + static_cast<float>(min(max(exp_above(vmax), -60), 120));
+        };
+        if (whole && (VAR < 2 || a.cap <= kCapFast)) {
+          // ---- every row sees the whole tile: one pass for the largest score,
+          // one for P, 32 scores at a time, the next 32 on their way from TMEM
+          const ulonglong2* sk2 = reinterpret_cast<const ulonglong2*>(sk);
+          const ulonglong2* sv2 = reinterpret_cast<const ulonglong2*>(sv);
+          const uint64_t zs2 = f2_pack(zs, zs);
+          // the bias of tokens 2 i, 2 i + 1: -slope (pos - j)
+          const float b0 = VAR > 0 ? slope * static_cast<float>(j0 - pos) : 0.f;
+          const uint64_t bias = f2_pack(b0, b0 + slope), step = f2_pack(2.f * slope, 2.f * slope);
+          auto score = [&](const uint32_t* r, uint64_t sc, int i, uint64_t bias) {
+            uint64_t z = f2_mul(f2_pack(__uint_as_float(r[0]), __uint_as_float(r[1])), sc);
+            if constexpr (VAR > 0) {
+              const uint64_t b = f2_fma(
+                  step, f2_pack(static_cast<float>(i), static_cast<float>(i)), bias);
+              if constexpr (VAR == 1) {
+                z = f2_fma(z, zs2, b);
+              } else {  // cap tanh(z / cap) = cap - 2 cap / (2^x + 1)
+                float x, y;
+                f2_unpack(f2_mul(z, zs2), x, y);
+                x = fmaf(__fdividef(1.f, ex2(x) + 1.f), -2.f * cap_log2, cap_log2);
+                y = fmaf(__fdividef(1.f, ex2(y) + 1.f), -2.f * cap_log2, cap_log2);
+                z = f2_add(f2_pack(x, y), b);
+              }
             }
+            return z;
+          };
+          uint32_t raw[2][32];
+          tmem_ld32(ts, raw[0]);
+          float m4[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) m4[x] = __int_as_float(0xff800000);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait();
+            tmem_ld32(ts + ((c + 1) & 3) * 32, raw[(c + 1) & 1]);
+            uint32_t* r = raw[c & 1];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const ulonglong2 s = sk2[c * 8 + i / 2];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                float p, q;
+                const uint64_t z = score(r + (i + x) * 2, x ? s.y : s.x, c * 16 + i + x, bias);
+                f2_unpack(z, p, q);
+                m4[(i + x) & 3] = fmaxf(fmaxf(m4[(i + x) & 3], p), q);
+                if constexpr (VAR == 2) {
+                  r[(i + x) * 2] = __float_as_uint(p);
+                  r[(i + x) * 2 + 1] = __float_as_uint(q);
+                }
+              }
+            }
+            // a capped score is not computed twice
+            if constexpr (VAR == 2) tmem_st32(ts + c * 32, raw[c & 1]);
+          }
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          const float zf = VAR > 0 ? 1.f : zs;
+          move_ref(bound_of(mx * zf, fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w))));
+          const float c0 = kShift - ref;
+          const uint64_t zf2 = f2_pack(zf, zf), c02 = f2_pack(c0, c0);
+          const uint64_t bias2 = f2_add(bias, c02);  // the exponent's offset in it too
+          uint64_t la = 0, lb = 0;                    // (0.f, 0.f)
+          if constexpr (VAR == 2) {
+            tmem_st_wait();
+            tmem_ld32(ts, raw[0]);
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait();
+            if (c < 3) tmem_ld32(ts + (c + 1) * 32, raw[(c + 1) & 1]);
+            const uint32_t* r = raw[c & 1];
+            uint32_t pw[16];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const ulonglong2 v = sv2[c * 8 + i / 2], s = sk2[c * 8 + i / 2];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                float p, q;
+                const uint64_t z =
+                    VAR == 2 ? f2_pack(__uint_as_float(r[(i + x) * 2]),
+                                       __uint_as_float(r[(i + x) * 2 + 1]))
+                             : score(r + (i + x) * 2, x ? s.y : s.x, c * 16 + i + x, bias2);
+                f2_unpack(VAR == 2 ? f2_add(z, c02) : (VAR ? z : f2_fma(z, zf2, c02)), p, q);
+                const uint64_t p2 = f2_pack(ex2(p), ex2(q));
+                if (x) lb = f2_add(lb, p2);
+                else la = f2_add(la, p2);
+                f2_unpack(f2_mul(p2, x ? v.y : v.x), p, q);
+                pw[i + x] = pack_half2(p, q);
+              }
+            }
+            tmem_st16(ts + c * 16, pw);
+          }
+          float x, y;
+          f2_unpack(f2_add(la, lb), x, y);
+          l += x + y;
+        } else {
+          // ---- masked tiles, two passes over the scores in TMEM: final scores,
+          // then P.  A row's V bound is that of the tokens it sees.
+          const float zf = VAR > 0 ? 1.f : zs;
+          float mx = __int_as_float(0xff800000), vmax = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t raw[32];
+            tmem_ld32(ts + c * 32, raw);
+            tmem_ld_wait();
+            const int jc = j0 + c * 32;
+            const uint32_t mw =
+                (word_bits(jc, wf, pos + 1) | word_bits(jc, 0, pre)) & infos[s4].valid[c];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float z = __uint_as_float(raw[i]) * sk[c * 32 + i];
+              if constexpr (VAR > 0) {
+                z *= zs;
+                if constexpr (VAR == 2) z = cap_log2 * tanh_f32(z * (0.5f / kLog2e));
+                z = fmaf(-slope, fabsf(static_cast<float>(pos - jc - i)), z);
+              }
+              const bool see = (mw >> i) & 1;
+              z = see ? z : __int_as_float(0xff800000);
+              mx = fmaxf(mx, z);
+              vmax = fmaxf(vmax, see ? sv[c * 32 + i] : 0.f);
+              raw[i] = __float_as_uint(z);
+            }
+            tmem_st32(ts + c * 32, raw);
+          }
+          tmem_st_wait();
+          move_ref(bound_of(mx * zf, vmax));
+          const float c0 = kShift - ref;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t raw[32], pw[16];
+            tmem_ld32(ts + c * 32, raw);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float p = ex2(fmaf(__uint_as_float(raw[i]), zf, c0));
+              const float q = ex2(fmaf(__uint_as_float(raw[i + 1]), zf, c0));
+              l += p + q;
+              // a masked token's scale may be anything
+              pw[i / 2] = pack_half2(p != 0.f ? p * sv[c * 32 + i] : 0.f,
+                                     q != 0.f ? q * sv[c * 32 + i + 1] : 0.f);
+            }
+            tmem_st16(ts + c * 16, pw);
           }
         }
-        // ---- pass 2: P and its sum
-        const float c0 = kShift - ref;
-        // scores as they stand in TMEM: raw (K scale still to come), or final
-        const bool fin = VAR > 0 || !whole;
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t raw[32];
-          tmem_ld32(ts + c * 32, raw);
-          tmem_ld_wait();
-          uint32_t pw[16];
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            float z[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) z[x] = __uint_as_float(raw[i + x]);
-            if (!fin) {
-              const float4 s = *reinterpret_cast<const float4*>(sk + c * 32 + i);
-              z[0] *= s.x;
-              z[1] *= s.y;
-              z[2] *= s.z;
-              z[3] *= s.w;
-            }
-            float p[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) p[x] = ex2(fmaf(z[x], zf, c0));
-            l0 += p[0] + p[2];
-            l1 += p[1] + p[3];
-            const float4 v4 = *reinterpret_cast<const float4*>(sv + c * 32 + i);
-            const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) p[x] = (whole || p[x] != 0.f) ? p[x] * vv[x] : 0.f;
-            pw[i / 2] = pack_half2(p[0], p[1]);
-            pw[i / 2 + 1] = pack_half2(p[2], p[3]);
-          }
-          tmem_st16(ts + c * 16, pw);
-        }
-        l += l0 + l1;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -888,7 +996,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
       tc_fence_after();
       const bool piece = im.t0 > 0 || im.t1 < im.tl.count;
       const float inv = piece ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-      const float unit = code_unit<FMT>() * inv;
       const int slot = blockIdx.x * 2 + (im.t0 > 0 ? 0 : 1);
       const bool stat = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
       const float* vch = a.v_scale + static_cast<long>(im.kvh) * D;
@@ -901,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
         float f[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          f[i] = __uint_as_float(o[i]) * unit;
+          f[i] = __uint_as_float(o[i]) * inv;
           if (stat) f[i] *= __ldg(vch + c * 32 + i);
         }
         if (piece || a.out_f32) {

@@ -21,6 +21,9 @@ largest V scale the row sees at most, so the sum it divides by is at least
 2^(12 - e) >= 2^11 / vs_max.  Every visible token adds at most
 2^-25 |code_jd| * vs_max / 2^11, W = 2^-36 vs_max sum_j |code_jd| in all (times
 the channel's scale where scales are static).
+
+A cap of at most 64 may take tanh as 1 - 2 / (e^2x + 1), whose quotient is good to
+2^-21: 2^-20 cap more in dz.
 """
 from __future__ import annotations
 
@@ -195,13 +198,15 @@ def half_step_bf16(x):
     return np.exp2(e - 8)
 
 
-def check(got, ref, d, bf16=False, f16_p=False, f16_q=False, what=""):
+def check(got, ref, d, bf16=False, f16_p=False, f16_q=False, cap=0.0, what=""):
     """Hold `got` to the bound at the head of this file."""
     want, A, Z, B, W = ref
     got = got.double().cpu().numpy()
     assert got.shape == want.shape, (got.shape, want.shape)
     assert np.isfinite(got).all(), f"{what}: not finite"
     dz = (d / 16 + 4) * 2.0 ** -22 * Z + 4 * 2.0 ** -22 * B + (2.0 ** -11 * Z if f16_q else 0.0)
+    if f16_p and cap <= 64:
+        dz = dz + 2.0 ** -20 * cap
     bound = A * (2 * dz + 2.0 ** -19 + (2.0 ** -11 if f16_p else 0.0)) + 1e-30
     if f16_p:
         bound = bound + W

@@ -58,7 +58,8 @@ class Batch:
         for dt in (torch.float32, torch.bfloat16):
             got = self.run(F, out_dtype=dt, **mods)
             R.check(got, ref, self.d, bf16=dt == torch.bfloat16, f16_p=True,
-                    f16_q=self.form["scale_mode"] == R.STATIC, what=f"{what} {dt}")
+                    f16_q=self.form["scale_mode"] == R.STATIC,
+                    cap=mods.get("cap", 0.0), what=f"{what} {dt}")
         assert F.get_device_error() == 0
         return got
 
@@ -119,8 +120,9 @@ def test_distance_bias_at_steep_and_flat_slopes(F):
 def test_long_contexts(F, kw):
     b = Batch([4100, 1337], [300, 1337], 8, 1, 128, 16, R.E4M3, R.TOKEN_HEAD, seed=7)
     ref = b.ref(device=DEV, **kw)
-    R.check(b.run(F, **kw), ref, 128, f16_p=True)
-    R.check(b.run(F, out_dtype=torch.bfloat16, **kw), ref, 128, bf16=True, f16_p=True)
+    cap = kw.get("cap", 0.0)
+    R.check(b.run(F, **kw), ref, 128, f16_p=True, cap=cap)
+    R.check(b.run(F, out_dtype=torch.bfloat16, **kw), ref, 128, bf16=True, f16_p=True, cap=cap)
 
 
 def test_requests_without_queries_or_tokens(F):
@@ -294,7 +296,7 @@ def test_the_operators_in_a_row(F):
         values = tuple(x.cpu() for x in R.chunk_values((kc, vc, ks, vs), fmt, R.TOKEN_HEAD, 0))
         ref = R.chunk_ref(q.cpu(), off, lens, bt, values, hkv, d ** -0.5, bs, prefix=prefix,
                           **mods)
-        R.check(got, ref, d, f16_p=not decode)
+        R.check(got, ref, d, f16_p=not decode, cap=mods["cap"])
         # the queries and the newest keys really are turned
         want = R.rotate(qkv[:, :hq * d].cpu().unflatten(1, (hq, d)), cs[pos][:, :half],
                         cs[pos][:, half:]).bfloat16()
