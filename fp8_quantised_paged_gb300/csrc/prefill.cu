@@ -27,10 +27,10 @@
 // inside f16 whatever the scales; it moves only when passed by 2^kTau, which
 // is exact, as sums and O carry the same reference.
 //
-// Roles (13 warps): 0-3 and 4-7 softmax of row tiles 0 and 1 (a thread per
-// row), 8-11 convert codes into shared memory (the next tile's loads in flight
-// meanwhile), 12 issues the MMAs.  While the tensor cores work on one row tile,
-// the other's softmax runs.  Every wait is bounded.
+// Roles (17 warps): 0-3 and 4-7 the softmax of row tiles 0 and 1 (a thread per
+// row), 8-11 and 12-15 convert K and V codes into shared memory (the next tile's
+// loads in flight meanwhile), 16 issues the MMAs (one thread).  While the tensor cores work on one row tile, the other's softmax runs.
+// Every wait is bounded.
 #include <float.h>
 
 #include "common.cuh"
@@ -44,7 +44,7 @@ namespace {
 
 constexpr int kRows = 256;   // rows of a block: two tiles of 128
 constexpr int kT = 128;      // tokens per tile
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 17 * 32;
 constexpr int kSnap = 4;     // a cut this near an item's edge moves to it
 constexpr float kShift = 12.f;  // P = 2^(z - ref + 12): at most 2^15 with the lazy bound
 constexpr float kTau = 3.f;     // the reference may lag by 2^3
@@ -257,15 +257,16 @@ struct Smem {
   static constexpr int kScale = 6 * kTile;  // four stages of [K scales][V scales] f32
   static constexpr int kInfo = kScale + 4 * 2 * kT * 4;  // four stages of StageInfo
   static constexpr int kBars = kInfo + 4 * 64;
-  static constexpr int kBytes = kBars + 256;
+  static constexpr int kMisc = kBars + 256;  // TMEM base, abort flag
+  static constexpr int kBytes = kMisc + 16;
 };
 struct StageInfo {
   uint32_t valid[4];  // tokens whose page exists
   float vmax[4];      // largest V scale of each 32 tokens
 };
 
-// Barriers: one arrival per warp of a group of four on the first twelve, one
-// commit of the tensor cores on the others.
+// Barriers: one arrival per warp of a warpgroup on the first twelve (the scales:
+// of the two converting groups), one commit of the tensor cores on the others.
 enum { kBarQ = 0, kBarScale = 2, kBarKFull = 6, kBarVFull = 8, kBarP = 10, kBarKFree = 12,
        kBarVFree = 14, kBarS = 16, kBarO = 18, kBarDrain = 20, kNumBars = 21 };
 
@@ -326,6 +327,13 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], one thread.
 __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                               bool accumulate) {
@@ -353,8 +361,10 @@ struct Item {
   int t0, t1;
 };
 
-__device__ __forceinline__ Item load_item(const PrefillArgs& a, const PlanView& v, int it, int u,
-                                          int u1) {
+// Out of line: every role calls it once per item, and the roles' loops have to
+// share the instruction caches.
+__device__ __noinline__ Item load_item(const PrefillArgs& a, const PlanView& v, int it, int u,
+                                       int u1) {
   Item r;
   const int rb = it / a.hkv;
   r.kvh = it - rb * a.hkv;
@@ -376,6 +386,214 @@ __device__ __forceinline__ int tile_token(const Item& it, int k) {
   return (k < it.tl.np ? k : k + it.tl.skip) * kT;
 }
 
+// ---------------------------------------------------------------- conversion
+// One converting warp's work for the CTA's range: tokens 32 dw .. + 31 of every
+// tile of K (V false) or V.  A lane holds row r8 of four 8-row groups and, of
+// each, the 16-byte chunks c4 (and c4 + 4): loads take 64 contiguous bytes of
+// 8 rows, stores the 8 rows of a core matrix, free of bank conflicts.  A tile's
+// codes and scales are loaded as soon as the tile before it is stored, its
+// block ids one tile earlier.
+template <int D, int FMT, bool V>
+__device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanView& pv,
+                                              uint8_t* sm, int* abort_flag, int it, int u, int u1,
+                                              int dw, int lane) {
+  using SM = Smem<D>;
+  constexpr int H = D / 64;  // 16-byte chunks of a row per lane
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
+  StageInfo* infos = reinterpret_cast<StageInfo*>(sm + SM::kInfo);
+  const uint8_t* cache = V ? a.v_cache : a.k_cache;
+  const float* gscale = V ? a.v_scale : a.k_scale;
+  const int r8 = lane & 7, c4 = lane >> 3;
+  const int lgbs = 31 - __clz(a.bs);  // block sizes are powers of two
+  const bool mx = FMT != FP8PA_INT8 && a.mode == FP8PA_SCALE_MX_BLOCK;
+  const int nbx = mx ? D / a.gs : 0;
+  constexpr int kG = V ? D * 16 : 128, kC = V ? 4 * 256 : 4 * 4096, kH = V ? 128 : 2048;
+  uint8_t* dst0 = sm + (V ? SM::kV + dw * (4 * kG) + c4 * 256 : SM::kK + dw * (4 * kG) + c4 * 4096) +
+                  r8 * 16;
+
+  // the open item: tiles left of it, its block table, the tokens that some row
+  // sees ([lo, hi) and [0, pre); others are neither looked up nor read) and,
+  // for V, those that every row sees
+  Tiles tl;
+  int k = 0, n = 0, kt = 0, kvh = 0, lo = 0, hi = 0, pre = 0, all_lo = 0, all_hi = 0;
+  const int32_t* table = nullptr;
+  auto open_item = [&]() {
+    const Item im = load_item(a, pv, it, u, u1);
+    k = 0;
+    n = im.t1 - im.t0;
+    kt = im.t0;
+    u += n;
+    tl = im.tl;
+    kvh = im.kvh;
+    pre = im.c.pre;
+    table = a.block_tables + static_cast<long>(im.b) * a.max_blocks;
+    const int pA = im.c.L - im.c.n + im.row0 / a.G;
+    const int pB = im.c.L - im.c.n + (im.row0 + im.rows - 1) / a.G;
+    lo = a.window > 0 ? max(pA - a.window + 1, 0) : 0;
+    hi = pB + 1;
+    all_lo = a.window > 0 ? max(pB - a.window + 1, 0) : 0;
+    all_hi = pA + 1;
+  };
+  auto token_of = [&](int i) { return (i < tl.np ? i : i + tl.skip) * kT + dw * 32; };
+  auto wanted = [&](int j) { return (j < hi && j >= lo) || j < pre; };
+  // block ids of the warp's two 16-token halves (a half lies in one block); -1
+  // where no row sees any of its tokens
+  auto load_ids = [&](int i, int (&id)[2]) {
+    const int j = token_of(i);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int t = j + 16 * x;
+      id[x] = (t < hi && t + 16 > lo) || t < pre
+                  ? __ldg(table + static_cast<int>(static_cast<uint32_t>(t) >> lgbs))
+                  : -1;
+    }
+  };
+
+  int ids[2];
+  for (uint32_t g = 0;; ++g) {
+    // ---- the next tile's loads, as soon as the last one is stored
+    if (k == n) {
+      if (u >= u1) return;
+      open_item();
+      ++it;
+      load_ids(kt, ids);
+    }
+    const int j = token_of(kt + k);
+    const bool whole =
+        (j - dw * 32 >= all_lo && j - dw * 32 + kT <= all_hi) || j - dw * 32 + kT <= pre;
+    uint4 buf[4][H];
+    uint32_t okm = 0;  // groups whose row is wanted and exists
+    uint32_t row[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int blk = ids[x >> 1], t = j + x * 8 + r8;
+      const bool ok = wanted(t) && blk >= 0 && blk < a.num_blocks;
+      row[x] = ok ? (static_cast<uint32_t>(blk) * a.hkv + kvh) * a.bs + (t & (a.bs - 1)) : 0u;
+      if (ok) okm |= 1u << x;
+      const uint4* src =
+          reinterpret_cast<const uint4*>(cache + static_cast<size_t>(row[x]) * D) + c4;
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        buf[x][h] = ok ? __ldg(src + h * 4) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    float sc = 1.f;  // scale of token 32 dw + lane
+    bool sok;
+    uint32_t ex[H];  // MX: exponent bytes of the lane's chunks, by group
+    {
+      const int blk = lane < 16 ? ids[0] : ids[1], t = j + lane;
+      sok = wanted(t) && blk >= 0 && blk < a.num_blocks;
+      if (wanted(t) && !sok && !V) raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
+      const long rw =
+          sok ? (static_cast<long>(blk) * a.hkv + kvh) * a.bs + (t & (a.bs - 1)) : 0;
+      if (a.mode == FP8PA_SCALE_TOKEN_HEAD) {
+        if (sok) sc = __ldg(gscale + rw);
+      } else if (a.mode == FP8PA_SCALE_SEGMENT) {
+        if (sok) sc = __ldg(gscale + static_cast<long>(blk) * a.hp + kvh);
+      } else if (mx) {
+        const uint8_t* exps = reinterpret_cast<const uint8_t*>(gscale);
+        if (sok) {
+          int e = 0;
+          for (int i = 0; i < nbx; ++i) e = max(e, static_cast<int>(__ldg(exps + rw * nbx + i)));
+          sc = exp2i(e - 127);
+        }
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          ex[h] = 0;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if ((okm >> x) & 1)
+              ex[h] |= static_cast<uint32_t>(__ldg(exps + static_cast<size_t>(row[x]) * nbx +
+                                                   (h * 4 + c4) * 16 / a.gs))
+                       << (8 * x);
+        }
+      }
+    }
+    if (++k < n) load_ids(kt + k, ids);
+
+    const int st = g & 1, s4 = g & 3;
+    float* ss = reinterpret_cast<float*>(sm + SM::kScale) + s4 * 2 * kT + (V ? kT : 0) + dw * 32;
+    // The stage's last reader was the MMA of tile g - 2; the scale stage's the
+    // softmax of tile g - 4, whose P was waited for before that MMA.
+    if (g >= 2 && !__all_sync(0xffffffffu,
+                              tc_wait(bars + (V ? kBarVFree : kBarKFree) + st,
+                                      ((g >> 1) - 1) & 1, abort_flag, a.err)))
+      return;
+    ss[lane] = sc;
+    if constexpr (V) {
+      const float m = warp_max_f32(sok && sc <= FLT_MAX ? sc : 0.f);
+      if (lane == 0) infos[s4].vmax[dw] = m;
+    } else {
+      const uint32_t m = __ballot_sync(0xffffffffu, sok);
+      if (lane == 0) infos[s4].valid[dw] = m;
+    }
+    __syncwarp();
+    // Groups to keep; the others become zero.  In a tile that some row does
+    // not see whole, a non-finite V code would reach rows that mask its token
+    // (0 * NaN): it is zeroed and its token's scale made NaN, for the rows that
+    // do see it.
+    uint32_t keep = okm;
+    if (V && FMT != FP8PA_INT8 && !whole) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        bool nf = false;
+#pragma unroll
+        for (int h = 0; h < H; ++h) nf = nf || codes_nonfinite<FMT>(buf[x][h]);
+        uint32_t any = nf ? 1u : 0u;
+        any |= __shfl_xor_sync(0xffffffffu, any, 8);
+        any |= __shfl_xor_sync(0xffffffffu, any, 16);
+        if (any && ((okm >> x) & 1)) {
+          keep &= ~(1u << x);
+          if (c4 == 0) ss[x * 8 + r8] = __int_as_float(0x7FC00000);
+        }
+      }
+    }
+    uint8_t* dst = dst0 + st * SM::kTile;
+    auto store = [&](int x, int h, const uint4& p, const uint4& q) {
+      *reinterpret_cast<uint4*>(dst + x * kG + h * kC) = p;
+      *reinterpret_cast<uint4*>(dst + x * kG + h * kC + kH) = q;
+    };
+    if (keep == 0xFu && !mx) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          uint4 p, q;
+          codes16_to_f16<FMT>(buf[x][h], p, q);
+          store(x, h, p, q);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const bool kept = (keep >> x) & 1;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          uint4 p, q;
+          codes16_to_f16<FMT>(buf[x][h], p, q);
+          if (mx) {
+            // the block's power of two relative to the row's largest, its scale
+            const int em = static_cast<int>(__float_as_uint(ss[x * 8 + r8]) >> 23) & 0xFF;
+            const int e = (ex[h] >> (8 * x)) & 0xFF;
+            const float f = __int_as_float((max(min(e - em, 0), -126) + 127) << 23);
+            const __half2 f2 = __floats2half2_rn(f, f);
+            const uint32_t fw = *reinterpret_cast<const uint32_t*>(&f2);
+            p = hmul8(p, fw);
+            q = hmul8(q, fw);
+          }
+          if (!kept) p = q = make_uint4(0u, 0u, 0u, 0u);
+          store(x, h, p, q);
+        }
+      }
+    }
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(bars + kBarScale + s4);
+      mbar_arrive(bars + (V ? kBarVFull : kBarKFull) + st);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- kernel
 // VAR: 0 no score modifier but the masks, 1 distance bias, 2 capped scores
 // (with or without a bias).
@@ -383,11 +601,10 @@ template <int D, int FMT, int VAR>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs a,
                                                               const PlanView pv) {
   using SM = Smem<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
+  // used as it stands, so that its accesses stay in the shared space
+  extern __shared__ __align__(128) uint8_t sm[];
+  uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + SM::kMisc);
+  int& s_abort = *reinterpret_cast<int*>(sm + SM::kMisc + 4);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
   float* scales = reinterpret_cast<float*>(sm + SM::kScale);
   StageInfo* infos = reinterpret_cast<StageInfo*>(sm + SM::kInfo);
@@ -399,21 +616,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
   if (u0 >= u1) return;
   const int it0 = pv.item[blockIdx.x];
 
-  if (warp == 12) tmem_alloc(&s_tmem, 512);
+  if (warp == 16) tmem_alloc(&s_tmem, 512);
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < kNumBars; ++i) {
-      mbar_init(bars + i, i < kBarKFree ? 4 : 1);
+      mbar_init(bars + i, i >= kBarKFree ? 1 : (i >= kBarScale && i < kBarKFull ? 8 : 4));
     }
     fence_barrier_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_relinquish();
+  if (warp == 16) tmem_relinquish();
   const uint32_t tmem = s_tmem;
   int* abort_flag = &s_abort;
-  const int lgbs = 31 - __clz(a.bs);  // block sizes are powers of two
   auto wait = [&](int bar, uint32_t parity) {
     return tc_wait(bars + bar, parity, abort_flag, a.err);
   };
@@ -422,297 +638,70 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
     return __all_sync(0xffffffffu, tc_wait(bars + bar, parity, abort_flag, a.err)) != 0;
   };
 
-  if (warp == 12) {
+  if (warp == 16) {
     // ================================================= MMA issuer
     if (lane == 0) {
       const uint32_t idesc_s = tc_idesc(0, 0, 0, 0, 128, kT);  // f16, both K-major
       const uint32_t idesc_o = tc_idesc(0, 0, 0, 1, 128, D);   // A in TMEM, B MN-major
       const uint32_t base = smem_u32(sm);
-      const uint64_t dq[2] = {tc_desc(base + SM::kQ, 2048, 128, 0),
-                              tc_desc(base + SM::kQ + SM::kTile, 2048, 128, 0)};
-      const uint64_t dk[2] = {tc_desc(base + SM::kK, 2048, 128, 0),
-                              tc_desc(base + SM::kK + SM::kTile, 2048, 128, 0)};
-      const uint64_t dv[2] = {tc_desc(base + SM::kV, D * 16, 128, 0),
-                              tc_desc(base + SM::kV + SM::kTile, D * 16, 128, 0)};
+      const uint64_t dq0 = tc_desc(base + SM::kQ, 2048, 128, 0);
+      const uint64_t dk0 = tc_desc(base + SM::kK, 2048, 128, 0);
+      const uint64_t dv0 = tc_desc(base + SM::kV, D * 16, 128, 0);
+      constexpr uint32_t kNext = SM::kTile >> 4;  // the other row tile or stage
       auto mma_s = [&](int t, int st) {  // S_t = Q_t K^T
+        const uint64_t dq = dq0 + t * kNext, dk = dk0 + st * kNext;
+        const uint32_t d = tmem + t * kT;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          tc_mma_f16(tmem + t * kT, dq[t] + k * (4096 >> 4), dk[st] + k * (4096 >> 4), idesc_s,
-                     k > 0);
+          tc_mma_f16(d, dq + k * (4096 >> 4), dk + k * (4096 >> 4), idesc_s, k > 0);
+        tc_commit(bars + kBarS + t);
       };
       auto mma_o = [&](int t, int st, bool first) {  // O_t += P_t V
+        const uint64_t dv = dv0 + st * kNext;
+        const uint32_t d = tmem + 256 + t * 128, p = tmem + t * kT;
 #pragma unroll
         for (int k = 0; k < kT / 16; ++k)
-          tc_mma_f16_ts(tmem + 256 + t * 128, tmem + t * kT + k * 8,
-                        dv[st] + k * (2 * D * 16 >> 4), idesc_o, !(first && k == 0));
+          tc_mma_f16_ts(d, p + k * 8, dv + k * (2 * D * 16 >> 4), idesc_o, !(first && k == 0));
       };
-      uint32_t g = 0;     // tiles done by this CTA
-      uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;  // Q and P tiles consumed
+      uint32_t g = 0;              // tiles done by this CTA
+      uint32_t nq = 0, np = 0;     // bit t: phase of row tile t's Q and P
       bool ok = true;
       for (int it = it0, u = u0; u < u1 && ok; ++it) {
         const Item im = load_item(a, pv, it, u, u1);
         const int n = im.t1 - im.t0;
         u += n;
-        const bool two = im.rows > 128;
-        ok = wait(kBarQ, nq0 & 1) && (!two || wait(kBarQ + 1, nq1 & 1)) &&
-             wait(kBarKFull + (g & 1), (g >> 1) & 1);
-        if (!ok) break;
-        ++nq0;
-        nq1 += two ? 1 : 0;
-        tc_fence_after();
-        mma_s(0, g & 1);
-        tc_commit(bars + kBarS);
-        if (two) {
-          mma_s(1, g & 1);
-          tc_commit(bars + kBarS + 1);
-        }
-        tc_commit(bars + kBarKFree + (g & 1));
-        for (int k = 0; k < n && ok; ++k, ++g) {
-          const uint32_t g1 = g + 1;
+        const int two = im.rows > 128 ? 2 : 1;
+        // k = -1 issues the first S of the row tiles, k >= 0 P V of tile k and
+        // S of tile k + 1
+        for (int k = -1; k < n && ok; ++k) {
           const bool more = k + 1 < n;
+          const uint32_t g1 = g + (k >= 0 ? 1 : 0);  // tile k + 1
           if (more) ok = wait(kBarKFull + (g1 & 1), (g1 >> 1) & 1);
-          ok = ok && wait(kBarVFull + (g & 1), (g >> 1) & 1) && wait(kBarP, np0 & 1);
-          if (!ok) break;
-          ++np0;
-          tc_fence_after();
-          mma_o(0, g & 1, k == 0);
-          if (!two) tc_commit(bars + kBarVFree + (g & 1));
-          if (more) {
-            mma_s(0, g1 & 1);
-            tc_commit(bars + kBarS);
-          } else {
-            tc_commit(bars + kBarO);
-          }
-          if (two) {
-            if (!(ok = wait(kBarP + 1, np1 & 1))) break;
-            ++np1;
+          if (k >= 0) ok = ok && wait(kBarVFull + (g & 1), (g >> 1) & 1);
+#pragma unroll 1
+          for (int t = 0; t < two && ok; ++t) {
+            const uint32_t phase = k < 0 ? nq : np;
+            ok = wait((k < 0 ? kBarQ : kBarP) + t, (phase >> t) & 1);
+            if (!ok) break;
+            if (k < 0) nq ^= 1u << t;
+            else np ^= 1u << t;
             tc_fence_after();
-            mma_o(1, g & 1, k == 0);
-            tc_commit(bars + kBarVFree + (g & 1));
-            if (more) {
-              mma_s(1, g1 & 1);
-              tc_commit(bars + kBarS + 1);
-            } else {
-              tc_commit(bars + kBarO + 1);
+            if (k >= 0) {
+              mma_o(t, g & 1, k == 0);
+              if (t + 1 == two) tc_commit(bars + kBarVFree + (g & 1));
+              if (!more) tc_commit(bars + kBarO + t);
             }
+            if (more) mma_s(t, g1 & 1);
           }
           if (more) tc_commit(bars + kBarKFree + (g1 & 1));
+          g = g1;
         }
       }
     }
+  } else if (warp >= 12) {
+    convert_tiles<D, FMT, true>(a, pv, sm, abort_flag, it0, u0, u1, warp - 12, lane);
   } else if (warp >= 8) {
-    // ================================================= converting warps
-    // Warp dw has tokens 32 dw .. + 31 of a tile: four groups of 8 rows, of
-    // which a lane holds row r8 and the 16-byte chunks c4 (and c4 + 4).  Loads
-    // take 64 contiguous bytes of 8 rows, stores 8 rows of a core matrix.
-    const int dw = warp - 8, r8 = lane & 7, c4 = lane >> 3;
-    constexpr int H = D / 64;  // 16-byte chunks of a row per lane
-    const bool mx = a.mode == FP8PA_SCALE_MX_BLOCK;
-    const int nbx = mx ? D / a.gs : 0;
-    uint8_t* kdst = sm + SM::kK + dw * 512 + c4 * 4096 + r8 * 16;
-    uint8_t* vdst = sm + SM::kV + dw * (D * 64) + c4 * 256 + r8 * 16;
-
-    // The tile being loaded: its item, and what a lane keeps of it.  Tokens
-    // that no row of the item sees are neither looked up nor read.
-    struct Next {
-      uint32_t row[4];  // code rows of the lane's tokens
-      uint32_t kx[H], vx[H];  // MX: exponent bytes of the lane's chunks, by group
-      uint32_t okm;     // ... that are to be read
-      float ks, vs;     // scales of token 32 dw + lane
-      bool sok, whole;  // ... that exists; every row sees every token
-    };
-    int it = it0, u = u0, k = 0, n = 0;
-    Item im;
-    int lo = 0, hi = 0, wB = 0, pA = 0;
-    auto open_item = [&]() {
-      im = load_item(a, pv, it, u, u1);
-      n = im.t1 - im.t0;
-      u += n;
-      pA = im.c.L - im.c.n + im.row0 / a.G;
-      const int pB = im.c.L - im.c.n + (im.row0 + im.rows - 1) / a.G;
-      wB = a.window > 0 ? max(pB - a.window + 1, 0) : 0;
-      lo = a.window > 0 ? max(pA - a.window + 1, 0) : 0;
-      hi = pB + 1;
-    };
-    auto block_of = [&](int j) {
-      const int blk = __ldg(a.block_tables + static_cast<long>(im.b) * a.max_blocks +
-                            static_cast<int>(static_cast<uint32_t>(j) >> lgbs));
-      return blk >= 0 && blk < a.num_blocks ? blk : -1;
-    };
-    auto locate = [&](Next& t) {
-      const int j0 = tile_token(im, im.t0 + k);
-      t.whole = (j0 >= wB && j0 + kT - 1 <= pA) || j0 + kT <= im.c.pre;
-      t.okm = 0;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int j = j0 + dw * 32 + g * 8;
-        t.row[g] = 0;
-        if ((j < hi && j + 8 > lo) || j < im.c.pre) {
-          const int blk = block_of(j);
-          if (blk >= 0) {
-            t.row[g] = (static_cast<uint32_t>(blk) * a.hkv + im.kvh) * a.bs + (j & (a.bs - 1)) + r8;
-            const int x = j + r8;
-            if ((x < hi && x >= lo) || x < im.c.pre) t.okm |= 1u << g;
-          } else if (lane == 0) {
-            raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
-          }
-        }
-      }
-      if (FMT != FP8PA_INT8 && mx) {
-        auto byte_of = [&](const float* sc, int g, int h) {
-          return static_cast<uint32_t>(__ldg(reinterpret_cast<const uint8_t*>(sc) +
-                                             static_cast<size_t>(t.row[g]) * nbx +
-                                             (h * 4 + c4) * 16 / a.gs));
-        };
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          t.kx[h] = t.vx[h] = 0;
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            if (!((t.okm >> g) & 1)) continue;
-            t.kx[h] |= byte_of(a.k_scale, g, h) << (8 * g);
-            t.vx[h] |= byte_of(a.v_scale, g, h) << (8 * g);
-          }
-        }
-      }
-      const int j = j0 + dw * 32 + lane;
-      t.sok = false;
-      t.ks = t.vs = 1.f;
-      if ((j < hi && j >= lo) || j < im.c.pre) {
-        const int blk = block_of(j);
-        if (blk >= 0) {
-          t.sok = true;
-          const long rw = (static_cast<long>(blk) * a.hkv + im.kvh) * a.bs + (j & (a.bs - 1));
-          if (a.mode == FP8PA_SCALE_TOKEN_HEAD) {
-            t.ks = __ldg(a.k_scale + rw);
-            t.vs = __ldg(a.v_scale + rw);
-          } else if (a.mode == FP8PA_SCALE_SEGMENT) {
-            t.ks = __ldg(a.k_scale + static_cast<long>(blk) * a.hp + im.kvh);
-            t.vs = __ldg(a.v_scale + static_cast<long>(blk) * a.hp + im.kvh);
-          } else if (mx) {
-            const uint8_t* kx = reinterpret_cast<const uint8_t*>(a.k_scale) + rw * nbx;
-            const uint8_t* vx = reinterpret_cast<const uint8_t*>(a.v_scale) + rw * nbx;
-            int ek = 0, ev = 0;
-            for (int x = 0; x < nbx; ++x) {
-              ek = max(ek, static_cast<int>(__ldg(kx + x)));
-              ev = max(ev, static_cast<int>(__ldg(vx + x)));
-            }
-            t.ks = exp2i(ek - 127);
-            t.vs = exp2i(ev - 127);
-          }
-        }
-      }
-    };
-    auto load_codes = [&](const Next& t, const uint8_t* cache, uint4 (&buf)[4][H]) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const uint4* src =
-            reinterpret_cast<const uint4*>(cache + static_cast<size_t>(t.row[g]) * D) + c4;
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-          buf[g][h] = (t.okm >> g) & 1 ? __ldg(src + h * 4) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    // Convert the buffered codes into a tile.  `keep`: groups whose row is
-    // wanted, the others become zero.  MX blocks take their power of two
-    // relative to the row's largest, which the row's scale `sc` holds.
-    auto store_tile = [&](const uint4 (&buf)[4][H], uint8_t* dst, int gstep, int cstep, int hstep,
-                          const float* sc, const uint32_t (&ex)[H], uint32_t keep) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          uint4 x, y;
-          codes16_to_f16<FMT>(buf[g][h], x, y);
-          if (FMT != FP8PA_INT8 && mx && ((keep >> g) & 1)) {
-            const int em = static_cast<int>(__float_as_uint(sc[g * 8 + r8]) >> 23);
-            const int e = (ex[h] >> (8 * g)) & 0xFF;
-            const float f = __int_as_float((max(e - em, -126) + 127) << 23);
-            const __half2 f2 = __floats2half2_rn(f, f);
-            const uint32_t fw = *reinterpret_cast<const uint32_t*>(&f2);
-            x = hmul8(x, fw);
-            y = hmul8(y, fw);
-          }
-          if (keep != 0xFu && ((keep >> g) & 1) == 0) x = y = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(dst + g * gstep + h * cstep) = x;
-          *reinterpret_cast<uint4*>(dst + g * gstep + h * cstep + hstep) = y;
-        }
-      }
-    };
-
-    uint4 kb[4][H], vb[4][H];
-    Next t;
-    open_item();
-    locate(t);
-    load_codes(t, a.k_cache, kb);
-    load_codes(t, a.v_cache, vb);
-    for (uint32_t g = 0;; ++g) {
-      const int st = g & 1, s4 = g & 3;
-      float* sk = scales + s4 * 2 * kT + dw * 32;
-      float* sv = sk + kT;
-      // Scale stage s4 was last read by the softmax of tile g - 4, whose P V
-      // is done: the V stage of tile g - 1 was waited for, and with it P V of
-      // tile g - 3.
-      if (g >= 2 && !wait_warp(kBarKFree + st, ((g >> 1) - 1) & 1)) break;
-      const uint32_t vmask = __ballot_sync(0xffffffffu, t.sok);
-      const float vmx = warp_max_f32(t.sok && t.vs <= FLT_MAX ? t.vs : 0.f);
-      sk[lane] = t.ks;
-      sv[lane] = t.vs;
-      if (lane == 0) {
-        infos[s4].valid[dw] = vmask;
-        infos[s4].vmax[dw] = vmx;
-      }
-      __syncwarp();
-      store_tile(kb, kdst + st * SM::kTile, 128, 4 * 4096, 2048, sk, t.kx, t.okm);
-      // In a tile that some row does not see whole, a non-finite V code would
-      // reach rows that mask its token (0 * NaN): it is zeroed and its token's
-      // scale made NaN, for the rows that do see it.
-      uint32_t keep = t.okm;
-      if (FMT != FP8PA_INT8 && !t.whole) {
-#pragma unroll
-        for (int gg = 0; gg < 4; ++gg) {
-          bool nf = false;
-#pragma unroll
-          for (int h = 0; h < H; ++h) nf = nf || codes_nonfinite<FMT>(vb[gg][h]);
-          uint32_t any = nf ? 1u : 0u;
-          any |= __shfl_xor_sync(0xffffffffu, any, 8);
-          any |= __shfl_xor_sync(0xffffffffu, any, 16);
-          if (any && ((t.okm >> gg) & 1)) {
-            keep &= ~(1u << gg);
-            if (c4 == 0) sv[gg * 8 + r8] = __int_as_float(0x7FC00000);
-          }
-        }
-      }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bars + kBarScale + s4);
-        mbar_arrive(bars + kBarKFull + st);
-      }
-      // the tile behind this one: its K codes are on their way while V is
-      // converted, its V codes while the next K is
-      uint32_t vx[H];
-#pragma unroll
-      for (int h = 0; h < H; ++h) vx[h] = t.vx[h];
-      bool more = true;
-      if (++k == n) {
-        k = 0;
-        ++it;
-        more = u < u1;
-        if (more) open_item();
-      }
-      if (more) {
-        locate(t);
-        load_codes(t, a.k_cache, kb);
-      }
-      if (g >= 2 && !wait_warp(kBarVFree + st, ((g >> 1) - 1) & 1)) break;
-      store_tile(vb, vdst + st * SM::kTile, D * 16, 4 * 256, 128, sv, vx, keep);
-      if (more) load_codes(t, a.v_cache, vb);
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + kBarVFull + st);
-      if (!more) break;
-    }
+    convert_tiles<D, FMT, false>(a, pv, sm, abort_flag, it0, u0, u1, warp - 8, lane);
   } else {
     // ================================================= softmax warps
     const int t = warp >> 2;            // row tile
@@ -743,12 +732,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
         const float sgn = a.sm_scale < 0.f ? -1.f : 1.f;
         const bool st = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
         const float* kc = a.k_scale + static_cast<long>(im.kvh) * D;
-        uint4 raw[D / 8];
         float amax = 0.f;
-#pragma unroll
-        for (int x = 0; x < D / 8; ++x) raw[x] = __ldg(src + x);
         auto get = [&](int x, float (&f)[8]) {
-          const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+          const uint4 raw = __ldg(src + x);
+          const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             f[2 * e] = __uint_as_float(w[e] << 16) * sgn;
@@ -759,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
             for (int e = 0; e < 8; ++e) f[e] *= __ldg(kc + x * 8 + e);
           }
         };
-#pragma unroll
+#pragma unroll 4
         for (int x = 0; x < D / 8; ++x) {
           float f[8];
           get(x, f);
@@ -769,8 +756,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
         const int eq = amax > 0.f ? exp_above(amax) : 0;
         const float fq = exp2i(14 - eq);
         uint8_t* dst = sm + SM::kQ + t * SM::kTile + (rl >> 3) * 128 + (rl & 7) * 16;
-#pragma unroll
-        for (int x = 0; x < D / 8; ++x) {
+#pragma unroll 4
+        for (int x = 0; x < D / 8; ++x) {  // from L1 this time
           float f[8];
           get(x, f);
           const uint4 o = make_uint4(pack_half2(f[0] * fq, f[1] * fq),
@@ -825,28 +812,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           l *= al;
           if (k == 0) return;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(to + c * 32, o);
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(to + c * 16, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-            tmem_st32(to + c * 32, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+            tmem_st16(to + c * 16, o);
           }
         };
         auto bound_of = [&](float zmax, float vmax) {
           return zmax + static_cast<float>(min(max(exp_above(vmax), -60), 120));
         };
         if (whole && (VAR < 2 || a.cap <= kCapFast)) {
-          // ---- every row sees the whole tile: one pass for the largest score,
-          // one for P, 32 scores at a time, the next 32 on their way from TMEM
+          // ---- every row sees the whole tile: one pass that scales the scores
+          // and finds the largest, one for P, 16 scores at a time, the next 16
+          // on their way from TMEM.  Between the passes the scaled scores stay
+          // in TMEM: reading the K scales a second time would cost shared-memory
+          // bandwidth, which the MMAs' operands need.
           const ulonglong2* sk2 = reinterpret_cast<const ulonglong2*>(sk);
           const ulonglong2* sv2 = reinterpret_cast<const ulonglong2*>(sv);
           const uint64_t zs2 = f2_pack(zs, zs);
           // the bias of tokens 2 i, 2 i + 1: -slope (pos - j)
           const float b0 = VAR > 0 ? slope * static_cast<float>(j0 - pos) : 0.f;
           const uint64_t bias = f2_pack(b0, b0 + slope), step = f2_pack(2.f * slope, 2.f * slope);
-          auto score = [&](const uint32_t* r, uint64_t sc, int i, uint64_t bias) {
+          auto score = [&](const uint32_t* r, uint64_t sc, uint64_t bias, int i) {
             uint64_t z = f2_mul(f2_pack(__uint_as_float(r[0]), __uint_as_float(r[1])), sc);
             if constexpr (VAR > 0) {
               const uint64_t b = f2_fma(
@@ -863,62 +853,64 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
             }
             return z;
           };
-          uint32_t raw[2][32];
-          tmem_ld32(ts, raw[0]);
+          uint32_t raw[2][16];
+          tmem_ld16(ts, raw[0]);
           float m4[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) m4[x] = __int_as_float(0xff800000);
+#pragma unroll 1
+          for (int c2 = 0; c2 < 8; c2 += 2) {
+            const uint64_t b2 = f2_fma(step, f2_pack(c2 * 8.f, c2 * 8.f), bias);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld_wait();
-            tmem_ld32(ts + ((c + 1) & 3) * 32, raw[(c + 1) & 1]);
-            uint32_t* r = raw[c & 1];
+            for (int cc = 0; cc < 2; ++cc) {
+              const int c = c2 + cc;
+              tmem_ld_wait();
+              // (the last load is not used)
+              tmem_ld16(ts + ((c + 1) & 7) * 16, raw[cc ^ 1]);
+              uint32_t* r = raw[cc];
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const ulonglong2 s = sk2[c * 8 + i / 2];
+              for (int i = 0; i < 8; i += 2) {
+                const ulonglong2 s = sk2[c * 4 + i / 2];
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                float p, q;
-                const uint64_t z = score(r + (i + x) * 2, x ? s.y : s.x, c * 16 + i + x, bias);
-                f2_unpack(z, p, q);
-                m4[(i + x) & 3] = fmaxf(fmaxf(m4[(i + x) & 3], p), q);
-                if constexpr (VAR == 2) {
+                for (int x = 0; x < 2; ++x) {
+                  float p, q;
+                  const uint64_t z = score(r + (i + x) * 2, x ? s.y : s.x, b2, cc * 8 + i + x);
+                  f2_unpack(z, p, q);
+                  m4[(i + x) & 3] = fmaxf(fmaxf(m4[(i + x) & 3], p), q);
                   r[(i + x) * 2] = __float_as_uint(p);
                   r[(i + x) * 2 + 1] = __float_as_uint(q);
                 }
               }
+              tmem_st16(ts + c * 16, raw[cc]);
             }
-            // a capped score is not computed twice
-            if constexpr (VAR == 2) tmem_st32(ts + c * 32, raw[c & 1]);
           }
+          tmem_ld_wait();
+          tmem_st_wait();
+          tmem_ld16(ts, raw[0]);
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           const float zf = VAR > 0 ? 1.f : zs;
           move_ref(bound_of(mx * zf, fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w))));
           const float c0 = kShift - ref;
           const uint64_t zf2 = f2_pack(zf, zf), c02 = f2_pack(c0, c0);
-          const uint64_t bias2 = f2_add(bias, c02);  // the exponent's offset in it too
-          uint64_t la = 0, lb = 0;                    // (0.f, 0.f)
-          if constexpr (VAR == 2) {
-            tmem_st_wait();
-            tmem_ld32(ts, raw[0]);
-          }
+          uint64_t la = 0, lb = 0;  // (0.f, 0.f)
+#pragma unroll 1
+          for (int c2 = 0; c2 < 8; c2 += 2) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int cc = 0; cc < 2; ++cc) {
+            const int c = c2 + cc;
             tmem_ld_wait();
-            if (c < 3) tmem_ld32(ts + (c + 1) * 32, raw[(c + 1) & 1]);
-            const uint32_t* r = raw[c & 1];
-            uint32_t pw[16];
+            if (cc == 0 || c2 < 6) tmem_ld16(ts + (c + 1) * 16, raw[cc ^ 1]);
+            const uint32_t* r = raw[cc];
+            uint32_t pw[8];
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const ulonglong2 v = sv2[c * 8 + i / 2], s = sk2[c * 8 + i / 2];
+            for (int i = 0; i < 8; i += 2) {
+              const ulonglong2 v = sv2[c * 4 + i / 2];
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 float p, q;
-                const uint64_t z =
-                    VAR == 2 ? f2_pack(__uint_as_float(r[(i + x) * 2]),
-                                       __uint_as_float(r[(i + x) * 2 + 1]))
-                             : score(r + (i + x) * 2, x ? s.y : s.x, c * 16 + i + x, bias2);
-                f2_unpack(VAR == 2 ? f2_add(z, c02) : (VAR ? z : f2_fma(z, zf2, c02)), p, q);
+                const uint64_t z = f2_pack(__uint_as_float(r[(i + x) * 2]),
+                                           __uint_as_float(r[(i + x) * 2 + 1]));
+                f2_unpack(VAR > 0 ? f2_add(z, c02) : f2_fma(z, zf2, c02), p, q);
                 const uint64_t p2 = f2_pack(ex2(p), ex2(q));
                 if (x) lb = f2_add(lb, p2);
                 else la = f2_add(la, p2);
@@ -926,7 +918,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
                 pw[i + x] = pack_half2(p, q);
               }
             }
-            tmem_st16(ts + c * 16, pw);
+            tmem_st8(ts + c * 8, pw);
+          }
           }
           float x, y;
           f2_unpack(f2_add(la, lb), x, y);
@@ -937,16 +930,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           const float zf = VAR > 0 ? 1.f : zs;
           float mx = __int_as_float(0xff800000), vmax = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t raw[32];
-            tmem_ld32(ts + c * 32, raw);
+          for (int c = 0; c < 8; ++c) {
+            uint32_t raw[16];
+            tmem_ld16(ts + c * 16, raw);
             tmem_ld_wait();
-            const int jc = j0 + c * 32;
-            const uint32_t mw =
-                (word_bits(jc, wf, pos + 1) | word_bits(jc, 0, pre)) & infos[s4].valid[c];
+            const int jc = j0 + c * 16;
+            const uint32_t mw = (word_bits(jc, wf, pos + 1) | word_bits(jc, 0, pre)) &
+                                (infos[s4].valid[c >> 1] >> (16 * (c & 1)));
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float z = __uint_as_float(raw[i]) * sk[c * 32 + i];
+            for (int i = 0; i < 16; ++i) {
+              float z = __uint_as_float(raw[i]) * sk[c * 16 + i];
               if constexpr (VAR > 0) {
                 z *= zs;
                 if constexpr (VAR == 2) z = cap_log2 * tanh_f32(z * (0.5f / kLog2e));
@@ -955,29 +948,29 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
               const bool see = (mw >> i) & 1;
               z = see ? z : __int_as_float(0xff800000);
               mx = fmaxf(mx, z);
-              vmax = fmaxf(vmax, see ? sv[c * 32 + i] : 0.f);
+              vmax = fmaxf(vmax, see ? sv[c * 16 + i] : 0.f);
               raw[i] = __float_as_uint(z);
             }
-            tmem_st32(ts + c * 32, raw);
+            tmem_st16(ts + c * 16, raw);
           }
           tmem_st_wait();
           move_ref(bound_of(mx * zf, vmax));
           const float c0 = kShift - ref;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t raw[32], pw[16];
-            tmem_ld32(ts + c * 32, raw);
+          for (int c = 0; c < 8; ++c) {
+            uint32_t raw[16], pw[8];
+            tmem_ld16(ts + c * 16, raw);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
+            for (int i = 0; i < 16; i += 2) {
               const float p = ex2(fmaf(__uint_as_float(raw[i]), zf, c0));
               const float q = ex2(fmaf(__uint_as_float(raw[i + 1]), zf, c0));
               l += p + q;
               // a masked token's scale may be anything
-              pw[i / 2] = pack_half2(p != 0.f ? p * sv[c * 32 + i] : 0.f,
-                                     q != 0.f ? q * sv[c * 32 + i + 1] : 0.f);
+              pw[i / 2] = pack_half2(p != 0.f ? p * sv[c * 16 + i] : 0.f,
+                                     q != 0.f ? q * sv[c * 16 + i + 1] : 0.f);
             }
-            tmem_st16(ts + c * 16, pw);
+            tmem_st8(ts + c * 8, pw);
           }
         }
         tmem_st_wait();
@@ -999,29 +992,29 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
       const int slot = blockIdx.x * 2 + (im.t0 > 0 ? 0 : 1);
       const bool stat = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
       const float* vch = a.v_scale + static_cast<long>(im.kvh) * D;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(to + c * 32, o);
+#pragma unroll 2
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t o[16];
+        tmem_ld16(to + c * 16, o);
         tmem_ld_wait();
         if (!live) continue;
-        float f[32];
+        float f[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < 16; ++i) {
           f[i] = __uint_as_float(o[i]) * inv;
-          if (stat) f[i] *= __ldg(vch + c * 32 + i);
+          if (stat) f[i] *= __ldg(vch + c * 16 + i);
         }
         if (piece || a.out_f32) {
-          float* dst = piece ? pv.o + (static_cast<long>(slot) * kRows + r) * D + c * 32
-                             : reinterpret_cast<float*>(a.out) + grow * D + c * 32;
+          float* dst = piece ? pv.o + (static_cast<long>(slot) * kRows + r) * D + c * 16
+                             : reinterpret_cast<float*>(a.out) + grow * D + c * 16;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
+          for (int i = 0; i < 16; i += 4)
             *reinterpret_cast<float4*>(dst + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
         } else {
           uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + grow * D +
-                                                c * 32);
+                                                c * 16);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2; ++i) {
             uint32_t w[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -1040,14 +1033,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
 
   // ---- drain and free: no MMA may still be in flight
   __syncwarp();
-  if (warp == 12 && lane == 0) {
+  if (warp == 16 && lane == 0) {
     tc_commit(bars + kBarDrain);
     (void)mbar_wait_bounded(bars + kBarDrain, 0, kWaitLimitCycles);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------- merge
@@ -1140,7 +1133,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   plan_layout(static_cast<char*>(a.workspace), a.total_q, a.batch, a.G, a.d, ranges, &pv);
   const int var = a.cap > 0.f ? 2 : (a.slopes ? 1 : 0);
   const PrefillFn fn = a.d == 128 ? pick_fmt<128>(a.fmt, var) : pick_fmt<64>(a.fmt, var);
-  const int smem = (a.d == 128 ? Smem<128>::kBytes : Smem<64>::kBytes) + 128;
+  const int smem = a.d == 128 ? Smem<128>::kBytes : Smem<64>::kBytes;
   if ((e = ensure_smem_attr(reinterpret_cast<const void*>(fn), smem)) != cudaSuccess) return e;
 
   cudaLaunchAttribute pdl[1];
