@@ -27,11 +27,14 @@
 // inside f16 whatever the scales; it moves only when passed by 2^kTau, which
 // is exact, as sums and O carry the same reference.
 //
-// Roles (17 warps): 0-3 and 4-7 the softmax of row tiles 0 and 1 (a thread per
-// row), 8-11 and 12-15 convert K and V codes into shared memory (the next tile's
-// loads in flight meanwhile), 16 issues the MMAs (one thread).  While the tensor cores work on one row tile, the other's softmax runs.
+// Roles (16 warps): 0-3 and 4-7 the softmax of row tiles 0 and 1 (a thread per
+// row), 8-14 convert codes into shared memory, 15 issues the MMAs (one thread).
+// Scores are made in steps of 64 tokens into two TMEM buffers per row tile, so
+// that the softmax of a step runs while the tensor cores make the next one.
 // Every wait is bounded.
 #include <float.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -44,7 +47,9 @@ namespace {
 
 constexpr int kRows = 256;   // rows of a block: two tiles of 128
 constexpr int kT = 128;      // tokens per tile
-constexpr int kThreads = 17 * 32;
+constexpr int kS = 64;       // ... in steps of
+constexpr int kThreads = 512;
+constexpr int kConvWarps = 7, kIssueWarp = 15;
 constexpr int kSnap = 4;     // a cut this near an item's edge moves to it
 constexpr float kShift = 12.f;  // P = 2^(z - ref + 12): at most 2^15 with the lazy bound
 constexpr float kTau = 3.f;     // the reference may lag by 2^3
@@ -265,10 +270,12 @@ struct StageInfo {
   float vmax[4];      // largest V scale of each 32 tokens
 };
 
-// Barriers: one arrival per warp of a warpgroup on the first twelve (the scales:
-// of the two converting groups), one commit of the tensor cores on the others.
-enum { kBarQ = 0, kBarScale = 2, kBarKFull = 6, kBarVFull = 8, kBarP = 10, kBarKFree = 12,
-       kBarVFree = 14, kBarS = 16, kBarO = 18, kBarDrain = 20, kNumBars = 21 };
+// Barriers: one arrival per warp of four (the scales: per job of eight) on the
+// first fourteen, one commit of the tensor cores on the others.  P, S and O (P V
+// of the step is done): index 2 * row tile + score buffer, so that no waiter is
+// ever two phases behind.
+enum { kBarQ = 0, kBarScale = 2, kBarKFull = 6, kBarVFull = 8, kBarP = 10, kBarKFree = 14,
+       kBarVFree = 16, kBarS = 18, kBarO = 22, kBarDrain = 26, kNumBars = 27 };
 
 // ---------------------------------------------------------------- conversions
 // 16 codes -> 16 f16 (two 16-byte core-matrix rows), exactly.
@@ -334,6 +341,15 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
       : "memory");
 }
 
+// Registers that a tcgen05.ld filled: what uses them stays behind the
+// tcgen05.wait::ld before this.
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[16]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], one thread.
 __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                               bool accumulate) {
@@ -357,7 +373,7 @@ __device__ __forceinline__ uint32_t word_bits(int t0, int lo, int hi) {
 struct Item {
   int b, kvh, row0, rows;  // first row within the request, rows of the block
   Chunk c;
-  Tiles tl;
+  Tiles tl{0, 0, 0};
   int t0, t1;
 };
 
@@ -387,59 +403,38 @@ __device__ __forceinline__ int tile_token(const Item& it, int k) {
 }
 
 // ---------------------------------------------------------------- conversion
-// One converting warp's work for the CTA's range: tokens 32 dw .. + 31 of every
-// tile of K (V false) or V.  A lane holds row r8 of four 8-row groups and, of
-// each, the 16-byte chunks c4 (and c4 + 4): loads take 64 contiguous bytes of
-// 8 rows, stores the 8 rows of a core matrix, free of bank conflicts.  A tile's
-// codes and scales are loaded as soon as the tile before it is stored, its
-// block ids one tile earlier.
-template <int D, int FMT, bool V>
+// The work of one converting warp.  A tile has eight jobs, 32 tokens of K or V
+// each (part 0-3: K, 4-7: V), dealt round robin over the converting warps.  A
+// lane holds row r8 of four 8-row groups and, of each, the 16-byte chunks c4
+// (and c4 + 4): loads take 64 contiguous bytes of 8 rows, stores the 8 rows of a
+// core matrix, free of bank conflicts.  A job's codes and scales are loaded as
+// soon as the job before it is stored, its block ids one job earlier, and with
+// them its codes are asked for into L2.
+template <int D, int FMT>
 __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanView& pv,
                                               uint8_t* sm, int* abort_flag, int it, int u, int u1,
-                                              int dw, int lane) {
+                                              int first, int lane) {
   using SM = Smem<D>;
   constexpr int H = D / 64;  // 16-byte chunks of a row per lane
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
   StageInfo* infos = reinterpret_cast<StageInfo*>(sm + SM::kInfo);
-  const uint8_t* cache = V ? a.v_cache : a.k_cache;
-  const float* gscale = V ? a.v_scale : a.k_scale;
   const int r8 = lane & 7, c4 = lane >> 3;
   const int lgbs = 31 - __clz(a.bs);  // block sizes are powers of two
   const bool mx = FMT != FP8PA_INT8 && a.mode == FP8PA_SCALE_MX_BLOCK;
   const int nbx = mx ? D / a.gs : 0;
-  constexpr int kG = V ? D * 16 : 128, kC = V ? 4 * 256 : 4 * 4096, kH = V ? 128 : 2048;
-  uint8_t* dst0 = sm + (V ? SM::kV + dw * (4 * kG) + c4 * 256 : SM::kK + dw * (4 * kG) + c4 * 4096) +
-                  r8 * 16;
 
   // the open item: tiles left of it, its block table, the tokens that some row
-  // sees ([lo, hi) and [0, pre); others are neither looked up nor read) and,
-  // for V, those that every row sees
-  Tiles tl;
+  // sees ([lo, hi) and [0, pre); others are neither looked up nor read) and
+  // those that every row sees
+  Tiles tl{0, 0, 0};
   int k = 0, n = 0, kt = 0, kvh = 0, lo = 0, hi = 0, pre = 0, all_lo = 0, all_hi = 0;
   const int32_t* table = nullptr;
-  auto open_item = [&]() {
-    const Item im = load_item(a, pv, it, u, u1);
-    k = 0;
-    n = im.t1 - im.t0;
-    kt = im.t0;
-    u += n;
-    tl = im.tl;
-    kvh = im.kvh;
-    pre = im.c.pre;
-    table = a.block_tables + static_cast<long>(im.b) * a.max_blocks;
-    const int pA = im.c.L - im.c.n + im.row0 / a.G;
-    const int pB = im.c.L - im.c.n + (im.row0 + im.rows - 1) / a.G;
-    lo = a.window > 0 ? max(pA - a.window + 1, 0) : 0;
-    hi = pB + 1;
-    all_lo = a.window > 0 ? max(pB - a.window + 1, 0) : 0;
-    all_hi = pA + 1;
-  };
-  auto token_of = [&](int i) { return (i < tl.np ? i : i + tl.skip) * kT + dw * 32; };
+  auto token_of = [&](int i) { return (i < tl.np ? i : i + tl.skip) * kT; };
   auto wanted = [&](int j) { return (j < hi && j >= lo) || j < pre; };
-  // block ids of the warp's two 16-token halves (a half lies in one block); -1
+  // block ids of a job's two 16-token halves (a half lies in one block); -1
   // where no row sees any of its tokens
-  auto load_ids = [&](int i, int (&id)[2]) {
-    const int j = token_of(i);
+  auto load_ids = [&](int i, int part, int (&id)[2]) {
+    const int j = token_of(i) + (part & 3) * 32;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int t = j + 16 * x;
@@ -448,30 +443,48 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
                   : -1;
     }
   };
+  auto row_of = [&](int blk, int t) {
+    return (static_cast<uint32_t>(blk) * a.hkv + kvh) * a.bs + (t & (a.bs - 1));
+  };
 
-  int ids[2];
-  for (uint32_t g = 0;; ++g) {
-    // ---- the next tile's loads, as soon as the last one is stored
-    if (k == n) {
+  int ids[2], part = first;  // of this job
+  bool have = false;         // ids are loaded
+  for (uint32_t g = 0;;) {   // g: the job's tile, counted over the range
+    while (k >= n) {
       if (u >= u1) return;
-      open_item();
+      const Item im = load_item(a, pv, it, u, u1);
       ++it;
-      load_ids(kt, ids);
+      k -= n;
+      n = im.t1 - im.t0;
+      kt = im.t0;
+      u += n;
+      tl = im.tl;
+      kvh = im.kvh;
+      pre = im.c.pre;
+      table = a.block_tables + static_cast<long>(im.b) * a.max_blocks;
+      const int pA = im.c.L - im.c.n + im.row0 / a.G;
+      const int pB = im.c.L - im.c.n + (im.row0 + im.rows - 1) / a.G;
+      lo = a.window > 0 ? max(pA - a.window + 1, 0) : 0;
+      hi = pB + 1;
+      all_lo = a.window > 0 ? max(pB - a.window + 1, 0) : 0;
+      all_hi = pA + 1;
     }
-    const int j = token_of(kt + k);
-    const bool whole =
-        (j - dw * 32 >= all_lo && j - dw * 32 + kT <= all_hi) || j - dw * 32 + kT <= pre;
+    if (!have) load_ids(kt + k, part, ids);
+    const bool V = part >= 4;
+    const int dw = part & 3;
+    const uint8_t* cache = V ? a.v_cache : a.k_cache;
+    const float* gscale = V ? a.v_scale : a.k_scale;
+    const int j0 = token_of(kt + k), j = j0 + dw * 32;
+    const bool whole = (j0 >= all_lo && j0 + kT <= all_hi) || j0 + kT <= pre;
     uint4 buf[4][H];
     uint32_t okm = 0;  // groups whose row is wanted and exists
-    uint32_t row[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const int blk = ids[x >> 1], t = j + x * 8 + r8;
       const bool ok = wanted(t) && blk >= 0 && blk < a.num_blocks;
-      row[x] = ok ? (static_cast<uint32_t>(blk) * a.hkv + kvh) * a.bs + (t & (a.bs - 1)) : 0u;
       if (ok) okm |= 1u << x;
-      const uint4* src =
-          reinterpret_cast<const uint4*>(cache + static_cast<size_t>(row[x]) * D) + c4;
+      const uint4* src = reinterpret_cast<const uint4*>(
+                             cache + static_cast<size_t>(ok ? row_of(blk, t) : 0u) * D) + c4;
 #pragma unroll
       for (int h = 0; h < H; ++h)
         buf[x][h] = ok ? __ldg(src + h * 4) : make_uint4(0u, 0u, 0u, 0u);
@@ -482,9 +495,8 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
     {
       const int blk = lane < 16 ? ids[0] : ids[1], t = j + lane;
       sok = wanted(t) && blk >= 0 && blk < a.num_blocks;
-      if (wanted(t) && !sok && !V) raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
-      const long rw =
-          sok ? (static_cast<long>(blk) * a.hkv + kvh) * a.bs + (t & (a.bs - 1)) : 0;
+      if (wanted(t) && !sok) raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
+      const size_t rw = sok ? row_of(blk, t) : 0u;
       if (a.mode == FP8PA_SCALE_TOKEN_HEAD) {
         if (sok) sc = __ldg(gscale + rw);
       } else if (a.mode == FP8PA_SCALE_SEGMENT) {
@@ -502,15 +514,23 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             if ((okm >> x) & 1)
-              ex[h] |= static_cast<uint32_t>(__ldg(exps + static_cast<size_t>(row[x]) * nbx +
-                                                   (h * 4 + c4) * 16 / a.gs))
+              ex[h] |= static_cast<uint32_t>(
+                           __ldg(exps + static_cast<size_t>(row_of(ids[x >> 1], j + x * 8 + r8)) *
+                                            nbx + (h * 4 + c4) * 16 / a.gs))
                        << (8 * x);
         }
       }
     }
-    if (++k < n) load_ids(kt + k, ids);
+    // ---- the job behind this one
+    int nk = k, npart = part + kConvWarps;
+    if (npart >= 8) {
+      npart -= 8;
+      ++nk;
+    }
+    have = nk < n;
+    if (have) load_ids(kt + nk, npart, ids);
 
-    const int st = g & 1, s4 = g & 3;
+    const uint32_t st = g & 1, s4 = g & 3;
     float* ss = reinterpret_cast<float*>(sm + SM::kScale) + s4 * 2 * kT + (V ? kT : 0) + dw * 32;
     // The stage's last reader was the MMA of tile g - 2; the scale stage's the
     // softmax of tile g - 4, whose P was waited for before that MMA.
@@ -519,12 +539,11 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
                                       ((g >> 1) - 1) & 1, abort_flag, a.err)))
       return;
     ss[lane] = sc;
-    if constexpr (V) {
-      const float m = warp_max_f32(sok && sc <= FLT_MAX ? sc : 0.f);
-      if (lane == 0) infos[s4].vmax[dw] = m;
-    } else {
-      const uint32_t m = __ballot_sync(0xffffffffu, sok);
-      if (lane == 0) infos[s4].valid[dw] = m;
+    const uint32_t valid = __ballot_sync(0xffffffffu, sok);
+    const float vmax = warp_max_f32(sok && sc <= FLT_MAX ? sc : 0.f);
+    if (lane == 0) {
+      if (V) infos[s4].vmax[dw] = vmax;
+      else infos[s4].valid[dw] = valid;
     }
     __syncwarp();
     // Groups to keep; the others become zero.  In a tile that some row does
@@ -532,7 +551,7 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
     // (0 * NaN): it is zeroed and its token's scale made NaN, for the rows that
     // do see it.
     uint32_t keep = okm;
-    if (V && FMT != FP8PA_INT8 && !whole) {
+    if (FMT != FP8PA_INT8 && V && !whole) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         bool nf = false;
@@ -547,7 +566,11 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
         }
       }
     }
-    uint8_t* dst = dst0 + st * SM::kTile;
+    // K: core matrices (8 tokens x 8 dims) 128 bytes apart along the tokens,
+    // 2048 along the dims; V: D * 16 along the tokens, 128 along the dims
+    uint8_t* dst = sm + (V ? SM::kV : SM::kK) + st * SM::kTile + r8 * 16 +
+                   (V ? dw * (D * 64) + c4 * 256 : dw * 512 + c4 * 4096);
+    const int kG = V ? D * 16 : 128, kC = V ? 4 * 256 : 4 * 4096, kH = V ? 128 : 2048;
     auto store = [&](int x, int h, const uint4& p, const uint4& q) {
       *reinterpret_cast<uint4*>(dst + x * kG + h * kC) = p;
       *reinterpret_cast<uint4*>(dst + x * kG + h * kC + kH) = q;
@@ -591,6 +614,16 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
       mbar_arrive(bars + kBarScale + s4);
       mbar_arrive(bars + (V ? kBarVFull : kBarKFull) + st);
     }
+    g += nk - k;
+    k = nk;
+    part = npart;
+    if (have && lane < 2) {
+      // the next job's half `lane`: 16 rows of D bytes
+      const int blk = lane ? ids[1] : ids[0], t = token_of(kt + k) + (part & 3) * 32 + lane * 16;
+      if (blk >= 0 && blk < a.num_blocks)
+        prefetch_l2((part >= 4 ? a.v_cache : a.k_cache) + static_cast<size_t>(row_of(blk, t)) * D,
+                    16 * D);
+    }
   }
 }
 
@@ -616,18 +649,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
   if (u0 >= u1) return;
   const int it0 = pv.item[blockIdx.x];
 
-  if (warp == 16) tmem_alloc(&s_tmem, 512);
+  if (warp == kIssueWarp) tmem_alloc(&s_tmem, 512);
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < kNumBars; ++i) {
+    for (int i = 0; i < kNumBars; ++i)
       mbar_init(bars + i, i >= kBarKFree ? 1 : (i >= kBarScale && i < kBarKFull ? 8 : 4));
-    }
     fence_barrier_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) tmem_relinquish();
+  if (warp == kIssueWarp) tmem_relinquish();
   const uint32_t tmem = s_tmem;
   int* abort_flag = &s_abort;
   auto wait = [&](int bar, uint32_t parity) {
@@ -638,92 +670,117 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
     return __all_sync(0xffffffffu, tc_wait(bars + bar, parity, abort_flag, a.err)) != 0;
   };
 
-  if (warp == 16) {
+  if (warp == kIssueWarp) {
     // ================================================= MMA issuer
+    // Steps of 64 tokens: S of step s goes to score buffer s & 1 of its row
+    // tile, where P of step s replaces it; it is issued once P V of step s - 2,
+    // which read the buffer last, is done (MMAs of different shapes need not
+    // complete in the order of their issue).  The softmax of step s - 1 runs
+    // meanwhile.
     if (lane == 0) {
-      const uint32_t idesc_s = tc_idesc(0, 0, 0, 0, 128, kT);  // f16, both K-major
+      const uint32_t idesc_s = tc_idesc(0, 0, 0, 0, 128, kS);  // f16, both K-major
       const uint32_t idesc_o = tc_idesc(0, 0, 0, 1, 128, D);   // A in TMEM, B MN-major
       const uint32_t base = smem_u32(sm);
       const uint64_t dq0 = tc_desc(base + SM::kQ, 2048, 128, 0);
       const uint64_t dk0 = tc_desc(base + SM::kK, 2048, 128, 0);
       const uint64_t dv0 = tc_desc(base + SM::kV, D * 16, 128, 0);
       constexpr uint32_t kNext = SM::kTile >> 4;  // the other row tile or stage
-      auto mma_s = [&](int t, int st) {  // S_t = Q_t K^T
-        const uint64_t dq = dq0 + t * kNext, dk = dk0 + st * kNext;
-        const uint32_t d = tmem + t * kT;
+      // S_t of half `half` of the tile in stage st
+      auto mma_s = [&](int t, uint32_t st, uint32_t half) {
+        const uint64_t dq = dq0 + t * kNext, dk = dk0 + st * kNext + half * (kS * 16 >> 4);
+        const uint32_t d = tmem + t * 128 + half * kS;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           tc_mma_f16(d, dq + k * (4096 >> 4), dk + k * (4096 >> 4), idesc_s, k > 0);
-        tc_commit(bars + kBarS + t);
+        tc_commit(bars + kBarS + t * 2 + half);
       };
-      auto mma_o = [&](int t, int st, bool first) {  // O_t += P_t V
-        const uint64_t dv = dv0 + st * kNext;
-        const uint32_t d = tmem + 256 + t * 128, p = tmem + t * kT;
+      auto mma_o = [&](int t, uint32_t st, uint32_t half, bool first) {  // O_t += P_t V
+        const uint64_t dv = dv0 + st * kNext + half * (kS * 2 * D >> 4);
+        const uint32_t d = tmem + 256 + t * 128, p = tmem + t * 128 + half * kS;
 #pragma unroll
-        for (int k = 0; k < kT / 16; ++k)
+        for (int k = 0; k < kS / 16; ++k)
           tc_mma_f16_ts(d, p + k * 8, dv + k * (2 * D * 16 >> 4), idesc_o, !(first && k == 0));
+        tc_commit(bars + kBarO + t * 2 + half);
       };
-      uint32_t g = 0;              // tiles done by this CTA
-      uint32_t nq = 0, np = 0;     // bit t: phase of row tile t's Q and P
+      uint32_t g = 0;      // tiles done by this CTA
+      uint32_t nq = 0;     // bit t: phase of row tile t's Q
+      uint32_t np = 0;     // bit 2 t + half: phase of a P buffer
+      uint32_t no = 0;     // ... and of its P V
       bool ok = true;
       for (int it = it0, u = u0; u < u1 && ok; ++it) {
         const Item im = load_item(a, pv, it, u, u1);
-        const int n = im.t1 - im.t0;
+        const int n = im.t1 - im.t0, two = im.rows > 128 ? 2 : 1;
         u += n;
-        const int two = im.rows > 128 ? 2 : 1;
-        // k = -1 issues the first S of the row tiles, k >= 0 P V of tile k and
-        // S of tile k + 1
-        for (int k = -1; k < n && ok; ++k) {
-          const bool more = k + 1 < n;
-          const uint32_t g1 = g + (k >= 0 ? 1 : 0);  // tile k + 1
-          if (more) ok = wait(kBarKFull + (g1 & 1), (g1 >> 1) & 1);
-          if (k >= 0) ok = ok && wait(kBarVFull + (g & 1), (g >> 1) & 1);
+        // the first tile's scores
+        ok = wait(kBarKFull + (g & 1), (g >> 1) & 1);
 #pragma unroll 1
-          for (int t = 0; t < two && ok; ++t) {
-            const uint32_t phase = k < 0 ? nq : np;
-            ok = wait((k < 0 ? kBarQ : kBarP) + t, (phase >> t) & 1);
-            if (!ok) break;
-            if (k < 0) nq ^= 1u << t;
-            else np ^= 1u << t;
+        for (int x = 0; x < 2 * two && ok; ++x) {
+          const int t = x >> 1;
+          if ((x & 1) == 0) {
+            ok = wait(kBarQ + t, (nq >> t) & 1);
+            nq ^= 1u << t;
             tc_fence_after();
-            if (k >= 0) {
-              mma_o(t, g & 1, k == 0);
-              if (t + 1 == two) tc_commit(bars + kBarVFree + (g & 1));
-              if (!more) tc_commit(bars + kBarO + t);
-            }
-            if (more) mma_s(t, g1 & 1);
           }
+          if (ok) mma_s(t, g & 1, x & 1);
+        }
+        if (!ok) break;
+        tc_commit(bars + kBarKFree + (g & 1));
+        for (int k = 0; k < n && ok; ++k) {
+          const bool more = k + 1 < n;
+          const uint32_t g1 = g + 1;
+          ok = wait(kBarVFull + (g & 1), (g >> 1) & 1);
+          if (more) ok = ok && wait(kBarKFull + (g1 & 1), (g1 >> 1) & 1);
+#pragma unroll 1
+          for (uint32_t half = 0; half < 2 && ok; ++half) {
+#pragma unroll 1
+            for (int t = 0; t < two && ok; ++t) {
+              ok = wait(kBarP + t * 2 + half, (np >> (t * 2 + half)) & 1);
+              if (!ok) break;
+              np ^= 1u << (t * 2 + half);
+              tc_fence_after();
+              mma_o(t, g & 1, half, k == 0 && half == 0);
+            }
+#pragma unroll 1
+            for (int t = 0; t < two && ok; ++t) {
+              if (more) {
+                ok = wait(kBarO + t * 2 + half, (no >> (t * 2 + half)) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                mma_s(t, g1 & 1, half);
+              }
+              no ^= 1u << (t * 2 + half);
+            }
+          }
+          if (!ok) break;
+          tc_commit(bars + kBarVFree + (g & 1));
           if (more) tc_commit(bars + kBarKFree + (g1 & 1));
           g = g1;
         }
       }
     }
-  } else if (warp >= 12) {
-    convert_tiles<D, FMT, true>(a, pv, sm, abort_flag, it0, u0, u1, warp - 12, lane);
   } else if (warp >= 8) {
-    convert_tiles<D, FMT, false>(a, pv, sm, abort_flag, it0, u0, u1, warp - 8, lane);
+    convert_tiles<D, FMT>(a, pv, sm, abort_flag, it0, u0, u1, warp - 8, lane);
   } else {
     // ================================================= softmax warps
     const int t = warp >> 2;            // row tile
     const int rl = (warp & 3) * 32 + lane;  // row within it
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + t * kT + lanes, to = tmem + 256 + t * 128 + lanes;
-    uint32_t g = 0, ns = 0, no = 0;  // tiles of the CTA; S tiles and O tiles of this row tile
+    const uint32_t to = tmem + 256 + t * 128 + lanes;
+    uint32_t g = 0, steps = 0;  // tiles of the CTA; steps of this row tile
     bool ok = true;
     for (int it = it0, u = u0; u < u1 && ok; ++it) {
       const Item im = load_item(a, pv, it, u, u1);
       const int n = im.t1 - im.t0;
       u += n;
-      const bool active = t == 0 || im.rows > 128;  // row tile 1 of a short block idles
+      if (t == 1 && im.rows <= 128) {  // row tile 1 of a short block idles
+        g += n;
+        continue;
+      }
       const int r = t * 128 + rl;  // row of the block
       const bool live = r < im.rows;
       const int rr = im.row0 + min(r, im.rows - 1);
       const int qi = rr / a.G, h = im.kvh * a.G + rr % a.G;
       const long grow = (static_cast<long>(im.c.qlo) + qi) * a.hq + h;  // row of q and out
-      if (!active) {  // a block of at most 128 rows
-        g += n;
-        continue;
-      }
       float zs;
       {
         // ---- the row of q, normalised by a power of two, into shared memory
@@ -784,208 +841,183 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
       const float cap_log2 = VAR == 2 ? a.cap * kLog2e : 0.f;
       float ref = kNegBig, l = 0.f;
 
-      for (int k = 0; k < n; ++k, ++g) {
-        const int j0 = tile_token(im, im.t0 + k);
-        const int s4 = g & 3;
-        if (!wait_warp(kBarScale + s4, (g >> 2) & 1) || !wait_warp(kBarS + t, ns & 1)) {
+      for (int s = 0; s < 2 * n; ++s, ++steps) {
+        const int half = s & 1;
+        const uint32_t s4 = (g + (s >> 1)) & 3;
+        const int j0 = tile_token(im, im.t0 + (s >> 1)) + half * kS;
+        if (half == 0 && !wait_warp(kBarScale + s4, ((g + (s >> 1)) >> 2) & 1)) {
           ok = false;
           break;
         }
-        ++ns;
+        if (!wait_warp(kBarS + t * 2 + half, (steps >> 1) & 1)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        const float* sk = scales + s4 * 2 * kT;
+        const uint32_t ts = tmem + t * 128 + half * kS + lanes;
+        const float* sk = scales + s4 * 2 * kT + half * kS;
         const float* sv = sk + kT;
-        const uint4 val = *reinterpret_cast<const uint4*>(infos[s4].valid);
-        const float4 vm = *reinterpret_cast<const float4*>(infos[s4].vmax);
-        const bool whole =
-            ((j0 >= wB && j0 + kT - 1 <= pA) || (VAR == 0 && j0 + kT <= pre)) &&
-            (val.x & val.y & val.z & val.w) == 0xFFFFFFFFu;
-        // Raise the reference to `bound` where it was passed by 2^kTau, and
-        // with it the sum and O.
-        auto move_ref = [&](float bound) {
-          float al = 1.f;
-          if (bound > ref + kTau) {
-            al = ex2(ref - bound);
-            ref = bound;
-          }
-          if (!__any_sync(0xffffffffu, al != 1.f)) return;
-          l *= al;
-          if (k == 0) return;
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld16(to + c * 16, o);
-            tmem_ld_wait();
+        uint32_t raw[4][16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-            tmem_st16(to + c * 16, o);
-          }
-        };
-        auto bound_of = [&](float zmax, float vmax) {
-          return zmax + static_cast<float>(min(max(exp_above(vmax), -60), 120));
-        };
-        if (whole && (VAR < 2 || a.cap <= kCapFast)) {
-          // ---- every row sees the whole tile: one pass that scales the scores
-          // and finds the largest, one for P, 16 scores at a time, the next 16
-          // on their way from TMEM.  Between the passes the scaled scores stay
-          // in TMEM: reading the K scales a second time would cost shared-memory
-          // bandwidth, which the MMAs' operands need.
-          const ulonglong2* sk2 = reinterpret_cast<const ulonglong2*>(sk);
-          const ulonglong2* sv2 = reinterpret_cast<const ulonglong2*>(sv);
-          const uint64_t zs2 = f2_pack(zs, zs);
-          // the bias of tokens 2 i, 2 i + 1: -slope (pos - j)
-          const float b0 = VAR > 0 ? slope * static_cast<float>(j0 - pos) : 0.f;
-          const uint64_t bias = f2_pack(b0, b0 + slope), step = f2_pack(2.f * slope, 2.f * slope);
-          auto score = [&](const uint32_t* r, uint64_t sc, uint64_t bias, int i) {
-            uint64_t z = f2_mul(f2_pack(__uint_as_float(r[0]), __uint_as_float(r[1])), sc);
-            if constexpr (VAR > 0) {
-              const uint64_t b = f2_fma(
-                  step, f2_pack(static_cast<float>(i), static_cast<float>(i)), bias);
+        for (int c = 0; c < 4; ++c) tmem_ld16(ts + c * 16, raw[c]);
+        const uint2 val = *reinterpret_cast<const uint2*>(&infos[s4].valid[half * 2]);
+        const float4 vm = *reinterpret_cast<const float4*>(infos[s4].vmax);
+        // whether every row of the warp sees the whole step
+        const bool whole =
+            ((j0 >= wB && j0 + kS - 1 <= pA) || (VAR == 0 && j0 + kS <= pre)) &&
+            (val.x & val.y) == 0xFFFFFFFFu && (VAR < 2 || a.cap <= kCapFast);
+        float vmax = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
+        const ulonglong2* sk2 = reinterpret_cast<const ulonglong2*>(sk);
+        const ulonglong2* sv2 = reinterpret_cast<const ulonglong2*>(sv);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_landed(raw[c]);
+
+        // ---- scores times K scales (VAR > 0: final scores), and the largest
+        uint64_t z[32];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const ulonglong2 f = sk2[i / 2];
+          const uint32_t* r = &raw[i / 8][(i % 8) * 2];
+          z[i] = f2_mul(f2_pack(__uint_as_float(r[0]), __uint_as_float(r[1])), f.x);
+          z[i + 1] = f2_mul(f2_pack(__uint_as_float(r[2]), __uint_as_float(r[3])), f.y);
+        }
+        uint2 mw = make_uint2(0xFFFFFFFFu, 0xFFFFFFFFu);
+        if (whole) {
+          if constexpr (VAR > 0) {
+            // the bias of tokens 2 i, 2 i + 1: -slope (pos - j)
+            const uint64_t zs2 = f2_pack(zs, zs);
+            const float b0 = slope * static_cast<float>(j0 - pos);
+            const uint64_t bias = f2_pack(b0, b0 + slope), step = f2_pack(2.f * slope, 2.f * slope);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const uint64_t b =
+                  f2_fma(step, f2_pack(static_cast<float>(i), static_cast<float>(i)), bias);
               if constexpr (VAR == 1) {
-                z = f2_fma(z, zs2, b);
+                z[i] = f2_fma(z[i], zs2, b);
               } else {  // cap tanh(z / cap) = cap - 2 cap / (2^x + 1)
                 float x, y;
-                f2_unpack(f2_mul(z, zs2), x, y);
+                f2_unpack(f2_mul(z[i], zs2), x, y);
                 x = fmaf(__fdividef(1.f, ex2(x) + 1.f), -2.f * cap_log2, cap_log2);
                 y = fmaf(__fdividef(1.f, ex2(y) + 1.f), -2.f * cap_log2, cap_log2);
-                z = f2_add(f2_pack(x, y), b);
+                z[i] = f2_add(f2_pack(x, y), b);
               }
-            }
-            return z;
-          };
-          uint32_t raw[2][16];
-          tmem_ld16(ts, raw[0]);
-          float m4[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) m4[x] = __int_as_float(0xff800000);
-#pragma unroll 1
-          for (int c2 = 0; c2 < 8; c2 += 2) {
-            const uint64_t b2 = f2_fma(step, f2_pack(c2 * 8.f, c2 * 8.f), bias);
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-              const int c = c2 + cc;
-              tmem_ld_wait();
-              // (the last load is not used)
-              tmem_ld16(ts + ((c + 1) & 7) * 16, raw[cc ^ 1]);
-              uint32_t* r = raw[cc];
-#pragma unroll
-              for (int i = 0; i < 8; i += 2) {
-                const ulonglong2 s = sk2[c * 4 + i / 2];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  float p, q;
-                  const uint64_t z = score(r + (i + x) * 2, x ? s.y : s.x, b2, cc * 8 + i + x);
-                  f2_unpack(z, p, q);
-                  m4[(i + x) & 3] = fmaxf(fmaxf(m4[(i + x) & 3], p), q);
-                  r[(i + x) * 2] = __float_as_uint(p);
-                  r[(i + x) * 2 + 1] = __float_as_uint(q);
-                }
-              }
-              tmem_st16(ts + c * 16, raw[cc]);
             }
           }
-          tmem_ld_wait();
-          tmem_st_wait();
-          tmem_ld16(ts, raw[0]);
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          const float zf = VAR > 0 ? 1.f : zs;
-          move_ref(bound_of(mx * zf, fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w))));
-          const float c0 = kShift - ref;
-          const uint64_t zf2 = f2_pack(zf, zf), c02 = f2_pack(c0, c0);
-          uint64_t la = 0, lb = 0;  // (0.f, 0.f)
-#pragma unroll 1
-          for (int c2 = 0; c2 < 8; c2 += 2) {
+        } else {
+          // some row masks some token: masked scores become -inf, and a row's V
+          // bound is that of the tokens it sees
+          mw.x = (word_bits(j0, wf, pos + 1) | word_bits(j0, 0, pre)) & val.x;
+          mw.y = (word_bits(j0 + 32, wf, pos + 1) | word_bits(j0 + 32, 0, pre)) & val.y;
+          vmax = 0.f;
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            const int c = c2 + cc;
-            tmem_ld_wait();
-            if (cc == 0 || c2 < 6) tmem_ld16(ts + (c + 1) * 16, raw[cc ^ 1]);
-            const uint32_t* r = raw[cc];
+          for (int i = 0; i < 32; ++i) {
+            float x[2];
+            f2_unpack(z[i], x[0], x[1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int c = 2 * i + e;
+              if constexpr (VAR > 0) {
+                x[e] *= zs;
+                if constexpr (VAR == 2) x[e] = cap_log2 * tanh_f32(x[e] * (0.5f / kLog2e));
+                x[e] = fmaf(-slope, fabsf(static_cast<float>(pos - j0 - c)), x[e]);
+              }
+              const bool see = ((c < 32 ? mw.x : mw.y) >> (c & 31)) & 1;
+              x[e] = see ? x[e] : __int_as_float(0xff800000);
+              vmax = fmaxf(vmax, see ? sv[c] : 0.f);
+            }
+            z[i] = f2_pack(x[0], x[1]);
+          }
+        }
+        float m4[4];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float p, q;
+          f2_unpack(z[i], p, q);
+          m4[i & 3] = i < 4 ? fmaxf(p, q) : fmaxf(fmaxf(m4[i & 3], p), q);
+        }
+        const float zf = VAR > 0 ? 1.f : zs;
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        // ---- the reference: a bound of z + log2(V scale); where it was passed
+        // by 2^kTau it moves, and with it the sum and O
+        const float bound = fmaf(
+            mx, zf, static_cast<float>(min(max(exp_above(vmax), -60), 120)));
+        float al = 1.f;
+        if (bound > ref + kTau) {
+          al = ex2(ref - bound);
+          ref = bound;
+        }
+        if (__any_sync(0xffffffffu, al != 1.f)) {
+          l *= al;
+          if (s > 0) {
+            // O is at rest once P V of the last step is done
+            if (!wait_warp(kBarO + t * 2 + (half ^ 1), ((steps - 1) >> 1) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(to + c * 16, o);
+              tmem_ld_wait();
+              tmem_landed(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+              tmem_st16(to + c * 16, o);
+            }
+          }
+        }
+        // ---- P and its sum
+        const float c0 = kShift - ref;
+        const uint64_t zf2 = f2_pack(zf, zf), c02 = f2_pack(c0, c0);
+        uint64_t la = 0, lb = 0;  // (0.f, 0.f)
+        auto weigh = [&](auto masked) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
             uint32_t pw[8];
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
               const ulonglong2 v = sv2[c * 4 + i / 2];
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
+                const int zi = c * 8 + i + x;
                 float p, q;
-                const uint64_t z = f2_pack(__uint_as_float(r[(i + x) * 2]),
-                                           __uint_as_float(r[(i + x) * 2 + 1]));
-                f2_unpack(VAR > 0 ? f2_add(z, c02) : f2_fma(z, zf2, c02), p, q);
+                f2_unpack(VAR > 0 ? f2_add(z[zi], c02) : f2_fma(z[zi], zf2, c02), p, q);
                 const uint64_t p2 = f2_pack(ex2(p), ex2(q));
                 if (x) lb = f2_add(lb, p2);
                 else la = f2_add(la, p2);
-                f2_unpack(f2_mul(p2, x ? v.y : v.x), p, q);
+                uint64_t v2 = x ? v.y : v.x;
+                if constexpr (masked.value) {  // a masked token's scale may be anything
+                  const uint32_t b = (zi < 16 ? mw.x : mw.y) >> (2 * zi & 31);
+                  f2_unpack(v2, p, q);
+                  v2 = f2_pack(b & 1 ? p : 0.f, b & 2 ? q : 0.f);
+                }
+                f2_unpack(f2_mul(p2, v2), p, q);
                 pw[i + x] = pack_half2(p, q);
               }
             }
             tmem_st8(ts + c * 8, pw);
           }
-          }
-          float x, y;
-          f2_unpack(f2_add(la, lb), x, y);
-          l += x + y;
-        } else {
-          // ---- masked tiles, two passes over the scores in TMEM: final scores,
-          // then P.  A row's V bound is that of the tokens it sees.
-          const float zf = VAR > 0 ? 1.f : zs;
-          float mx = __int_as_float(0xff800000), vmax = 0.f;
-#pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t raw[16];
-            tmem_ld16(ts + c * 16, raw);
-            tmem_ld_wait();
-            const int jc = j0 + c * 16;
-            const uint32_t mw = (word_bits(jc, wf, pos + 1) | word_bits(jc, 0, pre)) &
-                                (infos[s4].valid[c >> 1] >> (16 * (c & 1)));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float z = __uint_as_float(raw[i]) * sk[c * 16 + i];
-              if constexpr (VAR > 0) {
-                z *= zs;
-                if constexpr (VAR == 2) z = cap_log2 * tanh_f32(z * (0.5f / kLog2e));
-                z = fmaf(-slope, fabsf(static_cast<float>(pos - jc - i)), z);
-              }
-              const bool see = (mw >> i) & 1;
-              z = see ? z : __int_as_float(0xff800000);
-              mx = fmaxf(mx, z);
-              vmax = fmaxf(vmax, see ? sv[c * 16 + i] : 0.f);
-              raw[i] = __float_as_uint(z);
-            }
-            tmem_st16(ts + c * 16, raw);
-          }
-          tmem_st_wait();
-          move_ref(bound_of(mx * zf, vmax));
-          const float c0 = kShift - ref;
-#pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t raw[16], pw[8];
-            tmem_ld16(ts + c * 16, raw);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float p = ex2(fmaf(__uint_as_float(raw[i]), zf, c0));
-              const float q = ex2(fmaf(__uint_as_float(raw[i + 1]), zf, c0));
-              l += p + q;
-              // a masked token's scale may be anything
-              pw[i / 2] = pack_half2(p != 0.f ? p * sv[c * 16 + i] : 0.f,
-                                     q != 0.f ? q * sv[c * 16 + i + 1] : 0.f);
-            }
-            tmem_st8(ts + c * 8, pw);
-          }
-        }
+        };
+        if (whole) weigh(std::false_type{});
+        else weigh(std::true_type{});
+        float x, y;
+        f2_unpack(f2_add(la, lb), x, y);
+        l += x + y;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars + kBarP + t);
+        if (lane == 0) mbar_arrive(bars + kBarP + t * 2 + half);
       }
       if (!ok) break;
+      g += n;
 
       // ---- the block's result, or this range's piece of it
-      if (!wait_warp(kBarO + t, no & 1)) {
+      if (!wait_warp(kBarO + t * 2 + 1, ((steps - 1) >> 1) & 1)) {
         ok = false;
         break;
       }
-      ++no;
       tc_fence_after();
       const bool piece = im.t0 > 0 || im.t1 < im.tl.count;
       const float inv = piece ? 1.f : (l == 0.f ? 0.f : 1.f / l);
@@ -997,6 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
         uint32_t o[16];
         tmem_ld16(to + c * 16, o);
         tmem_ld_wait();
+        tmem_landed(o);
         if (!live) continue;
         float f[16];
 #pragma unroll
@@ -1033,14 +1066,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
 
   // ---- drain and free: no MMA may still be in flight
   __syncwarp();
-  if (warp == 16 && lane == 0) {
+  if (warp == kIssueWarp && lane == 0) {
     tc_commit(bars + kBarDrain);
     (void)mbar_wait_bounded(bars + kBarDrain, 0, kWaitLimitCycles);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) tmem_dealloc(tmem, 512);
+  if (warp == kIssueWarp) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------- merge
