@@ -673,9 +673,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
   if (warp == kIssueWarp) {
     // ================================================= MMA issuer
     // Steps of 64 tokens: S of step s goes to score buffer s & 1 of its row
-    // tile, where P of step s replaces it; it is issued once P V of step s - 2,
-    // which read the buffer last, is done (MMAs of different shapes need not
-    // complete in the order of their issue).  The softmax of step s - 1 runs
+    // tile, where P of step s replaces it; it is issued behind P V of step
+    // s - 2, which read the buffer last: the tensor cores work through one
+    // thread's MMAs in the order of their issue.  The softmax of step s - 1 runs
     // meanwhile.
     if (lane == 0) {
       const uint32_t idesc_s = tc_idesc(0, 0, 0, 0, 128, kS);  // f16, both K-major
@@ -705,7 +705,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
       uint32_t g = 0;      // tiles done by this CTA
       uint32_t nq = 0;     // bit t: phase of row tile t's Q
       uint32_t np = 0;     // bit 2 t + half: phase of a P buffer
-      uint32_t no = 0;     // ... and of its P V
       bool ok = true;
       for (int it = it0, u = u0; u < u1 && ok; ++it) {
         const Item im = load_item(a, pv, it, u, u1);
@@ -739,16 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
               np ^= 1u << (t * 2 + half);
               tc_fence_after();
               mma_o(t, g & 1, half, k == 0 && half == 0);
-            }
-#pragma unroll 1
-            for (int t = 0; t < two && ok; ++t) {
-              if (more) {
-                ok = wait(kBarO + t * 2 + half, (no >> (t * 2 + half)) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                mma_s(t, g1 & 1, half);
-              }
-              no ^= 1u << (t * 2 + half);
+              if (more) mma_s(t, g1 & 1, half);
             }
           }
           if (!ok) break;
