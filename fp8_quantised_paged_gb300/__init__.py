@@ -36,5 +36,6 @@ __all__ = list(_API)
 def __getattr__(name):
     if name in _API:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)  # found at once from now on
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

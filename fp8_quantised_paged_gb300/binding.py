@@ -16,6 +16,7 @@ all arithmetic runs in the library's kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -83,6 +84,7 @@ def version() -> int:
 
 def set_decode_workers(workers: int) -> None:
     N.check(N.lib.fp8pa_set_decode_workers(int(workers)), "set_decode_workers")
+    _decode_need.cache_clear()
 
 
 def kv_append_quant(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, fmt=E4M3,
@@ -336,48 +338,71 @@ def decode_step(k_new, v_new, slot_mapping, q, k_cache, v_cache, k_scale, v_scal
     return out
 
 
+# The wrappers below run next to kernels of a few microseconds, so their checks
+# touch each tensor as little as they can.
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    """The handle of `stream`, or of the current stream of device `dev`."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _want(t, dtype, name, dev):
+    if t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        _need(t, dtype, name, dev)
+
+
 def _check_cache(k_cache, v_cache, k_scale, v_scale, n_kv_heads, head_dim, scale_mode,
                  group_size, dev):
     """The shapes of a paged cache and its scales; returns (num_blocks, block_size)."""
-    if k_cache.dim() != 4 or k_cache.shape[1] != n_kv_heads or k_cache.shape[3] != head_dim:
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[1] != n_kv_heads or shape[3] != head_dim:
         raise ValueError(f"k_cache must be [num_blocks, {n_kv_heads}, block_size, {head_dim}], "
-                         f"got {tuple(k_cache.shape)}")
-    nb, _, bs, _ = k_cache.shape
-    if scale_mode == SCALE_CHANNEL_STATIC:
+                         f"got {tuple(shape)}")
+    nb, _, bs, _ = shape
+    sdt = torch.float32
+    if scale_mode == SCALE_TOKEN_HEAD:
+        numel = nb * n_kv_heads * bs
+    elif scale_mode == SCALE_CHANNEL_STATIC:
         numel = n_kv_heads * head_dim
     elif scale_mode == SCALE_SEGMENT:
         numel = nb * segment_scale_heads(n_kv_heads)
-    elif scale_mode in (SCALE_MX_BLOCK, SCALE_TOKEN_GROUP):
-        numel = nb * n_kv_heads * bs * (head_dim // max(int(group_size), 1))
     else:
-        numel = nb * n_kv_heads * bs
-    sdt = torch.uint8 if scale_mode == SCALE_MX_BLOCK else torch.float32
-    for cache, scale, name in ((k_cache, k_scale, "k"), (v_cache, v_scale, "v")):
-        if cache is None and scale is None and name == "v":
-            continue
-        if cache is None or scale is None:
-            raise ValueError(f"{name}_cache and {name}_scale come together")
-        _need(cache, torch.uint8, name + "_cache", dev)
-        _need(scale, sdt, name + "_scale", dev)
-        if cache.shape != k_cache.shape:
-            raise ValueError(f"{name}_cache must have k_cache's shape")
-        if scale.numel() != numel:
-            raise ValueError(f"{name}_scale must hold {numel} values, got {scale.numel()}")
+        numel = nb * n_kv_heads * bs * (head_dim // max(int(group_size), 1))
+        if scale_mode == SCALE_MX_BLOCK:
+            sdt = torch.uint8
+    _want(k_cache, torch.uint8, "k_cache", dev)
+    _want(k_scale, sdt, "k_scale", dev)
+    if k_scale.numel() != numel:
+        raise ValueError(f"k_scale must hold {numel} values, got {k_scale.numel()}")
+    if v_cache is not None or v_scale is not None:
+        if v_cache is None or v_scale is None:
+            raise ValueError("v_cache and v_scale come together")
+        _want(v_cache, torch.uint8, "v_cache", dev)
+        _want(v_scale, sdt, "v_scale", dev)
+        if v_cache.shape != shape:
+            raise ValueError("v_cache must have k_cache's shape")
+        if v_scale.numel() != numel:
+            raise ValueError(f"v_scale must hold {numel} values, got {v_scale.numel()}")
     return nb, bs
 
 
 def _rows(t, name, n, heads, d, dev):
     """A bf16 [n, heads, d] tensor whose tokens may be strided; returns the stride."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-    if not t.is_cuda or t.device != dev:
+    if t.device != dev or not t.is_cuda:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if tuple(t.shape) != (n, heads, d):
+    if t.shape != (n, heads, d):
         raise ValueError(f"{name} must be {(n, heads, d)}, got {tuple(t.shape)}")
-    s = t.stride()
-    if (d > 1 and s[2] != 1) or (heads > 1 and s[1] != d):
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (heads > 1 and s1 != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s[0] if n > 1 else heads * d
+    return s0 if n > 1 else heads * d
 
 
 def kv_append_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale,
@@ -409,43 +434,49 @@ def kv_append_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, 
         qos = _rows(q_out, "q_out", n, hq, d, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _need(positions, torch.int32, "positions", dev)
-    _need(slot_mapping, torch.int32, "slot_mapping", dev)
-    _need(cos_sin, torch.float32, "cos_sin", dev)
+    _want(positions, torch.int32, "positions", dev)
+    _want(slot_mapping, torch.int32, "slot_mapping", dev)
+    _want(cos_sin, torch.float32, "cos_sin", dev)
     if positions.numel() != n or slot_mapping.numel() != n:
         raise ValueError(f"positions and slot_mapping must hold {n} entries")
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_position, rot_dim]")
-    if v is not None and (v_cache is None or v_scale is None):
+    if v is None:
+        v_cache = v_scale = None
+    elif v_cache is None or v_scale is None:
         raise ValueError("v needs v_cache and v_scale")
-    nb, bs = _check_cache(k_cache, None if v is None else v_cache, k_scale,
-                          None if v is None else v_scale, hkv, d, scale_mode, group_size, dev)
+    nb, bs = _check_cache(k_cache, v_cache, k_scale, v_scale, hkv, d, scale_mode, group_size, dev)
+    max_position, rot_dim = cos_sin.shape
     with _on(dev):
         rc = N.lib.fp8pa_kv_append_rope(
-            _ptr(q), _ptr(q_out), _ptr(k), _ptr(v), qs, qos, ks, vs, _ptr(positions),
-            _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], rot_offset, 1 if interleaved else 0,
-            _ptr(slot_mapping), n, hq, hkv, d, fmt, scale_mode, group_size, _ptr(k_cache),
-            _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), nb, bs, _stream(stream))
-    N.check(rc, "kv_append_rope")
+            _addr(q), _addr(q_out), k.data_ptr(), _addr(v), qs, qos, ks, vs, positions.data_ptr(),
+            cos_sin.data_ptr(), max_position, rot_dim, rot_offset, 1 if interleaved else 0,
+            slot_mapping.data_ptr(), n, hq, hkv, d, fmt, scale_mode, group_size,
+            k_cache.data_ptr(), _addr(v_cache), k_scale.data_ptr(), _addr(v_scale), nb, bs,
+            _raw_stream(stream, dev))
+    if rc:
+        N.check(rc, "kv_append_rope")
     return q_out
 
 
 def _check_mods(prefix_lens, alibi_slopes, batch, hq, dev):
-    _need(prefix_lens, torch.int32, "prefix_lens", dev)
-    _need(alibi_slopes, torch.float32, "alibi_slopes", dev)
-    if prefix_lens is not None and prefix_lens.numel() != batch:
-        raise ValueError(f"prefix_lens must hold {batch} entries")
-    if alibi_slopes is not None and alibi_slopes.numel() != hq:
-        raise ValueError(f"alibi_slopes must hold {hq} entries")
+    if prefix_lens is not None:
+        _want(prefix_lens, torch.int32, "prefix_lens", dev)
+        if prefix_lens.numel() != batch:
+            raise ValueError(f"prefix_lens must hold {batch} entries")
+    if alibi_slopes is not None:
+        _want(alibi_slopes, torch.float32, "alibi_slopes", dev)
+        if alibi_slopes.numel() != hq:
+            raise ValueError(f"alibi_slopes must hold {hq} entries")
 
 
 def _check_tables(block_tables, seq_lens, dev):
-    _need(block_tables, torch.int32, "block_tables", dev)
-    _need(seq_lens, torch.int32, "seq_lens", dev)
-    if block_tables.dim() != 2 or seq_lens.dim() != 1 or (
-            block_tables.shape[0] != seq_lens.shape[0]):
+    _want(block_tables, torch.int32, "block_tables", dev)
+    _want(seq_lens, torch.int32, "seq_lens", dev)
+    shape = block_tables.shape
+    if len(shape) != 2 or seq_lens.dim() != 1 or shape[0] != seq_lens.shape[0]:
         raise ValueError("block_tables must be [batch, max_blocks] and seq_lens [batch]")
-    return block_tables.shape
+    return shape
 
 
 def _output(out, shape, out_dtype, dev, stream):
@@ -454,12 +485,13 @@ def _output(out, shape, out_dtype, dev, stream):
         out = torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=dev)
         if stream is not None:
             out.record_stream(stream)
-    if out.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError("out must be bf16 or float32")
-    _need(out, out.dtype, "out", dev)
-    if tuple(out.shape) != tuple(shape):
+    elif out.shape != shape:
         raise ValueError(f"out must be {tuple(shape)}, got {tuple(out.shape)}")
-    return out, OUT_F32 if out.dtype == torch.float32 else OUT_BF16
+    dt = out.dtype
+    if dt is not torch.float32 and dt is not torch.bfloat16:
+        raise TypeError("out must be bf16 or float32")
+    _want(out, dt, "out", dev)
+    return out, OUT_F32 if dt is torch.float32 else OUT_BF16
 
 
 def _scratch(need, dev, stream):
@@ -470,6 +502,13 @@ def _scratch(need, dev, stream):
     if stream is not None:
         ws.record_stream(stream)
     return ws
+
+
+@functools.lru_cache(maxsize=4096)
+def _decode_need(device_index, *sizes):
+    """Workspace size of a decode of these sizes (device_index is current);
+    forgotten by set_decode_workers."""
+    return int(N.lib.fp8pa_decode_workspace_bytes(*sizes))
 
 
 def paged_decode_attention_mod(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
@@ -498,16 +537,18 @@ def paged_decode_attention_mod(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     out, odt = _output(out, (B, hq, d), out_dtype, dev, stream)
     with _on(dev):
         if workspace is None:
-            workspace = _scratch(int(N.lib.fp8pa_decode_workspace_bytes(
-                B, hq, n_kv_heads, d, d, bs, max_blocks)), dev, stream)
-        _need(workspace, torch.uint8, "workspace", dev)
+            workspace = _scratch(_decode_need(dev.index, B, hq, n_kv_heads, d, d, bs, max_blocks),
+                                 dev, stream)
+        else:
+            _want(workspace, torch.uint8, "workspace", dev)
         rc = N.lib.fp8pa_paged_decode_attention_mod(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            _ptr(block_tables), max_blocks, _ptr(seq_lens), B, bs, hq, n_kv_heads, d, fmt,
-            scale_mode, group_size, float(sm_scale), window, _ptr(prefix_lens), float(logit_cap),
-            _ptr(alibi_slopes), nb, _ptr(out), odt, _ptr(workspace),
-            0 if workspace is None else workspace.numel(), _stream(stream))
-    N.check(rc, "paged_decode_attention_mod")
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), block_tables.data_ptr(), max_blocks, seq_lens.data_ptr(), B, bs,
+            hq, n_kv_heads, d, fmt, scale_mode, group_size, sm_scale, window, _addr(prefix_lens),
+            logit_cap, _addr(alibi_slopes), nb, out.data_ptr(), odt, _addr(workspace),
+            0 if workspace is None else workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        N.check(rc, "paged_decode_attention_mod")
     return out
 
 
@@ -538,7 +579,7 @@ def paged_prefill_attention(q, q_offsets, k_cache, v_cache, k_scale, v_scale, bl
     dev = q.device
     total, hq, d = q.shape
     B, max_blocks = _check_tables(block_tables, seq_lens, dev)
-    _need(q_offsets, torch.int32, "q_offsets", dev)
+    _want(q_offsets, torch.int32, "q_offsets", dev)
     if q_offsets.numel() != B + 1:
         raise ValueError(f"q_offsets must hold {B + 1} entries")
     if v_cache is None or v_scale is None:
@@ -551,14 +592,17 @@ def paged_prefill_attention(q, q_offsets, k_cache, v_cache, k_scale, v_scale, bl
         if workspace is None:
             workspace = _scratch(int(N.lib.fp8pa_prefill_workspace_bytes(
                 total, B, hq, n_kv_heads, d)), dev, stream)
-        _need(workspace, torch.uint8, "workspace", dev)
+        else:
+            _want(workspace, torch.uint8, "workspace", dev)
         rc = N.lib.fp8pa_paged_prefill_attention(
-            _ptr(q), _ptr(q_offsets), total, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-            _ptr(v_scale), _ptr(block_tables), max_blocks, _ptr(seq_lens), B, bs, hq, n_kv_heads,
-            d, fmt, scale_mode, group_size, float(sm_scale), window, _ptr(prefix_lens),
-            float(logit_cap), _ptr(alibi_slopes), nb, _ptr(out), odt, _ptr(workspace),
-            0 if workspace is None else workspace.numel(), _stream(stream))
-    N.check(rc, "paged_prefill_attention")
+            q.data_ptr(), q_offsets.data_ptr(), total, k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), max_blocks,
+            seq_lens.data_ptr(), B, bs, hq, n_kv_heads, d, fmt, scale_mode, group_size, sm_scale,
+            window, _addr(prefix_lens), logit_cap, _addr(alibi_slopes), nb, out.data_ptr(), odt,
+            _addr(workspace), 0 if workspace is None else workspace.numel(),
+            _raw_stream(stream, dev))
+    if rc:
+        N.check(rc, "paged_prefill_attention")
     return out
 
 
