@@ -13,9 +13,11 @@
 //
 // GB300 design.  A sub-group of LPR lanes holds one row, each lane one
 // 16-byte chunk of 8 dims (three at head_dim 576).  Neighbouring pairs lie in
-// one lane; paired halves swap their packed words by a shuffle.  A warp works
-// on rows of ONE token, so its lanes load their angles once and keep them in
-// registers for all of the warp's rows.
+// one lane; paired halves swap their packed words by a shuffle.  Where whole
+// rows of paired halves turn (the usual case), a lane takes chunk i of both
+// halves instead and no word moves.  A warp works on rows of ONE token, so its
+// lanes load their angles once and keep them in registers for all of the warp's
+// rows.
 #include <float.h>
 
 #include "common.cuh"
@@ -39,6 +41,16 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Sums of two packed products, the second taken times sign (1 or -1).  The sums
+// are scalar on purpose: a packed sum was contracted with its products.
+__device__ __forceinline__ void turn2(uint64_t x, uint64_t y, float sign, float& lo, float& hi) {
+  float x0, x1, y0, y1;
+  f2_unpack(x, x0, x1);
+  f2_unpack(y, y0, y1);
+  lo = sign > 0.f ? __fadd_rn(x0, y0) : __fsub_rn(x0, y0);
+  hi = sign > 0.f ? __fadd_rn(x1, y1) : __fsub_rn(x1, y1);
 }
 
 // Where a row of the call lives: `row` counts a token's q rows, then its K
@@ -149,9 +161,11 @@ __device__ __forceinline__ void store_codes(const RopeArgs& a, const float (&v)[
   }
 }
 
-// STEPS steps of 32 / LPR rows per warp, their loads issued together.
-template <int FMT, int MODE, int LPR, int R, int STEPS>
-__global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const RopeArgs a) {
+// STEPS steps of 32 / LPR rows per warp, their loads issued together.  PAIR: a
+// lane's two chunks are the halves of its pairs (rot_dim = head_dim = 16 LPR).
+template <int FMT, int MODE, int LPR, int R, int STEPS, bool PAIR>
+__global__ void __launch_bounds__(kWarps * 32, STEPS > 1 && R < 3 ? 4 : 1)
+    append_rope_kernel(const RopeArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr int SG = 32 / LPR;
@@ -188,32 +202,47 @@ __global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const RopeArgs
   if (slot >= 0 && !in_pool && lane == 0) raise_error(a.err, FP8PA_DEVERR_SLOT_RANGE);
 
   // This lane's angles: chunk r_rot of the lane is the one that may turn (the
-  // range lies in one 256-dim span where rows have more than one chunk a lane).
+  // range lies in one 256-dim span where rows have more than one chunk a lane;
+  // PAIR: both turn, by the same angles).
   const int half = a.rot_dim / 2, hch = half / 8;
-  const int r_rot = a.rot_offset / (8 * LPR);
-  const int rc = sl + LPR * r_rot - a.rot_offset / 8;  // chunk within the range
-  const bool turns = rc >= 0 && rc < a.rot_dim / 8;
-  const bool hi = rc >= hch;  // second half of the range (paired halves)
-  float cs[8], sn[8];
+  const int r_rot = PAIR ? 0 : a.rot_offset / (8 * LPR);
+  const int rc = PAIR ? sl : sl + LPR * r_rot - a.rot_offset / 8;  // chunk within the range
+  const bool turns = PAIR || (rc >= 0 && rc < a.rot_dim / 8);
+  const bool hi = !PAIR && rc >= hch;  // second half of the range (paired halves)
+  // cosines, and the sines with the sign that they enter with: the pair's first
+  // dim becomes a c + b (-s), its second b c + a s
+  uint64_t cs[4], sn[4];
   if (turns) {
     const float* row = a.cos_sin + static_cast<long>(pos) * a.rot_dim;
-    if (a.interleaved) {
+    if (!PAIR && a.interleaved) {
       const float4 c = __ldg(reinterpret_cast<const float4*>(row + rc * 4));
       const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + rc * 4));
-      cs[0] = cs[1] = c.x; cs[2] = cs[3] = c.y; cs[4] = cs[5] = c.z; cs[6] = cs[7] = c.w;
-      sn[0] = sn[1] = s.x; sn[2] = sn[3] = s.y; sn[4] = sn[5] = s.z; sn[6] = sn[7] = s.w;
+      cs[0] = f2_pack(c.x, c.x);
+      cs[1] = f2_pack(c.y, c.y);
+      cs[2] = f2_pack(c.z, c.z);
+      cs[3] = f2_pack(c.w, c.w);
+      sn[0] = f2_pack(-s.x, s.x);
+      sn[1] = f2_pack(-s.y, s.y);
+      sn[2] = f2_pack(-s.z, s.z);
+      sn[3] = f2_pack(-s.w, s.w);
     } else {
-      const float4* cp = reinterpret_cast<const float4*>(row + (hi ? rc - hch : rc) * 8);
-      const float4* sp = reinterpret_cast<const float4*>(row + half + (hi ? rc - hch : rc) * 8);
+      const int at = (hi ? rc - hch : rc) * 8;
+      const float4* cp = reinterpret_cast<const float4*>(row + at);
+      const float4* sp = reinterpret_cast<const float4*>(row + half + at);
       const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
-      cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w;
-      cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
-      sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w;
-      sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+      const float m = hi ? 1.f : -1.f;
+      cs[0] = f2_pack(c0.x, c0.y);
+      cs[1] = f2_pack(c0.z, c0.w);
+      cs[2] = f2_pack(c1.x, c1.y);
+      cs[3] = f2_pack(c1.z, c1.w);
+      sn[0] = f2_pack(m * s0.x, m * s0.y);
+      sn[1] = f2_pack(m * s0.z, m * s0.w);
+      sn[2] = f2_pack(m * s1.x, m * s1.y);
+      sn[3] = f2_pack(m * s1.z, m * s1.w);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) cs[e] = sn[e] = 0.f;
+    for (int e = 0; e < 4; ++e) cs[e] = sn[e] = 0;
   }
   // lane holding the other half's chunk
   const int psl = turns ? (hi ? sl - hch : sl + hch) : sl;
@@ -225,33 +254,40 @@ __global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const RopeArgs
     float v[R][8];
 #pragma unroll
     for (int r = 0; r < R; ++r) unpack8(w[i][r], v[r]);
+    if constexpr (PAIR) {
+      if (kind < 2) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (R > 1 && r != r_rot) continue;  // warp-uniform
-      float y[8];
-      if (a.interleaved) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          y[e] = __fsub_rn(__fmul_rn(v[r][e], cs[e]), __fmul_rn(v[r][e + 1], sn[e]));
-          y[e + 1] = __fadd_rn(__fmul_rn(v[r][e + 1], cs[e]), __fmul_rn(v[r][e], sn[e]));
-        }
-      } else {
-        uint4 o;
-        o.x = __shfl_sync(0xffffffffu, w[i][r].x, plane);
-        o.y = __shfl_sync(0xffffffffu, w[i][r].y, plane);
-        o.z = __shfl_sync(0xffffffffu, w[i][r].z, plane);
-        o.w = __shfl_sync(0xffffffffu, w[i][r].w, plane);
-        float p[8];
-        unpack8(o, p);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = __fmul_rn(v[r][e], cs[e]), z = __fmul_rn(p[e], sn[e]);
-          y[e] = hi ? __fadd_rn(x, z) : __fsub_rn(x, z);
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t x = f2_pack(v[0][2 * e], v[0][2 * e + 1]);
+          const uint64_t y = f2_pack(v[1][2 * e], v[1][2 * e + 1]);
+          // (sn: - s)
+          turn2(f2_mul(x, cs[e]), f2_mul(y, sn[e]), 1.f, v[0][2 * e], v[0][2 * e + 1]);
+          turn2(f2_mul(y, cs[e]), f2_mul(x, sn[e]), -1.f, v[1][2 * e], v[1][2 * e + 1]);
         }
       }
-      if (turns && kind < 2) {
+    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[r][e] = y[e];
+      for (int r = 0; r < R; ++r) {
+        if (R > 1 && r != r_rot) continue;  // warp-uniform
+        float p[8];
+        if (a.interleaved) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[e] = v[r][e ^ 1];
+        } else {
+          uint4 o;
+          o.x = __shfl_sync(0xffffffffu, w[i][r].x, plane);
+          o.y = __shfl_sync(0xffffffffu, w[i][r].y, plane);
+          o.z = __shfl_sync(0xffffffffu, w[i][r].z, plane);
+          o.w = __shfl_sync(0xffffffffu, w[i][r].w, plane);
+          unpack8(o, p);
+        }
+        if (turns && kind < 2) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            turn2(f2_mul(f2_pack(v[r][2 * e], v[r][2 * e + 1]), cs[e]),
+                  f2_mul(f2_pack(p[2 * e], p[2 * e + 1]), sn[e]), 1.f, v[r][2 * e],
+                  v[r][2 * e + 1]);
+        }
       }
     }
     if (kind == 0) {
@@ -273,15 +309,15 @@ __global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const RopeArgs
   }
 }
 
-// Rows per call from which a warp takes four steps of rows (the angles loaded
+// Rows per call from which a warp takes several steps of rows (the angles loaded
 // once for all of them) instead of one.
 constexpr long kBulkRows = 16384;
 
-template <int FMT, int MODE, int LPR, int R>
+template <int FMT, int MODE, int LPR, int R, bool PAIR>
 cudaError_t launch_shape(RopeArgs a, cudaStream_t stream) {
-  constexpr int SG = 32 / LPR;
+  constexpr int SG = 32 / LPR, BULK = PAIR ? 2 : 3;
   const bool bulk = static_cast<long>(a.num_tokens) * a.rows >= kBulkRows;
-  const int per_warp = (bulk ? 4 : 1) * SG;
+  const int per_warp = (bulk ? BULK : 1) * SG;
   a.warps_per_token = static_cast<uint32_t>((a.rows + per_warp - 1) / per_warp);
   a.div_warps = make_fast_div(a.warps_per_token);
   const long warps = static_cast<long>(a.num_tokens) * a.warps_per_token;
@@ -294,17 +330,23 @@ cudaError_t launch_shape(RopeArgs a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  if (bulk) return cudaLaunchKernelEx(&cfg, append_rope_kernel<FMT, MODE, LPR, R, 4>, a);
-  return cudaLaunchKernelEx(&cfg, append_rope_kernel<FMT, MODE, LPR, R, 1>, a);
+  if (bulk) return cudaLaunchKernelEx(&cfg, append_rope_kernel<FMT, MODE, LPR, R, BULK, PAIR>, a);
+  return cudaLaunchKernelEx(&cfg, append_rope_kernel<FMT, MODE, LPR, R, 1, PAIR>, a);
 }
 
 template <int FMT, int MODE>
 cudaError_t launch_lanes(const RopeArgs& a, cudaStream_t stream) {
+  // whole rows of paired halves; a scale group lies within a half
+  const bool grouped = MODE == FP8PA_SCALE_TOKEN_GROUP || MODE == FP8PA_SCALE_MX_BLOCK;
+  if (!a.interleaved && a.rot_dim == a.d && !(grouped && a.gs > a.d / 2)) {
+    if (a.d == 64) return launch_shape<FMT, MODE, 4, 2, true>(a, stream);
+    if (a.d == 128) return launch_shape<FMT, MODE, 8, 2, true>(a, stream);
+  }
   const int nch = a.d / 8;
-  if (nch <= 8) return launch_shape<FMT, MODE, 8, 1>(a, stream);
-  if (nch <= 16) return launch_shape<FMT, MODE, 16, 1>(a, stream);
-  if (nch <= 32) return launch_shape<FMT, MODE, 32, 1>(a, stream);
-  return launch_shape<FMT, MODE, 32, 3>(a, stream);
+  if (nch <= 8) return launch_shape<FMT, MODE, 8, 1, false>(a, stream);
+  if (nch <= 16) return launch_shape<FMT, MODE, 16, 1, false>(a, stream);
+  if (nch <= 32) return launch_shape<FMT, MODE, 32, 1, false>(a, stream);
+  return launch_shape<FMT, MODE, 32, 3, false>(a, stream);
 }
 
 template <int FMT>

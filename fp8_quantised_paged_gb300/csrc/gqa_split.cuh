@@ -388,7 +388,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
       }
       zs = p.qk_scale_log2 * exp2i(eq - 14);
       if constexpr (MOD) {
-        if (p.mods.cap > 0.f) zs = p.sm_scale * exp2i(eq - 14);
+        // capped scores: of 2 z / cap (cap_fast), or natural
+        if (p.mods.cap > kCapFast) zs = p.sm_scale * exp2i(eq - 14);
+        else if (p.mods.cap > 0.f) zs *= 2.0f / p.mods.cap;
         wfirst = window_first(p.mods, Lb - 1);
         pre = prefix_len(p.mods, cc.b, Lb);
         slope0 = slope1 = 0.f;
@@ -416,7 +418,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
     // score modifiers: the slice's visible tokens
     uint32_t vis = 0;
     if constexpr (MOD) {
-      if (valid > 0) vis = tile_bits(tok0, wfirst, Lb) | tile_bits(tok0, 0, pre);
+      if (valid >= 16 && tok0 >= wfirst) vis = 0xFFFFu;
+      else if (valid > 0) vis = tile_bits(tok0, wfirst, Lb) | tile_bits(tok0, 0, pre);
     }
     const uint32_t kbase = smem_u32(pages + s * 2 * PAGE);
     const uint32_t vbase = kbase + PAGE;
@@ -536,13 +539,18 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
       }
       float z00, z01, z10, z11;
       if constexpr (MOD) {
-        // capped scores leave the log2 domain for the tanh
         float z[4] = {acc[0] * (zs * sk0), acc[1] * (zs * sk0), acc[2] * (zs * sk1),
                       acc[3] * (zs * sk1)};
         if (p.mods.cap > 0.f) {
-          const float inv = 1.0f / p.mods.cap, back = p.mods.cap * kLog2e;
+          const float back = p.mods.cap * kLog2e;
+          if (p.mods.cap <= kCapFast) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) z[e] = back * tanh_f32(z[e] * inv);
+            for (int e = 0; e < 4; ++e) z[e] = cap_fast(z[e], back);
+          } else {
+            const float inv = 1.0f / p.mods.cap;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = back * tanh_f32(z[e] * inv);
+          }
         }
         const float d0 = static_cast<float>(Lb - 1 - tok0 - g), d1 = d0 - 8.f;
         z00 = v0 ? fmaf(-slope0, d0, z[0]) : NEG_INF;

@@ -54,10 +54,6 @@ constexpr int kSnap = 4;     // a cut this near an item's edge moves to it
 constexpr float kShift = 12.f;  // P = 2^(z - ref + 12): at most 2^15 with the lazy bound
 constexpr float kTau = 3.f;     // the reference may lag by 2^3
 constexpr float kNegBig = -1e30f;
-// Caps up to this take tanh as 1 - 2 / (e^2x + 1) whatever x is: the quotient is
-// good to 2^-21, so the score is off by 2^-20 cap at most, 2^-14 here.  Larger
-// caps need tanh_f32, good relative to the score.
-constexpr float kCapFast = 64.f;
 
 // ---------------------------------------------------------------- plan
 // Workspace: header, block prefix of the requests, then per row block its
@@ -307,31 +303,6 @@ __device__ __forceinline__ uint4 hmul8(const uint4& a, uint32_t f) {
     return *reinterpret_cast<const uint32_t*>(&r);
   };
   return make_uint4(m(a.x), m(a.y), m(a.z), m(a.w));
-}
-
-// Packed fp32 pairs: half the issue slots of scalar operations.
-__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
 }
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -888,9 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
               } else {  // cap tanh(z / cap) = cap - 2 cap / (2^x + 1)
                 float x, y;
                 f2_unpack(f2_mul(z[i], zs2), x, y);
-                x = fmaf(__fdividef(1.f, ex2(x) + 1.f), -2.f * cap_log2, cap_log2);
-                y = fmaf(__fdividef(1.f, ex2(y) + 1.f), -2.f * cap_log2, cap_log2);
-                z[i] = f2_add(f2_pack(x, y), b);
+                z[i] = f2_add(f2_pack(cap_fast(x, cap_log2), cap_fast(y, cap_log2)), b);
               }
             }
           }

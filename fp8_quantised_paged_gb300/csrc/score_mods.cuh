@@ -24,6 +24,16 @@ __device__ __forceinline__ int window_first(const ScoreMods& m, int pos) {
   return m.window > 0 ? max(pos - m.window + 1, 0) : 0;
 }
 
+// Caps up to this take tanh as 1 - 2 / (2^x + 1), x = 2 log2(e) z / cap, whatever
+// x is: the quotient is good to 2^-21, so the score is off by 2^-20 cap at most,
+// 2^-14 here, for two special-function operations and three others.  Larger caps
+// need tanh_f32, good relative to the score.
+constexpr float kCapFast = 64.f;
+// cap tanh(z / cap) in the log2 domain, cap_log2 = cap log2(e).
+__device__ __forceinline__ float cap_fast(float x, float cap_log2) {
+  return fmaf(__fdividef(1.f, ex2(x) + 1.f), -2.f * cap_log2, cap_log2);
+}
+
 // tanh x to a relative error of about 2^-21, so that cap * tanh(z / cap) is
 // as near to z as fp32 for any cap.  Above 0.55, 1 - 2 / (e^2|x| + 1) loses at
 // most one bit to the subtraction; below, the Taylor series to x^13, whose

@@ -205,7 +205,7 @@ def check(got, ref, d, bf16=False, f16_p=False, f16_q=False, cap=0.0, what=""):
     assert got.shape == want.shape, (got.shape, want.shape)
     assert np.isfinite(got).all(), f"{what}: not finite"
     dz = (d / 16 + 4) * 2.0 ** -22 * Z + 4 * 2.0 ** -22 * B + (2.0 ** -11 * Z if f16_q else 0.0)
-    if f16_p and cap <= 64:
+    if cap <= 64:
         dz = dz + 2.0 ** -20 * cap
     bound = A * (2 * dz + 2.0 ** -19 + (2.0 ** -11 if f16_p else 0.0)) + 1e-30
     if f16_p:

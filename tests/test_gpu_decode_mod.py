@@ -48,7 +48,7 @@ def both(F, s, hkv, d, sm, fmt, mode, gs=32, **mods):
     ref = reference(s, hkv, sm, fmt, mode, gs, **mods)
     for dt in (torch.float32, torch.bfloat16):
         got = call(F, s, hkv, sm, fmt, mode, gs, out_dtype=dt, **mods)
-        R.check(got, ref, d, bf16=dt == torch.bfloat16, what=f"{dt}")
+        R.check(got, ref, d, bf16=dt == torch.bfloat16, cap=mods.get("cap", 0.0), what=f"{dt}")
     assert F.get_device_error() == 0
     return got
 
