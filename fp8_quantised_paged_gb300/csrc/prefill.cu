@@ -27,11 +27,12 @@
 // inside f16 whatever the scales; it moves only when passed by 2^kTau, which
 // is exact, as sums and O carry the same reference.
 //
-// Roles (16 warps): 0-3 and 4-7 the softmax of row tiles 0 and 1 (a thread per
-// row), 8-14 convert codes into shared memory, 15 issues the MMAs (one thread).
-// Scores are made in steps of 64 tokens into two TMEM buffers per row tile, so
-// that the softmax of a step runs while the tensor cores make the next one.
-// Every wait is bounded.
+// Roles (24 warps): 0-7 and 8-15 the softmax of row tiles 0 and 1, two threads
+// per row, each with 64 of a tile's 128 tokens (four warps per scheduler hide
+// one another's waits; the two agree on the row's reference through shared
+// memory); 16-22 convert codes into shared memory, 23 issues the MMAs (one
+// thread).  While the tensor cores work on one row tile, the other's softmax
+// runs.  Every wait is bounded.
 #include <float.h>
 
 #include <type_traits>
@@ -47,9 +48,10 @@ namespace {
 
 constexpr int kRows = 256;   // rows of a block: two tiles of 128
 constexpr int kT = 128;      // tokens per tile
-constexpr int kS = 64;       // ... in steps of
-constexpr int kThreads = 512;
-constexpr int kConvWarps = 7, kIssueWarp = 15;
+constexpr int kHalf = 64;    // ... of which a softmax thread has half
+constexpr int kThreads = 768;
+constexpr int kAhead = 3;    // jobs that a converting warp asks L2 for ahead
+constexpr int kConvWarp = 16, kConvWarps = 7, kIssueWarp = 23;
 constexpr int kSnap = 4;     // a cut this near an item's edge moves to it
 constexpr float kShift = 12.f;  // P = 2^(z - ref + 12): at most 2^15 with the lazy bound
 constexpr float kTau = 3.f;     // the reference may lag by 2^3
@@ -257,8 +259,9 @@ struct Smem {
   static constexpr int kV = 4 * kTile;      // two stages
   static constexpr int kScale = 6 * kTile;  // four stages of [K scales][V scales] f32
   static constexpr int kInfo = kScale + 4 * 2 * kT * 4;  // four stages of StageInfo
-  static constexpr int kBars = kInfo + 4 * 64;
-  static constexpr int kMisc = kBars + 256;  // TMEM base, abort flag
+  static constexpr int kXch = kInfo + 4 * 64;  // [parity][warp of softmax][lane] f32
+  static constexpr int kBars = kXch + 2 * 16 * 32 * 4;
+  static constexpr int kMisc = kBars + 320;  // TMEM base, abort flag
   static constexpr int kBytes = kMisc + 16;
 };
 struct StageInfo {
@@ -266,12 +269,12 @@ struct StageInfo {
   float vmax[4];      // largest V scale of each 32 tokens
 };
 
-// Barriers: one arrival per warp of four (the scales: per job of eight) on the
-// first fourteen, one commit of the tensor cores on the others.  P, S and O (P V
-// of the step is done): index 2 * row tile + score buffer, so that no waiter is
-// ever two phases behind.
-enum { kBarQ = 0, kBarScale = 2, kBarKFull = 6, kBarVFull = 8, kBarP = 10, kBarKFree = 14,
-       kBarVFree = 16, kBarS = 18, kBarO = 22, kBarDrain = 26, kNumBars = 27 };
+// Barriers and the arrivals that complete a phase.  Q and P: the eight softmax
+// warps of the row tile; scales: the eight conversion jobs of the tile; K and V
+// full: four jobs; X (t * 4 + lane quarter): the two softmax warps of the same
+// rows; the others: a commit of the tensor cores.
+enum { kBarQ = 0, kBarP = 2, kBarScale = 4, kBarKFull = 8, kBarVFull = 10, kBarX = 12,
+       kBarKFree = 20, kBarVFree = 22, kBarS = 24, kBarO = 26, kBarDrain = 28, kNumBars = 29 };
 
 // ---------------------------------------------------------------- conversions
 // 16 codes -> 16 f16 (two 16-byte core-matrix rows), exactly.
@@ -321,6 +324,16 @@ __device__ __forceinline__ void tmem_landed(uint32_t (&r)[16]) {
                  "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// A row's bound of z + log2(V scale) from the largest of each (vmax 0: none).
+__device__ __forceinline__ float bound_of(float zmax, float vmax) {
+  return zmax + static_cast<float>(min(max(exp_above(vmax), -60), 120));
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], one thread.
 __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                               bool accumulate) {
@@ -329,6 +342,13 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
+}
+
+// The largest of eight bytes.
+__device__ __forceinline__ uint32_t max_byte(const uint32_t (&w)[2]) {
+  uint32_t m = __vmaxu4(w[0], w[1]);
+  m = __vmaxu4(m, m >> 16);
+  return max(m & 0xFFu, (m >> 8) & 0xFFu);
 }
 
 // Bits t of a 32-token word at token t0 with lo <= t0 + t < hi.
@@ -379,8 +399,9 @@ __device__ __forceinline__ int tile_token(const Item& it, int k) {
 // lane holds row r8 of four 8-row groups and, of each, the 16-byte chunks c4
 // (and c4 + 4): loads take 64 contiguous bytes of 8 rows, stores the 8 rows of a
 // core matrix, free of bank conflicts.  A job's codes and scales are loaded as
-// soon as the job before it is stored, its block ids one job earlier, and with
-// them its codes are asked for into L2.
+// soon as the job before it is stored, its block ids one job earlier; kAhead jobs
+// earlier it is asked for into L2, which is what keeps HBM busy where a chunk
+// has few rows.
 template <int D, int FMT>
 __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanView& pv,
                                               uint8_t* sm, int* abort_flag, int it, int u, int u1,
@@ -420,11 +441,14 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
 
   int ids[2], part = first;  // of this job
   bool have = false;         // ids are loaded
+  int pf_blk = -1, pf_t = 0;  // a half-job to ask for into L2
+  bool pf_v = false;
   for (uint32_t g = 0;;) {   // g: the job's tile, counted over the range
     while (k >= n) {
       if (u >= u1) return;
       const Item im = load_item(a, pv, it, u, u1);
       ++it;
+      pf_blk = -1;
       k -= n;
       n = im.t1 - im.t0;
       kt = im.t0;
@@ -462,7 +486,7 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
     }
     float sc = 1.f;  // scale of token 32 dw + lane
     bool sok;
-    uint32_t ex[H];  // MX: exponent bytes of the lane's chunks, by group
+    uint32_t below[H];  // MX: exponents of the lane's chunks below their rows' largest, by group
     {
       const int blk = lane < 16 ? ids[0] : ids[1], t = j + lane;
       sok = wanted(t) && blk >= 0 && blk < a.num_blocks;
@@ -473,22 +497,31 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
       } else if (a.mode == FP8PA_SCALE_SEGMENT) {
         if (sok) sc = __ldg(gscale + static_cast<long>(blk) * a.hp + kvh);
       } else if (mx) {
-        const uint8_t* exps = reinterpret_cast<const uint8_t*>(gscale);
-        if (sok) {
-          int e = 0;
-          for (int i = 0; i < nbx; ++i) e = max(e, static_cast<int>(__ldg(exps + rw * nbx + i)));
-          sc = exp2i(e - 127);
+        // 2, 4 or 8 bytes a row; absent ones read as zero
+        auto row_bytes = [&](size_t row, uint32_t (&w)[2]) {
+          const uint8_t* e = reinterpret_cast<const uint8_t*>(gscale) + row * nbx;
+          w[1] = nbx == 8 ? __ldg(reinterpret_cast<const uint32_t*>(e) + 1) : 0u;
+          w[0] = nbx == 2 ? __ldg(reinterpret_cast<const uint16_t*>(e))
+                          : __ldg(reinterpret_cast<const uint32_t*>(e));
+        };
+#pragma unroll
+        for (int h = 0; h < H; ++h) below[h] = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (!((okm >> x) & 1)) continue;
+          uint32_t w[2];
+          row_bytes(row_of(ids[x >> 1], j + x * 8 + r8), w);
+          const uint32_t em = max_byte(w);
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            const int b = (h * 4 + c4) * 16 / a.gs;
+            below[h] |= (em - (((b & 4 ? w[1] : w[0]) >> (8 * (b & 3))) & 0xFF)) << (8 * x);
+          }
         }
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          ex[h] = 0;
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if ((okm >> x) & 1)
-              ex[h] |= static_cast<uint32_t>(
-                           __ldg(exps + static_cast<size_t>(row_of(ids[x >> 1], j + x * 8 + r8)) *
-                                            nbx + (h * 4 + c4) * 16 / a.gs))
-                       << (8 * x);
+        if (sok) {
+          uint32_t w[2];
+          row_bytes(rw, w);
+          sc = exp2i(static_cast<int>(max_byte(w)) - 127);
         }
       }
     }
@@ -500,6 +533,27 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
     }
     have = nk < n;
     if (have) load_ids(kt + nk, npart, ids);
+
+    // ---- a job further ahead is asked for into L2 (its block id was loaded one
+    // job ago), and the next one's block id; lane x < 2 for half x
+    if (pf_blk >= 0 && pf_blk < a.num_blocks) {
+      const size_t row = row_of(pf_blk, pf_t);
+      prefetch_l2((pf_v ? a.v_cache : a.k_cache) + row * D, 16 * D);
+      if (a.mode == FP8PA_SCALE_TOKEN_HEAD) prefetch_l2((pf_v ? a.v_scale : a.k_scale) + row, 64);
+      else if (mx)
+        prefetch_l2(reinterpret_cast<const uint8_t*>(pf_v ? a.v_scale : a.k_scale) + row * nbx,
+                    16 * nbx);
+    }
+    pf_blk = -1;
+    if (lane < 2) {
+      const int ahead = part + kAhead * kConvWarps, ak = k + (ahead >> 3);
+      if (ak < n) {
+        pf_v = (ahead & 7) >= 4;
+        pf_t = token_of(kt + ak) + (ahead & 3) * 32 + lane * 16;
+        if ((pf_t < hi && pf_t + 16 > lo) || pf_t < pre)
+          pf_blk = __ldg(table + static_cast<int>(static_cast<uint32_t>(pf_t) >> lgbs));
+      }
+    }
 
     const uint32_t st = g & 1, s4 = g & 3;
     float* ss = reinterpret_cast<float*>(sm + SM::kScale) + s4 * 2 * kT + (V ? kT : 0) + dw * 32;
@@ -565,10 +619,9 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
           uint4 p, q;
           codes16_to_f16<FMT>(buf[x][h], p, q);
           if (mx) {
-            // the block's power of two relative to the row's largest, its scale
-            const int em = static_cast<int>(__float_as_uint(ss[x * 8 + r8]) >> 23) & 0xFF;
-            const int e = (ex[h] >> (8 * x)) & 0xFF;
-            const float f = __int_as_float((max(min(e - em, 0), -126) + 127) << 23);
+            // the block's power of two relative to the row's largest
+            const int e = (below[h] >> (8 * x)) & 0xFF;
+            const float f = __int_as_float((127 - min(e, 126)) << 23);
             const __half2 f2 = __floats2half2_rn(f, f);
             const uint32_t fw = *reinterpret_cast<const uint32_t*>(&f2);
             p = hmul8(p, fw);
@@ -588,13 +641,6 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
     g += nk - k;
     k = nk;
     part = npart;
-    if (have && lane < 2) {
-      // the next job's half `lane`: 16 rows of D bytes
-      const int blk = lane ? ids[1] : ids[0], t = token_of(kt + k) + (part & 3) * 32 + lane * 16;
-      if (blk >= 0 && blk < a.num_blocks)
-        prefetch_l2((part >= 4 ? a.v_cache : a.k_cache) + static_cast<size_t>(row_of(blk, t)) * D,
-                    16 * D);
-    }
   }
 }
 
@@ -624,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bars + i, i >= kBarKFree ? 1 : (i >= kBarScale && i < kBarKFull ? 8 : 4));
+      mbar_init(bars + i, i >= kBarKFree ? 1 : (i >= kBarX ? 2 : (i >= kBarKFull ? 4 : 8)));
     fence_barrier_init();
   }
   tc_fence_before();
@@ -643,91 +689,92 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
 
   if (warp == kIssueWarp) {
     // ================================================= MMA issuer
-    // Steps of 64 tokens: S of step s goes to score buffer s & 1 of its row
-    // tile, where P of step s replaces it; it is issued behind P V of step
-    // s - 2, which read the buffer last: the tensor cores work through one
-    // thread's MMAs in the order of their issue.  The softmax of step s - 1 runs
-    // meanwhile.
+    // S_t of tile k + 1 goes where P_t of tile k was: it is issued behind the
+    // P V that reads it, and the tensor cores work through one thread's MMAs in
+    // the order of their issue.
     if (lane == 0) {
-      const uint32_t idesc_s = tc_idesc(0, 0, 0, 0, 128, kS);  // f16, both K-major
+      const uint32_t idesc_s = tc_idesc(0, 0, 0, 0, 128, kT);  // f16, both K-major
       const uint32_t idesc_o = tc_idesc(0, 0, 0, 1, 128, D);   // A in TMEM, B MN-major
       const uint32_t base = smem_u32(sm);
       const uint64_t dq0 = tc_desc(base + SM::kQ, 2048, 128, 0);
       const uint64_t dk0 = tc_desc(base + SM::kK, 2048, 128, 0);
       const uint64_t dv0 = tc_desc(base + SM::kV, D * 16, 128, 0);
       constexpr uint32_t kNext = SM::kTile >> 4;  // the other row tile or stage
-      // S_t of half `half` of the tile in stage st
-      auto mma_s = [&](int t, uint32_t st, uint32_t half) {
-        const uint64_t dq = dq0 + t * kNext, dk = dk0 + st * kNext + half * (kS * 16 >> 4);
-        const uint32_t d = tmem + t * 128 + half * kS;
+      auto mma_s = [&](int t, uint32_t st) {  // S_t = Q_t K^T
+        const uint64_t dq = dq0 + t * kNext, dk = dk0 + st * kNext;
+        const uint32_t d = tmem + t * kT;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           tc_mma_f16(d, dq + k * (4096 >> 4), dk + k * (4096 >> 4), idesc_s, k > 0);
-        tc_commit(bars + kBarS + t * 2 + half);
+        tc_commit(bars + kBarS + t);
       };
-      auto mma_o = [&](int t, uint32_t st, uint32_t half, bool first) {  // O_t += P_t V
-        const uint64_t dv = dv0 + st * kNext + half * (kS * 2 * D >> 4);
-        const uint32_t d = tmem + 256 + t * 128, p = tmem + t * 128 + half * kS;
+      auto mma_o = [&](int t, uint32_t st, bool first) {  // O_t += P_t V
+        const uint64_t dv = dv0 + st * kNext;
+        const uint32_t d = tmem + 256 + t * 128, p = tmem + t * kT;
 #pragma unroll
-        for (int k = 0; k < kS / 16; ++k)
-          tc_mma_f16_ts(d, p + k * 8, dv + k * (2 * D * 16 >> 4), idesc_o, !(first && k == 0));
-        tc_commit(bars + kBarO + t * 2 + half);
+        for (int k = 0; k < kT / 16; ++k)  // the halves of P start 64 columns apart
+          tc_mma_f16_ts(d, p + (k >> 2) * kHalf + (k & 3) * 8, dv + k * (2 * D * 16 >> 4), idesc_o,
+                        !(first && k == 0));
       };
-      uint32_t g = 0;      // tiles done by this CTA
-      uint32_t nq = 0;     // bit t: phase of row tile t's Q
-      uint32_t np = 0;     // bit 2 t + half: phase of a P buffer
+      uint32_t g = 0;              // tiles done by this CTA
+      uint32_t nq = 0, np = 0;     // bit t: phase of row tile t's Q and P
       bool ok = true;
       for (int it = it0, u = u0; u < u1 && ok; ++it) {
         const Item im = load_item(a, pv, it, u, u1);
-        const int n = im.t1 - im.t0, two = im.rows > 128 ? 2 : 1;
+        const int n = im.t1 - im.t0;
         u += n;
-        // the first tile's scores
-        ok = wait(kBarKFull + (g & 1), (g >> 1) & 1);
-#pragma unroll 1
-        for (int x = 0; x < 2 * two && ok; ++x) {
-          const int t = x >> 1;
-          if ((x & 1) == 0) {
-            ok = wait(kBarQ + t, (nq >> t) & 1);
-            nq ^= 1u << t;
-            tc_fence_after();
-          }
-          if (ok) mma_s(t, g & 1, x & 1);
-        }
-        if (!ok) break;
-        tc_commit(bars + kBarKFree + (g & 1));
-        for (int k = 0; k < n && ok; ++k) {
+        const int two = im.rows > 128 ? 2 : 1;
+        // k = -1 issues the first S of the row tiles, k >= 0 P V of tile k and
+        // S of tile k + 1
+        for (int k = -1; k < n && ok; ++k) {
           const bool more = k + 1 < n;
-          const uint32_t g1 = g + 1;
-          ok = wait(kBarVFull + (g & 1), (g >> 1) & 1);
-          if (more) ok = ok && wait(kBarKFull + (g1 & 1), (g1 >> 1) & 1);
+          const uint32_t g1 = g + (k >= 0 ? 1 : 0);  // tile k + 1
+          if (more) ok = wait(kBarKFull + (g1 & 1), (g1 >> 1) & 1);
+          if (k >= 0) ok = ok && wait(kBarVFull + (g & 1), (g >> 1) & 1);
 #pragma unroll 1
-          for (uint32_t half = 0; half < 2 && ok; ++half) {
-#pragma unroll 1
-            for (int t = 0; t < two && ok; ++t) {
-              ok = wait(kBarP + t * 2 + half, (np >> (t * 2 + half)) & 1);
-              if (!ok) break;
-              np ^= 1u << (t * 2 + half);
-              tc_fence_after();
-              mma_o(t, g & 1, half, k == 0 && half == 0);
-              if (more) mma_s(t, g1 & 1, half);
+          for (int t = 0; t < two && ok; ++t) {
+            const uint32_t phase = k < 0 ? nq : np;
+            ok = wait((k < 0 ? kBarQ : kBarP) + t, (phase >> t) & 1);
+            if (!ok) break;
+            if (k < 0) nq ^= 1u << t;
+            else np ^= 1u << t;
+            tc_fence_after();
+            if (k >= 0) {
+              mma_o(t, g & 1, k == 0);
+              if (t + 1 == two) tc_commit(bars + kBarVFree + (g & 1));
+              if (!more) tc_commit(bars + kBarO + t);
             }
+            if (more) mma_s(t, g1 & 1);
           }
-          if (!ok) break;
-          tc_commit(bars + kBarVFree + (g & 1));
           if (more) tc_commit(bars + kBarKFree + (g1 & 1));
           g = g1;
         }
       }
     }
-  } else if (warp >= 8) {
-    convert_tiles<D, FMT>(a, pv, sm, abort_flag, it0, u0, u1, warp - 8, lane);
+  } else if (warp >= kConvWarp) {
+    convert_tiles<D, FMT>(a, pv, sm, abort_flag, it0, u0, u1, warp - kConvWarp, lane);
   } else {
     // ================================================= softmax warps
-    const int t = warp >> 2;            // row tile
-    const int rl = (warp & 3) * 32 + lane;  // row within it
+    const int t = warp >> 3, half = (warp >> 2) & 1;  // row tile, and tokens of its tiles
+    const int rl = (warp & 3) * 32 + lane;            // row within it
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t to = tmem + 256 + t * 128 + lanes;
-    uint32_t g = 0, steps = 0;  // tiles of the CTA; steps of this row tile
+    const uint32_t ts = tmem + t * kT + half * kHalf + lanes, to = tmem + 256 + t * 128 + lanes;
+    float* xch = reinterpret_cast<float*>(sm + SM::kXch) + warp * 32 + lane;
+    uint32_t nx = 0;
+    // Trade one value per row with the other warp of the rows.  The slots
+    // alternate: one is written again only after the other warp's next arrival.
+    auto trade = [&](float mine, float& other) {
+      float* slot = xch + (nx & 1) * (16 * 32);
+      *slot = mine;
+      __syncwarp();
+      const int bar = kBarX + t * 4 + (warp & 3);
+      if (lane == 0) mbar_arrive(bars + bar);
+      const bool good = wait_warp(bar, nx & 1);
+      ++nx;
+      other = slot[half ? -4 * 32 : 4 * 32];
+      return good;
+    };
+    uint32_t g = 0, ns = 0, no = 0;  // tiles of the CTA; tiles and items of this row tile
     bool ok = true;
     for (int it = it0, u = u0; u < u1 && ok; ++it) {
       const Item im = load_item(a, pv, it, u, u1);
@@ -774,8 +821,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
         const int eq = amax > 0.f ? exp_above(amax) : 0;
         const float fq = exp2i(14 - eq);
         uint8_t* dst = sm + SM::kQ + t * SM::kTile + (rl >> 3) * 128 + (rl & 7) * 16;
-#pragma unroll 4
-        for (int x = 0; x < D / 8; ++x) {  // from L1 this time
+#pragma unroll 2
+        for (int x0 = 0; x0 < D / 16; ++x0) {  // this thread's half, from L1
+          const int x = half * (D / 16) + x0;
           float f[8];
           get(x, f);
           const uint4 o = make_uint4(pack_half2(f[0] * fq, f[1] * fq),
@@ -802,105 +850,112 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
       const float cap_log2 = VAR == 2 ? a.cap * kLog2e : 0.f;
       float ref = kNegBig, l = 0.f;
 
-      for (int s = 0; s < 2 * n; ++s, ++steps) {
-        const int half = s & 1;
-        const uint32_t s4 = (g + (s >> 1)) & 3;
-        const int j0 = tile_token(im, im.t0 + (s >> 1)) + half * kS;
-        if (half == 0 && !wait_warp(kBarScale + s4, ((g + (s >> 1)) >> 2) & 1)) {
+      for (int k = 0; k < n; ++k, ++g) {
+        const uint32_t s4 = g & 3;
+        const int j0 = tile_token(im, im.t0 + k) + half * kHalf;
+        if (!wait_warp(kBarScale + s4, (g >> 2) & 1) || !wait_warp(kBarS + t, ns & 1)) {
           ok = false;
           break;
         }
-        if (!wait_warp(kBarS + t * 2 + half, (steps >> 1) & 1)) {
-          ok = false;
-          break;
-        }
+        ++ns;
         tc_fence_after();
-        const uint32_t ts = tmem + t * 128 + half * kS + lanes;
-        const float* sk = scales + s4 * 2 * kT + half * kS;
+        const float* sk = scales + s4 * 2 * kT + half * kHalf;
         const float* sv = sk + kT;
-        uint32_t raw[4][16];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld16(ts + c * 16, raw[c]);
         const uint2 val = *reinterpret_cast<const uint2*>(&infos[s4].valid[half * 2]);
-        const float4 vm = *reinterpret_cast<const float4*>(infos[s4].vmax);
-        // whether every row of the warp sees the whole step
+        // whether every row of the warp sees all of the thread's tokens
         const bool whole =
-            ((j0 >= wB && j0 + kS - 1 <= pA) || (VAR == 0 && j0 + kS <= pre)) &&
+            ((j0 >= wB && j0 + kHalf - 1 <= pA) || (VAR == 0 && j0 + kHalf <= pre)) &&
             (val.x & val.y) == 0xFFFFFFFFu && (VAR < 2 || a.cap <= kCapFast);
-        float vmax = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
-        const ulonglong2* sk2 = reinterpret_cast<const ulonglong2*>(sk);
-        const ulonglong2* sv2 = reinterpret_cast<const ulonglong2*>(sv);
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_landed(raw[c]);
-
-        // ---- scores times K scales (VAR > 0: final scores), and the largest
-        uint64_t z[32];
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const ulonglong2 f = sk2[i / 2];
-          const uint32_t* r = &raw[i / 8][(i % 8) * 2];
-          z[i] = f2_mul(f2_pack(__uint_as_float(r[0]), __uint_as_float(r[1])), f.x);
-          z[i + 1] = f2_mul(f2_pack(__uint_as_float(r[2]), __uint_as_float(r[3])), f.y);
-        }
-        uint2 mw = make_uint2(0xFFFFFFFFu, 0xFFFFFFFFu);
+        uint2 mw = make_uint2(0xFFFFFFFFu, 0xFFFFFFFFu);  // tokens that the row sees
+        const float zf = VAR > 0 ? 1.f : zs;
+        float bound;
+        // ---- scores times K scales (VAR > 0: final scores) go back to TMEM:
+        // reading the scales a second time would cost shared-memory bandwidth
+        // that the MMAs' operands need.  And a bound of z + log2(V scale).
         if (whole) {
-          if constexpr (VAR > 0) {
-            // the bias of tokens 2 i, 2 i + 1: -slope (pos - j)
-            const uint64_t zs2 = f2_pack(zs, zs);
-            const float b0 = slope * static_cast<float>(j0 - pos);
-            const uint64_t bias = f2_pack(b0, b0 + slope), step = f2_pack(2.f * slope, 2.f * slope);
+          const float2 vm = *reinterpret_cast<const float2*>(&infos[s4].vmax[half * 2]);
+          const ulonglong2* sk2 = reinterpret_cast<const ulonglong2*>(sk);
+          const uint64_t zs2 = f2_pack(zs, zs), step = f2_pack(2.f * slope, 2.f * slope);
+          float m4[4];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const uint64_t b =
-                  f2_fma(step, f2_pack(static_cast<float>(i), static_cast<float>(i)), bias);
-              if constexpr (VAR == 1) {
-                z[i] = f2_fma(z[i], zs2, b);
-              } else {  // cap tanh(z / cap) = cap - 2 cap / (2^x + 1)
-                float x, y;
-                f2_unpack(f2_mul(z[i], zs2), x, y);
-                z[i] = f2_add(f2_pack(cap_fast(x, cap_log2), cap_fast(y, cap_log2)), b);
+          for (int x = 0; x < 4; ++x) m4[x] = __int_as_float(0xff800000);
+#pragma unroll 2
+          for (int c = 0; c < 4; ++c) {
+            uint32_t raw[16];
+            tmem_ld16(ts + c * 16, raw);
+            // the bias of tokens 2 i, 2 i + 1 of the chunk: -slope (pos - j)
+            const float b0 = VAR > 0 ? slope * static_cast<float>(j0 + c * 16 - pos) : 0.f;
+            const uint64_t bias = f2_pack(b0, b0 + slope);
+            tmem_ld_wait();
+            tmem_landed(raw);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const ulonglong2 f = sk2[c * 4 + i / 2];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                uint32_t* r = raw + (i + x) * 2;
+                uint64_t z = f2_mul(f2_pack(__uint_as_float(r[0]), __uint_as_float(r[1])),
+                                    x ? f.y : f.x);
+                float p, q;
+                if constexpr (VAR > 0) {
+                  const float fi = static_cast<float>(i + x);
+                  const uint64_t b = f2_fma(step, f2_pack(fi, fi), bias);
+                  if constexpr (VAR == 1) {
+                    z = f2_fma(z, zs2, b);
+                  } else {  // cap tanh(z / cap) = cap - 2 cap / (2^x + 1)
+                    f2_unpack(f2_mul(z, zs2), p, q);
+                    z = f2_add(f2_pack(cap_fast(p, cap_log2), cap_fast(q, cap_log2)), b);
+                  }
+                }
+                f2_unpack(z, p, q);
+                m4[(i + x) & 3] = max3(m4[(i + x) & 3], p, q);
+                r[0] = __float_as_uint(p);
+                r[1] = __float_as_uint(q);
               }
             }
+            tmem_st16(ts + c * 16, raw);
           }
+          bound = bound_of(max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * zf, fmaxf(vm.x, vm.y));
         } else {
           // some row masks some token: masked scores become -inf, and a row's V
           // bound is that of the tokens it sees
           mw.x = (word_bits(j0, wf, pos + 1) | word_bits(j0, 0, pre)) & val.x;
           mw.y = (word_bits(j0 + 32, wf, pos + 1) | word_bits(j0 + 32, 0, pre)) & val.y;
-          vmax = 0.f;
+          float mx = __int_as_float(0xff800000), vmax = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t raw[16];
+            tmem_ld16(ts + c * 16, raw);
+            tmem_ld_wait();
+            tmem_landed(raw);
+            const uint32_t m = (c < 2 ? mw.x : mw.y) >> (16 * (c & 1));
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float x[2];
-            f2_unpack(z[i], x[0], x[1]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int c = 2 * i + e;
+            for (int i = 0; i < 16; ++i) {
+              float z = __uint_as_float(raw[i]) * sk[c * 16 + i];
               if constexpr (VAR > 0) {
-                x[e] *= zs;
-                if constexpr (VAR == 2) x[e] = cap_log2 * tanh_f32(x[e] * (0.5f / kLog2e));
-                x[e] = fmaf(-slope, fabsf(static_cast<float>(pos - j0 - c)), x[e]);
+                z *= zs;
+                if constexpr (VAR == 2) z = cap_log2 * tanh_f32(z * (0.5f / kLog2e));
+                z = fmaf(-slope, fabsf(static_cast<float>(pos - j0 - c * 16 - i)), z);
               }
-              const bool see = ((c < 32 ? mw.x : mw.y) >> (c & 31)) & 1;
-              x[e] = see ? x[e] : __int_as_float(0xff800000);
-              vmax = fmaxf(vmax, see ? sv[c] : 0.f);
+              const bool see = (m >> i) & 1;
+              z = see ? z : __int_as_float(0xff800000);
+              mx = fmaxf(mx, z);
+              vmax = fmaxf(vmax, see ? sv[c * 16 + i] : 0.f);
+              raw[i] = __float_as_uint(z);
             }
-            z[i] = f2_pack(x[0], x[1]);
+            tmem_st16(ts + c * 16, raw);
           }
+          bound = bound_of(mx * zf, vmax);
         }
-        float m4[4];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float p, q;
-          f2_unpack(z[i], p, q);
-          m4[i & 3] = i < 4 ? fmaxf(p, q) : fmaxf(fmaxf(m4[i & 3], p), q);
+        tmem_st_wait();
+        // ---- the reference, shared by the row's two threads: where the bound
+        // passed it by 2^kTau it moves, and with it the sums and O
+        float other;
+        if (!trade(bound, other)) {
+          ok = false;
+          break;
         }
-        const float zf = VAR > 0 ? 1.f : zs;
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        // ---- the reference: a bound of z + log2(V scale); where it was passed
-        // by 2^kTau it moves, and with it the sum and O
-        const float bound = fmaf(
-            mx, zf, static_cast<float>(min(max(exp_above(vmax), -60), 120)));
+        bound = fmaxf(bound, other);
         float al = 1.f;
         if (bound > ref + kTau) {
           al = ex2(ref - bound);
@@ -908,49 +963,50 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
         }
         if (__any_sync(0xffffffffu, al != 1.f)) {
           l *= al;
-          if (s > 0) {
-            // O is at rest once P V of the last step is done
-            if (!wait_warp(kBarO + t * 2 + (half ^ 1), ((steps - 1) >> 1) & 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
+          if (k > 0) {  // (P V of the last tile is done: S of this one came behind it)
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
+            for (int c = 0; c < D / 32; ++c) {
+              const uint32_t at = to + half * (D / 2) + c * 16;
               uint32_t o[16];
-              tmem_ld16(to + c * 16, o);
+              tmem_ld16(at, o);
               tmem_ld_wait();
               tmem_landed(o);
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-              tmem_st16(to + c * 16, o);
+              tmem_st16(at, o);
             }
           }
         }
         // ---- P and its sum
         const float c0 = kShift - ref;
         const uint64_t zf2 = f2_pack(zf, zf), c02 = f2_pack(c0, c0);
+        const ulonglong2* sv2 = reinterpret_cast<const ulonglong2*>(sv);
         uint64_t la = 0, lb = 0;  // (0.f, 0.f)
         auto weigh = [&](auto masked) {
-#pragma unroll
+#pragma unroll 2
           for (int c = 0; c < 4; ++c) {
-            uint32_t pw[8];
+            uint32_t raw[16], pw[8];
+            tmem_ld16(ts + c * 16, raw);
+            tmem_ld_wait();
+            tmem_landed(raw);
+            const uint32_t m = (c < 2 ? mw.x : mw.y) >> (16 * (c & 1));
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
               const ulonglong2 v = sv2[c * 4 + i / 2];
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                const int zi = c * 8 + i + x;
+                const uint32_t* r = raw + (i + x) * 2;
+                const uint64_t z = f2_pack(__uint_as_float(r[0]), __uint_as_float(r[1]));
                 float p, q;
-                f2_unpack(VAR > 0 ? f2_add(z[zi], c02) : f2_fma(z[zi], zf2, c02), p, q);
+                f2_unpack(VAR > 0 ? f2_add(z, c02) : f2_fma(z, zf2, c02), p, q);
                 const uint64_t p2 = f2_pack(ex2(p), ex2(q));
                 if (x) lb = f2_add(lb, p2);
                 else la = f2_add(la, p2);
                 uint64_t v2 = x ? v.y : v.x;
                 if constexpr (masked.value) {  // a masked token's scale may be anything
-                  const uint32_t b = (zi < 16 ? mw.x : mw.y) >> (2 * zi & 31);
                   f2_unpack(v2, p, q);
-                  v2 = f2_pack(b & 1 ? p : 0.f, b & 2 ? q : 0.f);
+                  v2 = f2_pack((m >> (2 * (i + x))) & 1 ? p : 0.f,
+                               (m >> (2 * (i + x) + 1)) & 1 ? q : 0.f);
                 }
                 f2_unpack(f2_mul(p2, v2), p, q);
                 pw[i + x] = pack_half2(p, q);
@@ -967,24 +1023,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars + kBarP + t * 2 + half);
+        if (lane == 0) mbar_arrive(bars + kBarP + t);
       }
       if (!ok) break;
-      g += n;
 
-      // ---- the block's result, or this range's piece of it
-      if (!wait_warp(kBarO + t * 2 + 1, ((steps - 1) >> 1) & 1)) {
+      // ---- the block's result, or this range's piece of it: half the dims each
+      float other;
+      if (!trade(l, other) || !wait_warp(kBarO + t, no & 1)) {
         ok = false;
         break;
       }
+      ++no;
+      l += other;
       tc_fence_after();
       const bool piece = im.t0 > 0 || im.t1 < im.tl.count;
       const float inv = piece ? 1.f : (l == 0.f ? 0.f : 1.f / l);
       const int slot = blockIdx.x * 2 + (im.t0 > 0 ? 0 : 1);
       const bool stat = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
       const float* vch = a.v_scale + static_cast<long>(im.kvh) * D;
-#pragma unroll 2
-      for (int c = 0; c < D / 16; ++c) {
+#pragma unroll 1
+      for (int c0 = 0; c0 < D / 32; ++c0) {
+        const int c = half * (D / 32) + c0;
         uint32_t o[16];
         tmem_ld16(to + c * 16, o);
         tmem_ld_wait();
@@ -1018,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           }
         }
       }
-      if (piece && live) pv.ml[static_cast<long>(slot) * kRows + r] = make_float2(ref, l);
+      if (piece && live && half == 0) pv.ml[static_cast<long>(slot) * kRows + r] = make_float2(ref, l);
       tc_fence_before();
     }
   }
