@@ -19,13 +19,18 @@
 // results that a merge kernel folds with the log-sum-exp rule.  A long chunk
 // and a few rows over a long context are balanced alike.
 //
-// Numerics.  Codes become f16 exactly (E4M3 scaled by 2^-8).  q is exact in
-// f16 after a power-of-two normaliser per row (CHANNEL_STATIC folds the K
-// scales into it and rounds once, 2^-11).  K scales multiply the fp32 scores;
-// V scales go into P, which enters the second product as f16 (2^-11).  The
-// running reference of a row is a bound of max(z + log2 v_scale), so P stays
-// inside f16 whatever the scales; it moves only when passed by 2^kTau, which
-// is exact, as sums and O carry the same reference.
+// Numerics.  The converters give K^ and V^ as f16: a code times its token's scale
+// relative to the largest of its 32 tokens (a power of two 2^e that stays
+// outside), rounded once (2^-11; exact for MX blocks and static scales).  Scaling
+// the fp32 scores and P instead would keep the scales exact, but costs every
+// score two multiplications and two broadcast loads beside MMAs that fill the
+// shared-memory bandwidth: 1.45 ms against 0.9 ms for 2048 queries over 16384
+// tokens.  q is exact in f16 after a power-of-two normaliser per row
+// (CHANNEL_STATIC folds the K scales into it and rounds once, 2^-11).  P enters
+// the second product as f16 (2^-11).  The running reference of a row is a bound
+// of max(z + e), e the exponent of the V^ group, so P stays inside f16 whatever
+// the scales; it moves only when passed by 2^kTau, which is exact, as sums and O
+// carry the same reference.
 //
 // Roles (24 warps): 0-7 and 8-15 the softmax of row tiles 0 and 1, two threads
 // per row, each with 64 of a tile's 128 tokens (four warps per scheduler hide
@@ -136,24 +141,26 @@ __device__ __forceinline__ RowBlock load_row_block(const int4* p) {
 }
 
 // ---------------------------------------------------------------- shared memory
+// Of a tile's four groups of 32 tokens: the exponents that K^ and V^ leave out,
+// the tokens whose page exists, and those whose V is not finite (zeroed in V^
+// where some row masks them; rows that see one are NaN).
+struct StageInfo {
+  int ek[4], ev[4];
+  uint32_t valid[4], bad[4];
+};
+
 template <int D>
 struct Smem {
   static constexpr int kTile = kT * D * 2;  // a 128-row f16 tile
   static constexpr int kQ = 0;              // two row tiles
   static constexpr int kK = 2 * kTile;      // two stages
   static constexpr int kV = 4 * kTile;      // two stages
-  static constexpr int kScale = 6 * kTile;  // four stages of [K scales][V scales] f32
-  static constexpr int kInfo = kScale + 4 * 2 * kT * 4;  // four stages of StageInfo
-  static constexpr int kXch = kInfo + 4 * 64;  // [parity][warp of softmax][lane] f32
+  static constexpr int kInfo = 6 * kTile;   // four stages of StageInfo
+  static constexpr int kXch = kInfo + 4 * sizeof(StageInfo);  // [parity][warp of softmax][lane] f32
   static constexpr int kBars = kXch + 2 * 16 * 32 * 4;
   static constexpr int kMisc = kBars + 320;  // TMEM base, abort flag
   static constexpr int kBytes = kMisc + 16;
 };
-struct StageInfo {
-  uint32_t valid[4];  // tokens whose page exists
-  float vmax[4];      // largest V scale of each 32 tokens
-};
-
 // Barriers and the arrivals that complete a phase.  Q and P: the eight softmax
 // warps of the row tile; scales: the eight conversion jobs of the tile; K and V
 // full: four jobs; X (t * 4 + lane quarter): the two softmax warps of the same
@@ -194,12 +201,15 @@ __device__ __forceinline__ bool codes_nonfinite(const uint4& c) {
   return bad != 0;
 }
 
-__device__ __forceinline__ uint4 hmul8(const uint4& a, uint32_t f) {
-  auto m = [&](uint32_t x) {
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x),
-                              *reinterpret_cast<const __half2*>(&f));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  };
+__device__ __forceinline__ __half2 h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+__device__ __forceinline__ uint32_t h2_bits(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+// Eight f16 codes times a scale hi + lo, rounded once.
+__device__ __forceinline__ uint4 scale8(const uint4& a, __half2 hi, __half2 lo) {
+  auto m = [&](uint32_t x) { return h2_bits(__hfma2(h2(x), hi, __hmul2(h2(x), lo))); };
+  return make_uint4(m(a.x), m(a.y), m(a.z), m(a.w));
+}
+__device__ __forceinline__ uint4 scale8(const uint4& a, __half2 f) {
+  auto m = [&](uint32_t x) { return h2_bits(__hmul2(h2(x), f)); };
   return make_uint4(m(a.x), m(a.y), m(a.z), m(a.w));
 }
 
@@ -224,11 +234,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// A row's bound of z + log2(V scale) from the largest of each (vmax 0: none).
-__device__ __forceinline__ float bound_of(float zmax, float vmax) {
-  return zmax + static_cast<float>(min(max(exp_above(vmax), -60), 120));
-}
-
 // D[tmem] (+)= A[tmem] * B[smem], one thread.
 __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                               bool accumulate) {
@@ -382,7 +387,8 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
     }
     float sc = 1.f;  // scale of token 32 dw + lane
     bool sok;
-    uint32_t below[H];  // MX: exponents of the lane's chunks below their rows' largest, by group
+    uint32_t ex[H];  // MX: exponents of the lane's chunks, by group
+    int em = 0;      // ... and of the token's largest block
     {
       const bool want = wanted(j + lane);
       sok = want && (lane < 16 ? blk_ok[0] : blk_ok[1]);
@@ -393,31 +399,25 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
       } else if (a.mode == FP8PA_SCALE_SEGMENT) {
         if (sok) sc = __ldg(gscale + static_cast<long>(lane < 16 ? ids[0] : ids[1]) * a.hp + kvh);
       } else if constexpr (MX) {
-        // 2, 4 or 8 bytes a row; absent ones read as zero
-        auto row_bytes = [&](size_t row, uint32_t (&w)[2]) {
-          const uint8_t* e = reinterpret_cast<const uint8_t*>(gscale) + row * nbx;
-          w[1] = nbx == 8 ? __ldg(reinterpret_cast<const uint32_t*>(e) + 1) : 0u;
-          w[0] = nbx == 2 ? __ldg(reinterpret_cast<const uint16_t*>(e))
-                          : __ldg(reinterpret_cast<const uint32_t*>(e));
-        };
-        uint32_t w[4][2];  // (a missing block's rows read as block 0's: not used)
+        // 2, 4 or 8 bytes a row (a missing block's rows read as block 0's: not
+        // used)
+        const uint8_t* exps = reinterpret_cast<const uint8_t*>(gscale);
+        uint32_t w[2];
+        w[1] = nbx == 8 ? __ldg(reinterpret_cast<const uint32_t*>(exps + rw * 8) + 1) : 0u;
+        w[0] = nbx == 2 ? __ldg(reinterpret_cast<const uint16_t*>(exps + rw * 2))
+                        : __ldg(reinterpret_cast<const uint32_t*>(exps + rw * nbx));
+        em = sok ? static_cast<int>(max_byte(w)) : 0;
+        // the lane's rows' blocks from the lanes that hold them
 #pragma unroll
-        for (int x = 0; x < 4; ++x) row_bytes(row[x >> 1] + (x & 1) * 8 + r8, w[x]);
+        for (int h = 0; h < H; ++h) {
+          const int b = (h * 4 + c4) * 16 / a.gs;
+          ex[h] = 0;
 #pragma unroll
-        for (int h = 0; h < H; ++h) below[h] = 0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t em = max_byte(w[x]);
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            const int b = (h * 4 + c4) * 16 / a.gs;
-            below[h] |= (em - (((b & 4 ? w[x][1] : w[x][0]) >> (8 * (b & 3))) & 0xFF)) << (8 * x);
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t lo4 = __shfl_sync(0xffffffffu, w[0], x * 8 + r8);
+            const uint32_t hi4 = __shfl_sync(0xffffffffu, w[1], x * 8 + r8);
+            ex[h] |= (((b & 4 ? hi4 : lo4) >> (8 * (b & 3))) & 0xFFu) << (8 * x);
           }
-        }
-        if (sok) {
-          uint32_t w[2];
-          row_bytes(rw, w);
-          sc = exp2i(static_cast<int>(max_byte(w)) - 127);
         }
       }
     }
@@ -452,39 +452,57 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
     }
 
     const uint32_t st = g & 1, s4 = g & 3;
-    float* ss = reinterpret_cast<float*>(sm + SM::kScale) + s4 * 2 * kT + (V ? kT : 0) + dw * 32;
-    // The stage's last reader was the MMA of tile g - 2; the scale stage's the
+    // The stage's last reader was the MMA of tile g - 2; the info stage's the
     // softmax of tile g - 4, whose P was waited for before that MMA.
     if (g >= 2 && !__all_sync(0xffffffffu,
                               tc_wait(bars + (V ? kBarVFree : kBarKFree) + st,
                                       ((g >> 1) - 1) & 1, abort_flag, a.err)))
       return;
-    ss[lane] = sc;
     const uint32_t valid = __ballot_sync(0xffffffffu, sok);
-    const float vmax = warp_max_f32(sok && sc <= FLT_MAX ? sc : 0.f);
-    if (lane == 0) {
-      if (V) infos[s4].vmax[dw] = vmax;
-      else infos[s4].valid[dw] = valid;
+    // the exponent above the group's largest (finite) scale, and the scales
+    // relative to it
+    const bool finite = sc <= FLT_MAX;  // (not for a NaN)
+    int e;
+    if constexpr (MX) {
+      e = max(__reduce_max_sync(0xffffffffu, em) - 127, -100);
+    } else {
+      e = min(max(exp_above(warp_max_f32(sok && finite ? sc : 0.f)), -100), 120);
+      if (a.mode == FP8PA_SCALE_CHANNEL_STATIC) e = 0;
+      sc *= exp2i(-e);
     }
-    __syncwarp();
     // Groups to keep; the others become zero.  In a tile that some row does
-    // not see whole, a non-finite V code would reach rows that mask its token
-    // (0 * NaN): it is zeroed and its token's scale made NaN, for the rows that
-    // do see it.
-    uint32_t keep = okm;
-    if (FMT != FP8PA_INT8 && V && !whole) {
+    // not see whole, a V that is not finite would reach rows that mask its token
+    // (0 * NaN): it is zeroed and its token marked, for the rows that do see it.
+    uint32_t keep = okm, bad = 0;
+    if (V && !whole) {
+      uint32_t nf = 0;  // bit x: this lane's chunks of group x
+      if constexpr (FMT != FP8PA_INT8) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        bool nf = false;
+        for (int x = 0; x < 4; ++x) {
+          bool f = false;
 #pragma unroll
-        for (int h = 0; h < H; ++h) nf = nf || codes_nonfinite<FMT>(buf[x][h]);
-        uint32_t any = nf ? 1u : 0u;
-        any |= __shfl_xor_sync(0xffffffffu, any, 8);
-        any |= __shfl_xor_sync(0xffffffffu, any, 16);
-        if (any && ((okm >> x) & 1)) {
-          keep &= ~(1u << x);
-          if (c4 == 0) ss[x * 8 + r8] = __int_as_float(0x7FC00000);
+          for (int h = 0; h < H; ++h) f = f || codes_nonfinite<FMT>(buf[x][h]);
+          nf |= f ? 1u << x : 0u;
         }
+        nf |= __shfl_xor_sync(0xffffffffu, nf, 8);
+        nf |= __shfl_xor_sync(0xffffffffu, nf, 16);
+      }
+      const uint32_t nfs = __ballot_sync(0xffffffffu, sok && !finite);  // by token
+#pragma unroll
+      for (int x = 0; x < 4; ++x) nf |= ((nfs >> (x * 8 + r8)) & 1u) << x;
+      nf &= okm;
+      keep &= ~nf;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)  // lanes 0-7 hold the rows in order
+        bad |= (__ballot_sync(0xffffffffu, (nf >> x) & 1u) & 0xFFu) << (8 * x);
+    }
+    if (lane == 0) {
+      if (V) {
+        infos[s4].ev[dw] = e;
+        infos[s4].bad[dw] = bad;
+      } else {
+        infos[s4].ek[dw] = e;
+        infos[s4].valid[dw] = valid;
       }
     }
     // K: core matrices (8 tokens x 8 dims) 128 bytes apart along the tokens,
@@ -496,36 +514,33 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
       *reinterpret_cast<uint4*>(dst + x * kG + h * kC) = p;
       *reinterpret_cast<uint4*>(dst + x * kG + h * kC + kH) = q;
     };
-    if (!MX && keep == 0xFu) {
+    const bool plain = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          uint4 p, q;
-          codes16_to_f16<FMT>(buf[x][h], p, q);
-          store(x, h, p, q);
-        }
+    for (int x = 0; x < 4; ++x) {
+      __half2 hi, lo;
+      if constexpr (!MX) {
+        const float f = __shfl_sync(0xffffffffu, sc, x * 8 + r8);
+        const __half fh = __float2half_rn(f);
+        hi = __half2half2(fh);
+        lo = __half2half2(__float2half_rn(f - __half2float(fh)));
       }
-    } else {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const bool kept = (keep >> x) & 1;
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          uint4 p, q;
-          codes16_to_f16<FMT>(buf[x][h], p, q);
-          if constexpr (MX) {
-            // the block's power of two relative to the row's largest
-            const int e = (below[h] >> (8 * x)) & 0xFF;
-            const float f = __int_as_float((127 - min(e, 126)) << 23);
-            const __half2 f2 = __floats2half2_rn(f, f);
-            const uint32_t fw = *reinterpret_cast<const uint32_t*>(&f2);
-            p = hmul8(p, fw);
-            q = hmul8(q, fw);
-          }
-          if (!kept) p = q = make_uint4(0u, 0u, 0u, 0u);
-          store(x, h, p, q);
+      for (int h = 0; h < H; ++h) {
+        uint4 p, q;
+        codes16_to_f16<FMT>(buf[x][h], p, q);
+        if constexpr (MX) {
+          // the block's power of two relative to the group's largest
+          const int be = static_cast<int>((ex[h] >> (8 * x)) & 0xFFu) - 127 - e;
+          const float f = __int_as_float((max(min(be, 0), -126) + 127) << 23);
+          const __half2 f2 = __floats2half2_rn(f, f);
+          p = scale8(p, f2);
+          q = scale8(q, f2);
+        } else if (!plain) {
+          p = scale8(p, hi, lo);
+          q = scale8(q, hi, lo);
         }
+        if (keep != 0xFu && ((keep >> x) & 1) == 0) p = q = make_uint4(0u, 0u, 0u, 0u);
+        store(x, h, p, q);
       }
     }
     fence_proxy_async();
@@ -552,7 +567,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + SM::kMisc);
   int& s_abort = *reinterpret_cast<int*>(sm + SM::kMisc + 4);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
-  float* scales = reinterpret_cast<float*>(sm + SM::kScale);
   StageInfo* infos = reinterpret_cast<StageInfo*>(sm + SM::kInfo);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -785,97 +799,88 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++ns;
         tc_fence_after();
-        const float* sk = scales + s4 * 2 * kT + half * kHalf;
-        const float* sv = sk + kT;
         const uint2 val = *reinterpret_cast<const uint2*>(&infos[s4].valid[half * 2]);
+        const uint2 bad = *reinterpret_cast<const uint2*>(&infos[s4].bad[half * 2]);
+        const int2 ek = *reinterpret_cast<const int2*>(&infos[s4].ek[half * 2]);
+        const int2 ev = *reinterpret_cast<const int2*>(&infos[s4].ev[half * 2]);
         // whether every row of the warp sees all of the thread's tokens
         const bool whole =
             ((j0 >= wB && j0 + kHalf - 1 <= pA) || (VAR == 0 && j0 + kHalf <= pre)) &&
             (val.x & val.y) == 0xFFFFFFFFu && (VAR < 2 || a.cap <= kCapFast);
         uint2 mw = make_uint2(0xFFFFFFFFu, 0xFFFFFFFFu);  // tokens that the row sees
-        const float zf = VAR > 0 ? 1.f : zs;
-        float bound;
-        // ---- scores times K scales (VAR > 0: final scores) go back to TMEM:
-        // reading the scales a second time would cost shared-memory bandwidth
-        // that the MMAs' operands need.  And a bound of z + log2(V scale).
-        if (whole) {
-          const float2 vm = *reinterpret_cast<const float2*>(&infos[s4].vmax[half * 2]);
-          const ulonglong2* sk2 = reinterpret_cast<const ulonglong2*>(sk);
-          const uint64_t zs2 = f2_pack(zs, zs), step = f2_pack(2.f * slope, 2.f * slope);
-          float m4[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) m4[x] = __int_as_float(0xff800000);
-          uint32_t buf[2][16];
-          tmem_ld16(ts, buf[0]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t(&raw)[16] = buf[c & 1];
-            tmem_ld_wait();
-            tmem_landed(raw);
-            if (c < 3) tmem_ld16(ts + (c + 1) * 16, buf[(c + 1) & 1]);
-            // the bias of tokens 2 i, 2 i + 1 of the chunk: -slope (pos - j)
-            const float b0 = VAR > 0 ? slope * static_cast<float>(j0 + c * 16 - pos) : 0.f;
-            const uint64_t bias = f2_pack(b0, b0 + slope);
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const ulonglong2 f = sk2[c * 4 + i / 2];
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                uint32_t* r = raw + (i + x) * 2;
-                uint64_t z = f2_mul(f2_pack(__uint_as_float(r[0]), __uint_as_float(r[1])),
-                                    x ? f.y : f.x);
-                float p, q;
-                if constexpr (VAR > 0) {
-                  const float fi = static_cast<float>(i + x);
-                  const uint64_t b = f2_fma(step, f2_pack(fi, fi), bias);
-                  if constexpr (VAR == 1) {
-                    z = f2_fma(z, zs2, b);
-                  } else {  // cap tanh(z / cap) = cap - 2 cap / (2^x + 1)
-                    f2_unpack(f2_mul(z, zs2), p, q);
-                    z = f2_add(f2_pack(cap_fast(p, cap_log2), cap_fast(q, cap_log2)), b);
-                  }
-                }
-                f2_unpack(z, p, q);
-                m4[(i + x) & 3] = max3(m4[(i + x) & 3], p, q);
-                r[0] = __float_as_uint(p);
-                r[1] = __float_as_uint(q);
-              }
-            }
-            tmem_st16(ts + c * 16, raw);
-          }
-          bound = bound_of(max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * zf, fmaxf(vm.x, vm.y));
-        } else {
-          // some row masks some token: masked scores become -inf, and a row's V
-          // bound is that of the tokens it sees
+        if (!whole) {
           mw.x = (word_bits(j0, wf, pos + 1) | word_bits(j0, 0, pre)) & val.x;
           mw.y = (word_bits(j0 + 32, wf, pos + 1) | word_bits(j0 + 32, 0, pre)) & val.y;
-          float mx = __int_as_float(0xff800000), vmax = 0.f;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t raw[16];
-            tmem_ld16(ts + c * 16, raw);
+        }
+        if ((mw.x & bad.x) | (mw.y & bad.y)) l = __int_as_float(0x7FC00000);
+        // ---- a bound of z + e over the row's tokens, 32 scores at a time.  VAR >
+        // 0 puts the final scores back into TMEM.
+        float bound = __int_as_float(0xff800000);
+        auto find = [&](auto masked) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            uint32_t raw[2][16];
+            tmem_ld16(ts + w * 32, raw[0]);
+            tmem_ld16(ts + w * 32 + 16, raw[1]);
+            const uint32_t m = w ? mw.y : mw.x;
+            const float zw = zs * exp2i(w ? ek.y : ek.x);  // factor of this group's scores
+            const int jw = j0 + w * 32;
             tmem_ld_wait();
-            tmem_landed(raw);
-            const uint32_t m = (c < 2 ? mw.x : mw.y) >> (16 * (c & 1));
+            tmem_landed(raw[0]);
+            tmem_landed(raw[1]);
+            float m4[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) m4[x] = __int_as_float(0xff800000);
+            // the bias of tokens 2 i, 2 i + 1 of the group: -slope (pos - j)
+            const float b0 = VAR > 0 ? slope * static_cast<float>(jw - pos) : 0.f;
+            const uint64_t zw2 = f2_pack(zw, zw), bias = f2_pack(b0, b0 + slope);
+            const uint64_t step = f2_pack(2.f * slope, 2.f * slope);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              float z = __uint_as_float(raw[i]) * sk[c * 16 + i];
+              uint32_t* r = &raw[i / 8][(i % 8) * 2];
+              float x[2] = {__uint_as_float(r[0]), __uint_as_float(r[1])};
               if constexpr (VAR > 0) {
-                z *= zs;
-                if constexpr (VAR == 2) z = cap_log2 * tanh_f32(z * (0.5f / kLog2e));
-                z = fmaf(-slope, fabsf(static_cast<float>(pos - j0 - c * 16 - i)), z);
+                if constexpr (masked.value) {
+#pragma unroll
+                  for (int y = 0; y < 2; ++y) {
+                    x[y] *= zw;
+                    if constexpr (VAR == 2) x[y] = cap_log2 * tanh_f32(x[y] * (0.5f / kLog2e));
+                    x[y] = fmaf(-slope, fabsf(static_cast<float>(pos - jw - 2 * i - y)), x[y]);
+                  }
+                } else {
+                  const float fi = static_cast<float>(i);
+                  const uint64_t b = f2_fma(step, f2_pack(fi, fi), bias);
+                  uint64_t z = f2_pack(x[0], x[1]);
+                  if constexpr (VAR == 1) {
+                    z = f2_fma(z, zw2, b);
+                  } else {  // cap tanh(z / cap) = cap - 2 cap / (2^x + 1)
+                    f2_unpack(f2_mul(z, zw2), x[0], x[1]);
+                    z = f2_add(f2_pack(cap_fast(x[0], cap_log2), cap_fast(x[1], cap_log2)), b);
+                  }
+                  f2_unpack(z, x[0], x[1]);
+                }
               }
-              const bool see = (m >> i) & 1;
-              z = see ? z : __int_as_float(0xff800000);
-              mx = fmaxf(mx, z);
-              vmax = fmaxf(vmax, see ? sv[c * 16 + i] : 0.f);
-              raw[i] = __float_as_uint(z);
+              if constexpr (masked.value) {
+                x[0] = (m >> (2 * i)) & 1 ? x[0] : __int_as_float(0xff800000);
+                x[1] = (m >> (2 * i + 1)) & 1 ? x[1] : __int_as_float(0xff800000);
+              }
+              m4[i & 3] = max3(m4[i & 3], x[0], x[1]);
+              if constexpr (VAR > 0) {
+                r[0] = __float_as_uint(x[0]);
+                r[1] = __float_as_uint(x[1]);
+              }
             }
-            tmem_st16(ts + c * 16, raw);
+            if constexpr (VAR > 0) {
+              tmem_st16(ts + w * 32, raw[0]);
+              tmem_st16(ts + w * 32 + 16, raw[1]);
+            }
+            const float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+            bound = fmaxf(bound, fmaf(mx, VAR > 0 ? 1.f : zw, static_cast<float>(w ? ev.y : ev.x)));
           }
-          bound = bound_of(mx * zf, vmax);
-        }
-        tmem_st_wait();
+        };
+        if (whole) find(std::false_type{});
+        else find(std::true_type{});
+        if constexpr (VAR > 0) tmem_st_wait();
         // ---- the reference, shared by the row's two threads: where the bound
         // passed it by 2^kTau it moves, and with it the sums and O
         float other;
@@ -905,52 +910,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // ---- P and its sum
-        const float c0 = kShift - ref;
-        const uint64_t zf2 = f2_pack(zf, zf), c02 = f2_pack(c0, c0);
-        const ulonglong2* sv2 = reinterpret_cast<const ulonglong2*>(sv);
-        uint64_t la = 0, lb = 0;  // (0.f, 0.f)
+        // ---- P (with the V^ group's exponent in it) and its sum (without)
         auto weigh = [&](auto masked) {
-          uint32_t buf[2][16];
-          tmem_ld16(ts, buf[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t(&raw)[16] = buf[c & 1];
-            uint32_t pw[8];
+          for (int w = 0; w < 2; ++w) {
+            uint32_t raw[2][16];
+            tmem_ld16(ts + w * 32, raw[0]);
+            tmem_ld16(ts + w * 32 + 16, raw[1]);
+            const uint32_t m = w ? mw.y : mw.x;
+            const int e = w ? ev.y : ev.x;
+            const float zw = VAR > 0 ? 1.f : zs * exp2i(w ? ek.y : ek.x);
+            const float c0 = kShift - ref + static_cast<float>(e);
+            const uint64_t zw2 = f2_pack(zw, zw), c02 = f2_pack(c0, c0);
+            uint64_t la = 0, lb = 0;  // (0.f, 0.f)
             tmem_ld_wait();
-            tmem_landed(raw);
-            if (c < 3) tmem_ld16(ts + (c + 1) * 16, buf[(c + 1) & 1]);
-            const uint32_t m = (c < 2 ? mw.x : mw.y) >> (16 * (c & 1));
+            tmem_landed(raw[0]);
+            tmem_landed(raw[1]);
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const ulonglong2 v = sv2[c * 4 + i / 2];
+            for (int c = 0; c < 2; ++c) {
+              uint32_t pw[8];
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint32_t* r = raw + (i + x) * 2;
-                const uint64_t z = f2_pack(__uint_as_float(r[0]), __uint_as_float(r[1]));
-                float p, q;
-                f2_unpack(VAR > 0 ? f2_add(z, c02) : f2_fma(z, zf2, c02), p, q);
-                const uint64_t p2 = f2_pack(ex2(p), ex2(q));
-                if (x) lb = f2_add(lb, p2);
-                else la = f2_add(la, p2);
-                uint64_t v2 = x ? v.y : v.x;
-                if constexpr (masked.value) {  // a masked token's scale may be anything
-                  f2_unpack(v2, p, q);
-                  v2 = f2_pack((m >> (2 * (i + x))) & 1 ? p : 0.f,
-                               (m >> (2 * (i + x) + 1)) & 1 ? q : 0.f);
+              for (int i = 0; i < 8; ++i) {
+                float p = __uint_as_float(raw[c][2 * i]), q = __uint_as_float(raw[c][2 * i + 1]);
+                f2_unpack(VAR > 0 ? f2_add(f2_pack(p, q), c02) : f2_fma(f2_pack(p, q), zw2, c02), p,
+                          q);
+                if constexpr (masked.value && VAR == 0) {
+                  const int b = c * 16 + 2 * i;
+                  p = (m >> b) & 1 ? p : __int_as_float(0xff800000);
+                  q = (m >> (b + 1)) & 1 ? q : __int_as_float(0xff800000);
                 }
-                f2_unpack(f2_mul(p2, v2), p, q);
-                pw[i + x] = pack_half2(p, q);
+                p = ex2(p);
+                q = ex2(q);
+                if (i & 1) lb = f2_add(lb, f2_pack(p, q));
+                else la = f2_add(la, f2_pack(p, q));
+                pw[i] = pack_half2(p, q);
               }
+              tmem_st8(ts + (w * 2 + c) * 8, pw);
             }
-            tmem_st8(ts + c * 8, pw);
+            float x, y;
+            f2_unpack(f2_add(la, lb), x, y);
+            l = fmaf(x + y, exp2i(-e), l);
           }
         };
         if (whole) weigh(std::false_type{});
         else weigh(std::true_type{});
-        float x, y;
-        f2_unpack(f2_add(la, lb), x, y);
-        l += x + y;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();

@@ -12,15 +12,20 @@ one sum), of magnitude at most Z = sm_scale * sum_d |q_d k^_d|, and every later
 operation (scale, cap, bias, exponent) rounds a value of at most
 B = Z + |bias| by 2^-22.  Both p and the sum that divides it carry e^dz, hence
 the factor 2.  r collects what is relative to p: 2^-19 for exponent, scale and
-sums in fp32; where P enters the contraction as f16, 2^-11 more (half a step),
-and where q carries channel scales in f16, 2^-11 Z more in dz.
+sums in fp32.
 
-P as f16 also has a floor: a value below 2^-14 is off by up to 2^-25.  The
-kernel keeps 2^(z - ref + 12) * v_scale there, ref <= max z + e, 2^e twice the
-largest V scale the row sees at most, so the sum it divides by is at least
-2^(12 - e) >= 2^11 / vs_max.  Every visible token adds at most
-2^-25 |code_jd| * vs_max / 2^11, W = 2^-36 vs_max sum_j |code_jd| in all (times
-the channel's scale where scales are static).
+The prefill (`half`) adds f16 roundings of half a step, 2^-11: of P (r), of V^
+(r, where scales are per token or segment), and of K^ or of q with static channel
+scales in it (2^-11 Z in dz; MX scales are exact).  Below f16's normal range
+(2^-14) a rounding is off by up to 2^-25 instead:
+ - K^ holds code * ks / 2^e with 2^e at most twice the largest ks of its group:
+   sm_scale * sum_d |q_d| * 2^-24 ks_max more in dz (F);
+ - V^ likewise: 2^-24 vs_max more in the output;
+ - P = 2^(z - ref + 12 + e), ref <= max z + e_max, so the sum it is divided by is
+   at least 2^(12 - e_max) >= 2^11 / vs_max, and every visible token adds at most
+   2^-25 |code_jd| vs_max / 2^11: 2^-36 vs_max sum_j |code_jd| in all (times the
+   channel's scale where scales are static).
+W is the sum of the last two; vs_max and ks_max are taken over the request.
 
 A cap of at most 64 may take tanh as 1 - 2 / (e^2x + 1), whose quotient is good to
 2^-21: 2^-20 cap more in dz.
@@ -169,7 +174,7 @@ def attention_row(q, k, v, pos, prefix, sm, window=0, cap=0.0, slope=0.0):
 def attention_ref(q, rows, chunk_of, lens, bt, values, hkv, sm, bs, window=0, prefix=None,
                   cap=0.0, slopes=None):
     """Reference rows: q [n, hq, d]; row i belongs to request rows[i] at position
-    chunk_of[i].  Returns out, A, Z, B as numpy [n, hq, d] / [n, hq, 1], and no W."""
+    chunk_of[i].  Returns out, A, Z, B as numpy [n, hq, d] / [n, hq, 1], and no W and F."""
     kd, vd = values
     n, hq, d = q.shape
     g = hq // hkv
@@ -190,7 +195,7 @@ def attention_ref(q, rows, chunk_of, lens, bt, values, hkv, sm, bs, window=0, pr
             o, a, z, bm = attention_row(q[i, h], k[h // g], v[h // g], int(chunk_of[i]), pre, sm,
                                         window, cap, 0.0 if slopes is None else float(slopes[h]))
             out[i, h], A[i, h], Z[i, h], Bm[i, h] = o.numpy(), a.numpy(), z, bm
-    return out, A, Z, Bm, 0.0
+    return out, A, Z, Bm, 0.0, 0.0
 
 
 def half_step_bf16(x):
@@ -198,18 +203,21 @@ def half_step_bf16(x):
     return np.exp2(e - 8)
 
 
-def check(got, ref, d, bf16=False, f16_p=False, f16_q=False, cap=0.0, what=""):
-    """Hold `got` to the bound at the head of this file."""
-    want, A, Z, B, W = ref
+def check(got, ref, d, bf16=False, half=None, cap=0.0, what=""):
+    """Hold `got` to the bound at the head of this file; half: the scale mode of a
+    prefill (None: a decode)."""
+    want, A, Z, B, W, Fl = ref
     got = got.double().cpu().numpy()
     assert got.shape == want.shape, (got.shape, want.shape)
     assert np.isfinite(got).all(), f"{what}: not finite"
-    dz = (d / 16 + 4) * 2.0 ** -22 * Z + 4 * 2.0 ** -22 * B + (2.0 ** -11 * Z if f16_q else 0.0)
+    dz = (d / 16 + 4) * 2.0 ** -22 * Z + 4 * 2.0 ** -22 * B
+    r = 2.0 ** -19
     if cap <= 64:
         dz = dz + 2.0 ** -20 * cap
-    bound = A * (2 * dz + 2.0 ** -19 + (2.0 ** -11 if f16_p else 0.0)) + 1e-30
-    if f16_p:
-        bound = bound + W
+    if half is not None:
+        dz = dz + (2.0 ** -11 * Z if half != MX else 0.0) + Fl
+        r += 2.0 ** -11 * (2 if half in (TOKEN_HEAD, SEGMENT) else 1)
+    bound = A * (2 * dz + r) + 1e-30 + (W if half is not None else 0.0)
     if bf16:
         bound = bound + half_step_bf16(np.abs(want) + bound)
     over = np.abs(got - want) / bound
@@ -222,21 +230,21 @@ def chunk_ref(q, offsets, lens, bt, values, hkv, sm, bs, window=0, prefix=None, 
               slopes=None, device="cpu"):
     """attention_ref for ragged chunks: request b's queries are rows offsets[b] ..
     offsets[b + 1] - 1, the last one at position lens[b] - 1.  values: K, V, and
-    V's code values (channel scales in) and token scales (for W)."""
-    kd, vd, vcode, vscale = (x.to(device) for x in values)
+    V's code values (channel scales in), and both token scales (for W and F)."""
+    kd, vd, vcode, vscale, kscale = (x.to(device) for x in values)
     n, hq, d = q.shape
     g = hq // hkv
     q = q.double().to(device)
     out = torch.zeros(n, hq, d, dtype=torch.float64, device=device)
     A, Z, Bm = torch.zeros_like(out), torch.zeros_like(out[..., :1]), torch.zeros_like(out[..., :1])
-    W = torch.zeros_like(out)
+    W, Fl = torch.zeros_like(out), torch.zeros_like(Z)
     for b in range(len(lens)):
         lo, hi, L = int(offsets[b]), int(offsets[b + 1]), int(lens[b])
         if hi <= lo or L == 0:
             continue
         blk = bt[b, :(L + bs - 1) // bs].long().to(device)
-        k, v, vcd, vsc = (x[blk].permute(1, 0, 2, 3).flatten(1, 2)[:, :L]
-                          for x in (kd, vd, vcode, vscale))
+        k, v, vcd, vsc, ksc = (x[blk].permute(1, 0, 2, 3).flatten(1, 2)[:, :L]
+                               for x in (kd, vd, vcode, vscale, kscale))
         pos = torch.arange(L - (hi - lo), L, device=device)[:, None]
         j = torch.arange(L, device=device)[None]
         see = j <= pos
@@ -258,9 +266,11 @@ def chunk_ref(q, offsets, lens, bt, values, hkv, sm, bs, window=0, prefix=None, 
             A[lo:hi, h] = p @ v[h // g].abs()
             Z[lo:hi, h, 0] = torch.where(see, zabs, 0.0).amax(1)
             Bm[lo:hi, h, 0] = Z[lo:hi, h, 0] + torch.where(near, bias.abs(), 0.0).amax(1)
-            top = torch.where(see, vsc[h // g, :, 0], 0.0).amax(1, keepdim=True)
-            W[lo:hi, h] = 2.0 ** -36 * top * (see.double() @ vcd[h // g].abs())
-    return tuple(x.cpu().numpy() for x in (out, A, Z, Bm, W))
+            top = float(vsc[h // g].max())
+            W[lo:hi, h] = top * (2.0 ** -36 * (see.double() @ vcd[h // g].abs()) + 2.0 ** -24)
+            Fl[lo:hi, h, 0] = abs(sm) * q[lo:hi, h].abs().sum(1) * 2.0 ** -24 * float(
+                ksc[h // g].max())
+    return tuple(x.cpu().numpy() for x in (out, A, Z, Bm, W, Fl))
 
 
 def chunk_values(cache, fmt, mode, gs):
@@ -269,11 +279,16 @@ def chunk_values(cache, fmt, mode, gs):
     x = decode_codes(vc, fmt)
     nb, h, bs, d = x.shape
     if mode == STATIC:
-        x, s = x * vs.double().view(1, h, 1, d), torch.ones(nb, h, bs, 1)
-    elif mode == SEGMENT:
-        s = vs[:, :h].view(nb, h, 1, 1).expand(nb, h, bs, 1)
-    elif mode == MX:
-        s = torch.exp2(vs.view(nb, h, bs, d // gs).double().amax(-1, keepdim=True) - 127.0)
-    else:
-        s = vs.view(nb, h, bs, 1)
-    return dequant(kc, ks, fmt, mode, gs), dequant(vc, vs, fmt, mode, gs), x, s.double()
+        x = x * vs.double().view(1, h, 1, d)
+
+    def per_token(s):
+        if mode == STATIC:
+            return torch.ones(nb, h, bs, 1, dtype=torch.float64, device=x.device)
+        if mode == SEGMENT:
+            return s[:, :h].double().view(nb, h, 1, 1).expand(nb, h, bs, 1)
+        if mode == MX:
+            return torch.exp2(s.view(nb, h, bs, d // gs).double().amax(-1, keepdim=True) - 127.0)
+        return s.double().view(nb, h, bs, 1)
+
+    return (dequant(kc, ks, fmt, mode, gs), dequant(vc, vs, fmt, mode, gs), x, per_token(vs),
+            per_token(ks))

@@ -57,9 +57,8 @@ class Batch:
         ref = self.ref(**mods)
         for dt in (torch.float32, torch.bfloat16):
             got = self.run(F, out_dtype=dt, **mods)
-            R.check(got, ref, self.d, bf16=dt == torch.bfloat16, f16_p=True,
-                    f16_q=self.form["scale_mode"] == R.STATIC,
-                    cap=mods.get("cap", 0.0), what=f"{what} {dt}")
+            R.check(got, ref, self.d, bf16=dt == torch.bfloat16,
+                    half=self.form["scale_mode"], cap=mods.get("cap", 0.0), what=f"{what} {dt}")
         assert F.get_device_error() == 0
         return got
 
@@ -121,8 +120,8 @@ def test_long_contexts(F, kw):
     b = Batch([4100, 1337], [300, 1337], 8, 1, 128, 16, R.E4M3, R.TOKEN_HEAD, seed=7)
     ref = b.ref(device=DEV, **kw)
     cap = kw.get("cap", 0.0)
-    R.check(b.run(F, **kw), ref, 128, f16_p=True, cap=cap)
-    R.check(b.run(F, out_dtype=torch.bfloat16, **kw), ref, 128, bf16=True, f16_p=True, cap=cap)
+    R.check(b.run(F, **kw), ref, 128, half=R.TOKEN_HEAD, cap=cap)
+    R.check(b.run(F, out_dtype=torch.bfloat16, **kw), ref, 128, bf16=True, half=R.TOKEN_HEAD, cap=cap)
 
 
 def test_requests_without_queries_or_tokens(F):
@@ -140,7 +139,7 @@ def test_rows_outside_the_chunks_are_left_alone(F):
         out = torch.full((56, 4, 128), 77.0, dtype=dt, device=DEV)
         assert b.run(F, out=out, out_dtype=dt) is out
         assert (out[:4] == 77).all() and (out[51:] == 77).all()
-        R.check(out[4:51], ref, 128, bf16=dt == torch.bfloat16, f16_p=True)
+        R.check(out[4:51], ref, 128, bf16=dt == torch.bfloat16, half=R.TOKEN_HEAD)
 
 
 @pytest.mark.parametrize("fmt,nan", [(R.E4M3, 0x7F), (R.E5M2, 0x7E), (R.E5M2, 0x7C)])
@@ -167,7 +166,7 @@ def test_what_masked_tokens_hold_does_not_matter(F, fmt, nan, bad_scale):
                 sc[blk, :, j % 16] = bad_scale
     got = b.run(F, **mods)
     keep = [i for i in range(int(b.offsets[-1])) if i not in last]
-    R.check(got[keep], tuple(x[keep] for x in ref), 128, f16_p=True)
+    R.check(got[keep], tuple(x[keep] for x in ref), 128, half=R.TOKEN_HEAD)
 
 
 def test_pages_no_query_sees_are_not_read(F):
@@ -176,7 +175,7 @@ def test_pages_no_query_sees_are_not_read(F):
     ref = b.ref(**mods)
     b.bt[0, 2:(400 - 30 - 33) // 16] = -1
     b.bt[1, :(200 - 8 - 33) // 16] = 10 ** 6
-    R.check(b.run(F, **mods), ref, 64, f16_p=True)
+    R.check(b.run(F, **mods), ref, 64, half=R.TOKEN_HEAD)
     assert F.get_device_error() == 0
 
 
@@ -194,7 +193,7 @@ def test_bad_blocks_lengths_and_offsets_are_flagged(F):
     b.lens[0] = 2
     got = b.run(F)
     assert not got[:2].any() and got[2:].any()
-    R.check(got[4:], tuple(x[4:] for x in ref), 64, f16_p=True)
+    R.check(got[4:], tuple(x[4:] for x in ref), 64, half=R.TOKEN_HEAD)
     assert F.get_device_error() == N.DEVERR_SEQ_LEN
     for bad in ([0, 9, 6], [-1, 4, 6], [0, 4, 7]):
         b = Batch([4, 20], [4, 2], 4, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=12)
@@ -247,7 +246,7 @@ def test_offsets_past_32_bits(F):
         args[i] = w
     args[6] = torch.where(args[6] >= 0, args[6] + nb - b.cache[0].shape[0], -1).int()
     got = F.paged_prefill_attention(*args, out_dtype=torch.float32, **b.form)
-    R.check(got, ref, d, f16_p=True)
+    R.check(got, ref, d, half=R.TOKEN_HEAD)
 
 
 def test_the_operators_in_a_row(F):
@@ -296,7 +295,7 @@ def test_the_operators_in_a_row(F):
         values = tuple(x.cpu() for x in R.chunk_values((kc, vc, ks, vs), fmt, R.TOKEN_HEAD, 0))
         ref = R.chunk_ref(q.cpu(), off, lens, bt, values, hkv, d ** -0.5, bs, prefix=prefix,
                           **mods)
-        R.check(got, ref, d, f16_p=not decode, cap=mods["cap"])
+        R.check(got, ref, d, half=None if decode else R.TOKEN_HEAD, cap=mods["cap"])
         # the queries and the newest keys really are turned
         want = R.rotate(qkv[:, :hq * d].cpu().unflatten(1, (hq, d)), cs[pos][:, :half],
                         cs[pos][:, half:]).bfloat16()
