@@ -21,10 +21,13 @@
 //
 // Numerics.  The converters give K^ and V^ as f16: a code times its token's scale
 // relative to the largest of its 32 tokens (a power of two 2^e that stays
-// outside), rounded once (2^-11; exact for MX blocks and static scales).  Scaling
+// outside), rounded once (2^-11; exact for MX blocks and static scales).  The
+// largest is put as high as f16 allows, so that a token whose scale is 2^r below
+// it (which some rows may mask) is off by no more than 2^(r - 32) beside that
+// rounding; E5M2's codes fill f16's exponents by themselves: 2^(r - 25).  Scaling
 // the fp32 scores and P instead would keep the scales exact, but costs every
 // score two multiplications and two broadcast loads beside MMAs that fill the
-// shared-memory bandwidth: 1.45 ms against 0.9 ms for 2048 queries over 16384
+// shared-memory bandwidth: 1.45 ms against 1.30 ms for 2048 queries over 16384
 // tokens.  q is exact in f16 after a power-of-two normaliser per row
 // (CHANNEL_STATIC folds the K scales into it and rounds once, 2^-11).  P enters
 // the second product as f16 (2^-11).  The running reference of a row is a bound
@@ -293,6 +296,7 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
                                               uint8_t* sm, int* abort_flag, int it, int u, int u1,
                                               int first, int lane) {
   using SM = Smem<D>;
+  constexpr int kRoom = FMT == FP8PA_E5M2 ? 0 : 7;  // codes of at most 448 leave f16 this much
   constexpr int H = D / 64;  // 16-byte chunks of a row per lane
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
   StageInfo* infos = reinterpret_cast<StageInfo*>(sm + SM::kInfo);
@@ -459,14 +463,14 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
                                       ((g >> 1) - 1) & 1, abort_flag, a.err)))
       return;
     const uint32_t valid = __ballot_sync(0xffffffffu, sok);
-    // the exponent above the group's largest (finite) scale, and the scales
-    // relative to it
+    // the group's exponent, kRoom below the one above its largest (finite) scale,
+    // and the scales relative to it
     const bool finite = sc <= FLT_MAX;  // (not for a NaN)
     int e;
     if constexpr (MX) {
-      e = max(__reduce_max_sync(0xffffffffu, em) - 127, -100);
+      e = max(__reduce_max_sync(0xffffffffu, em) - 127, -100) - kRoom;
     } else {
-      e = min(max(exp_above(warp_max_f32(sok && finite ? sc : 0.f)), -100), 120);
+      e = min(max(exp_above(warp_max_f32(sok && finite ? sc : 0.f)), -100), 120) - kRoom;
       if (a.mode == FP8PA_SCALE_CHANNEL_STATIC) e = 0;
       sc *= exp2i(-e);
     }
@@ -531,7 +535,7 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
         if constexpr (MX) {
           // the block's power of two relative to the group's largest
           const int be = static_cast<int>((ex[h] >> (8 * x)) & 0xFFu) - 127 - e;
-          const float f = __int_as_float((max(min(be, 0), -126) + 127) << 23);
+          const float f = __int_as_float((max(min(be, kRoom), -126) + 127) << 23);
           const __half2 f2 = __floats2half2_rn(f, f);
           p = scale8(p, f2);
           q = scale8(q, f2);

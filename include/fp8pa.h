@@ -456,6 +456,10 @@ int fp8pa_paged_decode_attention_mod(const void* q, const uint8_t* k_cache,
  *              32 or 64; scale_mode TOKEN_HEAD, CHANNEL_STATIC, MX_BLOCK or
  *              SEGMENT; every code format (MX_BLOCK: FP8).
  * out          [total_q][n_q_heads][head_dim], bf16 or f32.
+ * Precision    codes times scales, and the softmax weights, are rounded to f16
+ *              (2^-11).  Among 32 tokens of one tile, a token whose scale is
+ *              2^r below the largest is off by up to 2^(r - 32) more (E5M2:
+ *              2^(r - 25)), whether or not a row sees the large one.
  * workspace    at least fp8pa_prefill_workspace_bytes(), 16-byte aligned; no
  *              initialisation; calls that share it must be stream-ordered.
  */

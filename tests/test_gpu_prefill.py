@@ -169,6 +169,59 @@ def test_what_masked_tokens_hold_does_not_matter(F, fmt, nan, bad_scale):
     R.check(got[keep], tuple(x[keep] for x in ref), 128, half=R.TOKEN_HEAD)
 
 
+@pytest.mark.parametrize("fmt,mode", [(R.E4M3, R.TOKEN_HEAD), (R.INT8, R.TOKEN_HEAD),
+                                      (R.E4M3, R.MX)])
+def test_a_huge_scale_beside_small_ones(F, fmt, mode):
+    """Tokens whose scales are 2^22 times their neighbours', in every group of 32: rows
+    that mask them keep their precision.
+
+    The bound, with S the largest scale (a request's largest small one, top, times
+    2^22) and rho the smallest over the largest of a group: K^ and V^ are held in units
+    that put S between 2^6 and 2^7, and a scale is split into two f16 halves, off by at
+    most 2^-25: 2^-31 / rho relative to the token (MX scales: exact).  A product below
+    the normal range is off by 2^-25 more: 2^-31 S in V^, and sm sum |q| 2^-31 S in a
+    score.  The term of P is 2^-36 S sum |code|, as ever."""
+    up, win = 22, 4
+    b = Batch([90, 40], [60, 33], 4, 2, 128, 16, fmt, mode, seed=17, qgain=0.01)
+    out, A, Z, B, W, Fl = b.ref(window=win)
+    *_, vscale, kscale = b.values()
+    top = float(max(vscale.max(), kscale.max()))
+    huge = [7, 37, 50, 75]
+    for r in range(2):
+        for j in [j for j in huge if j < b.lens[r]]:
+            for sc in b.cache[2:]:
+                row = sc[int(b.bt[r, j // 16]), :, j % 16]
+                if mode == R.MX:
+                    row += up
+                else:
+                    row *= 2.0 ** up
+    rho = min(float(x[x > 0].min() / x.max()) for x in (vscale, kscale)) * 2.0 ** -up
+    rel = 0.0 if mode == R.MX else 2.0 ** -31 / rho
+    for r in range(2):  # W without its own floor, 2^-24 of the request's largest scale
+        own = vscale[b.bt[r, :(b.lens[r] + 15) // 16].long()].transpose(0, 1).flatten(1, 2)
+        own = own[:, :b.lens[r]].amax((1, 2)).repeat_interleave(2).numpy()[:, None]
+        W[b.offsets[r]:b.offsets[r + 1]] -= 2.0 ** -24 * own
+    W = 2.0 ** up * (W + 2.0 ** -31 * top) + rel * A
+    Fl = 2.0 ** (up - 7) * Fl + rel * Z
+    got = b.run(F, window=win)
+    keep = []
+    for r in range(2):
+        for i in range(b.chunks[r]):
+            pos = b.lens[r] - b.chunks[r] + i
+            if not any(pos - win < j <= pos for j in huge):
+                keep.append(int(b.offsets[r]) + i)
+    R.check(got[keep], tuple(x[keep] for x in (out, A, Z, B, W, Fl)), 128, half=mode)
+    assert F.get_device_error() == 0
+
+
+@pytest.mark.parametrize("sm", [0.0, -0.1, 1e-30])
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+def test_scale_factors_of_zero_and_below(F, sm, cap):
+    b = Batch([70, 20], [30, 20], 4, 2, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=18)
+    b.sm = sm
+    b.check(F, window=9, cap=cap, slopes=slopes_of(4))
+
+
 def test_pages_no_query_sees_are_not_read(F):
     b = Batch([400, 200], [30, 8], 4, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=11)
     mods = dict(window=33, prefix=[18, 0])
