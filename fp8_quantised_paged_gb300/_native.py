@@ -58,7 +58,7 @@ _SIGS = {
                                           _P]),
     "fp8pa_paged_prefill_attention": (_I, [_P, _P, _I] + [_P] * 5 + [_I, _P] + [_I] * 8 +
                                       [_F, _I, _P, _F, _P, _I, _P, _I, _P, ctypes.c_size_t, _P]),
-    "fp8pa_prefill_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
+    "fp8pa_prefill_workspace_bytes": (ctypes.c_size_t, [_I] * 7),
     "fp8pa_get_device_error": (_I, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "fp8pa_selftest_bounded_wait": (_I, [ctypes.c_longlong, _P]),
     "fp8pa_set_decode_workers": (_I, [_I]),

@@ -552,11 +552,13 @@ def paged_decode_attention_mod(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     return out
 
 
-def prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, device=None) -> int:
+def prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
+                            max_blocks_per_seq, device=None) -> int:
     """Workspace bytes of paged_prefill_attention for these sizes."""
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
         nbytes = int(N.lib.fp8pa_prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads,
-                                                         head_dim))
+                                                         head_dim, block_size,
+                                                         max_blocks_per_seq))
     if nbytes == 0:
         raise Fp8paError(N.ERR_UNSUPPORTED, "prefill_workspace_bytes")
     return nbytes
@@ -591,7 +593,7 @@ def paged_prefill_attention(q, q_offsets, k_cache, v_cache, k_scale, v_scale, bl
     with _on(dev):
         if workspace is None:
             workspace = _scratch(int(N.lib.fp8pa_prefill_workspace_bytes(
-                total, B, hq, n_kv_heads, d)), dev, stream)
+                total, B, hq, n_kv_heads, d, bs, max_blocks)), dev, stream)
         else:
             _want(workspace, torch.uint8, "workspace", dev)
         rc = N.lib.fp8pa_paged_prefill_attention(

@@ -372,11 +372,13 @@ int append_prepare(const void* k, const void* v, const int32_t* slot_mapping, in
 }
 
 // The sizes of a prefill call that its workspace depends on.
-int prefill_shape(int total_q, int batch, int hq, int hkv, int d) {
-  if (total_q < 0 || batch < 0 || hq <= 0 || hkv <= 0 || hq % hkv != 0)
+int prefill_shape(int total_q, int batch, int hq, int hkv, int d, int bs, int max_blocks) {
+  if (total_q < 0 || batch < 0 || hq <= 0 || hkv <= 0 || hq % hkv != 0 || bs <= 0 ||
+      max_blocks <= 0)
     return FP8PA_ERR_BAD_SHAPE;
   if (d != 64 && d != 128) return FP8PA_ERR_UNSUPPORTED;
-  if ((static_cast<long long>(total_q) + 256ll * batch) * hq >= (1ll << 31))
+  if ((static_cast<long long>(total_q) + 256ll * batch) * hq >= (1ll << 31) ||
+      static_cast<long long>(bs) * max_blocks >= (1ll << 31))
     return FP8PA_ERR_UNSUPPORTED;
   return FP8PA_OK;
 }
@@ -705,11 +707,14 @@ int fp8pa_paged_decode_attention_mod(const void* q, const uint8_t* k_cache,
 }
 
 size_t fp8pa_prefill_workspace_bytes(int total_q, int batch, int n_q_heads, int n_kv_heads,
-                                     int head_dim) {
-  if (prefill_shape(total_q, batch, n_q_heads, n_kv_heads, head_dim) != FP8PA_OK) return 0;
+                                     int head_dim, int block_size, int max_blocks_per_seq) {
+  if (prefill_shape(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
+                    max_blocks_per_seq) != FP8PA_OK)
+    return 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  return prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, dev);
+  return prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
+                                 max_blocks_per_seq, dev);
 }
 
 int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int total_q,
@@ -724,7 +729,8 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
                                   int out_dtype, void* workspace, size_t workspace_bytes,
                                   void* stream) {
   if (window < 0) return FP8PA_ERR_BAD_SHAPE;
-  int st = prefill_shape(total_q, batch, n_q_heads, n_kv_heads, head_dim);
+  int st = prefill_shape(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
+                         max_blocks_per_seq);
   if (st != FP8PA_OK) return st;
   // formats, scale modes, block sizes and pool sizes as the decode's GQA layout
   st = decode_path(1, 1, n_kv_heads, n_kv_heads, head_dim, head_dim, block_size,
@@ -750,7 +756,8 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
   a.err = device_error_ptr(static_cast<cudaStream_t>(stream), &dev);
   if (!a.err) return FP8PA_ERR_CUDA;
   if (workspace_bytes <
-      prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, dev))
+      prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
+                              max_blocks_per_seq, dev))
     return FP8PA_ERR_WORKSPACE;
   a.q = static_cast<const uint16_t*>(q);
   a.q_offsets = q_offsets;

@@ -206,7 +206,8 @@ struct PrefillArgs {
   void* workspace;
   uint32_t* err;
 };
-size_t prefill_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, int device);
+size_t prefill_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, int bs,
+                               int max_blocks, int device);
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 
 // The tensor-core kernel for a causal chunk over the grouped-query layout:

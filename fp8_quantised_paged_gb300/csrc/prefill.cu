@@ -12,8 +12,22 @@ inline int block_bound(int total_q, int batch, int G) {
   return static_cast<int>((static_cast<long long>(total_q) * G + kRows - 1) / kRows) + batch;
 }
 
-inline size_t plan_layout(char* ws, int total_q, int batch, int G, int d, int ranges,
-                          PlanView* v) {
+// Whether tiles are converted once for all row blocks (ready_kernel) instead of by
+// each: where a request has kReadyBlocks of them or more on average, and the tiles
+// of the block tables' reach fit kReadyBytes.
+constexpr int kReadyBlocks = 6;
+constexpr long long kReadyBytes = 1ll << 30;
+inline int tiles_per_request(int bs, int max_blocks) {
+  return static_cast<int>((static_cast<long long>(bs) * max_blocks + kT - 1) / kT);
+}
+inline bool use_ready(int total_q, int batch, int G, int hkv, int d, int bs, int max_blocks) {
+  const double tiles = static_cast<double>(tiles_per_request(bs, max_blocks)) * batch * hkv;
+  return static_cast<long long>(total_q) * G >= static_cast<long long>(kReadyBlocks) * kRows * batch &&
+         tiles * (4.0 * kT * d) <= static_cast<double>(kReadyBytes);
+}
+
+inline size_t plan_layout(char* ws, int total_q, int batch, int G, int hkv, int d, int bs,
+                          int max_blocks, int ranges, PlanView* v) {
   const int nb = block_bound(total_q, batch, G);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -31,6 +45,13 @@ inline size_t plan_layout(char* ws, int total_q, int batch, int G, int d, int ra
   t.ml = reinterpret_cast<float2*>(take(sizeof(float2) * 2 * ranges * kRows));
   t.o = reinterpret_cast<float*>(take(sizeof(float) * 2 * ranges * kRows * d));
   t.blocks = nb;
+  t.tpr = tiles_per_request(bs, max_blocks);
+  t.tiles = t.info = nullptr;
+  if (use_ready(total_q, batch, G, hkv, d, bs, max_blocks)) {
+    const size_t tiles = static_cast<size_t>(t.tpr) * batch * hkv;
+    t.tiles = reinterpret_cast<uint8_t*>(take(tiles * 4 * kT * d));
+    t.info = reinterpret_cast<uint8_t*>(take(tiles * sizeof(StageInfo)));
+  }
   if (v) *v = t;
   return at;
 }
@@ -207,8 +228,10 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a,
 
 }  // namespace
 
-size_t prefill_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, int device) {
-  return plan_layout(nullptr, total_q, batch, hq / hkv, d, sm_count(device), nullptr);
+size_t prefill_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, int bs,
+                               int max_blocks, int device) {
+  return plan_layout(nullptr, total_q, batch, hq / hkv, hkv, d, bs, max_blocks, sm_count(device),
+                     nullptr);
 }
 
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
@@ -217,13 +240,15 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int ranges = sm_count(dev);
   PlanView pv;
-  plan_layout(static_cast<char*>(a.workspace), a.total_q, a.batch, a.G, a.d, ranges, &pv);
+  plan_layout(static_cast<char*>(a.workspace), a.total_q, a.batch, a.G, a.hkv, a.d, a.bs,
+              a.max_blocks, ranges, &pv);
   const int var = a.cap > 0.f ? 2 : (a.slopes ? 1 : 0);
-  int smem = 0;
   const bool mx = a.mode == FP8PA_SCALE_MX_BLOCK;
-  const PrefillFn fn = a.d == 128 ? pick_prefill_d128(a.fmt, var, mx, &smem)
-                                  : pick_prefill_d64(a.fmt, var, mx, &smem);
-  if ((e = ensure_smem_attr(reinterpret_cast<const void*>(fn), smem)) != cudaSuccess) return e;
+  const bool ready = use_ready(a.total_q, a.batch, a.G, a.hkv, a.d, a.bs, a.max_blocks);
+  const PrefillKernels fn = a.d == 128 ? pick_prefill_d128(a.fmt, var, mx, ready)
+                                       : pick_prefill_d64(a.fmt, var, mx, ready);
+  if ((e = ensure_smem_attr(reinterpret_cast<const void*>(fn.attend), fn.smem)) != cudaSuccess)
+    return e;
 
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -232,13 +257,18 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
+  if (ready) {
+    cfg.gridDim = dim3(static_cast<unsigned>(pv.tpr) * a.batch * a.hkv);
+    cfg.blockDim = dim3(256);
+    if ((e = cudaLaunchKernelEx(&cfg, fn.make, a, pv)) != cudaSuccess) return e;
+  }
   cfg.gridDim = dim3(1);
   cfg.blockDim = dim3(kPlanThreads);
   if ((e = cudaLaunchKernelEx(&cfg, prefill_plan_kernel, a, pv, ranges)) != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(ranges));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  if ((e = cudaLaunchKernelEx(&cfg, fn, a, pv)) != cudaSuccess) return e;
+  cfg.blockDim = dim3(static_cast<unsigned>(fn.threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(fn.smem);
+  if ((e = cudaLaunchKernelEx(&cfg, fn.attend, a, pv)) != cudaSuccess) return e;
   if (ranges < 2) return cudaSuccess;
   cfg.gridDim = dim3(static_cast<unsigned>(ranges - 1), kRows / kMergeRows);
   cfg.blockDim = dim3(256);

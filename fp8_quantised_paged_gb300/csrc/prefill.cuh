@@ -67,23 +67,34 @@ struct PlanView {
   int* item;     // [ranges + 1] the item that holds it
   float2* ml;    // [2 * ranges][kRows] reference and sum of a piece
   float* o;      // [2 * ranges][kRows][d]
+  uint8_t* tiles;  // ready tiles: [batch][KV heads][tpr][K^, V^] in their shared-memory form
+  uint8_t* info;   // ... and the StageInfo of each
   int blocks;    // bound of the row blocks
+  int tpr;       // tiles of a request
 };
 
 using PrefillFn = void (*)(const PrefillArgs, const PlanView);
-// The instance for a format, score variant and MX scales (prefill_d64.cu,
-// prefill_d128.cu), and its shared memory.
-PrefillFn pick_prefill_d64(int fmt, int var, bool mx, int* smem);
-PrefillFn pick_prefill_d128(int fmt, int var, bool mx, int* smem);
+// The instances for a format, MX scales and score variant (prefill_d64.cu,
+// prefill_d128.cu).  ready: the kernel over ready tiles, and the one that makes
+// them.
+struct PrefillKernels {
+  PrefillFn attend, make;
+  int smem, threads;
+};
+PrefillKernels pick_prefill_d64(int fmt, int var, bool mx, bool ready);
+PrefillKernels pick_prefill_d128(int fmt, int var, bool mx, bool ready);
 
 namespace {
 
 constexpr int kRows = 256;   // rows of a block: two tiles of 128
 constexpr int kT = 128;      // tokens per tile
 constexpr int kHalf = 64;    // ... of which a softmax thread has half
-constexpr int kThreads = 768;
 constexpr int kAhead = 3;    // jobs that a converting warp asks L2 for ahead
-constexpr int kConvWarp = 16, kConvWarps = 7, kIssueWarp = 23;
+constexpr int kConvWarp = 16, kConvWarps = 7;  // or a K and a V loader over ready tiles
+template <bool READY>
+constexpr int kIssueWarp = kConvWarp + (READY ? 2 : kConvWarps);
+template <bool READY>
+constexpr int kThreads = (kIssueWarp<READY> + 1) * 32;
 constexpr int kSnap = 4;     // a cut this near an item's edge moves to it
 constexpr float kShift = 12.f;  // P = 2^(z - ref + 12): at most 2^15 with the lazy bound
 constexpr float kTau = 3.f;     // the reference may lag by 2^3
@@ -283,48 +294,232 @@ __device__ __noinline__ Item load_item(const PrefillArgs& a, const PlanView& v, 
 }
 
 // ---------------------------------------------------------------- conversion
-// The work of one converting warp.  A tile has eight jobs, 32 tokens of K or V
-// each (part 0-3: K, 4-7: V), dealt round robin over the converting warps.  A
-// lane holds row r8 of four 8-row groups and, of each, the 16-byte chunks c4
-// (and c4 + 4): loads take 64 contiguous bytes of 8 rows, stores the 8 rows of a
-// core matrix, free of bank conflicts.  A job's codes and scales are loaded as
-// soon as the job before it is stored, its block ids one job earlier; kAhead jobs
-// earlier it is asked for into L2, which is what keeps HBM busy where a chunk
-// has few rows.
+// A job: 32 tokens of K or V of a tile (parts 0-3: K, 4-7: V) and one KV head, by
+// one warp.  A lane holds row r8 of four 8-row groups and, of each, the 16-byte
+// chunks c4 (and c4 + 4): loads take 64 contiguous bytes of 8 rows, stores the 8
+// rows of a core matrix, free of bank conflicts.
+template <int D>
+struct Job {
+  uint4 buf[4][D / 64];  // the lane's codes
+  uint32_t okm;          // groups whose row is wanted and exists
+  float sc;              // scale of token `lane`
+  bool sok;              // ... which is wanted and exists
+  uint32_t ex[D / 64];   // MX: exponents of the lane's chunks, by group
+  int em;                // ... and of the token's largest block
+};
+// The tokens that some row sees: [lo, hi) and [0, pre).  Others are neither
+// looked up nor read.
+struct Seen {
+  int lo, hi, pre;
+  __device__ __forceinline__ bool operator()(int j) const { return (j < hi && j >= lo) || j < pre; }
+};
+// Block ids of the two 16-token halves of a job at token j (a half lies in one
+// block); -1 where no row sees any of its tokens.
+__device__ __forceinline__ void job_blocks(const int32_t* table, int lgbs, const Seen& seen, int j,
+                                           int (&id)[2]) {
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int t = j + 16 * x;
+    id[x] = (t < seen.hi && t + 16 > seen.lo) || t < seen.pre
+                ? __ldg(table + static_cast<int>(static_cast<uint32_t>(t) >> lgbs))
+                : -1;
+  }
+}
+__device__ __forceinline__ uint32_t cache_row(const PrefillArgs& a, int kvh, int blk, int t) {
+  return (static_cast<uint32_t>(blk) * a.hkv + kvh) * a.bs + (t & (a.bs - 1));
+}
+
+template <int D, bool MX>
+__device__ __forceinline__ void load_job(const PrefillArgs& a, bool V, int kvh, const int (&ids)[2],
+                                         int j, const Seen& seen, int lane, Job<D>& job) {
+  constexpr int H = D / 64;
+  const int r8 = lane & 7, c4 = lane >> 3;
+  const uint8_t* cache = V ? a.v_cache : a.k_cache;
+  const float* gscale = V ? a.v_scale : a.k_scale;
+  job.okm = 0;
+  const int nbx = MX ? D / a.gs : 0;
+  // code rows of the two halves' first tokens
+  const bool blk_ok[2] = {ids[0] >= 0 && ids[0] < a.num_blocks,
+                          ids[1] >= 0 && ids[1] < a.num_blocks};
+  const uint32_t row[2] = {blk_ok[0] ? cache_row(a, kvh, ids[0], j) : 0u,
+                           blk_ok[1] ? cache_row(a, kvh, ids[1], j + 16) : 0u};
+  const uint32_t lane_at = r8 * D + c4 * 16;
+  if (((j >= seen.lo && j + 32 <= seen.hi) || j + 32 <= seen.pre) && blk_ok[0] && blk_ok[1]) {
+    job.okm = 0xFu;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const uint8_t* src =
+          cache + static_cast<size_t>(row[x >> 1]) * D + lane_at + (x & 1) * 8 * D;
+#pragma unroll
+      for (int h = 0; h < H; ++h) job.buf[x][h] = ld_codes(src + h * 64);
+    }
+  } else {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const bool ok = seen(j + x * 8 + r8) && blk_ok[x >> 1];
+      if (ok) job.okm |= 1u << x;
+      const uint8_t* src =
+          cache + static_cast<size_t>(row[x >> 1]) * D + lane_at + (x & 1) * 8 * D;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        job.buf[x][h] = make_uint4(0u, 0u, 0u, 0u);
+        if (ok) job.buf[x][h] = ld_codes(src + h * 64);
+      }
+    }
+  }
+  job.sc = 1.f;
+  job.em = 0;
+  {
+    const bool want = seen(j + lane);
+    job.sok = want && (lane < 16 ? blk_ok[0] : blk_ok[1]);
+    if (want && !job.sok) raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
+    const size_t rw = (lane < 16 ? row[0] : row[1]) + (lane & 15);
+    if (a.mode == FP8PA_SCALE_TOKEN_HEAD) {
+      if (job.sok) job.sc = __ldg(gscale + rw);
+    } else if (a.mode == FP8PA_SCALE_SEGMENT) {
+      if (job.sok) job.sc = __ldg(gscale + static_cast<long>(lane < 16 ? ids[0] : ids[1]) * a.hp + kvh);
+    } else if constexpr (MX) {
+      // 2, 4 or 8 bytes a row (a missing block's rows read as block 0's: not
+      // used)
+      const uint8_t* exps = reinterpret_cast<const uint8_t*>(gscale);
+      uint32_t w[2];
+      w[1] = nbx == 8 ? __ldg(reinterpret_cast<const uint32_t*>(exps + rw * 8) + 1) : 0u;
+      w[0] = nbx == 2 ? __ldg(reinterpret_cast<const uint16_t*>(exps + rw * 2))
+                      : __ldg(reinterpret_cast<const uint32_t*>(exps + rw * nbx));
+      job.em = job.sok ? static_cast<int>(max_byte(w)) : 0;
+      // the lane's rows' blocks from the lanes that hold them
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const int b = (h * 4 + c4) * 16 / a.gs;
+        job.ex[h] = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t lo4 = __shfl_sync(0xffffffffu, w[0], x * 8 + r8);
+          const uint32_t hi4 = __shfl_sync(0xffffffffu, w[1], x * 8 + r8);
+          job.ex[h] |= (((b & 4 ? hi4 : lo4) >> (8 * (b & 3))) & 0xFFu) << (8 * x);
+        }
+      }
+    }
+  }
+}
+
+// The job's part of a 128-token tile of f16, and of its info.  whole: every row
+// sees the whole tile.
+template <int D, int FMT, bool MX>
+__device__ __forceinline__ void finish_job(const PrefillArgs& a, Job<D>& job, bool V, int dw,
+                                           bool whole, uint8_t* tile, StageInfo* info, int lane) {
+  constexpr int H = D / 64;
+  constexpr int kRoom = FMT == FP8PA_E5M2 ? 0 : 7;  // codes of at most 448 leave f16 this much
+  const int r8 = lane & 7, c4 = lane >> 3;
+  const uint32_t valid = __ballot_sync(0xffffffffu, job.sok);
+  // the group's exponent, kRoom below the one above its largest (finite) scale,
+  // and the scales relative to it
+  const bool finite = job.sc <= FLT_MAX;  // (not for a NaN)
+  int e;
+  if constexpr (MX) {
+    e = max(__reduce_max_sync(0xffffffffu, job.em) - 127, -100) - kRoom;
+  } else {
+    e = min(max(exp_above(warp_max_f32(job.sok && finite ? job.sc : 0.f)), -100), 120) - kRoom;
+    if (a.mode == FP8PA_SCALE_CHANNEL_STATIC) e = 0;
+    job.sc *= exp2i(-e);
+  }
+  // Groups to keep; the others become zero.  In a tile that some row does
+  // not see whole, a V that is not finite would reach rows that mask its token
+  // (0 * NaN): it is zeroed and its token marked, for the rows that do see it.
+  uint32_t keep = job.okm, bad = 0;
+  if (V && !whole) {
+    uint32_t nf = 0;  // bit x: this lane's chunks of group x
+    if constexpr (FMT != FP8PA_INT8) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        bool f = false;
+#pragma unroll
+        for (int h = 0; h < H; ++h) f = f || codes_nonfinite<FMT>(job.buf[x][h]);
+        nf |= f ? 1u << x : 0u;
+      }
+      nf |= __shfl_xor_sync(0xffffffffu, nf, 8);
+      nf |= __shfl_xor_sync(0xffffffffu, nf, 16);
+    }
+    const uint32_t nfs = __ballot_sync(0xffffffffu, job.sok && !finite);  // by token
+#pragma unroll
+    for (int x = 0; x < 4; ++x) nf |= ((nfs >> (x * 8 + r8)) & 1u) << x;
+    nf &= job.okm;
+    keep &= ~nf;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)  // lanes 0-7 hold the rows in order
+      bad |= (__ballot_sync(0xffffffffu, (nf >> x) & 1u) & 0xFFu) << (8 * x);
+  }
+  if (lane == 0) {
+    if (V) {
+      info->ev[dw] = e;
+      info->bad[dw] = bad;
+    } else {
+      info->ek[dw] = e;
+      info->valid[dw] = valid;
+    }
+  }
+  // K: core matrices (8 tokens x 8 dims) 128 bytes apart along the tokens,
+  // 2048 along the dims; V: D * 16 along the tokens, 128 along the dims
+  uint8_t* dst =
+      tile + r8 * 16 + (V ? dw * (D * 64) + c4 * 256 : dw * 512 + c4 * 4096);
+  const int kG = V ? D * 16 : 128, kC = V ? 4 * 256 : 4 * 4096, kH = V ? 128 : 2048;
+  auto store = [&](int x, int h, const uint4& p, const uint4& q) {
+    *reinterpret_cast<uint4*>(dst + x * kG + h * kC) = p;
+    *reinterpret_cast<uint4*>(dst + x * kG + h * kC + kH) = q;
+  };
+  const bool plain = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    __half2 hi, lo;
+    if constexpr (!MX) {
+      const float f = __shfl_sync(0xffffffffu, job.sc, x * 8 + r8);
+      const __half fh = __float2half_rn(f);
+      hi = __half2half2(fh);
+      lo = __half2half2(__float2half_rn(f - __half2float(fh)));
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      uint4 p, q;
+      codes16_to_f16<FMT>(job.buf[x][h], p, q);
+      if constexpr (MX) {
+        // the block's power of two relative to the group's largest
+        const int be = static_cast<int>((job.ex[h] >> (8 * x)) & 0xFFu) - 127 - e;
+        const float f = __int_as_float((max(min(be, kRoom), -126) + 127) << 23);
+        const __half2 f2 = __floats2half2_rn(f, f);
+        p = scale8(p, f2);
+        q = scale8(q, f2);
+      } else if (!plain) {
+        p = scale8(p, hi, lo);
+        q = scale8(q, hi, lo);
+      }
+      if (keep != 0xFu && ((keep >> x) & 1) == 0) p = q = make_uint4(0u, 0u, 0u, 0u);
+      store(x, h, p, q);
+    }
+  }
+}
+
+// The work of one converting warp: jobs are dealt round robin over the warps.  A
+// job's codes and scales are loaded as soon as the job before it is stored, its
+// block ids one job earlier; kAhead jobs earlier it is asked for into L2, which
+// is what keeps HBM busy where a chunk has few rows.
 template <int D, int FMT, bool MX>
 __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanView& pv,
                                               uint8_t* sm, int* abort_flag, int it, int u, int u1,
                                               int first, int lane) {
   using SM = Smem<D>;
-  constexpr int kRoom = FMT == FP8PA_E5M2 ? 0 : 7;  // codes of at most 448 leave f16 this much
-  constexpr int H = D / 64;  // 16-byte chunks of a row per lane
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
   StageInfo* infos = reinterpret_cast<StageInfo*>(sm + SM::kInfo);
-  const int r8 = lane & 7, c4 = lane >> 3;
   const int lgbs = 31 - __clz(a.bs);  // block sizes are powers of two
   const int nbx = MX ? D / a.gs : 0;
 
   // the open item: tiles left of it, its block table, the tokens that some row
-  // sees ([lo, hi) and [0, pre); others are neither looked up nor read) and
-  // those that every row sees
-  int np = 0, skip = 0, k = 0, n = 0, kt = 0, kvh = 0, lo = 0, hi = 0, pre = 0, all_lo = 0, all_hi = 0;
+  // sees and those that every row sees
+  int np = 0, skip = 0, k = 0, n = 0, kt = 0, kvh = 0, all_lo = 0, all_hi = 0;
+  Seen seen{0, 0, 0};
   const int32_t* table = nullptr;
   auto token_of = [&](int i) { return (i < np ? i : i + skip) * kT; };
-  auto wanted = [&](int j) { return (j < hi && j >= lo) || j < pre; };
-  // block ids of a job's two 16-token halves (a half lies in one block); -1
-  // where no row sees any of its tokens
   auto load_ids = [&](int i, int part, int (&id)[2]) {
-    const int j = token_of(i) + (part & 3) * 32;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int t = j + 16 * x;
-      id[x] = (t < hi && t + 16 > lo) || t < pre
-                  ? __ldg(table + static_cast<int>(static_cast<uint32_t>(t) >> lgbs))
-                  : -1;
-    }
-  };
-  auto row_of = [&](int blk, int t) {
-    return (static_cast<uint32_t>(blk) * a.hkv + kvh) * a.bs + (t & (a.bs - 1));
+    job_blocks(table, lgbs, seen, token_of(i) + (part & 3) * 32, id);
   };
 
   int ids[2], part = first;  // of this job
@@ -344,87 +539,20 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
       np = im.r.np;
       skip = im.r.skip;
       kvh = im.kvh;
-      pre = im.r.pre;
+      seen.pre = im.r.pre;
       table = a.block_tables + static_cast<long>(im.r.b) * a.max_blocks;
-      lo = a.window > 0 ? max(im.r.pA - a.window + 1, 0) : 0;
-      hi = im.r.pB + 1;
+      seen.lo = a.window > 0 ? max(im.r.pA - a.window + 1, 0) : 0;
+      seen.hi = im.r.pB + 1;
       all_lo = a.window > 0 ? max(im.r.pB - a.window + 1, 0) : 0;
       all_hi = im.r.pA + 1;
     }
     if (!have) load_ids(kt + k, part, ids);
     const bool V = part >= 4;
     const int dw = part & 3;
-    const uint8_t* cache = V ? a.v_cache : a.k_cache;
-    const float* gscale = V ? a.v_scale : a.k_scale;
     const int j0 = token_of(kt + k), j = j0 + dw * 32;
-    const bool whole = (j0 >= all_lo && j0 + kT <= all_hi) || j0 + kT <= pre;
-    uint4 buf[4][H];
-    uint32_t okm = 0;  // groups whose row is wanted and exists
-    // code rows of the two halves' first tokens
-    const bool blk_ok[2] = {ids[0] >= 0 && ids[0] < a.num_blocks,
-                            ids[1] >= 0 && ids[1] < a.num_blocks};
-    const uint32_t row[2] = {blk_ok[0] ? row_of(ids[0], j) : 0u,
-                             blk_ok[1] ? row_of(ids[1], j + 16) : 0u};
-    const uint32_t lane_at = r8 * D + c4 * 16;
-    if (((j >= lo && j + 32 <= hi) || j + 32 <= pre) && blk_ok[0] && blk_ok[1]) {
-      okm = 0xFu;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint8_t* src =
-            cache + static_cast<size_t>(row[x >> 1]) * D + lane_at + (x & 1) * 8 * D;
-#pragma unroll
-        for (int h = 0; h < H; ++h) buf[x][h] = ld_codes(src + h * 64);
-      }
-    } else {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const bool ok = wanted(j + x * 8 + r8) && blk_ok[x >> 1];
-        if (ok) okm |= 1u << x;
-        const uint8_t* src =
-            cache + static_cast<size_t>(row[x >> 1]) * D + lane_at + (x & 1) * 8 * D;
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          buf[x][h] = make_uint4(0u, 0u, 0u, 0u);
-          if (ok) buf[x][h] = ld_codes(src + h * 64);
-        }
-      }
-    }
-    float sc = 1.f;  // scale of token 32 dw + lane
-    bool sok;
-    uint32_t ex[H];  // MX: exponents of the lane's chunks, by group
-    int em = 0;      // ... and of the token's largest block
-    {
-      const bool want = wanted(j + lane);
-      sok = want && (lane < 16 ? blk_ok[0] : blk_ok[1]);
-      if (want && !sok) raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
-      const size_t rw = (lane < 16 ? row[0] : row[1]) + (lane & 15);
-      if (a.mode == FP8PA_SCALE_TOKEN_HEAD) {
-        if (sok) sc = __ldg(gscale + rw);
-      } else if (a.mode == FP8PA_SCALE_SEGMENT) {
-        if (sok) sc = __ldg(gscale + static_cast<long>(lane < 16 ? ids[0] : ids[1]) * a.hp + kvh);
-      } else if constexpr (MX) {
-        // 2, 4 or 8 bytes a row (a missing block's rows read as block 0's: not
-        // used)
-        const uint8_t* exps = reinterpret_cast<const uint8_t*>(gscale);
-        uint32_t w[2];
-        w[1] = nbx == 8 ? __ldg(reinterpret_cast<const uint32_t*>(exps + rw * 8) + 1) : 0u;
-        w[0] = nbx == 2 ? __ldg(reinterpret_cast<const uint16_t*>(exps + rw * 2))
-                        : __ldg(reinterpret_cast<const uint32_t*>(exps + rw * nbx));
-        em = sok ? static_cast<int>(max_byte(w)) : 0;
-        // the lane's rows' blocks from the lanes that hold them
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          const int b = (h * 4 + c4) * 16 / a.gs;
-          ex[h] = 0;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t lo4 = __shfl_sync(0xffffffffu, w[0], x * 8 + r8);
-            const uint32_t hi4 = __shfl_sync(0xffffffffu, w[1], x * 8 + r8);
-            ex[h] |= (((b & 4 ? hi4 : lo4) >> (8 * (b & 3))) & 0xFFu) << (8 * x);
-          }
-        }
-      }
-    }
+    const bool whole = (j0 >= all_lo && j0 + kT <= all_hi) || j0 + kT <= seen.pre;
+    Job<D> job;
+    load_job<D, MX>(a, V, kvh, ids, j, seen, lane, job);
     // ---- the job behind this one
     int nk = k, npart = part + kConvWarps;
     if (npart >= 8) {
@@ -437,7 +565,7 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
     // ---- a job further ahead is asked for into L2 (its block id was loaded one
     // job ago), and the next one's block id; lane x < 2 for half x
     if (pf_blk >= 0 && pf_blk < a.num_blocks) {
-      const size_t row = row_of(pf_blk, pf_t);
+      const size_t row = cache_row(a, kvh, pf_blk, pf_t);
       prefetch_l2((pf_v ? a.v_cache : a.k_cache) + row * D, 16 * D);
       if (a.mode == FP8PA_SCALE_TOKEN_HEAD) prefetch_l2((pf_v ? a.v_scale : a.k_scale) + row, 64);
       else if (MX)
@@ -450,7 +578,7 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
       if (ak < n) {
         pf_v = (ahead & 7) >= 4;
         pf_t = token_of(kt + ak) + (ahead & 3) * 32 + lane * 16;
-        if ((pf_t < hi && pf_t + 16 > lo) || pf_t < pre)
+        if ((pf_t < seen.hi && pf_t + 16 > seen.lo) || pf_t < seen.pre)
           pf_blk = __ldg(table + static_cast<int>(static_cast<uint32_t>(pf_t) >> lgbs));
       }
     }
@@ -462,91 +590,8 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
                               tc_wait(bars + (V ? kBarVFree : kBarKFree) + st,
                                       ((g >> 1) - 1) & 1, abort_flag, a.err)))
       return;
-    const uint32_t valid = __ballot_sync(0xffffffffu, sok);
-    // the group's exponent, kRoom below the one above its largest (finite) scale,
-    // and the scales relative to it
-    const bool finite = sc <= FLT_MAX;  // (not for a NaN)
-    int e;
-    if constexpr (MX) {
-      e = max(__reduce_max_sync(0xffffffffu, em) - 127, -100) - kRoom;
-    } else {
-      e = min(max(exp_above(warp_max_f32(sok && finite ? sc : 0.f)), -100), 120) - kRoom;
-      if (a.mode == FP8PA_SCALE_CHANNEL_STATIC) e = 0;
-      sc *= exp2i(-e);
-    }
-    // Groups to keep; the others become zero.  In a tile that some row does
-    // not see whole, a V that is not finite would reach rows that mask its token
-    // (0 * NaN): it is zeroed and its token marked, for the rows that do see it.
-    uint32_t keep = okm, bad = 0;
-    if (V && !whole) {
-      uint32_t nf = 0;  // bit x: this lane's chunks of group x
-      if constexpr (FMT != FP8PA_INT8) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          bool f = false;
-#pragma unroll
-          for (int h = 0; h < H; ++h) f = f || codes_nonfinite<FMT>(buf[x][h]);
-          nf |= f ? 1u << x : 0u;
-        }
-        nf |= __shfl_xor_sync(0xffffffffu, nf, 8);
-        nf |= __shfl_xor_sync(0xffffffffu, nf, 16);
-      }
-      const uint32_t nfs = __ballot_sync(0xffffffffu, sok && !finite);  // by token
-#pragma unroll
-      for (int x = 0; x < 4; ++x) nf |= ((nfs >> (x * 8 + r8)) & 1u) << x;
-      nf &= okm;
-      keep &= ~nf;
-#pragma unroll
-      for (int x = 0; x < 4; ++x)  // lanes 0-7 hold the rows in order
-        bad |= (__ballot_sync(0xffffffffu, (nf >> x) & 1u) & 0xFFu) << (8 * x);
-    }
-    if (lane == 0) {
-      if (V) {
-        infos[s4].ev[dw] = e;
-        infos[s4].bad[dw] = bad;
-      } else {
-        infos[s4].ek[dw] = e;
-        infos[s4].valid[dw] = valid;
-      }
-    }
-    // K: core matrices (8 tokens x 8 dims) 128 bytes apart along the tokens,
-    // 2048 along the dims; V: D * 16 along the tokens, 128 along the dims
-    uint8_t* dst = sm + (V ? SM::kV : SM::kK) + st * SM::kTile + r8 * 16 +
-                   (V ? dw * (D * 64) + c4 * 256 : dw * 512 + c4 * 4096);
-    const int kG = V ? D * 16 : 128, kC = V ? 4 * 256 : 4 * 4096, kH = V ? 128 : 2048;
-    auto store = [&](int x, int h, const uint4& p, const uint4& q) {
-      *reinterpret_cast<uint4*>(dst + x * kG + h * kC) = p;
-      *reinterpret_cast<uint4*>(dst + x * kG + h * kC + kH) = q;
-    };
-    const bool plain = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      __half2 hi, lo;
-      if constexpr (!MX) {
-        const float f = __shfl_sync(0xffffffffu, sc, x * 8 + r8);
-        const __half fh = __float2half_rn(f);
-        hi = __half2half2(fh);
-        lo = __half2half2(__float2half_rn(f - __half2float(fh)));
-      }
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        uint4 p, q;
-        codes16_to_f16<FMT>(buf[x][h], p, q);
-        if constexpr (MX) {
-          // the block's power of two relative to the group's largest
-          const int be = static_cast<int>((ex[h] >> (8 * x)) & 0xFFu) - 127 - e;
-          const float f = __int_as_float((max(min(be, kRoom), -126) + 127) << 23);
-          const __half2 f2 = __floats2half2_rn(f, f);
-          p = scale8(p, f2);
-          q = scale8(q, f2);
-        } else if (!plain) {
-          p = scale8(p, hi, lo);
-          q = scale8(q, hi, lo);
-        }
-        if (keep != 0xFu && ((keep >> x) & 1) == 0) p = q = make_uint4(0u, 0u, 0u, 0u);
-        store(x, h, p, q);
-      }
-    }
+    finish_job<D, FMT, MX>(a, job, V, dw, whole, sm + (V ? SM::kV : SM::kK) + st * SM::kTile,
+                           infos + s4, lane);
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) {
@@ -559,11 +604,82 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
   }
 }
 
+// ---------------------------------------------------------------- ready tiles
+// A chunk of many row blocks converts each tile once for all of them: one CTA per
+// tile of a request and KV head, one warp per job, writes the tile as it lies in
+// shared memory.  V that is not finite is marked in every tile, as each may be
+// masked for some row.
+template <int D, int FMT, bool MX>
+__global__ void __launch_bounds__(256) ready_kernel(const __grid_constant__ PrefillArgs a,
+                                                    const __grid_constant__ PlanView pv) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int bh = blockIdx.x / pv.tpr, tile = blockIdx.x - bh * pv.tpr;
+  const int b = bh / a.hkv, kvh = bh - b * a.hkv;
+  bool bad_off, bad_len;
+  const Chunk c = load_chunk(a, b, &bad_off, &bad_len);
+  const Seen seen{a.window > 0 ? max(c.L - c.n - a.window + 1, 0) : 0, c.L, c.pre};
+  // the tiles of the request's row blocks (tile 0 for rows that see nothing)
+  if (c.n == 0 || (tile * kT >= seen.pre && (tile < seen.lo / kT || tile * kT >= max(c.L, 1))))
+    return;
+  const int part = threadIdx.x >> 5, lane = threadIdx.x & 31, dw = part & 3;
+  const bool V = part >= 4;
+  const int j = tile * kT + dw * 32;
+  int ids[2];
+  job_blocks(a.block_tables + static_cast<long>(b) * a.max_blocks, 31 - __clz(a.bs), seen, j, ids);
+  Job<D> job;
+  load_job<D, MX>(a, V, kvh, ids, j, seen, lane, job);
+  constexpr int kTile = Smem<D>::kTile;
+  finish_job<D, FMT, MX>(a, job, V, dw, false,
+                         pv.tiles + (static_cast<size_t>(blockIdx.x) * 2 + (V ? 1 : 0)) * kTile,
+                         reinterpret_cast<StageInfo*>(pv.info) + blockIdx.x, lane);
+}
+
+// One thread's work: the K^ tiles of a CTA's range and their infos, or the V^
+// tiles.  Its last copies are waited for, so that none is in flight at its end.
+template <int D>
+__device__ __forceinline__ void load_tiles(const PrefillArgs& a, const PlanView& pv, uint8_t* sm,
+                                           int* abort_flag, int it, int u, int u1, bool V) {
+  using SM = Smem<D>;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
+  uint64_t* full = bars + (V ? kBarVFull : kBarKFull);
+  uint64_t* free = bars + (V ? kBarVFree : kBarKFree);
+  // the tiles were written by ordinary stores, before griddep_wait
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+  uint32_t g = 0;
+  bool ok = true;
+  for (; u < u1 && ok; ++it) {
+    const Item im = load_item(a, pv, it, u, u1);
+    u += im.t1 - im.t0;
+    const size_t base = static_cast<size_t>(im.r.b * a.hkv + im.kvh) * pv.tpr;
+    for (int k = im.t0; k < im.t1; ++k, ++g) {
+      const uint32_t st = g & 1, s4 = g & 3;
+      // (an info's last reader: the softmax of tile g - 4, as in finish_job's order)
+      ok = g < 2 || tc_wait(free + st, ((g >> 1) - 1) & 1, abort_flag, a.err);
+      if (!ok) break;
+      const size_t at = base + (k < im.r.np ? k : k + im.r.skip);
+      if (!V) {
+        mbar_arrive_expect_tx(bars + kBarScale + s4, sizeof(StageInfo));
+        bulk_load(sm + SM::kInfo + s4 * sizeof(StageInfo), pv.info + at * sizeof(StageInfo),
+                  sizeof(StageInfo), bars + kBarScale + s4);
+      }
+      mbar_arrive_expect_tx(full + st, SM::kTile);
+      bulk_load(sm + (V ? SM::kV : SM::kK) + st * SM::kTile,
+                pv.tiles + (at * 2 + (V ? 1 : 0)) * SM::kTile, SM::kTile, full + st);
+    }
+  }
+  for (uint32_t x = g > 4 ? g - 4 : 0; x < g; ++x) {
+    if (!V) (void)mbar_wait_bounded(bars + kBarScale + (x & 3), (x >> 2) & 1, kWaitLimitCycles);
+    if (x + 2 >= g) (void)mbar_wait_bounded(full + (x & 1), (x >> 1) & 1, kWaitLimitCycles);
+  }
+}
+
 // ---------------------------------------------------------------- kernel
 // VAR: 0 no score modifier but the masks, 1 distance bias, 2 capped scores
-// (with or without a bias).  MX: scales are exponents of MX blocks.
-template <int D, int FMT, int VAR, bool MX>
-__global__ void __launch_bounds__(kThreads, 1)
+// (with or without a bias).  MX: scales are exponents of MX blocks.  READY: over
+// ready tiles, whatever the format.
+template <int D, int FMT, int VAR, bool MX, bool READY>
+__global__ void __launch_bounds__(kThreads<READY>, 1)
     prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ PlanView pv) {
   using SM = Smem<D>;
   // used as it stands, so that its accesses stay in the shared space
@@ -580,17 +696,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (u0 >= u1) return;
   const int it0 = pv.item[blockIdx.x];
 
-  if (warp == kIssueWarp) tmem_alloc(&s_tmem, 512);
+  if (warp == kIssueWarp<READY>) tmem_alloc(&s_tmem, 512);
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bars + i, i >= kBarKFree ? 1 : (i >= kBarX ? 2 : (i >= kBarKFull ? 4 : 8)));
+      mbar_init(bars + i, i >= kBarKFree                             ? 1
+                          : i >= kBarX                               ? 2
+                          : READY && i >= kBarScale                  ? 1
+                          : i >= kBarKFull                           ? 4
+                                                                     : 8);
     fence_barrier_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kIssueWarp) tmem_relinquish();
+  if (warp == kIssueWarp<READY>) tmem_relinquish();
   const uint32_t tmem = s_tmem;
   int* abort_flag = &s_abort;
   auto wait = [&](int bar, uint32_t parity) {
@@ -601,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, tc_wait(bars + bar, parity, abort_flag, a.err)) != 0;
   };
 
-  if (warp == kIssueWarp) {
+  if (warp == kIssueWarp<READY>) {
     // ================================================= MMA issuer
     // S_t of tile k + 1 goes where P_t of tile k was: it is issued behind the
     // P V that reads it, and the tensor cores work through one thread's MMAs in
@@ -666,7 +786,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= kConvWarp) {
-    convert_tiles<D, FMT, MX>(a, pv, sm, abort_flag, it0, u0, u1, warp - kConvWarp, lane);
+    if constexpr (READY) {
+      if (lane == 0) load_tiles<D>(a, pv, sm, abort_flag, it0, u0, u1, warp != kConvWarp);
+    } else {
+      convert_tiles<D, FMT, MX>(a, pv, sm, abort_flag, it0, u0, u1, warp - kConvWarp, lane);
+    }
   } else {
     // ================================================= softmax warps
     const int t = warp >> 3, half = (warp >> 2) & 1;  // row tile, and tokens of its tiles
@@ -1022,29 +1146,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- drain and free: no MMA may still be in flight
   __syncwarp();
-  if (warp == kIssueWarp && lane == 0) {
+  if (warp == kIssueWarp<READY> && lane == 0) {
     tc_commit(bars + kBarDrain);
     (void)mbar_wait_bounded(bars + kBarDrain, 0, kWaitLimitCycles);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kIssueWarp) tmem_dealloc(tmem, 512);
+  if (warp == kIssueWarp<READY>) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------- instances
-template <int D, int FMT, bool MX>
+template <int D, int FMT, bool MX, bool READY>
 PrefillFn pick_var(int var) {
-  return var == 0 ? prefill_kernel<D, FMT, 0, MX>
-                  : (var == 1 ? prefill_kernel<D, FMT, 1, MX> : prefill_kernel<D, FMT, 2, MX>);
+  return var == 0 ? prefill_kernel<D, FMT, 0, MX, READY>
+                  : (var == 1 ? prefill_kernel<D, FMT, 1, MX, READY>
+                              : prefill_kernel<D, FMT, 2, MX, READY>);
+}
+template <int D, int FMT, bool MX>
+PrefillKernels pick_mx(int var, bool ready) {
+  // over ready tiles the format no longer matters: one instance for all
+  return {ready ? pick_var<D, FP8PA_E4M3, false, true>(var) : pick_var<D, FMT, MX, false>(var),
+          ready ? ready_kernel<D, FMT, MX> : nullptr, Smem<D>::kBytes, ready ? kThreads<true> : kThreads<false>};
 }
 template <int D>
-PrefillFn pick_fmt(int fmt, int var, bool mx, int* smem) {
-  *smem = Smem<D>::kBytes;
-  if (fmt == FP8PA_INT8) return pick_var<D, FP8PA_INT8, false>(var);
+PrefillKernels pick_fmt(int fmt, int var, bool mx, bool ready) {
+  if (fmt == FP8PA_INT8) return pick_mx<D, FP8PA_INT8, false>(var, ready);
   if (fmt == FP8PA_E4M3)
-    return mx ? pick_var<D, FP8PA_E4M3, true>(var) : pick_var<D, FP8PA_E4M3, false>(var);
-  return mx ? pick_var<D, FP8PA_E5M2, true>(var) : pick_var<D, FP8PA_E5M2, false>(var);
+    return mx ? pick_mx<D, FP8PA_E4M3, true>(var, ready) : pick_mx<D, FP8PA_E4M3, false>(var, ready);
+  return mx ? pick_mx<D, FP8PA_E5M2, true>(var, ready) : pick_mx<D, FP8PA_E5M2, false>(var, ready);
 }
 
 }  // namespace

@@ -3,8 +3,8 @@
 
 namespace fp8pa {
 
-PrefillFn pick_prefill_d128(int fmt, int var, bool mx, int* smem) {
-  return pick_fmt<128>(fmt, var, mx, smem);
+PrefillKernels pick_prefill_d128(int fmt, int var, bool mx, bool ready) {
+  return pick_fmt<128>(fmt, var, mx, ready);
 }
 
 }  // namespace fp8pa

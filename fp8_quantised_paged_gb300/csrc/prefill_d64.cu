@@ -3,8 +3,8 @@
 
 namespace fp8pa {
 
-PrefillFn pick_prefill_d64(int fmt, int var, bool mx, int* smem) {
-  return pick_fmt<64>(fmt, var, mx, smem);
+PrefillKernels pick_prefill_d64(int fmt, int var, bool mx, bool ready) {
+  return pick_fmt<64>(fmt, var, mx, ready);
 }
 
 }  // namespace fp8pa

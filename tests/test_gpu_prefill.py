@@ -87,6 +87,25 @@ def test_all_modifiers_together(F, fmt, mode, gs, d):
     b.check(F, window=40, prefix=[3, 0, 5, 100, 17, 190, 1, 64], cap=3.0, slopes=slopes_of(8))
 
 
+# Heads per KV head that make the chunks below long: rows are queries times heads,
+# and from 1536 rows a request on, tiles are converted once for all row blocks.
+LONG = 96
+
+
+@pytest.mark.parametrize("fmt,mode,gs", KINDS)
+@pytest.mark.parametrize("d,hkv,bs", [(128, 1, 16), (64, 2, 64)])
+@pytest.mark.parametrize("mods", [{}, {"window": 40, "prefix": [3, 0, 150, 300, 1], "cap": 3.0}])
+def test_long_chunks_of_every_format(F, fmt, mode, gs, d, hkv, bs, mods):
+    b = Batch([130, 17, 200, 390, 1], [1, 17, 64, 50, 1], LONG * hkv, hkv, d, bs, fmt, mode, gs,
+              seed=19)
+    if mods:
+        mods = dict(mods, slopes=slopes_of(LONG * hkv))
+    ref = b.ref(device=DEV, **mods)
+    got = b.run(F, **mods)
+    R.check(got, ref, d, half=mode, cap=mods.get("cap", 0.0))
+    assert F.get_device_error() == 0
+
+
 @pytest.mark.parametrize("window", [0, 1, 2, 16, 17, 100, 128, 257, 5000])
 @pytest.mark.parametrize("prefix", [None, 0, 1, 40, 150, 400, -3])
 def test_windows_and_prefixes(F, window, prefix):
@@ -124,8 +143,9 @@ def test_long_contexts(F, kw):
     R.check(b.run(F, out_dtype=torch.bfloat16, **kw), ref, 128, bf16=True, half=R.TOKEN_HEAD, cap=cap)
 
 
-def test_requests_without_queries_or_tokens(F):
-    b = Batch([40, 0, 17, 9, 0], [0, 0, 17, 0, 0], 4, 2, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=8)
+@pytest.mark.parametrize("hq", [4, 2 * 452])
+def test_requests_without_queries_or_tokens(F, hq):
+    b = Batch([40, 0, 17, 9, 0], [0, 0, 17, 0, 0], hq, 2, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=8)
     b.check(F)
 
 
@@ -144,11 +164,12 @@ def test_rows_outside_the_chunks_are_left_alone(F):
 
 @pytest.mark.parametrize("fmt,nan", [(R.E4M3, 0x7F), (R.E5M2, 0x7E), (R.E5M2, 0x7C)])
 @pytest.mark.parametrize("bad_scale", [float("nan"), float("inf"), 1.0])
-def test_what_masked_tokens_hold_does_not_matter(F, fmt, nan, bad_scale):
+@pytest.mark.parametrize("hq", [8, LONG * 2])
+def test_what_masked_tokens_hold_does_not_matter(F, fmt, nan, bad_scale, hq):
     """Past the end of the request, before the window and, for all but the last
     query, after it: what a row does not see may be anything."""
     lens, chunks = [70, 50, 33, 17], [9, 50, 1, 4]
-    b = Batch(lens, chunks, 8, 2, 128, 16, fmt, R.TOKEN_HEAD, seed=10)
+    b = Batch(lens, chunks, hq, 2, 128, 16, fmt, R.TOKEN_HEAD, seed=10)
     mods = dict(window=20, prefix=[5, 0, 2, 0])
     ref = b.ref(**mods)
     kc, vc, ks, vs = b.cache
@@ -222,8 +243,9 @@ def test_scale_factors_of_zero_and_below(F, sm, cap):
     b.check(F, window=9, cap=cap, slopes=slopes_of(4))
 
 
-def test_pages_no_query_sees_are_not_read(F):
-    b = Batch([400, 200], [30, 8], 4, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=11)
+@pytest.mark.parametrize("hq", [4, LONG])
+def test_pages_no_query_sees_are_not_read(F, hq):
+    b = Batch([400, 200], [30, 8], hq, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=11)
     mods = dict(window=33, prefix=[18, 0])
     ref = b.ref(**mods)
     b.bt[0, 2:(400 - 30 - 33) // 16] = -1
@@ -232,16 +254,17 @@ def test_pages_no_query_sees_are_not_read(F):
     assert F.get_device_error() == 0
 
 
-def test_bad_blocks_lengths_and_offsets_are_flagged(F):
+@pytest.mark.parametrize("hq", [4, 1536])
+def test_bad_blocks_lengths_and_offsets_are_flagged(F, hq):
     from fp8_quantised_paged_gb300 import _native as N
-    b = Batch([40, 20, 10], [5, 2, 3], 4, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=12)
+    b = Batch([40, 20, 10], [5, 2, 3], hq, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=12)
     b.bt[0, 1] = 10 ** 6
     b.lens[1], b.lens[2] = 10 ** 7, -4
     got = b.run(F)
     assert torch.isfinite(got[:5]).all() and not got[7:].any()
     assert F.get_device_error() == N.DEVERR_BLOCK_RANGE | N.DEVERR_SEQ_LEN
     # a chunk longer than its request: the rows before position 0 see nothing
-    b = Batch([4, 20], [4, 2], 4, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=12)
+    b = Batch([4, 20], [4, 2], hq, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=12)
     ref = b.ref()
     b.lens[0] = 2
     got = b.run(F)
@@ -249,16 +272,18 @@ def test_bad_blocks_lengths_and_offsets_are_flagged(F):
     R.check(got[4:], tuple(x[4:] for x in ref), 64, half=R.TOKEN_HEAD)
     assert F.get_device_error() == N.DEVERR_SEQ_LEN
     for bad in ([0, 9, 6], [-1, 4, 6], [0, 4, 7]):
-        b = Batch([4, 20], [4, 2], 4, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=12)
+        b = Batch([4, 20], [4, 2], hq, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=12)
         b.offsets = np.array(bad, np.int32)
-        out = torch.full((6, 4, 64), 7.0, device=DEV)
+        out = torch.full((6, hq, 64), 7.0, device=DEV)
         b.run(F, out=out)
         assert F.get_device_error() & N.DEVERR_Q_OFFSETS
 
 
-def test_graphs_that_share_a_workspace_and_other_streams(F):
-    b = Batch([300, 7, 64], [200, 7, 1], 8, 2, 128, 16, R.E4M3, R.TOKEN_HEAD, seed=13)
-    ws = torch.empty(F.prefill_workspace_bytes(208, 3, 8, 2, 128), dtype=torch.uint8, device=DEV)
+@pytest.mark.parametrize("hq", [8, 48])
+def test_graphs_that_share_a_workspace_and_other_streams(F, hq):
+    b = Batch([300, 7, 64], [200, 7, 1], hq, 2, 128, 16, R.E4M3, R.TOKEN_HEAD, seed=13)
+    ws = torch.empty(F.prefill_workspace_bytes(208, 3, hq, 2, 128, 16, b.bt.shape[1]),
+                     dtype=torch.uint8, device=DEV)
     args = b.args()
     kws = [dict(window=50), dict(logit_cap=5.0)]
     run = lambda kw, **o: F.paged_prefill_attention(*args, **b.form, **kw, **o)  # noqa: E731

@@ -93,8 +93,9 @@ def test_prefill_status_codes(lib, want, kw):
 
 
 def test_prefill_workspace_of_refused_sizes_is_zero(lib):
-    for args in ((-1, 1, 8, 2, 128), (5, -1, 8, 2, 128), (5, 1, 7, 2, 128), (5, 1, 8, 0, 128),
-                 (5, 1, 8, 2, 96), (2 ** 29, 1, 8, 2, 128)):
+    for args in ((-1, 1, 8, 2, 128, 16, 4), (5, -1, 8, 2, 128, 16, 4), (5, 1, 7, 2, 128, 16, 4),
+                 (5, 1, 8, 0, 128, 16, 4), (5, 1, 8, 2, 96, 16, 4), (2 ** 29, 1, 8, 2, 128, 16, 4),
+                 (5, 1, 8, 2, 128, 0, 4), (5, 1, 8, 2, 128, 16, 0), (5, 1, 8, 2, 128, 64, 2 ** 25)):
         assert lib.fp8pa_prefill_workspace_bytes(*args) == 0
 
 
