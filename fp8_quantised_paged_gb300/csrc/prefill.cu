@@ -14,8 +14,11 @@ inline int block_bound(int total_q, int batch, int G) {
 
 // Whether tiles are converted once for all row blocks (ready_kernel) instead of by
 // each: where a request has kReadyBlocks of them or more on average, and the tiles
-// of the block tables' reach fit kReadyBytes.
-constexpr int kReadyBlocks = 6;
+// of the block tables' reach fit kReadyBytes.  One request over 16384 tokens, once
+// against by each: 110 and 114 us at 2 row blocks, 116 and 132 at 3, 127 and 149
+// at 4, 151 and 194 at 6; eight over 4096 tokens: 137 and 145 at 2, 173 and 202 at
+// 3, 260 and 348 at 6.
+constexpr int kReadyBlocks = 3;
 constexpr long long kReadyBytes = 1ll << 30;
 inline int tiles_per_request(int bs, int max_blocks) {
   return static_cast<int>((static_cast<long long>(bs) * max_blocks + kT - 1) / kT);

@@ -10,7 +10,8 @@
 // lane per row, and walks the 128-token tiles of its visible context:
 //   S_t = Q_t K^T (A, B in shared memory), P_t = softmax part (TMEM -> registers
 //   -> TMEM), O_t += P_t V (A = P_t in TMEM, B in shared memory).
-// Each K or V code is read and converted once for 256 rows.
+// Each K or V code is read and converted once for 256 rows, or, where a request
+// has many row blocks, once for all of them (ready tiles, below).
 //
 // Work is the flat list of (row block, KV head, token tile) units.  A planner
 // kernel counts the tiles that each row block can see and cuts the list into
@@ -28,19 +29,25 @@
 // the fp32 scores and P instead would keep the scales exact, but costs every
 // score two multiplications and two broadcast loads beside MMAs that fill the
 // shared-memory bandwidth: 1.45 ms against 1.30 ms for 2048 queries over 16384
-// tokens.  q is exact in f16 after a power-of-two normaliser per row
+// tokens (before the ready tiles).  q is exact in f16 after a power-of-two normaliser per row
 // (CHANNEL_STATIC folds the K scales into it and rounds once, 2^-11).  P enters
 // the second product as f16 (2^-11).  The running reference of a row is a bound
 // of max(z + e), e the exponent of the V^ group, so P stays inside f16 whatever
 // the scales; it moves only when passed by 2^kTau, which is exact, as sums and O
 // carry the same reference.
 //
-// Roles (24 warps): 0-7 and 8-15 the softmax of row tiles 0 and 1, two threads
-// per row, each with 64 of a tile's 128 tokens (four warps per scheduler hide
-// one another's waits; the two agree on the row's reference through shared
-// memory); 16-22 convert codes into shared memory, 23 issues the MMAs (one
-// thread).  While the tensor cores work on one row tile, the other's softmax
-// runs.  Every wait is bounded.
+// Roles: warps 0-7 and 8-15 the softmax of row tiles 0 and 1, two threads per
+// row, each with half of a step's tokens (four warps per scheduler hide one
+// another's waits; the two agree on the row's reference through shared memory);
+// then seven warps that convert codes into shared memory, or two that load ready
+// tiles (a thread each); the last issues the MMAs (one thread).  While the tensor
+// cores work on one row tile, the other's softmax runs.  Every wait is bounded.
+//
+// Measured, head_dim 128, 64 heads over 8: 2048 queries over 16384 tokens 904 us,
+// 1.14 PFLOP/s (59% of a large library product's rate); before the ready tiles
+// 1260 us.  Per 128-token tile of 256 rows that is 4200 cycles, 2800 of them with
+// MMAs under way (2048 at their own rate: the shared memory that feeds both
+// operands of S also takes the tiles in), the rest the softmax's own chain.
 #pragma once
 
 #include <float.h>
@@ -88,9 +95,17 @@ namespace {
 
 constexpr int kRows = 256;   // rows of a block: two tiles of 128
 constexpr int kT = 128;      // tokens per tile
-constexpr int kHalf = 64;    // ... of which a softmax thread has half
 constexpr int kAhead = 3;    // jobs that a converting warp asks L2 for ahead
 constexpr int kConvWarp = 16, kConvWarps = 7;  // or a K and a V loader over ready tiles
+// Tokens scored at a time.  Over ready tiles the MMAs are what is waited for, and a
+// step of 64 costs S nearly what one of 128 does (93 cycles against 87 for each 16
+// dims): 2048 queries over 16384 tokens take 1366 us by 64, 933 us by 128.  Without
+// them chunks are short, mostly of one row tile, and two steps of 64 in columns of
+// their own let S of one run beside the softmax of the other: 8 chunks of 64 rows
+// over 32768 tokens take 386 us, 453 us by 128 (with two row tiles, 512 rows over
+// 16384 tokens: 114 and 108 us).
+template <bool READY>
+constexpr int kStep = READY ? 128 : 64;
 template <bool READY>
 constexpr int kIssueWarp = kConvWarp + (READY ? 2 : kConvWarps);
 template <bool READY>
@@ -99,7 +114,6 @@ constexpr int kSnap = 4;     // a cut this near an item's edge moves to it
 constexpr float kShift = 12.f;  // P = 2^(z - ref + 12): at most 2^15 with the lazy bound
 constexpr float kTau = 3.f;     // the reference may lag by 2^3
 constexpr float kNegBig = -1e30f;
-
 
 // A request's chunk and its visible extent.
 struct Chunk {
@@ -175,12 +189,13 @@ struct Smem {
   static constexpr int kMisc = kBars + 320;  // TMEM base, abort flag
   static constexpr int kBytes = kMisc + 16;
 };
-// Barriers and the arrivals that complete a phase.  Q and P: the eight softmax
-// warps of the row tile; scales: the eight conversion jobs of the tile; K and V
-// full: four jobs; X (t * 4 + lane quarter): the two softmax warps of the same
-// rows; the others: a commit of the tensor cores.
-enum { kBarQ = 0, kBarP = 2, kBarScale = 4, kBarKFull = 8, kBarVFull = 10, kBarX = 12,
-       kBarKFree = 20, kBarVFree = 22, kBarS = 24, kBarO = 26, kBarDrain = 28, kNumBars = 29 };
+// Barriers and the arrivals that complete a phase.  Q (by row tile t) and P (t * 2
+// + step): the eight softmax warps of the row tile; scales: the eight conversion
+// jobs of the tile; K and V full: four jobs (over ready tiles, one thread and its
+// bytes for each of these); X (t * 4 + lane quarter): the two softmax warps of the
+// same rows; the others, S and O by t * 2 + step: a commit of the tensor cores.
+enum { kBarQ = 0, kBarP = 2, kBarScale = 6, kBarKFull = 10, kBarVFull = 12, kBarX = 14,
+       kBarKFree = 22, kBarVFree = 24, kBarS = 26, kBarO = 30, kBarDrain = 34, kNumBars = 35 };
 
 // ---------------------------------------------------------------- conversions
 // 16 codes -> 16 f16 (two 16-byte core-matrix rows), exactly.
@@ -234,8 +249,20 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
 // Registers that a tcgen05.ld filled: what uses them stays behind the
 // tcgen05.wait::ld before this.
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[8]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]));
+}
 __device__ __forceinline__ void tmem_landed(uint32_t (&r)[16]) {
   asm volatile(""
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
@@ -684,6 +711,9 @@ __global__ void __launch_bounds__(kThreads<READY>, 1)
   using SM = Smem<D>;
   // used as it stands, so that its accesses stay in the shared space
   extern __shared__ __align__(128) uint8_t sm[];
+  constexpr int kS = kStep<READY>, kSteps = kT / kS;
+  constexpr int kHalf = kS / 2;    // tokens of a step that a softmax thread has,
+  constexpr int kGroups = kHalf / 32;  // in groups of 32
   uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + SM::kMisc);
   int& s_abort = *reinterpret_cast<int*>(sm + SM::kMisc + 4);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
@@ -723,65 +753,69 @@ __global__ void __launch_bounds__(kThreads<READY>, 1)
 
   if (warp == kIssueWarp<READY>) {
     // ================================================= MMA issuer
-    // S_t of tile k + 1 goes where P_t of tile k was: it is issued behind the
-    // P V that reads it, and the tensor cores work through one thread's MMAs in
+    // S_t of a step goes where P_t was, kSteps steps before: it is issued behind
+    // the P V that reads it, and the tensor cores work through one thread's MMAs in
     // the order of their issue.
     if (lane == 0) {
-      const uint32_t idesc_s = tc_idesc(0, 0, 0, 0, 128, kT);  // f16, both K-major
-      const uint32_t idesc_o = tc_idesc(0, 0, 0, 1, 128, D);   // A in TMEM, B MN-major
+      const uint32_t idesc_s = tc_idesc(0, 0, 0, 0, 128, kS);  // f16, both K-major
+      const uint32_t idesc_o = tc_idesc(0, 0, 0, 1, 128, D);      // A in TMEM, B MN-major
       const uint32_t base = smem_u32(sm);
       const uint64_t dq0 = tc_desc(base + SM::kQ, 2048, 128, 0);
       const uint64_t dk0 = tc_desc(base + SM::kK, 2048, 128, 0);
       const uint64_t dv0 = tc_desc(base + SM::kV, D * 16, 128, 0);
       constexpr uint32_t kNext = SM::kTile >> 4;  // the other row tile or stage
-      auto mma_s = [&](int t, uint32_t st) {  // S_t = Q_t K^T
-        const uint64_t dq = dq0 + t * kNext, dk = dk0 + st * kNext;
-        const uint32_t d = tmem + t * kT;
+      auto mma_s = [&](int t, int step, uint32_t st) {  // S_t = Q_t K^T
+        const uint64_t dq = dq0 + t * kNext, dk = dk0 + st * kNext + step * (kS * 16 >> 4);
+        const uint32_t d = tmem + t * kT + step * kS;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           tc_mma_f16(d, dq + k * (4096 >> 4), dk + k * (4096 >> 4), idesc_s, k > 0);
-        tc_commit(bars + kBarS + t);
+        tc_commit(bars + kBarS + t * 2 + step);
       };
-      auto mma_o = [&](int t, uint32_t st, bool first) {  // O_t += P_t V
-        const uint64_t dv = dv0 + st * kNext;
-        const uint32_t d = tmem + 256 + t * 128, p = tmem + t * kT;
+      auto mma_o = [&](int t, int step, uint32_t st, bool first) {  // O_t += P_t V
+        const uint64_t dv = dv0 + st * kNext + step * (kS / 8 * D * 16 >> 4);
+        const uint32_t d = tmem + 256 + t * 128, p = tmem + t * kT + step * kS;
 #pragma unroll
-        for (int k = 0; k < kT / 16; ++k)  // the halves of P start 64 columns apart
-          tc_mma_f16_ts(d, p + (k >> 2) * kHalf + (k & 3) * 8, dv + k * (2 * D * 16 >> 4), idesc_o,
+        for (int k = 0; k < kS / 16; ++k)  // the halves of P start kHalf columns apart
+          tc_mma_f16_ts(d, p + k / (kS / 32) * kHalf + k % (kS / 32) * 8, dv + k * (2 * D * 16 >> 4), idesc_o,
                         !(first && k == 0));
+        tc_commit(bars + kBarO + t * 2 + step);
       };
-      uint32_t g = 0;              // tiles done by this CTA
-      uint32_t nq = 0, np = 0;     // bit t: phase of row tile t's Q and P
+      uint32_t g = 0;           // tiles done by this CTA
+      uint32_t nq = 0, np = 0;  // bit t: phase of row tile t's Q and P
       bool ok = true;
       for (int it = it0, u = u0; u < u1 && ok; ++it) {
         const Item im = load_item(a, pv, it, u, u1);
         const int n = im.t1 - im.t0;
         u += n;
         const int two = im.r.rows > 128 ? 2 : 1;
-        // k = -1 issues the first S of the row tiles, k >= 0 P V of tile k and
-        // S of tile k + 1
-        for (int k = -1; k < n && ok; ++k) {
-          const bool more = k + 1 < n;
-          const uint32_t g1 = g + (k >= 0 ? 1 : 0);  // tile k + 1
-          if (more) ok = wait(kBarKFull + (g1 & 1), (g1 >> 1) & 1);
-          if (k >= 0) ok = ok && wait(kBarVFull + (g & 1), (g >> 1) & 1);
+        ok = wait(kBarKFull + (g & 1), (g >> 1) & 1);
 #pragma unroll 1
-          for (int t = 0; t < two && ok; ++t) {
-            const uint32_t phase = k < 0 ? nq : np;
-            ok = wait((k < 0 ? kBarQ : kBarP) + t, (phase >> t) & 1);
+        for (int t = 0; t < two && ok; ++t) {  // the first tile's scores
+          ok = wait(kBarQ + t, (nq >> t) & 1);
+          if (!ok) break;
+          nq ^= 1u << t;
+          tc_fence_after();
+          for (int step = 0; step < kSteps; ++step) mma_s(t, step, g & 1);
+        }
+        tc_commit(bars + kBarKFree + (g & 1));
+        for (int k = 0; k < n && ok; ++k, ++g) {
+          const bool more = k + 1 < n;
+          ok = wait(kBarVFull + (g & 1), (g >> 1) & 1) &&
+               (!more || wait(kBarKFull + ((g + 1) & 1), ((g + 1) >> 1) & 1));
+#pragma unroll 1
+          for (int x = 0; x < 2 * kSteps && ok; ++x) {
+            const int step = x >> 1, t = x & 1;
+            if (t >= two) continue;
+            ok = wait(kBarP + t * 2 + step, (np >> t) & 1);
             if (!ok) break;
-            if (k < 0) nq ^= 1u << t;
-            else np ^= 1u << t;
+            if (step == kSteps - 1) np ^= 1u << t;
             tc_fence_after();
-            if (k >= 0) {
-              mma_o(t, g & 1, k == 0);
-              if (t + 1 == two) tc_commit(bars + kBarVFree + (g & 1));
-              if (!more) tc_commit(bars + kBarO + t);
-            }
-            if (more) mma_s(t, g1 & 1);
+            mma_o(t, step, g & 1, k == 0 && step == 0);
+            if (more) mma_s(t, step, (g + 1) & 1);
           }
-          if (more) tc_commit(bars + kBarKFree + (g1 & 1));
-          g = g1;
+          tc_commit(bars + kBarVFree + (g & 1));
+          if (more) tc_commit(bars + kBarKFree + ((g + 1) & 1));
         }
       }
     }
@@ -793,7 +827,7 @@ __global__ void __launch_bounds__(kThreads<READY>, 1)
     }
   } else {
     // ================================================= softmax warps
-    const int t = warp >> 3, half = (warp >> 2) & 1;  // row tile, and tokens of its tiles
+    const int t = warp >> 3, half = (warp >> 2) & 1;  // row tile, and half of a step's tokens
     const int rl = (warp & 3) * 32 + lane;            // row within it
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + t * kT + half * kHalf + lanes, to = tmem + 256 + t * 128 + lanes;
@@ -812,7 +846,7 @@ __global__ void __launch_bounds__(kThreads<READY>, 1)
       other = slot[half ? -4 * 32 : 4 * 32];
       return good;
     };
-    uint32_t g = 0, ns = 0, no = 0;  // tiles of the CTA; tiles and items of this row tile
+    uint32_t g = 0, ns = 0;  // tiles of the CTA, and of this row tile
     bool ok = true;
     for (int it = it0, u = u0; u < u1 && ok; ++it) {
       const Item im = load_item(a, pv, it, u, u1);
@@ -902,11 +936,8 @@ __global__ void __launch_bounds__(kThreads<READY>, 1)
           break;
         }
         const int er = static_cast<int>((lane >> 4) == half ? mine : theirs);
-        // log2-domain factor of a raw score (capped scores: of 2 z / cap); never
-        // zero, so that a masked -inf stays -inf
-        zs = fmaxf(fabsf(a.sm_scale) * exp2i(er - 14) * kLog2e *
-                       (VAR == 2 ? 2.f / a.cap : 1.f),
-                   1e-37f);
+        // log2-domain factor of a raw score (capped scores: of 2 z / cap)
+        zs = fabsf(a.sm_scale) * exp2i(er - 14) * kLog2e * (VAR == 2 ? 2.f / a.cap : 1.f);
       }
       const int pos = im.r.L - im.r.n + qi;
       const int wf = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
@@ -917,98 +948,114 @@ __global__ void __launch_bounds__(kThreads<READY>, 1)
       const float cap_log2 = VAR == 2 ? a.cap * kLog2e : 0.f;
       float ref = kNegBig, l = 0.f;
 
-      for (int k = 0; k < n; ++k, ++g) {
+      for (int x = 0; x < kSteps * n; ++x) {
+        const int step = x % kSteps, kt = im.t0 + x / kSteps;
         const uint32_t s4 = g & 3;
-        const int kt = im.t0 + k;
-        const int j0 = (kt < im.r.np ? kt : kt + im.r.skip) * kT + half * kHalf;
-        if (!wait_warp(kBarScale + s4, (g >> 2) & 1) || !wait_warp(kBarS + t, ns & 1)) {
+        const uint32_t sc = ts + step * kS;  // the thread's scores, then P
+        const int j0 = (kt < im.r.np ? kt : kt + im.r.skip) * kT + step * kS + half * kHalf;
+        if (step == 0 && !wait_warp(kBarScale + s4, (g >> 2) & 1)) {
           ok = false;
           break;
         }
-        ++ns;
-        tc_fence_after();
-        const uint2 val = *reinterpret_cast<const uint2*>(&infos[s4].valid[half * 2]);
-        const uint2 bad = *reinterpret_cast<const uint2*>(&infos[s4].bad[half * 2]);
-        const int2 ek = *reinterpret_cast<const int2*>(&infos[s4].ek[half * 2]);
-        const int2 ev = *reinterpret_cast<const int2*>(&infos[s4].ev[half * 2]);
+        // the groups' factors, exponents and the tokens that the row sees
+        const StageInfo& info = infos[s4];
+        const int first = (step * kS + half * kHalf) / 32;
+        float zw[kGroups], ev[kGroups];
+        uint32_t m[kGroups], all = 0xFFFFFFFFu, nan = 0;
+#pragma unroll
+        for (int w = 0; w < kGroups; ++w) {
+          ev[w] = static_cast<float>(info.ev[first + w]);
+          // (VAR 0 multiplies a masked -inf by the factor: not zero)
+          zw[w] = zs * exp2i(info.ek[first + w]);
+          if (VAR == 0) zw[w] = fmaxf(zw[w], 1e-37f);
+          m[w] = info.valid[first + w];
+          all &= m[w];
+        }
         // whether every row of the warp sees all of the thread's tokens
         const bool whole =
             ((j0 >= wB && j0 + kHalf - 1 <= pA) || (VAR == 0 && j0 + kHalf <= pre)) &&
-            (val.x & val.y) == 0xFFFFFFFFu && (VAR < 2 || a.cap <= kCapFast);
-        uint2 mw = make_uint2(0xFFFFFFFFu, 0xFFFFFFFFu);  // tokens that the row sees
-        if (!whole) {
-          mw.x = (word_bits(j0, wf, pos + 1) | word_bits(j0, 0, pre)) & val.x;
-          mw.y = (word_bits(j0 + 32, wf, pos + 1) | word_bits(j0 + 32, 0, pre)) & val.y;
+            all == 0xFFFFFFFFu && (VAR < 2 || a.cap <= kCapFast);
+#pragma unroll
+        for (int w = 0; w < kGroups; ++w) {
+          if (!whole)
+            m[w] &= word_bits(j0 + w * 32, wf, pos + 1) | word_bits(j0 + w * 32, 0, pre);
+          nan |= m[w] & info.bad[first + w];
         }
-        if ((mw.x & bad.x) | (mw.y & bad.y)) l = __int_as_float(0x7FC00000);
-        // ---- a bound of z + e over the row's tokens, 32 scores at a time.  VAR >
-        // 0 puts the final scores back into TMEM.
+        if (nan) l = __int_as_float(0x7FC00000);
+        if (!wait_warp(kBarS + t * 2 + step, ns & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // ---- a bound of z + e over the row's tokens.  The first group's scores stay
+        // in registers (VAR > 0: as final scores), the second's in TMEM.
+        uint32_t raw[2][16];
         float bound = __int_as_float(0xff800000);
-        auto find = [&](auto masked) {
+        auto find = [&](auto masked, int w) {
+          tmem_ld16(sc + w * 32, raw[0]);
+          tmem_ld16(sc + w * 32 + 16, raw[1]);
+          tmem_ld_wait();
+          tmem_landed(raw[0]);
+          tmem_landed(raw[1]);
+          const int jw = j0 + w * 32;
+          float m4[4];
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            uint32_t raw[2][16];
-            tmem_ld16(ts + w * 32, raw[0]);
-            tmem_ld16(ts + w * 32 + 16, raw[1]);
-            const uint32_t m = w ? mw.y : mw.x;
-            const float zw = zs * exp2i(w ? ek.y : ek.x);  // factor of this group's scores
-            const int jw = j0 + w * 32;
-            tmem_ld_wait();
-            tmem_landed(raw[0]);
-            tmem_landed(raw[1]);
-            float m4[4];
+          for (int y = 0; y < 4; ++y) m4[y] = __int_as_float(0xff800000);
+          // the bias of tokens 2 i, 2 i + 1 of the group: -slope (pos - j)
+          // (VAR 2: and the cap, less what the tanh leaves of it)
+          const float b0 = VAR > 0 ? fmaf(slope, static_cast<float>(jw - pos), cap_log2) : 0.f;
+          const uint64_t zw2 = f2_pack(zw[w], zw[w]), bias = f2_pack(b0, b0 + slope);
+          const uint64_t by2 = f2_pack(2.f * slope, 2.f * slope);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) m4[x] = __int_as_float(0xff800000);
-            // the bias of tokens 2 i, 2 i + 1 of the group: -slope (pos - j)
-            const float b0 = VAR > 0 ? slope * static_cast<float>(jw - pos) : 0.f;
-            const uint64_t zw2 = f2_pack(zw, zw), bias = f2_pack(b0, b0 + slope);
-            const uint64_t step = f2_pack(2.f * slope, 2.f * slope);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              uint32_t* r = &raw[i / 8][(i % 8) * 2];
-              float x[2] = {__uint_as_float(r[0]), __uint_as_float(r[1])};
-              if constexpr (VAR > 0) {
-                if constexpr (masked.value) {
-#pragma unroll
-                  for (int y = 0; y < 2; ++y) {
-                    x[y] *= zw;
-                    if constexpr (VAR == 2) x[y] = cap_log2 * tanh_f32(x[y] * (0.5f / kLog2e));
-                    x[y] = fmaf(-slope, fabsf(static_cast<float>(pos - jw - 2 * i - y)), x[y]);
-                  }
-                } else {
-                  const float fi = static_cast<float>(i);
-                  const uint64_t b = f2_fma(step, f2_pack(fi, fi), bias);
-                  uint64_t z = f2_pack(x[0], x[1]);
-                  if constexpr (VAR == 1) {
-                    z = f2_fma(z, zw2, b);
-                  } else {  // cap tanh(z / cap) = cap - 2 cap / (2^x + 1)
-                    f2_unpack(f2_mul(z, zw2), x[0], x[1]);
-                    z = f2_add(f2_pack(cap_fast(x[0], cap_log2), cap_fast(x[1], cap_log2)), b);
-                  }
-                  f2_unpack(z, x[0], x[1]);
-                }
-              }
-              if constexpr (masked.value) {
-                x[0] = (m >> (2 * i)) & 1 ? x[0] : __int_as_float(0xff800000);
-                x[1] = (m >> (2 * i + 1)) & 1 ? x[1] : __int_as_float(0xff800000);
-              }
-              m4[i & 3] = max3(m4[i & 3], x[0], x[1]);
-              if constexpr (VAR > 0) {
-                r[0] = __float_as_uint(x[0]);
-                r[1] = __float_as_uint(x[1]);
-              }
-            }
+          for (int i = 0; i < 16; ++i) {
+            uint32_t* r = &raw[i / 8][(i % 8) * 2];
+            float y[2] = {__uint_as_float(r[0]), __uint_as_float(r[1])};
             if constexpr (VAR > 0) {
-              tmem_st16(ts + w * 32, raw[0]);
-              tmem_st16(ts + w * 32 + 16, raw[1]);
+              if constexpr (masked.value) {
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                  y[v] *= zw[w];
+                  if constexpr (VAR == 2) y[v] = cap_log2 * tanh_f32(y[v] * (0.5f / kLog2e));
+                  y[v] = fmaf(-slope, fabsf(static_cast<float>(pos - jw - 2 * i - v)), y[v]);
+                }
+              } else {
+                const float fi = static_cast<float>(i);
+                const uint64_t b = f2_fma(by2, f2_pack(fi, fi), bias);
+                uint64_t z = f2_pack(y[0], y[1]);
+                if constexpr (VAR == 1) {
+                  z = f2_fma(z, zw2, b);
+                } else {  // cap tanh(z / cap) = cap - 2 cap / (2^x + 1), cap in the bias
+                  f2_unpack(f2_mul(z, zw2), y[0], y[1]);
+                  f2_unpack(f2_add(f2_pack(ex2(y[0]), ex2(y[1])), f2_pack(1.f, 1.f)), y[0], y[1]);
+                  z = f2_fma(f2_pack(rcp_fast(y[0]), rcp_fast(y[1])),
+                             f2_pack(-2.f * cap_log2, -2.f * cap_log2), b);
+                }
+                f2_unpack(z, y[0], y[1]);
+              }
             }
-            const float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-            bound = fmaxf(bound, fmaf(mx, VAR > 0 ? 1.f : zw, static_cast<float>(w ? ev.y : ev.x)));
+            if constexpr (masked.value) {
+              y[0] = (m[w] >> (2 * i)) & 1 ? y[0] : __int_as_float(0xff800000);
+              y[1] = (m[w] >> (2 * i + 1)) & 1 ? y[1] : __int_as_float(0xff800000);
+            }
+            m4[i & 3] = max3(m4[i & 3], y[0], y[1]);
+            if constexpr (VAR > 0 || masked.value) {
+              r[0] = __float_as_uint(y[0]);
+              r[1] = __float_as_uint(y[1]);
+            }
           }
+          if ((VAR > 0 || masked.value) && w > 0) {
+            tmem_st16(sc + w * 32, raw[0]);
+            tmem_st16(sc + w * 32 + 16, raw[1]);
+          }
+          const float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+          bound = fmaxf(bound, fmaf(mx, VAR > 0 ? 1.f : zw[w], ev[w]));
         };
-        if (whole) find(std::false_type{});
-        else find(std::true_type{});
-        if constexpr (VAR > 0) tmem_st_wait();
+#pragma unroll
+        for (int w = kGroups - 1; w >= 0; --w) {
+          if (whole) find(std::false_type{}, w);
+          else find(std::true_type{}, w);
+        }
+        if (kGroups > 1 && (VAR > 0 || !whole)) tmem_st_wait();
         // ---- the reference, shared by the row's two threads: where the bound
         // passed it by 2^kTau it moves, and with it the sums and O
         float other;
@@ -1024,78 +1071,78 @@ __global__ void __launch_bounds__(kThreads<READY>, 1)
         }
         if (__any_sync(0xffffffffu, al != 1.f)) {
           l *= al;
-          if (k > 0) {  // (P V of the last tile is done: S of this one came behind it)
+          if (x > 0) {
+            // behind P V of the step before: in the same columns, S of this step came
+            // after it
+            if (kSteps > 1 && !wait_warp(kBarO + t * 2 + (step ^ 1), (ns - (step ^ 1)) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              const uint32_t at = to + half * (D / 2) + c * 16;
-              uint32_t o[16];
-              tmem_ld16(at, o);
+            for (int c = 0; c < D / 16; ++c) {
+              const uint32_t at = to + half * (D / 2) + c * 8;
+              uint32_t o[8];
+              tmem_ld8(at, o);
               tmem_ld_wait();
               tmem_landed(o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-              tmem_st16(at, o);
+              for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+              tmem_st8(at, o);
             }
           }
         }
         // ---- P (with the V^ group's exponent in it) and its sum (without)
-        auto weigh = [&](auto masked) {
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            uint32_t raw[2][16];
-            tmem_ld16(ts + w * 32, raw[0]);
-            tmem_ld16(ts + w * 32 + 16, raw[1]);
-            const uint32_t m = w ? mw.y : mw.x;
-            const int e = w ? ev.y : ev.x;
-            const float zw = VAR > 0 ? 1.f : zs * exp2i(w ? ek.y : ek.x);
-            const float c0 = kShift - ref + static_cast<float>(e);
-            const uint64_t zw2 = f2_pack(zw, zw), c02 = f2_pack(c0, c0);
-            uint64_t la = 0, lb = 0;  // (0.f, 0.f)
+        for (int w = 0; w < kGroups; ++w) {
+          if (w > 0) {
+            tmem_ld16(sc + w * 32, raw[0]);
+            tmem_ld16(sc + w * 32 + 16, raw[1]);
             tmem_ld_wait();
             tmem_landed(raw[0]);
             tmem_landed(raw[1]);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t pw[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float p = __uint_as_float(raw[c][2 * i]), q = __uint_as_float(raw[c][2 * i + 1]);
-                f2_unpack(VAR > 0 ? f2_add(f2_pack(p, q), c02) : f2_fma(f2_pack(p, q), zw2, c02), p,
-                          q);
-                if constexpr (masked.value && VAR == 0) {
-                  const int b = c * 16 + 2 * i;
-                  p = (m >> b) & 1 ? p : __int_as_float(0xff800000);
-                  q = (m >> (b + 1)) & 1 ? q : __int_as_float(0xff800000);
-                }
-                p = ex2(p);
-                q = ex2(q);
-                if (i & 1) lb = f2_add(lb, f2_pack(p, q));
-                else la = f2_add(la, f2_pack(p, q));
-                pw[i] = pack_half2(p, q);
-              }
-              tmem_st8(ts + (w * 2 + c) * 8, pw);
-            }
-            float x, y;
-            f2_unpack(f2_add(la, lb), x, y);
-            l = fmaf(x + y, exp2i(-e), l);
           }
-        };
-        if (whole) weigh(std::false_type{});
-        else weigh(std::true_type{});
+          const float c0 = kShift - ref + ev[w], f = VAR > 0 ? 1.f : zw[w];
+          const uint64_t f2 = f2_pack(f, f), c02 = f2_pack(c0, c0);
+          uint64_t la = 0, lb = 0;  // (0.f, 0.f)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pw[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint64_t z =
+                  f2_pack(__uint_as_float(raw[c][2 * i]), __uint_as_float(raw[c][2 * i + 1]));
+              float p, q;
+              f2_unpack(VAR > 0 ? f2_add(z, c02) : f2_fma(z, f2, c02), p, q);
+              p = ex2(p);
+              q = ex2(q);
+              if (i & 1) lb = f2_add(lb, f2_pack(p, q));
+              else la = f2_add(la, f2_pack(p, q));
+              pw[i] = pack_half2(p, q);
+            }
+            tmem_st8(sc + (w * 2 + c) * 8, pw);
+          }
+          float y, z;
+          f2_unpack(f2_add(la, lb), y, z);
+          l = fmaf(y + z, ex2(-ev[w]), l);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars + kBarP + t);
+        if (lane == 0) mbar_arrive(bars + kBarP + t * 2 + step);
+        if (step == kSteps - 1) {
+          ++ns;
+          ++g;
+        }
       }
       if (!ok) break;
 
       // ---- the block's result, or this range's piece of it: half the dims each
       float other;
-      if (!trade(l, other) || !wait_warp(kBarO + t, no & 1)) {
+      if (!trade(l, other) || !wait_warp(kBarO + t * 2 + kSteps - 1, (ns - 1) & 1)) {
         ok = false;
         break;
       }
-      ++no;
       l += other;
       tc_fence_after();
       const bool piece = im.t0 > 0 || im.t1 < im.r.count;

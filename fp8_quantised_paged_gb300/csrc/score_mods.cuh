@@ -29,9 +29,15 @@ __device__ __forceinline__ int window_first(const ScoreMods& m, int pos) {
 // 2^-14 here, for two special-function operations and three others.  Larger caps
 // need tanh_f32, good relative to the score.
 constexpr float kCapFast = 64.f;
+// 1 / x, good to 2^-23; 0 for an infinity.
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // cap tanh(z / cap) in the log2 domain, cap_log2 = cap log2(e).
 __device__ __forceinline__ float cap_fast(float x, float cap_log2) {
-  return fmaf(__fdividef(1.f, ex2(x) + 1.f), -2.f * cap_log2, cap_log2);
+  return fmaf(rcp_fast(ex2(x) + 1.f), -2.f * cap_log2, cap_log2);
 }
 
 // tanh x to a relative error of about 2^-21, so that cap * tanh(z / cap) is

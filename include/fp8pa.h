@@ -478,7 +478,7 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
 /*
  * Bytes of device workspace fp8pa_paged_prefill_attention needs for these
  * sizes on the current device; 0 if they are rejected.  Where chunks are long
- * (1536 rows, queries times heads per KV head, of a request on average) it holds
+ * (768 rows, queries times heads per KV head, of a request on average) it holds
  * the block tables' whole reach in f16, up to 1 GiB; beyond that the tiles are
  * converted where they are used.
  */

@@ -88,7 +88,7 @@ def test_all_modifiers_together(F, fmt, mode, gs, d):
 
 
 # Heads per KV head that make the chunks below long: rows are queries times heads,
-# and from 1536 rows a request on, tiles are converted once for all row blocks.
+# and from 768 rows a request on, tiles are converted once for all row blocks.
 LONG = 96
 
 
