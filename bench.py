@@ -212,13 +212,13 @@ def flops_per_step(w: W.Workload) -> int:
     return 2 * int(w.seq_lens.sum()) * w.n_q_heads * (w.head_dim + w.head_dim_v)
 
 
-def kernel_source_sha(name="decode_gqa.cu") -> str:
+def kernel_source_sha(name="gqa_split.cuh") -> str:
     import hashlib
     with open(os.path.join(ROOT, "fp8_quantised_paged_gb300", "csrc", name), "rb") as f:
         return hashlib.sha256(f.read()).hexdigest()
 
 
-def traffic_per_launch(path, workload_name, source="decode_gqa.cu"):
+def traffic_per_launch(path, workload_name, source="gqa_split.cuh"):
     """DRAM bytes per launch of the split kernel from the recorded ncu
     capture, or None when none was recorded for this workload or the
     kernel source changed since."""
@@ -518,7 +518,7 @@ def split_kernel_name(w, q_len: int = 1):
         return "mla_tc_kernel", "decode_mla_tc.cu"
     if chunk_on_tensor_cores(w, q_len):
         return "gqa_tc_kernel", "decode_gqa_tc.cu"
-    return ("mla_split_kernel", "decode_mla.cu") if w.mla else ("gqa_split_kernel", "decode_gqa.cu")
+    return ("mla_split_kernel", "decode_mla.cu") if w.mla else ("gqa_split_kernel", "gqa_split.cuh")
 
 
 def split_roofline(w, acc, split_avg_ms, pk, traffic_json, q_len: int = 1):
