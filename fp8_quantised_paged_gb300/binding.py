@@ -511,6 +511,12 @@ def _decode_need(device_index, *sizes):
     return int(N.lib.fp8pa_decode_workspace_bytes(*sizes))
 
 
+@functools.lru_cache(maxsize=4096)
+def _prefill_need(device_index, *sizes):
+    """Workspace size of a prefill of these sizes (device_index is current)."""
+    return int(N.lib.fp8pa_prefill_workspace_bytes(*sizes))
+
+
 def paged_decode_attention_mod(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
                                n_kv_heads, sm_scale, window=0, prefix_lens=None, logit_cap=0.0,
                                alibi_slopes=None, fmt=E4M3, scale_mode=SCALE_TOKEN_HEAD,
@@ -592,8 +598,8 @@ def paged_prefill_attention(q, q_offsets, k_cache, v_cache, k_scale, v_scale, bl
     out, odt = _output(out, (total, hq, d), out_dtype, dev, stream)
     with _on(dev):
         if workspace is None:
-            workspace = _scratch(int(N.lib.fp8pa_prefill_workspace_bytes(
-                total, B, hq, n_kv_heads, d, bs, max_blocks)), dev, stream)
+            workspace = _scratch(_prefill_need(dev.index, total, B, hq, n_kv_heads, d, bs,
+                                               max_blocks), dev, stream)
         else:
             _want(workspace, torch.uint8, "workspace", dev)
         rc = N.lib.fp8pa_paged_prefill_attention(
