@@ -948,7 +948,12 @@ __global__ void __launch_bounds__(kThreads<READY>, 1)
       const float cap_log2 = VAR == 2 ? a.cap * kLog2e : 0.f;
       float ref = kNegBig, l = 0.f;
 
-      for (int x = 0; x < kSteps * n; ++x) {
+      // An item's first scores are waited for before its first info: a row tile that
+      // sat out the items before may be several phases of that barrier ahead, and a
+      // parity tells only two apart.  Once the issuer is here, every earlier phase is
+      // over, and the one after this waits for this row tile's P.
+      ok = wait_warp(kBarS + t * 2, ns & 1);
+      for (int x = 0; x < kSteps * n && ok; ++x) {
         const int step = x % kSteps, kt = im.t0 + x / kSteps;
         const uint32_t s4 = g & 3;
         const uint32_t sc = ts + step * kS;  // the thread's scores, then P

@@ -20,9 +20,13 @@ def F():
 class Batch:
     """Requests of `lens` cached tokens whose last `chunks` are queries."""
 
-    def __init__(self, lens, chunks, hq, hkv, d, bs, fmt, mode, gs=32, seed=0, qgain=1.0):
+    def __init__(self, lens, chunks, hq, hkv, d, bs, fmt, mode, gs=32, seed=0, qgain=1.0,
+                 reach=0):
         rng = np.random.default_rng(seed)
         self.bt, nb = R.make_tables(rng, lens, bs)
+        more = reach // bs - self.bt.shape[1]
+        if more > 0:
+            self.bt = torch.cat([self.bt, torch.full((len(lens), more), -1, dtype=torch.int32)], 1)
         self.cache = list(R.make_cache(rng, nb, hkv, bs, d, fmt, mode, gs))
         self.lens, self.chunks = list(lens), list(chunks)
         self.offsets = np.concatenate([[0], np.cumsum(chunks)]).astype(np.int32)
@@ -88,8 +92,9 @@ def test_all_modifiers_together(F, fmt, mode, gs, d):
 
 
 # Heads per KV head that make the chunks below long: rows are queries times heads,
-# and from 768 rows a request on, tiles are converted once for all row blocks.
-LONG = 96
+# and from 768 rows a request on, tiles are converted once for all row blocks, if
+# the tables have room for more than 256 tokens (REACH).
+LONG, REACH = 96, 320
 
 
 @pytest.mark.parametrize("fmt,mode,gs", KINDS)
@@ -143,9 +148,25 @@ def test_long_contexts(F, kw):
     R.check(b.run(F, out_dtype=torch.bfloat16, **kw), ref, 128, bf16=True, half=R.TOKEN_HEAD, cap=cap)
 
 
+@pytest.mark.parametrize("n,count", [(300, 12), (200, 16), (40, 60), (70, 30)])
+@pytest.mark.parametrize("kw", [{}, {"cap": 20.0}])
+def test_many_short_items_whose_last_block_has_one_row_tile(F, n, count, kw):
+    """A row block of at most 128 rows leaves the second row tile idle, whose threads
+    run ahead to their next block: what they read there has to be that block's.
+    300 queries: 2400 rows, ten row blocks, tiles converted once; the others by each."""
+    b = Batch([n] * count, [n] * count, 64, 8, 128, 16, R.E4M3, R.TOKEN_HEAD, seed=20)
+    ref = b.ref(device=DEV, **kw)
+    outs = [b.run(F, **kw) for _ in range(6)]
+    for got in outs:
+        R.check(got, ref, 128, half=R.TOKEN_HEAD, cap=kw.get("cap", 0.0))
+        assert torch.equal(got, outs[0])
+    assert F.get_device_error() == 0
+
+
 @pytest.mark.parametrize("hq", [4, 2 * 452])
 def test_requests_without_queries_or_tokens(F, hq):
-    b = Batch([40, 0, 17, 9, 0], [0, 0, 17, 0, 0], hq, 2, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=8)
+    b = Batch([40, 0, 17, 9, 0], [0, 0, 17, 0, 0], hq, 2, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=8,
+              reach=REACH)
     b.check(F)
 
 
@@ -169,7 +190,7 @@ def test_what_masked_tokens_hold_does_not_matter(F, fmt, nan, bad_scale, hq):
     """Past the end of the request, before the window and, for all but the last
     query, after it: what a row does not see may be anything."""
     lens, chunks = [70, 50, 33, 17], [9, 50, 1, 4]
-    b = Batch(lens, chunks, hq, 2, 128, 16, fmt, R.TOKEN_HEAD, seed=10)
+    b = Batch(lens, chunks, hq, 2, 128, 16, fmt, R.TOKEN_HEAD, seed=10, reach=REACH)
     mods = dict(window=20, prefix=[5, 0, 2, 0])
     ref = b.ref(**mods)
     kc, vc, ks, vs = b.cache
@@ -257,14 +278,16 @@ def test_pages_no_query_sees_are_not_read(F, hq):
 @pytest.mark.parametrize("hq", [4, 1536])
 def test_bad_blocks_lengths_and_offsets_are_flagged(F, hq):
     from fp8_quantised_paged_gb300 import _native as N
-    b = Batch([40, 20, 10], [5, 2, 3], hq, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=12)
+    b = Batch([40, 20, 10], [5, 2, 3], hq, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=12,
+              reach=REACH)
     b.bt[0, 1] = 10 ** 6
     b.lens[1], b.lens[2] = 10 ** 7, -4
     got = b.run(F)
     assert torch.isfinite(got[:5]).all() and not got[7:].any()
     assert F.get_device_error() == N.DEVERR_BLOCK_RANGE | N.DEVERR_SEQ_LEN
     # a chunk longer than its request: the rows before position 0 see nothing
-    b = Batch([4, 20], [4, 2], hq, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=12)
+    b = Batch([4, 20], [4, 2], hq, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=12,
+              reach=REACH)
     ref = b.ref()
     b.lens[0] = 2
     got = b.run(F)
@@ -272,7 +295,8 @@ def test_bad_blocks_lengths_and_offsets_are_flagged(F, hq):
     R.check(got[4:], tuple(x[4:] for x in ref), 64, half=R.TOKEN_HEAD)
     assert F.get_device_error() == N.DEVERR_SEQ_LEN
     for bad in ([0, 9, 6], [-1, 4, 6], [0, 4, 7]):
-        b = Batch([4, 20], [4, 2], hq, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=12)
+        b = Batch([4, 20], [4, 2], hq, 1, 64, 16, R.E4M3, R.TOKEN_HEAD, seed=12,
+              reach=REACH)
         b.offsets = np.array(bad, np.int32)
         out = torch.full((6, hq, 64), 7.0, device=DEV)
         b.run(F, out=out)
