@@ -17,15 +17,21 @@ inline int block_bound(int total_q, int batch, int G) {
 // of the block tables' reach fit kReadyBytes.  One request over 16384 tokens, once
 // against by each: 110 and 114 us at 2 row blocks, 116 and 132 at 3, 127 and 149
 // at 4, 151 and 194 at 6; eight over 4096 tokens: 137 and 145 at 2, 173 and 202 at
-// 3, 260 and 348 at 6.
+// 3, 260 and 348 at 6.  Not where the tables reach fewer than kReadyTiles tiles: a
+// prompt of 200 tokens takes 23.8 and 23.7 us, and a launch more; one of 300, 25.2
+// and 27.6.
 constexpr int kReadyBlocks = 3;
+constexpr int kReadyTiles = 3;
 constexpr long long kReadyBytes = 1ll << 30;
 inline int tiles_per_request(int bs, int max_blocks) {
   return static_cast<int>((static_cast<long long>(bs) * max_blocks + kT - 1) / kT);
 }
 inline bool use_ready(int total_q, int batch, int G, int hkv, int d, int bs, int max_blocks) {
-  const double tiles = static_cast<double>(tiles_per_request(bs, max_blocks)) * batch * hkv;
-  return static_cast<long long>(total_q) * G >= static_cast<long long>(kReadyBlocks) * kRows * batch &&
+  const int tpr = tiles_per_request(bs, max_blocks);
+  const double tiles = static_cast<double>(tpr) * batch * hkv;
+  return tpr >= kReadyTiles &&
+         static_cast<long long>(total_q) * G >=
+             static_cast<long long>(kReadyBlocks) * kRows * batch &&
          tiles * (4.0 * kT * d) <= static_cast<double>(kReadyBytes);
 }
 

@@ -478,8 +478,8 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
 /*
  * Bytes of device workspace fp8pa_paged_prefill_attention needs for these
  * sizes on the current device; 0 if they are rejected.  Where chunks are long
- * (768 rows, queries times heads per KV head, of a request on average) it holds
- * the block tables' whole reach in f16, up to 1 GiB; beyond that the tiles are
+ * (768 rows, queries times heads per KV head, of a request on average) and the
+ * block tables reach beyond 256 tokens it holds that reach in f16, up to 1 GiB; beyond that the tiles are
  * converted where they are used.
  */
 size_t fp8pa_prefill_workspace_bytes(int total_q, int batch, int n_q_heads, int n_kv_heads,
