@@ -29,7 +29,8 @@ __all__ = ["kv_append_quant", "kv_append_quant_segment", "segment_scale_heads",
            "kv_channel_scales", "kv_channel_absmax_update",
            "kv_scales_from_absmax", "paged_decode_attention", "paged_multiquery_attention",
            "kv_append_rope", "paged_decode_attention_mod", "paged_prefill_attention",
-           "prefill_workspace_bytes", "decode_step", "decode_workspace_bytes", "get_device_error", "set_decode_workers",
+           "prefill_workspace_bytes", "decode_step", "decode_workspace_bytes",
+           "get_device_error", "set_decode_workers",
            "version", "E4M3", "E5M2", "INT8", "SCALE_TOKEN_HEAD", "SCALE_CHANNEL_STATIC",
            "SCALE_TOKEN_GROUP", "SCALE_MX_BLOCK", "SCALE_SEGMENT", "SEGMENT_TOKENS", "OUT_BF16",
            "OUT_F32", "Fp8paError"]

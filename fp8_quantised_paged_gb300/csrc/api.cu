@@ -703,7 +703,8 @@ int fp8pa_paged_decode_attention_mod(const void* q, const uint8_t* k_cache,
                                    workspace_bytes, static_cast<cudaStream_t>(stream), &path, &a);
   if (st != FP8PA_OK || batch == 0) return st;
   const ScoreMods mods{prefix_lens, alibi_slopes, logit_cap, window};
-  return cuda_status(launch_decode_mod(path.shape, a, mods, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_decode_mod(path.shape, a, mods, workspace_bytes,
+                                       static_cast<cudaStream_t>(stream)));
 }
 
 size_t fp8pa_prefill_workspace_bytes(int total_q, int batch, int n_q_heads, int n_kv_heads,

@@ -12,10 +12,10 @@
 //
 // 4 requests of 131072 tokens with a distance bias: 202 us, 5.5 TB/s (82% of a
 // plain copy's rate).  12 of 16384 under a window of 4096: 34 us, most of it three
-// launches and the call.  The modifiers' registers cost the split kernel 7% (184
-// -> 198 us without any set), and with static channel scales and capped scores,
-// 128 registers and no room for a third ring stage, 64 ragged requests take 167 us
-// where the plain decode of the same cache takes 130.
+// launches and the call.  64 ragged requests, 546 MB of static-scale codes under
+// capped scores: 127 us, 4.3 TB/s, with two CTAs on an SM (this variant keeps to
+// 128 registers; with the plain kernel's one CTA, 167 us).  The modifiers' own
+// instructions cost 7% of a split kernel that sets none (184 -> 198 us).
 #include "gqa_split.cuh"
 
 namespace fp8pa {
@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(32) plan_mod_kernel(const int32_t* seq_lens, S
 }  // namespace
 
 cudaError_t launch_decode_mod(const DecodeShape& s, const DecodeArgs& a, const ScoreMods& mods,
-                              cudaStream_t stream) {
+                              size_t workspace_bytes, cudaStream_t stream) {
   const int G = s.hq / s.hkv;
   const auto k = pick<GqaModParams>(s.d, s.bs, a.fmt, kernel_mode(a.mode, G, a.gs));
   const void* fn = reinterpret_cast<const void*>(k.fn);
@@ -47,13 +47,18 @@ cudaError_t launch_decode_mod(const DecodeShape& s, const DecodeArgs& a, const S
   const int smem = k.smem(wpc);
   cudaError_t e = ensure_smem_attr(fn, smem);
   if (e != cudaSuccess) return e;
-  // One page range per resident CTA of this kernel, at most the plain
-  // decode's number, for which the workspace is sized.
+  // One page range per resident CTA of this kernel, or the plain decode's number
+  // where that is less and the workspace holds no more (the size function's answer
+  // is for the scale mode with the most ranges, and holds them).
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   int workers = s.workers;
-  if (g_decode_workers_override <= 0)
-    workers = max(1, min(workers, sm_count(dev) * ctas_per_sm(fn, wpc * 32, smem) / hsets));
+  if (g_decode_workers_override <= 0) {
+    DecodeShape own = s;
+    own.workers = max(1, sm_count(dev) * ctas_per_sm(fn, wpc * 32, smem) / hsets);
+    if (own.workers < workers || decode_workspace_bytes(own) <= workspace_bytes)
+      workers = own.workers;
+  }
 
   CUtensorMap tmk, tmv;
   const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * s.hkv * s.bs;

@@ -183,9 +183,9 @@ cudaError_t launch_decode_gqa(const DecodeShape& s, const DecodeArgs& a, cudaStr
 cudaError_t launch_decode_mla(const DecodeShape& s, const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_mla_tc(const DecodeShape& s, const DecodeArgs& a, cudaStream_t stream);
 // The grouped-query decode with score modifiers (decode_mod.cu); it fits the
-// workspace of the plain decode of the same shape.
+// workspace of the plain decode of the same shape, and uses more where it is given.
 cudaError_t launch_decode_mod(const DecodeShape& s, const DecodeArgs& a, const ScoreMods& mods,
-                              cudaStream_t stream);
+                              size_t workspace_bytes, cudaStream_t stream);
 
 // Attention of ragged query chunks (prefill.cu).
 struct PrefillArgs {

@@ -155,6 +155,35 @@ def test_bad_blocks_and_lengths_are_flagged(F):
     assert F.get_device_error() == N.DEVERR_BLOCK_RANGE | N.DEVERR_SEQ_LEN
 
 
+@pytest.mark.parametrize("mode", [R.TOKEN_HEAD, R.STATIC])
+def test_the_smallest_workspace_that_is_taken_is_not_overrun(F, mode):
+    """A workspace below the size function's answer is refused, or used with fewer
+    ranges; nothing behind it is written."""
+    hq, hkv, d, bs = 64, 8, 128, 32
+    s = setup([700, 3, 2000], hq, hkv, d, bs, R.E5M2, mode, seed=14)
+    ref = reference(s, hkv, 0.088, R.E5M2, mode, cap=5.0)
+    full = F.decode_workspace_bytes(3, hq, hkv, d, d, bs, s[5].shape[1])
+    buf = torch.empty(full, dtype=torch.uint8, device=DEV)
+
+    def run(n):
+        buf.fill_(0xA5)
+        got = call(F, s, hkv, 0.088, R.E5M2, mode, cap=5.0, workspace=buf[:n])
+        assert (buf[n:] == 0xA5).all()
+        R.check(got, ref, d, cap=5.0)
+
+    low, high = 0, full  # refused, taken
+    run(full)
+    while high - low > 256:
+        n = (low + high) // 512 * 256
+        try:
+            run(n)
+            high = n
+        except F.Fp8paError:
+            low = n
+    run(high)
+    assert F.get_device_error() == 0
+
+
 def test_graphs_that_share_a_workspace_and_other_streams(F):
     hq, hkv, d = 8, 2, 128
     s = setup([300, 7, 64], hq, hkv, d, 16, R.E4M3, R.TOKEN_HEAD, seed=12)
