@@ -1,6 +1,6 @@
 """FP8-quantised paged decode attention for GB300 (sm_103a).
 
-Two calls, both hand-written CUDA kernels behind a C ABI (``include/fp8pa.h``):
+The main calls, hand-written CUDA kernels behind a C ABI (``include/fp8pa.h``):
 
 * :func:`kv_append_quant` -- absmax-scale each new token's K/V rows, round
   them to E4M3 or E5M2 (or symmetric INT8 codes) and scatter codes and
@@ -8,6 +8,12 @@ Two calls, both hand-written CUDA kernels behind a C ABI (``include/fp8pa.h``):
 * :func:`paged_decode_attention` -- grouped-query (or shared-latent MLA)
   attention of one query token per request over its paged FP8 cache, split
   across the GPU and merged.
+* :func:`kv_append_rope` -- the append behind a rotation of q and k by their
+  positions.
+* :func:`paged_decode_attention_mod` -- the decode with a window, an
+  always-visible prefix, capped scores and a distance bias.
+* :func:`paged_prefill_attention` -- ragged query chunks of any length, with
+  the same modifiers.
 
 These wrappers only check torch tensors and pass their device pointers and
 the current CUDA stream to the library.  PyTorch provides memory and streams;
