@@ -43,8 +43,8 @@
 // tiles (a thread each); the last issues the MMAs (one thread).  While the tensor
 // cores work on one row tile, the other's softmax runs.  Every wait is bounded.
 //
-// Measured, head_dim 128, 64 heads over 8: 2048 queries over 16384 tokens 904 us,
-// 1.14 PFLOP/s (59% of a large library product's rate); before the ready tiles
+// Measured, head_dim 128, 64 heads over 8: 2048 queries over 16384 tokens 914-920
+// us, 1.12 PFLOP/s (58% of a large library product's rate); before the ready tiles
 // 1260 us.  Per 128-token tile of 256 rows that is 4200 cycles, 2800 of them with
 // MMAs under way (2048 at their own rate: the shared memory that feeds both
 // operands of S also takes the tiles in), the rest the softmax's own chain.

@@ -411,7 +411,9 @@ int fp8pa_kv_append_rope(const void* q, void* q_out, const void* k, const void* 
  * bidirectional prefix in a prefill, tokens kept ahead of a sliding window in
  * a decode step.  Values outside [0, seq_len] are taken as the nearer end.
  * A row that sees no token is zero.  What a masked token's codes and scales
- * hold (infinities and NaN among it) does not reach the output.
+ * hold (infinities and NaN among it) does not reach the output.  A row that
+ * sees a value that is not finite is not finite either, in some or in all of
+ * its elements.
  */
 
 /*

@@ -330,6 +330,33 @@ def test_graphs_that_share_a_workspace_and_other_streams(F, hq):
     assert torch.equal(got, want[0])
 
 
+def test_calls_at_once_on_several_streams(F):
+    """Both head sizes, both ways of conversion and a decode, each on a stream of its
+    own and all under way together."""
+    form = dict(fmt=R.E4M3, mode=R.TOKEN_HEAD)
+    batches = [Batch([900, 40], [300, 40], 8, 2, 128, 16, *form.values(), seed=21),
+               Batch([700] * 3, [9] * 3, 8, 2, 64, 16, *form.values(), seed=22),
+               Batch([1500], [700], 16, 4, 64, 32, *form.values(), seed=23),
+               Batch([2000] * 4, [5] * 4, 8, 2, 128, 64, *form.values(), seed=24)]
+    args = [b.args() for b in batches]
+    calls = [lambda a=a, b=b, **kw: F.paged_prefill_attention(*a, **b.form, **kw)
+             for a, b in zip(args, batches)]
+    dec = Batch([3000, 17], [1, 1], 8, 2, 128, 16, *form.values(), seed=25)
+    q, _, *rest = dec.args()
+    calls.append(lambda **kw: F.paged_decode_attention_mod(q, *rest, **dec.form, window=700, **kw))
+    want = [c().clone() for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    outs = [[] for _ in calls]
+    for _ in range(15):
+        for c, st, o in zip(calls, streams, outs):
+            o.append(c(stream=st))
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(x, w) for x in o)
+    assert F.get_device_error() == 0
+
+
 def test_repeated_calls_are_bit_identical(F):
     b = Batch([3000, 40, 1777], [500, 40, 33], 8, 2, 128, 16, R.E4M3, R.TOKEN_HEAD, seed=14)
     outs = [b.run(F, window=900, cap=20.0) for _ in range(3)]
