@@ -85,6 +85,20 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _alloc(shape, dtype, dev, stream, result=True):
+    """Memory for a call on `stream` (None: the current one), from the pool of that
+    stream: the block's earlier uses are that stream's own, so the call's kernels come
+    behind them.  A result is read on the current stream, too: its memory is not handed
+    out again before what that stream holds when the result is freed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if result:
+        t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
 def version() -> int:
     return int(N.lib.fp8pa_version())
 
@@ -163,7 +177,7 @@ def kv_channel_scales(x, fmt=E5M2, out=None, stream=None):
     _need(x, torch.bfloat16, "x")
     n, hkv, d = x.shape
     if out is None:
-        out = torch.empty((hkv, d), dtype=torch.float32, device=x.device)
+        out = _alloc((hkv, d), torch.float32, x.device, stream)
     _need(out, torch.float32, "out", x.device)
     with torch.cuda.device(x.device):
         rc = N.lib.fp8pa_kv_channel_scales(_ptr(x), n, hkv, d, fmt, _ptr(out), _stream(stream))
@@ -188,7 +202,7 @@ def kv_scales_from_absmax(absmax, fmt=E5M2, out=None, stream=None):
     """Static scales max(absmax / FMAX, 1e-12) from a running absmax."""
     _need(absmax, torch.float32, "absmax")
     if out is None:
-        out = torch.empty_like(absmax)
+        out = _alloc(absmax.shape, torch.float32, absmax.device, stream)
     _need(out, torch.float32, "out", absmax.device)
     with torch.cuda.device(absmax.device):
         rc = N.lib.fp8pa_kv_scales_from_absmax(_ptr(absmax), absmax.numel(), fmt, _ptr(out),
@@ -231,7 +245,7 @@ def paged_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, 
     nb, _, bs, _ = k_cache.shape
     max_blocks = block_tables.shape[1]
     if out is None:
-        out = torch.empty((B, hq, dv), dtype=out_dtype or torch.bfloat16, device=dev)
+        out = _alloc((B, hq, dv), out_dtype or torch.bfloat16, dev, stream)
     odt = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
     if out.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("out must be bf16 or float32")
@@ -241,7 +255,7 @@ def paged_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, 
             need = int(N.lib.fp8pa_decode_workspace_bytes(B, hq, n_kv_heads, dk, dv, bs,
                                                           max_blocks))
             if need > 0:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                workspace = _alloc(need, torch.uint8, dev, stream, result=False)
         # need == 0 means the shapes are rejected: the call below returns the
         # precise status code.
         _need(workspace, torch.uint8, "workspace", dev)
@@ -275,7 +289,7 @@ def paged_multiquery_attention(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     nb, _, bs, _ = k_cache.shape
     max_blocks = block_tables.shape[1]
     if out is None:
-        out = torch.empty((B, qlen, hq, dv), dtype=out_dtype or torch.bfloat16, device=dev)
+        out = _alloc((B, qlen, hq, dv), out_dtype or torch.bfloat16, dev, stream)
     if out.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("out must be bf16 or float32")
     odt = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
@@ -285,7 +299,7 @@ def paged_multiquery_attention(q, k_cache, v_cache, k_scale, v_scale, block_tabl
             need = int(N.lib.fp8pa_multiquery_workspace_bytes(B, qlen, hq, n_kv_heads, dk, dv,
                                                               bs, max_blocks))
             if need > 0:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                workspace = _alloc(need, torch.uint8, dev, stream, result=False)
         _need(workspace, torch.uint8, "workspace", dev)
         rc = N.lib.fp8pa_paged_multiquery_attention(
             _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
@@ -323,7 +337,7 @@ def decode_step(k_new, v_new, slot_mapping, q, k_cache, v_cache, k_scale, v_scal
     n_new = k_new.shape[0]
     if out is None:
         shape = (B, qlen, hq, dv) if multi else (B, hq, dv)
-        out = torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=dev)
+        out = _alloc(shape, out_dtype or torch.bfloat16, dev, stream)
     if out.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("out must be bf16 or float32")
     odt = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
@@ -333,7 +347,7 @@ def decode_step(k_new, v_new, slot_mapping, q, k_cache, v_cache, k_scale, v_scal
             need = int(N.lib.fp8pa_multiquery_workspace_bytes(B, qlen, hq, n_kv_heads, dk, dv,
                                                               bs, max_blocks))
             if need > 0:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                workspace = _alloc(need, torch.uint8, dev, stream, result=False)
         _need(workspace, torch.uint8, "workspace", dev)
         rc = N.lib.fp8pa_decode_step(
             _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), n_new, _ptr(q), _ptr(k_cache),
@@ -435,9 +449,7 @@ def kv_append_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, 
         hq = q.shape[1]
         qs = _rows(q, "q", n, hq, d, dev)
         if q_out is None:
-            q_out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=dev)
-            if stream is not None:
-                q_out.record_stream(stream)
+            q_out = _alloc((n, hq, d), torch.bfloat16, dev, stream)
         qos = _rows(q_out, "q_out", n, hq, d, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -489,9 +501,7 @@ def _check_tables(block_tables, seq_lens, dev):
 def _output(out, shape, out_dtype, dev, stream):
     """The output tensor and its element code."""
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=dev)
-        if stream is not None:
-            out.record_stream(stream)
+        out = _alloc(shape, out_dtype or torch.bfloat16, dev, stream)
     elif out.shape != shape:
         raise ValueError(f"out must be {tuple(shape)}, got {tuple(out.shape)}")
     dt = out.dtype
@@ -502,13 +512,8 @@ def _output(out, shape, out_dtype, dev, stream):
 
 
 def _scratch(need, dev, stream):
-    """Workspace of one call: freed for reuse only behind the call's own stream."""
-    if need == 0:
-        return None
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+    """Workspace of one call (None where the sizes are refused)."""
+    return _alloc(need, torch.uint8, dev, stream, result=False) if need else None
 
 
 @functools.lru_cache(maxsize=4096)
