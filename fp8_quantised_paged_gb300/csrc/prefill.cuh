@@ -25,7 +25,8 @@
 // outside), rounded once (2^-11; exact for MX blocks and static scales).  The
 // largest is put as high as f16 allows, so that a token whose scale is 2^r below
 // it (which some rows may mask) is off by no more than 2^(r - 32) beside that
-// rounding; E5M2's codes fill f16's exponents by themselves: 2^(r - 25).  Scaling
+// rounding; E5M2's codes fill f16's exponents by themselves: 2^(r - 25).  The
+// exponent of V has a floor (kLowV), which holds the sums of rows within fp32.  Scaling
 // the fp32 scores and P instead would keep the scales exact, but costs every
 // score two multiplications and two broadcast loads beside MMAs that fill the
 // shared-memory bandwidth: 1.45 ms against 1.30 ms for 2048 queries over 16384
@@ -114,6 +115,11 @@ constexpr int kSnap = 4;     // a cut this near an item's edge moves to it
 constexpr float kShift = 12.f;  // P = 2^(z - ref + 12): at most 2^15 with the lazy bound
 constexpr float kTau = 3.f;     // the reference may lag by 2^3
 constexpr float kNegBig = -1e30f;
+// The smallest exponents that K^ and V^ leave out.  A row's sum holds 2^(z - ref + 12)
+// of each token, and ref is at least max(z + e) - kTau: a token adds at
+// most 2^(15 - e), 2^95 here, so that 2^31 tokens whose V is next to nothing stay
+// within fp32.  Values of V below 2^-94 lose bits in V^ for it (half of 2^-104).
+constexpr int kLowK = -107, kLowV = -80;
 
 // A request's chunk and its visible extent.
 struct Chunk {
@@ -442,11 +448,12 @@ __device__ __forceinline__ void finish_job(const PrefillArgs& a, Job<D>& job, bo
   // the group's exponent, kRoom below the one above its largest (finite) scale,
   // and the scales relative to it
   const bool finite = job.sc <= FLT_MAX;  // (not for a NaN)
+  const int low = V ? kLowV : kLowK;
   int e;
   if constexpr (MX) {
-    e = max(__reduce_max_sync(0xffffffffu, job.em) - 127, -100) - kRoom;
+    e = max(__reduce_max_sync(0xffffffffu, job.em) - 127 - kRoom, low);
   } else {
-    e = min(max(exp_above(warp_max_f32(job.sok && finite ? job.sc : 0.f)), -100), 120) - kRoom;
+    e = max(min(exp_above(warp_max_f32(job.sok && finite ? job.sc : 0.f)), 120) - kRoom, low);
     if (a.mode == FP8PA_SCALE_CHANNEL_STATIC) e = 0;
     job.sc *= exp2i(-e);
   }
