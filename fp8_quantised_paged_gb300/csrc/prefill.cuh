@@ -445,15 +445,18 @@ __device__ __forceinline__ void finish_job(const PrefillArgs& a, Job<D>& job, bo
   constexpr int kRoom = FMT == FP8PA_E5M2 ? 0 : 7;  // codes of at most 448 leave f16 this much
   const int r8 = lane & 7, c4 = lane >> 3;
   const uint32_t valid = __ballot_sync(0xffffffffu, job.sok);
-  // the group's exponent, kRoom below the one above its largest (finite) scale,
-  // and the scales relative to it
-  const bool finite = job.sc <= FLT_MAX;  // (not for a NaN)
+  // The group's exponent, kRoom below the one above its largest finite scale, and the
+  // scales relative to it.  A scale counts as finite where its largest code is, in fp32
+  // (append writes no others): the relative scales of these stay below 2^kRoom, so that
+  // V^ is finite, and a larger one does not cost its group the precision.
+  const bool finite = MX ? job.em <= 254 - (FMT == FP8PA_E5M2 ? 15 : 8)
+                         : job.sc <= FLT_MAX / code_max<FMT>();  // (not for a NaN)
   const int low = V ? kLowV : kLowK;
   int e;
   if constexpr (MX) {
-    e = max(__reduce_max_sync(0xffffffffu, job.em) - 127 - kRoom, low);
+    e = max(__reduce_max_sync(0xffffffffu, finite ? job.em : 0) - 127 - kRoom, low);
   } else {
-    e = max(min(exp_above(warp_max_f32(job.sok && finite ? job.sc : 0.f)), 120) - kRoom, low);
+    e = max(exp_above(warp_max_f32(job.sok && finite ? job.sc : 0.f)) - kRoom, low);
     if (a.mode == FP8PA_SCALE_CHANNEL_STATIC) e = 0;
     job.sc *= exp2i(-e);
   }
@@ -516,9 +519,10 @@ __device__ __forceinline__ void finish_job(const PrefillArgs& a, Job<D>& job, bo
       uint4 p, q;
       codes16_to_f16<FMT>(job.buf[x][h], p, q);
       if constexpr (MX) {
-        // the block's power of two relative to the group's largest
+        // the block's power of two relative to the group's largest finite one (beyond
+        // it, infinite)
         const int be = static_cast<int>((job.ex[h] >> (8 * x)) & 0xFFu) - 127 - e;
-        const float f = __int_as_float((max(min(be, kRoom), -126) + 127) << 23);
+        const float f = __int_as_float((be > kRoom ? 255 : max(be, -126) + 127) << 23);
         const __half2 f2 = __floats2half2_rn(f, f);
         p = scale8(p, f2);
         q = scale8(q, f2);

@@ -411,9 +411,9 @@ int fp8pa_kv_append_rope(const void* q, void* q_out, const void* k, const void* 
  * bidirectional prefix in a prefill, tokens kept ahead of a sliding window in
  * a decode step.  Values outside [0, seq_len] are taken as the nearer end.
  * A row that sees no token is zero.  What a masked token's codes and scales
- * hold (infinities and NaN among it) does not reach the output.  A row that
- * sees a value that is not finite is not finite either, in some or in all of
- * its elements.
+ * hold (infinities and NaN among it) does not reach the output, but for the
+ * prefill's precision (below).  A row that sees a value that is not finite is
+ * not finite either, in some or in all of its elements.
  */
 
 /*
@@ -462,7 +462,8 @@ int fp8pa_paged_decode_attention_mod(const void* q, const uint8_t* k_cache,
  *              (2^-11).  Among 32 tokens of one tile, a token whose scale is
  *              2^r below the largest is off by up to 2^(r - 32) more (E5M2:
  *              2^(r - 25)), whether or not a row sees the large one.  Values of
- *              V below 2^-94 are off by up to 2^-105.
+ *              V below 2^-94 are off by up to 2^-105.  A scale whose largest code
+ *              passes FLT_MAX (no append writes one) may count as not finite.
  * workspace    at least fp8pa_prefill_workspace_bytes(), 16-byte aligned; no
  *              initialisation; calls that share it must be stream-ordered.
  */
