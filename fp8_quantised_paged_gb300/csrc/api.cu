@@ -702,7 +702,7 @@ int fp8pa_paged_decode_attention_mod(const void* q, const uint8_t* k_cache,
                                    sm_scale, num_blocks, out, out_dtype, workspace,
                                    workspace_bytes, static_cast<cudaStream_t>(stream), &path, &a);
   if (st != FP8PA_OK || batch == 0) return st;
-  const ScoreMods mods{prefix_lens, alibi_slopes, logit_cap, window};
+  const ScoreMods mods{prefix_lens, alibi_slopes, kernel_cap(logit_cap), window};
   return cuda_status(launch_decode_mod(path.shape, a, mods, workspace_bytes,
                                        static_cast<cudaStream_t>(stream)));
 }
@@ -770,7 +770,7 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
   a.seq_lens = seq_lens;
   a.prefix_lens = prefix_lens;
   a.slopes = alibi_slopes;
-  a.cap = logit_cap;
+  a.cap = kernel_cap(logit_cap);
   a.sm_scale = sm_scale;
   a.window = window;
   a.total_q = total_q;

@@ -542,14 +542,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
         float z[4] = {acc[0] * (zs * sk0), acc[1] * (zs * sk0), acc[2] * (zs * sk1),
                       acc[3] * (zs * sk1)};
         if (p.mods.cap > 0.f) {
-          const float back = p.mods.cap * kLog2e;
           if (p.mods.cap <= kCapFast) {
+            const float back = p.mods.cap * kLog2e;
 #pragma unroll
             for (int e = 0; e < 4; ++e) z[e] = cap_fast(z[e], back);
           } else {
             const float inv = 1.0f / p.mods.cap;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] = back * tanh_f32(z[e] * inv);
+            for (int e = 0; e < 4; ++e) z[e] = p.mods.cap * tanh_f32(z[e] * inv) * kLog2e;
           }
         }
         const float d0 = static_cast<float>(Lb - 1 - tok0 - g), d1 = d0 - 8.f;

@@ -200,6 +200,9 @@ struct PrefillArgs {
   const int32_t* prefix_lens;
   const float* slopes;
   float cap, sm_scale;
+  // Capped scores: z' = cap_in z goes into the tanh as tanh_in z', which is z / cap.
+  // Caps up to kCapFast: z' = 2 log2(e) z / cap, for cap_fast; larger ones: z' = z.
+  float cap_in, tanh_in;
   int window;
   int total_q, batch, hq, hkv, G, d, bs, max_blocks, num_blocks, fmt, mode, gs, hp, out_f32;
   void* out;

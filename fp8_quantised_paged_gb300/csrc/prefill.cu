@@ -243,7 +243,11 @@ size_t prefill_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, i
                      nullptr);
 }
 
-cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
+cudaError_t launch_prefill(const PrefillArgs& args, cudaStream_t stream) {
+  PrefillArgs a = args;
+  const bool fast = a.cap <= kCapFast;
+  a.cap_in = a.cap > 0.f && fast ? 2.f * kLog2e / a.cap : 1.f;
+  a.tanh_in = fast ? 0.5f / kLog2e : 1.f / a.cap;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

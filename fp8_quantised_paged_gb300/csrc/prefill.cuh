@@ -947,8 +947,8 @@ __global__ void __launch_bounds__(kThreads<READY>, 1)
           break;
         }
         const int er = static_cast<int>((lane >> 4) == half ? mine : theirs);
-        // log2-domain factor of a raw score (capped scores: of 2 z / cap)
-        zs = fabsf(a.sm_scale) * exp2i(er - 14) * kLog2e * (VAR == 2 ? 2.f / a.cap : 1.f);
+        // log2-domain factor of a raw score (capped scores: see cap_in)
+        zs = fabsf(a.sm_scale) * exp2i(er - 14) * (VAR == 2 ? a.cap_in : kLog2e);
       }
       const int pos = im.r.L - im.r.n + qi;
       const int wf = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
@@ -1031,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads<READY>, 1)
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
                   y[v] *= zw[w];
-                  if constexpr (VAR == 2) y[v] = cap_log2 * tanh_f32(y[v] * (0.5f / kLog2e));
+                  if constexpr (VAR == 2) y[v] = a.cap * tanh_f32(y[v] * a.tanh_in) * kLog2e;
                   y[v] = fmaf(-slope, fabsf(static_cast<float>(pos - jw - 2 * i - v)), y[v]);
                 }
               } else {

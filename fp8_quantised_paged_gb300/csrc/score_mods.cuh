@@ -29,6 +29,12 @@ __device__ __forceinline__ int window_first(const ScoreMods& m, int pos) {
 // 2^-14 here, for two special-function operations and three others.  Larger caps
 // need tanh_f32, good relative to the score.
 constexpr float kCapFast = 64.f;
+// The cap that the kernels take.  Scores within 2^-60 of zero weigh the same, to 2^-59,
+// so a smaller cap is this one, whose 2 / cap leaves the scores' factors in fp32.
+// Larger caps scale z by 1 / cap, which fp32 holds (FLT_MAX's as a subnormal, off by
+// 2^-150 and so by 2^-22 of z), and multiply the tanh by cap before log2(e), as cap
+// log2(e) need not be finite.
+inline float kernel_cap(float cap) { return cap > 0.f ? (cap < 0x1p-60f ? 0x1p-60f : cap) : 0.f; }
 // 1 / x, good to 2^-23; 0 for an infinity.
 __device__ __forceinline__ float rcp_fast(float x) {
   float r;
