@@ -120,6 +120,16 @@ __device__ __forceinline__ uint32_t tile_bits(int t0, int lo, int hi) {
   return ((1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
+// The larger of two scores.  With score modifiers a NaN among them stays, so that a row
+// whose visible scores are all NaN is not taken for one that sees nothing.
+template <bool MOD>
+__device__ __forceinline__ float max_score(float a, float b) {
+  if constexpr (!MOD) return fmaxf(a, b);
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 template <int D, int BS, int FMT, int MODE, int NST, class P>
 __global__ void __launch_bounds__(kMaxWarps * 32)
     gqa_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -563,13 +573,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
         z10 = v1 ? acc[2] * (zs * sk1) : NEG_INF;
         z11 = v1 ? acc[3] * (zs * sk1) : NEG_INF;
       }
-      float mx0 = fmaxf(z00, z10), mx1 = fmaxf(z01, z11);
+      float mx0 = max_score<MOD>(z00, z10), mx1 = max_score<MOD>(z01, z11);
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+        mx0 = max_score<MOD>(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+        mx1 = max_score<MOD>(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
       }
-      const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+      const float mn0 = max_score<MOD>(m0, mx0), mn1 = max_score<MOD>(m1, mx1);
       const bool live0 = mn0 != NEG_INF, live1 = mn1 != NEG_INF;
       const float al0 = live0 ? ex2(m0 - mn0) : 1.f;
       const float al1 = live1 ? ex2(m1 - mn1) : 1.f;
@@ -736,7 +746,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
         for (int e = 0; e < D / 32; ++e)
           po[e] = make_float4(vals[4 * e], vals[4 * e + 1], vals[4 * e + 2], vals[4 * e + 3]);
         if (g == 0) {
-          p.part_ml[(seg * p.G + hh) * 2] = hsel ? m1 : m0;
+          float m = hsel ? m1 : m0;
+          // (the merge weighs a piece by its maximum: a NaN's sums have to count)
+          if (MOD && m != m) m = -NEG_INF;
+          p.part_ml[(seg * p.G + hh) * 2] = m;
           p.part_ml[(seg * p.G + hh) * 2 + 1] = hsel ? l1 : l0;
         }
       }

@@ -412,8 +412,10 @@ int fp8pa_kv_append_rope(const void* q, void* q_out, const void* k, const void* 
  * a decode step.  Values outside [0, seq_len] are taken as the nearer end.
  * A row that sees no token is zero.  What a masked token's codes and scales
  * hold (infinities and NaN among it) does not reach the output, but for the
- * prefill's precision (below).  A row that sees a value that is not finite is
- * not finite either, in some or in all of its elements.
+ * prefill's precision (below).  A row that sees a NaN, or a V that is not finite,
+ * is not finite either, in some or in all of its elements.  An infinite K gives
+ * scores that are infinite or NaN; one of minus infinity has no weight (a row
+ * of nothing else is zero).
  */
 
 /*
