@@ -371,14 +371,19 @@ int append_prepare(const void* k, const void* v, const int32_t* slot_mapping, in
   return FP8PA_OK;
 }
 
-// The sizes of a prefill call that its workspace depends on.
+// The sizes of a prefill call that its workspace depends on: every limit that does not
+// need the pool's size, the format or the scale mode.
 int prefill_shape(int total_q, int batch, int hq, int hkv, int d, int bs, int max_blocks) {
   if (total_q < 0 || batch < 0 || hq <= 0 || hkv <= 0 || hq % hkv != 0 || bs <= 0 ||
       max_blocks <= 0)
     return FP8PA_ERR_BAD_SHAPE;
-  if (d != 64 && d != 128) return FP8PA_ERR_UNSUPPORTED;
+  if ((d != 64 && d != 128) || (bs != 16 && bs != 32 && bs != 64)) return FP8PA_ERR_UNSUPPORTED;
   if ((static_cast<long long>(total_q) + 256ll * batch) * hq >= (1ll << 31) ||
-      static_cast<long long>(bs) * max_blocks >= (1ll << 31))
+      static_cast<long long>(bs) * max_blocks * hkv >= (1ll << 31))
+    return FP8PA_ERR_UNSUPPORTED;
+  // the planner counts (256-row block, KV head, 128-token tile) units in 32 bits
+  const long long blocks = static_cast<long long>(total_q) * (hq / hkv) / 256 + 1 + batch;
+  if (blocks * hkv * (static_cast<long long>(max_blocks) * bs / 128 + 1) >= (1ll << 31))
     return FP8PA_ERR_UNSUPPORTED;
   return FP8PA_OK;
 }
@@ -739,12 +744,6 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
            .status;
   if (st != FP8PA_OK) return st;
   if (!(logit_cap >= 0.f) || logit_cap > FLT_MAX) return FP8PA_ERR_UNSUPPORTED;
-  // the planner counts (256-row block, KV head, 128-token tile) units in 32 bits
-  const long long blocks =
-      static_cast<long long>(total_q) * (n_q_heads / n_kv_heads) / 256 + 1 + batch;
-  if (blocks * n_kv_heads * (static_cast<long long>(max_blocks_per_seq) * block_size / 128 + 1) >=
-      (1ll << 31))
-    return FP8PA_ERR_UNSUPPORTED;
   if (batch == 0 || total_q == 0) return FP8PA_OK;
   if (!q || !q_offsets || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables ||
       !seq_lens || !out || !workspace)
