@@ -572,7 +572,8 @@ def paged_decode_attention_mod(q, k_cache, v_cache, k_scale, v_scale, block_tabl
 
 def prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
                             max_blocks_per_seq, device=None) -> int:
-    """Workspace bytes of paged_prefill_attention for these sizes."""
+    """Workspace bytes of paged_prefill_attention for these sizes.  A workspace made for
+    a larger batch is taken, too, but may not hold the tiles converted once."""
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
         nbytes = int(N.lib.fp8pa_prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads,
                                                          head_dim, block_size,

@@ -720,7 +720,7 @@ size_t fp8pa_prefill_workspace_bytes(int total_q, int batch, int n_q_heads, int 
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   return prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
-                                 max_blocks_per_seq, dev);
+                                 max_blocks_per_seq, dev, false);
 }
 
 int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int total_q,
@@ -757,7 +757,7 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
   if (!a.err) return FP8PA_ERR_CUDA;
   if (workspace_bytes <
       prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
-                              max_blocks_per_seq, dev))
+                              max_blocks_per_seq, dev, true))
     return FP8PA_ERR_WORKSPACE;
   a.q = static_cast<const uint16_t*>(q);
   a.q_offsets = q_offsets;
@@ -788,6 +788,7 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
   a.out_f32 = out_dtype == FP8PA_OUT_F32;
   a.out = out;
   a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
   return cuda_status(launch_prefill(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -207,10 +207,12 @@ struct PrefillArgs {
   int total_q, batch, hq, hkv, G, d, bs, max_blocks, num_blocks, fmt, mode, gs, hp, out_f32;
   void* out;
   void* workspace;
+  size_t workspace_bytes;
   uint32_t* err;
 };
+// What a prefill uses, or (least) what it cannot do without: the plan and the pieces.
 size_t prefill_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, int bs,
-                               int max_blocks, int device);
+                               int max_blocks, int device, bool least);
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 
 // The tensor-core kernel for a causal chunk over the grouped-query layout:

@@ -36,7 +36,7 @@ inline bool use_ready(int total_q, int batch, int G, int hkv, int d, int bs, int
 }
 
 inline size_t plan_layout(char* ws, int total_q, int batch, int G, int hkv, int d, int bs,
-                          int max_blocks, int ranges, PlanView* v) {
+                          int max_blocks, int ranges, bool ready, PlanView* v) {
   const int nb = block_bound(total_q, batch, G);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -56,7 +56,7 @@ inline size_t plan_layout(char* ws, int total_q, int batch, int G, int hkv, int 
   t.blocks = nb;
   t.tpr = tiles_per_request(bs, max_blocks);
   t.tiles = t.info = nullptr;
-  if (use_ready(total_q, batch, G, hkv, d, bs, max_blocks)) {
+  if (ready) {
     const size_t tiles = static_cast<size_t>(t.tpr) * batch * hkv;
     t.tiles = reinterpret_cast<uint8_t*>(take(tiles * 4 * kT * d));
     t.info = reinterpret_cast<uint8_t*>(take(tiles * sizeof(StageInfo)));
@@ -238,9 +238,10 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a,
 }  // namespace
 
 size_t prefill_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, int bs,
-                               int max_blocks, int device) {
-  return plan_layout(nullptr, total_q, batch, hq / hkv, hkv, d, bs, max_blocks, sm_count(device),
-                     nullptr);
+                               int max_blocks, int device, bool least) {
+  const int G = hq / hkv;
+  return plan_layout(nullptr, total_q, batch, G, hkv, d, bs, max_blocks, sm_count(device),
+                     !least && use_ready(total_q, batch, G, hkv, d, bs, max_blocks), nullptr);
 }
 
 cudaError_t launch_prefill(const PrefillArgs& args, cudaStream_t stream) {
@@ -252,12 +253,16 @@ cudaError_t launch_prefill(const PrefillArgs& args, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const int ranges = sm_count(dev);
+  // ready tiles where they pay and the workspace holds them
+  const bool ready =
+      use_ready(a.total_q, a.batch, a.G, a.hkv, a.d, a.bs, a.max_blocks) &&
+      plan_layout(nullptr, a.total_q, a.batch, a.G, a.hkv, a.d, a.bs, a.max_blocks, ranges, true,
+                  nullptr) <= a.workspace_bytes;
   PlanView pv;
   plan_layout(static_cast<char*>(a.workspace), a.total_q, a.batch, a.G, a.hkv, a.d, a.bs,
-              a.max_blocks, ranges, &pv);
+              a.max_blocks, ranges, ready, &pv);
   const int var = a.cap > 0.f ? 2 : (a.slopes ? 1 : 0);
   const bool mx = a.mode == FP8PA_SCALE_MX_BLOCK;
-  const bool ready = use_ready(a.total_q, a.batch, a.G, a.hkv, a.d, a.bs, a.max_blocks);
   const PrefillKernels fn = a.d == 128 ? pick_prefill_d128(a.fmt, var, mx, ready)
                                        : pick_prefill_d64(a.fmt, var, mx, ready);
   if ((e = ensure_smem_attr(reinterpret_cast<const void*>(fn.attend), fn.smem)) != cudaSuccess)

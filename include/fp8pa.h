@@ -466,8 +466,12 @@ int fp8pa_paged_decode_attention_mod(const void* q, const uint8_t* k_cache,
  *              2^(r - 25)), whether or not a row sees the large one.  Values of
  *              V below 2^-94 are off by up to 2^-105.  A scale whose largest code
  *              passes FLT_MAX (no append writes one) may count as not finite.
- * workspace    at least fp8pa_prefill_workspace_bytes(), 16-byte aligned; no
- *              initialisation; calls that share it must be stream-ordered.
+ * workspace    fp8pa_prefill_workspace_bytes(), 16-byte aligned; no initialisation;
+ *              calls that share it must be stream-ordered.  A smaller one is
+ *              taken where it holds the plan and the partial results, which
+ *              grow with total_q and batch alone: what is right for a batch
+ *              serves every smaller one of the same heads on the device, but
+ *              tiles that it does not hold are converted where they are used.
  */
 int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int total_q,
                                   const uint8_t* k_cache, const uint8_t* v_cache,
@@ -485,8 +489,9 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
  * Bytes of device workspace fp8pa_paged_prefill_attention needs for these
  * sizes on the current device; 0 if they are rejected.  Where chunks are long
  * (768 rows, queries times heads per KV head, of a request on average) and the
- * block tables reach beyond 256 tokens it holds that reach in f16, up to 1 GiB; beyond that the tiles are
- * converted where they are used.
+ * block tables reach beyond 256 tokens it holds that reach in f16, up to 1 GiB;
+ * beyond that the tiles are converted where they are used.  So it is not the
+ * larger for more requests or wider tables.
  */
 size_t fp8pa_prefill_workspace_bytes(int total_q, int batch, int n_q_heads, int n_kv_heads,
                                      int head_dim, int block_size, int max_blocks_per_seq);

@@ -39,3 +39,49 @@ def test_bad_offsets_skip_their_request_alone(F, hq, dt, offsets, skipped):  # n
     left = [i for i in range(total) if i not in rows]
     assert (out[left] == KEPT).all()
     assert (buf[:guard // 2] == KEPT).all() and (buf[guard // 2 + total:] == KEPT).all()
+
+
+@pytest.mark.parametrize("d,fmt,mode", [(128, R.E4M3, R.TOKEN_HEAD), (64, R.INT8, R.TOKEN_HEAD),
+                                        (128, R.E5M2, R.MX)])
+def test_any_workspace_that_is_taken_is_not_overrun(F, d, fmt, mode):  # noqa: F811
+    """Below the size function's answer tiles are converted where they are used; below
+    the plan and the pieces the call is refused.  Nothing behind is written."""
+    b = Batch([700, 3, 400], [300, 3, 200], 16, 2, d, 16, fmt, mode, seed=45)
+    ref = b.ref(device=DEV, window=350)
+    full = F.prefill_workspace_bytes(503, 3, 16, 2, d, 16, b.bt.shape[1])
+    buf = torch.empty(full, dtype=torch.uint8, device=DEV)
+
+    def run(n):
+        buf.fill_(0xA5)
+        got = b.run(F, window=350, workspace=buf[:n])
+        assert (buf[n:] == 0xA5).all()
+        R.check(got, ref, d, half=mode)
+        return got
+
+    once = run(full)
+    assert torch.equal(run(full), once)
+    each = run(full - 256)  # the tiles no longer fit
+    low, high = 0, full - 256  # refused, taken
+    while high - low > 256:
+        n = (low + high) // 512 * 256
+        try:
+            assert torch.equal(run(n), each)
+            high = n
+        except F.Fp8paError as e:
+            assert e.code == -5
+            low = n
+    assert high < full - 3 * (700 // 128) * 2 * 4 * 128 * d  # without any tile
+    assert F.get_device_error() == 0
+
+
+def test_a_workspace_of_a_large_batch_serves_a_small_one(F):  # noqa: F811
+    """40 requests of 9 queries need no tiles, one of 300 would."""
+    big = Batch([400] * 40, [9] * 40, 16, 2, 128, 16, R.E4M3, R.TOKEN_HEAD, seed=46)
+    size = lambda b: F.prefill_workspace_bytes(  # noqa: E731
+        int(b.offsets[-1]), len(b.lens), 16, 2, 128, 16, b.bt.shape[1])
+    ws = torch.empty(size(big), dtype=torch.uint8, device=DEV)
+    for small in (Batch([400], [300], 16, 2, 128, 16, R.E4M3, R.TOKEN_HEAD, seed=47),
+                  Batch([4000], [300], 16, 2, 128, 16, R.E4M3, R.TOKEN_HEAD, seed=48), big):
+        R.check(small.run(F, workspace=ws), small.ref(device=DEV), 128, half=R.TOKEN_HEAD)
+    assert size(Batch([4000], [300], 16, 2, 128, 16, R.E4M3, R.TOKEN_HEAD, seed=48)) > size(big)
+    assert F.get_device_error() == 0
