@@ -489,6 +489,11 @@ def _check_mods(prefix_lens, alibi_slopes, batch, hq, dev):
             raise ValueError(f"alibi_slopes must hold {hq} entries")
 
 
+def _window(window):
+    """A window as the library takes it (one wider than any context leaves all of it)."""
+    return max(-1, min(window, 0x7FFFFFFF))
+
+
 def _check_tables(block_tables, seq_lens, dev):
     _want(block_tables, torch.int32, "block_tables", dev)
     _want(seq_lens, torch.int32, "seq_lens", dev)
@@ -562,9 +567,10 @@ def paged_decode_attention_mod(q, k_cache, v_cache, k_scale, v_scale, block_tabl
         rc = N.lib.fp8pa_paged_decode_attention_mod(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), block_tables.data_ptr(), max_blocks, seq_lens.data_ptr(), B, bs,
-            hq, n_kv_heads, d, fmt, scale_mode, group_size, sm_scale, window, _addr(prefix_lens),
-            logit_cap, _addr(alibi_slopes), nb, out.data_ptr(), odt, _addr(workspace),
-            0 if workspace is None else workspace.numel(), _raw_stream(stream, dev))
+            hq, n_kv_heads, d, fmt, scale_mode, group_size, sm_scale, _window(window),
+            _addr(prefix_lens), logit_cap, _addr(alibi_slopes), nb, out.data_ptr(), odt,
+            _addr(workspace), 0 if workspace is None else workspace.numel(),
+            _raw_stream(stream, dev))
     if rc:
         N.check(rc, "paged_decode_attention_mod")
     return out
@@ -619,9 +625,9 @@ def paged_prefill_attention(q, q_offsets, k_cache, v_cache, k_scale, v_scale, bl
             q.data_ptr(), q_offsets.data_ptr(), total, k_cache.data_ptr(), v_cache.data_ptr(),
             k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), max_blocks,
             seq_lens.data_ptr(), B, bs, hq, n_kv_heads, d, fmt, scale_mode, group_size, sm_scale,
-            window, _addr(prefix_lens), logit_cap, _addr(alibi_slopes), nb, out.data_ptr(), odt,
-            _addr(workspace), 0 if workspace is None else workspace.numel(),
-            _raw_stream(stream, dev))
+            _window(window), _addr(prefix_lens), logit_cap, _addr(alibi_slopes), nb,
+            out.data_ptr(), odt, _addr(workspace),
+            0 if workspace is None else workspace.numel(), _raw_stream(stream, dev))
     if rc:
         N.check(rc, "paged_prefill_attention")
     return out

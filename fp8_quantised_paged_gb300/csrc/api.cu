@@ -379,7 +379,7 @@ int prefill_shape(int total_q, int batch, int hq, int hkv, int d, int bs, int ma
     return FP8PA_ERR_BAD_SHAPE;
   if ((d != 64 && d != 128) || (bs != 16 && bs != 32 && bs != 64)) return FP8PA_ERR_UNSUPPORTED;
   if ((static_cast<long long>(total_q) + 256ll * batch) * hq >= (1ll << 31) ||
-      static_cast<long long>(bs) * max_blocks * hkv >= (1ll << 31))
+      static_cast<long long>(bs) * max_blocks * hkv > (1ll << 31) - 128)  // whole tiles
     return FP8PA_ERR_UNSUPPORTED;
   // the planner counts (256-row block, KV head, 128-token tile) units in 32 bits
   const long long blocks = static_cast<long long>(total_q) * (hq / hkv) / 256 + 1 + batch;

@@ -162,7 +162,7 @@ __device__ __forceinline__ RowBlock make_row_block(const Chunk& c, int b, int wi
   r.rows = min(kRows, c.n * G - r.row0);
   r.pA = c.L - c.n + r.row0 / G;
   r.pB = c.L - c.n + (r.row0 + r.rows - 1) / G;
-  const int wf = window > 0 ? max(r.pA - window + 1, 0) : 0;
+  const int wf = window_first(window, r.pA);
   r.np = (c.pre + kT - 1) / kT;
   r.skip = max(wf / kT - r.np, 0);
   const int last = (max(max(r.pB + 1, c.pre), 0) + kT - 1) / kT;
@@ -579,9 +579,9 @@ __device__ __forceinline__ void convert_tiles(const PrefillArgs& a, const PlanVi
       kvh = im.kvh;
       seen.pre = im.r.pre;
       table = a.block_tables + static_cast<long>(im.r.b) * a.max_blocks;
-      seen.lo = a.window > 0 ? max(im.r.pA - a.window + 1, 0) : 0;
+      seen.lo = window_first(a.window, im.r.pA);
       seen.hi = im.r.pB + 1;
-      all_lo = a.window > 0 ? max(im.r.pB - a.window + 1, 0) : 0;
+      all_lo = window_first(a.window, im.r.pB);
       all_hi = im.r.pA + 1;
     }
     if (!have) load_ids(kt + k, part, ids);
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(256) ready_kernel(const __grid_constant__ Pref
   const int b = bh / a.hkv, kvh = bh - b * a.hkv;
   bool bad_off, bad_len;
   const Chunk c = load_chunk(a, b, &bad_off, &bad_len);
-  const Seen seen{a.window > 0 ? max(c.L - c.n - a.window + 1, 0) : 0, c.L, c.pre};
+  const Seen seen{window_first(a.window, c.L - c.n), c.L, c.pre};
   // the tiles of the request's row blocks (tile 0 for rows that see nothing)
   if (c.n == 0 || (tile * kT >= seen.pre && (tile < seen.lo / kT || tile * kT >= max(c.L, 1))))
     return;
@@ -951,7 +951,7 @@ __global__ void __launch_bounds__(kThreads<READY>, 1)
         zs = fabsf(a.sm_scale) * exp2i(er - 14) * (VAR == 2 ? a.cap_in : kLog2e);
       }
       const int pos = im.r.L - im.r.n + qi;
-      const int wf = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+      const int wf = window_first(a.window, pos);
       const int pre = im.r.pre;
       // extremes over the warp's rows (positions rise with the row)
       const int pA = __shfl_sync(0xffffffffu, pos, 0), wB = __shfl_sync(0xffffffffu, wf, 31);

@@ -20,8 +20,13 @@ struct ScoreMods {
 __device__ __forceinline__ int prefix_len(const ScoreMods& m, int b, int L) {
   return m.prefix_lens ? min(max(__ldg(m.prefix_lens + b), 0), L) : 0;
 }
+// (Compared before it is subtracted: a window may be any int, and the positions of a
+// chunk longer than its request begin below zero.)
+__device__ __forceinline__ int window_first(int window, int pos) {
+  return window > 0 && pos >= window ? pos - window + 1 : 0;
+}
 __device__ __forceinline__ int window_first(const ScoreMods& m, int pos) {
-  return m.window > 0 ? max(pos - m.window + 1, 0) : 0;
+  return window_first(m.window, pos);
 }
 
 // Caps up to this take tanh as 1 - 2 / (2^x + 1), x = 2 log2(e) z / cap, whatever
