@@ -464,7 +464,8 @@ int fp8pa_paged_decode_attention_mod(const void* q, const uint8_t* k_cache,
  * Precision    codes times scales, and the softmax weights, are rounded to f16
  *              (2^-11).  Among 32 tokens of one tile, a token whose scale is
  *              2^r below the largest is off by up to 2^(r - 32) more (E5M2:
- *              2^(r - 25)), whether or not a row sees the large one.  Values of
+ *              2^(r - 25)), whether or not a row sees the large one, and one of
+ *              the row's other tiles by 2^(r - 37).  Values of
  *              V below 2^-94 are off by up to 2^-105.  A scale whose largest code
  *              passes FLT_MAX (no append writes one) may count as not finite.
  *              A row's weights keep 2^-26 of the largest where the scales of V
