@@ -182,3 +182,70 @@ def test_a_call_on_another_stream_beside_one_under_way():
             torch.cuda.synchronize()
             assert torch.equal(a, want[0]) and torch.equal(b, want[1])
     assert F.get_device_error() == 0
+
+
+def _attention_calls(F, R):
+    """A prefill and a decode over one cache as functions of q and stream."""
+    dev = "cuda:0"
+    hq, hkv, d, bs, n = 16, 2, 128, 16, 1000
+    rng = np.random.default_rng(1)
+    bt, nb = R.make_tables(rng, [n], bs)
+    cache = [t.to(dev) for t in R.make_cache(rng, nb, hkv, bs, d, R.E4M3, R.TOKEN_HEAD)]
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+    bt, lens, offsets = bt.to(dev), i32(n), i32(0, 300)
+    q = torch.randn(300, hq, d, device=dev).bfloat16()
+    return [lambda s=None: F.paged_prefill_attention(q, offsets, *cache, bt, lens, hkv, 0.09,
+                                                     window=n // 2, stream=s),
+            lambda s=None: F.paged_decode_attention_mod(q[:1], *cache, bt, lens, hkv, 0.09,
+                                                        logit_cap=20.0, stream=s)]
+
+
+@pytest.mark.gpu
+def test_calls_captured_on_a_forked_stream():
+    import serving_ref as R
+    import fp8_quantised_paged_gb300 as F
+    runs = _attention_calls(F, R)
+    want = [r().clone() for r in runs]
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        outs = [r(side) for r in runs]
+        torch.cuda.current_stream().wait_stream(side)
+        copies = [o.clone() for o in outs]
+    for _ in range(3):
+        for o in outs + copies:
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs + copies, want + want))
+    assert F.get_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_threads_that_call_at_once():
+    """Each on a stream of its own, made current by it."""
+    import threading
+
+    import serving_ref as R
+    import fp8_quantised_paged_gb300 as F
+    runs = _attention_calls(F, R)
+    want = [r().clone() for r in runs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(k):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for i in range(60):
+                out = runs[(k + i) % 2]()
+                s.synchronize()
+                if not torch.equal(out, want[(k + i) % 2]):
+                    wrong.append((k, i))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and F.get_device_error() == 0
