@@ -14,6 +14,8 @@ The main calls, hand-written CUDA kernels behind a C ABI (``include/fp8pa.h``):
   always-visible prefix, capped scores and a distance bias.
 * :func:`paged_prefill_attention` -- ragged query chunks of any length, with
   the same modifiers.
+* :func:`kv_keep_accepted`, :func:`kv_fork`, :func:`kv_resize`, :func:`kv_compact` --
+  the pages of sequences that branch.
 
 These wrappers only check torch tensors and pass their device pointers and
 the current CUDA stream to the library.  PyTorch provides memory and streams;
@@ -35,7 +37,8 @@ __all__ = ["kv_append_quant", "kv_append_quant_segment", "segment_scale_heads",
            "kv_channel_scales", "kv_channel_absmax_update",
            "kv_scales_from_absmax", "paged_decode_attention", "paged_multiquery_attention",
            "kv_append_rope", "paged_decode_attention_mod", "paged_prefill_attention",
-           "prefill_workspace_bytes", "decode_step", "decode_workspace_bytes",
+           "prefill_workspace_bytes", "KvPages", "kv_keep_accepted", "kv_fork", "kv_resize",
+           "kv_compact", "pages_workspace_bytes", "decode_step", "decode_workspace_bytes",
            "get_device_error", "set_decode_workers",
            "version", "E4M3", "E5M2", "INT8", "SCALE_TOKEN_HEAD", "SCALE_CHANNEL_STATIC",
            "SCALE_TOKEN_GROUP", "SCALE_MX_BLOCK", "SCALE_SEGMENT", "SEGMENT_TOKENS", "OUT_BF16",
@@ -631,6 +634,163 @@ def paged_prefill_attention(q, q_offsets, k_cache, v_cache, k_scale, v_scale, bl
     if rc:
         N.check(rc, "paged_prefill_attention")
     return out
+
+
+class KvPages:
+    """The arrays of a cache whose pages the page operators move: codes and scales of
+    every layer's K and V, each contiguous with the pages as its first dimension and a
+    multiple of 16 bytes a page (static channel scales are not among them).  Made once,
+    next to the cache; it holds the tensors."""
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        if not self.tensors:
+            raise ValueError("KvPages needs a tensor")
+        self.device, self.num_blocks = self.tensors[0].device, self.tensors[0].shape[0]
+        rows = None
+        for i, t in enumerate(self.tensors):
+            _need(t, t.dtype, f"tensors[{i}]", self.device)
+            if t.dim() < 2 or t.shape[0] != self.num_blocks:
+                raise ValueError(f"tensors[{i}] must hold {self.num_blocks} pages, got "
+                                 f"{tuple(t.shape)}")
+            if t.dim() == 4:
+                if rows not in (None, tuple(t.shape[1:3])):
+                    raise ValueError(f"tensors[{i}]: heads and block size differ from the "
+                                     f"others'")
+                rows = tuple(t.shape[1:3])
+        self.n_kv_heads, self.block_size = rows or (None, None)
+        # whether every array has a row per token and head
+        self.per_token = all(t.dim() == 4 for t in self.tensors)
+        n = len(self.tensors)
+        self._ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.tensors])
+        self._bytes = (ctypes.c_longlong * n)(*[t[0].numel() * t.element_size()
+                                                for t in self.tensors])
+        self._args = (ctypes.cast(self._ptrs, ctypes.c_void_p),
+                      ctypes.cast(self._bytes, ctypes.c_void_p), n)
+
+
+def pages_workspace_bytes(rows, num_blocks) -> int:
+    """Workspace bytes of kv_fork, kv_resize and kv_compact."""
+    nbytes = int(N.lib.fp8pa_pages_workspace_bytes(rows, num_blocks))
+    if nbytes == 0:
+        raise Fp8paError(N.ERR_BAD_SHAPE, "pages_workspace_bytes")
+    return nbytes
+
+
+def _pages_scratch(workspace, rows, num_blocks, dev, stream):
+    if workspace is None:
+        return _scratch(int(N.lib.fp8pa_pages_workspace_bytes(rows, num_blocks)), dev, stream)
+    _want(workspace, torch.uint8, "workspace", dev)
+    return workspace
+
+
+def _check_pages(pages, block_tables, seq_lens, ref_counts):
+    """Tables, lengths and counts of a cache's rows; returns (device, rows, max_blocks)."""
+    dev = pages.device
+    rows, max_blocks = _check_tables(block_tables, seq_lens, dev)
+    if ref_counts is not None:
+        _want(ref_counts, torch.int32, "ref_counts", dev)
+        if ref_counts.numel() != pages.num_blocks:
+            raise ValueError(f"ref_counts must hold {pages.num_blocks} entries")
+    if pages.block_size is None:
+        raise ValueError("the pages hold no [num_blocks, n_kv_heads, block_size, ...] tensor")
+    return dev, rows, max_blocks
+
+
+def kv_keep_accepted(accepted, q_offsets, block_tables, seq_lens, pages, new_lens=None,
+                     stream=None):
+    """After a drafted tree's verification: move the accepted path's cached rows to the
+    front of the tree's tokens.  accepted: int32 [B, max_accepted], the path's node
+    numbers, then -1; request b's tree is its last q_offsets[b+1] - q_offsets[b] tokens.
+    pages: a KvPages of per-token arrays.  Returns the new lengths (int32 [B]); the
+    pages behind them stay the rows' until kv_resize."""
+    dev, B, max_blocks = _check_pages(pages, block_tables, seq_lens, None)
+    if not pages.per_token:
+        raise ValueError("kv_keep_accepted needs arrays of rows per token and head")
+    _want(accepted, torch.int32, "accepted", dev)
+    _want(q_offsets, torch.int32, "q_offsets", dev)
+    if accepted.dim() != 2 or accepted.shape[0] != B or q_offsets.numel() != B + 1:
+        raise ValueError(f"accepted must be [{B}, max_accepted] and q_offsets hold {B + 1}")
+    if new_lens is None:
+        new_lens = _alloc((B,), torch.int32, dev, stream)
+    _want(new_lens, torch.int32, "new_lens", dev)
+    if new_lens.numel() != B:
+        raise ValueError(f"new_lens must hold {B} entries")
+    with _on(dev):
+        rc = N.lib.fp8pa_kv_keep_accepted(
+            accepted.data_ptr(), accepted.shape[1], q_offsets.data_ptr(), block_tables.data_ptr(),
+            max_blocks, seq_lens.data_ptr(), B, *pages._args, pages.n_kv_heads, pages.num_blocks,
+            pages.block_size, new_lens.data_ptr(), _raw_stream(stream, dev))
+    if rc:
+        N.check(rc, "kv_keep_accepted")
+    return new_lens
+
+
+def kv_fork(src_rows, dst_rows, block_tables, seq_lens, ref_counts, pages, workspace=None,
+            stream=None):
+    """Make row dst_rows[i] (of length 0) a copy of the sequence in row src_rows[i]: full
+    pages are shared, a last page that is not full is copied to a free one.  src_rows,
+    dst_rows: int32 [n]; block_tables, seq_lens and ref_counts (int32 [num_blocks], the
+    table entries that hold a page) change in place."""
+    dev, rows, max_blocks = _check_pages(pages, block_tables, seq_lens, ref_counts)
+    _want(src_rows, torch.int32, "src_rows", dev)
+    _want(dst_rows, torch.int32, "dst_rows", dev)
+    n = src_rows.numel()
+    if dst_rows.numel() != n:
+        raise ValueError("src_rows and dst_rows must be of one length")
+    workspace = _pages_scratch(workspace, rows, pages.num_blocks, dev, stream)
+    with _on(dev):
+        rc = N.lib.fp8pa_kv_fork(
+            src_rows.data_ptr(), dst_rows.data_ptr(), n, block_tables.data_ptr(), max_blocks,
+            seq_lens.data_ptr(), rows, ref_counts.data_ptr(), *pages._args, pages.num_blocks,
+            pages.block_size, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        N.check(rc, "kv_fork")
+
+
+def kv_resize(new_lens, block_tables, seq_lens, ref_counts, block_size, workspace=None,
+              stream=None):
+    """Give every row the length new_lens[r] (int32 [rows]): pages behind it are given
+    back, missing ones taken from the free pages, the lowest first; 0 frees the row.
+    block_tables, seq_lens and ref_counts change in place."""
+    _want(ref_counts, torch.int32, "ref_counts", ref_counts.device)
+    dev = ref_counts.device
+    rows, max_blocks = _check_tables(block_tables, seq_lens, dev)
+    _want(new_lens, torch.int32, "new_lens", dev)
+    if new_lens.numel() != rows:
+        raise ValueError(f"new_lens must hold {rows} entries")
+    nb = ref_counts.numel()
+    workspace = _pages_scratch(workspace, rows, nb, dev, stream)
+    with _on(dev):
+        rc = N.lib.fp8pa_kv_resize(
+            new_lens.data_ptr(), block_tables.data_ptr(), max_blocks, seq_lens.data_ptr(), rows,
+            ref_counts.data_ptr(), nb, block_size, _addr(workspace),
+            0 if workspace is None else workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        N.check(rc, "kv_resize")
+
+
+def kv_compact(block_tables, seq_lens, ref_counts, pages, page_map=None, workspace=None,
+               stream=None):
+    """Move the live pages behind the number of live ones to the free pages before it, in
+    every array; block_tables and ref_counts follow in place.  Returns page_map (int32
+    [num_blocks]): the new number of each page, -1 for a free one."""
+    dev, rows, max_blocks = _check_pages(pages, block_tables, seq_lens, ref_counts)
+    nb = pages.num_blocks
+    if page_map is None:
+        page_map = _alloc((nb,), torch.int32, dev, stream)
+    _want(page_map, torch.int32, "page_map", dev)
+    if page_map.numel() != nb:
+        raise ValueError(f"page_map must hold {nb} entries")
+    workspace = _pages_scratch(workspace, rows, nb, dev, stream)
+    with _on(dev):
+        rc = N.lib.fp8pa_kv_compact(
+            block_tables.data_ptr(), max_blocks, seq_lens.data_ptr(), rows, ref_counts.data_ptr(),
+            *pages._args, nb, pages.block_size, page_map.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        N.check(rc, "kv_compact")
+    return page_map
 
 
 def get_device_error(stream=None, device=None) -> int:

@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "pages.cuh"
 #include "score_mods.cuh"
 
 namespace fp8pa {
@@ -386,6 +387,41 @@ int prefill_shape(int total_q, int batch, int hq, int hkv, int d, int bs, int ma
   if (blocks * hkv * (static_cast<long long>(max_blocks) * bs / 128 + 1) >= (1ll << 31))
     return FP8PA_ERR_UNSUPPORTED;
   return FP8PA_OK;
+}
+
+// Whether two stretches of n words overlap, other than by being the same.
+bool partly_overlap(const int32_t* a, const int32_t* b, long long n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t bytes = static_cast<uintptr_t>(n) * 4;
+  return x != y && x < y + bytes && y < x + bytes;
+}
+
+// Validate the arguments that the page operators share; fills r, its error word excluded.
+int pages_prepare(int32_t* tables, int max_blocks, int32_t* lens, int rows, int32_t* refs,
+                  void* const* pages, const long long* page_bytes, int arrays, int num_blocks,
+                  int bs, PageRows* r) {
+  if (rows < 0 || max_blocks <= 0 || num_blocks <= 0 || bs <= 0 || arrays < 0)
+    return FP8PA_ERR_BAD_SHAPE;
+  if (static_cast<long long>(num_blocks) * bs >= (1ll << 31) ||
+      static_cast<long long>(max_blocks) * bs >= (1ll << 31) || max_blocks > (1 << 20))
+    return FP8PA_ERR_UNSUPPORTED;
+  if ((rows > 0 && (!tables || !lens)) || (arrays > 0 && (!pages || !page_bytes)))
+    return FP8PA_ERR_NULL_POINTER;
+  for (int i = 0; i < arrays; ++i) {
+    if (!pages[i]) return FP8PA_ERR_NULL_POINTER;
+    if (page_bytes[i] <= 0) return FP8PA_ERR_BAD_SHAPE;
+    if (page_bytes[i] >= (1ll << 31)) return FP8PA_ERR_UNSUPPORTED;
+    if (!aligned16(pages[i]) || page_bytes[i] % 16 != 0) return FP8PA_ERR_ALIGNMENT;
+  }
+  *r = PageRows{tables, lens, refs, max_blocks, rows, num_blocks, bs, nullptr};
+  return FP8PA_OK;
+}
+
+// The workspace of a page operator, behind its other arguments.
+int pages_workspace(const void* workspace, size_t bytes, int rows, int num_blocks) {
+  if (!workspace) return FP8PA_ERR_NULL_POINTER;
+  if (reinterpret_cast<uintptr_t>(workspace) & 3u) return FP8PA_ERR_ALIGNMENT;
+  return bytes < 4 * pages_workspace_words(rows, num_blocks) ? FP8PA_ERR_WORKSPACE : FP8PA_OK;
 }
 
 }  // namespace
@@ -790,6 +826,90 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
   a.workspace = workspace;
   a.workspace_bytes = workspace_bytes;
   return cuda_status(launch_prefill(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp8pa_pages_workspace_bytes(int rows, int num_blocks) {
+  return rows < 0 || num_blocks <= 0 ? 0 : 4 * pages_workspace_words(rows, num_blocks);
+}
+
+int fp8pa_kv_keep_accepted(const int32_t* accepted, int max_accepted, const int32_t* q_offsets,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* seq_lens, int batch, void* const* pages,
+                           const long long* page_bytes, int n_arrays, int n_kv_heads,
+                           int num_blocks, int block_size, int32_t* new_lens, void* stream) {
+  if (max_accepted <= 0 || n_kv_heads <= 0) return FP8PA_ERR_BAD_SHAPE;
+  PageRows r;
+  const int st = pages_prepare(const_cast<int32_t*>(block_tables), max_blocks_per_seq,
+                               const_cast<int32_t*>(seq_lens), batch, nullptr, pages, page_bytes,
+                               n_arrays, num_blocks, block_size, &r);
+  if (st != FP8PA_OK || batch == 0) return st;
+  if (!accepted || !q_offsets || !new_lens) return FP8PA_ERR_NULL_POINTER;
+  const long long page_rows = static_cast<long long>(n_kv_heads) * block_size;
+  for (int i = 0; i < n_arrays; ++i) {
+    if (page_bytes[i] % page_rows != 0) return FP8PA_ERR_BAD_SHAPE;
+    if (page_bytes[i] / page_rows * max_accepted >= (1ll << 31) ||
+        static_cast<long long>(n_kv_heads) * n_arrays >= (1ll << 31))
+      return FP8PA_ERR_UNSUPPORTED;
+  }
+  if (new_lens == seq_lens || partly_overlap(new_lens, seq_lens, batch))
+    return FP8PA_ERR_UNSUPPORTED;
+  r.err = device_error_ptr(static_cast<cudaStream_t>(stream), nullptr);
+  if (!r.err) return FP8PA_ERR_CUDA;
+  return cuda_status(launch_keep_accepted(accepted, max_accepted, q_offsets, r, pages, page_bytes,
+                                          n_arrays, n_kv_heads, new_lens,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+int fp8pa_kv_fork(const int32_t* src_rows, const int32_t* dst_rows, int num_forks,
+                  int32_t* block_tables, int max_blocks_per_seq, int32_t* seq_lens, int rows,
+                  int32_t* ref_counts, void* const* pages, const long long* page_bytes,
+                  int n_arrays, int num_blocks, int block_size, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  if (num_forks < 0 || num_forks > rows) return FP8PA_ERR_BAD_SHAPE;
+  PageRows r;
+  int st = pages_prepare(block_tables, max_blocks_per_seq, seq_lens, rows, ref_counts, pages,
+                         page_bytes, n_arrays, num_blocks, block_size, &r);
+  if (st != FP8PA_OK || num_forks == 0) return st;
+  if (!src_rows || !dst_rows || !ref_counts) return FP8PA_ERR_NULL_POINTER;
+  if ((st = pages_workspace(workspace, workspace_bytes, rows, num_blocks)) != FP8PA_OK) return st;
+  r.err = device_error_ptr(static_cast<cudaStream_t>(stream), nullptr);
+  if (!r.err) return FP8PA_ERR_CUDA;
+  return cuda_status(launch_fork(src_rows, dst_rows, num_forks, r, pages, page_bytes, n_arrays,
+                                 static_cast<int32_t*>(workspace),
+                                 static_cast<cudaStream_t>(stream)));
+}
+
+int fp8pa_kv_resize(const int32_t* new_lens, int32_t* block_tables, int max_blocks_per_seq,
+                    int32_t* seq_lens, int rows, int32_t* ref_counts, int num_blocks,
+                    int block_size, void* workspace, size_t workspace_bytes, void* stream) {
+  PageRows r;
+  int st = pages_prepare(block_tables, max_blocks_per_seq, seq_lens, rows, ref_counts, nullptr,
+                         nullptr, 0, num_blocks, block_size, &r);
+  if (st != FP8PA_OK || rows == 0) return st;
+  if (!new_lens || !ref_counts) return FP8PA_ERR_NULL_POINTER;
+  if (partly_overlap(new_lens, seq_lens, rows)) return FP8PA_ERR_UNSUPPORTED;
+  if ((st = pages_workspace(workspace, workspace_bytes, rows, num_blocks)) != FP8PA_OK) return st;
+  r.err = device_error_ptr(static_cast<cudaStream_t>(stream), nullptr);
+  if (!r.err) return FP8PA_ERR_CUDA;
+  return cuda_status(launch_resize(new_lens, r, static_cast<int32_t*>(workspace),
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+int fp8pa_kv_compact(int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                     int rows, int32_t* ref_counts, void* const* pages,
+                     const long long* page_bytes, int n_arrays, int num_blocks, int block_size,
+                     int32_t* page_map, void* workspace, size_t workspace_bytes, void* stream) {
+  PageRows r;
+  int st = pages_prepare(block_tables, max_blocks_per_seq, const_cast<int32_t*>(seq_lens), rows,
+                         ref_counts, pages, page_bytes, n_arrays, num_blocks, block_size, &r);
+  if (st != FP8PA_OK) return st;
+  if (!ref_counts || !page_map) return FP8PA_ERR_NULL_POINTER;
+  if ((st = pages_workspace(workspace, workspace_bytes, rows, num_blocks)) != FP8PA_OK) return st;
+  r.err = device_error_ptr(static_cast<cudaStream_t>(stream), nullptr);
+  if (!r.err) return FP8PA_ERR_CUDA;
+  return cuda_status(launch_compact(r, pages, page_bytes, n_arrays, page_map,
+                                    static_cast<int32_t*>(workspace),
+                                    static_cast<cudaStream_t>(stream)));
 }
 
 int fp8pa_selftest_bounded_wait(long long limit_cycles, void* stream) {

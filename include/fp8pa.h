@@ -80,6 +80,10 @@ extern "C" {
 #define FP8PA_DEVERR_TIMEOUT 8u      /* decode: a bounded wait on an async copy ran out (work abandoned) */
 #define FP8PA_DEVERR_POSITION 16u    /* append_rope: position outside the table (token skipped) */
 #define FP8PA_DEVERR_Q_OFFSETS 32u   /* prefill: query offsets not increasing within [0, total_q] (request skipped) */
+#define FP8PA_DEVERR_TREE 64u        /* a parent or an accepted node out of order, or too large a tree */
+#define FP8PA_DEVERR_ROW 128u        /* fork: a row outside the tables, not empty or wanted twice (fork skipped) */
+#define FP8PA_DEVERR_NO_BLOCK 256u   /* fork, resize: no free page left (fork or row left as it was) */
+#define FP8PA_DEVERR_SHARED 512u     /* resize: the row would end inside a page that others hold (row left) */
 
 /* Code formats: FP8 E4M3 and E5M2, and symmetric INT8 (the alternate KV
  * codec; FMAX = 127, integer codes in [-127, 127] stored as the byte
@@ -500,6 +504,97 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
  */
 size_t fp8pa_prefill_workspace_bytes(int total_q, int batch, int n_q_heads, int n_kv_heads,
                                      int head_dim, int block_size, int max_blocks_per_seq);
+
+/*
+ * Pages of sequences that branch.  The five calls below serve what comes with paged
+ * blocks ("DeepSeek-V4.1 512K", hotelren.com/news/5711065, sec. 3.3) once a server
+ * drafts trees of tokens, samples one prompt several times or moves sequences in and
+ * out; the pages give no formulas for it.
+ *
+ * State (device, caller-owned, shared by the calls):
+ *   block_tables  i32 [rows][max_blocks_per_seq]: a row's pages, ceil(len / block_size)
+ *                 of them; the entries behind them are -1.
+ *   seq_lens      i32 [rows].
+ *   ref_counts    i32 [num_blocks]: how many table entries hold a page.  0 is free.  A
+ *                 caller that keeps a page for itself (a prompt's cache) adds to it.
+ *   pages         the arrays of every layer that hold num_blocks pages: a host array of
+ *                 n_arrays device pointers (codes and scales of K and V; not static
+ *                 scales), and page_bytes, the bytes of one page of each: a multiple of
+ *                 16, on 16-byte aligned arrays.  Both are read during the call only.
+ * A page is shared by any number of rows while it is full; the page that a row's next
+ * token goes to is its own.  Free pages are taken with the lowest number first, for the
+ * rows in order, so every result is determined by the arguments.
+ * workspace     fp8pa_pages_workspace_bytes(rows, num_blocks), 4-byte aligned, no
+ *               initialisation; calls that share it must be stream-ordered.
+ * Limits        num_blocks * block_size < 2^31, max_blocks_per_seq <= 2^20.
+ * An entry of a table outside the pool is left alone and sets
+ * FP8PA_DEVERR_BLOCK_RANGE, a length outside [0, max_blocks_per_seq * block_size]
+ * FP8PA_DEVERR_SEQ_LEN.
+ */
+size_t fp8pa_pages_workspace_bytes(int rows, int num_blocks);
+
+/*
+ * After the verification of a drafted tree: the rows of the accepted path move to the
+ * front of the tree's tokens.  Request b's tree is its last n = q_offsets[b + 1] -
+ * q_offsets[b] cached tokens, its path the nodes accepted[b][0], accepted[b][1], ...
+ * up to the first negative entry; path node t's row moves to position seq_lens[b] - n
+ * + t in every array, and new_lens[b] = seq_lens[b] - n + (nodes of the path).
+ * accepted   i32 [batch][max_accepted]: rising node numbers below n.  A path ends
+ *            before a node that is not (FP8PA_DEVERR_TREE).
+ * pages      arrays of rows per token: a page is [n_kv_heads][block_size] rows (page_bytes
+ *            a multiple of that).  Not the scales of FP8PA_SCALE_SEGMENT, nor codes
+ *            under them: a row's scale is its page's.
+ * new_lens   i32 [batch], not overlapping seq_lens.  A request with bad offsets
+ *            (FP8PA_DEVERR_Q_OFFSETS) or a tree longer than it is is left as it was.
+ * The pages behind the new length stay the row's: fp8pa_kv_resize gives them back.
+ */
+int fp8pa_kv_keep_accepted(const int32_t* accepted, int max_accepted, const int32_t* q_offsets,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* seq_lens, int batch, void* const* pages,
+                           const long long* page_bytes, int n_arrays, int n_kv_heads,
+                           int num_blocks, int block_size, int32_t* new_lens, void* stream);
+
+/*
+ * Forks: row dst_rows[i] becomes a copy of the sequence in row src_rows[i].  Its full
+ * pages are shared (their counts rise); a last page that is not full is copied to a
+ * free page, in every array, as both rows will write to it.
+ * dst_rows   rows of length 0, each wanted once.  A fork that breaks this, or whose rows
+ *            are outside the tables, is skipped (FP8PA_DEVERR_ROW); of several that
+ *            want one row the first is made.  One that finds no free page is skipped
+ *            (FP8PA_DEVERR_NO_BLOCK).  All forks see the rows as they were before.
+ * num_forks  at most rows.
+ */
+int fp8pa_kv_fork(const int32_t* src_rows, const int32_t* dst_rows, int num_forks,
+                  int32_t* block_tables, int max_blocks_per_seq, int32_t* seq_lens, int rows,
+                  int32_t* ref_counts, void* const* pages, const long long* page_bytes,
+                  int n_arrays, int num_blocks, int block_size, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/*
+ * Gives every row the length new_lens[r]: pages behind it are given back (a count falls;
+ * at 0 the page is free), missing ones are taken from the free pages, those given back
+ * in this call among them.  0 frees a row.
+ * Where the pool runs out, the row that does not fit and every growing row behind it
+ * are left as they were (FP8PA_DEVERR_NO_BLOCK).  A row whose length would change
+ * while the page of its next token holds tokens and is another row's, too, is left
+ * (FP8PA_DEVERR_SHARED).
+ * new_lens   i32 [rows]; may be seq_lens itself (then nothing changes), otherwise not
+ *            overlapping it.
+ */
+int fp8pa_kv_resize(const int32_t* new_lens, int32_t* block_tables, int max_blocks_per_seq,
+                    int32_t* seq_lens, int rows, int32_t* ref_counts, int num_blocks,
+                    int block_size, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Compacts the pool: with n pages in use (ref_counts > 0), those numbered n and above
+ * move to the free pages below n, the lowest to the lowest, in every array; tables and
+ * counts follow.
+ * page_map   i32 [num_blocks]: the new number of each page, -1 for a free one.
+ */
+int fp8pa_kv_compact(int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                     int rows, int32_t* ref_counts, void* const* pages,
+                     const long long* page_bytes, int n_arrays, int num_blocks, int block_size,
+                     int32_t* page_map, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Size of the scratch array built into the library for
