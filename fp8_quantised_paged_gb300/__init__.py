@@ -13,7 +13,7 @@ Around them: ``kv_append_rope`` turns q and K by rotary positions on the way
 into the cache, ``paged_decode_attention_mod`` decodes with a sliding window,
 an always-visible prefix, capped scores or a distance bias, and
 ``paged_prefill_attention`` attends ragged query chunks of any length under
-the same score modifiers.  ``kv_keep_accepted``, ``kv_fork``, ``kv_resize`` and
+the same score modifiers, ``paged_tree_attention`` trees of drafted tokens.  ``kv_keep_accepted``, ``kv_fork``, ``kv_resize`` and
 ``kv_compact`` keep the pages of sequences that branch.
 
 The torch-facing wrappers live in :mod:`.binding` and are re-exported here
@@ -26,6 +26,7 @@ _API = ("kv_append_quant", "kv_append_quant_segment", "segment_scale_heads",
         "kv_scales_from_absmax", "paged_decode_attention", "paged_multiquery_attention",
         "decode_step", "kv_append_rope", "paged_decode_attention_mod", "paged_prefill_attention",
         "prefill_workspace_bytes",
+        "paged_tree_attention", "tree_workspace_bytes", "MAX_TREE",
         "KvPages", "kv_keep_accepted", "kv_fork", "kv_resize", "kv_compact",
         "pages_workspace_bytes",
         "decode_workspace_bytes", "get_device_error", "set_decode_workers", "version",

@@ -24,6 +24,7 @@ SCALE_TOKEN_HEAD, SCALE_CHANNEL_STATIC, SCALE_TOKEN_GROUP, SCALE_MX_BLOCK = 0, 1
 SCALE_SEGMENT = 4
 SEGMENT_TOKENS = 1024
 OUT_BF16, OUT_F32 = 0, 1
+MAX_TREE = 256
 
 # Every symbol the header declares, with (restype, argtypes).
 _P = ctypes.c_void_p
@@ -60,6 +61,9 @@ _SIGS = {
     "fp8pa_paged_prefill_attention": (_I, [_P, _P, _I] + [_P] * 5 + [_I, _P] + [_I] * 8 +
                                       [_F, _I, _P, _F, _P, _I, _P, _I, _P, ctypes.c_size_t, _P]),
     "fp8pa_prefill_workspace_bytes": (ctypes.c_size_t, [_I] * 7),
+    "fp8pa_paged_tree_attention": (_I, [_P, _P, _I] + [_P] * 6 + [_I, _P] + [_I] * 8 +
+                                   [_F, _I, _P, _F, _P, _I, _P, _I, _P, ctypes.c_size_t, _P]),
+    "fp8pa_tree_workspace_bytes": (ctypes.c_size_t, [_I] * 7),
     "fp8pa_pages_workspace_bytes": (ctypes.c_size_t, [_I, _I]),
     "fp8pa_kv_keep_accepted": (_I, [_P, _I, _P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P]),
     "fp8pa_kv_fork": (_I, [_P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _P,

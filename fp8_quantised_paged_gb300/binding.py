@@ -14,6 +14,7 @@ The main calls, hand-written CUDA kernels behind a C ABI (``include/fp8pa.h``):
   always-visible prefix, capped scores and a distance bias.
 * :func:`paged_prefill_attention` -- ragged query chunks of any length, with
   the same modifiers.
+* :func:`paged_tree_attention` -- trees of drafted tokens, with the same modifiers.
 * :func:`kv_keep_accepted`, :func:`kv_fork`, :func:`kv_resize`, :func:`kv_compact` --
   the pages of sequences that branch.
 
@@ -29,7 +30,8 @@ import functools
 import torch
 
 from . import _native as N
-from ._native import (E4M3, E5M2, INT8, OUT_BF16, OUT_F32, SCALE_CHANNEL_STATIC, SCALE_MX_BLOCK,
+from ._native import (E4M3, E5M2, INT8, MAX_TREE, OUT_BF16, OUT_F32, SCALE_CHANNEL_STATIC,
+                      SCALE_MX_BLOCK,
                       SCALE_SEGMENT, SCALE_TOKEN_GROUP, SCALE_TOKEN_HEAD, SEGMENT_TOKENS,
                       Fp8paError)
 
@@ -37,7 +39,8 @@ __all__ = ["kv_append_quant", "kv_append_quant_segment", "segment_scale_heads",
            "kv_channel_scales", "kv_channel_absmax_update",
            "kv_scales_from_absmax", "paged_decode_attention", "paged_multiquery_attention",
            "kv_append_rope", "paged_decode_attention_mod", "paged_prefill_attention",
-           "prefill_workspace_bytes", "KvPages", "kv_keep_accepted", "kv_fork", "kv_resize",
+           "prefill_workspace_bytes", "paged_tree_attention",
+           "tree_workspace_bytes", "MAX_TREE", "KvPages", "kv_keep_accepted", "kv_fork", "kv_resize",
            "kv_compact", "pages_workspace_bytes", "decode_step", "decode_workspace_bytes",
            "get_device_error", "set_decode_workers",
            "version", "E4M3", "E5M2", "INT8", "SCALE_TOKEN_HEAD", "SCALE_CHANNEL_STATIC",
@@ -633,6 +636,69 @@ def paged_prefill_attention(q, q_offsets, k_cache, v_cache, k_scale, v_scale, bl
             0 if workspace is None else workspace.numel(), _raw_stream(stream, dev))
     if rc:
         N.check(rc, "paged_prefill_attention")
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _tree_need(device_index, *sizes):
+    """Workspace size of a tree attention of these sizes (device_index is current)."""
+    return int(N.lib.fp8pa_tree_workspace_bytes(*sizes))
+
+
+def tree_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
+                         max_blocks_per_seq, device=None) -> int:
+    """Workspace bytes of paged_tree_attention for these sizes; enough for every smaller
+    batch of the same heads."""
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        nbytes = int(N.lib.fp8pa_tree_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads,
+                                                      head_dim, block_size, max_blocks_per_seq))
+    if nbytes == 0:
+        raise Fp8paError(N.ERR_UNSUPPORTED, "tree_workspace_bytes")
+    return nbytes
+
+
+def paged_tree_attention(q, q_offsets, parents, k_cache, v_cache, k_scale, v_scale, block_tables,
+                         seq_lens, n_kv_heads, sm_scale, window=0, prefix_lens=None,
+                         logit_cap=0.0, alibi_slopes=None, fmt=E4M3, scale_mode=SCALE_TOKEN_HEAD,
+                         group_size=64, out=None, out_dtype=None, workspace=None, stream=None):
+    """Attention for trees of drafted tokens over the paged cache.  q: bf16 [total_q, Hq, D],
+    request b's nodes in rows q_offsets[b] .. q_offsets[b+1]-1 (int32 [B + 1]), already
+    appended as its last tokens; seq_lens counts them.  parents: int32 [total_q], a node's
+    parent within its tree (a smaller number), -1 for a child of the last token ahead of
+    the tree.  A node sees the tokens ahead of the tree, its ancestors and itself; score
+    modifiers as paged_prefill_attention, counted along its line.  At most MAX_TREE nodes a
+    request.  Rows outside every tree are left as they were.  Returns out [total_q, Hq, D]."""
+    _need(q, torch.bfloat16, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [total_q, n_q_heads, head_dim]")
+    dev = q.device
+    total, hq, d = q.shape
+    B, max_blocks = _check_tables(block_tables, seq_lens, dev)
+    _want(q_offsets, torch.int32, "q_offsets", dev)
+    _want(parents, torch.int32, "parents", dev)
+    if q_offsets.numel() != B + 1 or parents.numel() != total:
+        raise ValueError(f"q_offsets must hold {B + 1} entries and parents {total}")
+    if v_cache is None or v_scale is None:
+        raise ValueError("v_cache and v_scale are required")
+    nb, bs = _check_cache(k_cache, v_cache, k_scale, v_scale, n_kv_heads, d, scale_mode,
+                          group_size, dev)
+    _check_mods(prefix_lens, alibi_slopes, B, hq, dev)
+    out, odt = _output(out, (total, hq, d), out_dtype, dev, stream)
+    with _on(dev):
+        if workspace is None:
+            workspace = _scratch(_tree_need(dev.index, total, B, hq, n_kv_heads, d, bs,
+                                            max_blocks), dev, stream)
+        else:
+            _want(workspace, torch.uint8, "workspace", dev)
+        rc = N.lib.fp8pa_paged_tree_attention(
+            q.data_ptr(), q_offsets.data_ptr(), total, parents.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(),
+            max_blocks, seq_lens.data_ptr(), B, bs, hq, n_kv_heads, d, fmt, scale_mode,
+            group_size, sm_scale, _window(window), _addr(prefix_lens), logit_cap,
+            _addr(alibi_slopes), nb, out.data_ptr(), odt, _addr(workspace),
+            0 if workspace is None else workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        N.check(rc, "paged_tree_attention")
     return out
 
 

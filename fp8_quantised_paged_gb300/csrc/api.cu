@@ -389,6 +389,71 @@ int prefill_shape(int total_q, int batch, int hq, int hkv, int d, int bs, int ma
   return FP8PA_OK;
 }
 
+// Validate the arguments that the prefill and the tree attention share and fill a, the
+// size of the workspace excluded.  FP8PA_OK with nothing filled where there is nothing to
+// launch (batch or total_q 0).
+int prefill_prepare(const void* q, const int32_t* q_offsets, int total_q, const uint8_t* k_cache,
+                    const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                    int batch, int block_size, int n_q_heads, int n_kv_heads, int head_dim,
+                    int fmt, int scale_mode, int group_size, float sm_scale, int window,
+                    const int32_t* prefix_lens, float logit_cap, const float* alibi_slopes,
+                    int num_blocks, void* out, int out_dtype, void* workspace,
+                    size_t workspace_bytes, cudaStream_t stream, PrefillArgs* args, int* dev) {
+  if (window < 0) return FP8PA_ERR_BAD_SHAPE;
+  int st = prefill_shape(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
+                         max_blocks_per_seq);
+  if (st != FP8PA_OK) return st;
+  // formats, scale modes, block sizes and pool sizes as the decode's GQA layout
+  st = decode_path(1, 1, n_kv_heads, n_kv_heads, head_dim, head_dim, block_size,
+                   max_blocks_per_seq, fmt, scale_mode, group_size, num_blocks, out_dtype)
+           .status;
+  if (st != FP8PA_OK) return st;
+  if (!(logit_cap >= 0.f) || logit_cap > FLT_MAX) return FP8PA_ERR_UNSUPPORTED;
+  if (batch == 0 || total_q == 0) return FP8PA_OK;
+  if (!q || !q_offsets || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables ||
+      !seq_lens || !out || !workspace)
+    return FP8PA_ERR_NULL_POINTER;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) ||
+      !aligned16(v_scale) || !aligned16(workspace) || !aligned16(out))
+    return FP8PA_ERR_ALIGNMENT;
+  PrefillArgs& a = *args;
+  a = PrefillArgs{};
+  a.err = device_error_ptr(stream, dev);
+  if (!a.err) return FP8PA_ERR_CUDA;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_offsets = q_offsets;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.prefix_lens = prefix_lens;
+  a.slopes = alibi_slopes;
+  a.cap = kernel_cap(logit_cap);
+  a.sm_scale = sm_scale;
+  a.window = window;
+  a.total_q = total_q;
+  a.batch = batch;
+  a.hq = n_q_heads;
+  a.hkv = n_kv_heads;
+  a.G = n_q_heads / n_kv_heads;
+  a.d = head_dim;
+  a.bs = block_size;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.fmt = fmt;
+  a.mode = scale_mode;
+  a.gs = group_size;
+  a.hp = segment_scale_heads(n_kv_heads);
+  a.out_f32 = out_dtype == FP8PA_OUT_F32;
+  a.out = out;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  return FP8PA_OK;
+}
+
 // Whether two stretches of n words overlap, other than by being the same.
 bool partly_overlap(const int32_t* a, const int32_t* b, long long n) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -770,62 +835,57 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
                                   const float* alibi_slopes, int num_blocks, void* out,
                                   int out_dtype, void* workspace, size_t workspace_bytes,
                                   void* stream) {
-  if (window < 0) return FP8PA_ERR_BAD_SHAPE;
-  int st = prefill_shape(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
-                         max_blocks_per_seq);
-  if (st != FP8PA_OK) return st;
-  // formats, scale modes, block sizes and pool sizes as the decode's GQA layout
-  st = decode_path(1, 1, n_kv_heads, n_kv_heads, head_dim, head_dim, block_size,
-                   max_blocks_per_seq, fmt, scale_mode, group_size, num_blocks, out_dtype)
-           .status;
-  if (st != FP8PA_OK) return st;
-  if (!(logit_cap >= 0.f) || logit_cap > FLT_MAX) return FP8PA_ERR_UNSUPPORTED;
-  if (batch == 0 || total_q == 0) return FP8PA_OK;
-  if (!q || !q_offsets || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables ||
-      !seq_lens || !out || !workspace)
-    return FP8PA_ERR_NULL_POINTER;
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) ||
-      !aligned16(v_scale) || !aligned16(workspace) || !aligned16(out))
-    return FP8PA_ERR_ALIGNMENT;
+  PrefillArgs a;
   int dev = 0;
-  PrefillArgs a{};
-  a.err = device_error_ptr(static_cast<cudaStream_t>(stream), &dev);
-  if (!a.err) return FP8PA_ERR_CUDA;
+  const int st = prefill_prepare(q, q_offsets, total_q, k_cache, v_cache, k_scale, v_scale,
+                                 block_tables, max_blocks_per_seq, seq_lens, batch, block_size,
+                                 n_q_heads, n_kv_heads, head_dim, fmt, scale_mode, group_size,
+                                 sm_scale, window, prefix_lens, logit_cap, alibi_slopes,
+                                 num_blocks, out, out_dtype, workspace, workspace_bytes,
+                                 static_cast<cudaStream_t>(stream), &a, &dev);
+  if (st != FP8PA_OK || batch == 0 || total_q == 0) return st;
   if (workspace_bytes <
       prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
                               max_blocks_per_seq, dev, true))
     return FP8PA_ERR_WORKSPACE;
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_offsets = q_offsets;
-  a.k_cache = k_cache;
-  a.v_cache = v_cache;
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
-  a.block_tables = block_tables;
-  a.seq_lens = seq_lens;
-  a.prefix_lens = prefix_lens;
-  a.slopes = alibi_slopes;
-  a.cap = kernel_cap(logit_cap);
-  a.sm_scale = sm_scale;
-  a.window = window;
-  a.total_q = total_q;
-  a.batch = batch;
-  a.hq = n_q_heads;
-  a.hkv = n_kv_heads;
-  a.G = n_q_heads / n_kv_heads;
-  a.d = head_dim;
-  a.bs = block_size;
-  a.max_blocks = max_blocks_per_seq;
-  a.num_blocks = num_blocks;
-  a.fmt = fmt;
-  a.mode = scale_mode;
-  a.gs = group_size;
-  a.hp = segment_scale_heads(n_kv_heads);
-  a.out_f32 = out_dtype == FP8PA_OUT_F32;
-  a.out = out;
-  a.workspace = workspace;
-  a.workspace_bytes = workspace_bytes;
   return cuda_status(launch_prefill(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp8pa_tree_workspace_bytes(int total_q, int batch, int n_q_heads, int n_kv_heads,
+                                  int head_dim, int block_size, int max_blocks_per_seq) {
+  if (prefill_shape(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
+                    max_blocks_per_seq) != FP8PA_OK)
+    return 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return tree_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, dev);
+}
+
+int fp8pa_paged_tree_attention(const void* q, const int32_t* q_offsets, int total_q,
+                               const int32_t* parents, const uint8_t* k_cache,
+                               const uint8_t* v_cache, const float* k_scale,
+                               const float* v_scale, const int32_t* block_tables,
+                               int max_blocks_per_seq, const int32_t* seq_lens, int batch,
+                               int block_size, int n_q_heads, int n_kv_heads, int head_dim,
+                               int fmt, int scale_mode, int group_size, float sm_scale,
+                               int window, const int32_t* prefix_lens, float logit_cap,
+                               const float* alibi_slopes, int num_blocks, void* out,
+                               int out_dtype, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  if (!parents && batch > 0 && total_q > 0) return FP8PA_ERR_NULL_POINTER;
+  PrefillArgs a;
+  int dev = 0;
+  const int st = prefill_prepare(q, q_offsets, total_q, k_cache, v_cache, k_scale, v_scale,
+                                 block_tables, max_blocks_per_seq, seq_lens, batch, block_size,
+                                 n_q_heads, n_kv_heads, head_dim, fmt, scale_mode, group_size,
+                                 sm_scale, window, prefix_lens, logit_cap, alibi_slopes,
+                                 num_blocks, out, out_dtype, workspace, workspace_bytes,
+                                 static_cast<cudaStream_t>(stream), &a, &dev);
+  if (st != FP8PA_OK || batch == 0 || total_q == 0) return st;
+  if (workspace_bytes <
+      tree_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, dev))
+    return FP8PA_ERR_WORKSPACE;
+  return cuda_status(launch_tree(a, parents, static_cast<cudaStream_t>(stream)));
 }
 
 size_t fp8pa_pages_workspace_bytes(int rows, int num_blocks) {

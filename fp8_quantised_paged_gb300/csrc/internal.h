@@ -215,6 +215,10 @@ size_t prefill_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, i
                                int max_blocks, int device, bool least);
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 
+// Attention for trees of drafted tokens (tree.cu): a prefill's arguments and the parents.
+size_t tree_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, int device);
+cudaError_t launch_tree(const PrefillArgs& a, const int32_t* parents, cudaStream_t stream);
+
 // The tensor-core kernel for a causal chunk over the grouped-query layout:
 // FP8 codes, per-token scales, head_dim 128, G x q_len = 16 or 32 columns.
 bool gqa_tc_eligible(int fmt, int mode, int d, int dv, int bs, int hq, int hkv, int qlen);

@@ -506,6 +506,54 @@ size_t fp8pa_prefill_workspace_bytes(int total_q, int batch, int n_q_heads, int 
                                      int head_dim, int block_size, int max_blocks_per_seq);
 
 /*
+ * Attention for trees of drafted tokens over the paged cache, as a server makes it that
+ * verifies several drafts at once (speculative decoding: "Llama 3 70B FP8 deployment",
+ * dpshk.com/news/5605006, sec. 4.3, which names one line of drafts; the tree is an
+ * addition).  Request b's n = q_offsets[b + 1] - q_offsets[b] drafted tokens, its tree's
+ * nodes, were appended first (parents before children) and are its last n cached tokens.
+ * A node sees the seq_lens[b] - n tokens ahead of the tree, its ancestors and itself,
+ * and no other node.
+ *
+ * parents      i32 [total_q]: the number of a node's parent within its tree, -1 for a
+ *              child of the last token ahead of the tree.  A parent that is not in [-1,
+ *              own number) sets FP8PA_DEVERR_TREE and counts as -1.
+ * Score modifiers as above, with a node's position the number of tokens on its line:
+ * seq_lens[b] - n + depth (0 for a child of the last token ahead).  So the window and
+ * the distance bias count along a node's own line.  The prefix ends where the tree
+ * begins.
+ * A tree of more than FP8PA_MAX_TREE nodes (FP8PA_DEVERR_TREE), or one longer than its
+ * request or whose length is outside [0, cap] (FP8PA_DEVERR_SEQ_LEN), is skipped, as are
+ * bad offsets: its rows are left as they were, like rows outside every tree.
+ * Precision    fp32 scores of q to 2^-17 of a row's largest element (CHANNEL_STATIC: of q
+ *              times the scales to 2^-9 of each); the softmax weights, times V's scale,
+ *              are rounded to f16 (2^-11).  Values of V below 2^-94, and scales that lie
+ *              far apart, as in the prefill.
+ * workspace    fp8pa_tree_workspace_bytes(), 16-byte aligned; no initialisation; calls
+ *              that share it must be stream-ordered.  It grows with total_q and batch
+ *              alone: a larger batch's serves every smaller one of the same heads.
+ * Other arguments, limits and errors as fp8pa_paged_prefill_attention.
+ */
+#define FP8PA_MAX_TREE 256
+int fp8pa_paged_tree_attention(const void* q, const int32_t* q_offsets, int total_q,
+                               const int32_t* parents, const uint8_t* k_cache,
+                               const uint8_t* v_cache, const float* k_scale,
+                               const float* v_scale, const int32_t* block_tables,
+                               int max_blocks_per_seq, const int32_t* seq_lens, int batch,
+                               int block_size, int n_q_heads, int n_kv_heads, int head_dim,
+                               int fmt, int scale_mode, int group_size, float sm_scale,
+                               int window, const int32_t* prefix_lens, float logit_cap,
+                               const float* alibi_slopes, int num_blocks, void* out,
+                               int out_dtype, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
+ * Bytes of device workspace fp8pa_paged_tree_attention needs for these sizes on the
+ * current device; 0 if they are rejected.
+ */
+size_t fp8pa_tree_workspace_bytes(int total_q, int batch, int n_q_heads, int n_kv_heads,
+                                  int head_dim, int block_size, int max_blocks_per_seq);
+
+/*
  * Pages of sequences that branch.  The five calls below serve what comes with paged
  * blocks ("DeepSeek-V4.1 512K", hotelren.com/news/5711065, sec. 3.3) once a server
  * drafts trees of tokens, samples one prompt several times or moves sequences in and
