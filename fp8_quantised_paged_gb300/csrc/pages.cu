@@ -8,12 +8,12 @@
 #include "pages.cuh"
 
 #include "common.cuh"
+#include "scan.cuh"
 
 namespace fp8pa {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
 constexpr int kWarps = kPlanThreads / 32;
 constexpr int kChunk = 2048;  // bytes that a warp copies at a time: four 16-byte loads a lane
 constexpr int kCopyThreads = 256;
@@ -29,33 +29,6 @@ __device__ __forceinline__ bool good_page(const PageRows& r, int page) {
 }
 __device__ __forceinline__ int32_t* row_of(const PageRows& r, int row) {
   return r.tables + static_cast<long>(row) * r.max_blocks;
-}
-
-// Exclusive scan of one int per thread over the CTA; returns the total.
-__device__ __forceinline__ int cta_scan(int x, int* excl, int* s_warp) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int v = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += t;
-  }
-  if (lane == 31) s_warp[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    int w = s_warp[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += t;
-    }
-    s_warp[lane] = w;
-  }
-  __syncthreads();
-  *excl = v - x + (warp ? s_warp[warp - 1] : 0);
-  const int total = s_warp[kWarps - 1];
-  __syncthreads();
-  return total;
 }
 
 // The counts of a stretch of pages, a bit per page that is free.  A warp holds kSpan
@@ -92,7 +65,7 @@ __device__ __forceinline__ int take_free(const PageRows& r, int want, int32_t* l
 #pragma unroll
     for (int i = 0; i < kSpan; ++i) n += __popc(f.w[i]);
     int at;
-    const int total = cta_scan(lane == 0 ? n : 0, &at, s_warp);
+    const int total = block_scan(lane == 0 ? n : 0, &at, s_warp);
     at = got + __shfl_sync(0xffffffffu, at, 0);
 #pragma unroll
     for (int i = 0; i < kSpan; ++i) {
@@ -294,7 +267,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const int32_t* 
       }
     }
     int at;
-    const int total = cta_scan(what == 0 ? 1 : 0, &at, s_warp);
+    const int total = block_scan(what == 0 ? 1 : 0, &at, s_warp);
     if (i < forks) page[i] = what == 0 ? want + at : what;
     want += total;
   }
@@ -411,7 +384,7 @@ __global__ void __launch_bounds__(kPlanThreads) resize_grow_kernel(const int32_t
     if (i < r.rows && target[i] != kSkip) n = max(target[i] - pages_of(r.lens[i], r.bs), 0);
     int at;
     // (a chunk's sum stays below 1024 (2^20 + 1): larger growths fit no pool of fewer pages)
-    const int total = cta_scan(min(n, min(most, 1 << 20)), &at, s_warp);
+    const int total = block_scan(min(n, min(most, 1 << 20)), &at, s_warp);
     if (i < r.rows) prefix[i] = min(want + at, most);
     want = min(want + total, most);
   }
@@ -459,7 +432,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PageRo
     for (int i = 0; i < kSpan; ++i) n += __popc(f.w[i]);
   }
   int at;
-  const int live = r.num_blocks - cta_scan(lane == 0 ? n : 0, &at, s_warp);
+  const int live = r.num_blocks - block_scan(lane == 0 ? n : 0, &at, s_warp);
   // free pages below `live`, and live pages from there on, are as many
   int lows = 0, highs = 0;
   for (long long from = 0; from < r.num_blocks; from += kStretch) {
@@ -476,8 +449,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PageRo
       nh += __popc(~f.w[i] & in & ~lo);
     }
     int al, ah;
-    const int tl = cta_scan(lane == 0 ? nl : 0, &al, s_warp);
-    const int th = cta_scan(lane == 0 ? nh : 0, &ah, s_warp);
+    const int tl = block_scan(lane == 0 ? nl : 0, &al, s_warp);
+    const int th = block_scan(lane == 0 ? nh : 0, &ah, s_warp);
     al = lows + __shfl_sync(0xffffffffu, al, 0);
     ah = highs + __shfl_sync(0xffffffffu, ah, 0);
 #pragma unroll

@@ -1,16 +1,11 @@
 // prefill.cu -- the planner, the merge and the launch of the prefill attention,
 // whose method prefill.cuh states.
 #include "prefill.cuh"
+#include "ranges.cuh"
 
 namespace fp8pa {
 
 namespace {
-
-__host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
-inline int block_bound(int total_q, int batch, int G) {
-  return static_cast<int>((static_cast<long long>(total_q) * G + kRows - 1) / kRows) + batch;
-}
 
 // Whether tiles are converted once for all row blocks (ready_kernel) instead of by
 // each: where a request has kReadyBlocks of them or more on average, and the tiles
@@ -67,46 +62,6 @@ inline size_t plan_layout(char* ws, int total_q, int batch, int G, int hkv, int 
   return at;
 }
 
-constexpr int kPlanThreads = 1024;
-
-// Exclusive scan of one int per thread over the CTA; returns the total.
-__device__ __forceinline__ int block_scan(int x, int* excl, int* s_warp) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int v = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += t;
-  }
-  if (lane == 31) s_warp[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    int w = s_warp[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += t;
-    }
-    s_warp[lane] = w;
-  }
-  __syncthreads();
-  *excl = v - x + (warp ? s_warp[warp - 1] : 0);
-  const int total = s_warp[kPlanThreads / 32 - 1];
-  __syncthreads();
-  return total;
-}
-
-// Largest i in [0, n) with a[i] <= x (a nondecreasing, a[0] <= x).
-__device__ __forceinline__ int last_le(const int* a, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PrefillArgs a,
                                                                     const PlanView v, int ranges) {
   __shared__ int s_warp[kPlanThreads / 32];
@@ -154,30 +109,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
   }
   if (tid == 0) v.rb_pre[blocks] = carry;
   __syncthreads();
-  const int U = carry * a.hkv;
-  const int upw = max(1, (U + ranges - 1) / ranges);
-  if (tid == 0) {
-    v.head[0] = U;
-    v.head[1] = upw;
-  }
-  for (int w = tid; w <= ranges; w += kPlanThreads) {
-    const long long want = static_cast<long long>(w) * upw;
-    int u = want < U ? static_cast<int>(want) : U, it = blocks * a.hkv;
-    if (u < U) {
-      const int rb = last_le(v.rb_pre, blocks, u / a.hkv);
-      const int pre = v.rb_pre[rb], c = v.rb_pre[rb + 1] - pre;
-      const int h = (u - pre * a.hkv) / c, f = pre * a.hkv + h * c;
-      it = rb * a.hkv + h;
-      if (u - f < kSnap) {
-        u = f;
-      } else if (f + c - u < kSnap) {
-        u = f + c;
-        ++it;
-      }
-    }
-    v.start[w] = u;
-    v.item[w] = it;
-  }
+  cut_ranges(v, blocks, carry, a.hkv, ranges);
 }
 
 // ---------------------------------------------------------------- merge
@@ -289,10 +221,21 @@ cudaError_t launch_prefill(const PrefillArgs& args, cudaStream_t stream) {
   cfg.blockDim = dim3(static_cast<unsigned>(fn.threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(fn.smem);
   if ((e = cudaLaunchKernelEx(&cfg, fn.attend, a, pv)) != cudaSuccess) return e;
+  return launch_merge_ranges(a, pv, ranges, stream);
+}
+
+cudaError_t launch_merge_ranges(const PrefillArgs& a, const PlanView& pv, int ranges,
+                                cudaStream_t stream) {
   if (ranges < 2) return cudaSuccess;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(ranges - 1), kRows / kMergeRows);
   cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
   return a.d == 128 ? cudaLaunchKernelEx(&cfg, prefill_merge_kernel<128>, a, pv, ranges)
                     : cudaLaunchKernelEx(&cfg, prefill_merge_kernel<64>, a, pv, ranges);
 }

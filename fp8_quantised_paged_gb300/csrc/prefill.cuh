@@ -93,6 +93,9 @@ struct PrefillKernels {
 };
 PrefillKernels pick_prefill_d64(int fmt, int var, bool mx, bool ready);
 PrefillKernels pick_prefill_d128(int fmt, int var, bool mx, bool ready);
+// Folds the pieces of items that a cut between `ranges` ranges divides.
+cudaError_t launch_merge_ranges(const PrefillArgs& a, const PlanView& pv, int ranges,
+                                cudaStream_t stream);
 
 namespace {
 

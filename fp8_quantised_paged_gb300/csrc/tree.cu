@@ -1,152 +1,205 @@
-// tree.cu -- attention for trees of drafted tokens over the paged cache.
-//
-//   z_j = sm_scale q_i . k^_j;  z_j = cap tanh(z_j / cap);  z_j -= slope (pos_i - pos_j)
-//   out_i = sum_j softmax(z)_j v^_j  over the tokens ahead of the tree (as the window and
-//   the prefix leave them) and the nodes on i's line, itself among them
-//
-// The plain kernel: a warp per (node, query head) walks its visible tokens one at a time,
-// a lane holding head_dim / 32 dims, with the running maximum and sum of the softmax.
-#include "common.cuh"
-#include "internal.h"
-#include "score_mods.cuh"
+// tree.cu -- the planner and the launch of the tree attention, whose method tree.cuh
+// states.
+#include "ranges.cuh"
+#include "tree.cuh"
 
 namespace fp8pa {
 
 namespace {
 
-constexpr int kMaxTree = FP8PA_MAX_TREE;
-
-__device__ __forceinline__ float code_value(int fmt, uint8_t c) {
-  uint32_t r;
-  if (fmt == FP8PA_INT8) return static_cast<float>(c) - 128.f;
-  if (fmt == FP8PA_E4M3) r = codes2_to_f16x2<FP8PA_E4M3>(c);
-  else r = codes2_to_f16x2<FP8PA_E5M2>(c);
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(r & 0xFFFFu)));
+// A request's tree and its visible extent; n is 0 for a request that is skipped, `flag`
+// why.
+__device__ __forceinline__ Chunk load_tree(const PrefillArgs& a, int b, uint32_t* flag) {
+  bool bad_off, bad_len;
+  Chunk c = load_chunk(a, b, &bad_off, &bad_len);
+  *flag = bad_off ? FP8PA_DEVERR_Q_OFFSETS
+                  : (c.n > kMaxTree ? FP8PA_DEVERR_TREE : (bad_len ? FP8PA_DEVERR_SEQ_LEN : 0u));
+  if (*flag) c.n = 0;
+  c.pre = min(c.pre, c.L - c.n);
+  return c;
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) tree_plain_kernel(const PrefillArgs a,
-                                                         const int32_t* parents) {
-  constexpr int N = D / 32;
+// Row block t of a request.  Any node may see the whole context, and the window of a node
+// on the first level begins earliest.
+__device__ __forceinline__ RowBlock make_tree_block(const Chunk& c, int b, int window, int G,
+                                                    int t) {
+  RowBlock r;
+  r.b = b;
+  r.qlo = c.qlo;
+  r.n = c.n;
+  r.L = c.L;
+  r.pre = c.pre;
+  r.row0 = t * kRows;
+  r.rows = min(kRows, c.n * G - r.row0);
+  r.pA = c.L - c.n;  // tokens ahead of the tree
+  r.pB = c.L - 1;
+  r.np = (c.pre + kT - 1) / kT;
+  r.skip = max(window_first(window, r.pA) / kT - r.np, 0);
+  r.count = (c.L + kT - 1) / kT - r.skip;
+  return r;
+}
+
+// CTA 0 plans; CTA 1 + b writes the lines of request b's nodes, a thread each.
+__global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const PrefillArgs a,
+                                                                 const PlanView v,
+                                                                 const int32_t* parents,
+                                                                 uint32_t* lines, int32_t* depths,
+                                                                 int ranges) {
+  __shared__ int s_warp[kPlanThreads / 32];
+  __shared__ int s_parent[kMaxTree];
+  __shared__ uint32_t s_line[kMaxTree][kLineWords];
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const long wid = static_cast<long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int row = static_cast<int>(wid / a.hq), h = static_cast<int>(wid % a.hq);
-  if (row >= a.total_q) return;
-  // the request: the last one whose rows hold this one
-  int b = -1, lo = 0, hi = 0;
-  for (int i = 0; i < a.batch; ++i) {
-    lo = __ldg(a.q_offsets + i);
-    hi = __ldg(a.q_offsets + i + 1);
-    if (lo < 0 || hi < lo || hi > a.total_q) {
-      if (wid == 0 && lane == 0) raise_error(a.err, FP8PA_DEVERR_Q_OFFSETS);
-      continue;
+  const int tid = threadIdx.x;
+  uint32_t flag;
+  if (blockIdx.x > 0) {
+    const Chunk c = load_tree(a, blockIdx.x - 1, &flag);
+    if (tid < c.n) {
+      int p = __ldg(parents + c.qlo + tid);
+      if (p < -1 || p >= tid) {
+        raise_error(a.err, FP8PA_DEVERR_TREE);
+        p = -1;
+      }
+      s_parent[tid] = p;
+#pragma unroll
+      for (int i = 0; i < kLineWords; ++i) s_line[tid][i] = 0;
     }
-    if (row >= lo && row < hi) {
-      b = i;
-      if (wid != 0) break;
+    __syncthreads();
+    if (tid < c.n) {
+      int depth = -1;
+      for (int i = tid; i >= 0; i = s_parent[i])  // parents come first
+        if (++depth < a.window || a.window == 0) s_line[tid][i >> 5] |= 1u << (i & 31);
+      depths[c.qlo + tid] = depth;
     }
-  }
-  if (b < 0) return;
-  lo = __ldg(a.q_offsets + b);
-  hi = __ldg(a.q_offsets + b + 1);
-  const int n = hi - lo, L = __ldg(a.seq_lens + b);
-  if (n > kMaxTree) {
-    if (lane == 0) raise_error(a.err, FP8PA_DEVERR_TREE);
+    __syncthreads();
+    for (int i = tid; i < c.n * kLineWords; i += kPlanThreads)
+      lines[static_cast<long>(c.qlo) * kLineWords + i] = s_line[i / kLineWords][i % kLineWords];
     return;
   }
-  if (L < n || L > a.max_blocks * a.bs) {
-    if (lane == 0) raise_error(a.err, FP8PA_DEVERR_SEQ_LEN);
-    return;
+  int carry = 0;
+  for (int base = 0; base < a.batch; base += kPlanThreads) {
+    const int b = base + tid;
+    int n = 0;
+    if (b < a.batch) {
+      const Chunk c = load_tree(a, b, &flag);
+      if (flag) raise_error(a.err, flag);
+      // overlapping or repeated offsets cannot add blocks beyond the bound
+      n = static_cast<int>((static_cast<long long>(c.n) * a.G + kRows - 1) / kRows);
+    }
+    int ex;
+    const int total = block_scan(n, &ex, s_warp);
+    if (b < a.batch) v.rbase[b] = min(carry + ex, v.blocks);
+    carry = min(carry + total, v.blocks);
   }
-  const int ctx = L - n, kvh = h / a.G;
-  const int32_t* par = parents + lo;
-  auto parent = [&](int i) {
-    const int p = __ldg(par + i);
-    if (p >= -1 && p < i) return p;
-    if (lane == 0) raise_error(a.err, FP8PA_DEVERR_TREE);
-    return -1;
+  if (tid == 0) v.rbase[a.batch] = carry;
+  __syncthreads();
+  const int blocks = carry;
+  carry = 0;
+  for (int base = 0; base < blocks; base += kPlanThreads) {
+    const int i = base + tid;
+    int n = 0;
+    if (i < blocks) {
+      const int b = last_le(v.rbase, a.batch, i);
+      const Chunk c = load_tree(a, b, &flag);
+      const RowBlock r = make_tree_block(c, b, a.window, a.G, i - v.rbase[b]);
+      n = r.count;
+      v.rb[3 * i] = make_int4(r.b, r.qlo, r.n, r.L);
+      v.rb[3 * i + 1] = make_int4(r.pre, r.row0, r.rows, r.np);
+      v.rb[3 * i + 2] = make_int4(r.skip, r.count, r.pA, r.pB);
+    }
+    int ex;
+    const int total = block_scan(n, &ex, s_warp);
+    if (i < blocks) v.rb_pre[i] = carry + ex;
+    carry += total;
+  }
+  if (tid == 0) v.rb_pre[blocks] = carry;
+  __syncthreads();
+  cut_ranges(v, blocks, carry, a.hkv, ranges);
+}
+
+size_t tree_layout(char* ws, int total_q, int batch, int G, int d, int ranges, PlanView* v,
+                   uint32_t** line, int32_t** depth) {
+  const int nb = block_bound(total_q, batch, G);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* p = ws + at;
+    at += align256(bytes);
+    return p;
   };
-  int depth = 0;
-  for (int i = parent(row - lo); i >= 0; i = parent(i)) ++depth;
-  const int pos = ctx + depth;
-  const ScoreMods mods{a.prefix_lens, a.slopes, a.cap, a.window};
-  const int pre = prefix_len(mods, b, ctx), wf = window_first(a.window, pos);
-  const float slope = a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
-  float q[N], kcs[N], vcs[N], o[N], m = -1e30f, l = 0.f;
-#pragma unroll
-  for (int x = 0; x < N; ++x) {
-    const int d = lane * N + x;
-    q[x] = __uint_as_float(static_cast<uint32_t>(
-               __ldg(a.q + (static_cast<long>(row) * a.hq + h) * D + d)) << 16);
-    const bool st = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
-    kcs[x] = st ? __ldg(a.k_scale + static_cast<long>(kvh) * D + d) : 1.f;
-    vcs[x] = st ? __ldg(a.v_scale + static_cast<long>(kvh) * D + d) : 1.f;
-    o[x] = 0.f;
+  PlanView t{};
+  t.head = reinterpret_cast<int*>(take(16));
+  t.rbase = reinterpret_cast<int*>(take(sizeof(int) * (batch + 1)));
+  t.rb = reinterpret_cast<int4*>(take(sizeof(int4) * 3 * nb));
+  t.rb_pre = reinterpret_cast<int*>(take(sizeof(int) * (nb + 1)));
+  t.start = reinterpret_cast<int*>(take(sizeof(int) * (ranges + 1)));
+  t.item = reinterpret_cast<int*>(take(sizeof(int) * (ranges + 1)));
+  t.ml = reinterpret_cast<float2*>(take(sizeof(float2) * 2 * ranges * kRows));
+  t.o = reinterpret_cast<float*>(take(sizeof(float) * 2 * ranges * kRows * d));
+  t.blocks = nb;
+  char* l = take(sizeof(uint32_t) * kLineWords * total_q);
+  char* e = take(sizeof(int32_t) * total_q);
+  if (v) {
+    *v = t;
+    *line = reinterpret_cast<uint32_t*>(l);
+    *depth = reinterpret_cast<int32_t*>(e);
   }
-  const int32_t* table = a.block_tables + static_cast<long>(b) * a.max_blocks;
-  auto see = [&](int j, int pj) {  // cached token j, at position pj
-    const int page = __ldg(table + j / a.bs);
-    if (page < 0 || page >= a.num_blocks) {
-      if (lane == 0) raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
-      return;
-    }
-    const size_t r = (static_cast<size_t>(page) * a.hkv + kvh) * a.bs + j % a.bs;
-    auto scale = [&](const float* s, int d) {
-      if (a.mode == FP8PA_SCALE_TOKEN_HEAD) return __ldg(s + r);
-      if (a.mode == FP8PA_SCALE_SEGMENT) return __ldg(s + static_cast<size_t>(page) * a.hp + kvh);
-      if (a.mode == FP8PA_SCALE_CHANNEL_STATIC) return 1.f;
-      const int e = __ldg(reinterpret_cast<const uint8_t*>(s) + r * (D / a.gs) + d / a.gs);
-      return e == 255 ? __int_as_float(0x7FC00000)
-                      : (e == 0 ? __int_as_float(0x00400000) : __int_as_float(e << 23));
-    };
-    float z = 0.f;
-#pragma unroll
-    for (int x = 0; x < N; ++x) {
-      const int d = lane * N + x;
-      z += q[x] * kcs[x] * code_value(a.fmt, __ldg(a.k_cache + r * D + d)) * scale(a.k_scale, d);
-    }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
-    z *= a.sm_scale;
-    z = a.cap > 0.f ? a.cap * tanh_f32(z * (1.f / a.cap)) * kLog2e : z * kLog2e;
-    z -= slope * static_cast<float>(pos - pj);
-    const float mn = fmaxf(m, z), f = ex2(m - mn), p = ex2(z - mn);
-    m = mn;
-    l = l * f + p;
-#pragma unroll
-    for (int x = 0; x < N; ++x) {
-      const int d = lane * N + x;
-      o[x] = o[x] * f + p * (code_value(a.fmt, __ldg(a.v_cache + r * D + d)) * scale(a.v_scale, d));
-    }
-  };
-  for (int j = 0; j < min(pre, wf); ++j) see(j, j);
-  for (int j = wf; j < ctx; ++j) see(j, j);
-  for (int i = row - lo, d = depth; i >= 0; i = parent(i), --d)
-    if (a.window == 0 || depth - d < a.window) see(ctx + i, ctx + d);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const long at = (static_cast<long>(row) * a.hq + h) * D + lane * N;
-#pragma unroll
-  for (int x = 0; x < N; ++x) {
-    const float v = o[x] * inv * vcs[x];
-    if (a.out_f32) reinterpret_cast<float*>(a.out)[at + x] = v;
-    else reinterpret_cast<__nv_bfloat16*>(a.out)[at + x] = __float2bfloat16_rn(v);
-  }
+  return at;
 }
 
 }  // namespace
 
 size_t tree_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, int device) {
-  return 256;
+  return tree_layout(nullptr, total_q, batch, hq / hkv, d, sm_count(device), nullptr, nullptr,
+                     nullptr);
 }
 
-cudaError_t launch_tree(const PrefillArgs& a, const int32_t* parents, cudaStream_t stream) {
-  const long warps = static_cast<long>(a.total_q) * a.hq;
-  const unsigned grid = static_cast<unsigned>((warps + 3) / 4);
-  if (a.d == 128) tree_plain_kernel<128><<<grid, 128, 0, stream>>>(a, parents);
-  else tree_plain_kernel<64><<<grid, 128, 0, stream>>>(a, parents);
-  return cudaGetLastError();
+cudaError_t launch_tree(const PrefillArgs& args, const int32_t* parents, cudaStream_t stream) {
+  PrefillArgs a = args;
+  const bool fast = a.cap <= kCapFast;
+  a.cap_in = a.cap > 0.f && fast ? 2.f * kLog2e / a.cap : 1.f;
+  a.tanh_in = fast ? 0.5f / kLog2e : 1.f / a.cap;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int ranges = sm_count(dev);
+  PlanView pv;
+  uint32_t* line;
+  int32_t* depth;
+  tree_layout(static_cast<char*>(a.workspace), a.total_q, a.batch, a.G, a.d, ranges, &pv, &line,
+              &depth);
+  const int var = a.cap > 0.f ? 2 : (a.slopes ? 1 : 0);
+  const bool raw = a.fmt != FP8PA_INT8 && a.mode != FP8PA_SCALE_MX_BLOCK;
+  const TreeKernel fn = a.d == 128 ? pick_tree_d128(raw, var) : pick_tree_d64(raw, var);
+  if ((e = ensure_smem_attr(reinterpret_cast<const void*>(fn.fn), fn.smem)) != cudaSuccess)
+    return e;
+  CUtensorMap mk{}, mv{};
+  if (raw) {
+    const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.hkv * a.bs;
+    const CUtensorMapSwizzle swz =
+        a.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    if (!encode_tensor_map_2d_u8(&mk, a.k_cache, a.d, rows, a.d, a.bs, swz) ||
+        !encode_tensor_map_2d_u8(&mv, a.v_cache, a.d, rows, a.d, a.bs, swz))
+      return cudaErrorInvalidValue;
+  }
+
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(1u + static_cast<unsigned>(a.batch));
+  cfg.blockDim = dim3(kPlanThreads);
+  if ((e = cudaLaunchKernelEx(&cfg, tree_plan_kernel, a, pv, parents, line, depth, ranges)) !=
+      cudaSuccess)
+    return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(ranges));
+  cfg.blockDim = dim3(static_cast<unsigned>(fn.threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(fn.smem);
+  const TreeView tv{line, depth};
+  if ((e = cudaLaunchKernelEx(&cfg, fn.fn, a, pv, tv, mk, mv)) != cudaSuccess) return e;
+  return launch_merge_ranges(a, pv, ranges, stream);
 }
 
 }  // namespace fp8pa

@@ -1,0 +1,1165 @@
+// tree.cuh -- attention for trees of drafted tokens over the paged cache, on the
+// fifth-generation tensor cores.
+//
+//   z_j = sm_scale q_i . k^_j;  z_j = cap tanh(z_j / cap);  z_j -= slope (pos_i - pos_j)
+//   out_i = sum_j softmax(z)_j v^_j  over the tokens ahead of the tree (as the window and
+//   the prefix leave them) and the nodes on i's line, itself among them
+//
+// Rows and work.  The (node, head) pairs of a request and KV head are rows, a TMEM lane
+// each, in blocks of 256; (row block, KV head, 128-token tile) units are cut into one
+// range per SM, and cut items leave pieces, as in the prefill (ranges.cuh, prefill.cu).  A
+// tree has few rows over a long context, so the cache's bytes bound it, and two things
+// keep the tensor cores and the softmax out of their way:
+//  - A block of at most 128 rows (narrow) runs as two streams, one on the even tiles and
+//    one on the odd ones, with scores, weights, sums and O of their own: while one is in its
+//    softmax the tensor cores work for the other.  A block of more rows (wide) has a stream
+//    for each half of its rows.
+//  - A block of at most 64 rows stands in both halves of the lanes: lanes 0-63 weigh the
+//    first 64 tokens of a tile, lanes 64-127 the others, each with zeros for what the other
+//    weighs.  The product with V is the same, the softmax half.
+// The partial results of a narrow block (2 or 4 a row) are added up at its end.
+//
+// Products.  S = Q K^T on FP8 tensor cores: the K codes as TMA lands them, q as two E4M3
+// terms hi + lo (exact for bf16 but for elements 2^-9 below the row's largest), the token's
+// scale multiplied to the fp32 score.  O += P V on f16: V's codes are exact in f16, their
+// scale goes into P in fp32 before its one rounding (2^-11).  So no code is rounded, and a
+// K tile needs no converting.  INT8 codes and MX blocks (RAW false) are converted for both
+// products: INT8 exactly, an MX block's codes times its power of two relative to the
+// token's largest.
+//
+// References and sums as in the prefill: a row's reference is a bound of max(z + e), e the
+// exponent of the token group's V scales, and moves only when passed by 2^kTau.
+//
+// Roles: warps 0-7 and 8-15 the softmax of streams 0 and 1, two threads a row; four warps
+// that convert V (RAW false: and four for K), one that issues the MMAs, and one that
+// copies pages by TMA.  Every wait is bounded.
+#pragma once
+
+#include "prefill.cuh"
+
+namespace fp8pa {
+
+// What the tree attention needs beside the prefill's arguments.
+struct TreeView {
+  const uint32_t* line;  // [total_q][8] the nodes on a node's line, as the window leaves them
+  const int32_t* depth;  // [total_q]
+};
+
+using TreeFn = void (*)(const PrefillArgs, const PlanView, const TreeView, const CUtensorMap,
+                        const CUtensorMap);
+struct TreeKernel {
+  TreeFn fn;
+  int smem, threads;
+};
+// raw: FP8 codes with a scale per token, segment or channel.
+TreeKernel pick_tree_d64(bool raw, int var);
+TreeKernel pick_tree_d128(bool raw, int var);
+
+namespace {
+
+constexpr int kMaxTree = FP8PA_MAX_TREE;
+constexpr int kLineWords = kMaxTree / 32;
+
+template <bool RAW>
+constexpr int kTreeConv = RAW ? 4 : 8;  // converting warps
+template <bool RAW>
+constexpr int kTreeIssue = 16 + kTreeConv<RAW>;
+template <bool RAW>
+constexpr int kTreeThreads = (kTreeIssue<RAW> + (RAW ? 2 : 1)) * 32;
+
+// Of a tile: its tokens' scales (V's relative to the 2^ev of their group of 32), the
+// tokens' positions (with a distance bias), the groups' exponents, the tokens whose page
+// exists, and those whose V is not finite.
+struct TileInfo {
+  float ks[kT], vs[kT];
+  int pos[kT];
+  int ev[4];
+  uint32_t valid[4], bad[4];
+  uint32_t pad[4];
+};
+
+template <int D, bool RAW>
+struct TreeSmem {
+  static constexpr int kHalf = 2 * kT * D;         // a 128-row f16 tile, or both terms of q
+  static constexpr int kCodes = kT * D;            // a tile of codes
+  static constexpr int kQ = 0;                     // two streams; between items, sums of O
+  static constexpr int kV = 2 * kHalf;             // two tiles of V in f16
+  static constexpr int kK = 4 * kHalf;             // K: three tiles of codes, or two of f16
+  static constexpr int kKTile = RAW ? kCodes : kHalf;
+  static constexpr int kKStages = RAW ? 3 : 2;
+  static constexpr int kVCodes = kK + kKStages * kKTile;  // RAW: two tiles of V codes
+  static constexpr int kInfo = kVCodes + (RAW ? 2 * kCodes : 0);
+  static constexpr int kXch = kInfo + 4 * static_cast<int>(sizeof(TileInfo));
+  static constexpr int kMl = kXch + 2 * 16 * 32 * 4;  // [stream][lane] reference and sum
+  static constexpr int kBars = kMl + 2 * 128 * 8;
+  static constexpr int kMisc = kBars + 320;  // TMEM base, abort flag
+  static constexpr int kBytes = kMisc + 16;
+};
+// Barriers and the arrivals that complete a phase: Q and P (by stream) the stream's eight
+// softmax warps; Info the converting warps; K full one thread and its bytes (RAW) or four
+// warps; V codes full a thread and its bytes, free the four warps; V full four warps; X
+// (stream * 4 + lane quarter) the two warps of the same rows; All the 16 softmax warps;
+// from kTKFree on a commit of the tensor cores.
+enum { kTQ = 0, kTP = 2, kTInfo = 4, kTKFull = 8, kTVCFull = 11, kTVCFree = 13, kTVFull = 15,
+       kTX = 17, kTAll = 25, kTKFree = 26, kTVFree = 29, kTS = 31, kTO = 33, kTDrain = 35,
+       kTreeBars = 36 };
+template <bool RAW>
+__device__ __forceinline__ int tree_bar_count(int i) {
+  return i < kTInfo    ? 8
+         : i < kTKFull ? kTreeConv<RAW>
+         : i < kTVCFull ? (RAW ? 1 : 4)
+         : i < kTVCFree ? 1
+         : i < kTX ? 4
+         : i < kTAll ? 2
+         : i < kTKFree ? 16
+                       : 1;
+}
+
+// An item's rows over the streams: wide, or narrow with `parts` shares of a tile's tokens
+// by lane.
+struct Streams {
+  bool wide;
+  int lanes;  // lanes of a share
+  __device__ __forceinline__ explicit Streams(const RowBlock& r)
+      : wide(r.rows > 128), lanes(r.rows <= 64 ? 64 : 128) {}
+  __device__ __forceinline__ bool shared() const { return lanes == 64; }
+  // tiles of stream t among n
+  __device__ __forceinline__ int tiles(int t, int n) const { return wide ? n : (n + 1 - t) >> 1; }
+};
+
+// Byte of chunk c (16 bytes) of row r in a tile of D-byte rows, as TMA's swizzle over D
+// bytes places it.
+template <int D>
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+  return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// What a converting warp's open item says of its tokens.
+struct OpenItem {
+  int np, skip, kvh, ctx, L, qlo, all_lo;
+  Seen seen;
+  const int32_t* table;
+  __device__ __forceinline__ void open(const PrefillArgs& a, const Item& im) {
+    np = im.r.np;
+    skip = im.r.skip;
+    kvh = im.kvh;
+    ctx = im.r.pA;
+    L = im.r.L;
+    qlo = im.r.qlo;
+    all_lo = window_first(a.window, L - 1);
+    seen = Seen{window_first(a.window, ctx), L, im.r.pre};
+    table = a.block_tables + static_cast<long>(im.r.b) * a.max_blocks;
+  }
+  __device__ __forceinline__ int token_of(int tile) const { return (tile < np ? tile : tile + skip) * kT; }
+  // whether every row sees the whole tile at token j0
+  __device__ __forceinline__ bool whole(int j0) const {
+    return (j0 >= all_lo && j0 + kT <= ctx) || j0 + kT <= seen.pre;
+  }
+};
+
+// ---------------------------------------------------------------- copies (RAW)
+// One warp: the pages of a CTA's tiles, K into three stages, V into two; lane x copies
+// page x of K, lane 16 + x that of V.  Pages that no row sees are not read.
+template <int D>
+__device__ __forceinline__ void copy_tiles(const PrefillArgs& a, const PlanView& pv, uint8_t* sm,
+                                           int* abort_flag, const CUtensorMap* mk,
+                                           const CUtensorMap* mv, int it, int u, int u1, int lane) {
+  using SM = TreeSmem<D, true>;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
+  const int pg = lane & 15, per = kT / a.bs, lgbs = 31 - __clz(a.bs);
+  const bool V = lane >= 16;
+  uint32_t g = 0, gv = 0, k3 = 0, kp = 1;  // tiles of K and V, the K stage, its release's parity
+  OpenItem o;
+  bool ok = true;
+  while (u < u1 && ok) {
+    const Item im = load_item(a, pv, it, u, u1);
+    ++it;
+    u += im.t1 - im.t0;
+    o.open(a, im);
+    auto page_of = [&](int tile) {
+      const int t = o.token_of(tile) + pg * a.bs;
+      const bool want = pg < per && ((t < o.seen.hi && t + a.bs > o.seen.lo) || t < o.seen.pre);
+      return want ? __ldg(o.table + (t >> lgbs)) : -1;
+    };
+    int id = page_of(im.t0);
+    for (int k = im.t0; k < im.t1; ++k, ++g) {
+      const bool have = id >= 0 && id < a.num_blocks;
+      const uint32_t mask = __ballot_sync(0xffffffffu, have);
+      const int y = have ? (id * a.hkv + o.kvh) * a.bs : 0;
+      id = k + 1 < im.t1 ? page_of(k + 1) : -1;
+      const uint32_t bytes = a.bs * D, st = g & 1;
+      if (g >= 3) ok = __all_sync(0xffffffffu, tc_wait(bars + kTKFree + k3, kp, abort_flag, a.err));
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(bars + kTKFull + k3, __popc(mask & 0xFFFFu) * bytes);
+      __syncwarp();
+      if (have && !V)
+        tma_load_2d(sm + SM::kK + k3 * SM::kCodes + pg * bytes, mk, 0, y, bars + kTKFull + k3);
+      if (g >= 2)
+        ok = __all_sync(0xffffffffu,
+                        tc_wait(bars + kTVCFree + st, ((g >> 1) - 1) & 1, abort_flag, a.err));
+      if (!ok) {
+        ++g;
+        break;
+      }
+      ++gv;
+      if (lane == 0) mbar_arrive_expect_tx(bars + kTVCFull + st, __popc(mask >> 16) * bytes);
+      __syncwarp();
+      if (have && V)
+        tma_load_2d(sm + SM::kVCodes + st * SM::kCodes + pg * bytes, mv, 0, y,
+                    bars + kTVCFull + st);
+      if (++k3 == 3) {
+        k3 = 0;
+        kp ^= 1;
+      }
+    }
+  }
+  if (lane == 0) {  // no copy is in flight at the end
+    for (uint32_t x = g > 3 ? g - 3 : 0; x < g; ++x)
+      (void)mbar_wait_bounded(bars + kTKFull + x % 3, (x / 3) & 1, kWaitLimitCycles);
+    for (uint32_t x = gv > 2 ? gv - 2 : 0; x < gv; ++x)
+      (void)mbar_wait_bounded(bars + kTVCFull + (x & 1), (x >> 1) & 1, kWaitLimitCycles);
+  }
+  __syncwarp();
+}
+
+// ---------------------------------------------------------------- conversions
+// 2^e for e >= -149.
+__device__ __forceinline__ float pow2_any(int e) {
+  return __int_as_float(e >= -126 ? (e + 127) << 23 : (e >= -149 ? 1 << (e + 149) : 0));
+}
+
+// The scales of a token: what multiplies its scores, and its V.
+struct Scales {
+  float k, v;
+  bool ok;  // wanted, and its page exists
+};
+__device__ __forceinline__ Scales load_scales(const PrefillArgs& a, const OpenItem& o,
+                                              const int (&ids)[2], int j, int lane) {
+  Scales s{1.f, 1.f, false};
+  const int id = lane < 16 ? ids[0] : ids[1];
+  const bool want = o.seen(j + lane);
+  s.ok = want && id >= 0 && id < a.num_blocks;
+  if (want && !s.ok) raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
+  if (!s.ok) return s;
+  if (a.mode == FP8PA_SCALE_TOKEN_HEAD) {
+    const uint32_t row = cache_row(a, o.kvh, id, j + lane);
+    s.k = __ldg(a.k_scale + row);
+    s.v = __ldg(a.v_scale + row);
+  } else if (a.mode == FP8PA_SCALE_SEGMENT) {
+    const size_t at = static_cast<size_t>(id) * a.hp + o.kvh;
+    s.k = __ldg(a.k_scale + at);
+    s.v = __ldg(a.v_scale + at);
+  }
+  return s;
+}
+
+// K's part of a tile's info, for the 32 tokens at j of group dw (a lane each).
+__device__ __forceinline__ void put_k_info(const TreeView& tv, const OpenItem& o, TileInfo* info,
+                                           int dw, int j, int lane, float scale, bool ok,
+                                           bool bias) {
+  const uint32_t valid = __ballot_sync(0xffffffffu, ok);
+  info->ks[dw * 32 + lane] = scale;
+  if (bias) {
+    const int p = j + lane;
+    info->pos[dw * 32 + lane] =
+        p < o.ctx || p >= o.L ? p : o.ctx + __ldg(tv.depth + o.qlo + p - o.ctx);
+  }
+  if (lane == 0) info->valid[dw] = valid;
+}
+// V's part; bad: bits of the tokens whose codes are not finite.  A scale counts as finite
+// where its largest code is (append writes no others).
+template <int FMT>
+__device__ __forceinline__ void put_v_info(TileInfo* info, int dw, int lane, float scale, bool ok,
+                                           uint32_t bad) {
+  const bool finite = scale <= FLT_MAX / code_max<FMT>();  // (not for a NaN)
+  const int e = max(exp_above(warp_max_f32(ok && finite ? scale : 0.f)), kLowV);
+  info->vs[dw * 32 + lane] = ok && finite ? scale * exp2i(-e) : 0.f;
+  bad |= __ballot_sync(0xffffffffu, ok && !finite);
+  if (lane == 0) {
+    info->ev[dw] = e;
+    info->bad[dw] = bad;
+  }
+}
+
+// A job's codes as f16 into a tile: its rows of V are zero where the token is not wanted,
+// or, where some row masks it (partly), not finite; these are returned by token.
+template <int D, int FMT, bool MX>
+__device__ __forceinline__ uint32_t put_tile(const PrefillArgs& a, Job<D>& job, bool V, int dw,
+                                             bool whole, uint8_t* tile, int lane) {
+  constexpr int H = D / 64;
+  constexpr int kRoom = FMT == FP8PA_E5M2 ? 0 : 7;
+  const int r8 = lane & 7, c4 = lane >> 3;
+  uint32_t keep = job.okm, bad = 0;
+  if (V && !whole && FMT != FP8PA_INT8) {
+    uint32_t nf = 0;  // bit x: this lane's chunks of row group x
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      bool f = false;
+#pragma unroll
+      for (int h = 0; h < H; ++h) f = f || codes_nonfinite<FMT>(job.buf[x][h]);
+      nf |= f ? 1u << x : 0u;
+    }
+    nf |= __shfl_xor_sync(0xffffffffu, nf, 8);
+    nf |= __shfl_xor_sync(0xffffffffu, nf, 16);
+    nf &= job.okm;
+    keep &= ~nf;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)  // lanes 0-7 hold the rows in order
+      bad |= (__ballot_sync(0xffffffffu, (nf >> x) & 1u) & 0xFFu) << (8 * x);
+  }
+  // core matrices as in the prefill's tiles
+  uint8_t* dst =
+      tile + r8 * 16 + (V ? dw * (D * 64) + c4 * 256 : dw * 512 + c4 * 4096);
+  const int kG = V ? D * 16 : 128, kC = V ? 4 * 256 : 4 * 4096, kH = V ? 128 : 2048;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    int em = 0;
+    if constexpr (MX) em = __shfl_sync(0xffffffffu, job.em, x * 8 + r8);
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      uint4 p, q;
+      codes16_to_f16<FMT>(job.buf[x][h], p, q);
+      if constexpr (MX) {
+        const int be = static_cast<int>((job.ex[h] >> (8 * x)) & 0xFFu) - em + kRoom;
+        const float f = exp2i(be);
+        const __half2 f2 = __floats2half2_rn(f, f);
+        p = scale8(p, f2);
+        q = scale8(q, f2);
+      }
+      if (V && ((keep >> x) & 1) == 0) p = q = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(dst + x * kG + h * kC) = p;
+      *reinterpret_cast<uint4*>(dst + x * kG + h * kC + kH) = q;
+    }
+  }
+  return bad;
+}
+
+// RAW: a warp's 32 tokens of every tile: their scales, and V's codes from the copied stage
+// into the f16 tile.
+template <int D, int FMT>
+__device__ __forceinline__ void convert_raw(const PrefillArgs& a, const PlanView& pv,
+                                            const TreeView& tv, uint8_t* sm, int* abort_flag,
+                                            int it, int u, int u1, int dw, int lane, bool bias) {
+  using SM = TreeSmem<D, true>;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
+  TileInfo* infos = reinterpret_cast<TileInfo*>(sm + SM::kInfo);
+  const int lgbs = 31 - __clz(a.bs), r8 = lane & 7, c4 = lane >> 3;
+  uint32_t g = 0;
+  OpenItem o;
+  while (u < u1) {
+    const Item im = load_item(a, pv, it, u, u1);
+    ++it;
+    u += im.t1 - im.t0;
+    o.open(a, im);
+    int ids[2];
+    job_blocks(o.table, lgbs, o.seen, o.token_of(im.t0) + dw * 32, ids);
+    Scales s = load_scales(a, o, ids, o.token_of(im.t0) + dw * 32, lane);
+    if (im.t0 + 1 < im.t1) job_blocks(o.table, lgbs, o.seen, o.token_of(im.t0 + 1) + dw * 32, ids);
+    for (int k = im.t0; k < im.t1; ++k, ++g) {
+      const uint32_t st = g & 1, s4 = g & 3;
+      const int j0 = o.token_of(k), j = j0 + dw * 32;
+      const bool whole = o.whole(j0);
+      const Scales now = s;
+      // the next tile's scales, and the block ids of the one behind it
+      if (k + 1 < im.t1) {
+        s = load_scales(a, o, ids, o.token_of(k + 1) + dw * 32, lane);
+        if (k + 2 < im.t1)
+          job_blocks(o.table, lgbs, o.seen, o.token_of(k + 2) + dw * 32, ids);
+      }
+      // (an info's last reader, the softmax of tile g - 4, came before the product with V that
+      // freed the tile waited for below, two tiles ago)
+      TileInfo* info = infos + s4;
+      put_k_info(tv, o, info, dw, j, lane, now.k, now.ok, bias);
+      // V codes: rows r8 of four groups of 8, 16-byte chunks c4 (and c4 + 4)
+      if (!__all_sync(0xffffffffu, tc_wait(bars + kTVCFull + st, (g >> 1) & 1, abort_flag, a.err)))
+        return;
+      Job<D> job;
+      const uint8_t* src = sm + SM::kVCodes + st * SM::kCodes;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          job.buf[x][h] = *reinterpret_cast<const uint4*>(
+              src + swizzled<D>(dw * 32 + x * 8 + r8, c4 + h * 4));
+      const uint32_t held = __ballot_sync(0xffffffffu, now.ok);
+      job.okm = 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) job.okm |= ((held >> (x * 8 + r8)) & 1u) << x;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + kTVCFree + st);
+      if (g >= 2 && !__all_sync(0xffffffffu, tc_wait(bars + kTVFree + st, ((g >> 1) - 1) & 1,
+                                                     abort_flag, a.err)))
+        return;
+      const uint32_t bad = put_tile<D, FMT, false>(a, job, true, dw, whole,
+                                                   sm + SM::kV + st * SM::kHalf, lane);
+      put_v_info<FMT>(info, dw, lane, now.v, now.ok, bad);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bars + kTInfo + s4);
+        mbar_arrive(bars + kTVFull + st);
+      }
+    }
+  }
+}
+
+// RAW false: a warp's 32 tokens of K or of V of every tile, from the cache into the f16
+// tile; a tile kAhead on is asked for into L2.
+template <int D, int FMT, bool MX>
+__device__ __forceinline__ void convert_loaded(const PrefillArgs& a, const PlanView& pv,
+                                               const TreeView& tv, uint8_t* sm, int* abort_flag,
+                                               int it, int u, int u1, int part, int lane,
+                                               bool bias) {
+  using SM = TreeSmem<D, false>;
+  constexpr int kRoom = FMT == FP8PA_E5M2 ? 0 : 7;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
+  TileInfo* infos = reinterpret_cast<TileInfo*>(sm + SM::kInfo);
+  const int lgbs = 31 - __clz(a.bs), dw = part & 3, nbx = MX ? D / a.gs : 0;
+  const bool V = part >= 4;
+  uint32_t g = 0;
+  OpenItem o;
+  while (u < u1) {
+    const Item im = load_item(a, pv, it, u, u1);
+    ++it;
+    u += im.t1 - im.t0;
+    o.open(a, im);
+    int ids[2];
+    job_blocks(o.table, lgbs, o.seen, o.token_of(im.t0) + dw * 32, ids);
+    for (int k = im.t0; k < im.t1; ++k, ++g) {
+      const uint32_t st = g & 1, s4 = g & 3;
+      const int j0 = o.token_of(k), j = j0 + dw * 32;
+      Job<D> job;
+      load_job<D, MX>(a, V, o.kvh, ids, j, o.seen, lane, job);
+      if (k + 1 < im.t1) job_blocks(o.table, lgbs, o.seen, o.token_of(k + 1) + dw * 32, ids);
+      if (lane < 2 && k + kAhead < im.t1) {
+        const int t = o.token_of(k + kAhead) + dw * 32 + lane * 16;
+        const int id = (t < o.seen.hi && t + 16 > o.seen.lo) || t < o.seen.pre
+                           ? __ldg(o.table + (t >> lgbs)) : -1;
+        if (id >= 0 && id < a.num_blocks) {
+          const size_t row = cache_row(a, o.kvh, id, t);
+          prefetch_l2((V ? a.v_cache : a.k_cache) + row * D, 16 * D);
+          if (a.mode == FP8PA_SCALE_TOKEN_HEAD) prefetch_l2((V ? a.v_scale : a.k_scale) + row, 64);
+          else if (MX)
+            prefetch_l2(reinterpret_cast<const uint8_t*>(V ? a.v_scale : a.k_scale) + row * nbx,
+                        16 * nbx);
+        }
+      }
+      float scale = job.sc;
+      if constexpr (MX)
+        scale = job.em == 255 ? __int_as_float(0x7FC00000) : pow2_any(job.em - 127 - kRoom);
+      // (an info's last reader, the softmax of tile g - 4, came before S of tile g - 2 and
+      // before the product with V of tile g - 2)
+      if (g >= 2 && !__all_sync(0xffffffffu, tc_wait(bars + (V ? kTVFree : kTKFree) + st,
+                                                     ((g >> 1) - 1) & 1, abort_flag, a.err)))
+        return;
+      TileInfo* info = infos + s4;
+      const uint32_t bad = put_tile<D, FMT, MX>(a, job, V, dw, o.whole(j0),
+                                                sm + (V ? SM::kV : SM::kK) + st * SM::kHalf, lane);
+      if (V) put_v_info<FMT>(info, dw, lane, scale, job.sok, bad);
+      else put_k_info(tv, o, info, dw, j, lane, scale, job.sok, bias);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bars + kTInfo + s4);
+        mbar_arrive(bars + (V ? kTVFull : kTKFull) + st);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- kernel
+// VAR: 0 no score modifier but the masks, 1 distance bias, 2 capped scores (with or
+// without a bias).
+template <int D, bool RAW, int VAR>
+__global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
+    tree_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ PlanView pv,
+                const __grid_constant__ TreeView tv, const __grid_constant__ CUtensorMap mk,
+                const __grid_constant__ CUtensorMap mv) {
+  using SM = TreeSmem<D, RAW>;
+  // (the swizzled tiles start at multiples of 1024 bytes)
+  extern __shared__ __align__(1024) uint8_t tree_sm[];
+  uint8_t* const sm = tree_sm;
+  uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + SM::kMisc);
+  int& s_abort = *reinterpret_cast<int*>(sm + SM::kMisc + 4);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
+  TileInfo* infos = reinterpret_cast<TileInfo*>(sm + SM::kInfo);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kIssue = kTreeIssue<RAW>;
+
+  griddep_wait();
+  griddep_launch_dependents();
+  const int u0 = pv.start[blockIdx.x], u1 = pv.start[blockIdx.x + 1];
+  if (u0 >= u1) return;
+  const int it0 = pv.item[blockIdx.x];
+
+  if (warp == kIssue) tmem_alloc(&s_tmem, 512);
+  if (tid == 0) {
+    s_abort = 0;
+    for (int i = 0; i < kTreeBars; ++i) mbar_init(bars + i, tree_bar_count<RAW>(i));
+    fence_barrier_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kIssue) tmem_relinquish();
+  const uint32_t tmem = s_tmem;
+  int* abort_flag = &s_abort;
+  auto wait = [&](int bar, uint32_t parity) {
+    return tc_wait(bars + bar, parity, abort_flag, a.err);
+  };
+  // a wait of a whole warp: one answer for all lanes
+  auto wait_warp = [&](int bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, tc_wait(bars + bar, parity, abort_flag, a.err)) != 0;
+  };
+
+  if (warp == kIssue) {
+    // ================================================= MMA issuer
+    // S of a stream goes where its P was: it is issued behind the product with V that
+    // reads that P.  TMEM: S at 0 and 128, O at 256 and 384.
+    if (lane == 0) {
+      const uint32_t base = smem_u32(sm);
+      const uint32_t idesc_s = RAW ? tc_idesc(0, a.fmt == FP8PA_E5M2 ? 1 : 0, 0, 0, 128, kT)
+                                   : tc_idesc(0, 0, 0, 0, 128, kT);
+      const uint32_t idesc_o = tc_idesc(0, 0, 0, 1, 128, D);  // A in TMEM, B MN-major
+      const uint64_t dv0 = tc_desc(base + SM::kV, D * 16, 128, 0);
+      const uint64_t dq0 = RAW ? tc_desc(base + SM::kQ, 16, D * 8, D == 128 ? 2 : 4)
+                               : tc_desc(base + SM::kQ, 2048, 128, 0);
+      const uint64_t dk0 = RAW ? tc_desc(base + SM::kK, 16, D * 8, D == 128 ? 2 : 4)
+                               : tc_desc(base + SM::kK, 2048, 128, 0);
+      uint32_t g = 0;                   // tiles done by this CTA
+      uint32_t k3 = 0, kp = 0;          // K stage of the next S, and its parity
+      uint32_t nq = 0, np = 0;          // bit t: phase of stream t's Q and P
+      bool ok = true;
+      auto mma_s = [&](int t, uint32_t st) {
+        const uint64_t dq = dq0 + t * (SM::kHalf >> 4), dk = dk0 + st * (SM::kKTile >> 4);
+        const uint32_t d = tmem + t * kT;
+        if constexpr (RAW) {
+#pragma unroll
+          for (int term = 0; term < 2; ++term)
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+              tc_mma_f8(d, dq + term * (SM::kCodes >> 4) + k * 2, dk + k * 2, idesc_s,
+                        (term | k) != 0);
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tc_mma_f16(d, dq + k * (4096 >> 4), dk + k * (4096 >> 4), idesc_s, k > 0);
+        }
+        tc_commit(bars + kTS + t);
+      };
+      auto mma_o = [&](int t, uint32_t st, bool first) {
+        const uint64_t dv = dv0 + st * (SM::kHalf >> 4);
+        const uint32_t d = tmem + 256 + t * 128, p = tmem + t * kT;
+#pragma unroll
+        for (int k = 0; k < kT / 16; ++k)  // the groups of P start 32 columns apart
+          tc_mma_f16_ts(d, p + (k >> 1) * 32 + (k & 1) * 8, dv + k * (2 * D * 16 >> 4), idesc_o,
+                        !(first && k == 0));
+        tc_commit(bars + kTO + t);
+      };
+      auto k_next = [&]() {
+        if (++k3 == SM::kKStages) {
+          k3 = 0;
+          kp ^= 1;
+        }
+      };
+      auto wait_q = [&](int t) {
+        const bool good = wait(kTQ + t, (nq >> t) & 1);
+        nq ^= 1u << t;
+        return good;
+      };
+      auto wait_p = [&](int t) {
+        const bool good = wait(kTP + t, (np >> t) & 1);
+        np ^= 1u << t;
+        return good;
+      };
+      for (int it = it0, u = u0; u < u1 && ok; ++it) {
+        const Item im = load_item(a, pv, it, u, u1);
+        const int n = im.t1 - im.t0;
+        u += n;
+        if (Streams(im.r).wide) {
+          for (int k = -1; k < n && ok; ++k) {  // S of tile k + 1 behind the product of tile k
+            const bool more = k + 1 < n;
+            if (k >= 0) ok = wait(kTVFull + (g & 1), (g >> 1) & 1);
+            if (ok && more) ok = wait(kTKFull + k3, kp);
+#pragma unroll 1
+            for (int t = 0; t < 2 && ok; ++t) {
+              ok = k < 0 ? wait_q(t) : wait_p(t);
+              if (!ok) break;
+              tc_fence_after();
+              if (k >= 0) mma_o(t, g & 1, k == 0);
+              if (more) mma_s(t, k3);
+            }
+            if (k >= 0) {
+              tc_commit(bars + kTVFree + (g & 1));
+              ++g;
+            }
+            if (more) {
+              tc_commit(bars + kTKFree + k3);
+              k_next();
+            }
+          }
+        } else {
+          for (int k = -2; k < n && ok; ++k) {  // S of tile k + 2, of the same stream
+            const bool more = k + 2 < n;
+            const int t = k & 1;
+            if (k >= 0) {
+              ok = wait(kTVFull + (g & 1), (g >> 1) & 1) && wait_p(t);
+              if (!ok) break;
+              tc_fence_after();
+              mma_o(t, g & 1, k < 2);
+              tc_commit(bars + kTVFree + (g & 1));
+              ++g;
+            }
+            if (more) {
+              ok = wait(kTKFull + k3, kp) && (k >= 0 || wait_q(t));
+              if (!ok) break;
+              tc_fence_after();
+              mma_s(t, k3);
+              tc_commit(bars + kTKFree + k3);
+              k_next();
+            }
+          }
+        }
+      }
+    }
+  } else if (RAW && warp == kIssue + 1) {
+    if constexpr (RAW) copy_tiles<D>(a, pv, sm, abort_flag, &mk, &mv, it0, u0, u1, lane);
+  } else if (warp >= 16) {
+    const bool bias = VAR > 0 && a.slopes;
+    const int part = warp - 16;
+    if constexpr (RAW) {
+      if (a.fmt == FP8PA_E4M3)
+        convert_raw<D, FP8PA_E4M3>(a, pv, tv, sm, abort_flag, it0, u0, u1, part, lane, bias);
+      else
+        convert_raw<D, FP8PA_E5M2>(a, pv, tv, sm, abort_flag, it0, u0, u1, part, lane, bias);
+    } else {
+      if (a.fmt == FP8PA_INT8)
+        convert_loaded<D, FP8PA_INT8, false>(a, pv, tv, sm, abort_flag, it0, u0, u1, part, lane,
+                                             bias);
+      else if (a.fmt == FP8PA_E4M3)
+        convert_loaded<D, FP8PA_E4M3, true>(a, pv, tv, sm, abort_flag, it0, u0, u1, part, lane,
+                                            bias);
+      else
+        convert_loaded<D, FP8PA_E5M2, true>(a, pv, tv, sm, abort_flag, it0, u0, u1, part, lane,
+                                            bias);
+    }
+  } else {
+    // ================================================= softmax warps
+    const int t = warp >> 3, half = (warp >> 2) & 1;  // stream, and half of a share's tokens
+    const int rl = (warp & 3) * 32 + lane;            // lane of the tile
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + t * kT + lanes, to = tmem + 256 + t * 128 + lanes;
+    float* xch = reinterpret_cast<float*>(sm + SM::kXch) + warp * 32 + lane;
+    float2* ml = reinterpret_cast<float2*>(sm + SM::kMl);
+    uint32_t nx = 0, na = 0;
+    // Trade one value per row with the other warp of the rows.  The slots alternate: one
+    // is written again only after the other warp's next arrival.
+    auto trade = [&](float mine, float& other) {
+      float* slot = xch + (nx & 1) * (16 * 32);
+      *slot = mine;
+      __syncwarp();
+      const int bar = kTX + t * 4 + (warp & 3);
+      if (lane == 0) mbar_arrive(bars + bar);
+      const bool good = wait_warp(bar, nx & 1);
+      ++nx;
+      other = slot[half ? -4 * 32 : 4 * 32];
+      return good;
+    };
+    auto sync_all = [&]() {  // all softmax warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + kTAll);
+      const bool good = wait_warp(kTAll, na & 1);
+      ++na;
+      return good;
+    };
+    uint32_t g = 0, ns = 0;  // tiles of the CTA, and of this stream
+    bool ok = true;
+    for (int it = it0, u = u0; u < u1 && ok; ++it) {
+      const Item im = load_item(a, pv, it, u, u1);
+      const int n = im.t1 - im.t0;
+      u += n;
+      const Streams sp(im.r);
+      const int mine = sp.tiles(t, n);  // tiles of this stream
+      // row of the block of a lane (lanes past its end: the last row)
+      auto row_of = [&](int l) { return sp.wide ? t * 128 + l : l & (sp.lanes - 1); };
+      auto query_of = [&](int l, int& qi, int& h) {
+        const int rr = im.r.row0 + min(row_of(l), im.r.rows - 1);
+        qi = rr / a.G;
+        h = im.kvh * a.G + rr - qi * a.G;
+      };
+      const int r = row_of(rl);
+      const bool live = r < im.r.rows;
+      int qi, h;
+      query_of(rl, qi, h);
+      const long qrow = static_cast<long>(im.r.qlo) + qi;
+      const long grow = qrow * a.hq + h;  // row of q and out
+      float ref = kNegBig, l = 0.f;
+      if (mine > 0) {
+        float zs;
+        {
+          // ---- the rows of q, each normalised by a power of two, into shared memory
+          // (every S of the stream's previous item is done: its last was read)
+          const float sgn = a.sm_scale < 0.f ? -1.f : 1.f;
+          const bool st = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
+          const float* kc = a.k_scale + static_cast<long>(im.kvh) * D;
+          constexpr int kTop = RAW ? 8 : 14;  // exponent of the normalised row
+          const int r8 = lane & 7, c4 = lane >> 3;
+          uint4 raw[2][D / 32];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            int qy, hy;
+            query_of((warp & 3) * 32 + (half * 2 + y) * 8 + r8, qy, hy);
+            const uint4* src = reinterpret_cast<const uint4*>(
+                                   a.q + ((static_cast<long>(im.r.qlo) + qy) * a.hq + hy) * D) + c4;
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) raw[y][x] = __ldg(src + x * 4);
+          }
+          int eq[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            auto get = [&](int x, float (&f)[8]) {
+              const uint32_t w[4] = {raw[y][x].x, raw[y][x].y, raw[y][x].z, raw[y][x].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                f[2 * e] = __uint_as_float(w[e] << 16) * sgn;
+                f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * sgn;
+              }
+              if (st) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] *= __ldg(kc + (x * 4 + c4) * 8 + e);
+              }
+            };
+            float amax = 0.f;
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) {
+              float f[8];
+              get(x, f);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
+            // (129 for an infinity: such a row is NaN)
+            eq[y] = amax > 0.f ? exp_above(amax) : 0;
+            const float fq = exp2i(kTop - eq[y]);
+            const int row = (warp & 3) * 32 + (half * 2 + y) * 8 + r8;
+            uint8_t* dst = sm + SM::kQ + t * SM::kHalf;
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) {
+              float f[8];
+              get(x, f);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] *= fq;
+              if constexpr (RAW) {  // hi, and lo = what hi leaves
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  hi[e] = f32x2_to_codes2<FP8PA_E4M3>(f[2 * e], f[2 * e + 1]);
+                  const uint32_t back = codes2_to_f16x2<FP8PA_E4M3>(hi[e]);
+                  const float2 b = __half22float2(h2(back));
+                  lo[e] = f32x2_to_codes2<FP8PA_E4M3>(f[2 * e] - b.x, f[2 * e + 1] - b.y);
+                }
+                const int c8 = x * 4 + c4;  // 8 dims: half a 16-byte chunk
+                uint8_t* p = dst + swizzled<D>(row, c8 >> 1) + (c8 & 1) * 8;
+                *reinterpret_cast<uint2*>(p) =
+                    make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                *reinterpret_cast<uint2*>(p + SM::kCodes) =
+                    make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+              } else {
+                *reinterpret_cast<uint4*>(dst + (row >> 3) * 128 + r8 * 16 + (x * 4 + c4) * 2048) =
+                    make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]),
+                               pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+              }
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + kTQ + t);
+          // this lane's row: group lane / 8 of four, in this warp's half or the other's
+          float own = static_cast<float>((lane >> 3) & 1 ? eq[1] : eq[0]), theirs;
+          if (!trade(own, theirs)) {
+            ok = false;
+            break;
+          }
+          const int er = static_cast<int>((lane >> 4) == half ? own : theirs);
+          // log2-domain factor of a raw score (capped scores: see cap_in)
+          zs = er > 128 ? __int_as_float(0x7FC00000)
+                        : fabsf(a.sm_scale) * exp2i(er - kTop) * (VAR == 2 ? a.cap_in : kLog2e);
+          // (VAR 0 multiplies a masked -inf by the factor: not zero)
+          if (VAR == 0 && er <= 128) zs = fmaxf(zs, 1e-37f);
+        }
+        const int ctx = im.r.pA, pre = im.r.pre;
+        const uint32_t* line = tv.line + qrow * kLineWords;
+        const int pos = ctx + __ldg(tv.depth + qrow), wf = window_first(a.window, pos);
+        const int wB = window_first(a.window, im.r.L - 1);  // no row's window begins behind it
+        const float slope = (VAR > 0 && a.slopes) ? __ldg(a.slopes + h) * kLog2e : 0.f;
+        const float cap_log2 = VAR == 2 ? a.cap * kLog2e : 0.f;
+        // the thread's groups of 32 tokens: first, and how many
+        const int ng = sp.shared() ? 1 : 2;
+        const int g0 = sp.shared() ? (rl >> 6) * 2 + half : half * 2;
+        const uint32_t first_tile = g + (sp.wide ? 0 : t);
+        for (int x = 0; x < mine; ++x) {
+          const uint32_t gt = first_tile + (sp.wide ? x : 2 * x), s4 = gt & 3;
+          const int kt = im.t0 + static_cast<int>(gt - g);
+          const int j0 = (kt < im.r.np ? kt : kt + im.r.skip) * kT + g0 * 32;
+          // Scores first: an info barrier may be phases behind a stream that sat tiles out,
+          // but by the time of its scores every earlier tile's info is complete.
+          if (!wait_warp(kTS + t, ns & 1) || !wait_warp(kTInfo + s4, (gt >> 2) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const TileInfo& info = infos[s4];
+          const uint32_t all = info.valid[g0] & info.valid[g0 + ng - 1];
+          // whether every row of the warp sees all of the thread's tokens
+          const bool whole =
+              ((j0 >= wB && j0 + ng * 32 <= ctx) || (VAR == 0 && j0 + ng * 32 <= pre)) &&
+              all == 0xFFFFFFFFu && (VAR < 2 || a.cap <= kCapFast);
+          // ---- a bound of z + e over the row's tokens.  The scores of the first group
+          // stay in registers, those of the second go back to TMEM.
+          uint32_t raw[2][16];
+          float bound = __int_as_float(0xff800000);
+          auto find = [&](auto masked, int w) {
+            const int gw = g0 + w, jw = j0 + w * 32;
+            const uint32_t sc = ts + gw * 32;
+            tmem_ld16(sc, raw[0]);
+            tmem_ld16(sc + 16, raw[1]);
+            uint32_t m = info.valid[gw];
+            if constexpr (masked.value) {
+              uint32_t see = word_bits(jw, wf, ctx) | word_bits(jw, 0, pre);
+              const int o = jw - ctx;  // the group's first token as a node
+              if (o > -32) {
+                const int w0 = max(o, 0) >> 5, s = o & 31;
+                uint32_t bits = 0;
+                if (o < 0) bits = __ldg(line) << (-o);
+                else if (w0 < kLineWords)
+                  bits = __funnelshift_r(__ldg(line + w0),
+                                         w0 + 1 < kLineWords ? __ldg(line + w0 + 1) : 0u, s);
+                see |= bits;
+              }
+              m &= see;
+            }
+            if (m & info.bad[gw]) l = __int_as_float(0x7FC00000);
+            const float4* ks = reinterpret_cast<const float4*>(info.ks + gw * 32);
+            const float e = static_cast<float>(info.ev[gw]);
+            tmem_ld_wait();
+            tmem_landed(raw[0]);
+            tmem_landed(raw[1]);
+            float m4[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) m4[y] = __int_as_float(0xff800000);
+            // the bias of tokens 2 i, 2 i + 1 of the group: -slope (pos - j)
+            // (VAR 2: and the cap, less what the tanh leaves of it)
+            const float b0 = VAR > 0 ? fmaf(slope, static_cast<float>(jw - pos), cap_log2) : 0.f;
+            const uint64_t zs2 = f2_pack(zs, zs), bias = f2_pack(b0, b0 + slope);
+            const uint64_t by2 = f2_pack(2.f * slope, 2.f * slope);
+#pragma unroll
+            for (int i4 = 0; i4 < 8; ++i4) {
+              const float4 k4 = ks[i4];
+#pragma unroll
+              for (int i2 = 0; i2 < 2; ++i2) {
+                const int i = i4 * 2 + i2;
+                uint32_t* rr = &raw[i / 8][(i % 8) * 2];
+                uint64_t z = f2_mul(f2_pack(__uint_as_float(rr[0]), __uint_as_float(rr[1])),
+                                    i2 ? f2_pack(k4.z, k4.w) : f2_pack(k4.x, k4.y));
+                float y[2];
+                if constexpr (VAR > 0) {
+                  if constexpr (masked.value) {
+                    f2_unpack(f2_mul(z, zs2), y[0], y[1]);
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                      if constexpr (VAR == 2) y[v] = a.cap * tanh_f32(y[v] * a.tanh_in) * kLog2e;
+                      if (slope != 0.f)
+                        y[v] = fmaf(-slope, static_cast<float>(pos - info.pos[gw * 32 + 2 * i + v]),
+                                    y[v]);
+                    }
+                  } else {
+                    const float fi = static_cast<float>(i);
+                    const uint64_t b = f2_fma(by2, f2_pack(fi, fi), bias);
+                    if constexpr (VAR == 1) {
+                      z = f2_fma(z, zs2, b);
+                    } else {  // cap tanh(z / cap) = cap - 2 cap / (2^x + 1), cap in the bias
+                      f2_unpack(f2_mul(z, zs2), y[0], y[1]);
+                      f2_unpack(f2_add(f2_pack(ex2(y[0]), ex2(y[1])), f2_pack(1.f, 1.f)), y[0],
+                                y[1]);
+                      z = f2_fma(f2_pack(rcp_fast(y[0]), rcp_fast(y[1])),
+                                 f2_pack(-2.f * cap_log2, -2.f * cap_log2), b);
+                    }
+                    f2_unpack(z, y[0], y[1]);
+                  }
+                } else {
+                  f2_unpack(z, y[0], y[1]);
+                }
+                if constexpr (masked.value) {
+                  y[0] = (m >> (2 * i)) & 1 ? y[0] : __int_as_float(0xff800000);
+                  y[1] = (m >> (2 * i + 1)) & 1 ? y[1] : __int_as_float(0xff800000);
+                }
+                m4[i & 3] = max3(m4[i & 3], y[0], y[1]);
+                rr[0] = __float_as_uint(y[0]);
+                rr[1] = __float_as_uint(y[1]);
+              }
+            }
+            if (w > 0) {
+              tmem_st16(sc, raw[0]);
+              tmem_st16(sc + 16, raw[1]);
+            }
+            const float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+            bound = fmaxf(bound, fmaf(mx, VAR > 0 ? 1.f : zs, e));
+          };
+#pragma unroll 1
+          for (int w = ng - 1; w >= 0; --w) {
+            if (whole) find(std::false_type{}, w);
+            else find(std::true_type{}, w);
+          }
+          if (ng > 1) tmem_st_wait();
+          // ---- the reference, shared by the lane's two threads: where the bound passed it
+          // by 2^kTau it moves, and with it the sums and O
+          float other;
+          if (!trade(bound, other)) {
+            ok = false;
+            break;
+          }
+          bound = fmaxf(bound, other);
+          float al = 1.f;
+          if (bound > ref + kTau) {
+            al = ex2(ref - bound);
+            ref = bound;
+          }
+          if (__any_sync(0xffffffffu, al != 1.f)) {
+            l *= al;
+            if (x > 0) {
+              // (the product of the stream's tile before came ahead of this one's scores)
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                const uint32_t at = to + half * (D / 2) + c * 8;
+                uint32_t o[8];
+                tmem_ld8(at, o);
+                tmem_ld_wait();
+                tmem_landed(o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                tmem_st8(at, o);
+              }
+            }
+          }
+          // ---- P times V's scale, and the sum of P
+#pragma unroll 1
+          for (int w = 0; w < ng; ++w) {
+            const int gw = g0 + w;
+            const uint32_t sc = ts + gw * 32;
+            if (w > 0) {
+              tmem_ld16(sc, raw[0]);
+              tmem_ld16(sc + 16, raw[1]);
+              tmem_ld_wait();
+              tmem_landed(raw[0]);
+              tmem_landed(raw[1]);
+            }
+            const float4* vs = reinterpret_cast<const float4*>(info.vs + gw * 32);
+            const float e = static_cast<float>(info.ev[gw]);
+            const float c0 = kShift - ref + e, f = VAR > 0 ? 1.f : zs;
+            const uint64_t f2 = f2_pack(f, f), c02 = f2_pack(c0, c0);
+            uint64_t la = 0, lb = 0;  // (0.f, 0.f)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t pw[8];
+#pragma unroll
+              for (int i2 = 0; i2 < 4; ++i2) {
+                const float4 v4 = vs[c * 4 + i2];
+#pragma unroll
+                for (int i1 = 0; i1 < 2; ++i1) {
+                  const int i = i2 * 2 + i1;
+                  const uint64_t z =
+                      f2_pack(__uint_as_float(raw[c][2 * i]), __uint_as_float(raw[c][2 * i + 1]));
+                  float p, q;
+                  f2_unpack(VAR > 0 ? f2_add(z, c02) : f2_fma(z, f2, c02), p, q);
+                  const uint64_t e2 = f2_pack(ex2(p), ex2(q));
+                  if (i & 1) lb = f2_add(lb, e2);
+                  else la = f2_add(la, e2);
+                  f2_unpack(f2_mul(e2, i1 ? f2_pack(v4.z, v4.w) : f2_pack(v4.x, v4.y)), p, q);
+                  pw[i] = pack_half2(p, q);
+                }
+              }
+              tmem_st8(sc + c * 8, pw);
+            }
+            float y, z;
+            f2_unpack(f2_add(la, lb), y, z);
+            l = fmaf(y + z, ex2(-e), l);
+          }
+          if (sp.shared()) {  // nothing for the other share's tokens
+            const uint32_t zero[16] = {};
+            tmem_st16(ts + (g0 ^ 2) * 32, zero);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + kTP + t);
+          ++ns;
+        }
+        if (!ok) break;
+        // the row's sum, and the last product
+        float other;
+        if (!trade(l, other) || !wait_warp(kTO + t, (ns - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        l += other;
+        tc_fence_after();
+      }
+      g += n;
+
+      // ---- the block's result, or this range's piece of it: half the dims each
+      const bool piece = im.t0 > 0 || im.t1 < im.r.count;
+      const int slot = blockIdx.x * 2 + (im.t0 > 0 ? 0 : 1);
+      const bool stat = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
+      const float* vch = a.v_scale + static_cast<long>(im.kvh) * D;
+      auto put = [&](int c, float (&f)[16]) {  // dims 16 c .. 16 c + 15 of row r
+        if (stat) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) f[i] *= __ldg(vch + c * 16 + i);
+        }
+        if (piece || a.out_f32) {
+          float* dst = piece ? pv.o + (static_cast<long>(slot) * kRows + r) * D + c * 16
+                             : reinterpret_cast<float*>(a.out) + grow * D + c * 16;
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4*>(dst + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + grow * D +
+                                                c * 16);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const __nv_bfloat162 b2 =
+                  __floats2bfloat162_rn(f[8 * i + 2 * x], f[8 * i + 2 * x + 1]);
+              w[x] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      };
+      auto take = [&](int c, float scale, float (&f)[16]) {  // of this lane's O
+        uint32_t o[16];
+        tmem_ld16(to + c * 16, o);
+        tmem_ld_wait();
+        tmem_landed(o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(o[i]) * scale;
+      };
+      if (sp.wide) {
+        const float inv = piece ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D / 32; ++c0) {
+          const int c = half * (D / 32) + c0;
+          float f[16];
+          take(c, inv, f);
+          if (live) put(c, f);
+        }
+        if (piece && live && half == 0)
+          pv.ml[static_cast<long>(slot) * kRows + r] = make_float2(ref, l);
+      } else {
+        // the row's partial results: of both streams, and of both shares of the lanes
+        if (half == 0) ml[t * 128 + rl] = make_float2(ref, l);
+        if (!sync_all()) {
+          ok = false;
+          break;
+        }
+        float M = kNegBig, sum = 0.f;
+        for (int x = r; x < 256; x += sp.lanes) M = fmaxf(M, ml[x].x);
+        for (int x = r; x < 256; x += sp.lanes) sum += ml[x].y * ex2(ml[x].x - M);
+        const float scale = ex2(ref - M) * (piece ? 1.f : (sum == 0.f ? 0.f : 1.f / sum));
+        // dims 4 c .. 4 c + 3 of lane y's row among the sums, free of bank conflicts
+        auto at = [&](int y, int c) {
+          return reinterpret_cast<float4*>(sm + SM::kQ + y * (D * 4) +
+                                           (((c & ~7) | ((c ^ y) & 7)) << 4));
+        };
+        auto leave = [&](int c, const float (&f)[16]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *at(rl, c * 4 + i) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        };
+        auto add = [&](int y, int c, float (&f)[16]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 v = *at(y, c * 4 + i);
+            f[4 * i] += v.x;
+            f[4 * i + 1] += v.y;
+            f[4 * i + 2] += v.z;
+            f[4 * i + 3] += v.w;
+          }
+        };
+        const bool both = n > 1;  // whether stream 1 had a tile
+        if (t == 1 && both) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < D / 32; ++c0) {
+            float f[16];
+            take(half * (D / 32) + c0, scale, f);
+            leave(half * (D / 32) + c0, f);
+          }
+        }
+        if (!sync_all()) {
+          ok = false;
+          break;
+        }
+        if (sp.shared()) {
+          if (t == 0 && rl >= 64) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < D / 32; ++c0) {
+              const int c = half * (D / 32) + c0;
+              float f[16];
+              take(c, scale, f);
+              if (both) add(rl, c, f);
+              leave(c, f);
+            }
+          }
+          if (!sync_all()) {
+            ok = false;
+            break;
+          }
+        }
+        if (t == 0 && rl < sp.lanes) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < D / 32; ++c0) {
+            const int c = half * (D / 32) + c0;
+            float f[16];
+            take(c, scale, f);
+            if (both) add(rl, c, f);
+            if (sp.shared()) add(rl + 64, c, f);
+            if (live) put(c, f);
+          }
+          if (piece && live && half == 0)
+            pv.ml[static_cast<long>(slot) * kRows + r] = make_float2(M, sum);
+        }
+        if (!sync_all()) {  // the sums lie where the next item's q goes
+          ok = false;
+          break;
+        }
+      }
+      tc_fence_before();
+    }
+  }
+
+  // ---- drain and free: no MMA may still be in flight
+  __syncwarp();
+  if (warp == kIssue && lane == 0) {
+    tc_commit(bars + kTDrain);
+    (void)mbar_wait_bounded(bars + kTDrain, 0, kWaitLimitCycles);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kIssue) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- instances
+template <int D, bool RAW>
+TreeKernel pick_tree(int var) {
+  return {var == 0 ? tree_kernel<D, RAW, 0>
+                   : (var == 1 ? tree_kernel<D, RAW, 1> : tree_kernel<D, RAW, 2>),
+          TreeSmem<D, RAW>::kBytes, kTreeThreads<RAW>};
+}
+
+}  // namespace
+
+}  // namespace fp8pa
