@@ -31,8 +31,8 @@
 // exponent of the token group's V scales, and moves only when passed by 2^kTau.
 //
 // Roles: warps 0-7 and 8-15 the softmax of streams 0 and 1, two threads a row; four warps
-// that convert V (RAW false: and four for K), one that issues the MMAs, and one that
-// copies pages by TMA.  Every wait is bounded.
+// that convert V (RAW false: and four for K), one that issues MMAs for each stream, and
+// one that copies K's pages by TMA and lays out their scales, and one for V's.  Every wait is bounded.
 #pragma once
 
 #include "prefill.cuh"
@@ -65,18 +65,20 @@ constexpr int kTreeConv = RAW ? 4 : 8;  // converting warps
 template <bool RAW>
 constexpr int kTreeIssue = 16 + kTreeConv<RAW>;
 template <bool RAW>
-constexpr int kTreeThreads = (kTreeIssue<RAW> + (RAW ? 2 : 1)) * 32;
+constexpr int kTreeThreads = (kTreeIssue<RAW> + (RAW ? 4 : 2)) * 32;
 
 // Of a tile: its tokens' scales (V's relative to the 2^ev of their group of 32), the
 // tokens' positions (with a distance bias), the groups' exponents, the tokens whose page
-// exists, and those whose V is not finite.
+// exists (held: as V's copies say it), those whose V's scale is not finite, and, written
+// with V in f16, those with codes that are not, where some row does not see the whole tile.
 struct TileInfo {
   float ks[kT], vs[kT];
   int pos[kT];
   int ev[4];
-  uint32_t valid[4], bad[4];
-  uint32_t pad[4];
+  uint32_t valid[4], bad[4], held[4], cbad[4];
+  uint32_t whole, pad[3];
 };
+constexpr uint32_t kInfos = 8;  // stages
 
 template <int D, bool RAW>
 struct TreeSmem {
@@ -84,35 +86,35 @@ struct TreeSmem {
   static constexpr int kCodes = kT * D;            // a tile of codes
   static constexpr int kQ = 0;                     // two streams; between items, sums of O
   static constexpr int kV = 2 * kHalf;             // two tiles of V in f16
-  static constexpr int kK = 4 * kHalf;             // K: three tiles of codes, or two of f16
+  static constexpr int kK = 4 * kHalf;             // K: tiles of codes, or of f16
   static constexpr int kKTile = RAW ? kCodes : kHalf;
-  static constexpr int kKStages = RAW ? 3 : 2;
+  // (an even number: a stage then serves one stream within an item)
+  static constexpr int kKStages = RAW && D == 64 ? 4 : 2;
   static constexpr int kVCodes = kK + kKStages * kKTile;  // RAW: two tiles of V codes
   static constexpr int kInfo = kVCodes + (RAW ? 2 * kCodes : 0);
-  static constexpr int kXch = kInfo + 4 * static_cast<int>(sizeof(TileInfo));
-  static constexpr int kMl = kXch + 2 * 16 * 32 * 4;  // [stream][lane] reference and sum
+  static constexpr int kXch = kInfo + static_cast<int>(kInfos * sizeof(TileInfo));
+  static constexpr int kMl = kXch + 2 * 16 * 32 * 8;  // [stream][lane] reference and sum
   static constexpr int kBars = kMl + 2 * 128 * 8;
   static constexpr int kMisc = kBars + 320;  // TMEM base, abort flag
   static constexpr int kBytes = kMisc + 16;
 };
 // Barriers and the arrivals that complete a phase: Q and P (by stream) the stream's eight
-// softmax warps; Info the converting warps; K full one thread and its bytes (RAW) or four
-// warps; V codes full a thread and its bytes, free the four warps; V full four warps; X
-// (stream * 4 + lane quarter) the two warps of the same rows; All the 16 softmax warps;
-// from kTKFree on a commit of the tensor cores.
-enum { kTQ = 0, kTP = 2, kTInfo = 4, kTKFull = 8, kTVCFull = 11, kTVCFree = 13, kTVFull = 15,
-       kTX = 17, kTAll = 25, kTKFree = 26, kTVFree = 29, kTS = 31, kTO = 33, kTDrain = 35,
-       kTreeBars = 36 };
+// softmax warps; Info the copying warps (RAW) or the converting ones; K full one thread and its bytes (RAW) or four
+// warps; V codes full a thread and its bytes, free the four warps; V full four warps; All
+// the 16 softmax warps; K and V free two commits of the tensor cores (one of each stream's
+// issuer, or two of the one whose tile it is); S, O and Drain one.
+enum { kTQ = 0, kTP = 2, kTInfo = 4, kTKFull = 12, kTVCFull = 16, kTVCFree = 18, kTVFull = 20,
+       kTAll = 22, kTKFree = 23, kTVFree = 27, kTS = 29, kTO = 31, kTDrain = 33, kTreeBars = 35 };
 template <bool RAW>
 __device__ __forceinline__ int tree_bar_count(int i) {
   return i < kTInfo    ? 8
-         : i < kTKFull ? kTreeConv<RAW>
+         : i < kTKFull ? (RAW ? 2 : 8)
          : i < kTVCFull ? (RAW ? 1 : 4)
          : i < kTVCFree ? 1
-         : i < kTX ? 4
-         : i < kTAll ? 2
+         : i < kTAll ? 4
          : i < kTKFree ? 16
-                       : 1;
+         : i < kTS ? 2
+                   : 1;
 }
 
 // An item's rows over the streams: wide, or narrow with `parts` shares of a tile's tokens
@@ -134,14 +136,22 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
   return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
+// First token of tile x of a row block's list.  The list is walked from its end: with a
+// distance bias the newest tokens weigh most, and a reference that starts there stays
+// (rescaling O with every tile took 1700 cycles of 13000).
+__device__ __forceinline__ int first_token(int np, int skip, int x) {
+  return (x < np ? x : x + skip) * kT;
+}
+
 // What a converting warp's open item says of its tokens.
 struct OpenItem {
-  int np, skip, kvh, ctx, L, qlo, all_lo;
+  int np, skip, last, kvh, ctx, L, qlo, all_lo;
   Seen seen;
   const int32_t* table;
   __device__ __forceinline__ void open(const PrefillArgs& a, const Item& im) {
     np = im.r.np;
     skip = im.r.skip;
+    last = im.r.count - 1;
     kvh = im.kvh;
     ctx = im.r.pA;
     L = im.r.L;
@@ -150,7 +160,7 @@ struct OpenItem {
     seen = Seen{window_first(a.window, ctx), L, im.r.pre};
     table = a.block_tables + static_cast<long>(im.r.b) * a.max_blocks;
   }
-  __device__ __forceinline__ int token_of(int tile) const { return (tile < np ? tile : tile + skip) * kT; }
+  __device__ __forceinline__ int token_of(int tile) const { return first_token(np, skip, last - tile); }
   // whether every row sees the whole tile at token j0
   __device__ __forceinline__ bool whole(int j0) const {
     return (j0 >= all_lo && j0 + kT <= ctx) || j0 + kT <= seen.pre;
@@ -158,17 +168,53 @@ struct OpenItem {
 };
 
 // ---------------------------------------------------------------- copies (RAW)
-// One warp: the pages of a CTA's tiles, K into three stages, V into two; lane x copies
-// page x of K, lane 16 + x that of V.  Pages that no row sees are not read.
-template <int D>
-__device__ __forceinline__ void copy_tiles(const PrefillArgs& a, const PlanView& pv, uint8_t* sm,
-                                           int* abort_flag, const CUtensorMap* mk,
-                                           const CUtensorMap* mv, int it, int u, int u1, int lane) {
+// The scales of a tile, lane x those of tokens x, 32 + x, 64 + x and 96 + x.
+struct TileScales {
+  float s[4];
+  uint32_t ok;  // bit of a token: wanted, and its page exists
+};
+// pages: lane x holds the tile's page x.
+template <bool V>
+__device__ __forceinline__ TileScales load_scales(const PrefillArgs& a, const OpenItem& o,
+                                                  int pages, int j0, int lgbs, int lane) {
+  TileScales r;
+  r.ok = 0;
+  const float* scale = V ? a.v_scale : a.k_scale;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int id = __shfl_sync(0xffffffffu, pages, (i * 32 + lane) >> lgbs);
+    const int j = j0 + i * 32 + lane;
+    const bool want = o.seen(j), ok = want && id >= 0 && id < a.num_blocks;
+    if (!V && want && !ok) raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
+    r.ok |= ok ? 1u << i : 0u;
+    r.s[i] = 1.f;
+    if (ok && a.mode == FP8PA_SCALE_TOKEN_HEAD)
+      r.s[i] = __ldg(scale + cache_row(a, o.kvh, id, j));
+    else if (ok && a.mode == FP8PA_SCALE_SEGMENT)
+      r.s[i] = __ldg(scale + static_cast<size_t>(id) * a.hp + o.kvh);
+  }
+  return r;
+}
+
+// One warp for K or V: the pages of a CTA's tiles into its stages (lane x copies page x;
+// pages that no row sees are not read), and its part of the tiles' infos.  Scales are
+// loaded a tile ahead, block ids two.  (An info's last reader, the softmax of tile g - 8,
+// came before S of tile g - 6, and before the product with V of that tile.)
+template <int D, bool V>
+__device__ __forceinline__ void copy_tiles(const PrefillArgs& a, const PlanView& pv,
+                                           const TreeView& tv, uint8_t* sm, int* abort_flag,
+                                           const CUtensorMap* map, int it, int u, int u1, int lane,
+                                           bool bias) {
   using SM = TreeSmem<D, true>;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
-  const int pg = lane & 15, per = kT / a.bs, lgbs = 31 - __clz(a.bs);
-  const bool V = lane >= 16;
-  uint32_t g = 0, gv = 0, k3 = 0, kp = 1;  // tiles of K and V, the K stage, its release's parity
+  TileInfo* infos = reinterpret_cast<TileInfo*>(sm + SM::kInfo);
+  constexpr uint32_t kS = V ? 2 : SM::kKStages;
+  constexpr int kFull = V ? kTVCFull : kTKFull, kFree = V ? kTVCFree : kTKFree;
+  const int per = kT / a.bs, lgbs = 31 - __clz(a.bs);
+  const uint32_t bytes = a.bs * D;
+  const float top = FLT_MAX / (a.fmt == FP8PA_E4M3 ? code_max<FP8PA_E4M3>()
+                                                   : code_max<FP8PA_E5M2>());
+  uint32_t g = 0;
   OpenItem o;
   bool ok = true;
   while (u < u1 && ok) {
@@ -177,47 +223,70 @@ __device__ __forceinline__ void copy_tiles(const PrefillArgs& a, const PlanView&
     u += im.t1 - im.t0;
     o.open(a, im);
     auto page_of = [&](int tile) {
-      const int t = o.token_of(tile) + pg * a.bs;
-      const bool want = pg < per && ((t < o.seen.hi && t + a.bs > o.seen.lo) || t < o.seen.pre);
+      const int t = o.token_of(tile) + lane * a.bs;
+      const bool want = tile < im.t1 && lane < per &&
+                        ((t < o.seen.hi && t + a.bs > o.seen.lo) || t < o.seen.pre);
       return want ? __ldg(o.table + (t >> lgbs)) : -1;
     };
-    int id = page_of(im.t0);
+    int id = page_of(im.t0), id1 = page_of(im.t0 + 1);
+    TileScales s = load_scales<V>(a, o, id, o.token_of(im.t0), lgbs, lane);
     for (int k = im.t0; k < im.t1; ++k, ++g) {
-      const bool have = id >= 0 && id < a.num_blocks;
-      const uint32_t mask = __ballot_sync(0xffffffffu, have);
-      const int y = have ? (id * a.hkv + o.kvh) * a.bs : 0;
-      id = k + 1 < im.t1 ? page_of(k + 1) : -1;
-      const uint32_t bytes = a.bs * D, st = g & 1;
-      if (g >= 3) ok = __all_sync(0xffffffffu, tc_wait(bars + kTKFree + k3, kp, abort_flag, a.err));
-      if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(bars + kTKFull + k3, __popc(mask & 0xFFFFu) * bytes);
-      __syncwarp();
-      if (have && !V)
-        tma_load_2d(sm + SM::kK + k3 * SM::kCodes + pg * bytes, mk, 0, y, bars + kTKFull + k3);
-      if (g >= 2)
-        ok = __all_sync(0xffffffffu,
-                        tc_wait(bars + kTVCFree + st, ((g >> 1) - 1) & 1, abort_flag, a.err));
-      if (!ok) {
-        ++g;
+      const int j0 = o.token_of(k), here = id;
+      const TileScales now = s;
+      id = id1;
+      if (k + 1 < im.t1) s = load_scales<V>(a, o, id, o.token_of(k + 1), lgbs, lane);
+      id1 = page_of(k + 2);
+      const bool have = here >= 0 && here < a.num_blocks;
+      const uint32_t count = __popc(__ballot_sync(0xffffffffu, have)), st = g % kS;
+      TileInfo* info = infos + g % kInfos;
+      if (g >= kS &&
+          !__all_sync(0xffffffffu, tc_wait(bars + kFree + st, (g / kS - 1) & 1, abort_flag, a.err))) {
+        ok = false;
         break;
       }
-      ++gv;
-      if (lane == 0) mbar_arrive_expect_tx(bars + kTVCFull + st, __popc(mask >> 16) * bytes);
-      __syncwarp();
-      if (have && V)
-        tma_load_2d(sm + SM::kVCodes + st * SM::kCodes + pg * bytes, mv, 0, y,
-                    bars + kTVCFull + st);
-      if (++k3 == 3) {
-        k3 = 0;
-        kp ^= 1;
+      uint32_t held[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) held[i] = __ballot_sync(0xffffffffu, (now.ok >> i) & 1u);
+      if (V && lane == 0) {  // what the converting warps need comes with the codes
+#pragma unroll
+        for (int i = 0; i < 4; ++i) info->held[i] = held[i];
+        info->whole = o.whole(j0);
       }
+      if (lane == 0) mbar_arrive_expect_tx(bars + kFull + st, count * bytes);
+      __syncwarp();
+      if (have)
+        tma_load_2d(sm + (V ? SM::kVCodes : SM::kK) + st * SM::kCodes + lane * bytes, map, 0,
+                    (here * a.hkv + o.kvh) * a.bs, bars + kFull + st);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool there = (now.ok >> i) & 1u;
+        if constexpr (V) {
+          // a scale counts as finite where its largest code is (append writes no others)
+          const bool finite = now.s[i] <= top;  // (not for a NaN)
+          const int e = max(exp_above(warp_max_f32(there && finite ? now.s[i] : 0.f)), kLowV);
+          info->vs[i * 32 + lane] = there && finite ? now.s[i] * exp2i(-e) : 0.f;
+          const uint32_t bad = __ballot_sync(0xffffffffu, there && !finite);
+          if (lane == 0) {
+            info->ev[i] = e;
+            info->bad[i] = bad;
+          }
+        } else {
+          info->ks[i * 32 + lane] = there ? now.s[i] : 0.f;
+          if (bias) {
+            const int p = j0 + i * 32 + lane;
+            info->pos[i * 32 + lane] =
+                p < o.ctx || p >= o.L ? p : o.ctx + __ldg(tv.depth + o.qlo + p - o.ctx);
+          }
+          if (lane == 0) info->valid[i] = held[i];
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + kTInfo + g % kInfos);
     }
   }
   if (lane == 0) {  // no copy is in flight at the end
-    for (uint32_t x = g > 3 ? g - 3 : 0; x < g; ++x)
-      (void)mbar_wait_bounded(bars + kTKFull + x % 3, (x / 3) & 1, kWaitLimitCycles);
-    for (uint32_t x = gv > 2 ? gv - 2 : 0; x < gv; ++x)
-      (void)mbar_wait_bounded(bars + kTVCFull + (x & 1), (x >> 1) & 1, kWaitLimitCycles);
+    for (uint32_t x = g > kS ? g - kS : 0; x < g; ++x)
+      (void)mbar_wait_bounded(bars + kFull + x % kS, (x / kS) & 1, kWaitLimitCycles);
   }
   __syncwarp();
 }
@@ -226,31 +295,6 @@ __device__ __forceinline__ void copy_tiles(const PrefillArgs& a, const PlanView&
 // 2^e for e >= -149.
 __device__ __forceinline__ float pow2_any(int e) {
   return __int_as_float(e >= -126 ? (e + 127) << 23 : (e >= -149 ? 1 << (e + 149) : 0));
-}
-
-// The scales of a token: what multiplies its scores, and its V.
-struct Scales {
-  float k, v;
-  bool ok;  // wanted, and its page exists
-};
-__device__ __forceinline__ Scales load_scales(const PrefillArgs& a, const OpenItem& o,
-                                              const int (&ids)[2], int j, int lane) {
-  Scales s{1.f, 1.f, false};
-  const int id = lane < 16 ? ids[0] : ids[1];
-  const bool want = o.seen(j + lane);
-  s.ok = want && id >= 0 && id < a.num_blocks;
-  if (want && !s.ok) raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
-  if (!s.ok) return s;
-  if (a.mode == FP8PA_SCALE_TOKEN_HEAD) {
-    const uint32_t row = cache_row(a, o.kvh, id, j + lane);
-    s.k = __ldg(a.k_scale + row);
-    s.v = __ldg(a.v_scale + row);
-  } else if (a.mode == FP8PA_SCALE_SEGMENT) {
-    const size_t at = static_cast<size_t>(id) * a.hp + o.kvh;
-    s.k = __ldg(a.k_scale + at);
-    s.v = __ldg(a.v_scale + at);
-  }
-  return s;
 }
 
 // K's part of a tile's info, for the 32 tokens at j of group dw (a lane each).
@@ -281,36 +325,40 @@ __device__ __forceinline__ void put_v_info(TileInfo* info, int dw, int lane, flo
   }
 }
 
-// A job's codes as f16 into a tile: its rows of V are zero where the token is not wanted,
-// or, where some row masks it (partly), not finite; these are returned by token.
+// The tokens of a job of V whose codes are not all finite (bits of the 32); their rows are
+// taken out of job.okm.
+template <int D, int FMT>
+__device__ __forceinline__ uint32_t drop_nonfinite(Job<D>& job, int lane) {
+  if constexpr (FMT == FP8PA_INT8) return 0;
+  uint32_t nf = 0, bad = 0;  // bit x of nf: this lane's chunks of row group x
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    bool f = false;
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) f = f || codes_nonfinite<FMT>(job.buf[x][h]);
+    nf |= f ? 1u << x : 0u;
+  }
+  nf |= __shfl_xor_sync(0xffffffffu, nf, 8);
+  nf |= __shfl_xor_sync(0xffffffffu, nf, 16);
+  nf &= job.okm;
+  job.okm &= ~nf;
+#pragma unroll
+  for (int x = 0; x < 4; ++x)  // lanes 0-7 hold the rows in order
+    bad |= (__ballot_sync(0xffffffffu, (nf >> x) & 1u) & 0xFFu) << (8 * x);
+  return bad;
+}
+
+// A job's codes as f16 into a tile; rows of V that are not in job.okm are zero.
 template <int D, int FMT, bool MX>
-__device__ __forceinline__ uint32_t put_tile(const PrefillArgs& a, Job<D>& job, bool V, int dw,
-                                             bool whole, uint8_t* tile, int lane) {
+__device__ __forceinline__ void put_tile(Job<D>& job, bool V, int dw, uint8_t* tile, int lane) {
   constexpr int H = D / 64;
   constexpr int kRoom = FMT == FP8PA_E5M2 ? 0 : 7;
   const int r8 = lane & 7, c4 = lane >> 3;
-  uint32_t keep = job.okm, bad = 0;
-  if (V && !whole && FMT != FP8PA_INT8) {
-    uint32_t nf = 0;  // bit x: this lane's chunks of row group x
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      bool f = false;
-#pragma unroll
-      for (int h = 0; h < H; ++h) f = f || codes_nonfinite<FMT>(job.buf[x][h]);
-      nf |= f ? 1u << x : 0u;
-    }
-    nf |= __shfl_xor_sync(0xffffffffu, nf, 8);
-    nf |= __shfl_xor_sync(0xffffffffu, nf, 16);
-    nf &= job.okm;
-    keep &= ~nf;
-#pragma unroll
-    for (int x = 0; x < 4; ++x)  // lanes 0-7 hold the rows in order
-      bad |= (__ballot_sync(0xffffffffu, (nf >> x) & 1u) & 0xFFu) << (8 * x);
-  }
   // core matrices as in the prefill's tiles
   uint8_t* dst =
       tile + r8 * 16 + (V ? dw * (D * 64) + c4 * 256 : dw * 512 + c4 * 4096);
   const int kG = V ? D * 16 : 128, kC = V ? 4 * 256 : 4 * 4096, kH = V ? 128 : 2048;
+  const bool drop = V && !__all_sync(0xffffffffu, job.okm == 0xFu);
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
     int em = 0;
@@ -326,80 +374,55 @@ __device__ __forceinline__ uint32_t put_tile(const PrefillArgs& a, Job<D>& job, 
         p = scale8(p, f2);
         q = scale8(q, f2);
       }
-      if (V && ((keep >> x) & 1) == 0) p = q = make_uint4(0u, 0u, 0u, 0u);
+      if (drop && ((job.okm >> x) & 1) == 0) p = q = make_uint4(0u, 0u, 0u, 0u);
       *reinterpret_cast<uint4*>(dst + x * kG + h * kC) = p;
       *reinterpret_cast<uint4*>(dst + x * kG + h * kC + kH) = q;
     }
   }
-  return bad;
 }
 
-// RAW: a warp's 32 tokens of every tile: their scales, and V's codes from the copied stage
-// into the f16 tile.
+// RAW: a warp's 32 tokens of each of n tiles, V's codes from the copied stage into the f16
+// tile.
 template <int D, int FMT>
-__device__ __forceinline__ void convert_raw(const PrefillArgs& a, const PlanView& pv,
-                                            const TreeView& tv, uint8_t* sm, int* abort_flag,
-                                            int it, int u, int u1, int dw, int lane, bool bias) {
+__device__ __forceinline__ void convert_raw(const PrefillArgs& a, uint8_t* sm, int* abort_flag,
+                                            uint32_t n, int dw, int lane) {
   using SM = TreeSmem<D, true>;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::kBars);
   TileInfo* infos = reinterpret_cast<TileInfo*>(sm + SM::kInfo);
-  const int lgbs = 31 - __clz(a.bs), r8 = lane & 7, c4 = lane >> 3;
-  uint32_t g = 0;
-  OpenItem o;
-  while (u < u1) {
-    const Item im = load_item(a, pv, it, u, u1);
-    ++it;
-    u += im.t1 - im.t0;
-    o.open(a, im);
-    int ids[2];
-    job_blocks(o.table, lgbs, o.seen, o.token_of(im.t0) + dw * 32, ids);
-    Scales s = load_scales(a, o, ids, o.token_of(im.t0) + dw * 32, lane);
-    if (im.t0 + 1 < im.t1) job_blocks(o.table, lgbs, o.seen, o.token_of(im.t0 + 1) + dw * 32, ids);
-    for (int k = im.t0; k < im.t1; ++k, ++g) {
-      const uint32_t st = g & 1, s4 = g & 3;
-      const int j0 = o.token_of(k), j = j0 + dw * 32;
-      const bool whole = o.whole(j0);
-      const Scales now = s;
-      // the next tile's scales, and the block ids of the one behind it
-      if (k + 1 < im.t1) {
-        s = load_scales(a, o, ids, o.token_of(k + 1) + dw * 32, lane);
-        if (k + 2 < im.t1)
-          job_blocks(o.table, lgbs, o.seen, o.token_of(k + 2) + dw * 32, ids);
-      }
-      // (an info's last reader, the softmax of tile g - 4, came before the product with V that
-      // freed the tile waited for below, two tiles ago)
-      TileInfo* info = infos + s4;
-      put_k_info(tv, o, info, dw, j, lane, now.k, now.ok, bias);
-      // V codes: rows r8 of four groups of 8, 16-byte chunks c4 (and c4 + 4)
-      if (!__all_sync(0xffffffffu, tc_wait(bars + kTVCFull + st, (g >> 1) & 1, abort_flag, a.err)))
-        return;
-      Job<D> job;
-      const uint8_t* src = sm + SM::kVCodes + st * SM::kCodes;
+  const int r8 = lane & 7, c4 = lane >> 3;
+  for (uint32_t g = 0; g < n; ++g) {
+    const uint32_t st = g & 1;
+    if (!__all_sync(0xffffffffu, tc_wait(bars + kTVCFull + st, (g >> 1) & 1, abort_flag, a.err)))
+      return;
+    // rows r8 of four groups of 8, 16-byte chunks c4 (and c4 + 4)
+    Job<D> job;
+    const uint8_t* src = sm + SM::kVCodes + st * SM::kCodes;
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
+    for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-          job.buf[x][h] = *reinterpret_cast<const uint4*>(
-              src + swizzled<D>(dw * 32 + x * 8 + r8, c4 + h * 4));
-      const uint32_t held = __ballot_sync(0xffffffffu, now.ok);
-      job.okm = 0;
+      for (int h = 0; h < D / 64; ++h)
+        job.buf[x][h] = *reinterpret_cast<const uint4*>(
+            src + swizzled<D>(dw * 32 + x * 8 + r8, c4 + h * 4));
+    TileInfo* info = infos + g % kInfos;
+    const uint32_t held = info->held[dw];
+    const bool whole = info->whole;
+    // the codes are in registers before the next copy may land on them: without the fence
+    // copies from L2 overtook these loads (in every call of 8 trees over 2500 tokens)
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + kTVCFree + st);
+    job.okm = 0;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) job.okm |= ((held >> (x * 8 + r8)) & 1u) << x;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + kTVCFree + st);
-      if (g >= 2 && !__all_sync(0xffffffffu, tc_wait(bars + kTVFree + st, ((g >> 1) - 1) & 1,
-                                                     abort_flag, a.err)))
-        return;
-      const uint32_t bad = put_tile<D, FMT, false>(a, job, true, dw, whole,
-                                                   sm + SM::kV + st * SM::kHalf, lane);
-      put_v_info<FMT>(info, dw, lane, now.v, now.ok, bad);
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bars + kTInfo + s4);
-        mbar_arrive(bars + kTVFull + st);
-      }
-    }
+    for (int x = 0; x < 4; ++x) job.okm |= ((held >> (x * 8 + r8)) & 1u) << x;
+    const uint32_t bad = whole ? 0u : drop_nonfinite<D, FMT>(job, lane);
+    if (g >= 2 && !__all_sync(0xffffffffu, tc_wait(bars + kTVFree + st, ((g >> 1) - 1) & 1,
+                                                   abort_flag, a.err)))
+      return;
+    put_tile<D, FMT, false>(job, true, dw, sm + SM::kV + st * SM::kHalf, lane);
+    if (lane == 0) info->cbad[dw] = bad;
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + kTVFull + st);
   }
 }
 
@@ -426,7 +449,7 @@ __device__ __forceinline__ void convert_loaded(const PrefillArgs& a, const PlanV
     int ids[2];
     job_blocks(o.table, lgbs, o.seen, o.token_of(im.t0) + dw * 32, ids);
     for (int k = im.t0; k < im.t1; ++k, ++g) {
-      const uint32_t st = g & 1, s4 = g & 3;
+      const uint32_t st = g & 1, si = g % kInfos;
       const int j0 = o.token_of(k), j = j0 + dw * 32;
       Job<D> job;
       load_job<D, MX>(a, V, o.kvh, ids, j, o.seen, lane, job);
@@ -447,24 +470,88 @@ __device__ __forceinline__ void convert_loaded(const PrefillArgs& a, const PlanV
       float scale = job.sc;
       if constexpr (MX)
         scale = job.em == 255 ? __int_as_float(0x7FC00000) : pow2_any(job.em - 127 - kRoom);
-      // (an info's last reader, the softmax of tile g - 4, came before S of tile g - 2 and
-      // before the product with V of tile g - 2)
+      // V's info goes first, as S waits for it.  (An info's last reader, the softmax of tile
+      // g - 8, came before the waits of tiles before.)
+      TileInfo* info = infos + si;
+      if (V) {
+        const uint32_t bad = o.whole(j0) ? 0u : drop_nonfinite<D, FMT>(job, lane);
+        put_v_info<FMT>(info, dw, lane, scale, job.sok, bad);
+        if (lane == 0) info->cbad[dw] = 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + kTInfo + si);
+      }
       if (g >= 2 && !__all_sync(0xffffffffu, tc_wait(bars + (V ? kTVFree : kTKFree) + st,
                                                      ((g >> 1) - 1) & 1, abort_flag, a.err)))
         return;
-      TileInfo* info = infos + s4;
-      const uint32_t bad = put_tile<D, FMT, MX>(a, job, V, dw, o.whole(j0),
-                                                sm + (V ? SM::kV : SM::kK) + st * SM::kHalf, lane);
-      if (V) put_v_info<FMT>(info, dw, lane, scale, job.sok, bad);
-      else put_k_info(tv, o, info, dw, j, lane, scale, job.sok, bias);
+      put_tile<D, FMT, MX>(job, V, dw, sm + (V ? SM::kV : SM::kK) + st * SM::kHalf, lane);
+      if (!V) put_k_info(tv, o, info, dw, j, lane, scale, job.sok, bias);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bars + kTInfo + s4);
+        if (!V) mbar_arrive(bars + kTInfo + si);
         mbar_arrive(bars + (V ? kTVFull : kTKFull) + st);
       }
     }
   }
+}
+
+// The tokens of the 32 from jw on that a row sees (of those that exist): the window and the
+// prefix ahead of the tree, and the nodes on its line.
+__device__ __noinline__ uint32_t seen_bits(int jw, int wf, int ctx, int pre,
+                                           const uint32_t* line) {
+  uint32_t see = word_bits(jw, wf, ctx) | word_bits(jw, 0, pre);
+  const int o = jw - ctx;  // the first token as a node
+  if (o > -32) {
+    const int w0 = max(o, 0) >> 5;
+    if (o < 0) see |= __ldg(line) << (-o);
+    else if (w0 < kLineWords)
+      see |= __funnelshift_r(__ldg(line + w0), w0 + 1 < kLineWords ? __ldg(line + w0 + 1) : 0u,
+                             o & 31);
+  }
+  return see;
+}
+
+// Waits for the word at `from` to carry `tag`, for all lanes of a warp; its value.  Gives up
+// as tc_wait does.
+__device__ __forceinline__ bool poll_word(uint32_t from, uint32_t tag, float& value) {
+  uint64_t v;
+  asm volatile("ld.volatile.shared.b64 %0, [%1];" : "=l"(v) : "r"(from) : "memory");
+  value = __uint_as_float(static_cast<uint32_t>(v));
+  return __all_sync(0xffffffffu, static_cast<uint32_t>(v >> 32) == tag) != 0;
+}
+__device__ __noinline__ bool take_word_slow(uint32_t from, uint32_t tag, float* value,
+                                            int* abort_flag, uint32_t* err) {
+  const long long t0 = clock64();
+  while (!poll_word(from, tag, *value)) {
+    if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(abort_flag) != 0 ||
+                                    clock64() - t0 > kWaitLimitCycles)) {
+      raise_error(err, FP8PA_DEVERR_TIMEOUT);
+      *reinterpret_cast<volatile int*>(abort_flag) = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool take_word(uint32_t from, uint32_t tag, float& value,
+                                          int* abort_flag, uint32_t* err) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (poll_word(from, tag, value)) return true;
+  float v;
+  const bool good = take_word_slow(from, tag, &v, abort_flag, err);
+  value = v;
+  return good;
+}
+
+// One lane of a whole warp, the same each time.  Under a branch on it the operands of an MMA
+// stay in uniform registers; under one on the lane's number each costs a move, and eight
+// MMAs take 930 cycles to issue beside busy warps.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // ---------------------------------------------------------------- kernel
@@ -498,141 +585,136 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
     for (int i = 0; i < kTreeBars; ++i) mbar_init(bars + i, tree_bar_count<RAW>(i));
     fence_barrier_init();
   }
+  for (int i = tid; i < 2 * 16 * 32; i += kTreeThreads<RAW>)  // no tag is zero
+    reinterpret_cast<uint64_t*>(sm + SM::kXch)[i] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == kIssue) tmem_relinquish();
   const uint32_t tmem = s_tmem;
   int* abort_flag = &s_abort;
-  auto wait = [&](int bar, uint32_t parity) {
-    return tc_wait(bars + bar, parity, abort_flag, a.err);
-  };
   // a wait of a whole warp: one answer for all lanes
   auto wait_warp = [&](int bar, uint32_t parity) {
     return __all_sync(0xffffffffu, tc_wait(bars + bar, parity, abort_flag, a.err)) != 0;
   };
 
-  if (warp == kIssue) {
-    // ================================================= MMA issuer
-    // S of a stream goes where its P was: it is issued behind the product with V that
-    // reads that P.  TMEM: S at 0 and 128, O at 256 and 384.
-    if (lane == 0) {
-      const uint32_t base = smem_u32(sm);
-      const uint32_t idesc_s = RAW ? tc_idesc(0, a.fmt == FP8PA_E5M2 ? 1 : 0, 0, 0, 128, kT)
-                                   : tc_idesc(0, 0, 0, 0, 128, kT);
-      const uint32_t idesc_o = tc_idesc(0, 0, 0, 1, 128, D);  // A in TMEM, B MN-major
-      const uint64_t dv0 = tc_desc(base + SM::kV, D * 16, 128, 0);
-      const uint64_t dq0 = RAW ? tc_desc(base + SM::kQ, 16, D * 8, D == 128 ? 2 : 4)
-                               : tc_desc(base + SM::kQ, 2048, 128, 0);
-      const uint64_t dk0 = RAW ? tc_desc(base + SM::kK, 16, D * 8, D == 128 ? 2 : 4)
-                               : tc_desc(base + SM::kK, 2048, 128, 0);
-      uint32_t g = 0;                   // tiles done by this CTA
-      uint32_t k3 = 0, kp = 0;          // K stage of the next S, and its parity
-      uint32_t nq = 0, np = 0;          // bit t: phase of stream t's Q and P
-      bool ok = true;
-      auto mma_s = [&](int t, uint32_t st) {
-        const uint64_t dq = dq0 + t * (SM::kHalf >> 4), dk = dk0 + st * (SM::kKTile >> 4);
-        const uint32_t d = tmem + t * kT;
-        if constexpr (RAW) {
+  if (warp >= kIssue && warp < kIssue + 2) {
+    // ================================================= MMA issuers
+    // A warp for each stream, so that neither waits behind the other's barriers.  TMEM: S at
+    // 0 and 128, O at 256 and 384.
+    const int t = __shfl_sync(0xffffffffu, warp - kIssue, 0);
+    const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t idesc_s = RAW ? tc_idesc(0, a.fmt == FP8PA_E5M2 ? 1 : 0, 0, 0, 128, kT)
+                                 : tc_idesc(0, 0, 0, 0, 128, kT);
+    const uint32_t idesc_o = tc_idesc(0, 0, 0, 1, 128, D);  // A in TMEM, B MN-major
+    const uint64_t dv0 = tc_desc(base + SM::kV, D * 16, 128, 0);
+    const uint64_t dq = (RAW ? tc_desc(base + SM::kQ, 16, D * 8, D == 128 ? 2 : 4)
+                             : tc_desc(base + SM::kQ, 2048, 128, 0)) + t * (SM::kHalf >> 4);
+    const uint64_t dk0 = RAW ? tc_desc(base + SM::kK, 16, D * 8, D == 128 ? 2 : 4)
+                             : tc_desc(base + SM::kK, 2048, 128, 0);
+    const uint32_t ds = tm + t * kT, d_o = tm + 256 + t * 128;
+    uint32_t g = 0;             // tiles before the item
+    uint32_t nq = 0, np = 0;    // items, and tiles, of the stream
+    bool ok = true;
+    auto mma_s = [&](uint32_t st) {
+      const uint64_t dk = dk0 + st * (SM::kKTile >> 4);
+      if constexpr (RAW) {
 #pragma unroll
-          for (int term = 0; term < 2; ++term)
+        for (int term = 0; term < 2; ++term)
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-              tc_mma_f8(d, dq + term * (SM::kCodes >> 4) + k * 2, dk + k * 2, idesc_s,
-                        (term | k) != 0);
+          for (int k = 0; k < D / 32; ++k)
+            tc_mma_f8(ds, dq + term * (SM::kCodes >> 4) + k * 2, dk + k * 2, idesc_s,
+                      (term | k) != 0);
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma_f16(ds, dq + k * (4096 >> 4), dk + k * (4096 >> 4), idesc_s, k > 0);
+      }
+      tc_commit(bars + kTS + t);
+    };
+    auto mma_o = [&](uint32_t st, bool first) {
+      const uint64_t dv = dv0 + st * (SM::kHalf >> 4);
+#pragma unroll
+      for (int k = 0; k < kT / 16; ++k)  // the groups of P start 32 columns apart
+        tc_mma_f16_ts(d_o, ds + (k >> 1) * 32 + (k & 1) * 8, dv + k * (2 * D * 16 >> 4), idesc_o,
+                      !(first && k == 0));
+      tc_commit(bars + kTO + t);
+    };
+    for (int it = it0, u = u0; u < u1 && ok; ++it) {
+      const Item im = load_item(a, pv, it, u, u1);
+      const int n = __shfl_sync(0xffffffffu, im.t1 - im.t0, 0);
+      u += n;
+      const Streams sp(im.r);
+      const bool wide = __shfl_sync(0xffffffffu, static_cast<int>(sp.wide), 0) != 0;
+      const int step = wide ? 1 : 2, first = wide ? 0 : t;
+      // S of the first tile; then each tile's product with V, and S of the stream's next:
+      // all that they need but P is waited for before P
+      for (int k = first - step; k < n && ok; k += step) {
+        const int next = k + step;
+        const bool more = next < n;
+        const uint32_t gk = g + k, vs = gk & 1, gn = g + next, ks = gn % SM::kKStages;
+        if (k < 0) {
+          if (!more) break;
+          // q first: once an item's q is there, every tile before the item is over, and a
+          // parity of the barriers below can mean no phase but its own (later ones follow
+          // its own, as the stages are even in number)
+          ok = wait_warp(kTQ + t, nq & 1);
+          ++nq;
         } else {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc_mma_f16(d, dq + k * (4096 >> 4), dk + k * (4096 >> 4), idesc_s, k > 0);
+          ok = wait_warp(kTVFull + vs, (gk >> 1) & 1);
         }
-        tc_commit(bars + kTS + t);
-      };
-      auto mma_o = [&](int t, uint32_t st, bool first) {
-        const uint64_t dv = dv0 + st * (SM::kHalf >> 4);
-        const uint32_t d = tmem + 256 + t * 128, p = tmem + t * kT;
-#pragma unroll
-        for (int k = 0; k < kT / 16; ++k)  // the groups of P start 32 columns apart
-          tc_mma_f16_ts(d, p + (k >> 1) * 32 + (k & 1) * 8, dv + k * (2 * D * 16 >> 4), idesc_o,
-                        !(first && k == 0));
-        tc_commit(bars + kTO + t);
-      };
-      auto k_next = [&]() {
-        if (++k3 == SM::kKStages) {
-          k3 = 0;
-          kp ^= 1;
+        if (more)
+          ok = ok && wait_warp(kTKFull + ks, (gn / SM::kKStages) & 1) &&
+               wait_warp(kTInfo + gn % kInfos, (gn / kInfos) & 1);
+        if (k >= 0) {
+          ok = ok && wait_warp(kTP + t, np & 1);
+          ++np;
         }
-      };
-      auto wait_q = [&](int t) {
-        const bool good = wait(kTQ + t, (nq >> t) & 1);
-        nq ^= 1u << t;
-        return good;
-      };
-      auto wait_p = [&](int t) {
-        const bool good = wait(kTP + t, (np >> t) & 1);
-        np ^= 1u << t;
-        return good;
-      };
-      for (int it = it0, u = u0; u < u1 && ok; ++it) {
-        const Item im = load_item(a, pv, it, u, u1);
-        const int n = im.t1 - im.t0;
-        u += n;
-        if (Streams(im.r).wide) {
-          for (int k = -1; k < n && ok; ++k) {  // S of tile k + 1 behind the product of tile k
-            const bool more = k + 1 < n;
-            if (k >= 0) ok = wait(kTVFull + (g & 1), (g >> 1) & 1);
-            if (ok && more) ok = wait(kTKFull + k3, kp);
-#pragma unroll 1
-            for (int t = 0; t < 2 && ok; ++t) {
-              ok = k < 0 ? wait_q(t) : wait_p(t);
-              if (!ok) break;
-              tc_fence_after();
-              if (k >= 0) mma_o(t, g & 1, k == 0);
-              if (more) mma_s(t, k3);
-            }
-            if (k >= 0) {
-              tc_commit(bars + kTVFree + (g & 1));
-              ++g;
-            }
-            if (more) {
-              tc_commit(bars + kTKFree + k3);
-              k_next();
-            }
+        if (!ok) break;
+        tc_fence_after();
+        if (k >= 0) {
+          if (elect_one()) {
+            mma_o(vs, k == first);
+            tc_commit(bars + kTVFree + vs);
+            if (!wide) mbar_arrive(bars + kTVFree + vs);
           }
-        } else {
-          for (int k = -2; k < n && ok; ++k) {  // S of tile k + 2, of the same stream
-            const bool more = k + 2 < n;
-            const int t = k & 1;
-            if (k >= 0) {
-              ok = wait(kTVFull + (g & 1), (g >> 1) & 1) && wait_p(t);
-              if (!ok) break;
-              tc_fence_after();
-              mma_o(t, g & 1, k < 2);
-              tc_commit(bars + kTVFree + (g & 1));
-              ++g;
-            }
-            if (more) {
-              ok = wait(kTKFull + k3, kp) && (k >= 0 || wait_q(t));
-              if (!ok) break;
-              tc_fence_after();
-              mma_s(t, k3);
-              tc_commit(bars + kTKFree + k3);
-              k_next();
-            }
+          __syncwarp();
+        }
+        if (more) {
+          // S goes where P lies, and products of different kinds and accumulators keep no order
+          // of their own (the wait is 2% of 12 x 16K tokens)
+          if (k >= 0 && !wait_warp(kTO + t, (np - 1) & 1)) {
+            ok = false;
+            break;
           }
+          if (elect_one()) {
+            mma_s(ks);
+            tc_commit(bars + kTKFree + ks);
+            if (!wide) mbar_arrive(bars + kTKFree + ks);
+          }
+          __syncwarp();
         }
       }
+      g += n;
     }
-  } else if (RAW && warp == kIssue + 1) {
-    if constexpr (RAW) copy_tiles<D>(a, pv, sm, abort_flag, &mk, &mv, it0, u0, u1, lane);
+  } else if (RAW && warp >= kIssue + 2) {
+    if constexpr (RAW) {
+      const bool bias = VAR > 0 && a.slopes;
+      if (warp == kIssue + 2)
+        copy_tiles<D, false>(a, pv, tv, sm, abort_flag, &mk, it0, u0, u1, lane, bias);
+      else
+        copy_tiles<D, true>(a, pv, tv, sm, abort_flag, &mv, it0, u0, u1, lane, bias);
+    }
   } else if (warp >= 16) {
-    const bool bias = VAR > 0 && a.slopes;
     const int part = warp - 16;
     if constexpr (RAW) {
       if (a.fmt == FP8PA_E4M3)
-        convert_raw<D, FP8PA_E4M3>(a, pv, tv, sm, abort_flag, it0, u0, u1, part, lane, bias);
+        convert_raw<D, FP8PA_E4M3>(a, sm, abort_flag, u1 - u0, part, lane);
       else
-        convert_raw<D, FP8PA_E5M2>(a, pv, tv, sm, abort_flag, it0, u0, u1, part, lane, bias);
+        convert_raw<D, FP8PA_E5M2>(a, sm, abort_flag, u1 - u0, part, lane);
     } else {
+      const bool bias = VAR > 0 && a.slopes;
       if (a.fmt == FP8PA_INT8)
         convert_loaded<D, FP8PA_INT8, false>(a, pv, tv, sm, abort_flag, it0, u0, u1, part, lane,
                                              bias);
@@ -649,21 +731,20 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
     const int rl = (warp & 3) * 32 + lane;            // lane of the tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + t * kT + lanes, to = tmem + 256 + t * 128 + lanes;
-    float* xch = reinterpret_cast<float*>(sm + SM::kXch) + warp * 32 + lane;
+    const uint32_t xch = smem_u32(sm + SM::kXch) + (warp * 32 + lane) * 8;
     float2* ml = reinterpret_cast<float2*>(sm + SM::kMl);
     uint32_t nx = 0, na = 0;
-    // Trade one value per row with the other warp of the rows.  The slots alternate: one
-    // is written again only after the other warp's next arrival.
+    // Trade one value per row with the other warp of the rows: a word with a running tag,
+    // which the other lane polls (a barrier's polls take three times as long).  The slots
+    // alternate: one is written again only after the other lane was seen a trade further.
     auto trade = [&](float mine, float& other) {
-      float* slot = xch + (nx & 1) * (16 * 32);
-      *slot = mine;
-      __syncwarp();
-      const int bar = kTX + t * 4 + (warp & 3);
-      if (lane == 0) mbar_arrive(bars + bar);
-      const bool good = wait_warp(bar, nx & 1);
       ++nx;
-      other = slot[half ? -4 * 32 : 4 * 32];
-      return good;
+      const uint32_t slot = xch + (nx & 1) * (16 * 32 * 8);
+      asm volatile("st.volatile.shared.b64 [%0], %1;" ::"r"(slot),
+                   "l"(static_cast<uint64_t>(nx) << 32 | __float_as_uint(mine))
+                   : "memory");
+      const uint32_t from = slot + (half ? -4 * 32 * 8 : 4 * 32 * 8);
+      return take_word(from, nx, other, abort_flag, a.err);
     };
     auto sync_all = [&]() {  // all softmax warps
       __syncwarp();
@@ -798,18 +879,33 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
         const int ng = sp.shared() ? 1 : 2;
         const int g0 = sp.shared() ? (rl >> 6) * 2 + half : half * 2;
         const uint32_t first_tile = g + (sp.wide ? 0 : t);
+        auto token_of = [&](uint32_t gt) {  // first token of tile gt
+          return first_token(im.r.np, im.r.skip, im.r.count - 1 - im.t0 - static_cast<int>(gt - g));
+        };
+        // makes the row NaN where it saw codes of tile gt that are not finite
+        auto late_nan = [&](uint32_t gt) {
+          const TileInfo& info = infos[gt % kInfos];
+          const uint4 c = *reinterpret_cast<const uint4*>(info.cbad);
+          if ((c.x | c.y | c.z | c.w) == 0) return;
+          for (int w = 0; w < ng; ++w) {
+            const int gw = g0 + w;
+            if (info.cbad[gw] & info.valid[gw] &
+                seen_bits(token_of(gt) + gw * 32, wf, ctx, pre, line))
+              l = __int_as_float(0x7FC00000);
+          }
+        };
         for (int x = 0; x < mine; ++x) {
-          const uint32_t gt = first_tile + (sp.wide ? x : 2 * x), s4 = gt & 3;
-          const int kt = im.t0 + static_cast<int>(gt - g);
-          const int j0 = (kt < im.r.np ? kt : kt + im.r.skip) * kT + g0 * 32;
-          // Scores first: an info barrier may be phases behind a stream that sat tiles out,
-          // but by the time of its scores every earlier tile's info is complete.
-          if (!wait_warp(kTS + t, ns & 1) || !wait_warp(kTInfo + s4, (gt >> 2) & 1)) {
+          const uint32_t gt = first_tile + (sp.wide ? x : 2 * x);
+          const int j0 = token_of(gt) + g0 * 32;
+          // (S is issued once the tile's info is complete)
+          if (!wait_warp(kTS + t, ns & 1)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const TileInfo& info = infos[s4];
+          // (what the tile before brought that is not finite is known by now)
+          if (x > 0) late_nan(gt - (sp.wide ? 1 : 2));
+          const TileInfo& info = infos[gt % kInfos];
           const uint32_t all = info.valid[g0] & info.valid[g0 + ng - 1];
           // whether every row of the warp sees all of the thread's tokens
           const bool whole =
@@ -826,18 +922,7 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
             tmem_ld16(sc + 16, raw[1]);
             uint32_t m = info.valid[gw];
             if constexpr (masked.value) {
-              uint32_t see = word_bits(jw, wf, ctx) | word_bits(jw, 0, pre);
-              const int o = jw - ctx;  // the group's first token as a node
-              if (o > -32) {
-                const int w0 = max(o, 0) >> 5, s = o & 31;
-                uint32_t bits = 0;
-                if (o < 0) bits = __ldg(line) << (-o);
-                else if (w0 < kLineWords)
-                  bits = __funnelshift_r(__ldg(line + w0),
-                                         w0 + 1 < kLineWords ? __ldg(line + w0 + 1) : 0u, s);
-                see |= bits;
-              }
-              m &= see;
+              m &= seen_bits(jw, wf, ctx, pre, line);
             }
             if (m & info.bad[gw]) l = __int_as_float(0x7FC00000);
             const float4* ks = reinterpret_cast<const float4*>(info.ks + gw * 32);
@@ -996,14 +1081,19 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           ++ns;
         }
         if (!ok) break;
-        // the row's sum, and the last product
+        // the last product, and the row's sum
         float other;
-        if (!trade(l, other) || !wait_warp(kTO + t, (ns - 1) & 1)) {
+        if (!wait_warp(kTO + t, (ns - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        late_nan(first_tile + (sp.wide ? mine - 1 : 2 * (mine - 1)));
+        if (!trade(l, other)) {
           ok = false;
           break;
         }
         l += other;
-        tc_fence_after();
       }
       g += n;
 
@@ -1142,9 +1232,10 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
 
   // ---- drain and free: no MMA may still be in flight
   __syncwarp();
-  if (warp == kIssue && lane == 0) {
-    tc_commit(bars + kTDrain);
-    (void)mbar_wait_bounded(bars + kTDrain, 0, kWaitLimitCycles);
+  if (warp >= kIssue && warp < kIssue + 2) {
+    if (elect_one()) tc_commit(bars + kTDrain + warp - kIssue);
+    __syncwarp();
+    (void)mbar_wait_bounded(bars + kTDrain + warp - kIssue, 0, kWaitLimitCycles);
   }
   tc_fence_before();
   __syncthreads();
