@@ -14,10 +14,10 @@
 //    one on the odd ones, with scores, weights, sums and O of their own: while one is in its
 //    softmax the tensor cores work for the other.  A block of more rows (wide) has a stream
 //    for each half of its rows.
-//  - A block of at most 64 rows stands in both halves of the lanes: lanes 0-63 weigh the
-//    first 64 tokens of a tile, lanes 64-127 the others, each with zeros for what the other
-//    weighs.  The product with V is the same, the softmax half.
-// The partial results of a narrow block (2 or 4 a row) are added up at its end.
+//  - A block of at most 64 (or 32) rows stands twice (four times) in the lanes: each of the
+//    copies weighs its share of a tile's tokens, with zeros for the others'.  The product
+//    with V is the same, the softmax half (a quarter).
+// The partial results of a narrow block (2 to 8 a row) are added up at its end.
 //
 // Products.  S = Q K^T on FP8 tensor cores: the K codes as TMA lands them, q as two E4M3
 // terms hi + lo (exact for bf16 but for elements 2^-9 below the row's largest), the token's
@@ -30,7 +30,7 @@
 // References and sums as in the prefill: a row's reference is a bound of max(z + e), e the
 // exponent of the token group's V scales, and moves only when passed by 2^kTau.
 //
-// Roles: warps 0-7 and 8-15 the softmax of streams 0 and 1, two threads a row; four warps
+// Roles: warps 0-3 and 4-7 the softmax of streams 0 and 1, a thread a lane; four warps
 // that convert V (RAW false: and four for K), one that issues MMAs for each stream, and
 // one that copies K's pages by TMA and lays out their scales, and one for V's.  Every wait is bounded.
 #pragma once
@@ -60,25 +60,29 @@ namespace {
 constexpr int kMaxTree = FP8PA_MAX_TREE;
 constexpr int kLineWords = kMaxTree / 32;
 
+constexpr int kTreeConv = 8;  // first converting warp
 template <bool RAW>
-constexpr int kTreeConv = RAW ? 4 : 8;  // converting warps
-template <bool RAW>
-constexpr int kTreeIssue = 16 + kTreeConv<RAW>;
+constexpr int kTreeIssue = kTreeConv + (RAW ? 4 : 8);
 template <bool RAW>
 constexpr int kTreeThreads = (kTreeIssue<RAW> + (RAW ? 4 : 2)) * 32;
 
-// Of a tile: its tokens' scales (V's relative to the 2^ev of their group of 32), the
-// tokens' positions (with a distance bias), the groups' exponents, the tokens whose page
+// Of a tile: its tokens' scales (V's relative to the 2^ev of their group of 32), their
+// positions behind the tokens ahead of the tree (for a distance bias), the groups' exponents, the tokens whose page
 // exists (held: as V's copies say it), those whose V's scale is not finite, and, written
-// with V in f16, those with codes that are not, where some row does not see the whole tile.
+// with V in f16, those with codes that are not, where some row does not see the whole tile;
+// the groups that every row sees whole; the first token, and what masks it.
 struct TileInfo {
-  float ks[kT], vs[kT];
-  int pos[kT];
+  float ks[kT], vs[kT], pos[kT];
   int ev[4];
-  uint32_t valid[4], bad[4], held[4], cbad[4];
-  uint32_t whole, pad[3];
+  uint32_t valid[4], bad[4], held[4], cbad[4], seen[4];
+  int j0, ctx, pre;
+  uint32_t whole;
 };
 constexpr uint32_t kInfos = 8;  // stages
+// Of a row: where its window begins, and its node's line.
+struct RowMask {
+  int wf, node;
+};
 
 template <int D, bool RAW>
 struct TreeSmem {
@@ -92,39 +96,38 @@ struct TreeSmem {
   static constexpr int kKStages = RAW && D == 64 ? 4 : 2;
   static constexpr int kVCodes = kK + kKStages * kKTile;  // RAW: two tiles of V codes
   static constexpr int kInfo = kVCodes + (RAW ? 2 * kCodes : 0);
-  static constexpr int kXch = kInfo + static_cast<int>(kInfos * sizeof(TileInfo));
-  static constexpr int kMl = kXch + 2 * 16 * 32 * 8;  // [stream][lane] reference and sum
-  static constexpr int kBars = kMl + 2 * 128 * 8;
+  static constexpr int kMl = kInfo + static_cast<int>(kInfos * sizeof(TileInfo));  // [stream][lane] reference and sum
+  static constexpr int kRow = kMl + 2 * 128 * 8;  // [stream][lane] RowMask
+  static constexpr int kBars = kRow + 2 * 128 * static_cast<int>(sizeof(RowMask));
   static constexpr int kMisc = kBars + 320;  // TMEM base, abort flag
   static constexpr int kBytes = kMisc + 16;
 };
-// Barriers and the arrivals that complete a phase: Q and P (by stream) the stream's eight
+// Barriers and the arrivals that complete a phase: Q and P (by stream) the stream's four
 // softmax warps; Info the copying warps (RAW) or the converting ones; K full one thread and its bytes (RAW) or four
 // warps; V codes full a thread and its bytes, free the four warps; V full four warps; All
-// the 16 softmax warps; K and V free two commits of the tensor cores (one of each stream's
+// the eight softmax warps; K and V free two commits of the tensor cores (one of each stream's
 // issuer, or two of the one whose tile it is); S, O and Drain one.
 enum { kTQ = 0, kTP = 2, kTInfo = 4, kTKFull = 12, kTVCFull = 16, kTVCFree = 18, kTVFull = 20,
        kTAll = 22, kTKFree = 23, kTVFree = 27, kTS = 29, kTO = 31, kTDrain = 33, kTreeBars = 35 };
 template <bool RAW>
 __device__ __forceinline__ int tree_bar_count(int i) {
-  return i < kTInfo    ? 8
+  return i < kTInfo    ? 4
          : i < kTKFull ? (RAW ? 2 : 8)
          : i < kTVCFull ? (RAW ? 1 : 4)
          : i < kTVCFree ? 1
          : i < kTAll ? 4
-         : i < kTKFree ? 16
+         : i < kTKFree ? 8
          : i < kTS ? 2
                    : 1;
 }
 
-// An item's rows over the streams: wide, or narrow with `parts` shares of a tile's tokens
-// by lane.
+// An item's rows over the streams: wide, or narrow, where a share of `lanes` lanes weighs
+// lanes / 128 of a tile's tokens.
 struct Streams {
   bool wide;
-  int lanes;  // lanes of a share
+  int lanes;
   __device__ __forceinline__ explicit Streams(const RowBlock& r)
-      : wide(r.rows > 128), lanes(r.rows <= 64 ? 64 : 128) {}
-  __device__ __forceinline__ bool shared() const { return lanes == 64; }
+      : wide(r.rows > 128), lanes(r.rows <= 32 ? 32 : (r.rows <= 64 ? 64 : 128)) {}
   // tiles of stream t among n
   __device__ __forceinline__ int tiles(int t, int n) const { return wide ? n : (n + 1 - t) >> 1; }
 };
@@ -161,7 +164,10 @@ struct OpenItem {
     table = a.block_tables + static_cast<long>(im.r.b) * a.max_blocks;
   }
   __device__ __forceinline__ int token_of(int tile) const { return first_token(np, skip, last - tile); }
-  // whether every row sees the whole tile at token j0
+  // whether every row sees the group of 32 tokens at jw, the whole tile at token j0
+  __device__ __forceinline__ bool sees(int jw) const {
+    return (jw >= all_lo && jw + 32 <= ctx) || jw + 32 <= seen.pre;
+  }
   __device__ __forceinline__ bool whole(int j0) const {
     return (j0 >= all_lo && j0 + kT <= ctx) || j0 + kT <= seen.pre;
   }
@@ -274,11 +280,19 @@ __device__ __forceinline__ void copy_tiles(const PrefillArgs& a, const PlanView&
           info->ks[i * 32 + lane] = there ? now.s[i] : 0.f;
           if (bias) {
             const int p = j0 + i * 32 + lane;
-            info->pos[i * 32 + lane] =
-                p < o.ctx || p >= o.L ? p : o.ctx + __ldg(tv.depth + o.qlo + p - o.ctx);
+            info->pos[i * 32 + lane] = static_cast<float>(
+                p < o.ctx || p >= o.L ? p - o.ctx : __ldg(tv.depth + o.qlo + p - o.ctx));
           }
-          if (lane == 0) info->valid[i] = held[i];
+          if (lane == 0) {
+            info->valid[i] = held[i];
+            info->seen[i] = o.sees(j0 + i * 32) && held[i] == 0xFFFFFFFFu;
+          }
         }
+      }
+      if (!V && lane == 0) {
+        info->j0 = j0;
+        info->ctx = o.ctx;
+        info->pre = o.seen.pre;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + kTInfo + g % kInfos);
@@ -305,10 +319,18 @@ __device__ __forceinline__ void put_k_info(const TreeView& tv, const OpenItem& o
   info->ks[dw * 32 + lane] = scale;
   if (bias) {
     const int p = j + lane;
-    info->pos[dw * 32 + lane] =
-        p < o.ctx || p >= o.L ? p : o.ctx + __ldg(tv.depth + o.qlo + p - o.ctx);
+    info->pos[dw * 32 + lane] = static_cast<float>(
+        p < o.ctx || p >= o.L ? p - o.ctx : __ldg(tv.depth + o.qlo + p - o.ctx));
   }
-  if (lane == 0) info->valid[dw] = valid;
+  if (lane == 0) {
+    info->valid[dw] = valid;
+    info->seen[dw] = o.sees(j) && valid == 0xFFFFFFFFu;
+    if (dw == 0) {
+      info->j0 = j;
+      info->ctx = o.ctx;
+      info->pre = o.seen.pre;
+    }
+  }
 }
 // V's part; bad: bits of the tokens whose codes are not finite.  A scale counts as finite
 // where its largest code is (append writes no others).
@@ -495,52 +517,47 @@ __device__ __forceinline__ void convert_loaded(const PrefillArgs& a, const PlanV
   }
 }
 
-// The tokens of the 32 from jw on that a row sees (of those that exist): the window and the
-// prefix ahead of the tree, and the nodes on its line.
-__device__ __noinline__ uint32_t seen_bits(int jw, int wf, int ctx, int pre,
-                                           const uint32_t* line) {
-  uint32_t see = word_bits(jw, wf, ctx) | word_bits(jw, 0, pre);
+// The tokens of group w of a tile that a row sees: the window and the prefix ahead of the
+// tree, and the nodes on its line.  Out of line, with all that it needs in shared memory:
+// few groups are not seen whole, and registers are short.
+__device__ __noinline__ uint32_t seen_bits(const TileInfo* info, int w, const RowMask* row,
+                                           const uint32_t* lines) {
+  const int jw = info->j0 + w * 32, ctx = info->ctx;
+  uint32_t see = word_bits(jw, row->wf, ctx) | word_bits(jw, 0, info->pre);
   const int o = jw - ctx;  // the first token as a node
   if (o > -32) {
+    const uint32_t* line = lines + static_cast<long>(row->node) * kLineWords;
     const int w0 = max(o, 0) >> 5;
     if (o < 0) see |= __ldg(line) << (-o);
     else if (w0 < kLineWords)
       see |= __funnelshift_r(__ldg(line + w0), w0 + 1 < kLineWords ? __ldg(line + w0 + 1) : 0u,
                              o & 31);
   }
-  return see;
+  return see & info->valid[w];
+}
+// Whether a row saw, among groups [w, end) of a tile, codes of V that are not finite.
+__device__ __noinline__ bool saw_nan(const TileInfo* info, int w, int end, const RowMask* row,
+                                     const uint32_t* lines) {
+  uint32_t bad = 0;
+  for (; w < end; ++w) bad |= info->cbad[w] ? info->cbad[w] & seen_bits(info, w, row, lines) : 0u;
+  return bad != 0;
 }
 
-// Waits for the word at `from` to carry `tag`, for all lanes of a warp; its value.  Gives up
-// as tc_wait does.
-__device__ __forceinline__ bool poll_word(uint32_t from, uint32_t tag, float& value) {
-  uint64_t v;
-  asm volatile("ld.volatile.shared.b64 %0, [%1];" : "=l"(v) : "r"(from) : "memory");
-  value = __uint_as_float(static_cast<uint32_t>(v));
-  return __all_sync(0xffffffffu, static_cast<uint32_t>(v >> 32) == tag) != 0;
+// 32 registers that a tcgen05.ld filled: what uses them stays behind the wait before this.
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]));
+  asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
-__device__ __noinline__ bool take_word_slow(uint32_t from, uint32_t tag, float* value,
-                                            int* abort_flag, uint32_t* err) {
-  const long long t0 = clock64();
-  while (!poll_word(from, tag, *value)) {
-    if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(abort_flag) != 0 ||
-                                    clock64() - t0 > kWaitLimitCycles)) {
-      raise_error(err, FP8PA_DEVERR_TIMEOUT);
-      *reinterpret_cast<volatile int*>(abort_flag) = 1;
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ bool take_word(uint32_t from, uint32_t tag, float& value,
-                                          int* abort_flag, uint32_t* err) {
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (poll_word(from, tag, value)) return true;
-  float v;
-  const bool good = take_word_slow(from, tag, &v, abort_flag, err);
-  value = v;
-  return good;
+
+__device__ __forceinline__ uint64_t u2_pack(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // One lane of a whole warp, the same each time.  Under a branch on it the operands of an MMA
@@ -585,8 +602,6 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
     for (int i = 0; i < kTreeBars; ++i) mbar_init(bars + i, tree_bar_count<RAW>(i));
     fence_barrier_init();
   }
-  for (int i = tid; i < 2 * 16 * 32; i += kTreeThreads<RAW>)  // no tag is zero
-    reinterpret_cast<uint64_t*>(sm + SM::kXch)[i] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -700,21 +715,21 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
     }
   } else if (RAW && warp >= kIssue + 2) {
     if constexpr (RAW) {
-      const bool bias = VAR > 0 && a.slopes;
+      constexpr bool bias = VAR > 0;
       if (warp == kIssue + 2)
         copy_tiles<D, false>(a, pv, tv, sm, abort_flag, &mk, it0, u0, u1, lane, bias);
       else
         copy_tiles<D, true>(a, pv, tv, sm, abort_flag, &mv, it0, u0, u1, lane, bias);
     }
-  } else if (warp >= 16) {
-    const int part = warp - 16;
+  } else if (warp >= kTreeConv) {
+    const int part = warp - kTreeConv;
     if constexpr (RAW) {
       if (a.fmt == FP8PA_E4M3)
         convert_raw<D, FP8PA_E4M3>(a, sm, abort_flag, u1 - u0, part, lane);
       else
         convert_raw<D, FP8PA_E5M2>(a, sm, abort_flag, u1 - u0, part, lane);
     } else {
-      const bool bias = VAR > 0 && a.slopes;
+      constexpr bool bias = VAR > 0;
       if (a.fmt == FP8PA_INT8)
         convert_loaded<D, FP8PA_INT8, false>(a, pv, tv, sm, abort_flag, it0, u0, u1, part, lane,
                                              bias);
@@ -727,25 +742,15 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
     }
   } else {
     // ================================================= softmax warps
-    const int t = warp >> 3, half = (warp >> 2) & 1;  // stream, and half of a share's tokens
-    const int rl = (warp & 3) * 32 + lane;            // lane of the tile
+    // A thread per lane: four warps a stream.  (Two threads a lane, each with half of the
+    // tokens, agreed on a reference through shared memory: 195 us where this takes %TIME%.)
+    const int t = warp >> 2;                // stream
+    const int rl = (warp & 3) * 32 + lane;  // lane of the tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + t * kT + lanes, to = tmem + 256 + t * 128 + lanes;
-    const uint32_t xch = smem_u32(sm + SM::kXch) + (warp * 32 + lane) * 8;
     float2* ml = reinterpret_cast<float2*>(sm + SM::kMl);
-    uint32_t nx = 0, na = 0;
-    // Trade one value per row with the other warp of the rows: a word with a running tag,
-    // which the other lane polls (a barrier's polls take three times as long).  The slots
-    // alternate: one is written again only after the other lane was seen a trade further.
-    auto trade = [&](float mine, float& other) {
-      ++nx;
-      const uint32_t slot = xch + (nx & 1) * (16 * 32 * 8);
-      asm volatile("st.volatile.shared.b64 [%0], %1;" ::"r"(slot),
-                   "l"(static_cast<uint64_t>(nx) << 32 | __float_as_uint(mine))
-                   : "memory");
-      const uint32_t from = slot + (half ? -4 * 32 * 8 : 4 * 32 * 8);
-      return take_word(from, nx, other, abort_flag, a.err);
-    };
+    const bool cap_quick = a.cap <= kCapFast;
+    uint32_t na = 0;
     auto sync_all = [&]() {  // all softmax warps
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + kTAll);
@@ -776,30 +781,28 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
       const long grow = qrow * a.hq + h;  // row of q and out
       float ref = kNegBig, l = 0.f;
       if (mine > 0) {
-        float zs;
+        // ---- the rows of q, each normalised by a power of two, into shared memory (every S
+        // of the stream's previous item is done: its last was read); 8 rows x 64 bytes a load
+        constexpr int kTop = RAW ? 8 : 14;  // exponent of the normalised row
+        int er = 0;
         {
-          // ---- the rows of q, each normalised by a power of two, into shared memory
-          // (every S of the stream's previous item is done: its last was read)
           const float sgn = a.sm_scale < 0.f ? -1.f : 1.f;
           const bool st = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
           const float* kc = a.k_scale + static_cast<long>(im.kvh) * D;
-          constexpr int kTop = RAW ? 8 : 14;  // exponent of the normalised row
           const int r8 = lane & 7, c4 = lane >> 3;
-          uint4 raw[2][D / 32];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
+          uint8_t* dst = sm + SM::kQ + t * SM::kHalf;
+#pragma unroll 2
+          for (int y = 0; y < 4; ++y) {
+            const int row = (warp & 3) * 32 + y * 8 + r8;
             int qy, hy;
-            query_of((warp & 3) * 32 + (half * 2 + y) * 8 + r8, qy, hy);
+            query_of(row, qy, hy);
             const uint4* src = reinterpret_cast<const uint4*>(
                                    a.q + ((static_cast<long>(im.r.qlo) + qy) * a.hq + hy) * D) + c4;
+            uint4 raw[D / 32];
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x) raw[y][x] = __ldg(src + x * 4);
-          }
-          int eq[2];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
+            for (int x = 0; x < D / 32; ++x) raw[x] = __ldg(src + x * 4);
             auto get = [&](int x, float (&f)[8]) {
-              const uint32_t w[4] = {raw[y][x].x, raw[y][x].y, raw[y][x].z, raw[y][x].w};
+              const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 f[2 * e] = __uint_as_float(w[e] << 16) * sgn;
@@ -821,10 +824,9 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
             // (129 for an infinity: such a row is NaN)
-            eq[y] = amax > 0.f ? exp_above(amax) : 0;
-            const float fq = exp2i(kTop - eq[y]);
-            const int row = (warp & 3) * 32 + (half * 2 + y) * 8 + r8;
-            uint8_t* dst = sm + SM::kQ + t * SM::kHalf;
+            const int eq = amax > 0.f ? exp_above(amax) : 0;
+            if (c4 == y) er = eq;  // this lane's row
+            const float fq = exp2i(kTop - eq);
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) {
               float f[8];
@@ -836,8 +838,7 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   hi[e] = f32x2_to_codes2<FP8PA_E4M3>(f[2 * e], f[2 * e + 1]);
-                  const uint32_t back = codes2_to_f16x2<FP8PA_E4M3>(hi[e]);
-                  const float2 b = __half22float2(h2(back));
+                  const float2 b = __half22float2(h2(codes2_to_f16x2<FP8PA_E4M3>(hi[e])));
                   lo[e] = f32x2_to_codes2<FP8PA_E4M3>(f[2 * e] - b.x, f[2 * e + 1] - b.y);
                 }
                 const int c8 = x * 4 + c4;  // 8 dims: half a 16-byte chunk
@@ -856,47 +857,31 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(bars + kTQ + t);
-          // this lane's row: group lane / 8 of four, in this warp's half or the other's
-          float own = static_cast<float>((lane >> 3) & 1 ? eq[1] : eq[0]), theirs;
-          if (!trade(own, theirs)) {
-            ok = false;
-            break;
-          }
-          const int er = static_cast<int>((lane >> 4) == half ? own : theirs);
-          // log2-domain factor of a raw score (capped scores: see cap_in)
-          zs = er > 128 ? __int_as_float(0x7FC00000)
-                        : fabsf(a.sm_scale) * exp2i(er - kTop) * (VAR == 2 ? a.cap_in : kLog2e);
-          // (VAR 0 multiplies a masked -inf by the factor: not zero)
-          if (VAR == 0 && er <= 128) zs = fmaxf(zs, 1e-37f);
         }
-        const int ctx = im.r.pA, pre = im.r.pre;
-        const uint32_t* line = tv.line + qrow * kLineWords;
-        const int pos = ctx + __ldg(tv.depth + qrow), wf = window_first(a.window, pos);
-        const int wB = window_first(a.window, im.r.L - 1);  // no row's window begins behind it
+        // log2-domain factor of a raw score (capped scores: see cap_in)
+        float zs = fabsf(a.sm_scale) * exp2i(er - kTop) * (VAR == 2 ? a.cap_in : kLog2e);
+        if (VAR == 0) zs = fmaxf(zs, 1e-37f);  // (it multiplies a masked -inf: not zero)
+        if (er > 128) zs = __int_as_float(0x7FC00000);
+        const int depth = __ldg(tv.depth + qrow);
+        RowMask* const row = reinterpret_cast<RowMask*>(sm + SM::kRow) + t * 128 + rl;
+        *row = RowMask{window_first(a.window, im.r.pA + depth), static_cast<int>(qrow)};
         const float slope = (VAR > 0 && a.slopes) ? __ldg(a.slopes + h) * kLog2e : 0.f;
         const float cap_log2 = VAR == 2 ? a.cap * kLog2e : 0.f;
+        // the bias of a token is slope pos + b0 (and the cap, where its tanh is taken from 1)
+        const float b0 = (cap_quick ? cap_log2 : 0.f) - slope * static_cast<float>(depth);
         // the thread's groups of 32 tokens: first, and how many
-        const int ng = sp.shared() ? 1 : 2;
-        const int g0 = sp.shared() ? (rl >> 6) * 2 + half : half * 2;
-        const uint32_t first_tile = g + (sp.wide ? 0 : t);
-        auto token_of = [&](uint32_t gt) {  // first token of tile gt
-          return first_token(im.r.np, im.r.skip, im.r.count - 1 - im.t0 - static_cast<int>(gt - g));
-        };
+        const int ng = sp.lanes >> 5, g0 = rl / sp.lanes * ng;
+        const uint32_t first_tile = g + (sp.wide ? 0 : t), step = sp.wide ? 1 : 2;
         // makes the row NaN where it saw codes of tile gt that are not finite
         auto late_nan = [&](uint32_t gt) {
-          const TileInfo& info = infos[gt % kInfos];
-          const uint4 c = *reinterpret_cast<const uint4*>(info.cbad);
-          if ((c.x | c.y | c.z | c.w) == 0) return;
-          for (int w = 0; w < ng; ++w) {
-            const int gw = g0 + w;
-            if (info.cbad[gw] & info.valid[gw] &
-                seen_bits(token_of(gt) + gw * 32, wf, ctx, pre, line))
-              l = __int_as_float(0x7FC00000);
-          }
+          const TileInfo* info = infos + gt % kInfos;
+          const uint4 c = *reinterpret_cast<const uint4*>(info->cbad);
+          if ((c.x | c.y | c.z | c.w) != 0 && saw_nan(info, g0, g0 + ng, row, tv.line))
+            l = __int_as_float(0x7FC00000);
         };
+        uint32_t ra[32];  // a group's scores
         for (int x = 0; x < mine; ++x) {
-          const uint32_t gt = first_tile + (sp.wide ? x : 2 * x);
-          const int j0 = token_of(gt) + g0 * 32;
+          const uint32_t gt = first_tile + step * x;
           // (S is issued once the tile's info is complete)
           if (!wait_warp(kTS + t, ns & 1)) {
             ok = false;
@@ -904,107 +889,77 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           }
           tc_fence_after();
           // (what the tile before brought that is not finite is known by now)
-          if (x > 0) late_nan(gt - (sp.wide ? 1 : 2));
+          if (x > 0) late_nan(gt - step);
           const TileInfo& info = infos[gt % kInfos];
-          const uint32_t all = info.valid[g0] & info.valid[g0 + ng - 1];
-          // whether every row of the warp sees all of the thread's tokens
-          const bool whole =
-              ((j0 >= wB && j0 + ng * 32 <= ctx) || (VAR == 0 && j0 + ng * 32 <= pre)) &&
-              all == 0xFFFFFFFFu && (VAR < 2 || a.cap <= kCapFast);
-          // ---- a bound of z + e over the row's tokens.  The scores of the first group
-          // stay in registers, those of the second go back to TMEM.
-          uint32_t raw[2][16];
-          float bound = __int_as_float(0xff800000);
-          auto find = [&](auto masked, int w) {
-            const int gw = g0 + w, jw = j0 + w * 32;
-            const uint32_t sc = ts + gw * 32;
-            tmem_ld16(sc, raw[0]);
-            tmem_ld16(sc + 16, raw[1]);
-            uint32_t m = info.valid[gw];
-            if constexpr (masked.value) {
-              m &= seen_bits(jw, wf, ctx, pre, line);
-            }
-            if (m & info.bad[gw]) l = __int_as_float(0x7FC00000);
-            const float4* ks = reinterpret_cast<const float4*>(info.ks + gw * 32);
-            const float e = static_cast<float>(info.ev[gw]);
+          uint4 sc[8];  // a group's scales, loaded beside its scores
+          auto load = [&](int w, const float* scale) {
+            tmem_ld32(ts + w * 32, ra);
+            const uint32_t at = smem_u32(scale + w * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sc[i] = lds128(at + i * 16);
             tmem_ld_wait();
-            tmem_landed(raw[0]);
-            tmem_landed(raw[1]);
+            tmem_landed(ra);
+          };
+          // ---- a bound of z + e over the row's tokens; the scores go back to TMEM
+          float bound = __int_as_float(0xff800000);
+#pragma unroll 1
+          for (int w = g0; w < g0 + ng; ++w) {
+            const uint32_t whole = info.seen[w], bad = info.bad[w];
+            load(w, info.ks);
+            const uint64_t zs2 = f2_pack(zs, zs), sl2 = f2_pack(slope, slope);
+            const uint64_t b02 = f2_pack(b0, b0);
+#pragma unroll
+            for (int i4 = 0; i4 < 8; ++i4) {
+              float4 p4;
+              if constexpr (VAR > 0) p4 = reinterpret_cast<const float4*>(info.pos + w * 32)[i4];
+#pragma unroll
+              for (int i2 = 0; i2 < 2; ++i2) {
+                uint32_t* v = ra + i4 * 4 + i2 * 2;
+                uint64_t z = f2_mul(u2_pack(v[0], v[1]),
+                                    i2 ? u2_pack(sc[i4].z, sc[i4].w) : u2_pack(sc[i4].x, sc[i4].y));
+                float y0, y1;
+                if constexpr (VAR > 0) {
+                  const uint64_t b =
+                      f2_fma(sl2, i2 ? f2_pack(p4.z, p4.w) : f2_pack(p4.x, p4.y), b02);
+                  if constexpr (VAR == 1) {
+                    z = f2_fma(z, zs2, b);
+                  } else if (cap_quick) {  // cap tanh(z / cap) = cap - 2 cap / (2^x + 1)
+                    f2_unpack(f2_mul(z, zs2), y0, y1);
+                    f2_unpack(f2_add(f2_pack(ex2(y0), ex2(y1)), f2_pack(1.f, 1.f)), y0, y1);
+                    z = f2_fma(f2_pack(rcp_fast(y0), rcp_fast(y1)),
+                               f2_pack(-2.f * cap_log2, -2.f * cap_log2), b);
+                  } else {
+                    f2_unpack(f2_mul(z, zs2), y0, y1);
+                    y0 = a.cap * tanh_f32(y0 * a.tanh_in) * kLog2e;
+                    y1 = a.cap * tanh_f32(y1 * a.tanh_in) * kLog2e;
+                    z = f2_add(f2_pack(y0, y1), b);
+                  }
+                }
+                f2_unpack(z, y0, y1);
+                v[0] = __float_as_uint(y0);
+                v[1] = __float_as_uint(y1);
+              }
+            }
+            if (!whole || bad) {
+              const uint32_t m = seen_bits(&info, w, row, tv.line);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (((m >> i) & 1) == 0) ra[i] = 0xff800000u;
+              if (m & bad) l = __int_as_float(0x7FC00000);
+            }
             float m4[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) m4[y] = __int_as_float(0xff800000);
-            // the bias of tokens 2 i, 2 i + 1 of the group: -slope (pos - j)
-            // (VAR 2: and the cap, less what the tanh leaves of it)
-            const float b0 = VAR > 0 ? fmaf(slope, static_cast<float>(jw - pos), cap_log2) : 0.f;
-            const uint64_t zs2 = f2_pack(zs, zs), bias = f2_pack(b0, b0 + slope);
-            const uint64_t by2 = f2_pack(2.f * slope, 2.f * slope);
 #pragma unroll
-            for (int i4 = 0; i4 < 8; ++i4) {
-              const float4 k4 = ks[i4];
-#pragma unroll
-              for (int i2 = 0; i2 < 2; ++i2) {
-                const int i = i4 * 2 + i2;
-                uint32_t* rr = &raw[i / 8][(i % 8) * 2];
-                uint64_t z = f2_mul(f2_pack(__uint_as_float(rr[0]), __uint_as_float(rr[1])),
-                                    i2 ? f2_pack(k4.z, k4.w) : f2_pack(k4.x, k4.y));
-                float y[2];
-                if constexpr (VAR > 0) {
-                  if constexpr (masked.value) {
-                    f2_unpack(f2_mul(z, zs2), y[0], y[1]);
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                      if constexpr (VAR == 2) y[v] = a.cap * tanh_f32(y[v] * a.tanh_in) * kLog2e;
-                      if (slope != 0.f)
-                        y[v] = fmaf(-slope, static_cast<float>(pos - info.pos[gw * 32 + 2 * i + v]),
-                                    y[v]);
-                    }
-                  } else {
-                    const float fi = static_cast<float>(i);
-                    const uint64_t b = f2_fma(by2, f2_pack(fi, fi), bias);
-                    if constexpr (VAR == 1) {
-                      z = f2_fma(z, zs2, b);
-                    } else {  // cap tanh(z / cap) = cap - 2 cap / (2^x + 1), cap in the bias
-                      f2_unpack(f2_mul(z, zs2), y[0], y[1]);
-                      f2_unpack(f2_add(f2_pack(ex2(y[0]), ex2(y[1])), f2_pack(1.f, 1.f)), y[0],
-                                y[1]);
-                      z = f2_fma(f2_pack(rcp_fast(y[0]), rcp_fast(y[1])),
-                                 f2_pack(-2.f * cap_log2, -2.f * cap_log2), b);
-                    }
-                    f2_unpack(z, y[0], y[1]);
-                  }
-                } else {
-                  f2_unpack(z, y[0], y[1]);
-                }
-                if constexpr (masked.value) {
-                  y[0] = (m >> (2 * i)) & 1 ? y[0] : __int_as_float(0xff800000);
-                  y[1] = (m >> (2 * i + 1)) & 1 ? y[1] : __int_as_float(0xff800000);
-                }
-                m4[i & 3] = max3(m4[i & 3], y[0], y[1]);
-                rr[0] = __float_as_uint(y[0]);
-                rr[1] = __float_as_uint(y[1]);
-              }
-            }
-            if (w > 0) {
-              tmem_st16(sc, raw[0]);
-              tmem_st16(sc + 16, raw[1]);
-            }
+            for (int i = 0; i < 16; ++i)
+              m4[i & 3] = max3(m4[i & 3], __uint_as_float(ra[2 * i]), __uint_as_float(ra[2 * i + 1]));
+            tmem_st32(ts + w * 32, ra);
             const float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-            bound = fmaxf(bound, fmaf(mx, VAR > 0 ? 1.f : zs, e));
-          };
-#pragma unroll 1
-          for (int w = ng - 1; w >= 0; --w) {
-            if (whole) find(std::false_type{}, w);
-            else find(std::true_type{}, w);
+            bound = fmaxf(bound, fmaf(mx, VAR > 0 ? 1.f : zs, static_cast<float>(info.ev[w])));
           }
-          if (ng > 1) tmem_st_wait();
-          // ---- the reference, shared by the lane's two threads: where the bound passed it
-          // by 2^kTau it moves, and with it the sums and O
-          float other;
-          if (!trade(bound, other)) {
-            ok = false;
-            break;
-          }
-          bound = fmaxf(bound, other);
+          tmem_st_wait();
+          // ---- the reference: where the bound passed it by 2^kTau it moves, and with it the
+          // sums and O
           float al = 1.f;
           if (bound > ref + kTau) {
             al = ex2(ref - bound);
@@ -1013,66 +968,48 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           if (__any_sync(0xffffffffu, al != 1.f)) {
             l *= al;
             if (x > 0) {
-              // (the product of the stream's tile before came ahead of this one's scores)
+              // (the product of the stream's tile before is over: its S waited for it)
 #pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                const uint32_t at = to + half * (D / 2) + c * 8;
-                uint32_t o[8];
-                tmem_ld8(at, o);
+              for (int c = 0; c < D / 32; ++c) {
+                tmem_ld32(to + c * 32, ra);
                 tmem_ld_wait();
-                tmem_landed(o);
+                tmem_landed(ra);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                tmem_st8(at, o);
+                for (int i = 0; i < 32; ++i) ra[i] = __float_as_uint(__uint_as_float(ra[i]) * al);
+                tmem_st32(to + c * 32, ra);
               }
             }
           }
           // ---- P times V's scale, and the sum of P
 #pragma unroll 1
-          for (int w = 0; w < ng; ++w) {
-            const int gw = g0 + w;
-            const uint32_t sc = ts + gw * 32;
-            if (w > 0) {
-              tmem_ld16(sc, raw[0]);
-              tmem_ld16(sc + 16, raw[1]);
-              tmem_ld_wait();
-              tmem_landed(raw[0]);
-              tmem_landed(raw[1]);
-            }
-            const float4* vs = reinterpret_cast<const float4*>(info.vs + gw * 32);
-            const float e = static_cast<float>(info.ev[gw]);
+          for (int w = g0; w < g0 + ng; ++w) {
+            const float e = static_cast<float>(info.ev[w]);
+            load(w, info.vs);
             const float c0 = kShift - ref + e, f = VAR > 0 ? 1.f : zs;
             const uint64_t f2 = f2_pack(f, f), c02 = f2_pack(c0, c0);
             uint64_t la = 0, lb = 0;  // (0.f, 0.f)
+            uint32_t pw[16];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t pw[8];
-#pragma unroll
-              for (int i2 = 0; i2 < 4; ++i2) {
-                const float4 v4 = vs[c * 4 + i2];
-#pragma unroll
-                for (int i1 = 0; i1 < 2; ++i1) {
-                  const int i = i2 * 2 + i1;
-                  const uint64_t z =
-                      f2_pack(__uint_as_float(raw[c][2 * i]), __uint_as_float(raw[c][2 * i + 1]));
-                  float p, q;
-                  f2_unpack(VAR > 0 ? f2_add(z, c02) : f2_fma(z, f2, c02), p, q);
-                  const uint64_t e2 = f2_pack(ex2(p), ex2(q));
-                  if (i & 1) lb = f2_add(lb, e2);
-                  else la = f2_add(la, e2);
-                  f2_unpack(f2_mul(e2, i1 ? f2_pack(v4.z, v4.w) : f2_pack(v4.x, v4.y)), p, q);
-                  pw[i] = pack_half2(p, q);
-                }
-              }
-              tmem_st8(sc + c * 8, pw);
+            for (int i = 0; i < 16; ++i) {
+              const uint4 v4 = sc[i >> 1];
+              const uint64_t z = u2_pack(ra[2 * i], ra[2 * i + 1]);
+              float p, q;
+              f2_unpack(VAR > 0 ? f2_add(z, c02) : f2_fma(z, f2, c02), p, q);
+              const uint64_t e2 = f2_pack(ex2(p), ex2(q));
+              if (i & 1) lb = f2_add(lb, e2);
+              else la = f2_add(la, e2);
+              f2_unpack(f2_mul(e2, i & 1 ? u2_pack(v4.z, v4.w) : u2_pack(v4.x, v4.y)), p, q);
+              pw[i] = pack_half2(p, q);
             }
+            tmem_st16(ts + w * 32, pw);
             float y, z;
             f2_unpack(f2_add(la, lb), y, z);
             l = fmaf(y + z, ex2(-e), l);
           }
-          if (sp.shared()) {  // nothing for the other share's tokens
+          if (ng < 4) {  // nothing for the other shares' tokens
             const uint32_t zero[16] = {};
-            tmem_st16(ts + (g0 ^ 2) * 32, zero);
+            for (int w = 0; w < 4; ++w)
+              if (w < g0 || w >= g0 + ng) tmem_st16(ts + w * 32, zero);
           }
           tmem_st_wait();
           tc_fence_before();
@@ -1080,24 +1017,17 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           if (lane == 0) mbar_arrive(bars + kTP + t);
           ++ns;
         }
-        if (!ok) break;
-        // the last product, and the row's sum
-        float other;
-        if (!wait_warp(kTO + t, (ns - 1) & 1)) {
+        // the last product
+        if (!ok || !wait_warp(kTO + t, (ns - 1) & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        late_nan(first_tile + (sp.wide ? mine - 1 : 2 * (mine - 1)));
-        if (!trade(l, other)) {
-          ok = false;
-          break;
-        }
-        l += other;
+        late_nan(first_tile + step * (mine - 1));
       }
       g += n;
 
-      // ---- the block's result, or this range's piece of it: half the dims each
+      // ---- the block's result, or this range's piece of it
       const bool piece = im.t0 > 0 || im.t1 < im.r.count;
       const int slot = blockIdx.x * 2 + (im.t0 > 0 ? 0 : 1);
       const bool stat = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
@@ -1140,17 +1070,15 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
       if (sp.wide) {
         const float inv = piece ? 1.f : (l == 0.f ? 0.f : 1.f / l);
 #pragma unroll 1
-        for (int c0 = 0; c0 < D / 32; ++c0) {
-          const int c = half * (D / 32) + c0;
+        for (int c = 0; c < D / 16; ++c) {
           float f[16];
           take(c, inv, f);
           if (live) put(c, f);
         }
-        if (piece && live && half == 0)
-          pv.ml[static_cast<long>(slot) * kRows + r] = make_float2(ref, l);
+        if (piece && live) pv.ml[static_cast<long>(slot) * kRows + r] = make_float2(ref, l);
       } else {
-        // the row's partial results: of both streams, and of both shares of the lanes
-        if (half == 0) ml[t * 128 + rl] = make_float2(ref, l);
+        // the row's partial results: of both streams, and of the shares of the lanes
+        ml[t * 128 + rl] = make_float2(ref, l);
         if (!sync_all()) {
           ok = false;
           break;
@@ -1182,21 +1110,20 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
         const bool both = n > 1;  // whether stream 1 had a tile
         if (t == 1 && both) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < D / 32; ++c0) {
+          for (int c = 0; c < D / 16; ++c) {
             float f[16];
-            take(half * (D / 32) + c0, scale, f);
-            leave(half * (D / 32) + c0, f);
+            take(c, scale, f);
+            leave(c, f);
           }
         }
         if (!sync_all()) {
           ok = false;
           break;
         }
-        if (sp.shared()) {
-          if (t == 0 && rl >= 64) {
+        if (sp.lanes < 128) {
+          if (t == 0 && rl >= sp.lanes) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < D / 32; ++c0) {
-              const int c = half * (D / 32) + c0;
+            for (int c = 0; c < D / 16; ++c) {
               float f[16];
               take(c, scale, f);
               if (both) add(rl, c, f);
@@ -1210,16 +1137,14 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
         }
         if (t == 0 && rl < sp.lanes) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < D / 32; ++c0) {
-            const int c = half * (D / 32) + c0;
+          for (int c = 0; c < D / 16; ++c) {
             float f[16];
             take(c, scale, f);
             if (both) add(rl, c, f);
-            if (sp.shared()) add(rl + 64, c, f);
+            for (int y = rl + sp.lanes; y < 128; y += sp.lanes) add(y, c, f);
             if (live) put(c, f);
           }
-          if (piece && live && half == 0)
-            pv.ml[static_cast<long>(slot) * kRows + r] = make_float2(M, sum);
+          if (piece && live) pv.ml[static_cast<long>(slot) * kRows + r] = make_float2(M, sum);
         }
         if (!sync_all()) {  // the sums lie where the next item's q goes
           ok = false;
