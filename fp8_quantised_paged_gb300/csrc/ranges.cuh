@@ -11,9 +11,9 @@ namespace {
 
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Bound of the row blocks of a batch.
-inline int block_bound(int total_q, int batch, int G) {
-  return static_cast<int>((static_cast<long long>(total_q) * G + kRows - 1) / kRows) + batch;
+// Bound of a batch's blocks of `rows` rows.
+inline int block_bound(int total_q, int batch, int G, int rows = kRows) {
+  return static_cast<int>((static_cast<long long>(total_q) * G + rows - 1) / rows) + batch;
 }
 
 // Largest i in [0, n) with a[i] <= x (a nondecreasing, a[0] <= x).

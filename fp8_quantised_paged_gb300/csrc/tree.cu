@@ -29,8 +29,8 @@ __device__ __forceinline__ RowBlock make_tree_block(const Chunk& c, int b, int w
   r.n = c.n;
   r.L = c.L;
   r.pre = c.pre;
-  r.row0 = t * kRows;
-  r.rows = min(kRows, c.n * G - r.row0);
+  r.row0 = t * kTreeRows;
+  r.rows = min(kTreeRows, c.n * G - r.row0);
   r.pA = c.L - c.n;  // tokens ahead of the tree
   r.pB = c.L - 1;
   r.np = (c.pre + kT - 1) / kT;
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const PrefillAr
       const Chunk c = load_tree(a, b, &flag);
       if (flag) raise_error(a.err, flag);
       // overlapping or repeated offsets cannot add blocks beyond the bound
-      n = static_cast<int>((static_cast<long long>(c.n) * a.G + kRows - 1) / kRows);
+      n = static_cast<int>((static_cast<long long>(c.n) * a.G + kTreeRows - 1) / kTreeRows);
     }
     int ex;
     const int total = block_scan(n, &ex, s_warp);
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const PrefillAr
 
 size_t tree_layout(char* ws, int total_q, int batch, int G, int d, int ranges, PlanView* v,
                    uint32_t** line, int32_t** depth) {
-  const int nb = block_bound(total_q, batch, G);
+  const int nb = block_bound(total_q, batch, G, kTreeRows);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     char* p = ws + at;

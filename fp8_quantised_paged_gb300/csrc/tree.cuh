@@ -6,18 +6,18 @@
 //   the prefix leave them) and the nodes on i's line, itself among them
 //
 // Rows and work.  The (node, head) pairs of a request and KV head are rows, a TMEM lane
-// each, in blocks of 256; (row block, KV head, 128-token tile) units are cut into one
-// range per SM, and cut items leave pieces, as in the prefill (ranges.cuh, prefill.cu).  A
-// tree has few rows over a long context, so the cache's bytes bound it, and two things
-// keep the tensor cores and the softmax out of their way:
-//  - A block of at most 128 rows (narrow) runs as two streams, one on the even tiles and
-//    one on the odd ones, with scores, weights, sums and O of their own: while one is in its
-//    softmax the tensor cores work for the other.  A block of more rows (wide) has a stream
-//    for each half of its rows.
+// each, in blocks of 128; (row block, KV head, 128-token tile) units are cut into one range
+// per SM, and cut items leave pieces, as in the prefill (ranges.cuh, prefill.cu).  A tree
+// has few rows over a long context, so the cache's bytes bound it, and three things keep
+// the tensor cores and the softmax out of their way:
+//  - A block runs as two streams, one on the even tiles and one on the odd ones, with
+//    scores, weights, sums and O of their own.
+//  - A stream takes a tile by halves: while its softmax is at one half, the tensor cores
+//    multiply the other half's weights and make the next tile's scores in its place.
 //  - A block of at most 64 (or 32) rows stands twice (four times) in the lanes: each of the
-//    copies weighs its share of a tile's tokens, with zeros for the others'.  The product
-//    with V is the same, the softmax half (a quarter).
-// The partial results of a narrow block (2 to 8 a row) are added up at its end.
+//    copies weighs its share of a tile's tokens, with zeros for the others'.  The products
+//    are the same, the softmax is half (a quarter).
+// The partial results (2 to 8 a row) are added up at the block's end.
 //
 // Products.  S = Q K^T on FP8 tensor cores: the K codes as TMA lands them, q as two E4M3
 // terms hi + lo (exact for bf16 but for elements 2^-9 below the row's largest), the token's
@@ -32,7 +32,8 @@
 //
 // Roles: warps 0-3 and 4-7 the softmax of streams 0 and 1, a thread a lane; four warps
 // that convert V (RAW false: and four for K), one that issues MMAs for each stream, and
-// one that copies K's pages by TMA and lays out their scales, and one for V's.  Every wait is bounded.
+// (RAW) one that copies K's pages by TMA and lays out their scales, and one for V's.  Every
+// wait is bounded.
 #pragma once
 
 #include "prefill.cuh"
@@ -66,11 +67,12 @@ constexpr int kTreeIssue = kTreeConv + (RAW ? 4 : 8);
 template <bool RAW>
 constexpr int kTreeThreads = (kTreeIssue<RAW> + (RAW ? 4 : 2)) * 32;
 
-// Of a tile: its tokens' scales (V's relative to the 2^ev of their group of 32), their
-// positions behind the tokens ahead of the tree (for a distance bias), the groups' exponents, the tokens whose page
-// exists (held: as V's copies say it), those whose V's scale is not finite, and, written
-// with V in f16, those with codes that are not, where some row does not see the whole tile;
-// the groups that every row sees whole; the first token, and what masks it.
+// Of a tile: its tokens' scales (V's relative to the 2^ev of their group of 32) and their
+// positions behind the tokens ahead of the tree (for a distance bias), the groups'
+// exponents, the tokens whose page exists (held: as V's copies say it), those whose V's
+// scale is not finite, and, written with V in f16, those with codes that are not, where some
+// row does not see the whole tile; the groups that every row sees whole; the first token,
+// and what masks it.
 struct TileInfo {
   float ks[kT], vs[kT], pos[kT];
   int ev[4];
@@ -84,53 +86,50 @@ struct RowMask {
   int wf, node;
 };
 
+constexpr int kTreeRows = 128;  // rows of a block
+
 template <int D, bool RAW>
 struct TreeSmem {
   static constexpr int kHalf = 2 * kT * D;         // a 128-row f16 tile, or both terms of q
   static constexpr int kCodes = kT * D;            // a tile of codes
-  static constexpr int kQ = 0;                     // two streams; between items, sums of O
-  static constexpr int kV = 2 * kHalf;             // two tiles of V in f16
-  static constexpr int kK = 4 * kHalf;             // K: tiles of codes, or of f16
+  static constexpr int kQ = 0;                     // q; between items, sums of O
+  static constexpr int kV = kHalf;                 // two tiles of V in f16
+  static constexpr int kK = 3 * kHalf;             // K: tiles of codes, or of f16
   static constexpr int kKTile = RAW ? kCodes : kHalf;
   // (an even number: a stage then serves one stream within an item)
-  static constexpr int kKStages = RAW && D == 64 ? 4 : 2;
+  static constexpr int kKStages = RAW ? 4 : 2;
   static constexpr int kVCodes = kK + kKStages * kKTile;  // RAW: two tiles of V codes
   static constexpr int kInfo = kVCodes + (RAW ? 2 * kCodes : 0);
-  static constexpr int kMl = kInfo + static_cast<int>(kInfos * sizeof(TileInfo));  // [stream][lane] reference and sum
-  static constexpr int kRow = kMl + 2 * 128 * 8;  // [stream][lane] RowMask
-  static constexpr int kBars = kRow + 2 * 128 * static_cast<int>(sizeof(RowMask));
-  static constexpr int kMisc = kBars + 320;  // TMEM base, abort flag
+  static constexpr int kMl = kInfo + static_cast<int>(kInfos * sizeof(TileInfo));
+  static constexpr int kRow = kMl + 2 * 128 * 8;   // [lane] RowMask (kMl: [stream][lane] float2)
+  static constexpr int kExp = kRow + 128 * static_cast<int>(sizeof(RowMask));  // [lane] of q
+  static constexpr int kBars = kExp + 128 * 4;
+  static constexpr int kMisc = kBars + 320;        // TMEM base, abort flag
   static constexpr int kBytes = kMisc + 16;
 };
-// Barriers and the arrivals that complete a phase: Q and P (by stream) the stream's four
-// softmax warps; Info the copying warps (RAW) or the converting ones; K full one thread and its bytes (RAW) or four
-// warps; V codes full a thread and its bytes, free the four warps; V full four warps; All
-// the eight softmax warps; K and V free two commits of the tensor cores (one of each stream's
-// issuer, or two of the one whose tile it is); S, O and Drain one.
-enum { kTQ = 0, kTP = 2, kTInfo = 4, kTKFull = 12, kTVCFull = 16, kTVCFree = 18, kTVFull = 20,
-       kTAll = 22, kTKFree = 23, kTVFree = 27, kTS = 29, kTO = 31, kTDrain = 33, kTreeBars = 35 };
+// Barriers and the arrivals that complete a phase: Q the eight softmax warps; P (stream * 2
+// + half) the stream's four; Info the copying warps (RAW) or the converting ones; K full
+// one thread and its bytes (RAW) or four warps; V codes full a thread and its bytes, free
+// the four converting warps; V full four warps; All the eight softmax warps; K and V free, S
+// and O (stream * 2 + half) and Drain (by stream) a commit of the tensor cores.
+enum { kTQ = 0, kTP = 1, kTInfo = 5, kTKFull = 13, kTVCFull = 17, kTVCFree = 19, kTVFull = 21,
+       kTAll = 23, kTKFree = 24, kTVFree = 28, kTS = 30, kTO = 34, kTDrain = 38, kTreeBars = 40 };
 template <bool RAW>
 __device__ __forceinline__ int tree_bar_count(int i) {
-  return i < kTInfo    ? 4
-         : i < kTKFull ? (RAW ? 2 : 8)
+  return i < kTP        ? 8
+         : i < kTInfo   ? 4
+         : i < kTKFull  ? (RAW ? 2 : 8)
          : i < kTVCFull ? (RAW ? 1 : 4)
          : i < kTVCFree ? 1
-         : i < kTAll ? 4
-         : i < kTKFree ? 8
-         : i < kTS ? 2
-                   : 1;
+         : i < kTAll    ? 4
+         : i < kTKFree  ? 8
+                        : 1;
 }
 
-// An item's rows over the streams: wide, or narrow, where a share of `lanes` lanes weighs
-// lanes / 128 of a tile's tokens.
-struct Streams {
-  bool wide;
-  int lanes;
-  __device__ __forceinline__ explicit Streams(const RowBlock& r)
-      : wide(r.rows > 128), lanes(r.rows <= 32 ? 32 : (r.rows <= 64 ? 64 : 128)) {}
-  // tiles of stream t among n
-  __device__ __forceinline__ int tiles(int t, int n) const { return wide ? n : (n + 1 - t) >> 1; }
-};
+// The lanes of a share of a block's tokens.
+__device__ __forceinline__ int share_lanes(const RowBlock& r) {
+  return r.rows <= 32 ? 32 : (r.rows <= 64 ? 64 : 128);
+}
 
 // Byte of chunk c (16 bytes) of row r in a tile of D-byte rows, as TMA's swizzle over D
 // bytes places it.
@@ -204,8 +203,8 @@ __device__ __forceinline__ TileScales load_scales(const PrefillArgs& a, const Op
 
 // One warp for K or V: the pages of a CTA's tiles into its stages (lane x copies page x;
 // pages that no row sees are not read), and its part of the tiles' infos.  Scales are
-// loaded a tile ahead, block ids two.  (An info's last reader, the softmax of tile g - 8,
-// came before S of tile g - 6, and before the product with V of that tile.)
+// loaded a tile ahead, block ids two.  (An info's last reader, the softmax of the stream's
+// tile after g - 8, is over once S of tile g - 4 is, or the product with V of tile g - 6.)
 template <int D, bool V>
 __device__ __forceinline__ void copy_tiles(const PrefillArgs& a, const PlanView& pv,
                                            const TreeView& tv, uint8_t* sm, int* abort_flag,
@@ -492,8 +491,8 @@ __device__ __forceinline__ void convert_loaded(const PrefillArgs& a, const PlanV
       float scale = job.sc;
       if constexpr (MX)
         scale = job.em == 255 ? __int_as_float(0x7FC00000) : pow2_any(job.em - 127 - kRoom);
-      // V's info goes first, as S waits for it.  (An info's last reader, the softmax of tile
-      // g - 8, came before the waits of tiles before.)
+      // V's info goes first, as S waits for it.  (An info's last reader, the softmax of the
+      // stream's tile after g - 8, came before the waits of tiles before.)
       TileInfo* info = infos + si;
       if (V) {
         const uint32_t bad = o.whole(j0) ? 0u : drop_nonfinite<D, FMT>(job, lane);
@@ -535,11 +534,13 @@ __device__ __noinline__ uint32_t seen_bits(const TileInfo* info, int w, const Ro
   }
   return see & info->valid[w];
 }
-// Whether a row saw, among groups [w, end) of a tile, codes of V that are not finite.
-__device__ __noinline__ bool saw_nan(const TileInfo* info, int w, int end, const RowMask* row,
+// Whether a row saw, among the groups of a set, codes of V that are not finite.
+__device__ __noinline__ bool saw_nan(const TileInfo* info, uint32_t groups, const RowMask* row,
                                      const uint32_t* lines) {
   uint32_t bad = 0;
-  for (; w < end; ++w) bad |= info->cbad[w] ? info->cbad[w] & seen_bits(info, w, row, lines) : 0u;
+  for (int w = 0; w < 4; ++w)
+    if (((groups >> w) & 1u) != 0 && info->cbad[w] != 0)
+      bad |= info->cbad[w] & seen_bits(info, w, row, lines);
   return bad != 0;
 }
 
@@ -616,99 +617,93 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
   if (warp >= kIssue && warp < kIssue + 2) {
     // ================================================= MMA issuers
     // A warp for each stream, so that neither waits behind the other's barriers.  TMEM: S at
-    // 0 and 128, O at 256 and 384.
+    // 0 and 128, O at 256 and 384; a half of a tile has 64 columns of S, and its P lies in
+    // them, so that the next S waits for the product with V: products of different kinds
+    // and accumulators keep no order of their own.
     const int t = __shfl_sync(0xffffffffu, warp - kIssue, 0);
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint32_t idesc_s = RAW ? tc_idesc(0, a.fmt == FP8PA_E5M2 ? 1 : 0, 0, 0, 128, kT)
-                                 : tc_idesc(0, 0, 0, 0, 128, kT);
+    const uint32_t idesc_s = RAW ? tc_idesc(0, a.fmt == FP8PA_E5M2 ? 1 : 0, 0, 0, 128, kT / 2)
+                                 : tc_idesc(0, 0, 0, 0, 128, kT / 2);
     const uint32_t idesc_o = tc_idesc(0, 0, 0, 1, 128, D);  // A in TMEM, B MN-major
     const uint64_t dv0 = tc_desc(base + SM::kV, D * 16, 128, 0);
-    const uint64_t dq = (RAW ? tc_desc(base + SM::kQ, 16, D * 8, D == 128 ? 2 : 4)
-                             : tc_desc(base + SM::kQ, 2048, 128, 0)) + t * (SM::kHalf >> 4);
+    const uint64_t dq = RAW ? tc_desc(base + SM::kQ, 16, D * 8, D == 128 ? 2 : 4)
+                            : tc_desc(base + SM::kQ, 2048, 128, 0);
     const uint64_t dk0 = RAW ? tc_desc(base + SM::kK, 16, D * 8, D == 128 ? 2 : 4)
                              : tc_desc(base + SM::kK, 2048, 128, 0);
-    const uint32_t ds = tm + t * kT, d_o = tm + 256 + t * 128;
-    uint32_t g = 0;             // tiles before the item
-    uint32_t nq = 0, np = 0;    // items, and tiles, of the stream
+    const uint32_t ds0 = tm + t * kT, d_o = tm + 256 + t * 128;
+    uint32_t g = 0, nq = 0, np = 0;  // tiles before the item; items; tiles of the stream
     bool ok = true;
-    auto mma_s = [&](uint32_t st) {
-      const uint64_t dk = dk0 + st * (SM::kKTile >> 4);
-      if constexpr (RAW) {
+    auto mma_s = [&](uint32_t st, int h) {
+      const uint64_t dk = dk0 + st * (SM::kKTile >> 4) + h * (RAW ? kT / 2 * D >> 4 : 1024 >> 4);
+      const uint32_t ds = ds0 + h * (kT / 2);
+      if (elect_one()) {
+        if constexpr (RAW) {
 #pragma unroll
-        for (int term = 0; term < 2; ++term)
+          for (int term = 0; term < 2; ++term)
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-            tc_mma_f8(ds, dq + term * (SM::kCodes >> 4) + k * 2, dk + k * 2, idesc_s,
-                      (term | k) != 0);
-      } else {
+            for (int k = 0; k < D / 32; ++k)
+              tc_mma_f8(ds, dq + term * (SM::kCodes >> 4) + k * 2, dk + k * 2, idesc_s,
+                        (term | k) != 0);
+        } else {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc_mma_f16(ds, dq + k * (4096 >> 4), dk + k * (4096 >> 4), idesc_s, k > 0);
+          for (int k = 0; k < D / 16; ++k)
+            tc_mma_f16(ds, dq + k * (4096 >> 4), dk + k * (4096 >> 4), idesc_s, k > 0);
+        }
+        tc_commit(bars + kTS + t * 2 + h);
+        if (h == 1) tc_commit(bars + kTKFree + st);
       }
-      tc_commit(bars + kTS + t);
+      __syncwarp();
     };
-    auto mma_o = [&](uint32_t st, bool first) {
-      const uint64_t dv = dv0 + st * (SM::kHalf >> 4);
+    auto mma_o = [&](uint32_t st, int h, bool first) {
+      const uint64_t dv = dv0 + st * (SM::kHalf >> 4) + h * (kT / 2 * D * 2 >> 4);
+      const uint32_t p = ds0 + h * (kT / 2);
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < kT / 16; ++k)  // the groups of P start 32 columns apart
-        tc_mma_f16_ts(d_o, ds + (k >> 1) * 32 + (k & 1) * 8, dv + k * (2 * D * 16 >> 4), idesc_o,
-                      !(first && k == 0));
-      tc_commit(bars + kTO + t);
+        for (int k = 0; k < kT / 32; ++k)  // the groups of P start 32 columns apart
+          tc_mma_f16_ts(d_o, p + (k >> 1) * 32 + (k & 1) * 8, dv + k * (2 * D * 16 >> 4), idesc_o,
+                        !(first && k == 0));
+        tc_commit(bars + kTO + t * 2 + h);
+        if (h == 1) tc_commit(bars + kTVFree + st);
+      }
+      __syncwarp();
+    };
+    auto wait_s = [&](uint32_t x) {  // what S of tile x needs
+      return wait_warp(kTKFull + x % SM::kKStages, (x / SM::kKStages) & 1) &&
+             wait_warp(kTInfo + x % kInfos, (x / kInfos) & 1);
     };
     for (int it = it0, u = u0; u < u1 && ok; ++it) {
       const Item im = load_item(a, pv, it, u, u1);
       const int n = __shfl_sync(0xffffffffu, im.t1 - im.t0, 0);
       u += n;
-      const Streams sp(im.r);
-      const bool wide = __shfl_sync(0xffffffffu, static_cast<int>(sp.wide), 0) != 0;
-      const int step = wide ? 1 : 2, first = wide ? 0 : t;
-      // S of the first tile; then each tile's product with V, and S of the stream's next:
-      // all that they need but P is waited for before P
-      for (int k = first - step; k < n && ok; k += step) {
-        const int next = k + step;
-        const bool more = next < n;
-        const uint32_t gk = g + k, vs = gk & 1, gn = g + next, ks = gn % SM::kKStages;
-        if (k < 0) {
-          if (!more) break;
-          // q first: once an item's q is there, every tile before the item is over, and a
-          // parity of the barriers below can mean no phase but its own (later ones follow
-          // its own, as the stages are even in number)
-          ok = wait_warp(kTQ + t, nq & 1);
-          ++nq;
-        } else {
-          ok = wait_warp(kTVFull + vs, (gk >> 1) & 1);
-        }
-        if (more)
-          ok = ok && wait_warp(kTKFull + ks, (gn / SM::kKStages) & 1) &&
-               wait_warp(kTInfo + gn % kInfos, (gn / kInfos) & 1);
-        if (k >= 0) {
-          ok = ok && wait_warp(kTP + t, np & 1);
-          ++np;
-        }
+      // q first, and every item's: once it is there, every tile before the item is over, and
+      // a parity of the barriers below can mean no phase but its own (later ones follow its
+      // own, as the stages are even in number)
+      ok = wait_warp(kTQ, nq & 1);
+      ++nq;
+      if (ok && t < n) {
+        ok = wait_s(g + t);
         if (!ok) break;
         tc_fence_after();
-        if (k >= 0) {
-          if (elect_one()) {
-            mma_o(vs, k == first);
-            tc_commit(bars + kTVFree + vs);
-            if (!wide) mbar_arrive(bars + kTVFree + vs);
-          }
-          __syncwarp();
-        }
-        if (more) {
-          // S goes where P lies, and products of different kinds and accumulators keep no order
-          // of their own (the wait is 2% of 12 x 16K tokens)
-          if (k >= 0 && !wait_warp(kTO + t, (np - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          if (elect_one()) {
-            mma_s(ks);
-            tc_commit(bars + kTKFree + ks);
-            if (!wide) mbar_arrive(bars + kTKFree + ks);
-          }
-          __syncwarp();
+        mma_s((g + t) % SM::kKStages, 0);
+        mma_s((g + t) % SM::kKStages, 1);
+      }
+      for (int k = t; k < n && ok; k += 2, ++np) {
+        const uint32_t gk = g + k, gn = gk + 2;
+        const bool more = k + 2 < n;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (h == 0) ok = wait_warp(kTVFull + (gk & 1), (gk >> 1) & 1);
+          ok = ok && wait_warp(kTP + t * 2 + h, np & 1);
+          if (!ok) break;
+          tc_fence_after();
+          mma_o(gk & 1, h, k == t && h == 0);
+          if (!more) continue;
+          if (h == 0) ok = wait_s(gn);
+          ok = ok && wait_warp(kTO + t * 2 + h, np & 1);
+          if (!ok) break;
+          tc_fence_after();
+          mma_s(gn % SM::kKStages, h);
         }
       }
       g += n;
@@ -742,14 +737,15 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
     }
   } else {
     // ================================================= softmax warps
-    // A thread per lane: four warps a stream.  (Two threads a lane, each with half of the
-    // tokens, agreed on a reference through shared memory: 195 us where this takes %TIME%.)
     const int t = warp >> 2;                // stream
     const int rl = (warp & 3) * 32 + lane;  // lane of the tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + t * kT + lanes, to = tmem + 256 + t * 128 + lanes;
     float2* ml = reinterpret_cast<float2*>(sm + SM::kMl);
+    RowMask* const row = reinterpret_cast<RowMask*>(sm + SM::kRow) + rl;
+    int* exps = reinterpret_cast<int*>(sm + SM::kExp);
     const bool cap_quick = a.cap <= kCapFast;
+    constexpr int kTop = RAW ? 8 : 14;  // exponent of a normalised row of q
     uint32_t na = 0;
     auto sync_all = [&]() {  // all softmax warps
       __syncwarp();
@@ -764,338 +760,307 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
       const Item im = load_item(a, pv, it, u, u1);
       const int n = im.t1 - im.t0;
       u += n;
-      const Streams sp(im.r);
-      const int mine = sp.tiles(t, n);  // tiles of this stream
-      // row of the block of a lane (lanes past its end: the last row)
-      auto row_of = [&](int l) { return sp.wide ? t * 128 + l : l & (sp.lanes - 1); };
+      const int sl = share_lanes(im.r);
+      const int mine = (n + 1 - t) >> 1;  // tiles of this stream
+      // query and head of a lane's row (lanes past the block's end: its last row)
       auto query_of = [&](int l, int& qi, int& h) {
-        const int rr = im.r.row0 + min(row_of(l), im.r.rows - 1);
+        const int rr = im.r.row0 + min(l & (sl - 1), im.r.rows - 1);
         qi = rr / a.G;
         h = im.kvh * a.G + rr - qi * a.G;
       };
-      const int r = row_of(rl);
-      const bool live = r < im.r.rows;
-      int qi, h;
-      query_of(rl, qi, h);
-      const long qrow = static_cast<long>(im.r.qlo) + qi;
-      const long grow = qrow * a.hq + h;  // row of q and out
-      float ref = kNegBig, l = 0.f;
-      if (mine > 0) {
+      {
         // ---- the rows of q, each normalised by a power of two, into shared memory (every S
-        // of the stream's previous item is done: its last was read); 8 rows x 64 bytes a load
-        constexpr int kTop = RAW ? 8 : 14;  // exponent of the normalised row
-        int er = 0;
-        {
-          const float sgn = a.sm_scale < 0.f ? -1.f : 1.f;
-          const bool st = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
-          const float* kc = a.k_scale + static_cast<long>(im.kvh) * D;
-          const int r8 = lane & 7, c4 = lane >> 3;
-          uint8_t* dst = sm + SM::kQ + t * SM::kHalf;
-#pragma unroll 2
-          for (int y = 0; y < 4; ++y) {
-            const int row = (warp & 3) * 32 + y * 8 + r8;
-            int qy, hy;
-            query_of(row, qy, hy);
-            const uint4* src = reinterpret_cast<const uint4*>(
-                                   a.q + ((static_cast<long>(im.r.qlo) + qy) * a.hq + hy) * D) + c4;
-            uint4 raw[D / 32];
+        // of the item before was read), 16 lanes' a warp; 8 rows x 64 bytes a load
+        const float sgn = a.sm_scale < 0.f ? -1.f : 1.f;
+        const bool st = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
+        const float* kc = a.k_scale + static_cast<long>(im.kvh) * D;
+        const int r8 = lane & 7, c4 = lane >> 3;
+        uint8_t* dst = sm + SM::kQ;
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x) raw[x] = __ldg(src + x * 4);
-            auto get = [&](int x, float (&f)[8]) {
-              const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+        for (int y = 0; y < 2; ++y) {
+          const int to_row = warp * 16 + y * 8 + r8;
+          int qy, hy;
+          query_of(to_row, qy, hy);
+          const uint4* src = reinterpret_cast<const uint4*>(
+                                 a.q + ((static_cast<long>(im.r.qlo) + qy) * a.hq + hy) * D) + c4;
+          uint4 raw[D / 32];
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) raw[x] = __ldg(src + x * 4);
+          auto get = [&](int x, float (&f)[8]) {
+            const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              f[2 * e] = __uint_as_float(w[e] << 16) * sgn;
+              f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * sgn;
+            }
+            if (st) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] *= __ldg(kc + (x * 4 + c4) * 8 + e);
+            }
+          };
+          float amax = 0.f;
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) {
+            float f[8];
+            get(x, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+          }
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
+          // (129 for an infinity: such a row is NaN)
+          const int eq = amax > 0.f ? exp_above(amax) : 0;
+          if (c4 == 0) exps[to_row] = eq;
+          const float fq = exp2i(kTop - eq);
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) {
+            float f[8];
+            get(x, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] *= fq;
+            if constexpr (RAW) {  // hi, and lo = what hi leaves
+              uint32_t hi[4], lo[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                f[2 * e] = __uint_as_float(w[e] << 16) * sgn;
-                f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * sgn;
+                hi[e] = f32x2_to_codes2<FP8PA_E4M3>(f[2 * e], f[2 * e + 1]);
+                const float2 b = __half22float2(h2(codes2_to_f16x2<FP8PA_E4M3>(hi[e])));
+                lo[e] = f32x2_to_codes2<FP8PA_E4M3>(f[2 * e] - b.x, f[2 * e + 1] - b.y);
               }
-              if (st) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] *= __ldg(kc + (x * 4 + c4) * 8 + e);
-              }
-            };
-            float amax = 0.f;
-#pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
-              float f[8];
-              get(x, f);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
-            }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
-            // (129 for an infinity: such a row is NaN)
-            const int eq = amax > 0.f ? exp_above(amax) : 0;
-            if (c4 == y) er = eq;  // this lane's row
-            const float fq = exp2i(kTop - eq);
-#pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
-              float f[8];
-              get(x, f);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] *= fq;
-              if constexpr (RAW) {  // hi, and lo = what hi leaves
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  hi[e] = f32x2_to_codes2<FP8PA_E4M3>(f[2 * e], f[2 * e + 1]);
-                  const float2 b = __half22float2(h2(codes2_to_f16x2<FP8PA_E4M3>(hi[e])));
-                  lo[e] = f32x2_to_codes2<FP8PA_E4M3>(f[2 * e] - b.x, f[2 * e + 1] - b.y);
-                }
-                const int c8 = x * 4 + c4;  // 8 dims: half a 16-byte chunk
-                uint8_t* p = dst + swizzled<D>(row, c8 >> 1) + (c8 & 1) * 8;
-                *reinterpret_cast<uint2*>(p) =
-                    make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-                *reinterpret_cast<uint2*>(p + SM::kCodes) =
-                    make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-              } else {
-                *reinterpret_cast<uint4*>(dst + (row >> 3) * 128 + r8 * 16 + (x * 4 + c4) * 2048) =
-                    make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]),
-                               pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
-              }
+              const int c8 = x * 4 + c4;  // 8 dims: half a 16-byte chunk
+              uint8_t* p = dst + swizzled<D>(to_row, c8 >> 1) + (c8 & 1) * 8;
+              *reinterpret_cast<uint2*>(p) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+              *reinterpret_cast<uint2*>(p + SM::kCodes) =
+                  make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            } else {
+              *reinterpret_cast<uint4*>(dst + (to_row >> 3) * 128 + r8 * 16 +
+                                        (x * 4 + c4) * 2048) =
+                  make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]),
+                             pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
             }
           }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bars + kTQ + t);
         }
-        // log2-domain factor of a raw score (capped scores: see cap_in)
-        float zs = fabsf(a.sm_scale) * exp2i(er - kTop) * (VAR == 2 ? a.cap_in : kLog2e);
-        if (VAR == 0) zs = fmaxf(zs, 1e-37f);  // (it multiplies a masked -inf: not zero)
-        if (er > 128) zs = __int_as_float(0x7FC00000);
-        const int depth = __ldg(tv.depth + qrow);
-        RowMask* const row = reinterpret_cast<RowMask*>(sm + SM::kRow) + t * 128 + rl;
-        *row = RowMask{window_first(a.window, im.r.pA + depth), static_cast<int>(qrow)};
-        const float slope = (VAR > 0 && a.slopes) ? __ldg(a.slopes + h) * kLog2e : 0.f;
-        const float cap_log2 = VAR == 2 ? a.cap * kLog2e : 0.f;
-        // the bias of a token is slope pos + b0 (and the cap, where its tanh is taken from 1)
-        const float b0 = (cap_quick ? cap_log2 : 0.f) - slope * static_cast<float>(depth);
-        // the thread's groups of 32 tokens: first, and how many
-        const int ng = sp.lanes >> 5, g0 = rl / sp.lanes * ng;
-        const uint32_t first_tile = g + (sp.wide ? 0 : t), step = sp.wide ? 1 : 2;
-        // makes the row NaN where it saw codes of tile gt that are not finite
-        auto late_nan = [&](uint32_t gt) {
-          const TileInfo* info = infos + gt % kInfos;
-          const uint4 c = *reinterpret_cast<const uint4*>(info->cbad);
-          if ((c.x | c.y | c.z | c.w) != 0 && saw_nan(info, g0, g0 + ng, row, tv.line))
-            l = __int_as_float(0x7FC00000);
-        };
-        uint32_t ra[32];  // a group's scores
-        for (int x = 0; x < mine; ++x) {
-          const uint32_t gt = first_tile + step * x;
-          // (S is issued once the tile's info is complete)
-          if (!wait_warp(kTS + t, ns & 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          // (what the tile before brought that is not finite is known by now)
-          if (x > 0) late_nan(gt - step);
-          const TileInfo& info = infos[gt % kInfos];
-          uint4 sc[8];  // a group's scales, loaded beside its scores
-          auto load = [&](int w, const float* scale) {
-            tmem_ld32(ts + w * 32, ra);
-            const uint32_t at = smem_u32(scale + w * 32);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sc[i] = lds128(at + i * 16);
-            tmem_ld_wait();
-            tmem_landed(ra);
-          };
-          // ---- a bound of z + e over the row's tokens; the scores go back to TMEM
-          float bound = __int_as_float(0xff800000);
-#pragma unroll 1
-          for (int w = g0; w < g0 + ng; ++w) {
-            const uint32_t whole = info.seen[w], bad = info.bad[w];
-            load(w, info.ks);
-            const uint64_t zs2 = f2_pack(zs, zs), sl2 = f2_pack(slope, slope);
-            const uint64_t b02 = f2_pack(b0, b0);
-#pragma unroll
-            for (int i4 = 0; i4 < 8; ++i4) {
-              float4 p4;
-              if constexpr (VAR > 0) p4 = reinterpret_cast<const float4*>(info.pos + w * 32)[i4];
-#pragma unroll
-              for (int i2 = 0; i2 < 2; ++i2) {
-                uint32_t* v = ra + i4 * 4 + i2 * 2;
-                uint64_t z = f2_mul(u2_pack(v[0], v[1]),
-                                    i2 ? u2_pack(sc[i4].z, sc[i4].w) : u2_pack(sc[i4].x, sc[i4].y));
-                float y0, y1;
-                if constexpr (VAR > 0) {
-                  const uint64_t b =
-                      f2_fma(sl2, i2 ? f2_pack(p4.z, p4.w) : f2_pack(p4.x, p4.y), b02);
-                  if constexpr (VAR == 1) {
-                    z = f2_fma(z, zs2, b);
-                  } else if (cap_quick) {  // cap tanh(z / cap) = cap - 2 cap / (2^x + 1)
-                    f2_unpack(f2_mul(z, zs2), y0, y1);
-                    f2_unpack(f2_add(f2_pack(ex2(y0), ex2(y1)), f2_pack(1.f, 1.f)), y0, y1);
-                    z = f2_fma(f2_pack(rcp_fast(y0), rcp_fast(y1)),
-                               f2_pack(-2.f * cap_log2, -2.f * cap_log2), b);
-                  } else {
-                    f2_unpack(f2_mul(z, zs2), y0, y1);
-                    y0 = a.cap * tanh_f32(y0 * a.tanh_in) * kLog2e;
-                    y1 = a.cap * tanh_f32(y1 * a.tanh_in) * kLog2e;
-                    z = f2_add(f2_pack(y0, y1), b);
-                  }
-                }
-                f2_unpack(z, y0, y1);
-                v[0] = __float_as_uint(y0);
-                v[1] = __float_as_uint(y1);
-              }
-            }
-            if (!whole || bad) {
-              const uint32_t m = seen_bits(&info, w, row, tv.line);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (((m >> i) & 1) == 0) ra[i] = 0xff800000u;
-              if (m & bad) l = __int_as_float(0x7FC00000);
-            }
-            float m4[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) m4[y] = __int_as_float(0xff800000);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              m4[i & 3] = max3(m4[i & 3], __uint_as_float(ra[2 * i]), __uint_as_float(ra[2 * i + 1]));
-            tmem_st32(ts + w * 32, ra);
-            const float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-            bound = fmaxf(bound, fmaf(mx, VAR > 0 ? 1.f : zs, static_cast<float>(info.ev[w])));
-          }
-          tmem_st_wait();
-          // ---- the reference: where the bound passed it by 2^kTau it moves, and with it the
-          // sums and O
-          float al = 1.f;
-          if (bound > ref + kTau) {
-            al = ex2(ref - bound);
-            ref = bound;
-          }
-          if (__any_sync(0xffffffffu, al != 1.f)) {
-            l *= al;
-            if (x > 0) {
-              // (the product of the stream's tile before is over: its S waited for it)
-#pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                tmem_ld32(to + c * 32, ra);
-                tmem_ld_wait();
-                tmem_landed(ra);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) ra[i] = __float_as_uint(__uint_as_float(ra[i]) * al);
-                tmem_st32(to + c * 32, ra);
-              }
-            }
-          }
-          // ---- P times V's scale, and the sum of P
-#pragma unroll 1
-          for (int w = g0; w < g0 + ng; ++w) {
-            const float e = static_cast<float>(info.ev[w]);
-            load(w, info.vs);
-            const float c0 = kShift - ref + e, f = VAR > 0 ? 1.f : zs;
-            const uint64_t f2 = f2_pack(f, f), c02 = f2_pack(c0, c0);
-            uint64_t la = 0, lb = 0;  // (0.f, 0.f)
-            uint32_t pw[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint4 v4 = sc[i >> 1];
-              const uint64_t z = u2_pack(ra[2 * i], ra[2 * i + 1]);
-              float p, q;
-              f2_unpack(VAR > 0 ? f2_add(z, c02) : f2_fma(z, f2, c02), p, q);
-              const uint64_t e2 = f2_pack(ex2(p), ex2(q));
-              if (i & 1) lb = f2_add(lb, e2);
-              else la = f2_add(la, e2);
-              f2_unpack(f2_mul(e2, i & 1 ? u2_pack(v4.z, v4.w) : u2_pack(v4.x, v4.y)), p, q);
-              pw[i] = pack_half2(p, q);
-            }
-            tmem_st16(ts + w * 32, pw);
-            float y, z;
-            f2_unpack(f2_add(la, lb), y, z);
-            l = fmaf(y + z, ex2(-e), l);
-          }
-          if (ng < 4) {  // nothing for the other shares' tokens
-            const uint32_t zero[16] = {};
-            for (int w = 0; w < 4; ++w)
-              if (w < g0 || w >= g0 + ng) tmem_st16(ts + w * 32, zero);
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bars + kTP + t);
-          ++ns;
-        }
-        // the last product
-        if (!ok || !wait_warp(kTO + t, (ns - 1) & 1)) {
+      }
+      int qi, h;
+      query_of(rl, qi, h);
+      const int qrow = im.r.qlo + qi;
+      const int depth = __ldg(tv.depth + qrow);
+      if (t == 0) *row = RowMask{window_first(a.window, im.r.pA + depth), qrow};
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + kTQ);
+      const float slope = (VAR > 0 && a.slopes) ? __ldg(a.slopes + h) * kLog2e : 0.f;
+      const float cap_log2 = VAR == 2 ? a.cap * kLog2e : 0.f;
+      // the bias of a token is slope pos + b0 (and the cap, where its tanh is taken from 1)
+      const float b0 = (cap_quick ? cap_log2 : 0.f) - slope * static_cast<float>(depth);
+      // the thread's groups of 32 tokens
+      const int part = rl / sl;
+      const uint32_t groups = sl == 128 ? 0xFu : (sl == 64 ? 5u << part : 1u << part);
+      float ref = kNegBig, l = 0.f, zs = 0.f;
+      // makes the row NaN where it saw codes of tile gt that are not finite
+      auto late_nan = [&](uint32_t gt) {
+        const TileInfo* info = infos + gt % kInfos;
+        const uint4 c = *reinterpret_cast<const uint4*>(info->cbad);
+        if ((c.x | c.y | c.z | c.w) != 0 && saw_nan(info, groups, row, tv.line))
+          l = __int_as_float(0x7FC00000);
+      };
+      uint32_t ra[32];  // a group's scores
+      uint4 sc[8];      // and their scales, loaded beside them
+      for (int x = 0; x < 2 * mine; ++x) {  // halves of the stream's tiles
+        const int half = x & 1;
+        const uint32_t gt = g + t + (x & ~1);
+        // (S is issued once the tile's info is complete)
+        if (!wait_warp(kTS + t * 2 + half, ns & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        late_nan(first_tile + step * (mine - 1));
-      }
-      g += n;
-
-      // ---- the block's result, or this range's piece of it
-      const bool piece = im.t0 > 0 || im.t1 < im.r.count;
-      const int slot = blockIdx.x * 2 + (im.t0 > 0 ? 0 : 1);
-      const bool stat = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
-      const float* vch = a.v_scale + static_cast<long>(im.kvh) * D;
-      auto put = [&](int c, float (&f)[16]) {  // dims 16 c .. 16 c + 15 of row r
-        if (stat) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) f[i] *= __ldg(vch + c * 16 + i);
+        if (x == 0) {
+          // log2-domain factor of a raw score (capped scores: see cap_in)
+          const int er = exps[rl];
+          zs = fabsf(a.sm_scale) * exp2i(er - kTop) * (VAR == 2 ? a.cap_in : kLog2e);
+          if (VAR == 0) zs = fmaxf(zs, 1e-37f);  // (it multiplies a masked -inf: not zero)
+          if (er > 128) zs = __int_as_float(0x7FC00000);
+        } else if (half == 0) {
+          late_nan(gt - 2);  // (what the tile before brought that is not finite is known by now)
         }
-        if (piece || a.out_f32) {
-          float* dst = piece ? pv.o + (static_cast<long>(slot) * kRows + r) * D + c * 16
-                             : reinterpret_cast<float*>(a.out) + grow * D + c * 16;
+        const TileInfo& info = infos[gt % kInfos];
+        auto load = [&](int w, const float* scale) {
+          tmem_ld32(ts + w * 32, ra);
+          const uint32_t at = smem_u32(scale + w * 32);
 #pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4*>(dst + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + grow * D +
-                                                c * 16);
+          for (int i = 0; i < 8; ++i) sc[i] = lds128(at + i * 16);
+          tmem_ld_wait();
+          tmem_landed(ra);
+        };
+        // ---- a bound of z + e over the row's tokens; the scores go back to TMEM
+        float bound = __int_as_float(0xff800000);
+#pragma unroll 1
+        for (int w = half * 2; w < half * 2 + 2; ++w) {
+          if (((groups >> w) & 1u) == 0) continue;
+          const uint32_t whole = info.seen[w], bad = info.bad[w];
+          load(w, info.ks);
+          const uint64_t zs2 = f2_pack(zs, zs), sl2 = f2_pack(slope, slope);
+          const uint64_t b02 = f2_pack(b0, b0);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t w[4];
+          for (int i4 = 0; i4 < 8; ++i4) {
+            float4 p4;
+            if constexpr (VAR > 0) p4 = reinterpret_cast<const float4*>(info.pos + w * 32)[i4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const __nv_bfloat162 b2 =
-                  __floats2bfloat162_rn(f[8 * i + 2 * x], f[8 * i + 2 * x + 1]);
-              w[x] = *reinterpret_cast<const uint32_t*>(&b2);
+            for (int i2 = 0; i2 < 2; ++i2) {
+              uint32_t* v = ra + i4 * 4 + i2 * 2;
+              uint64_t z = f2_mul(u2_pack(v[0], v[1]),
+                                  i2 ? u2_pack(sc[i4].z, sc[i4].w) : u2_pack(sc[i4].x, sc[i4].y));
+              float y0, y1;
+              if constexpr (VAR > 0) {
+                const uint64_t b =
+                    f2_fma(sl2, i2 ? f2_pack(p4.z, p4.w) : f2_pack(p4.x, p4.y), b02);
+                if constexpr (VAR == 1) {
+                  z = f2_fma(z, zs2, b);
+                } else if (cap_quick) {  // cap tanh(z / cap) = cap - 2 cap / (2^x + 1)
+                  f2_unpack(f2_mul(z, zs2), y0, y1);
+                  f2_unpack(f2_add(f2_pack(ex2(y0), ex2(y1)), f2_pack(1.f, 1.f)), y0, y1);
+                  z = f2_fma(f2_pack(rcp_fast(y0), rcp_fast(y1)),
+                             f2_pack(-2.f * cap_log2, -2.f * cap_log2), b);
+                } else {
+                  f2_unpack(f2_mul(z, zs2), y0, y1);
+                  y0 = a.cap * tanh_f32(y0 * a.tanh_in) * kLog2e;
+                  y1 = a.cap * tanh_f32(y1 * a.tanh_in) * kLog2e;
+                  z = f2_add(f2_pack(y0, y1), b);
+                }
+              }
+              f2_unpack(z, y0, y1);
+              v[0] = __float_as_uint(y0);
+              v[1] = __float_as_uint(y1);
             }
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (!whole || bad) {
+            const uint32_t m = seen_bits(&info, w, row, tv.line);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (((m >> i) & 1) == 0) ra[i] = 0xff800000u;
+            if (m & bad) l = __int_as_float(0x7FC00000);
+          }
+          float m4[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) m4[y] = __int_as_float(0xff800000);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            m4[i & 3] = max3(m4[i & 3], __uint_as_float(ra[2 * i]), __uint_as_float(ra[2 * i + 1]));
+          tmem_st32(ts + w * 32, ra);
+          const float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+          bound = fmaxf(bound, fmaf(mx, VAR > 0 ? 1.f : zs, static_cast<float>(info.ev[w])));
+        }
+        tmem_st_wait();
+        // ---- the reference: where the bound passed it by 2^kTau it moves, and with it the
+        // sums and O
+        float al = 1.f;
+        if (bound > ref + kTau) {
+          al = ex2(ref - bound);
+          ref = bound;
+        }
+        if (__any_sync(0xffffffffu, al != 1.f)) {
+          l *= al;
+          if (x > 0) {  // behind the product of the half before
+            if (!wait_warp(kTO + t * 2 + (half ^ 1), (ns - (half ^ 1)) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              tmem_ld32(to + c * 32, ra);
+              tmem_ld_wait();
+              tmem_landed(ra);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) ra[i] = __float_as_uint(__uint_as_float(ra[i]) * al);
+              tmem_st32(to + c * 32, ra);
+            }
           }
         }
-      };
-      auto take = [&](int c, float scale, float (&f)[16]) {  // of this lane's O
-        uint32_t o[16];
-        tmem_ld16(to + c * 16, o);
-        tmem_ld_wait();
-        tmem_landed(o);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(o[i]) * scale;
-      };
-      if (sp.wide) {
-        const float inv = piece ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+        // ---- P times V's scale, and the sum of P; zeros for the other shares' tokens
 #pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-          float f[16];
-          take(c, inv, f);
-          if (live) put(c, f);
+        for (int w = half * 2; w < half * 2 + 2; ++w) {
+          uint32_t pw[16];
+          if (((groups >> w) & 1u) == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pw[i] = 0;
+            tmem_st16(ts + w * 32, pw);
+            continue;
+          }
+          const float e = static_cast<float>(info.ev[w]);
+          load(w, info.vs);
+          const float c0 = kShift - ref + e, f = VAR > 0 ? 1.f : zs;
+          const uint64_t f2 = f2_pack(f, f), c02 = f2_pack(c0, c0);
+          uint64_t la = 0, lb = 0;  // (0.f, 0.f)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint4 v4 = sc[i >> 1];
+            const uint64_t z = u2_pack(ra[2 * i], ra[2 * i + 1]);
+            float p, q;
+            f2_unpack(VAR > 0 ? f2_add(z, c02) : f2_fma(z, f2, c02), p, q);
+            const uint64_t e2 = f2_pack(ex2(p), ex2(q));
+            if (i & 1) lb = f2_add(lb, e2);
+            else la = f2_add(la, e2);
+            f2_unpack(f2_mul(e2, i & 1 ? u2_pack(v4.z, v4.w) : u2_pack(v4.x, v4.y)), p, q);
+            pw[i] = pack_half2(p, q);
+          }
+          tmem_st16(ts + w * 32, pw);
+          float y, z;
+          f2_unpack(f2_add(la, lb), y, z);
+          l = fmaf(y + z, ex2(-e), l);
         }
-        if (piece && live) pv.ml[static_cast<long>(slot) * kRows + r] = make_float2(ref, l);
-      } else {
-        // the row's partial results: of both streams, and of the shares of the lanes
-        ml[t * 128 + rl] = make_float2(ref, l);
-        if (!sync_all()) {
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + kTP + t * 2 + half);
+        ns += half;
+      }
+      if (!ok) break;
+      if (mine > 0) {  // the last product
+        if (!wait_warp(kTO + t * 2 + 1, (ns - 1) & 1)) {
           ok = false;
           break;
         }
-        float M = kNegBig, sum = 0.f;
-        for (int x = r; x < 256; x += sp.lanes) M = fmaxf(M, ml[x].x);
-        for (int x = r; x < 256; x += sp.lanes) sum += ml[x].y * ex2(ml[x].x - M);
-        const float scale = ex2(ref - M) * (piece ? 1.f : (sum == 0.f ? 0.f : 1.f / sum));
-        // dims 4 c .. 4 c + 3 of lane y's row among the sums, free of bank conflicts
-        auto at = [&](int y, int c) {
-          return reinterpret_cast<float4*>(sm + SM::kQ + y * (D * 4) +
-                                           (((c & ~7) | ((c ^ y) & 7)) << 4));
-        };
-        auto leave = [&](int c, const float (&f)[16]) {
+        tc_fence_after();
+        late_nan(g + t + 2 * (mine - 1));
+      }
+      g += n;
+
+      // ---- the block's result, or this range's piece of it, from the row's partial
+      // results: of both streams, and of the shares of the lanes
+      const int r = rl & (sl - 1);
+      const bool first = t == 0 && rl < sl, live = first && r < im.r.rows;  // (first: whole warps)
+      const bool piece = im.t0 > 0 || im.t1 < im.r.count;
+      const long at_row = piece ? (static_cast<long>(blockIdx.x) * 2 + (im.t0 > 0 ? 0 : 1)) * kRows + r
+                                : static_cast<long>(qrow) * a.hq + h;
+      const bool stat = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
+      const float* vch = a.v_scale + static_cast<long>(im.kvh) * D;
+      ml[t * 128 + rl] = make_float2(ref, l);
+      if (!sync_all()) {
+        ok = false;
+        break;
+      }
+      float M = kNegBig, sum = 0.f;
+      for (int x = r; x < 256; x += sl) M = fmaxf(M, ml[x].x);
+      for (int x = r; x < 256; x += sl) sum += ml[x].y * ex2(ml[x].x - M);
+      const float scale = ex2(ref - M) * (piece ? 1.f : (sum == 0.f ? 0.f : 1.f / sum));
+      if (piece && live) pv.ml[at_row] = make_float2(M, sum);
+      // half of the dims at a time, in q's place: chunk c (4 dims) of lane y's, free of bank
+      // conflicts
+      auto at = [&](int y, int c) {
+        return reinterpret_cast<float4*>(sm + SM::kQ + y * (D * 2) +
+                                         (((c & ~7) | ((c ^ y) & 7)) << 4));
+      };
+      const bool both = n > 1;  // whether stream 1 had a tile
+#pragma unroll 1
+      for (int dh = 0; dh < 2 && ok; ++dh) {
+        auto take = [&](int c, float (&f)[16]) {  // of this lane's O
+          uint32_t o[16];
+          tmem_ld16(to + dh * (D / 2) + c * 16, o);
+          tmem_ld_wait();
+          tmem_landed(o);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *at(rl, c * 4 + i) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+          for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(o[i]) * scale;
         };
         auto add = [&](int y, int c, float (&f)[16]) {
 #pragma unroll
@@ -1107,49 +1072,58 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
             f[4 * i + 3] += v.w;
           }
         };
-        const bool both = n > 1;  // whether stream 1 had a tile
-        if (t == 1 && both) {
 #pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            float f[16];
-            take(c, scale, f);
-            leave(c, f);
-          }
-        }
-        if (!sync_all()) {
-          ok = false;
-          break;
-        }
-        if (sp.lanes < 128) {
-          if (t == 0 && rl >= sp.lanes) {
+        for (int s = 0; s < 2 && ok; ++s) {  // stream 1 to stream 0, then the shares to the first
+          if (s == 0 ? t == 1 && both : t == 0 && rl >= sl) {
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
+            for (int c = 0; c < D / 32; ++c) {
               float f[16];
-              take(c, scale, f);
-              if (both) add(rl, c, f);
-              leave(c, f);
+              take(c, f);
+              if (s == 1 && both) add(rl, c, f);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *at(rl, c * 4 + i) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
             }
           }
-          if (!sync_all()) {
-            ok = false;
-            break;
-          }
+          if (s == 0 || sl < 128) ok = sync_all();
         }
-        if (t == 0 && rl < sp.lanes) {
+        if (ok && first) {
 #pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
+          for (int c = 0; c < D / 32; ++c) {
             float f[16];
-            take(c, scale, f);
+            take(c, f);
             if (both) add(rl, c, f);
-            for (int y = rl + sp.lanes; y < 128; y += sp.lanes) add(y, c, f);
-            if (live) put(c, f);
+            for (int y = rl + sl; y < 128; y += sl) add(y, c, f);
+            if (!live) continue;
+            const int d0 = dh * (D / 2) + c * 16;
+            if (stat) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) f[i] *= __ldg(vch + d0 + i);
+            }
+            if (piece || a.out_f32) {
+              float* dst = (piece ? pv.o : reinterpret_cast<float*>(a.out)) + at_row * D + d0;
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(dst + i) =
+                    make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+            } else {
+              uint4* dst =
+                  reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at_row * D + d0);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  const __nv_bfloat162 b2 =
+                      __floats2bfloat162_rn(f[8 * i + 2 * y], f[8 * i + 2 * y + 1]);
+                  w[y] = *reinterpret_cast<const uint32_t*>(&b2);
+                }
+                dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
           }
-          if (piece && live) pv.ml[static_cast<long>(slot) * kRows + r] = make_float2(M, sum);
         }
-        if (!sync_all()) {  // the sums lie where the next item's q goes
-          ok = false;
-          break;
-        }
+        if (ok) ok = sync_all();  // (also: the sums lie where the next item's q goes)
       }
       tc_fence_before();
     }
