@@ -173,32 +173,43 @@ struct OpenItem {
 };
 
 // ---------------------------------------------------------------- copies (RAW)
-// The scales of a tile, lane x those of tokens x, 32 + x, 64 + x and 96 + x.
+// The scales of a tile, lane x those of tokens 4 x .. 4 x + 3 (of one page).
 struct TileScales {
-  float s[4];
-  uint32_t ok;  // bit of a token: wanted, and its page exists
+  float4 s;
+  uint32_t ok;  // bits of the four: wanted, and their page exists
 };
-// pages: lane x holds the tile's page x.
+// pages: lane x holds the tile's page x.  whole: every row sees the whole tile.
 template <bool V>
 __device__ __forceinline__ TileScales load_scales(const PrefillArgs& a, const OpenItem& o,
-                                                  int pages, int j0, int lgbs, int lane) {
+                                                  int pages, int j0, bool whole, int lgbs,
+                                                  int lane) {
   TileScales r;
-  r.ok = 0;
-  const float* scale = V ? a.v_scale : a.k_scale;
+  const int id = __shfl_sync(0xffffffffu, pages, (lane * 4) >> lgbs), j = j0 + lane * 4;
+  const bool there = id >= 0 && id < a.num_blocks;
+  uint32_t want = 0xFu;
+  if (!whole) {
+    want = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int id = __shfl_sync(0xffffffffu, pages, (i * 32 + lane) >> lgbs);
-    const int j = j0 + i * 32 + lane;
-    const bool want = o.seen(j), ok = want && id >= 0 && id < a.num_blocks;
-    if (!V && want && !ok) raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
-    r.ok |= ok ? 1u << i : 0u;
-    r.s[i] = 1.f;
-    if (ok && a.mode == FP8PA_SCALE_TOKEN_HEAD)
-      r.s[i] = __ldg(scale + cache_row(a, o.kvh, id, j));
-    else if (ok && a.mode == FP8PA_SCALE_SEGMENT)
-      r.s[i] = __ldg(scale + static_cast<size_t>(id) * a.hp + o.kvh);
+    for (int i = 0; i < 4; ++i) want |= o.seen(j + i) ? 1u << i : 0u;
+  }
+  if (!V && want != 0 && !there) raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
+  r.ok = there ? want : 0u;
+  r.s = make_float4(1.f, 1.f, 1.f, 1.f);
+  const float* scale = V ? a.v_scale : a.k_scale;
+  if (there && a.mode == FP8PA_SCALE_TOKEN_HEAD) {
+    r.s = __ldg(reinterpret_cast<const float4*>(scale + cache_row(a, o.kvh, id, j)));
+  } else if (there && a.mode == FP8PA_SCALE_SEGMENT) {
+    const float x = __ldg(scale + static_cast<size_t>(id) * a.hp + o.kvh);
+    r.s = make_float4(x, x, x, x);
   }
   return r;
+}
+// Bits of 32 tokens from four of each of eight lanes, the same word in all eight.
+__device__ __forceinline__ uint32_t group_bits(uint32_t four, int lane) {
+  uint32_t w = four << (4 * (lane & 7));
+#pragma unroll
+  for (int s = 1; s < 8; s <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, s);
+  return w;
 }
 
 // One warp for K or V: the pages of a CTA's tiles into its stages (lane x copies page x;
@@ -234,12 +245,19 @@ __device__ __forceinline__ void copy_tiles(const PrefillArgs& a, const PlanView&
       return want ? __ldg(o.table + (t >> lgbs)) : -1;
     };
     int id = page_of(im.t0), id1 = page_of(im.t0 + 1);
-    TileScales s = load_scales<V>(a, o, id, o.token_of(im.t0), lgbs, lane);
+    TileScales s = load_scales<V>(a, o, id, o.token_of(im.t0), o.whole(o.token_of(im.t0)), lgbs,
+                                  lane);
+    bool whole = o.whole(o.token_of(im.t0));
     for (int k = im.t0; k < im.t1; ++k, ++g) {
       const int j0 = o.token_of(k), here = id;
       const TileScales now = s;
+      const bool all_rows = whole;
       id = id1;
-      if (k + 1 < im.t1) s = load_scales<V>(a, o, id, o.token_of(k + 1), lgbs, lane);
+      if (k + 1 < im.t1) {
+        const int next = o.token_of(k + 1);
+        whole = o.whole(next);
+        s = load_scales<V>(a, o, id, next, whole, lgbs, lane);
+      }
       id1 = page_of(k + 2);
       const bool have = here >= 0 && here < a.num_blocks;
       const uint32_t count = __popc(__ballot_sync(0xffffffffu, have)), st = g % kS;
@@ -249,50 +267,70 @@ __device__ __forceinline__ void copy_tiles(const PrefillArgs& a, const PlanView&
         ok = false;
         break;
       }
-      uint32_t held[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) held[i] = __ballot_sync(0xffffffffu, (now.ok >> i) & 1u);
-      if (V && lane == 0) {  // what the converting warps need comes with the codes
-#pragma unroll
-        for (int i = 0; i < 4; ++i) info->held[i] = held[i];
-        info->whole = o.whole(j0);
+      // the word of a lane's group, written by the first of its eight lanes
+      const int grp = lane >> 3;
+      const bool lead = (lane & 7) == 0;
+      uint32_t held = 0xFFFFFFFFu;
+      if (!__all_sync(0xffffffffu, now.ok == 0xFu)) held = group_bits(now.ok, lane);
+      if (V) {  // what the converting warps need comes with the codes
+        if (lead) info->held[grp] = held;
+        if (lane == 0) info->whole = all_rows;
+        __syncwarp();
       }
       if (lane == 0) mbar_arrive_expect_tx(bars + kFull + st, count * bytes);
       __syncwarp();
       if (have)
         tma_load_2d(sm + (V ? SM::kVCodes : SM::kK) + st * SM::kCodes + lane * bytes, map, 0,
                     (here * a.hkv + o.kvh) * a.bs, bars + kFull + st);
+      const float x[4] = {now.s.x, now.s.y, now.s.z, now.s.w};
+      float y[4];
+      if constexpr (V) {
+        // a scale counts as finite where its largest code is (append writes no others)
+        uint32_t fin = 0;
+        float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool there = (now.ok >> i) & 1u;
-        if constexpr (V) {
-          // a scale counts as finite where its largest code is (append writes no others)
-          const bool finite = now.s[i] <= top;  // (not for a NaN)
-          const int e = max(exp_above(warp_max_f32(there && finite ? now.s[i] : 0.f)), kLowV);
-          info->vs[i * 32 + lane] = there && finite ? now.s[i] * exp2i(-e) : 0.f;
-          const uint32_t bad = __ballot_sync(0xffffffffu, there && !finite);
-          if (lane == 0) {
-            info->ev[i] = e;
-            info->bad[i] = bad;
+        for (int i = 0; i < 4; ++i) {
+          const bool f = x[i] <= top;  // (not for a NaN)
+          fin |= f ? 1u << i : 0u;
+          y[i] = f && (now.ok >> i) & 1u ? x[i] : 0.f;
+          m = fmaxf(m, y[i]);
+        }
+#pragma unroll
+        for (int i = 1; i < 8; i <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+        const int e = max(exp_above(m), kLowV);
+        const float f = exp2i(-e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] *= f;
+        uint32_t bad = 0;
+        if (__any_sync(0xffffffffu, (now.ok & ~fin) != 0)) bad = group_bits(now.ok & ~fin, lane);
+        if (lead) {
+          info->ev[grp] = e;
+          info->bad[grp] = bad;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = (now.ok >> i) & 1u ? x[i] : 0.f;
+        if (bias) {
+          float p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = j0 + lane * 4 + i;
+            p[i] = static_cast<float>(j < o.ctx || j >= o.L ? j - o.ctx
+                                                            : __ldg(tv.depth + o.qlo + j - o.ctx));
           }
-        } else {
-          info->ks[i * 32 + lane] = there ? now.s[i] : 0.f;
-          if (bias) {
-            const int p = j0 + i * 32 + lane;
-            info->pos[i * 32 + lane] = static_cast<float>(
-                p < o.ctx || p >= o.L ? p - o.ctx : __ldg(tv.depth + o.qlo + p - o.ctx));
-          }
-          if (lane == 0) {
-            info->valid[i] = held[i];
-            info->seen[i] = o.sees(j0 + i * 32) && held[i] == 0xFFFFFFFFu;
-          }
+          reinterpret_cast<float4*>(info->pos)[lane] = make_float4(p[0], p[1], p[2], p[3]);
+        }
+        if (lead) {
+          info->valid[grp] = held;
+          info->seen[grp] = held == 0xFFFFFFFFu && (all_rows || o.sees(j0 + grp * 32));
+        }
+        if (lane == 0) {
+          info->j0 = j0;
+          info->ctx = o.ctx;
+          info->pre = o.seen.pre;
         }
       }
-      if (!V && lane == 0) {
-        info->j0 = j0;
-        info->ctx = o.ctx;
-        info->pre = o.seen.pre;
-      }
+      reinterpret_cast<float4*>(V ? info->vs : info->ks)[lane] = make_float4(y[0], y[1], y[2], y[3]);
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + kTInfo + g % kInfos);
     }
