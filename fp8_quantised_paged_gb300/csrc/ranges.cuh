@@ -27,28 +27,40 @@ __device__ __forceinline__ int last_le(const int* a, int n, int x) {
   return lo;
 }
 
-// Cuts the blocks' `tiles` token tiles (v.rb_pre), for every KV head, into ranges; a cut
-// within kSnap tiles of an item's edge moves there.  Run by one CTA.
+// Cuts the blocks' `tiles` token tiles (v.rb_pre), for every KV head, into ranges of the
+// same cost: an item (a block and KV head) costs its tiles and kCost more.  A cut within
+// kSnap tiles of an item's edge moves there.  Run by one CTA.
+template <int kCost = 0>
 __device__ __forceinline__ void cut_ranges(const PlanView& v, int blocks, int tiles, int hkv,
                                            int ranges) {
   const int tid = threadIdx.x;
   const int U = tiles * hkv;
-  const int upw = max(1, (U + ranges - 1) / ranges);
+  const long long all = U + static_cast<long long>(kCost) * blocks * hkv;
+  const long long upw = max(1ll, (all + ranges - 1) / ranges);
   if (tid == 0) {
     v.head[0] = U;
-    v.head[1] = upw;
+    v.head[1] = static_cast<int>(upw);
   }
   for (int w = tid; w <= ranges; w += kPlanThreads) {
-    const long long want = static_cast<long long>(w) * upw;
-    int u = want < U ? static_cast<int>(want) : U, it = blocks * hkv;
-    if (u < U) {
-      const int rb = last_le(v.rb_pre, blocks, u / hkv);
-      const int pre = v.rb_pre[rb], c = v.rb_pre[rb + 1] - pre;
-      const int h = (u - pre * hkv) / c, f = pre * hkv + h * c;
+    const long long want = w * upw;
+    int u = U, it = blocks * hkv;
+    if (want < all) {
+      // the block that holds it, of those that start at cost (rb_pre + kCost rb) hkv or before
+      int lo = 0, hi = blocks;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((v.rb_pre[mid] + static_cast<long long>(kCost) * mid) * hkv <= want) lo = mid;
+        else hi = mid;
+      }
+      const int rb = lo, pre = v.rb_pre[rb], c = v.rb_pre[rb + 1] - pre;
+      const long long in = want - (pre + static_cast<long long>(kCost) * rb) * hkv;
+      const int h = static_cast<int>(in / (c + kCost)), f = pre * hkv + h * c;
+      const int tile = max(static_cast<int>(in - static_cast<long long>(h) * (c + kCost)) - kCost, 0);
       it = rb * hkv + h;
-      if (u - f < kSnap) {
+      u = f + tile;
+      if (tile < kSnap) {
         u = f;
-      } else if (f + c - u < kSnap) {
+      } else if (c - tile < kSnap) {
         u = f + c;
         ++it;
       }

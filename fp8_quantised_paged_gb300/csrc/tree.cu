@@ -7,6 +7,9 @@ namespace fp8pa {
 
 namespace {
 
+// What an item costs beside its tiles, in tiles.
+constexpr int kItemCost = 11;
+
 // A request's tree and its visible extent; n is 0 for a request that is skipped, `flag`
 // why.
 __device__ __forceinline__ Chunk load_tree(const PrefillArgs& a, int b, uint32_t* flag) {
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const PrefillAr
   }
   if (tid == 0) v.rb_pre[blocks] = carry;
   __syncthreads();
-  cut_ranges(v, blocks, carry, a.hkv, ranges);
+  cut_ranges<kItemCost>(v, blocks, carry, a.hkv, ranges);
 }
 
 size_t tree_layout(char* ws, int total_q, int batch, int G, int d, int ranges, PlanView* v,
@@ -197,7 +200,7 @@ cudaError_t launch_tree(const PrefillArgs& args, const int32_t* parents, cudaStr
   cfg.gridDim = dim3(static_cast<unsigned>(ranges));
   cfg.blockDim = dim3(static_cast<unsigned>(fn.threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(fn.smem);
-  const TreeView tv{line, depth};
+  const TreeView tv{line, depth, make_fast_div(static_cast<uint32_t>(a.G))};
   if ((e = cudaLaunchKernelEx(&cfg, fn.fn, a, pv, tv, mk, mv)) != cudaSuccess) return e;
   return launch_merge_ranges(a, pv, ranges, stream);
 }

@@ -44,6 +44,7 @@ namespace fp8pa {
 struct TreeView {
   const uint32_t* line;  // [total_q][8] the nodes on a node's line, as the window leaves them
   const int32_t* depth;  // [total_q]
+  FastDiv div_g;         // by the heads of a KV head
 };
 
 using TreeFn = void (*)(const PrefillArgs, const PlanView, const TreeView, const CUtensorMap,
@@ -803,7 +804,7 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
       // query and head of a lane's row (lanes past the block's end: its last row)
       auto query_of = [&](int l, int& qi, int& h) {
         const int rr = im.r.row0 + min(l & (sl - 1), im.r.rows - 1);
-        qi = rr / a.G;
+        qi = static_cast<int>(fast_div(static_cast<uint32_t>(rr), tv.div_g));
         h = im.kvh * a.G + rr - qi * a.G;
       };
       {
@@ -824,25 +825,24 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           uint4 raw[D / 32];
 #pragma unroll
           for (int x = 0; x < D / 32; ++x) raw[x] = __ldg(src + x * 4);
-          auto get = [&](int x, float (&f)[8]) {
+          float f[D / 32][8], amax = 0.f;
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) {
             const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              f[2 * e] = __uint_as_float(w[e] << 16) * sgn;
-              f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * sgn;
+              f[x][2 * e] = __uint_as_float(w[e] << 16) * sgn;
+              f[x][2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * sgn;
             }
             if (st) {
+              const float4* k8 = reinterpret_cast<const float4*>(kc + (x * 4 + c4) * 8);
+              const float4 k0 = __ldg(k8), k1 = __ldg(k8 + 1);
+              const float k[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] *= __ldg(kc + (x * 4 + c4) * 8 + e);
+              for (int e = 0; e < 8; ++e) f[x][e] *= k[e];
             }
-          };
-          float amax = 0.f;
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            float f[8];
-            get(x, f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[x][e]));
           }
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
@@ -852,17 +852,15 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           const float fq = exp2i(kTop - eq);
 #pragma unroll
           for (int x = 0; x < D / 32; ++x) {
-            float f[8];
-            get(x, f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] *= fq;
+            for (int e = 0; e < 8; ++e) f[x][e] *= fq;
             if constexpr (RAW) {  // hi, and lo = what hi leaves
               uint32_t hi[4], lo[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                hi[e] = f32x2_to_codes2<FP8PA_E4M3>(f[2 * e], f[2 * e + 1]);
+                hi[e] = f32x2_to_codes2<FP8PA_E4M3>(f[x][2 * e], f[x][2 * e + 1]);
                 const float2 b = __half22float2(h2(codes2_to_f16x2<FP8PA_E4M3>(hi[e])));
-                lo[e] = f32x2_to_codes2<FP8PA_E4M3>(f[2 * e] - b.x, f[2 * e + 1] - b.y);
+                lo[e] = f32x2_to_codes2<FP8PA_E4M3>(f[x][2 * e] - b.x, f[x][2 * e + 1] - b.y);
               }
               const int c8 = x * 4 + c4;  // 8 dims: half a 16-byte chunk
               uint8_t* p = dst + swizzled<D>(to_row, c8 >> 1) + (c8 & 1) * 8;
@@ -872,8 +870,8 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
             } else {
               *reinterpret_cast<uint4*>(dst + (to_row >> 3) * 128 + r8 * 16 +
                                         (x * 4 + c4) * 2048) =
-                  make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]),
-                             pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+                  make_uint4(pack_half2(f[x][0], f[x][1]), pack_half2(f[x][2], f[x][3]),
+                             pack_half2(f[x][4], f[x][5]), pack_half2(f[x][6], f[x][7]));
             }
           }
         }
@@ -1066,102 +1064,85 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
 
       // ---- the block's result, or this range's piece of it, from the row's partial
       // results: of both streams, and of the shares of the lanes
-      const int r = rl & (sl - 1);
-      const bool first = t == 0 && rl < sl, live = first && r < im.r.rows;  // (first: whole warps)
       const bool piece = im.t0 > 0 || im.t1 < im.r.count;
-      const long at_row = piece ? (static_cast<long>(blockIdx.x) * 2 + (im.t0 > 0 ? 0 : 1)) * kRows + r
-                                : static_cast<long>(qrow) * a.hq + h;
       const bool stat = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
       const float* vch = a.v_scale + static_cast<long>(im.kvh) * D;
+      const long slot = (static_cast<long>(blockIdx.x) * 2 + (im.t0 > 0 ? 0 : 1)) * kRows;
+      const int partials = n > 1 ? 256 : 128;  // lanes of the streams that had a tile
       ml[t * 128 + rl] = make_float2(ref, l);
       if (!sync_all()) {
         ok = false;
         break;
       }
       float M = kNegBig, sum = 0.f;
-      for (int x = r; x < 256; x += sl) M = fmaxf(M, ml[x].x);
-      for (int x = r; x < 256; x += sl) sum += ml[x].y * ex2(ml[x].x - M);
+      for (int x = rl & (sl - 1); x < 256; x += sl) M = fmaxf(M, ml[x].x);
+      for (int x = rl & (sl - 1); x < 256; x += sl) sum += ml[x].y * ex2(ml[x].x - M);
       const float scale = ex2(ref - M) * (piece ? 1.f : (sum == 0.f ? 0.f : 1.f / sum));
-      if (piece && live) pv.ml[at_row] = make_float2(M, sum);
-      // half of the dims at a time, in q's place: chunk c (4 dims) of lane y's, free of bank
-      // conflicts
+      if (piece && t == 0 && rl < im.r.rows && rl < sl) pv.ml[slot + rl] = make_float2(M, sum);
+      // a quarter of the dims at a time: every lane leaves its part, in q's place, then all
+      // threads add them up, four dims of a row each.  Chunk c (4 dims) of lane y's part,
+      // free of bank conflicts:
+      constexpr int kChunks = D / 16;
       auto at = [&](int y, int c) {
-        return reinterpret_cast<float4*>(sm + SM::kQ + y * (D * 2) +
-                                         (((c & ~7) | ((c ^ y) & 7)) << 4));
+        return reinterpret_cast<float4*>(sm + SM::kQ + y * (kChunks * 16) +
+                                         ((c ^ y) & (kChunks - 1)) * 16);
       };
-      const bool both = n > 1;  // whether stream 1 had a tile
 #pragma unroll 1
-      for (int dh = 0; dh < 2 && ok; ++dh) {
-        auto take = [&](int c, float (&f)[16]) {  // of this lane's O
-          uint32_t o[16];
-          tmem_ld16(to + dh * (D / 2) + c * 16, o);
-          tmem_ld_wait();
-          tmem_landed(o);
+      for (int dq = 0; dq < 4 && ok; ++dq) {
+        if (t * 128 < partials) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(o[i]) * scale;
-        };
-        auto add = [&](int y, int c, float (&f)[16]) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 v = *at(y, c * 4 + i);
-            f[4 * i] += v.x;
-            f[4 * i + 1] += v.y;
-            f[4 * i + 2] += v.z;
-            f[4 * i + 3] += v.w;
-          }
-        };
-#pragma unroll 1
-        for (int s = 0; s < 2 && ok; ++s) {  // stream 1 to stream 0, then the shares to the first
-          if (s == 0 ? t == 1 && both : t == 0 && rl >= sl) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              float f[16];
-              take(c, f);
-              if (s == 1 && both) add(rl, c, f);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *at(rl, c * 4 + i) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-            }
-          }
-          if (s == 0 || sl < 128) ok = sync_all();
-        }
-        if (ok && first) {
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t o[16];
+            tmem_ld16(to + dq * (D / 4) + c * 16, o);
+            tmem_ld_wait();
+            tmem_landed(o);
             float f[16];
-            take(c, f);
-            if (both) add(rl, c, f);
-            for (int y = rl + sl; y < 128; y += sl) add(y, c, f);
-            if (!live) continue;
-            const int d0 = dh * (D / 2) + c * 16;
-            if (stat) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) f[i] *= __ldg(vch + d0 + i);
-            }
-            if (piece || a.out_f32) {
-              float* dst = (piece ? pv.o : reinterpret_cast<float*>(a.out)) + at_row * D + d0;
+            for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(o[i]) * scale;
 #pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4*>(dst + i) =
-                    make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
-            } else {
-              uint4* dst =
-                  reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at_row * D + d0);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                uint32_t w[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  const __nv_bfloat162 b2 =
-                      __floats2bfloat162_rn(f[8 * i + 2 * y], f[8 * i + 2 * y + 1]);
-                  w[y] = *reinterpret_cast<const uint32_t*>(&b2);
-                }
-                dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            }
+            for (int i = 0; i < 4; ++i)
+              *at(t * 128 + rl, c * 4 + i) =
+                  make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
           }
         }
-        if (ok) ok = sync_all();  // (also: the sums lie where the next item's q goes)
+        if (!sync_all()) {
+          ok = false;
+          break;
+        }
+        for (int i = tid; i < im.r.rows * kChunks; i += 256) {
+          const int r = i / kChunks, c = i % kChunks, d0 = dq * (D / 4) + c * 4;
+          float4 v = *at(r, c);
+          for (int y = r + sl; y < partials; y += sl) {
+            const float4 x = *at(y, c);
+            v.x += x.x;
+            v.y += x.y;
+            v.z += x.z;
+            v.w += x.w;
+          }
+          if (stat) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(vch + d0));
+            v.x *= x.x;
+            v.y *= x.y;
+            v.z *= x.z;
+            v.w *= x.w;
+          }
+          if (piece) {
+            *reinterpret_cast<float4*>(pv.o + (slot + r) * D + d0) = v;
+            continue;
+          }
+          int qy, hy;
+          query_of(r, qy, hy);
+          const long to_row = ((static_cast<long>(im.r.qlo) + qy) * a.hq + hy) * D + d0;
+          if (a.out_f32) {
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + to_row) = v;
+          } else {
+            const __nv_bfloat162 b[2] = {__floats2bfloat162_rn(v.x, v.y),
+                                         __floats2bfloat162_rn(v.z, v.w)};
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + to_row) =
+                *reinterpret_cast<const uint2*>(b);
+          }
+        }
+        if (!sync_all()) ok = false;  // (also: the next item's q goes there)
       }
       tc_fence_before();
     }
