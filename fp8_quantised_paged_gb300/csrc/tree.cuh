@@ -385,10 +385,59 @@ __device__ __forceinline__ void put_v_info(TileInfo* info, int dw, int lane, flo
   }
 }
 
+// 32 tokens of a tile and KV head, by one warp: a lane holds row r8 = lane % 8 of four
+// 8-row groups and, of each, the 16-byte chunks lane / 8 (and 4 more), as the prefill's
+// Job, but has the exponents of its rows from memory and not from other lanes.
+template <int D>
+struct Codes {
+  uint4 buf[4][D / 64];
+  uint32_t okm;    // groups whose row is wanted and exists
+  uint2 ex[4];     // MX: the exponents of the rows' blocks
+  float sc;        // scale of token `lane`
+  bool sok;        // ... which is wanted and exists
+};
+template <int D, bool MX>
+__device__ __forceinline__ void load_codes(const PrefillArgs& a, const OpenItem& o, bool V,
+                                           const int (&ids)[2], int j, int lane, Codes<D>& c) {
+  const int r8 = lane & 7, c4 = lane >> 3;
+  const uint8_t* cache = V ? a.v_cache : a.k_cache;
+  const float* scale = V ? a.v_scale : a.k_scale;
+  const bool there[2] = {ids[0] >= 0 && ids[0] < a.num_blocks,
+                         ids[1] >= 0 && ids[1] < a.num_blocks};
+  // (a missing block's rows read as block 0's: not used)
+  const uint32_t row[2] = {there[0] ? cache_row(a, o.kvh, ids[0], j) : 0u,
+                           there[1] ? cache_row(a, o.kvh, ids[1], j + 16) : 0u};
+  c.okm = 0;
+  const int nbx = MX ? D / a.gs : 0;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const uint32_t rw = row[x >> 1] + (x & 1) * 8 + r8;
+    const uint8_t* src = cache + static_cast<size_t>(rw) * D + c4 * 16;
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) c.buf[x][h] = ld_codes(src + h * 64);
+    if (o.seen(j + x * 8 + r8) && there[x >> 1]) c.okm |= 1u << x;
+    if constexpr (MX) {
+      const uint8_t* e = reinterpret_cast<const uint8_t*>(scale) + static_cast<size_t>(rw) * nbx;
+      c.ex[x] = make_uint2(0u, 0u);
+      if (nbx == 8) c.ex[x] = __ldg(reinterpret_cast<const uint2*>(e));
+      else if (nbx == 4) c.ex[x].x = __ldg(reinterpret_cast<const uint32_t*>(e));
+      else c.ex[x].x = __ldg(reinterpret_cast<const uint16_t*>(e));
+    }
+  }
+  const bool want = o.seen(j + lane);
+  c.sok = want && (lane < 16 ? there[0] : there[1]);
+  if (!V && want && !c.sok) raise_error(a.err, FP8PA_DEVERR_BLOCK_RANGE);
+  c.sc = 1.f;
+  if (a.mode == FP8PA_SCALE_TOKEN_HEAD)
+    c.sc = __ldg(scale + (lane < 16 ? row[0] : row[1]) + (lane & 15));
+  else if (a.mode == FP8PA_SCALE_SEGMENT && c.sok)
+    c.sc = __ldg(scale + static_cast<size_t>(lane < 16 ? ids[0] : ids[1]) * a.hp + o.kvh);
+}
+
 // The tokens of a job of V whose codes are not all finite (bits of the 32); their rows are
 // taken out of job.okm.
 template <int D, int FMT>
-__device__ __forceinline__ uint32_t drop_nonfinite(Job<D>& job, int lane) {
+__device__ __forceinline__ uint32_t drop_nonfinite(Codes<D>& job, int lane) {
   if constexpr (FMT == FP8PA_INT8) return 0;
   uint32_t nf = 0, bad = 0;  // bit x of nf: this lane's chunks of row group x
 #pragma unroll
@@ -410,7 +459,8 @@ __device__ __forceinline__ uint32_t drop_nonfinite(Job<D>& job, int lane) {
 
 // A job's codes as f16 into a tile; rows of V that are not in job.okm are zero.
 template <int D, int FMT, bool MX>
-__device__ __forceinline__ void put_tile(Job<D>& job, bool V, int dw, uint8_t* tile, int lane) {
+__device__ __forceinline__ void put_tile(const Codes<D>& job, bool V, int dw, int gs,
+                                         uint8_t* tile, int lane) {
   constexpr int H = D / 64;
   constexpr int kRoom = FMT == FP8PA_E5M2 ? 0 : 7;
   const int r8 = lane & 7, c4 = lane >> 3;
@@ -421,15 +471,16 @@ __device__ __forceinline__ void put_tile(Job<D>& job, bool V, int dw, uint8_t* t
   const bool drop = V && !__all_sync(0xffffffffu, job.okm == 0xFu);
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
-    int em = 0;
-    if constexpr (MX) em = __shfl_sync(0xffffffffu, job.em, x * 8 + r8);
+    int top = 0;  // the row's largest exponent
+    if constexpr (MX) top = static_cast<int>(max_byte(reinterpret_cast<const uint32_t(&)[2]>(job.ex[x])));
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       uint4 p, q;
       codes16_to_f16<FMT>(job.buf[x][h], p, q);
       if constexpr (MX) {
-        const int be = static_cast<int>((job.ex[h] >> (8 * x)) & 0xFFu) - em + kRoom;
-        const float f = exp2i(be);
+        const int b = (h * 4 + c4) * 16 / gs;
+        const uint32_t e = (b & 4 ? job.ex[x].y : job.ex[x].x) >> (8 * (b & 3)) & 0xFFu;
+        const float f = exp2i(static_cast<int>(e) - top + kRoom);
         const __half2 f2 = __floats2half2_rn(f, f);
         p = scale8(p, f2);
         q = scale8(q, f2);
@@ -454,8 +505,7 @@ __device__ __forceinline__ void convert_raw(const PrefillArgs& a, uint8_t* sm, i
     const uint32_t st = g & 1;
     if (!__all_sync(0xffffffffu, tc_wait(bars + kTVCFull + st, (g >> 1) & 1, abort_flag, a.err)))
       return;
-    // rows r8 of four groups of 8, 16-byte chunks c4 (and c4 + 4)
-    Job<D> job;
+    Codes<D> job;
     const uint8_t* src = sm + SM::kVCodes + st * SM::kCodes;
 #pragma unroll
     for (int x = 0; x < 4; ++x)
@@ -478,7 +528,7 @@ __device__ __forceinline__ void convert_raw(const PrefillArgs& a, uint8_t* sm, i
     if (g >= 2 && !__all_sync(0xffffffffu, tc_wait(bars + kTVFree + st, ((g >> 1) - 1) & 1,
                                                    abort_flag, a.err)))
       return;
-    put_tile<D, FMT, false>(job, true, dw, sm + SM::kV + st * SM::kHalf, lane);
+    put_tile<D, FMT, false>(job, true, dw, 0, sm + SM::kV + st * SM::kHalf, lane);
     if (lane == 0) info->cbad[dw] = bad;
     fence_proxy_async();
     __syncwarp();
@@ -511,8 +561,8 @@ __device__ __forceinline__ void convert_loaded(const PrefillArgs& a, const PlanV
     for (int k = im.t0; k < im.t1; ++k, ++g) {
       const uint32_t st = g & 1, si = g % kInfos;
       const int j0 = o.token_of(k), j = j0 + dw * 32;
-      Job<D> job;
-      load_job<D, MX>(a, V, o.kvh, ids, j, o.seen, lane, job);
+      Codes<D> job;
+      load_codes<D, MX>(a, o, V, ids, j, lane, job);
       if (k + 1 < im.t1) job_blocks(o.table, lgbs, o.seen, o.token_of(k + 1) + dw * 32, ids);
       if (lane < 2 && k + kAhead < im.t1) {
         const int t = o.token_of(k + kAhead) + dw * 32 + lane * 16;
@@ -528,8 +578,12 @@ __device__ __forceinline__ void convert_loaded(const PrefillArgs& a, const PlanV
         }
       }
       float scale = job.sc;
-      if constexpr (MX)
-        scale = job.em == 255 ? __int_as_float(0x7FC00000) : pow2_any(job.em - 127 - kRoom);
+      if constexpr (MX) {  // of token `lane`: this lane's row of group c4
+        const uint2 e = lane < 16 ? (lane < 8 ? job.ex[0] : job.ex[1])
+                                  : (lane < 24 ? job.ex[2] : job.ex[3]);
+        const int top = static_cast<int>(max_byte(reinterpret_cast<const uint32_t(&)[2]>(e)));
+        scale = top == 255 ? __int_as_float(0x7FC00000) : pow2_any(top - 127 - kRoom);
+      }
       // V's info goes first, as S waits for it.  (An info's last reader, the softmax of the
       // stream's tile after g - 8, came before the waits of tiles before.)
       TileInfo* info = infos + si;
@@ -543,7 +597,7 @@ __device__ __forceinline__ void convert_loaded(const PrefillArgs& a, const PlanV
       if (g >= 2 && !__all_sync(0xffffffffu, tc_wait(bars + (V ? kTVFree : kTKFree) + st,
                                                      ((g >> 1) - 1) & 1, abort_flag, a.err)))
         return;
-      put_tile<D, FMT, MX>(job, V, dw, sm + (V ? SM::kV : SM::kK) + st * SM::kHalf, lane);
+      put_tile<D, FMT, MX>(job, V, dw, a.gs, sm + (V ? SM::kV : SM::kK) + st * SM::kHalf, lane);
       if (!V) put_k_info(tv, o, info, dw, j, lane, scale, job.sok, bias);
       fence_proxy_async();
       __syncwarp();
