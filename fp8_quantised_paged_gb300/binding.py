@@ -819,7 +819,7 @@ def kv_resize(new_lens, block_tables, seq_lens, ref_counts, block_size, workspac
     """Give every row the length new_lens[r] (int32 [rows]): pages behind it are given
     back, missing ones taken from the free pages, the lowest first; 0 frees the row.
     block_tables, seq_lens and ref_counts change in place."""
-    _want(ref_counts, torch.int32, "ref_counts", ref_counts.device)
+    _need(ref_counts, torch.int32, "ref_counts")
     dev = ref_counts.device
     rows, max_blocks = _check_tables(block_tables, seq_lens, dev)
     _want(new_lens, torch.int32, "new_lens", dev)

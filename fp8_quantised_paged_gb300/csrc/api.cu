@@ -372,9 +372,10 @@ int append_prepare(const void* k, const void* v, const int32_t* slot_mapping, in
   return FP8PA_OK;
 }
 
-// The sizes of a prefill call that its workspace depends on: every limit that does not
-// need the pool's size, the format or the scale mode.
-int prefill_shape(int total_q, int batch, int hq, int hkv, int d, int bs, int max_blocks) {
+// The sizes of a prefill or tree call that its workspace depends on: every limit that does
+// not need the pool's size, the format or the scale mode.  rows: of its planner's blocks.
+int prefill_shape(int total_q, int batch, int hq, int hkv, int d, int bs, int max_blocks,
+                  int rows) {
   if (total_q < 0 || batch < 0 || hq <= 0 || hkv <= 0 || hq % hkv != 0 || bs <= 0 ||
       max_blocks <= 0)
     return FP8PA_ERR_BAD_SHAPE;
@@ -382,8 +383,8 @@ int prefill_shape(int total_q, int batch, int hq, int hkv, int d, int bs, int ma
   if ((static_cast<long long>(total_q) + 256ll * batch) * hq >= (1ll << 31) ||
       static_cast<long long>(bs) * max_blocks * hkv > (1ll << 31) - 128)  // whole tiles
     return FP8PA_ERR_UNSUPPORTED;
-  // the planner counts (256-row block, KV head, 128-token tile) units in 32 bits
-  const long long blocks = static_cast<long long>(total_q) * (hq / hkv) / 256 + 1 + batch;
+  // the planner counts (row block, KV head, 128-token tile) units in 32 bits
+  const long long blocks = static_cast<long long>(total_q) * (hq / hkv) / rows + 1 + batch;
   if (blocks * hkv * (static_cast<long long>(max_blocks) * bs / 128 + 1) >= (1ll << 31))
     return FP8PA_ERR_UNSUPPORTED;
   return FP8PA_OK;
@@ -399,10 +400,11 @@ int prefill_prepare(const void* q, const int32_t* q_offsets, int total_q, const 
                     int fmt, int scale_mode, int group_size, float sm_scale, int window,
                     const int32_t* prefix_lens, float logit_cap, const float* alibi_slopes,
                     int num_blocks, void* out, int out_dtype, void* workspace,
-                    size_t workspace_bytes, cudaStream_t stream, PrefillArgs* args, int* dev) {
+                    size_t workspace_bytes, cudaStream_t stream, int rows, PrefillArgs* args,
+                    int* dev) {
   if (window < 0) return FP8PA_ERR_BAD_SHAPE;
   int st = prefill_shape(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
-                         max_blocks_per_seq);
+                         max_blocks_per_seq, rows);
   if (st != FP8PA_OK) return st;
   // formats, scale modes, block sizes and pool sizes as the decode's GQA layout
   st = decode_path(1, 1, n_kv_heads, n_kv_heads, head_dim, head_dim, block_size,
@@ -816,7 +818,7 @@ int fp8pa_paged_decode_attention_mod(const void* q, const uint8_t* k_cache,
 size_t fp8pa_prefill_workspace_bytes(int total_q, int batch, int n_q_heads, int n_kv_heads,
                                      int head_dim, int block_size, int max_blocks_per_seq) {
   if (prefill_shape(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
-                    max_blocks_per_seq) != FP8PA_OK)
+                    max_blocks_per_seq, kPrefillRows) != FP8PA_OK)
     return 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
@@ -842,7 +844,7 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
                                  n_q_heads, n_kv_heads, head_dim, fmt, scale_mode, group_size,
                                  sm_scale, window, prefix_lens, logit_cap, alibi_slopes,
                                  num_blocks, out, out_dtype, workspace, workspace_bytes,
-                                 static_cast<cudaStream_t>(stream), &a, &dev);
+                                 static_cast<cudaStream_t>(stream), kPrefillRows, &a, &dev);
   if (st != FP8PA_OK || batch == 0 || total_q == 0) return st;
   if (workspace_bytes <
       prefill_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
@@ -854,7 +856,7 @@ int fp8pa_paged_prefill_attention(const void* q, const int32_t* q_offsets, int t
 size_t fp8pa_tree_workspace_bytes(int total_q, int batch, int n_q_heads, int n_kv_heads,
                                   int head_dim, int block_size, int max_blocks_per_seq) {
   if (prefill_shape(total_q, batch, n_q_heads, n_kv_heads, head_dim, block_size,
-                    max_blocks_per_seq) != FP8PA_OK)
+                    max_blocks_per_seq, kTreeRows) != FP8PA_OK)
     return 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
@@ -880,7 +882,7 @@ int fp8pa_paged_tree_attention(const void* q, const int32_t* q_offsets, int tota
                                  n_q_heads, n_kv_heads, head_dim, fmt, scale_mode, group_size,
                                  sm_scale, window, prefix_lens, logit_cap, alibi_slopes,
                                  num_blocks, out, out_dtype, workspace, workspace_bytes,
-                                 static_cast<cudaStream_t>(stream), &a, &dev);
+                                 static_cast<cudaStream_t>(stream), kTreeRows, &a, &dev);
   if (st != FP8PA_OK || batch == 0 || total_q == 0) return st;
   if (workspace_bytes <
       tree_workspace_bytes(total_q, batch, n_q_heads, n_kv_heads, head_dim, dev))

@@ -210,12 +210,14 @@ struct PrefillArgs {
   size_t workspace_bytes;
   uint32_t* err;
 };
+constexpr int kPrefillRows = 256;  // rows (queries times heads per KV head) of a block
 // What a prefill uses, or (least) what it cannot do without: the plan and the pieces.
 size_t prefill_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, int bs,
                                int max_blocks, int device, bool least);
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 
 // Attention for trees of drafted tokens (tree.cu): a prefill's arguments and the parents.
+constexpr int kTreeRows = 128;
 size_t tree_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, int device);
 cudaError_t launch_tree(const PrefillArgs& a, const int32_t* parents, cudaStream_t stream);
 

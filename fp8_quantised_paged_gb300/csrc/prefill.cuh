@@ -99,7 +99,7 @@ cudaError_t launch_merge_ranges(const PrefillArgs& a, const PlanView& pv, int ra
 
 namespace {
 
-constexpr int kRows = 256;   // rows of a block: two tiles of 128
+constexpr int kRows = kPrefillRows;  // two tiles of 128
 constexpr int kT = 128;      // tokens per tile
 constexpr int kAhead = 3;    // jobs that a converting warp asks L2 for ahead
 constexpr int kConvWarp = 16, kConvWarps = 7;  // or a K and a V loader over ready tiles

@@ -87,7 +87,6 @@ struct RowMask {
   int wf, node;
 };
 
-constexpr int kTreeRows = 128;  // rows of a block
 
 template <int D, bool RAW>
 struct TreeSmem {
