@@ -69,10 +69,11 @@ namespace fp8pa {
 // request and the prefix of its tiles, then the ranges' first units, then the
 // partial pieces.
 struct PlanView {
-  int* head;     // [0] units, [1] units per range (before cuts move)
+  int* head;     // [0] units
   int* rbase;    // [batch + 1] first row block of a request
   int4* rb;      // [blocks][3] a row block: see RowBlock
   int* rb_pre;   // [blocks + 1] tiles before a row block (of one KV head)
+  int* rb_wide;  // trees: and those among them of blocks of more than 128 rows
   int* start;    // [ranges + 1] first unit of a range
   int* item;     // [ranges + 1] the item that holds it
   float2* ml;    // [2 * ranges][kRows] reference and sum of a piece

@@ -28,34 +28,31 @@ __device__ __forceinline__ int last_le(const int* a, int n, int x) {
 }
 
 // Cuts the blocks' `tiles` token tiles (v.rb_pre), for every KV head, into ranges of the
-// same cost: an item (a block and KV head) costs its tiles and kCost more.  A cut within
-// kSnap tiles of an item's edge moves there.  Run by one CTA.
-template <int kCost = 0>
+// same cost.  cost(i): of the blocks before block i (of one KV head), where an item (a block
+// and KV head) costs kCost and as much for each of its tiles.  A cut within kSnap tiles of an
+// item's edge moves there.  Run by one CTA.
+template <int kCost = 0, typename Cost>
 __device__ __forceinline__ void cut_ranges(const PlanView& v, int blocks, int tiles, int hkv,
-                                           int ranges) {
+                                           int ranges, const Cost& cost) {
   const int tid = threadIdx.x;
   const int U = tiles * hkv;
-  const long long all = U + static_cast<long long>(kCost) * blocks * hkv;
+  const long long all = cost(blocks) * hkv;
   const long long upw = max(1ll, (all + ranges - 1) / ranges);
-  if (tid == 0) {
-    v.head[0] = U;
-    v.head[1] = static_cast<int>(upw);
-  }
+  if (tid == 0) v.head[0] = U;
   for (int w = tid; w <= ranges; w += kPlanThreads) {
     const long long want = w * upw;
     int u = U, it = blocks * hkv;
     if (want < all) {
-      // the block that holds it, of those that start at cost (rb_pre + kCost rb) hkv or before
-      int lo = 0, hi = blocks;
+      int lo = 0, hi = blocks;  // the block that holds it
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((v.rb_pre[mid] + static_cast<long long>(kCost) * mid) * hkv <= want) lo = mid;
+        if (cost(mid) * hkv <= want) lo = mid;
         else hi = mid;
       }
       const int rb = lo, pre = v.rb_pre[rb], c = v.rb_pre[rb + 1] - pre;
-      const long long in = want - (pre + static_cast<long long>(kCost) * rb) * hkv;
-      const int h = static_cast<int>(in / (c + kCost)), f = pre * hkv + h * c;
-      const int tile = max(static_cast<int>(in - static_cast<long long>(h) * (c + kCost)) - kCost, 0);
+      const long long first = cost(rb), each = cost(rb + 1) - first, in = want - first * hkv;
+      const int h = static_cast<int>(in / each), f = pre * hkv + h * c;
+      const int tile = static_cast<int>(max(in - h * each - kCost, 0ll) * c / (each - kCost));
       it = rb * hkv + h;
       u = f + tile;
       if (tile < kSnap) {

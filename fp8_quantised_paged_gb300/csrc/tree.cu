@@ -7,8 +7,9 @@ namespace fp8pa {
 
 namespace {
 
-// What an item costs beside its tiles, in tiles.
-constexpr int kItemCost = 11;
+// What a tile costs, of a block of at most 128 rows and of a larger one, and what an item
+// costs beside its tiles.
+constexpr int kTileCost = 5, kWideCost = 7, kItemCost = 55;
 
 // A request's tree and its visible extent; n is 0 for a request that is skipped, `flag`
 // why.
@@ -22,18 +23,18 @@ __device__ __forceinline__ Chunk load_tree(const PrefillArgs& a, int b, uint32_t
   return c;
 }
 
-// Row block t of a request.  Any node may see the whole context, and the window of a node
+// Block t, of `rows` rows, of a request.  Any node may see the whole context, and the window of a node
 // on the first level begins earliest.
 __device__ __forceinline__ RowBlock make_tree_block(const Chunk& c, int b, int window, int G,
-                                                    int t) {
+                                                    int rows, int t) {
   RowBlock r;
   r.b = b;
   r.qlo = c.qlo;
   r.n = c.n;
   r.L = c.L;
   r.pre = c.pre;
-  r.row0 = t * kTreeRows;
-  r.rows = min(kTreeRows, c.n * G - r.row0);
+  r.row0 = t * rows;
+  r.rows = min(rows, c.n * G - r.row0);
   r.pA = c.L - c.n;  // tokens ahead of the tree
   r.pB = c.L - 1;
   r.np = (c.pre + kT - 1) / kT;
@@ -42,12 +43,12 @@ __device__ __forceinline__ RowBlock make_tree_block(const Chunk& c, int b, int w
   return r;
 }
 
-// CTA 0 plans; CTA 1 + b writes the lines of request b's nodes, a thread each.
+// CTA 0 plans blocks of `rows` rows; CTA 1 + b writes the lines of request b's nodes, a thread each.
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const PrefillArgs a,
                                                                  const PlanView v,
                                                                  const int32_t* parents,
                                                                  uint32_t* lines, int32_t* depths,
-                                                                 int ranges) {
+                                                                 int rows, int ranges) {
   __shared__ int s_warp[kPlanThreads / 32];
   __shared__ int s_parent[kMaxTree];
   __shared__ uint32_t s_line[kMaxTree][kLineWords];
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const PrefillAr
       const Chunk c = load_tree(a, b, &flag);
       if (flag) raise_error(a.err, flag);
       // overlapping or repeated offsets cannot add blocks beyond the bound
-      n = static_cast<int>((static_cast<long long>(c.n) * a.G + kTreeRows - 1) / kTreeRows);
+      n = static_cast<int>((static_cast<long long>(c.n) * a.G + rows - 1) / rows);
     }
     int ex;
     const int total = block_scan(n, &ex, s_warp);
@@ -98,14 +99,16 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const PrefillAr
   __syncthreads();
   const int blocks = carry;
   carry = 0;
+  int wide = 0;
   for (int base = 0; base < blocks; base += kPlanThreads) {
     const int i = base + tid;
-    int n = 0;
+    int n = 0, nw = 0;
     if (i < blocks) {
       const int b = last_le(v.rbase, a.batch, i);
       const Chunk c = load_tree(a, b, &flag);
-      const RowBlock r = make_tree_block(c, b, a.window, a.G, i - v.rbase[b]);
+      const RowBlock r = make_tree_block(c, b, a.window, a.G, rows, i - v.rbase[b]);
       n = r.count;
+      nw = r.rows > kTreeRows ? n : 0;
       v.rb[3 * i] = make_int4(r.b, r.qlo, r.n, r.L);
       v.rb[3 * i + 1] = make_int4(r.pre, r.row0, r.rows, r.np);
       v.rb[3 * i + 2] = make_int4(r.skip, r.count, r.pA, r.pB);
@@ -114,10 +117,20 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const PrefillAr
     const int total = block_scan(n, &ex, s_warp);
     if (i < blocks) v.rb_pre[i] = carry + ex;
     carry += total;
+    const int more = block_scan(nw, &ex, s_warp);
+    if (i < blocks) v.rb_wide[i] = wide + ex;
+    wide += more;
   }
-  if (tid == 0) v.rb_pre[blocks] = carry;
+  if (tid == 0) {
+    v.rb_pre[blocks] = carry;
+    v.rb_wide[blocks] = wide;
+  }
   __syncthreads();
-  cut_ranges<kItemCost>(v, blocks, carry, a.hkv, ranges);
+  cut_ranges<kItemCost>(v, blocks, carry, a.hkv, ranges, [&](int i) {
+    return static_cast<long long>(kTileCost) * v.rb_pre[i] +
+           static_cast<long long>(kWideCost - kTileCost) * v.rb_wide[i] +
+           static_cast<long long>(kItemCost) * i;
+  });
 }
 
 size_t tree_layout(char* ws, int total_q, int batch, int G, int d, int ranges, PlanView* v,
@@ -134,6 +147,7 @@ size_t tree_layout(char* ws, int total_q, int batch, int G, int d, int ranges, P
   t.rbase = reinterpret_cast<int*>(take(sizeof(int) * (batch + 1)));
   t.rb = reinterpret_cast<int4*>(take(sizeof(int4) * 3 * nb));
   t.rb_pre = reinterpret_cast<int*>(take(sizeof(int) * (nb + 1)));
+  t.rb_wide = reinterpret_cast<int*>(take(sizeof(int) * (nb + 1)));
   t.start = reinterpret_cast<int*>(take(sizeof(int) * (ranges + 1)));
   t.item = reinterpret_cast<int*>(take(sizeof(int) * (ranges + 1)));
   t.ml = reinterpret_cast<float2*>(take(sizeof(float2) * 2 * ranges * kRows));
@@ -194,7 +208,8 @@ cudaError_t launch_tree(const PrefillArgs& args, const int32_t* parents, cudaStr
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(1u + static_cast<unsigned>(a.batch));
   cfg.blockDim = dim3(kPlanThreads);
-  if ((e = cudaLaunchKernelEx(&cfg, tree_plan_kernel, a, pv, parents, line, depth, ranges)) !=
+  if ((e = cudaLaunchKernelEx(&cfg, tree_plan_kernel, a, pv, parents, line, depth,
+                              raw ? kTreeRows : kRows, ranges)) !=
       cudaSuccess)
     return e;
   cfg.gridDim = dim3(static_cast<unsigned>(ranges));

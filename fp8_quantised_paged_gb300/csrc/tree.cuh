@@ -92,9 +92,9 @@ template <int D, bool RAW>
 struct TreeSmem {
   static constexpr int kHalf = 2 * kT * D;         // a 128-row f16 tile, or both terms of q
   static constexpr int kCodes = kT * D;            // a tile of codes
-  static constexpr int kQ = 0;                     // q; between items, sums of O
-  static constexpr int kV = kHalf;                 // two tiles of V in f16
-  static constexpr int kK = 3 * kHalf;             // K: tiles of codes, or of f16
+  static constexpr int kQ = 0;                     // q (RAW false: two tiles); between items, sums of O
+  static constexpr int kV = (RAW ? 1 : 2) * kHalf;  // two tiles of V in f16
+  static constexpr int kK = kV + 2 * kHalf;             // K: tiles of codes, or of f16
   static constexpr int kKTile = RAW ? kCodes : kHalf;
   // (an even number: a stage then serves one stream within an item)
   static constexpr int kKStages = RAW ? 4 : 2;
@@ -102,8 +102,8 @@ struct TreeSmem {
   static constexpr int kInfo = kVCodes + (RAW ? 2 * kCodes : 0);
   static constexpr int kMl = kInfo + static_cast<int>(kInfos * sizeof(TileInfo));
   static constexpr int kRow = kMl + 2 * 128 * 8;   // [lane] RowMask (kMl: [stream][lane] float2)
-  static constexpr int kExp = kRow + 128 * static_cast<int>(sizeof(RowMask));  // [lane] of q
-  static constexpr int kBars = kExp + 128 * 4;
+  static constexpr int kExp = kRow + 256 * static_cast<int>(sizeof(RowMask));  // [lane] of q
+  static constexpr int kBars = kExp + 256 * 4;
   static constexpr int kMisc = kBars + 320;        // TMEM base, abort flag
   static constexpr int kBytes = kMisc + 16;
 };
@@ -123,12 +123,13 @@ __device__ __forceinline__ int tree_bar_count(int i) {
          : i < kTVCFree ? 1
          : i < kTAll    ? 4
          : i < kTKFree  ? 8
+         : i < kTS      ? 2
                         : 1;
 }
 
 // The lanes of a share of a block's tokens.
 __device__ __forceinline__ int share_lanes(const RowBlock& r) {
-  return r.rows <= 32 ? 32 : (r.rows <= 64 ? 64 : 128);
+  return r.rows <= 32 ? 32 : (r.rows <= 64 ? 64 : (r.rows <= 128 ? 128 : 256));
 }
 
 // Byte of chunk c (16 bytes) of row r in a tile of D-byte rows, as TMA's swizzle over D
@@ -719,14 +720,20 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
                                  : tc_idesc(0, 0, 0, 0, 128, kT / 2);
     const uint32_t idesc_o = tc_idesc(0, 0, 0, 1, 128, D);  // A in TMEM, B MN-major
     const uint64_t dv0 = tc_desc(base + SM::kV, D * 16, 128, 0);
-    const uint64_t dq = RAW ? tc_desc(base + SM::kQ, 16, D * 8, D == 128 ? 2 : 4)
-                            : tc_desc(base + SM::kQ, 2048, 128, 0);
+    const uint64_t dq0 = RAW ? tc_desc(base + SM::kQ, 16, D * 8, D == 128 ? 2 : 4)
+                             : tc_desc(base + SM::kQ, 2048, 128, 0);
     const uint64_t dk0 = RAW ? tc_desc(base + SM::kK, 16, D * 8, D == 128 ? 2 : 4)
                              : tc_desc(base + SM::kK, 2048, 128, 0);
     const uint32_t ds0 = tm + t * kT, d_o = tm + 256 + t * 128;
     uint32_t g = 0, nq = 0, np = 0;  // tiles before the item; items; tiles of the stream
     bool ok = true;
+    int wide = 0;
+    auto free_stage = [&](int bar) {  // a stream that has the tile to itself speaks for both
+      tc_commit(bars + bar);
+      if (!wide) tc_commit(bars + bar);
+    };
     auto mma_s = [&](uint32_t st, int h) {
+      const uint64_t dq = dq0 + (wide ? t * (SM::kHalf >> 4) : 0);
       const uint64_t dk = dk0 + st * (SM::kKTile >> 4) + h * (RAW ? kT / 2 * D >> 4 : 1024 >> 4);
       const uint32_t ds = ds0 + h * (kT / 2);
       if (elect_one()) {
@@ -743,7 +750,7 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
             tc_mma_f16(ds, dq + k * (4096 >> 4), dk + k * (4096 >> 4), idesc_s, k > 0);
         }
         tc_commit(bars + kTS + t * 2 + h);
-        if (h == 1) tc_commit(bars + kTKFree + st);
+        if (h == 1) free_stage(kTKFree + st);
       }
       __syncwarp();
     };
@@ -756,7 +763,7 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           tc_mma_f16_ts(d_o, p + (k >> 1) * 32 + (k & 1) * 8, dv + k * (2 * D * 16 >> 4), idesc_o,
                         !(first && k == 0));
         tc_commit(bars + kTO + t * 2 + h);
-        if (h == 1) tc_commit(bars + kTVFree + st);
+        if (h == 1) free_stage(kTVFree + st);
       }
       __syncwarp();
     };
@@ -773,23 +780,25 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
       // own, as the stages are even in number)
       ok = wait_warp(kTQ, nq & 1);
       ++nq;
-      if (ok && t < n) {
-        ok = wait_s(g + t);
+      wide = __shfl_sync(0xffffffffu, !RAW && im.r.rows > 128, 0);
+      const int k0 = wide ? 0 : t, step = wide ? 1 : 2;
+      if (ok && k0 < n) {
+        ok = wait_s(g + k0);
         if (!ok) break;
         tc_fence_after();
-        mma_s((g + t) % SM::kKStages, 0);
-        mma_s((g + t) % SM::kKStages, 1);
+        mma_s((g + k0) % SM::kKStages, 0);
+        mma_s((g + k0) % SM::kKStages, 1);
       }
-      for (int k = t; k < n && ok; k += 2, ++np) {
-        const uint32_t gk = g + k, gn = gk + 2;
-        const bool more = k + 2 < n;
+      for (int k = k0; k < n && ok; k += step, ++np) {
+        const uint32_t gk = g + k, gn = gk + step;
+        const bool more = k + step < n;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           if (h == 0) ok = wait_warp(kTVFull + (gk & 1), (gk >> 1) & 1);
           ok = ok && wait_warp(kTP + t * 2 + h, np & 1);
           if (!ok) break;
           tc_fence_after();
-          mma_o(gk & 1, h, k == t && h == 0);
+          mma_o(gk & 1, h, k == k0 && h == 0);
           if (!more) continue;
           if (h == 0) ok = wait_s(gn);
           ok = ok && wait_warp(kTO + t * 2 + h, np & 1);
@@ -834,7 +843,6 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + t * kT + lanes, to = tmem + 256 + t * 128 + lanes;
     float2* ml = reinterpret_cast<float2*>(sm + SM::kMl);
-    RowMask* const row = reinterpret_cast<RowMask*>(sm + SM::kRow) + rl;
     int* exps = reinterpret_cast<int*>(sm + SM::kExp);
     const bool cap_quick = a.cap <= kCapFast;
     constexpr int kTop = RAW ? 8 : 14;  // exponent of a normalised row of q
@@ -853,7 +861,12 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
       const int n = im.t1 - im.t0;
       u += n;
       const int sl = share_lanes(im.r);
-      const int mine = (n + 1 - t) >> 1;  // tiles of this stream
+      // rows of two tiles of lanes: each stream has its own, and every token tile
+      const bool wide = !RAW && sl == 256;
+      const int mine = wide ? n : (n + 1 - t) >> 1;  // tiles of this stream
+      const uint32_t g0 = wide ? g : g + t, step = wide ? 1 : 2;
+      const int bl = wide ? t * 128 + rl : rl;  // lane of the block
+      RowMask* const row = reinterpret_cast<RowMask*>(sm + SM::kRow) + bl;
       // query and head of a lane's row (lanes past the block's end: its last row)
       auto query_of = [&](int l, int& qi, int& h) {
         const int rr = im.r.row0 + min(l & (sl - 1), im.r.rows - 1);
@@ -867,12 +880,12 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
         const bool st = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
         const float* kc = a.k_scale + static_cast<long>(im.kvh) * D;
         const int r8 = lane & 7, c4 = lane >> 3;
-        uint8_t* dst = sm + SM::kQ;
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int to_row = warp * 16 + y * 8 + r8;
+#pragma unroll 1
+        for (int y = 0; y < (wide ? 4 : 2); ++y) {
+          const int of_block = (warp * (wide ? 4 : 2) + y) * 8 + r8, to_row = of_block & 127;
+          uint8_t* dst = sm + SM::kQ + (of_block >> 7) * SM::kHalf;
           int qy, hy;
-          query_of(to_row, qy, hy);
+          query_of(of_block, qy, hy);
           const uint4* src = reinterpret_cast<const uint4*>(
                                  a.q + ((static_cast<long>(im.r.qlo) + qy) * a.hq + hy) * D) + c4;
           uint4 raw[D / 32];
@@ -901,7 +914,7 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
           // (129 for an infinity: such a row is NaN)
           const int eq = amax > 0.f ? exp_above(amax) : 0;
-          if (c4 == 0) exps[to_row] = eq;
+          if (c4 == 0) exps[of_block] = eq;
           const float fq = exp2i(kTop - eq);
 #pragma unroll
           for (int x = 0; x < D / 32; ++x) {
@@ -930,10 +943,10 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
         }
       }
       int qi, h;
-      query_of(rl, qi, h);
+      query_of(bl, qi, h);
       const int qrow = im.r.qlo + qi;
       const int depth = __ldg(tv.depth + qrow);
-      if (t == 0) *row = RowMask{window_first(a.window, im.r.pA + depth), qrow};
+      if (wide || t == 0) *row = RowMask{window_first(a.window, im.r.pA + depth), qrow};
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + kTQ);
@@ -943,7 +956,7 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
       const float b0 = (cap_quick ? cap_log2 : 0.f) - slope * static_cast<float>(depth);
       // the thread's groups of 32 tokens
       const int part = rl / sl;
-      const uint32_t groups = sl == 128 ? 0xFu : (sl == 64 ? 5u << part : 1u << part);
+      const uint32_t groups = sl >= 128 ? 0xFu : (sl == 64 ? 5u << part : 1u << part);
       float ref = kNegBig, l = 0.f, zs = 0.f;
       // makes the row NaN where it saw codes of tile gt that are not finite
       auto late_nan = [&](uint32_t gt) {
@@ -956,7 +969,7 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
       uint4 sc[8];      // and their scales, loaded beside them
       for (int x = 0; x < 2 * mine; ++x) {  // halves of the stream's tiles
         const int half = x & 1;
-        const uint32_t gt = g + t + (x & ~1);
+        const uint32_t gt = g0 + (x >> 1) * step;
         // (S is issued once the tile's info is complete)
         if (!wait_warp(kTS + t * 2 + half, ns & 1)) {
           ok = false;
@@ -965,12 +978,12 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
         tc_fence_after();
         if (x == 0) {
           // log2-domain factor of a raw score (capped scores: see cap_in)
-          const int er = exps[rl];
+          const int er = exps[bl];
           zs = fabsf(a.sm_scale) * exp2i(er - kTop) * (VAR == 2 ? a.cap_in : kLog2e);
           if (VAR == 0) zs = fmaxf(zs, 1e-37f);  // (it multiplies a masked -inf: not zero)
           if (er > 128) zs = __int_as_float(0x7FC00000);
         } else if (half == 0) {
-          late_nan(gt - 2);  // (what the tile before brought that is not finite is known by now)
+          late_nan(gt - step);  // (what the tile before brought that is not finite is known by now)
         }
         const TileInfo& info = infos[gt % kInfos];
         auto load = [&](int w, const float* scale) {
@@ -1111,7 +1124,7 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           break;
         }
         tc_fence_after();
-        late_nan(g + t + 2 * (mine - 1));
+        late_nan(g0 + step * (mine - 1));
       }
       g += n;
 
@@ -1121,17 +1134,17 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
       const bool stat = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
       const float* vch = a.v_scale + static_cast<long>(im.kvh) * D;
       const long slot = (static_cast<long>(blockIdx.x) * 2 + (im.t0 > 0 ? 0 : 1)) * kRows;
-      const int partials = n > 1 ? 256 : 128;  // lanes of the streams that had a tile
+      const int partials = n > 1 || wide ? 256 : 128;  // lanes of the streams that had a tile
       ml[t * 128 + rl] = make_float2(ref, l);
       if (!sync_all()) {
         ok = false;
         break;
       }
       float M = kNegBig, sum = 0.f;
-      for (int x = rl & (sl - 1); x < 256; x += sl) M = fmaxf(M, ml[x].x);
-      for (int x = rl & (sl - 1); x < 256; x += sl) sum += ml[x].y * ex2(ml[x].x - M);
+      for (int x = bl & (sl - 1); x < 256; x += sl) M = fmaxf(M, ml[x].x);
+      for (int x = bl & (sl - 1); x < 256; x += sl) sum += ml[x].y * ex2(ml[x].x - M);
       const float scale = ex2(ref - M) * (piece ? 1.f : (sum == 0.f ? 0.f : 1.f / sum));
-      if (piece && t == 0 && rl < im.r.rows && rl < sl) pv.ml[slot + rl] = make_float2(M, sum);
+      if (piece && (wide || t == 0) && bl < im.r.rows && bl < sl) pv.ml[slot + bl] = make_float2(M, sum);
       // a quarter of the dims at a time: every lane leaves its part, in q's place, then all
       // threads add them up, four dims of a row each.  Chunk c (4 dims) of lane y's part,
       // free of bank conflicts:
