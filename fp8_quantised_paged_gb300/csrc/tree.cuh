@@ -6,10 +6,10 @@
 //   the prefix leave them) and the nodes on i's line, itself among them
 //
 // Rows and work.  The (node, head) pairs of a request and KV head are rows, a TMEM lane
-// each, in blocks of 128; (row block, KV head, 128-token tile) units are cut into one range
-// per SM, and cut items leave pieces, as in the prefill (ranges.cuh, prefill.cu).  A tree
-// has few rows over a long context, so the cache's bytes bound it, and three things keep
-// the tensor cores and the softmax out of their way:
+// each, in blocks of 128 (RAW false: 256); (row block, KV head, 128-token tile) units are cut
+// into one range per SM, and cut items leave pieces, as in the prefill (ranges.cuh,
+// prefill.cu).  A tree has few rows over a long context, so the cache's bytes bound it, and
+// three things keep the tensor cores and the softmax out of their way:
 //  - A block runs as two streams, one on the even tiles and one on the odd ones, with
 //    scores, weights, sums and O of their own.
 //  - A stream takes a tile by halves: while its softmax is at one half, the tensor cores
@@ -17,7 +17,20 @@
 //  - A block of at most 64 (or 32) rows stands twice (four times) in the lanes: each of the
 //    copies weighs its share of a tile's tokens, with zeros for the others'.  The products
 //    are the same, the softmax is half (a quarter).
-// The partial results (2 to 8 a row) are added up at the block's end.
+// The partial results (2 to 8 a row) are added up at the block's end.  A block of more than
+// 128 rows gives each stream 128 of its own, and every tile: what is converted serves twice
+// the rows (64 nodes x 4 heads of 8 x 32K tokens, MX: 559 us, in blocks of 128 rows 788).
+// FP8 codes gain less by it, since K needs no converting and the second q takes the place of
+// two of the four K tiles (12 x 16K, 64 nodes: 448 us against 498; a ragged batch of 64, 64
+// nodes: 278 against 254; one request of 16K: 88 against 76), and keep to 128 rows.
+//
+// Measured (layer of 64 query and 8 KV heads of 128 dims, E4M3, a scale per token): 12 x 16K
+// tokens and 16 nodes 150-152 us a call, 2.8 TB/s of the cache; one request of 700 tokens
+// 28 us, of which two thirds are the three launches and their gaps.  What bounds it is
+// neither DRAM (35 % of its cycles at 12 x 16K) nor the tensor pipe (26 %) but the chain of a
+// stream, softmax -> P V -> S, at half of the issue slots: 3500 cycles for a tile on an SM.
+// A suspend hint in the waits, scores held in registers between the passes (196-204 us, for
+// spills) and two threads a lane (195 us) were no faster.
 //
 // Products.  S = Q K^T on FP8 tensor cores: the K codes as TMA lands them, q as two E4M3
 // terms hi + lo (exact for bf16 but for elements 2^-9 below the row's largest), the token's
@@ -32,8 +45,10 @@
 //
 // Roles: warps 0-3 and 4-7 the softmax of streams 0 and 1, a thread a lane; four warps
 // that convert V (RAW false: and four for K), one that issues MMAs for each stream, and
-// (RAW) one that copies K's pages by TMA and lays out their scales, and one for V's.  Every
-// wait is bounded.
+// (RAW) one that copies K's pages by TMA and lays out their scales, and one for V's.  RAW
+// has 512 threads of 128 registers and no spills; 576 of 96 spill some in the softmax, but
+// six converting warps of 128 registers, 32-token jobs dealt among them, took 1735 us where
+// eight took 788.  Every wait is bounded.
 #pragma once
 
 #include "prefill.cuh"
@@ -87,7 +102,6 @@ struct RowMask {
   int wf, node;
 };
 
-
 template <int D, bool RAW>
 struct TreeSmem {
   static constexpr int kHalf = 2 * kT * D;         // a 128-row f16 tile, or both terms of q
@@ -110,8 +124,9 @@ struct TreeSmem {
 // Barriers and the arrivals that complete a phase: Q the eight softmax warps; P (stream * 2
 // + half) the stream's four; Info the copying warps (RAW) or the converting ones; K full
 // one thread and its bytes (RAW) or four warps; V codes full a thread and its bytes, free
-// the four converting warps; V full four warps; All the eight softmax warps; K and V free, S
-// and O (stream * 2 + half) and Drain (by stream) a commit of the tensor cores.
+// the four converting warps; V full four warps; All the eight softmax warps; K and V free two
+// commits of the tensor cores, one for each stream; S and O (stream * 2 + half) and Drain (by
+// stream) one.
 enum { kTQ = 0, kTP = 1, kTInfo = 5, kTKFull = 13, kTVCFull = 17, kTVCFree = 19, kTVFull = 21,
        kTAll = 23, kTKFree = 24, kTVFree = 28, kTS = 30, kTO = 34, kTDrain = 38, kTreeBars = 40 };
 template <bool RAW>
@@ -127,7 +142,7 @@ __device__ __forceinline__ int tree_bar_count(int i) {
                         : 1;
 }
 
-// The lanes of a share of a block's tokens.
+// The lanes of a share of a block's tokens (256: of both streams).
 __device__ __forceinline__ int share_lanes(const RowBlock& r) {
   return r.rows <= 32 ? 32 : (r.rows <= 64 ? 64 : (r.rows <= 128 ? 128 : 256));
 }
@@ -875,7 +890,7 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
       };
       {
         // ---- the rows of q, each normalised by a power of two, into shared memory (every S
-        // of the item before was read), 16 lanes' a warp; 8 rows x 64 bytes a load
+        // of the item before was read), 8 rows x 64 bytes of a warp a load
         const float sgn = a.sm_scale < 0.f ? -1.f : 1.f;
         const bool st = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
         const float* kc = a.k_scale + static_cast<long>(im.kvh) * D;
