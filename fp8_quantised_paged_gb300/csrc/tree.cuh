@@ -19,7 +19,8 @@
 //    are the same, the softmax is half (a quarter).
 // The partial results (2 to 8 a row) are added up at the block's end.  A block of more than
 // 128 rows gives each stream 128 of its own, and every tile: what is converted serves twice
-// the rows (64 nodes x 4 heads of 8 x 32K tokens, MX: 559 us, in blocks of 128 rows 788).
+// the rows (64 nodes x 4 heads of 8 x 32K tokens, MX: 542 us; 559 where blocks of 128
+// rows took 788).
 // FP8 codes gain less by it, since K needs no converting and the second q takes the place of
 // two of the four K tiles (12 x 16K, 64 nodes: 448 us against 498; a ragged batch of 64, 64
 // nodes: 278 against 254; one request of 16K: 88 against 76), and keep to 128 rows.
@@ -91,7 +92,7 @@ constexpr int kTreeThreads = (kTreeIssue<RAW> + (RAW ? 4 : 2)) * 32;
 // and what masks it.
 struct TileInfo {
   float ks[kT], vs[kT], pos[kT];
-  int ev[4];
+  float ev[4];
   uint32_t valid[4], bad[4], held[4], cbad[4], seen[4];
   int j0, ctx, pre;
   uint32_t whole;
@@ -320,7 +321,7 @@ __device__ __forceinline__ void copy_tiles(const PrefillArgs& a, const PlanView&
         uint32_t bad = 0;
         if (__any_sync(0xffffffffu, (now.ok & ~fin) != 0)) bad = group_bits(now.ok & ~fin, lane);
         if (lead) {
-          info->ev[grp] = e;
+          info->ev[grp] = static_cast<float>(e);
           info->bad[grp] = bad;
         }
       } else {
@@ -395,7 +396,7 @@ __device__ __forceinline__ void put_v_info(TileInfo* info, int dw, int lane, flo
   info->vs[dw * 32 + lane] = ok && finite ? scale * exp2i(-e) : 0.f;
   bad |= __ballot_sync(0xffffffffu, ok && !finite);
   if (lane == 0) {
-    info->ev[dw] = e;
+    info->ev[dw] = static_cast<float>(e);
     info->bad[dw] = bad;
   }
 }
@@ -1010,11 +1011,18 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           tmem_landed(ra);
         };
         // ---- a bound of z + e over the row's tokens; the scores go back to TMEM
+        const int w0 = half * 2;
+        const float2 ev = *reinterpret_cast<const float2*>(info.ev + w0);
+        const uint2 seen = *reinterpret_cast<const uint2*>(info.seen + w0);
+        const uint2 bads = *reinterpret_cast<const uint2*>(info.bad + w0);
         float bound = __int_as_float(0xff800000);
-#pragma unroll 1
-        for (int w = half * 2; w < half * 2 + 2; ++w) {
+        // (both groups laid out: MX, 64 nodes of 8 x 32K 542 us, in a loop 565; FP8 codes, the
+        // ragged 64 209 us, in a loop 197)
+#pragma unroll (RAW ? 1 : 2)
+        for (int y = 0; y < 2; ++y) {
+          const int w = w0 + y;
           if (((groups >> w) & 1u) == 0) continue;
-          const uint32_t whole = info.seen[w], bad = info.bad[w];
+          const uint32_t whole = y ? seen.y : seen.x, bad = y ? bads.y : bads.x;
           load(w, info.ks);
           const uint64_t zs2 = f2_pack(zs, zs), sl2 = f2_pack(slope, slope);
           const uint64_t b02 = f2_pack(b0, b0);
@@ -1059,13 +1067,13 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           }
           float m4[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) m4[y] = __int_as_float(0xff800000);
+          for (int i = 0; i < 4; ++i) m4[i] = __int_as_float(0xff800000);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             m4[i & 3] = max3(m4[i & 3], __uint_as_float(ra[2 * i]), __uint_as_float(ra[2 * i + 1]));
           tmem_st32(ts + w * 32, ra);
           const float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-          bound = fmaxf(bound, fmaf(mx, VAR > 0 ? 1.f : zs, static_cast<float>(info.ev[w])));
+          bound = fmaxf(bound, fmaf(mx, VAR > 0 ? 1.f : zs, y ? ev.y : ev.x));
         }
         tmem_st_wait();
         // ---- the reference: where the bound passed it by 2^kTau it moves, and with it the
@@ -1096,7 +1104,8 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
         }
         // ---- P times V's scale, and the sum of P; zeros for the other shares' tokens
 #pragma unroll 1
-        for (int w = half * 2; w < half * 2 + 2; ++w) {
+        for (int y = 0; y < 2; ++y) {
+          const int w = w0 + y;
           uint32_t pw[16];
           if (((groups >> w) & 1u) == 0) {
 #pragma unroll
@@ -1104,7 +1113,7 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
             tmem_st16(ts + w * 32, pw);
             continue;
           }
-          const float e = static_cast<float>(info.ev[w]);
+          const float e = y ? ev.y : ev.x;
           load(w, info.vs);
           const float c0 = kShift - ref + e, f = VAR > 0 ? 1.f : zs;
           const uint64_t f2 = f2_pack(f, f), c02 = f2_pack(c0, c0);
@@ -1122,9 +1131,9 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
             pw[i] = pack_half2(p, q);
           }
           tmem_st16(ts + w * 32, pw);
-          float y, z;
-          f2_unpack(f2_add(la, lb), y, z);
-          l = fmaf(y + z, ex2(-e), l);
+          float sa, sb;
+          f2_unpack(f2_add(la, lb), sa, sb);
+          l = fmaf(sa + sb, ex2(-e), l);
         }
         tmem_st_wait();
         tc_fence_before();
