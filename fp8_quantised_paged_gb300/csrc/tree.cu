@@ -8,10 +8,11 @@ namespace fp8pa {
 namespace {
 
 // What a tile costs, of a block of at most 128 rows and of a larger one, and what an item
-// costs beside its tiles: 1.4 and 11 tiles, as measured.  (12 x 16K tokens, and 64 requests of
-// 1K to 32K, with items at no cost 154 and 635 us; at 3 tiles 153 and 339, 8: 151 and 214, 11:
-// 152 and 203, 14: 153 and 212, 24: 163 and 255.)
-constexpr int kTileCost = 5, kWideCost = 7, kItemCost = 55;
+// costs beside its tiles: 1.4 and 8.4 tiles, as measured.  (12 x 16K tokens, and 64 requests of
+// 1K to 32K, with items at no cost 154 and 635 us, before sums were faster; now at 6 tiles 146
+// and 221, 7.2: 146 and 208, 8.4: 146 and 204, 9.6: 148 and 205, 11: 148 and 210, 12.4: 150
+// and 209, beside a slower start of items.)
+constexpr int kTileCost = 5, kWideCost = 7, kItemCost = 42;
 
 // A request's tree and its visible extent; n is 0 for a request that is skipped, `flag`
 // why.

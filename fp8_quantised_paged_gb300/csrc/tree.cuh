@@ -19,17 +19,20 @@
 //    are the same, the softmax is half (a quarter).
 // The partial results (2 to 8 a row) are added up at the block's end.  A block of more than
 // 128 rows gives each stream 128 of its own, and every tile: what is converted serves twice
-// the rows (64 nodes x 4 heads of 8 x 32K tokens, MX: 542 us; 559 where blocks of 128
+// the rows (64 nodes x 4 heads of 8 x 32K tokens, MX: 544 us; 559 where blocks of 128
 // rows took 788).
 // FP8 codes gain less by it, since K needs no converting and the second q takes the place of
 // two of the four K tiles (12 x 16K, 64 nodes: 448 us against 498; a ragged batch of 64, 64
 // nodes: 278 against 254; one request of 16K: 88 against 76), and keep to 128 rows.
 //
 // Measured (layer of 64 query and 8 KV heads of 128 dims, E4M3, a scale per token): 12 x 16K
-// tokens and 16 nodes 150-152 us a call, 2.8 TB/s of the cache; one request of 700 tokens
-// 28 us, of which two thirds are the three launches and their gaps.  What bounds it is
-// neither DRAM (35 % of its cycles at 12 x 16K) nor the tensor pipe (26 %) but the chain of a
-// stream, softmax -> P V -> S, at half of the issue slots: 3500 cycles for a tile on an SM.
+// tokens and 16 nodes 146 us a call, 2.9 TB/s of the cache; one request of 700 tokens 28-31 us,
+// which is the host's time (17.6 on the device, three dependent launches).  What bounds it is
+// neither DRAM (35 % of its cycles at 12 x 16K) nor the tensor pipe (26 %) but the softmax, at
+// half of the issue slots: its warps find S ready, and take 2650 cycles for half a tile (190
+// for a wait that is over, 1100 for the bound, 110 for the reference, 950 for P), so that an
+// SM takes that for a tile of one of its two streams.  An item beside its tiles costs 17000
+// cycles: 5000 until q stands in shared memory, 2000 until the first P, 8000 for the sums.
 // A suspend hint in the waits, scores held in registers between the passes (196-204 us, for
 // spills) and two threads a lane (195 us) were no faster.
 //
@@ -896,6 +899,8 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
         const bool st = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
         const float* kc = a.k_scale + static_cast<long>(im.kvh) * D;
         const int r8 = lane & 7, c4 = lane >> 3;
+        // (a turn at a time: rows asked for a turn ahead, or two turns laid out, were slower, 203
+        // and 200 us against 197 for the ragged 64)
 #pragma unroll 1
         for (int y = 0; y < (wide ? 4 : 2); ++y) {
           const int of_block = (warp * (wide ? 4 : 2) + y) * 8 + r8, to_row = of_block & 127;
@@ -1165,8 +1170,17 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
         break;
       }
       float M = kNegBig, sum = 0.f;
-      for (int x = bl & (sl - 1); x < 256; x += sl) M = fmaxf(M, ml[x].x);
-      for (int x = bl & (sl - 1); x < 256; x += sl) sum += ml[x].y * ex2(ml[x].x - M);
+      {
+        float2 part[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          part[k] = k * sl < 256 ? ml[(bl & (sl - 1)) + k * sl] : make_float2(kNegBig, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) M = fmaxf(M, part[k].x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k * sl < 256) sum += part[k].y * ex2(part[k].x - M);
+      }
       const float scale = ex2(ref - M) * (piece ? 1.f : (sum == 0.f ? 0.f : 1.f / sum));
       if (piece && (wide || t == 0) && bl < im.r.rows && bl < sl) pv.ml[slot + bl] = make_float2(M, sum);
       // a quarter of the dims at a time: every lane leaves its part, in q's place, then all
@@ -1179,11 +1193,15 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
       };
 #pragma unroll 1
       for (int dq = 0; dq < 4 && ok; ++dq) {
+        // a thread adds up chunk c of lanes r, r + 32, ...: all are asked for at once
+        const int c = tid % kChunks, r = tid / kChunks, d0 = dq * (D / 4) + c * 4;
+        float4 ch = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (stat) ch = __ldg(reinterpret_cast<const float4*>(vch + d0));
         if (t * 128 < partials) {
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
+          for (int x = 0; x < D / 64; ++x) {
             uint32_t o[16];
-            tmem_ld16(to + dq * (D / 4) + c * 16, o);
+            tmem_ld16(to + dq * (D / 4) + x * 16, o);
             tmem_ld_wait();
             tmem_landed(o);
             float f[16];
@@ -1191,7 +1209,7 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
             for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(o[i]) * scale;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              *at(t * 128 + rl, c * 4 + i) =
+              *at(t * 128 + rl, x * 4 + i) =
                   make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
           }
         }
@@ -1199,37 +1217,50 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           ok = false;
           break;
         }
-        for (int i = tid; i < im.r.rows * kChunks; i += 256) {
-          const int r = i / kChunks, c = i % kChunks, d0 = dq * (D / 4) + c * 4;
-          float4 v = *at(r, c);
-          for (int y = r + sl; y < partials; y += sl) {
-            const float4 x = *at(y, c);
-            v.x += x.x;
-            v.y += x.y;
-            v.z += x.z;
-            v.w += x.w;
+        if (r < 32 && r < im.r.rows) {
+          float4 v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            v[k] = k * 32 < partials ? *at(r + k * 32, c) : make_float4(0.f, 0.f, 0.f, 0.f);
+          auto fold = [&](int k, int from) {
+            v[k].x += v[from].x;
+            v[k].y += v[from].y;
+            v[k].z += v[from].z;
+            v[k].w += v[from].w;
+          };
+          if (sl <= 128) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) fold(k, k + 4);
           }
-          if (stat) {
-            const float4 x = __ldg(reinterpret_cast<const float4*>(vch + d0));
-            v.x *= x.x;
-            v.y *= x.y;
-            v.z *= x.z;
-            v.w *= x.w;
+          if (sl <= 64) {
+            fold(0, 2);
+            fold(1, 3);
           }
-          if (piece) {
-            *reinterpret_cast<float4*>(pv.o + (slot + r) * D + d0) = v;
-            continue;
-          }
-          int qy, hy;
-          query_of(r, qy, hy);
-          const long to_row = ((static_cast<long>(im.r.qlo) + qy) * a.hq + hy) * D + d0;
-          if (a.out_f32) {
-            *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + to_row) = v;
-          } else {
-            const __nv_bfloat162 b[2] = {__floats2bfloat162_rn(v.x, v.y),
-                                         __floats2bfloat162_rn(v.z, v.w)};
-            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + to_row) =
-                *reinterpret_cast<const uint2*>(b);
+          if (sl <= 32) fold(0, 1);
+#pragma unroll
+          for (int k = 0; k < (RAW ? 4 : 8); ++k) {
+            const int row = r + k * 32;
+            if (k * 32 >= sl || row >= im.r.rows) continue;
+            float4 o = v[k];
+            o.x *= ch.x;
+            o.y *= ch.y;
+            o.z *= ch.z;
+            o.w *= ch.w;
+            if (piece) {
+              *reinterpret_cast<float4*>(pv.o + (slot + row) * D + d0) = o;
+              continue;
+            }
+            int qy, hy;
+            query_of(row, qy, hy);
+            const long to_row = ((static_cast<long>(im.r.qlo) + qy) * a.hq + hy) * D + d0;
+            if (a.out_f32) {
+              *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + to_row) = o;
+            } else {
+              const __nv_bfloat162 b[2] = {__floats2bfloat162_rn(o.x, o.y),
+                                           __floats2bfloat162_rn(o.z, o.w)};
+              *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + to_row) =
+                  *reinterpret_cast<const uint2*>(b);
+            }
           }
         }
         if (!sync_all()) ok = false;  // (also: the next item's q goes there)
