@@ -768,8 +768,9 @@ def kv_keep_accepted(accepted, q_offsets, block_tables, seq_lens, pages, new_len
     """After a drafted tree's verification: move the accepted path's cached rows to the
     front of the tree's tokens.  accepted: int32 [B, max_accepted], the path's node
     numbers, then -1; request b's tree is its last q_offsets[b+1] - q_offsets[b] tokens.
-    pages: a KvPages of per-token arrays.  Returns the new lengths (int32 [B]); the
-    pages behind them stay the rows' until kv_resize."""
+    pages: a KvPages of per-token arrays; a row with a tree is not forked before this call.
+    Returns the new lengths (int32 [B]); the pages behind them stay the rows' until
+    kv_resize."""
     dev, B, max_blocks = _check_pages(pages, block_tables, seq_lens, None)
     if not pages.per_token:
         raise ValueError("kv_keep_accepted needs arrays of rows per token and head")

@@ -591,7 +591,8 @@ size_t fp8pa_pages_workspace_bytes(int rows, int num_blocks);
  *            before a node that is not (FP8PA_DEVERR_TREE).
  * pages      arrays of rows per token: a page is [n_kv_heads][block_size] rows (page_bytes
  *            a multiple of that).  Not the scales of FP8PA_SCALE_SEGMENT, nor codes
- *            under them: a row's scale is its page's.
+ *            under them: a row's scale is its page's.  Pages that hold tokens of a tree
+ *            are its row's alone: a row is forked before its draft or after this call.
  * new_lens   i32 [batch], not overlapping seq_lens.  A request with bad offsets
  *            (FP8PA_DEVERR_Q_OFFSETS) or a tree longer than it is is left as it was.
  * The pages behind the new length stay the row's: fp8pa_kv_resize gives them back.

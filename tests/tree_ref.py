@@ -17,13 +17,15 @@ With static channel scales q times the scales (rounded to fp32) has no such step
 what hi leaves, at most 2^(e - 4), by 2^-5 of that (half a step of E4M3 in the binade
 below): 2^-9 of each element more, 2^-9 Z.  Codes that no E4M3 or E5M2 product takes (INT8,
 MX blocks) meet q as f16, 2^-11 Z (it is exact for all but elements 2^-17 below the
-largest, as there), and their K^ is exact in f16 but for factors 2^-21 below the token's
-largest block (2^-25 of that).
+largest, as there), and their K^ is exact in f16 but for small factors (see W).
 r: 2^-19 as there, and 2^-11 for the softmax weights, which enter the second product as f16
 times V's scale.
 W: a weight times V's scale, relative to the largest scale of its group of 32 tokens, is
-below f16's normal range off by 2^-25: 2^-36 vs_max sum_j |code_j| as there; V^ of MX blocks
-is a code times a factor relative to the token's largest block, off by 2^-25 2^-6 of it.
+below f16's normal range off by 2^-25: 2^-36 vs_max sum_j |code_j| as there.  V^ of MX blocks
+is a code times its block's factor relative to the token's largest, and K^ likewise.  An
+E4M3 code (at most 448 < 2^9) leaves f16 (2^16) seven exponents, by which the factor is raised:
+half of f16's smallest step, 2^-25, is then 2^-32 of the largest factor, and 2^-31 is allowed.
+An E5M2 code (at most 57344) leaves none: half a step is 2^-25 of it.
 """
 import numpy as np
 import torch
@@ -49,6 +51,7 @@ def tree_ref(q, offsets, parents, lens, bt, values, hkv, sm, bs, fmt, mode, wind
     g = hq // hkv
     q = q.double().to(device)
     f16_k = fmt == 2 or mode == MX
+    mx_step = 2.0 ** -25 if fmt == 1 else 2.0 ** -31
     out = torch.zeros(n, hq, d, dtype=torch.float64, device=device)
     A, Z, Bm = torch.zeros_like(out), torch.zeros_like(out[..., :1]), torch.zeros_like(out[..., :1])
     W, Fl = torch.zeros_like(out), torch.zeros_like(Z)
@@ -95,7 +98,7 @@ def tree_ref(q, offsets, parents, lens, bt, values, hkv, sm, bs, fmt, mode, wind
             codes = torch.where(torch.isfinite(vcd[h // g]), vcd[h // g], 0.0).abs()
             W[lo:hi, h] = top * 2.0 ** -36 * (see.double() @ codes)
             if mode == MX:
-                W[lo:hi, h] += top * 2.0 ** -31
+                W[lo:hi, h] += top * mx_step
             if mode == STATIC:
                 ks = kchan.double().to(device)[h // g]
                 codes = torch.where(ks > 0, kk / ks, 0.0).abs().sum(1)
@@ -104,7 +107,7 @@ def tree_ref(q, offsets, parents, lens, bt, values, hkv, sm, bs, fmt, mode, wind
             elif f16_k:
                 Fl[lo:hi, h, 0] = 2.0 ** -11 * Z[lo:hi, h, 0]
                 if mode == MX:
-                    Fl[lo:hi, h, 0] += abs(sm) * q[lo:hi, h].abs().sum(1) * 2.0 ** -31 * float(
+                    Fl[lo:hi, h, 0] += abs(sm) * q[lo:hi, h].abs().sum(1) * mx_step * float(
                         ksc[h // g][some].max())
             else:
                 Fl[lo:hi, h, 0] = abs(sm) * 2.0 ** -17 * q[lo:hi, h].abs().amax(1) * float(
