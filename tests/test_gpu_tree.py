@@ -362,3 +362,17 @@ def test_a_larger_batchs_workspace_serves_a_smaller_one(F):
     ws = torch.empty(F.tree_workspace_bytes(500, 40, 16, 2, 128, 16, 9999), dtype=torch.uint8, device=DEV)
     ws.random_(0, 256)
     assert torch.equal(c.run(F, workspace=ws), want)
+
+
+@pytest.mark.parametrize("fmt,mode,d", [(INT8, TOKEN_HEAD, 128), (E4M3, MX, 64), (E5M2, STATIC, 128)])
+def test_row_blocks_of_every_kind_in_one_range(F, fmt, mode, d):
+    """Shared lanes, blocks of up to 128 and of 256 rows behind one another on an SM, and the
+    same call again."""
+    rng = np.random.default_rng(23)
+    nodes = [int(n) for n in rng.choice([0, 1, 4, 9, 16, 17, 32, 33, 64, 100], 60)]
+    ctx = [int(c) for c in rng.integers(0, 900, 60)]
+    c = Case(23, ctx, nodes, 32, 4, d, 16, fmt, mode)
+    c.check(F)
+    want = c.run(F)
+    for _ in range(10):
+        assert torch.equal(c.run(F), want)
