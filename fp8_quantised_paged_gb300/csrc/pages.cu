@@ -5,6 +5,12 @@
 // taken first, in the order of the rows, so that the result is the same whatever order
 // the threads come in.  Counts are added to and taken from by atomics on integers,
 // whose order does not show.
+//
+// Device times of the calls, in a captured graph (a plain call is bound by its host side, 13
+// to 23 us): keep 2.3 us for one request's layer, 13.0 for 64 requests of 16 layers; fork 7.5
+// for one row to 4, 20.4 for 16 rows to 128 in 16 layers; resize 8.9 for 256 rows, 22.4 for
+// 1024 rows of which many end or begin; compact 11.8 for 2K pages, 196 for 16K pages of 4
+// layers, half of them free.
 #include "pages.cuh"
 
 #include "common.cuh"
@@ -104,6 +110,8 @@ __device__ __forceinline__ void copy_chunk(const PageArrays& a, uint32_t c, int 
   }
 }
 
+// Bound by HBM where pages are many: 1.1 GB read and written at 5.7 TB/s, 85 % of the rate of
+// a plain copy (16K pages of 4 layers, half of them moved).
 // Every pair's chunks, dealt over the warps of the grid: pair(k, &from, &to) says
 // whether pair k < pairs is copied, and from where to where.
 template <class Pair>
@@ -126,7 +134,8 @@ __device__ __forceinline__ void copy_pairs(const PageArrays& a, int pairs, Pair 
 // The rows of the kept nodes move to the front of the tree's tokens: node a[t] to
 // place t.  A path's nodes rise and a[t] >= t, so a move never writes a row that a
 // later move reads; a warp takes one (request, array, KV head) and its moves in order,
-// up to four rows' units a lane, all read before any is written.
+// up to four rows' units a lane, all read before any is written.  Bound by latency: a table
+// entry, a row, a write, for a few rows of 128 bytes a warp.
 template <class T>
 __device__ __forceinline__ void keep_rows(const PageRows& r, const int32_t* acc, int count,
                                           int ctx, const int32_t* table, uint8_t* base, int hkv,
@@ -225,7 +234,9 @@ __global__ void __launch_bounds__(kCopyThreads) keep_kernel(const int32_t* accep
 // Workspace: claim[rows] the first fork that wants a row; by fork, page[rows] the page
 // that its last, partly filled page is copied to, kWhole where there is none, kSkip
 // where the fork is not made, and size[rows] the length that it takes over (a source may
-// be another fork's row: all see the rows as they were); then the free pages.
+// be another fork's row: all see the rows as they were); then the free pages.  One CTA
+// plans, bound by the round trips of the counts and of the rows' lengths; the copies of the
+// last pages are bound by HBM (16 rows to 128: 20.4 us in all, 138 MB).
 constexpr int kSkip = -2, kWhole = -1;
 
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const int32_t* src,
@@ -321,7 +332,8 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const int32_t* src, 
 // Workspace: the rows' new page counts (kSkip: the row is left), the prefix of the
 // pages that rows grow by, then the free pages.  All rows are looked at before any
 // page is given back, so that what a row may do does not depend on its neighbours'
-// order.
+// order.  Three launches, as each has to see all of the one before; the last is one CTA,
+// which gives out the free pages in order and is bound by its round trips.
 __global__ void __launch_bounds__(256) resize_check_kernel(const int32_t* new_lens,
                                                            const PageRows r, int32_t* target) {
   griddep_wait();
