@@ -351,8 +351,9 @@ __global__ void __launch_bounds__(256) resize_check_kernel(const int32_t* new_le
     const int keep = min(len, then);
     if (then != len && keep % r.bs != 0) {
       const int p = row_of(r, i)[keep / r.bs];
-      if (good_page(r, p) && r.refs[p] > 1) {
-        raise_error(r.err, FP8PA_DEVERR_SHARED);
+      const bool there = good_page(r, p);
+      if (!there || r.refs[p] > 1) {
+        raise_error(r.err, there ? FP8PA_DEVERR_SHARED : FP8PA_DEVERR_BLOCK_RANGE);
         t = kSkip;
       }
     }

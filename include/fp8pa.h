@@ -575,9 +575,9 @@ size_t fp8pa_tree_workspace_bytes(int total_q, int batch, int n_q_heads, int n_k
  * workspace     fp8pa_pages_workspace_bytes(rows, num_blocks), 4-byte aligned, no
  *               initialisation; calls that share it must be stream-ordered.
  * Limits        num_blocks * block_size < 2^31, max_blocks_per_seq <= 2^20.
- * An entry of a table outside the pool is left alone and sets
- * FP8PA_DEVERR_BLOCK_RANGE, a length outside [0, max_blocks_per_seq * block_size]
- * FP8PA_DEVERR_SEQ_LEN.
+ * An entry of a table outside the pool sets FP8PA_DEVERR_BLOCK_RANGE and names no page: no
+ * count changes for it (a resize that gives it back makes it -1, like the others).  A
+ * length outside [0, max_blocks_per_seq * block_size] sets FP8PA_DEVERR_SEQ_LEN.
  */
 size_t fp8pa_pages_workspace_bytes(int rows, int num_blocks);
 
@@ -626,7 +626,8 @@ int fp8pa_kv_fork(const int32_t* src_rows, const int32_t* dst_rows, int num_fork
  * Where the pool runs out, the row that does not fit and every growing row behind it
  * are left as they were (FP8PA_DEVERR_NO_BLOCK).  A row whose length would change
  * while the page of its next token holds tokens and is another row's, too, is left
- * (FP8PA_DEVERR_SHARED).
+ * (FP8PA_DEVERR_SHARED), and so is one whose table names no such page
+ * (FP8PA_DEVERR_BLOCK_RANGE).
  * new_lens   i32 [rows]; may be seq_lens itself (then nothing changes), otherwise not
  *            overlapping it.
  */
