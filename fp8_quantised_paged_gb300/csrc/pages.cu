@@ -231,13 +231,32 @@ __global__ void __launch_bounds__(kCopyThreads) keep_kernel(const int32_t* accep
 }
 
 // ---------------------------------------------------------------- forks
-// Workspace: claim[rows] the first fork that wants a row; by fork, page[rows] the page
+// Workspace: claim[rows] the first sound fork that wants a row; by fork, page[rows] the page
 // that its last, partly filled page is copied to, kWhole where there is none, kSkip
 // where the fork is not made, and size[rows] the length that it takes over (a source may
 // be another fork's row: all see the rows as they were); then the free pages.  One CTA
 // plans, bound by the round trips of the counts and of the rows' lengths; the copies of the
 // last pages are bound by HBM (16 rows to 128: 20.4 us in all, 138 MB).
-constexpr int kSkip = -2, kWhole = -1;
+constexpr int kSkip = -2, kWhole = -1, kTail = 0;
+
+// What fork i needs: a page of its own for the last tokens (kTail) or none (kWhole); kSkip,
+// with its error raised, where its rows or its source are not as a fork needs them.
+__device__ __forceinline__ int look_at_fork(const PageRows& r, int s, int d, int* size) {
+  if (s < 0 || s >= r.rows || d < 0 || d >= r.rows || s == d || r.lens[d] != 0) {
+    raise_error(r.err, FP8PA_DEVERR_ROW);
+    return kSkip;
+  }
+  const int len = r.lens[s];
+  *size = len;
+  if (!good_len(r, len)) {
+    raise_error(r.err, FP8PA_DEVERR_SEQ_LEN);
+    return kSkip;
+  }
+  if (len % r.bs == 0) return kWhole;
+  if (good_page(r, row_of(r, s)[len / r.bs])) return kTail;
+  raise_error(r.err, FP8PA_DEVERR_BLOCK_RANGE);
+  return kSkip;
+}
 
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const int32_t* src,
                                                                  const int32_t* dst, int forks,
@@ -250,8 +269,9 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const int32_t* 
   for (int i = tid; i < r.rows; i += kPlanThreads) claim[i] = forks;
   __syncthreads();
   for (int i = tid; i < forks; i += kPlanThreads) {
-    const int d = __ldg(dst + i);
-    if (d >= 0 && d < r.rows) atomicMin(claim + d, i);
+    const int d = __ldg(dst + i), what = look_at_fork(r, __ldg(src + i), d, size + i);
+    page[i] = what;
+    if (what != kSkip) atomicMin(claim + d, i);
   }
   __syncthreads();
   int want = 0;
@@ -259,27 +279,15 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const int32_t* 
     const int i = base + tid;
     int what = kSkip;
     if (i < forks) {
-      const int s = __ldg(src + i), d = __ldg(dst + i);
-      const bool rows = s >= 0 && s < r.rows && d >= 0 && d < r.rows && s != d;
-      if (!rows || r.lens[d] != 0 || __ldcg(claim + d) != i) {
+      what = page[i];
+      if (what != kSkip && __ldcg(claim + __ldg(dst + i)) != i) {
         raise_error(r.err, FP8PA_DEVERR_ROW);
-      } else {
-        const int len = r.lens[s];
-        size[i] = len;
-        if (!good_len(r, len)) {
-          raise_error(r.err, FP8PA_DEVERR_SEQ_LEN);
-        } else if (len % r.bs == 0) {
-          what = kWhole;
-        } else if (!good_page(r, row_of(r, s)[len / r.bs])) {
-          raise_error(r.err, FP8PA_DEVERR_BLOCK_RANGE);
-        } else {
-          what = 0;
-        }
+        what = kSkip;
       }
     }
     int at;
-    const int total = block_scan(what == 0 ? 1 : 0, &at, s_warp);
-    if (i < forks) page[i] = what == 0 ? want + at : what;
+    const int total = block_scan(what == kTail ? 1 : 0, &at, s_warp);
+    if (i < forks) page[i] = what == kTail ? want + at : what;
     want += total;
   }
   const int got = take_free(r, want, list, s_warp);

@@ -608,9 +608,11 @@ int fp8pa_kv_keep_accepted(const int32_t* accepted, int max_accepted, const int3
  * pages are shared (their counts rise); a last page that is not full is copied to a
  * free page, in every array, as both rows will write to it.
  * dst_rows   rows of length 0, each wanted once.  A fork that breaks this, or whose rows
- *            are outside the tables, is skipped (FP8PA_DEVERR_ROW); of several that
- *            want one row the first is made.  One that finds no free page is skipped
- *            (FP8PA_DEVERR_NO_BLOCK).  All forks see the rows as they were before.
+ *            are outside the tables, is skipped (FP8PA_DEVERR_ROW), and so is one whose
+ *            source has a length or a last page that is none.  Of several others that
+ *            want one row the first gets it; where it finds no free page, it is skipped
+ *            all the same (FP8PA_DEVERR_NO_BLOCK), and the row stays empty.  All forks see
+ *            the rows as they were before.
  * num_forks  at most rows.
  */
 int fp8pa_kv_fork(const int32_t* src_rows, const int32_t* dst_rows, int num_forks,
