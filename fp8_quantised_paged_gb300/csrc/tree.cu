@@ -189,7 +189,8 @@ cudaError_t launch_tree(const PrefillArgs& args, const int32_t* parents, cudaStr
               &depth);
   const int var = a.cap > 0.f ? 2 : (a.slopes ? 1 : 0);
   const bool raw = a.fmt != FP8PA_INT8 && a.mode != FP8PA_SCALE_MX_BLOCK;
-  const TreeKernel fn = a.d == 128 ? pick_tree_d128(raw, var) : pick_tree_d64(raw, var);
+  const bool st = a.mode == FP8PA_SCALE_CHANNEL_STATIC;
+  const TreeKernel fn = a.d == 128 ? pick_tree_d128(raw, st, var) : pick_tree_d64(raw, st, var);
   if ((e = ensure_smem_attr(reinterpret_cast<const void*>(fn.fn), fn.smem)) != cudaSuccess)
     return e;
   CUtensorMap mk{}, mv{};

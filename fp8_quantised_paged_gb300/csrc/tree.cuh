@@ -38,7 +38,9 @@
 //
 // Products.  S = Q K^T on FP8 tensor cores: the K codes as TMA lands them, q as two E4M3
 // terms hi + lo (exact for bf16 but for elements 2^-9 below the row's largest), the token's
-// scale multiplied to the fp32 score.  O += P V on f16: V's codes are exact in f16, their
+// scale multiplied to the fp32 score.  Static channel scales go into q, whose products with
+// them have more bits: a third term keeps these to 2^-14 (two terms to 2^-9, where the f16 of
+// other formats holds 2^-11).  O += P V on f16: V's codes are exact in f16, their
 // scale goes into P in fp32 before its one rounding (2^-11).  So no code is rounded, and a
 // K tile needs no converting.  INT8 codes and MX blocks (RAW false) are converted for both
 // products: INT8 exactly, an MX block's codes times its power of two relative to the
@@ -72,9 +74,9 @@ struct TreeKernel {
   TreeFn fn;
   int smem, threads;
 };
-// raw: FP8 codes with a scale per token, segment or channel.
-TreeKernel pick_tree_d64(bool raw, int var);
-TreeKernel pick_tree_d128(bool raw, int var);
+// raw: FP8 codes with a scale per token, segment or channel (st).
+TreeKernel pick_tree_d64(bool raw, bool st, int var);
+TreeKernel pick_tree_d128(bool raw, bool st, int var);
 
 namespace {
 
@@ -124,6 +126,9 @@ struct TreeSmem {
   static constexpr int kBars = kExp + 256 * 4;
   static constexpr int kMisc = kBars + 320;        // TMEM base, abort flag
   static constexpr int kBytes = kMisc + 16;
+  static constexpr int kQ3 = (kBytes + 1023) / 1024 * 1024;  // the third term of q, where it has one
+  static constexpr int kBytesThree = kQ3 + kCodes;
+  static_assert((RAW ? kBytesThree : kBytes) <= 227 * 1024);
 };
 // Barriers and the arrivals that complete a phase: Q the eight softmax warps; P (stream * 2
 // + half) the stream's four; Info the copying warps (RAW) or the converting ones; K full
@@ -686,8 +691,10 @@ __device__ __forceinline__ bool elect_one() {
 
 // ---------------------------------------------------------------- kernel
 // VAR: 0 no score modifier but the masks, 1 distance bias, 2 capped scores (with or
-// without a bias).
-template <int D, bool RAW, int VAR>
+// without a bias).  THREE: q in three terms, for static channel scales (RAW), 4-5 % slower
+// than two (12 x 16K, E4M3: 153 us, 147; ragged 64, E5M2: 206, 199), so an instance of its own: a
+// branch on the mode cost calls with token scales 2 % as well (ragged 64, E4M3: 232 us, 227).
+template <int D, bool RAW, int VAR, bool THREE>
 __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
     tree_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ PlanView pv,
                 const __grid_constant__ TreeView tv, const __grid_constant__ CUtensorMap mk,
@@ -763,6 +770,11 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
             for (int k = 0; k < D / 32; ++k)
               tc_mma_f8(ds, dq + term * (SM::kCodes >> 4) + k * 2, dk + k * 2, idesc_s,
                         (term | k) != 0);
+          if constexpr (THREE) {
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+              tc_mma_f8(ds, dq + ((SM::kQ3 - SM::kQ) >> 4) + k * 2, dk + k * 2, idesc_s, true);
+          }
         } else {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
@@ -941,19 +953,30 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           for (int x = 0; x < D / 32; ++x) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[x][e] *= fq;
-            if constexpr (RAW) {  // hi, and lo = what hi leaves
+            if constexpr (RAW) {  // hi, lo = what hi leaves, and (THREE) what both leave
               uint32_t hi[4], lo[4];
+              // the codes of f[x], which is left as what they do not hold
+              auto term = [&](uint32_t (&code)[4]) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                hi[e] = f32x2_to_codes2<FP8PA_E4M3>(f[x][2 * e], f[x][2 * e + 1]);
-                const float2 b = __half22float2(h2(codes2_to_f16x2<FP8PA_E4M3>(hi[e])));
-                lo[e] = f32x2_to_codes2<FP8PA_E4M3>(f[x][2 * e] - b.x, f[x][2 * e + 1] - b.y);
-              }
+                for (int e = 0; e < 4; ++e) {
+                  code[e] = f32x2_to_codes2<FP8PA_E4M3>(f[x][2 * e], f[x][2 * e + 1]);
+                  const float2 b = __half22float2(h2(codes2_to_f16x2<FP8PA_E4M3>(code[e])));
+                  f[x][2 * e] -= b.x;
+                  f[x][2 * e + 1] -= b.y;
+                }
+              };
+              term(hi);
+              term(lo);
               const int c8 = x * 4 + c4;  // 8 dims: half a 16-byte chunk
               uint8_t* p = dst + swizzled<D>(to_row, c8 >> 1) + (c8 & 1) * 8;
               *reinterpret_cast<uint2*>(p) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
               *reinterpret_cast<uint2*>(p + SM::kCodes) =
                   make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+              if constexpr (THREE) {
+                term(lo);
+                *reinterpret_cast<uint2*>(p + (SM::kQ3 - SM::kQ)) =
+                    make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+              }
             } else {
               *reinterpret_cast<uint4*>(dst + (to_row >> 3) * 128 + r8 * 16 +
                                         (x * 4 + c4) * 2048) =
@@ -1283,11 +1306,16 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
 }
 
 // ---------------------------------------------------------------- instances
-template <int D, bool RAW>
+template <int D, bool RAW, bool THREE>
 TreeKernel pick_tree(int var) {
-  return {var == 0 ? tree_kernel<D, RAW, 0>
-                   : (var == 1 ? tree_kernel<D, RAW, 1> : tree_kernel<D, RAW, 2>),
-          TreeSmem<D, RAW>::kBytes, kTreeThreads<RAW>};
+  return {var == 0 ? tree_kernel<D, RAW, 0, THREE>
+                   : (var == 1 ? tree_kernel<D, RAW, 1, THREE> : tree_kernel<D, RAW, 2, THREE>),
+          THREE ? TreeSmem<D, RAW>::kBytesThree : TreeSmem<D, RAW>::kBytes, kTreeThreads<RAW>};
+}
+template <int D>
+TreeKernel pick_tree(bool raw, bool st, int var) {
+  return !raw ? pick_tree<D, false, false>(var)
+              : (st ? pick_tree<D, true, true>(var) : pick_tree<D, true, false>(var));
 }
 
 }  // namespace

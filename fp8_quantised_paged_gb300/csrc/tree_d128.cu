@@ -3,8 +3,6 @@
 
 namespace fp8pa {
 
-TreeKernel pick_tree_d128(bool raw, int var) {
-  return raw ? pick_tree<128, true>(var) : pick_tree<128, false>(var);
-}
+TreeKernel pick_tree_d128(bool raw, bool st, int var) { return pick_tree<128>(raw, st, var); }
 
 }  // namespace fp8pa

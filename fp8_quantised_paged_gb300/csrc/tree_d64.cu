@@ -3,8 +3,6 @@
 
 namespace fp8pa {
 
-TreeKernel pick_tree_d64(bool raw, int var) {
-  return raw ? pick_tree<64, true>(var) : pick_tree<64, false>(var);
-}
+TreeKernel pick_tree_d64(bool raw, bool st, int var) { return pick_tree<64>(raw, st, var); }
 
 }  // namespace fp8pa

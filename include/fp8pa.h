@@ -524,10 +524,10 @@ size_t fp8pa_prefill_workspace_bytes(int total_q, int batch, int n_q_heads, int 
  * A tree of more than FP8PA_MAX_TREE nodes (FP8PA_DEVERR_TREE), or one longer than its
  * request or whose length is outside [0, cap] (FP8PA_DEVERR_SEQ_LEN), is skipped, as are
  * bad offsets: its rows are left as they were, like rows outside every tree.
- * Precision    fp32 scores of q to 2^-17 of a row's largest element (CHANNEL_STATIC: of q
- *              times the scales to 2^-9 of each); the softmax weights, times V's scale,
- *              are rounded to f16 (2^-11).  Values of V below 2^-94, and scales that lie
- *              far apart, as in the prefill.
+ * Precision    scores in fp32, of q to 2^-17 of its row's largest element; CHANNEL_STATIC:
+ *              of q times the scales to 2^-14 of each element besides (INT8 codes: to
+ *              2^-11).  The softmax weights, times V's scale, are rounded to f16 (2^-11).
+ *              Values of V below 2^-94, and scales that lie far apart, as in the prefill.
  * workspace    fp8pa_tree_workspace_bytes(), 16-byte aligned; no initialisation; calls
  *              that share it must be stream-ordered.  It grows with total_q and batch
  *              alone: a larger batch's serves every smaller one of the same heads.
