@@ -130,7 +130,7 @@ struct TreeSmem {
   static constexpr int kBytesThree = kQ3 + kCodes;
   static_assert((RAW ? kBytesThree : kBytes) <= 227 * 1024);
 };
-// Barriers and the arrivals that complete a phase: Q the eight softmax warps; P (stream * 2
+// Barriers and the arrivals that complete a phase: Q the eight softmax warps and the issuers; P (stream * 2
 // + half) the stream's four; Info the copying warps (RAW) or the converting ones; K full
 // one thread and its bytes (RAW) or four warps; V codes full a thread and its bytes, free
 // the four converting warps; V full four warps; All the eight softmax warps; K and V free two
@@ -140,7 +140,7 @@ enum { kTQ = 0, kTP = 1, kTInfo = 5, kTKFull = 13, kTVCFull = 17, kTVCFree = 19,
        kTAll = 23, kTKFree = 24, kTVFree = 28, kTS = 30, kTO = 34, kTDrain = 38, kTreeBars = 40 };
 template <bool RAW>
 __device__ __forceinline__ int tree_bar_count(int i) {
-  return i < kTP        ? 8
+  return i < kTP        ? 10
          : i < kTInfo   ? 4
          : i < kTKFull  ? (RAW ? 2 : 8)
          : i < kTVCFull ? (RAW ? 1 : 4)
@@ -808,7 +808,11 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
       u += n;
       // q first, and every item's: once it is there, every tile before the item is over, and
       // a parity of the barriers below can mean no phase but its own (later ones follow its
-      // own, as the stages are even in number)
+      // own, as the stages are even in number).  The issuer arrives there itself: one that
+      // has no tile in some items would otherwise hold none of them back, and q of two more
+      // could pass it by.
+      if (elect_one()) mbar_arrive(bars + kTQ);
+      __syncwarp();
       ok = wait_warp(kTQ, nq & 1);
       ++nq;
       wide = __shfl_sync(0xffffffffu, !RAW && im.r.rows > 128, 0);
