@@ -66,6 +66,8 @@ _SIGS = {
     "fp8pa_tree_workspace_bytes": (ctypes.c_size_t, [_I] * 7),
     "fp8pa_pages_workspace_bytes": (ctypes.c_size_t, [_I, _I]),
     "fp8pa_kv_keep_accepted": (_I, [_P, _I, _P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "fp8pa_kv_keep_accepted_counted": (_I, [_P, _I, _P, _P, _I, _P, _I, _P, _P, _P, _I, _I, _I,
+                                            _I, _P, _P]),
     "fp8pa_kv_fork": (_I, [_P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _P,
                            ctypes.c_size_t, _P]),
     "fp8pa_kv_resize": (_I, [_P, _P, _I, _P, _I, _P, _I, _I, _P, ctypes.c_size_t, _P]),

@@ -764,14 +764,16 @@ def _check_pages(pages, block_tables, seq_lens, ref_counts):
 
 
 def kv_keep_accepted(accepted, q_offsets, block_tables, seq_lens, pages, new_lens=None,
-                     stream=None):
+                     stream=None, ref_counts=None):
     """After a drafted tree's verification: move the accepted path's cached rows to the
     front of the tree's tokens.  accepted: int32 [B, max_accepted], the path's node
     numbers, then -1; request b's tree is its last q_offsets[b+1] - q_offsets[b] tokens.
-    pages: a KvPages of per-token arrays; a row with a tree is not forked before this call.
-    Returns the new lengths (int32 [B]); the pages behind them stay the rows' until
-    kv_resize."""
-    dev, B, max_blocks = _check_pages(pages, block_tables, seq_lens, None)
+    pages: a KvPages of per-token arrays, not the codes of SCALE_SEGMENT (a row there has
+    its page's scale).  A row with a tree is not forked before this call; with ref_counts
+    (as kv_fork's) a request whose rows would move into a page that another row holds, too,
+    is left as it was (DEVERR_SHARED), without them it is not noticed.  Returns the new
+    lengths (int32 [B]); the pages behind them stay the rows' until kv_resize."""
+    dev, B, max_blocks = _check_pages(pages, block_tables, seq_lens, ref_counts)
     if not pages.per_token:
         raise ValueError("kv_keep_accepted needs arrays of rows per token and head")
     _want(accepted, torch.int32, "accepted", dev)
@@ -783,11 +785,15 @@ def kv_keep_accepted(accepted, q_offsets, block_tables, seq_lens, pages, new_len
     _want(new_lens, torch.int32, "new_lens", dev)
     if new_lens.numel() != B:
         raise ValueError(f"new_lens must hold {B} entries")
+    head = (accepted.data_ptr(), accepted.shape[1], q_offsets.data_ptr(), block_tables.data_ptr(),
+            max_blocks, seq_lens.data_ptr(), B)
+    tail = (*pages._args, pages.n_kv_heads, pages.num_blocks, pages.block_size,
+            new_lens.data_ptr(), _raw_stream(stream, dev))
     with _on(dev):
-        rc = N.lib.fp8pa_kv_keep_accepted(
-            accepted.data_ptr(), accepted.shape[1], q_offsets.data_ptr(), block_tables.data_ptr(),
-            max_blocks, seq_lens.data_ptr(), B, *pages._args, pages.n_kv_heads, pages.num_blocks,
-            pages.block_size, new_lens.data_ptr(), _raw_stream(stream, dev))
+        if ref_counts is None:
+            rc = N.lib.fp8pa_kv_keep_accepted(*head, *tail)
+        else:
+            rc = N.lib.fp8pa_kv_keep_accepted_counted(*head, ref_counts.data_ptr(), *tail)
     if rc:
         N.check(rc, "kv_keep_accepted")
     return new_lens

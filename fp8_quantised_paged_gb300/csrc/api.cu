@@ -491,6 +491,35 @@ int pages_workspace(const void* workspace, size_t bytes, int rows, int num_block
   return bytes < 4 * pages_workspace_words(rows, num_blocks) ? FP8PA_ERR_WORKSPACE : FP8PA_OK;
 }
 
+// Keep accepted paths; refs: the pages' counts, or null where no page that is written is shared.
+int keep_impl(const int32_t* accepted, int max_accepted, const int32_t* q_offsets,
+              const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+              int batch, const int32_t* refs, void* const* pages, const long long* page_bytes,
+              int n_arrays, int n_kv_heads, int num_blocks, int block_size, int32_t* new_lens,
+              void* stream) {
+  if (max_accepted <= 0 || n_kv_heads <= 0) return FP8PA_ERR_BAD_SHAPE;
+  PageRows r;
+  const int st = pages_prepare(const_cast<int32_t*>(block_tables), max_blocks_per_seq,
+                               const_cast<int32_t*>(seq_lens), batch, const_cast<int32_t*>(refs),
+                               pages, page_bytes, n_arrays, num_blocks, block_size, &r);
+  if (st != FP8PA_OK || batch == 0) return st;
+  if (!accepted || !q_offsets || !new_lens) return FP8PA_ERR_NULL_POINTER;
+  const long long page_rows = static_cast<long long>(n_kv_heads) * block_size;
+  for (int i = 0; i < n_arrays; ++i) {
+    if (page_bytes[i] % page_rows != 0) return FP8PA_ERR_BAD_SHAPE;
+    if (page_bytes[i] / page_rows * max_accepted >= (1ll << 31) ||
+        static_cast<long long>(n_kv_heads) * n_arrays >= (1ll << 31))
+      return FP8PA_ERR_UNSUPPORTED;
+  }
+  if (new_lens == seq_lens || partly_overlap(new_lens, seq_lens, batch))
+    return FP8PA_ERR_UNSUPPORTED;
+  r.err = device_error_ptr(static_cast<cudaStream_t>(stream), nullptr);
+  if (!r.err) return FP8PA_ERR_CUDA;
+  return cuda_status(launch_keep_accepted(accepted, max_accepted, q_offsets, r, pages, page_bytes,
+                                          n_arrays, n_kv_heads, new_lens,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -899,27 +928,22 @@ int fp8pa_kv_keep_accepted(const int32_t* accepted, int max_accepted, const int3
                            const int32_t* seq_lens, int batch, void* const* pages,
                            const long long* page_bytes, int n_arrays, int n_kv_heads,
                            int num_blocks, int block_size, int32_t* new_lens, void* stream) {
-  if (max_accepted <= 0 || n_kv_heads <= 0) return FP8PA_ERR_BAD_SHAPE;
-  PageRows r;
-  const int st = pages_prepare(const_cast<int32_t*>(block_tables), max_blocks_per_seq,
-                               const_cast<int32_t*>(seq_lens), batch, nullptr, pages, page_bytes,
-                               n_arrays, num_blocks, block_size, &r);
-  if (st != FP8PA_OK || batch == 0) return st;
-  if (!accepted || !q_offsets || !new_lens) return FP8PA_ERR_NULL_POINTER;
-  const long long page_rows = static_cast<long long>(n_kv_heads) * block_size;
-  for (int i = 0; i < n_arrays; ++i) {
-    if (page_bytes[i] % page_rows != 0) return FP8PA_ERR_BAD_SHAPE;
-    if (page_bytes[i] / page_rows * max_accepted >= (1ll << 31) ||
-        static_cast<long long>(n_kv_heads) * n_arrays >= (1ll << 31))
-      return FP8PA_ERR_UNSUPPORTED;
-  }
-  if (new_lens == seq_lens || partly_overlap(new_lens, seq_lens, batch))
-    return FP8PA_ERR_UNSUPPORTED;
-  r.err = device_error_ptr(static_cast<cudaStream_t>(stream), nullptr);
-  if (!r.err) return FP8PA_ERR_CUDA;
-  return cuda_status(launch_keep_accepted(accepted, max_accepted, q_offsets, r, pages, page_bytes,
-                                          n_arrays, n_kv_heads, new_lens,
-                                          static_cast<cudaStream_t>(stream)));
+  return keep_impl(accepted, max_accepted, q_offsets, block_tables, max_blocks_per_seq, seq_lens,
+                   batch, nullptr, pages, page_bytes, n_arrays, n_kv_heads, num_blocks, block_size,
+                   new_lens, stream);
+}
+
+int fp8pa_kv_keep_accepted_counted(const int32_t* accepted, int max_accepted,
+                                   const int32_t* q_offsets, const int32_t* block_tables,
+                                   int max_blocks_per_seq, const int32_t* seq_lens, int batch,
+                                   const int32_t* ref_counts, void* const* pages,
+                                   const long long* page_bytes, int n_arrays, int n_kv_heads,
+                                   int num_blocks, int block_size, int32_t* new_lens,
+                                   void* stream) {
+  if (!ref_counts && batch > 0) return FP8PA_ERR_NULL_POINTER;
+  return keep_impl(accepted, max_accepted, q_offsets, block_tables, max_blocks_per_seq, seq_lens,
+                   batch, ref_counts, pages, page_bytes, n_arrays, n_kv_heads, num_blocks,
+                   block_size, new_lens, stream);
 }
 
 int fp8pa_kv_fork(const int32_t* src_rows, const int32_t* dst_rows, int num_forks,

@@ -214,8 +214,23 @@ __global__ void __launch_bounds__(kCopyThreads) keep_kernel(const int32_t* accep
     last = __shfl_sync(0xffffffffu, x, 31);
   }
   const int ctx = len - n;
-  if (first && lane == 0 && new_lens) new_lens[b] = ctx + count;
   const int32_t* table = row_of(r, b);
+  if (r.refs) {  // no row moves into a page that another table holds, too
+    bool shared = false;
+    for (int t = lane; t < count; t += 32) {
+      if (__ldg(acc + t) == t) continue;
+      const int page = __ldg(table + (ctx + t) / r.bs);
+      shared = shared || (good_page(r, page) && __ldg(r.refs + page) > 1);
+    }
+    if (__any_sync(0xffffffffu, shared)) {
+      if (first && lane == 0) {
+        raise_error(r.err, FP8PA_DEVERR_SHARED);
+        if (new_lens) new_lens[b] = len;
+      }
+      return;
+    }
+  }
+  if (first && lane == 0 && new_lens) new_lens[b] = ctx + count;
   for (int w = blockIdx.y * (kCopyThreads / 32) + (threadIdx.x >> 5); w < a.n * hkv;
        w += gridDim.y * (kCopyThreads / 32)) {
     const int i = w / hkv, head = w - i * hkv;

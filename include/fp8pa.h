@@ -83,7 +83,7 @@ extern "C" {
 #define FP8PA_DEVERR_TREE 64u        /* a parent or an accepted node out of order, or too large a tree */
 #define FP8PA_DEVERR_ROW 128u        /* fork: a row outside the tables, not empty or wanted twice (fork skipped) */
 #define FP8PA_DEVERR_NO_BLOCK 256u   /* fork, resize: no free page left (fork or row left as it was) */
-#define FP8PA_DEVERR_SHARED 512u     /* resize: the row would end inside a page that others hold (row left) */
+#define FP8PA_DEVERR_SHARED 512u     /* resize, keep: the row would write to a page that others hold (row left) */
 
 /* Code formats: FP8 E4M3 and E5M2, and symmetric INT8 (the alternate KV
  * codec; FMAX = 127, integer codes in [-127, 127] stored as the byte
@@ -593,6 +593,9 @@ size_t fp8pa_pages_workspace_bytes(int rows, int num_blocks);
  *            a multiple of that).  Not the scales of FP8PA_SCALE_SEGMENT, nor codes
  *            under them: a row's scale is its page's.  Pages that hold tokens of a tree
  *            are its row's alone: a row is forked before its draft or after this call.
+ *            The second form sees to that by the pages' counts: a request of which a row
+ *            would move into a page that another table holds, too, is left as it was
+ *            (FP8PA_DEVERR_SHARED).
  * new_lens   i32 [batch], not overlapping seq_lens.  A request with bad offsets
  *            (FP8PA_DEVERR_Q_OFFSETS) or a tree longer than it is is left as it was.
  * The pages behind the new length stay the row's: fp8pa_kv_resize gives them back.
@@ -602,6 +605,13 @@ int fp8pa_kv_keep_accepted(const int32_t* accepted, int max_accepted, const int3
                            const int32_t* seq_lens, int batch, void* const* pages,
                            const long long* page_bytes, int n_arrays, int n_kv_heads,
                            int num_blocks, int block_size, int32_t* new_lens, void* stream);
+int fp8pa_kv_keep_accepted_counted(const int32_t* accepted, int max_accepted,
+                                   const int32_t* q_offsets, const int32_t* block_tables,
+                                   int max_blocks_per_seq, const int32_t* seq_lens, int batch,
+                                   const int32_t* ref_counts, void* const* pages,
+                                   const long long* page_bytes, int n_arrays, int n_kv_heads,
+                                   int num_blocks, int block_size, int32_t* new_lens,
+                                   void* stream);
 
 /*
  * Forks: row dst_rows[i] becomes a copy of the sequence in row src_rows[i].  Its full
