@@ -705,7 +705,8 @@ def paged_tree_attention(q, q_offsets, parents, k_cache, v_cache, k_scale, v_sca
 class KvPages:
     """The arrays of a cache whose pages the page operators move: codes and scales of
     every layer's K and V, each contiguous with the pages as its first dimension and a
-    multiple of 16 bytes a page (static channel scales are not among them).  Made once,
+    multiple of 16 bytes a page, no two overlapping (static channel scales are not among
+    them).  Made once,
     next to the cache; it holds the tensors."""
 
     def __init__(self, tensors):
@@ -724,6 +725,12 @@ class KvPages:
                     raise ValueError(f"tensors[{i}]: heads and block size differ from the "
                                      f"others'")
                 rows = tuple(t.shape[1:3])
+        # an array given twice would have its rows moved twice, by threads at once
+        spans = sorted((t.data_ptr(), t.numel() * t.element_size(), i)
+                       for i, t in enumerate(self.tensors))
+        for (p, n, i), (q, _, j) in zip(spans, spans[1:]):
+            if p + n > q:
+                raise ValueError(f"tensors[{i}] and tensors[{j}] overlap")
         self.n_kv_heads, self.block_size = rows or (None, None)
         # whether every array has a row per token and head
         self.per_token = all(t.dim() == 4 for t in self.tensors)

@@ -568,7 +568,8 @@ size_t fp8pa_tree_workspace_bytes(int total_q, int batch, int n_q_heads, int n_k
  *   pages         the arrays of every layer that hold num_blocks pages: a host array of
  *                 n_arrays device pointers (codes and scales of K and V; not static
  *                 scales), and page_bytes, the bytes of one page of each: a multiple of
- *                 16, on 16-byte aligned arrays.  Both are read during the call only.
+ *                 16, on 16-byte aligned arrays that do not overlap.  Both are read
+ *                 during the call only.
  * A page is shared by any number of rows while it is full; the page that a row's next
  * token goes to is its own.  Free pages are taken with the lowest number first, for the
  * rows in order, so every result is determined by the arguments.
