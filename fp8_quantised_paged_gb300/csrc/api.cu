@@ -469,7 +469,7 @@ int pages_prepare(int32_t* tables, int max_blocks, int32_t* lens, int rows, int3
                   int bs, PageRows* r) {
   if (rows < 0 || max_blocks <= 0 || num_blocks <= 0 || bs <= 0 || arrays < 0)
     return FP8PA_ERR_BAD_SHAPE;
-  if (static_cast<long long>(num_blocks) * bs >= (1ll << 31) ||
+  if (static_cast<long long>(num_blocks) * bs >= (1ll << 31) - 1 ||  // (one more is counted)
       static_cast<long long>(max_blocks) * bs >= (1ll << 31) || max_blocks > (1 << 20))
     return FP8PA_ERR_UNSUPPORTED;
   if ((rows > 0 && (!tables || !lens)) || (arrays > 0 && (!pages || !page_bytes)))

@@ -411,9 +411,10 @@ __global__ void __launch_bounds__(kPlanThreads) resize_grow_kernel(const int32_t
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x;
-  // more pages than the pool has are not there: the sum stops at one more than that
+  // more pages than the pool has are not there: the sum stops at one more than that (in 64
+  // bits, as rows of 2^20 pages each pass 32 before it is looked at)
   const int most = r.num_blocks + 1;
-  int want = 0;
+  long long want = 0;
   for (int base = 0; base < r.rows; base += kPlanThreads) {
     const int i = base + tid;
     int n = 0;
@@ -421,11 +422,11 @@ __global__ void __launch_bounds__(kPlanThreads) resize_grow_kernel(const int32_t
     int at;
     // (a chunk's sum stays below 1024 (2^20 + 1): larger growths fit no pool of fewer pages)
     const int total = block_scan(min(n, min(most, 1 << 20)), &at, s_warp);
-    if (i < r.rows) prefix[i] = min(want + at, most);
-    want = min(want + total, most);
+    if (i < r.rows) prefix[i] = static_cast<int>(min(want + at, static_cast<long long>(most)));
+    want = min(want + total, static_cast<long long>(most));
   }
-  if (tid == 0) prefix[r.rows] = want;
-  const int got = take_free(r, want, list, s_warp);
+  if (tid == 0) prefix[r.rows] = static_cast<int>(want);
+  const int got = take_free(r, static_cast<int>(want), list, s_warp);
   __syncthreads();
   // rows that got all their pages: those whose prefix ends within them
   for (int k = tid; k < got; k += kPlanThreads) {

@@ -575,7 +575,7 @@ size_t fp8pa_tree_workspace_bytes(int total_q, int batch, int n_q_heads, int n_k
  * rows in order, so every result is determined by the arguments.
  * workspace     fp8pa_pages_workspace_bytes(rows, num_blocks), 4-byte aligned, no
  *               initialisation; calls that share it must be stream-ordered.
- * Limits        num_blocks * block_size < 2^31, max_blocks_per_seq <= 2^20.
+ * Limits        num_blocks * block_size < 2^31 - 1, max_blocks_per_seq <= 2^20.
  * An entry of a table outside the pool sets FP8PA_DEVERR_BLOCK_RANGE and names no page: no
  * count changes for it (a resize that gives it back makes it -1, like the others).  A
  * length outside [0, max_blocks_per_seq * block_size] sets FP8PA_DEVERR_SEQ_LEN.
