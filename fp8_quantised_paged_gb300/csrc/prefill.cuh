@@ -289,6 +289,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// The larger of two, NaN where either is (a NaN of the caller's score scale stays one).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // D[tmem] (+)= A[tmem] * B[smem], one thread.
 __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                               bool accumulate) {
@@ -991,7 +997,7 @@ __global__ void __launch_bounds__(kThreads<READY>, 1)
           ev[w] = static_cast<float>(info.ev[first + w]);
           // (VAR 0 multiplies a masked -inf by the factor: not zero)
           zw[w] = zs * exp2i(info.ek[first + w]);
-          if (VAR == 0) zw[w] = fmaxf(zw[w], 1e-37f);
+          if (VAR == 0) zw[w] = max_nan(zw[w], 1e-37f);
           m[w] = info.valid[first + w];
           all &= m[w];
         }

@@ -1028,7 +1028,7 @@ __global__ void __launch_bounds__(kTreeThreads<RAW>, 1)
           // log2-domain factor of a raw score (capped scores: see cap_in)
           const int er = exps[bl];
           zs = fabsf(a.sm_scale) * exp2i(er - kTop) * (VAR == 2 ? a.cap_in : kLog2e);
-          if (VAR == 0) zs = fmaxf(zs, 1e-37f);  // (it multiplies a masked -inf: not zero)
+          if (VAR == 0) zs = max_nan(zs, 1e-37f);  // (it multiplies a masked -inf: not zero)
           if (er > 128) zs = __int_as_float(0x7FC00000);
         } else if (half == 0) {
           late_nan(gt - step);  // (what the tile before brought that is not finite is known by now)
