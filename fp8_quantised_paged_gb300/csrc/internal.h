@@ -217,7 +217,7 @@ size_t prefill_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, i
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 
 // Attention for trees of drafted tokens (tree.cu): a prefill's arguments and the parents.
-constexpr int kTreeRows = 128;  // a block of 256 is planned as the work of two
+constexpr int kTreeRows = 128;  // of a block; INT8 and MX take 256, a tile of which counts 1.4
 size_t tree_workspace_bytes(int total_q, int batch, int hq, int hkv, int d, int device);
 cudaError_t launch_tree(const PrefillArgs& a, const int32_t* parents, cudaStream_t stream);
 

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
   }
   if (tid == 0) v.rb_pre[blocks] = carry;
   __syncthreads();
-  cut_ranges(v, blocks, carry, a.hkv, ranges,
+  cut_ranges(v, blocks, carry, a.hkv, ranges, 0,
              [&](int i) { return static_cast<long long>(v.rb_pre[i]); });
 }
 

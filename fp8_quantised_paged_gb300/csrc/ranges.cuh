@@ -29,11 +29,11 @@ __device__ __forceinline__ int last_le(const int* a, int n, int x) {
 
 // Cuts the blocks' `tiles` token tiles (v.rb_pre), for every KV head, into ranges of the
 // same cost.  cost(i): of the blocks before block i (of one KV head), where an item (a block
-// and KV head) costs kCost and as much for each of its tiles.  A cut within kSnap tiles of an
+// and KV head) costs `item` and as much for each of its tiles.  A cut within kSnap tiles of an
 // item's edge moves there.  Run by one CTA.
-template <int kCost = 0, typename Cost>
+template <typename Cost>
 __device__ __forceinline__ void cut_ranges(const PlanView& v, int blocks, int tiles, int hkv,
-                                           int ranges, const Cost& cost) {
+                                           int ranges, int item, const Cost& cost) {
   const int tid = threadIdx.x;
   const int U = tiles * hkv;
   const long long all = cost(blocks) * hkv;
@@ -52,7 +52,7 @@ __device__ __forceinline__ void cut_ranges(const PlanView& v, int blocks, int ti
       const int rb = lo, pre = v.rb_pre[rb], c = v.rb_pre[rb + 1] - pre;
       const long long first = cost(rb), each = cost(rb + 1) - first, in = want - first * hkv;
       const int h = static_cast<int>(in / each), f = pre * hkv + h * c;
-      const int tile = static_cast<int>(max(in - h * each - kCost, 0ll) * c / (each - kCost));
+      const int tile = static_cast<int>(max(in - h * each - item, 0ll) * c / (each - item));
       it = rb * hkv + h;
       u = f + tile;
       if (tile < kSnap) {

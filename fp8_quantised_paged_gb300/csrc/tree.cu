@@ -7,12 +7,28 @@ namespace fp8pa {
 
 namespace {
 
-// What a tile costs, of a block of at most 128 rows and of a larger one, and what an item
-// costs beside its tiles: 1.4 and 8.4 tiles, as measured.  (12 x 16K tokens, and 64 requests of
-// 1K to 32K, with items at no cost 154 and 635 us, before sums were faster; now at 6 tiles 146
-// and 221, 7.2: 146 and 208, 8.4: 146 and 204, 9.6: 148 and 205, 11: 148 and 210, 12.4: 150
-// and 209, beside a slower start of items.)
-constexpr int kTileCost = 5, kWideCost = 7, kItemCost = 42;
+// What a tile costs, of a block of at most 128 rows and of a larger one (6 to 10 fifths are within
+// 2 % of one another, for MX and INT8 trees of up to 64 nodes).
+constexpr int kTileCost = 5, kWideCost = 7;
+// What an item costs beside its tiles, 3 to 8 tiles: its time (q laid out, sums added up) is
+// much the same in every instance, while a tile takes longer where codes are converted and scores
+// capped, and less at 64 dims.  Three ragged batches of 64 requests to 32K, 8 KV heads of 4, in
+// us (the sum of the three; 64: dims):
+//   cost            8    12    16    20    24    28    32    36    42    47
+//   FP8          1073   980   890   797   751   700   670   647   637   646
+//   FP8, bias    1080   993   911   813   771   715   698   694   699   711
+//   FP8, 64       904   809   731   651   619   578   567   567   576   587
+//   FP8, 64, bias 920   819   748   666   634   621   629   640   655   666
+//   FP8, cap     1132  1034   962   872   849   862   875   892   910   929
+//   FP8, 64, cap  988   898   834   809   824   842   860   875   896   915
+//   INT8         1300  1132  1050  1042  1058  1077  1096  1117  1143  1166
+//   INT8, 64     1006   868   777   738   744   763   774   789   807   824
+//   MX           1334  1234  1260  1290  1309  1338  1363  1394  1427  1455
+//   MX, cap      1498  1361  1331  1356  1374  1402  1428  1459  1491  1514
+// 12 x 16K tokens differ by 2 % between 16 and 42.
+inline int item_cost(bool raw, float cap, int d) {
+  return !raw ? 16 : (cap > 0.f ? 22 : (d == 64 ? 30 : 42));
+}
 
 // A request's tree and its visible extent; n is 0 for a request that is skipped, `flag`
 // why.
@@ -46,12 +62,12 @@ __device__ __forceinline__ RowBlock make_tree_block(const Chunk& c, int b, int w
   return r;
 }
 
-// CTA 0 plans blocks of `rows` rows; CTA 1 + b writes the lines of request b's nodes, a thread each.
+// CTA 0 plans blocks of `rows` rows, cost: of an item; CTA 1 + b writes the lines of request b's nodes, a thread each.
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const PrefillArgs a,
                                                                  const PlanView v,
                                                                  const int32_t* parents,
                                                                  uint32_t* lines, int32_t* depths,
-                                                                 int rows, int ranges) {
+                                                                 int rows, int cost, int ranges) {
   __shared__ int s_warp[kPlanThreads / 32];
   __shared__ int s_parent[kMaxTree];
   __shared__ uint32_t s_line[kMaxTree][kLineWords];
@@ -129,10 +145,10 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const PrefillAr
     v.rb_wide[blocks] = wide;
   }
   __syncthreads();
-  cut_ranges<kItemCost>(v, blocks, carry, a.hkv, ranges, [&](int i) {
+  cut_ranges(v, blocks, carry, a.hkv, ranges, cost, [&](int i) {
     return static_cast<long long>(kTileCost) * v.rb_pre[i] +
            static_cast<long long>(kWideCost - kTileCost) * v.rb_wide[i] +
-           static_cast<long long>(kItemCost) * i;
+           static_cast<long long>(cost) * i;
   });
 }
 
@@ -213,7 +229,7 @@ cudaError_t launch_tree(const PrefillArgs& args, const int32_t* parents, cudaStr
   cfg.gridDim = dim3(1u + static_cast<unsigned>(a.batch));
   cfg.blockDim = dim3(kPlanThreads);
   if ((e = cudaLaunchKernelEx(&cfg, tree_plan_kernel, a, pv, parents, line, depth,
-                              raw ? kTreeRows : kRows, ranges)) !=
+                              raw ? kTreeRows : kRows, item_cost(raw, a.cap, a.d), ranges)) !=
       cudaSuccess)
     return e;
   cfg.gridDim = dim3(static_cast<unsigned>(ranges));
