@@ -10,25 +10,24 @@ namespace {
 // What a tile costs, of a block of at most 128 rows and of a larger one (6 to 10 fifths are within
 // 2 % of one another, for MX and INT8 trees of up to 64 nodes).
 constexpr int kTileCost = 5, kWideCost = 7;
-// What an item costs beside its tiles, 3 to 8 tiles: its time (q laid out, sums added up) is
-// much the same in every instance, while a tile takes longer where codes are converted and scores
-// capped, and less at 64 dims.  Three ragged batches of 64 requests to 32K, 8 KV heads of 4, in
-// us (the sum of the three; 64: dims):
+// What an item costs beside its tiles, 5 or 8 tiles: its time (q laid out, sums added up) is much
+// the same in every instance, while a tile takes longer where codes are converted or scores
+// capped.  Three ragged batches of 64 requests to 32K, 8 KV heads of 4, in us (the sum of the
+// three; 64: dims):
 //   cost            8    12    16    20    24    28    32    36    42    47
 //   FP8          1073   980   890   797   751   700   670   647   637   646
 //   FP8, bias    1080   993   911   813   771   715   698   694   699   711
 //   FP8, 64       904   809   731   651   619   578   567   567   576   587
-//   FP8, 64, bias 920   819   748   666   634   621   629   640   655   666
 //   FP8, cap     1132  1034   962   872   849   862   875   892   910   929
 //   FP8, 64, cap  988   898   834   809   824   842   860   875   896   915
 //   INT8         1300  1132  1050  1042  1058  1077  1096  1117  1143  1166
 //   INT8, 64     1006   868   777   738   744   763   774   789   807   824
 //   MX           1334  1234  1260  1290  1309  1338  1363  1394  1427  1455
 //   MX, cap      1498  1361  1331  1356  1374  1402  1428  1459  1491  1514
-// 12 x 16K tokens differ by 2 % between 16 and 42.
-inline int item_cost(bool raw, float cap, int d) {
-  return !raw ? 16 : (cap > 0.f ? 22 : (d == 64 ? 30 : 42));
-}
+// Few equal requests have tiles that fall well or badly for a cost, whatever the instance, and
+// both values are among the good ones: MX, 64 nodes of 1 x 32K 124, 115, 126 and 115 us at 16,
+// 24, 30 and 42, 16 nodes of 8 x 2K 64, 66, 66 and 80; INT8 125, 115, 127, 115 and 57, 59, 58, 69.
+inline int item_cost(bool raw, float cap) { return raw && cap == 0.f ? 42 : 24; }
 
 // A request's tree and its visible extent; n is 0 for a request that is skipped, `flag`
 // why.
@@ -229,7 +228,7 @@ cudaError_t launch_tree(const PrefillArgs& args, const int32_t* parents, cudaStr
   cfg.gridDim = dim3(1u + static_cast<unsigned>(a.batch));
   cfg.blockDim = dim3(kPlanThreads);
   if ((e = cudaLaunchKernelEx(&cfg, tree_plan_kernel, a, pv, parents, line, depth,
-                              raw ? kTreeRows : kRows, item_cost(raw, a.cap, a.d), ranges)) !=
+                              raw ? kTreeRows : kRows, item_cost(raw, a.cap), ranges)) !=
       cudaSuccess)
     return e;
   cfg.gridDim = dim3(static_cast<unsigned>(ranges));
