@@ -6,11 +6,11 @@
 // the threads come in.  Counts are added to and taken from by atomics on integers,
 // whose order does not show.
 //
-// Device times of the calls, in a captured graph (a plain call is bound by its host side, 13
-// to 23 us): keep 2.3 us for one request's layer, 13.0 for 64 requests of 16 layers; fork 7.5
-// for one row to 4, 20.4 for 16 rows to 128 in 16 layers; resize 8.9 for 256 rows, 22.4 for
-// 1024 rows of which many end or begin; compact 11.8 for 2K pages, 196 for 16K pages of 4
-// layers, half of them free.
+// Device times of the calls, in a captured graph (a plain call takes longer for its host side,
+// 13 to 23 us): keep 2.8 us for one request's layer, 13.6 for 64 requests of 16 layers (3.1 and
+// 15.9 where the pages' counts are looked at); fork 7.6 for one row to 4, 20.8 for 16 rows to
+// 128 in 16 layers; resize 8.2 for 256 rows, 22.3 for 1024 rows of which many end or begin;
+// compact 12.0 for 2K pages, 195.6 for 16K pages of 4 layers, half of them free.
 #include "pages.cuh"
 
 #include "common.cuh"
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kCopyThreads) keep_kernel(const int32_t* accep
 // where the fork is not made, and size[rows] the length that it takes over (a source may
 // be another fork's row: all see the rows as they were); then the free pages.  One CTA
 // plans, bound by the round trips of the counts and of the rows' lengths; the copies of the
-// last pages are bound by HBM (16 rows to 128: 20.4 us in all, 138 MB).
+// last pages are bound by HBM (16 rows to 128: 20.8 us in all, 138 MB).
 constexpr int kSkip = -2, kWhole = -1, kTail = 0;
 
 // What fork i needs: a page of its own for the last tokens (kTail) or none (kWhole); kSkip,
@@ -355,8 +355,9 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const int32_t* src, 
 // Workspace: the rows' new page counts (kSkip: the row is left), the prefix of the
 // pages that rows grow by, then the free pages.  All rows are looked at before any
 // page is given back, so that what a row may do does not depend on its neighbours'
-// order.  Three launches, as each has to see all of the one before; the last is one CTA,
-// which gives out the free pages in order and is bound by its round trips.
+// order.  Three launches: the first two take a thread and a CTA for each row, the last is one
+// CTA, which gives out the free pages in order and is bound by its round trips.  (One CTA
+// behind barriers could take all three steps of as many rows as it has threads; not tried.)
 __global__ void __launch_bounds__(256) resize_check_kernel(const int32_t* new_lens,
                                                            const PageRows r, int32_t* target) {
   griddep_wait();

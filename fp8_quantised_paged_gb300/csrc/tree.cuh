@@ -17,9 +17,9 @@
 //  - A block of at most 64 (or 32) rows stands twice (four times) in the lanes: each of the
 //    copies weighs its share of a tile's tokens, with zeros for the others'.  The products
 //    are the same, the softmax is half (a quarter).
-// The partial results (2 to 8 a row) are added up at the block's end.  A block of more than
+// The partial results (1 to 8 a row) are added up at the block's end.  A block of more than
 // 128 rows gives each stream 128 of its own, and every tile: what is converted serves twice
-// the rows (64 nodes x 4 heads of 8 x 32K tokens, MX: 544 us; 559 where blocks of 128
+// the rows (64 nodes x 4 heads of 8 x 32K tokens, MX: 538-543 us; 559 where blocks of 128
 // rows took 788).
 // FP8 codes gain less by it, since K needs no converting and the second q takes the place of
 // two of the four K tiles (12 x 16K, 64 nodes: 448 us against 498; a ragged batch of 64, 64
@@ -28,11 +28,11 @@
 // Measured (layer of 64 query and 8 KV heads of 128 dims, E4M3, a scale per token): 12 x 16K
 // tokens and 16 nodes 146 us a call, 2.9 TB/s of the cache; one request of 700 tokens 28-31 us,
 // which is the host's time (17.6 on the device, three dependent launches).  What bounds it is
-// neither DRAM (35 % of its cycles at 12 x 16K) nor the tensor pipe (26 %) but the softmax, at
-// half of the issue slots: its warps find S ready, and take 2650 cycles for half a tile (190
-// for a wait that is over, 1100 for the bound, 110 for the reference, 950 for P), so that an
-// SM takes that for a tile of one of its two streams.  An item beside its tiles costs 17000
-// cycles: 5000 until q stands in shared memory, 2000 until the first P, 8000 for the sums.
+// neither DRAM (44 % of its cycles at 12 x 16K) nor the tensor pipe (34 %) but the softmax, at
+// half of the issue slots (51 %): its warps find S ready, and take 2650 cycles for half a tile
+// (190 for a wait that is over, 1100 for the bound, 110 for the reference, 950 for P), so that
+// an SM takes that for a tile of one of its two streams.  An item beside its tiles costs 17000
+// cycles (q in two terms): 5000 until q stands in shared memory, 2000 until the first P, 8000 for the sums.
 // A suspend hint in the waits, scores held in registers between the passes (196-204 us, for
 // spills) and two threads a lane (195 us) were no faster.
 //
@@ -52,7 +52,7 @@
 // Roles: warps 0-3 and 4-7 the softmax of streams 0 and 1, a thread a lane; four warps
 // that convert V (RAW false: and four for K), one that issues MMAs for each stream, and
 // (RAW) one that copies K's pages by TMA and lays out their scales, and one for V's.  RAW
-// has 512 threads of 128 registers and no spills; 576 of 96 spill some in the softmax, but
+// has 512 threads of 128 registers and spills 8 bytes at most; 576 of 96 spill some in the softmax, but
 // six converting warps of 128 registers, 32-token jobs dealt among them, took 1735 us where
 // eight took 788.  Every wait is bounded.
 #pragma once
