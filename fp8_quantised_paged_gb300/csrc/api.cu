@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 #include <float.h>
 
+#include <initializer_list>
 #include <mutex>
 #include <utility>
 #include <vector>
@@ -456,12 +457,26 @@ int prefill_prepare(const void* q, const int32_t* q_offsets, int total_q, const 
   return FP8PA_OK;
 }
 
-// Whether two stretches of n words overlap, other than by being the same.
-bool partly_overlap(const int32_t* a, const int32_t* b, long long n) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  const uintptr_t bytes = static_cast<uintptr_t>(n) * 4;
-  return x != y && x < y + bytes && y < x + bytes;
+// A stretch of words (none at a null pointer).
+struct Words {
+  const int32_t* p;
+  long long n;
+};
+// Whether a stretch overlaps any of the others.
+bool overlaps(Words a, std::initializer_list<Words> others) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), xn = x + static_cast<uintptr_t>(a.n) * 4;
+  for (const Words& b : others) {
+    const uintptr_t y = reinterpret_cast<uintptr_t>(b.p);
+    if (b.p && x < y + static_cast<uintptr_t>(b.n) * 4 && y < xn) return true;
+  }
+  return false;
 }
+// The tables, lengths and counts of a page operator's rows.
+Words tables_of(const PageRows& r) {
+  return {r.tables, static_cast<long long>(r.rows) * r.max_blocks};
+}
+Words lens_of(const PageRows& r) { return {r.lens, r.rows}; }
+Words refs_of(const PageRows& r) { return {r.refs, r.num_blocks}; }
 
 // Validate the arguments that the page operators share; fills r, its error word excluded.
 int pages_prepare(int32_t* tables, int max_blocks, int32_t* lens, int rows, int32_t* refs,
@@ -511,7 +526,10 @@ int keep_impl(const int32_t* accepted, int max_accepted, const int32_t* q_offset
         static_cast<long long>(n_kv_heads) * n_arrays >= (1ll << 31))
       return FP8PA_ERR_UNSUPPORTED;
   }
-  if (new_lens == seq_lens || partly_overlap(new_lens, seq_lens, batch))
+  // new_lens is written while other requests' arguments are still read
+  if (overlaps({new_lens, batch},
+               {{accepted, static_cast<long long>(batch) * max_accepted},
+                {q_offsets, batch + 1ll}, tables_of(r), lens_of(r), refs_of(r)}))
     return FP8PA_ERR_UNSUPPORTED;
   r.err = device_error_ptr(static_cast<cudaStream_t>(stream), nullptr);
   if (!r.err) return FP8PA_ERR_CUDA;
@@ -958,6 +976,10 @@ int fp8pa_kv_fork(const int32_t* src_rows, const int32_t* dst_rows, int num_fork
   if (st != FP8PA_OK || num_forks == 0) return st;
   if (!src_rows || !dst_rows || !ref_counts) return FP8PA_ERR_NULL_POINTER;
   if ((st = pages_workspace(workspace, workspace_bytes, rows, num_blocks)) != FP8PA_OK) return st;
+  // the rows change while other forks are still read
+  if (overlaps({src_rows, num_forks}, {tables_of(r), lens_of(r), refs_of(r)}) ||
+      overlaps({dst_rows, num_forks}, {tables_of(r), lens_of(r), refs_of(r)}))
+    return FP8PA_ERR_UNSUPPORTED;
   r.err = device_error_ptr(static_cast<cudaStream_t>(stream), nullptr);
   if (!r.err) return FP8PA_ERR_CUDA;
   return cuda_status(launch_fork(src_rows, dst_rows, num_forks, r, pages, page_bytes, n_arrays,
@@ -973,8 +995,10 @@ int fp8pa_kv_resize(const int32_t* new_lens, int32_t* block_tables, int max_bloc
                          nullptr, 0, num_blocks, block_size, &r);
   if (st != FP8PA_OK || rows == 0) return st;
   if (!new_lens || !ref_counts) return FP8PA_ERR_NULL_POINTER;
-  if (partly_overlap(new_lens, seq_lens, rows)) return FP8PA_ERR_UNSUPPORTED;
+  if (new_lens != seq_lens && overlaps({new_lens, rows}, {lens_of(r)}))
+    return FP8PA_ERR_UNSUPPORTED;
   if ((st = pages_workspace(workspace, workspace_bytes, rows, num_blocks)) != FP8PA_OK) return st;
+  if (overlaps({new_lens, rows}, {tables_of(r), refs_of(r)})) return FP8PA_ERR_UNSUPPORTED;
   r.err = device_error_ptr(static_cast<cudaStream_t>(stream), nullptr);
   if (!r.err) return FP8PA_ERR_CUDA;
   return cuda_status(launch_resize(new_lens, r, static_cast<int32_t*>(workspace),
@@ -991,6 +1015,8 @@ int fp8pa_kv_compact(int32_t* block_tables, int max_blocks_per_seq, const int32_
   if (st != FP8PA_OK) return st;
   if (!ref_counts || !page_map) return FP8PA_ERR_NULL_POINTER;
   if ((st = pages_workspace(workspace, workspace_bytes, rows, num_blocks)) != FP8PA_OK) return st;
+  if (overlaps({page_map, num_blocks}, {tables_of(r), lens_of(r), refs_of(r)}))
+    return FP8PA_ERR_UNSUPPORTED;
   r.err = device_error_ptr(static_cast<cudaStream_t>(stream), nullptr);
   if (!r.err) return FP8PA_ERR_CUDA;
   return cuda_status(launch_compact(r, pages, page_bytes, n_arrays, page_map,

@@ -575,7 +575,9 @@ size_t fp8pa_tree_workspace_bytes(int total_q, int batch, int n_q_heads, int n_k
  * rows in order, so every result is determined by the arguments.
  * workspace     fp8pa_pages_workspace_bytes(rows, num_blocks), 4-byte aligned, no
  *               initialisation; calls that share it must be stream-ordered.
- * Limits        num_blocks * block_size < 2^31 - 1, max_blocks_per_seq <= 2^20.
+ * Limits        num_blocks * block_size < 2^31 - 1, max_blocks_per_seq <= 2^20.  Of the other
+ *               arguments none overlaps the state, and new_lens of fp8pa_kv_keep_accepted
+ *               no other at all (FP8PA_ERR_UNSUPPORTED).
  * An entry of a table outside the pool sets FP8PA_DEVERR_BLOCK_RANGE and names no page: no
  * count changes for it (a resize that gives it back makes it -1, like the others).  A
  * length outside [0, max_blocks_per_seq * block_size] sets FP8PA_DEVERR_SEQ_LEN.
@@ -597,7 +599,7 @@ size_t fp8pa_pages_workspace_bytes(int rows, int num_blocks);
  *            The second form sees to that by the pages' counts: a request of which a row
  *            would move into a page that another table holds, too, is left as it was
  *            (FP8PA_DEVERR_SHARED).
- * new_lens   i32 [batch], not overlapping seq_lens.  A request with bad offsets
+ * new_lens   i32 [batch].  A request with bad offsets
  *            (FP8PA_DEVERR_Q_OFFSETS) or a tree longer than it is is left as it was.
  * The pages behind the new length stay the row's: fp8pa_kv_resize gives them back.
  */
@@ -641,8 +643,7 @@ int fp8pa_kv_fork(const int32_t* src_rows, const int32_t* dst_rows, int num_fork
  * while the page of its next token holds tokens and is another row's, too, is left
  * (FP8PA_DEVERR_SHARED), and so is one whose table names no such page
  * (FP8PA_DEVERR_BLOCK_RANGE).
- * new_lens   i32 [rows]; may be seq_lens itself (then nothing changes), otherwise not
- *            overlapping it.
+ * new_lens   i32 [rows]; may be seq_lens itself (then nothing changes).
  */
 int fp8pa_kv_resize(const int32_t* new_lens, int32_t* block_tables, int max_blocks_per_seq,
                     int32_t* seq_lens, int rows, int32_t* ref_counts, int num_blocks,
