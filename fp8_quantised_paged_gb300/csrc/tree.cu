@@ -61,7 +61,8 @@ __device__ __forceinline__ RowBlock make_tree_block(const Chunk& c, int b, int w
   return r;
 }
 
-// CTA 0 plans blocks of `rows` rows, cost: of an item; CTA 1 + b writes the lines of request b's nodes, a thread each.
+// CTA 0 plans blocks of `rows` rows (cost: of an item); CTA 1 + b writes the lines of request
+// b's nodes, a thread each.
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const PrefillArgs a,
                                                                  const PlanView v,
                                                                  const int32_t* parents,

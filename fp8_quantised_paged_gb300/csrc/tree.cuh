@@ -32,7 +32,8 @@
 // half of the issue slots (51 %): its warps find S ready, and take 2650 cycles for half a tile
 // (190 for a wait that is over, 1100 for the bound, 110 for the reference, 950 for P), so that
 // an SM takes that for a tile of one of its two streams.  An item beside its tiles costs 17000
-// cycles (q in two terms): 5000 until q stands in shared memory, 2000 until the first P, 8000 for the sums.
+// cycles (q in two terms): 5000 until q stands in shared memory, 2000 until the first P, 8000
+// for the sums.
 // A suspend hint in the waits, scores held in registers between the passes (196-204 us, for
 // spills) and two threads a lane (195 us) were no faster.
 //
@@ -52,9 +53,9 @@
 // Roles: warps 0-3 and 4-7 the softmax of streams 0 and 1, a thread a lane; four warps
 // that convert V (RAW false: and four for K), one that issues MMAs for each stream, and
 // (RAW) one that copies K's pages by TMA and lays out their scales, and one for V's.  RAW
-// has 512 threads of 128 registers and spills 8 bytes at most; 576 of 96 spill some in the softmax, but
-// six converting warps of 128 registers, 32-token jobs dealt among them, took 1735 us where
-// eight took 788.  Every wait is bounded.
+// has 512 threads of 128 registers and spills 8 bytes at most; 576 of 96 spill some in the
+// softmax, but six converting warps of 128 registers, 32-token jobs dealt among them, took 1735
+// us where eight took 788.  Every wait is bounded.
 #pragma once
 
 #include "prefill.cuh"
@@ -126,12 +127,12 @@ struct TreeSmem {
   static constexpr int kBars = kExp + 256 * 4;
   static constexpr int kMisc = kBars + 320;        // TMEM base, abort flag
   static constexpr int kBytes = kMisc + 16;
-  static constexpr int kQ3 = (kBytes + 1023) / 1024 * 1024;  // the third term of q, where it has one
+  static constexpr int kQ3 = (kBytes + 1023) / 1024 * 1024;  // the third term of q, if any
   static constexpr int kBytesThree = kQ3 + kCodes;
   static_assert((RAW ? kBytesThree : kBytes) <= 227 * 1024);
 };
-// Barriers and the arrivals that complete a phase: Q the eight softmax warps and the issuers; P (stream * 2
-// + half) the stream's four; Info the copying warps (RAW) or the converting ones; K full
+// Barriers and the arrivals that complete a phase: Q the eight softmax warps and the two
+// issuers; P (stream * 2 + half) the stream's four; Info the copying warps (RAW) or the converting ones; K full
 // one thread and its bytes (RAW) or four warps; V codes full a thread and its bytes, free
 // the four converting warps; V full four warps; All the eight softmax warps; K and V free two
 // commits of the tensor cores, one for each stream; S and O (stream * 2 + half) and Drain (by
