@@ -132,11 +132,11 @@ struct TreeSmem {
   static_assert((RAW ? kBytesThree : kBytes) <= 227 * 1024);
 };
 // Barriers and the arrivals that complete a phase: Q the eight softmax warps and the two
-// issuers; P (stream * 2 + half) the stream's four; Info the copying warps (RAW) or the converting ones; K full
-// one thread and its bytes (RAW) or four warps; V codes full a thread and its bytes, free
-// the four converting warps; V full four warps; All the eight softmax warps; K and V free two
-// commits of the tensor cores, one for each stream; S and O (stream * 2 + half) and Drain (by
-// stream) one.
+// issuers; P (stream * 2 + half) the stream's four; Info the copying warps (RAW) or the
+// converting ones; K full one thread and its bytes (RAW) or four warps; V codes full a thread
+// and its bytes, free the four converting warps; V full four warps; All the eight softmax
+// warps; K and V free two commits of the tensor cores, one for each stream; S and O (stream *
+// 2 + half) and Drain (by stream) one.
 enum { kTQ = 0, kTP = 1, kTInfo = 5, kTKFull = 13, kTVCFull = 17, kTVCFree = 19, kTVFull = 21,
        kTAll = 23, kTKFree = 24, kTVFree = 28, kTS = 30, kTO = 34, kTDrain = 38, kTreeBars = 40 };
 template <bool RAW>
